@@ -4,7 +4,7 @@ the operator's definition in 64 bits.
 
 The cache holds K and V in blocks of ``block`` tokens. A full block is held as 8-bit codes with one scale per
 (block, KV head, K or V); the last, partial block is exact. Codes: ``e4m3`` with the smallest power-of-two scale that
-fits, or ``int8`` with scale amax / 127.
+fits, or ``int8`` with scale amax / 127; scales are 2^-100 at least, and 1 where all values are zero.
 """
 import math
 import random
@@ -161,11 +161,11 @@ def _quantised(x, case):
     if case["code"] == "e4m3":
         m, e = torch.frexp(amax)
         # the power of two from its bits: pow() is not exact
-        scale = ((torch.where(m <= 0.875, e - 9, e - 8).clamp(min=-126) + 127) << 23).view(torch.float32)
+        scale = ((torch.where(m <= 0.875, e - 9, e - 8).clamp(min=-100) + 127) << 23).view(torch.float32)
         scale = torch.where(amax == 0, torch.ones_like(scale), scale)
         codes = (x.float() / scale[:, :, None, :, None]).to(torch.float8_e4m3fn)
     else:
-        scale = torch.where(amax == 0, torch.ones_like(amax), (amax / 127).clamp(min=2.0 ** -126))
+        scale = torch.where(amax == 0, torch.ones_like(amax), (amax / 127).clamp(min=2.0 ** -100))
         # in 64 bits: a quotient next to the middle of two codes
         codes = (x.double() / scale[:, :, None, :, None].double()).round_().clamp_(-127, 127).to(torch.int8)
     return codes, scale  # [batch][blocks][block][heads][dim], [batch][blocks][heads]
@@ -198,8 +198,8 @@ def prepare(case, seed):
         state["q"] = torch.randn((rows, case["hq"], case["dim"]), device="cuda", generator=g).to(dtype)
         state["scale"] = case["dim"] ** -0.5
     if own:  # the cache that a program keeps; for attention, with the tokens in it
-        from quantized_kv_cache_seal_gb300.b8 import B8Cache
-        cache = B8Cache(num_layers=1, max_seqs=len(lens), num_q_heads=case.get("hq", case["hkv"]),
+        from quantized_kv_cache_seal_gb300.block_cache import BlockCache
+        cache = BlockCache(num_layers=1, max_seqs=len(lens), num_q_heads=case.get("hq", case["hkv"]),
                         num_kv_heads=case["hkv"], head_dim=case["dim"], block_tokens=case["block"], code=case["code"],
                         dtype=dtype, max_seq_len=max(lens), pool_blocks=sum(n // case["block"] for n in lens))
         if case["op"] == "write_read":
@@ -357,12 +357,12 @@ def _exact_block(x, code):
     top = x.abs().amax(dim=(0, 2), keepdim=True)
     one = torch.ones_like(top)
     if code == "int8":
-        scale = torch.where(top == 0, one, (top / 127).float().double().clamp(min=2.0 ** -126))  # held in 32 bits
+        scale = torch.where(top == 0, one, (top / 127).float().double().clamp(min=2.0 ** -100))  # held in 32 bits
         return _nearest_even(x / scale, 1.0).clamp(-127, 127) * scale
     exponent = torch.ceil(torch.log2(torch.where(top == 0, 448 * one, top) / 448))
     exponent = torch.where(448 * _power(exponent - 1) >= top, exponent - 1, exponent)  # log2 next to a whole number
     exponent = torch.where(448 * _power(exponent) < top, exponent + 1, exponent)
-    scale = torch.where(top == 0, one, _power(exponent.clamp(min=-126)))
+    scale = torch.where(top == 0, one, _power(exponent.clamp(min=-100)))
     y = (x / scale).abs()
     # e4m3: three bits behind the leading one, down to steps of 2^-9
     lead = torch.floor(torch.log2(torch.where(y == 0, torch.ones_like(y), y)))
