@@ -303,10 +303,138 @@ kvarn_status kvarn_check_device_error(kvarn_cache* cache, void* stream);
  * CUDA runtime cannot answer. Host only; launches nothing. */
 kvarn_status kvarn_device_accessible(const void* ptr, int32_t* accessible);
 
+/* ---- Block cache: K and V in 8 bits with one scale per block of tokens and KV head ----
+ * The plain 8-bit cache that the KVarN pages compare with (anbeeld.com section 6 names
+ * q8_0), for head_dim 64 or 128, fp16 or bf16 and 1 to 8 query heads per KV head; the pages
+ * have no interface for it, these calls are an addition. A sequence is held in blocks of
+ * block_tokens tokens. A block is sealed when its last token arrives; until then its tokens
+ * stay exact, so the cache's content never depends on how the tokens were cut into calls.
+ * Sealed, for each (block, KV head, K or V) with amax the largest absolute value:
+ *   KVARN_CODE_E4M3  scale s = 2^e, e >= -100 the smallest with amax <= 448 2^e; codes are
+ *                    x / s rounded to nearest even in fp8 e4m3;
+ *   KVARN_CODE_INT8  s = max(amax / 127 in fp32, 2^-100); codes are the whole numbers nearest
+ *                    to x / s (the real quotient, ties to even), at most 127 in size;
+ * s = 1 where amax = 0. The value held is code * s. A block that holds an infinity or NaN
+ * reads NaN throughout. Layout of the device block: private to the library.
+ *
+ * The conventions at the top of this file hold (memory, streams, errors, threads), and:
+ *   - q and out are dense, [rows][num_q_heads][head_dim], of the cache's type. k and v are
+ *     [rows][num_kv_heads][head_dim] with k_stride / v_stride elements between tokens (at
+ *     least num_kv_heads * head_dim, a multiple of 8), so that they may be parts of a packed
+ *     projection. All pointers are 16-byte aligned.
+ *   - The current device must be the one that holds the cache (EINVAL otherwise).
+ *   - Calls that change a cache, and the first call on one, cannot be captured into a graph
+ *     (KVARN_ESTATE): the host's lengths would not follow a replay. decode_attention,
+ *     prefill_attention and read can; a replay sees the lengths of the capture, and the
+ *     sequences must not have been released since.
+ *   - kvarn_last_error says what a refused call was refused for. */
+#define KVARN_TYPE_F16 0
+#define KVARN_TYPE_BF16 1
+#define KVARN_CODE_E4M3 0
+#define KVARN_CODE_INT8 1
+
+typedef struct kvarn_block_cache kvarn_block_cache;
+
+typedef struct {
+    int32_t num_layers;
+    int32_t max_seqs;       /* sequence ids are 0 .. max_seqs-1 */
+    int32_t num_q_heads;    /* 1 to 8 times num_kv_heads */
+    int32_t num_kv_heads;
+    int32_t head_dim;       /* 64 or 128 */
+    int32_t block_tokens;   /* 32, 64 or 128 */
+    int32_t code;           /* KVARN_CODE_* */
+    int32_t type;           /* KVARN_TYPE_* of exact values, inputs and outputs */
+    int32_t max_seq_len;    /* longest sequence, tokens */
+    int32_t pool_blocks;    /* blocks in the pool; one holds one (sequence, layer, block) for all KV heads */
+    int32_t flags;          /* 0 or KVARN_FLAG_HOST_ONLY */
+} kvarn_block_config;
+
+/* As kvarn_cache_required_bytes, kvarn_cache_create and kvarn_cache_destroy. */
+kvarn_status kvarn_block_required_bytes(const kvarn_block_config* cfg, size_t* bytes);
+kvarn_status kvarn_block_create(const kvarn_block_config* cfg, void* dev_mem, size_t bytes, kvarn_block_cache** out);
+void kvarn_block_destroy(kvarn_block_cache* cache);
+
+/* Append n_tokens[i] tokens to sequence seq_ids[i] of `layer`, i < n_seqs <= 256, the
+ * sequences' tokens back to back in k and v, sealing every block that fills. ECAPACITY
+ * (state unchanged) if the pool or max_seq_len would overflow. Duplicate ids: EINVAL. */
+kvarn_status kvarn_block_append(kvarn_block_cache* cache, int32_t layer, int32_t n_seqs, const int32_t* seq_ids,
+                                const int32_t* n_tokens, const void* k, int64_t k_stride, const void* v,
+                                int64_t v_stride, void* stream);
+
+/* Read back tokens starts[i] .. starts[i] + counts[i] - 1 of each sequence (starts NULL:
+ * from 0) into dense k and v, [sum(counts)][num_kv_heads][head_dim], of the cache's type (a
+ * finite value beyond its range becomes its largest) or fp32 if out_fp32. EINVAL if a range
+ * is outside its sequence. */
+kvarn_status kvarn_block_read(kvarn_block_cache* cache, int32_t layer, int32_t n_seqs, const int32_t* seq_ids,
+                              const int32_t* starts, const int32_t* counts, void* k, void* v, int32_t out_fp32,
+                              void* stream);
+
+/* Attention of one query token per sequence over all its cached tokens; zeros for an empty
+ * sequence. */
+kvarn_status kvarn_block_decode_attention(kvarn_block_cache* cache, int32_t layer, int32_t n_seqs,
+                                          const int32_t* seq_ids, const void* q, void* out, float softmax_scale,
+                                          void* stream);
+
+/* kvarn_block_append of one token per sequence, then kvarn_block_decode_attention; the
+ * arguments of both are checked before anything is enqueued. */
+kvarn_status kvarn_block_decode_step(kvarn_block_cache* cache, int32_t layer, int32_t n_seqs, const int32_t* seq_ids,
+                                     const void* k, int64_t k_stride, const void* v, int64_t v_stride, const void* q,
+                                     void* out, float softmax_scale, void* stream);
+
+/* Attention of the last q_lens[i] tokens of each sequence, each over the cached tokens at
+ * positions up to its own; 0 <= q_lens[i] <= length. */
+kvarn_status kvarn_block_prefill_attention(kvarn_block_cache* cache, int32_t layer, int32_t n_seqs,
+                                           const int32_t* seq_ids, const int32_t* q_lens, const void* q, void* out,
+                                           float softmax_scale, void* stream);
+
+/* kvarn_block_append, then kvarn_block_prefill_attention with q_lens = n_tokens. */
+kvarn_status kvarn_block_prefill(kvarn_block_cache* cache, int32_t layer, int32_t n_seqs, const int32_t* seq_ids,
+                                 const int32_t* n_tokens, const void* k, int64_t k_stride, const void* v,
+                                 int64_t v_stride, const void* q, void* out, float softmax_scale, void* stream);
+
+/* Drop sequences in every layer and return their pool blocks (an id may be given twice). */
+kvarn_status kvarn_block_release(kvarn_block_cache* cache, int32_t n_seqs, const int32_t* seq_ids);
+
+/* Number of tokens of seq_id cached in `layer`. */
+kvarn_status kvarn_block_length(const kvarn_block_cache* cache, int32_t layer, int32_t seq_id, int64_t* len);
+
+/* As kvarn_check_device_error. */
+kvarn_status kvarn_block_check_device_error(kvarn_block_cache* cache, void* stream);
+
+/* ---- RMS norm of query and key heads, with the position rotation in the same pass ----
+ * What the caches take as post-rotation queries and keys. For each token and head, in fp32:
+ *   y_j = x_j / sqrt(mean(x^2) + eps) * weight_j   (weight NULL: y = x), then for i < rot_dim / 2
+ *   with phi = position * freqs[i] (reduced exactly, so positions may be as large as int32):
+ *   (a, b) -> (a cos phi - b sin phi, b cos phi + a sin phi)
+ *   on (y_i, y_{i + rot_dim / 2}), or on (y_2i, y_{2i + 1}) if interleaved; channels from
+ *   rot_dim on pass through; rounded once to out_type. */
+typedef struct {
+    int32_t num_q_heads;  /* 0 with q and q_out NULL: keys alone */
+    int32_t num_kv_heads; /* 0 with k and k_out NULL: queries alone */
+    int32_t head_dim;     /* a multiple of 8, 8 to 256 */
+    int32_t rot_dim;      /* a multiple of 8, 0 to head_dim */
+    int32_t interleaved;
+    int32_t in_type;      /* KVARN_TYPE_* of q and k */
+    int32_t out_type;     /* KVARN_TYPE_* of q_out and k_out */
+    float eps;
+} kvarn_qk_config;
+
+/* q: [n_tokens][num_q_heads][head_dim] with q_stride elements between tokens (at least
+ * num_q_heads * head_dim, a multiple of 8; k, q_out, k_out likewise), so that q and k may be
+ * parts of a packed projection; 16-byte aligned. q_weight, k_weight: f32 [head_dim] or NULL.
+ * positions: int32 [n_tokens]; freqs: f64 [rot_dim / 2], radians per position (both may be
+ * NULL if rot_dim is 0). An output may be its own input (same address, stride and type);
+ * any other overlap is not allowed. All pointers device. Can be captured. */
+kvarn_status kvarn_qk_norm_rope(const kvarn_qk_config* cfg, int64_t n_tokens, const void* q, int64_t q_stride,
+                                const void* k, int64_t k_stride, const float* q_weight, const float* k_weight,
+                                const int32_t* positions, const double* freqs, void* q_out, int64_t q_out_stride,
+                                void* k_out, int64_t k_out_stride, void* stream);
+
 /* Static text for a status code. */
 const char* kvarn_status_string(kvarn_status status);
 
-/* Last CUDA error message seen by a call on this thread ("" if none). */
+/* Last CUDA error message, or reason of a refused block-cache or norm call, seen by a call on
+ * this thread ("" if none). */
 const char* kvarn_last_error(void);
 
 #ifdef __cplusplus

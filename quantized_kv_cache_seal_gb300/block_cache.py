@@ -1,0 +1,183 @@
+"""Owner object of a block cache (8-bit codes, one scale per block of tokens and KV head): allocates its device
+block with torch, checks tensors and forwards every call to libkvarn.so (``include/kvarn.h``, "Block cache")."""
+from __future__ import annotations
+
+import contextlib
+import math
+from typing import Optional, Sequence, Union
+
+import torch
+
+from . import kvarn as K
+
+_TYPES = {torch.float16: K.KVARN_TYPE_F16, torch.bfloat16: K.KVARN_TYPE_BF16}
+_CODES = {"e4m3": K.KVARN_CODE_E4M3, "int8": K.KVARN_CODE_INT8}
+
+
+class BlockCache:
+    """K and V of ``num_layers`` layers and ``max_seqs`` sequences in blocks of ``block_tokens`` (32, 64 or 128)
+    tokens, sealed at 8 bits when full and exact until then. ``code``: "e4m3" (power-of-two scales; keeps small
+    channels beside outliers) or "int8" (scale amax / 127; finer where values are alike). Tensors are ``dtype``
+    (fp16 or bf16) on ``device``; calls go to ``stream`` or the device's current stream and do not synchronise."""
+
+    def __init__(self, num_layers=1, max_seqs=1, num_q_heads=32, num_kv_heads=8, head_dim=128, block_tokens=64,
+                 code="e4m3", dtype=torch.float16, max_seq_len=32768, pool_blocks=None, device="cuda", flags=0):
+        if code not in _CODES or dtype not in _TYPES:
+            raise ValueError(f"code must be one of {sorted(_CODES)} and dtype fp16 or bf16, got {code!r}, {dtype}")
+        if pool_blocks is None:
+            pool_blocks = max_seqs * num_layers * (max_seq_len // max(1, block_tokens))
+        self.cfg = K.kvarn_block_config(num_layers, max_seqs, num_q_heads, num_kv_heads, head_dim, block_tokens,
+                                        _CODES[code], _TYPES[dtype], max_seq_len, pool_blocks, flags)
+        self.handle = None
+        self.dtype = dtype
+        self.scale = 1.0 / math.sqrt(head_dim)
+        self.nbytes = K.kvarn_block_required_bytes(self.cfg)
+        self.mem = torch.empty(self.nbytes + 256, dtype=torch.uint8, device=device)
+        self.device = self.mem.device
+        base = (self.mem.data_ptr() + 255) // 256 * 256
+        with self._here():
+            self.handle = K.kvarn_block_create(self.cfg, base, self.nbytes)
+
+    def close(self):
+        if self.handle:
+            K.kvarn_block_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    # -- tensors, streams ------------------------------------------------------------------------------------
+    def _here(self):
+        """The cache's device as the current one (nothing to do where it is)."""
+        if self.device.type != "cuda" or torch.cuda.current_device() == self.device.index:
+            return contextlib.nullcontext()
+        return torch.cuda.device(self.device)
+
+    def _stream(self, stream):
+        if stream is not None or self.device.type != "cuda":
+            return stream
+        return torch.cuda.current_stream(self.device)
+
+    def _empty(self, shape, dtype, stream):
+        """A result of a call on `stream`, allocated there: freed memory of another stream may still be in use."""
+        if stream is None or self.device.type != "cuda":
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=self.device)
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def _dense(self, x, rows, heads, name, dtype=None):
+        want = (rows, heads, self.cfg.head_dim)
+        if tuple(x.shape) != want or x.dtype != (dtype or self.dtype) or x.device != self.device or not x.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype or self.dtype} tensor {want} on {self.device}, got "
+                             f"{x.dtype} {tuple(x.shape)} with strides {x.stride()} on {x.device}")
+        return x
+
+    def _tokens(self, x, rows, name):
+        """Elements between the tokens of k or v; its heads and channels are dense."""
+        c = self.cfg
+        if (tuple(x.shape) != (rows, c.num_kv_heads, c.head_dim) or x.dtype != self.dtype or x.device != self.device
+                or (rows > 0 and (x.stride(2) != 1 or (c.num_kv_heads > 1 and x.stride(1) != c.head_dim)))):
+            raise ValueError(f"{name} must be a {self.dtype} tensor {(rows, c.num_kv_heads, c.head_dim)} on {self.device} "
+                             f"with dense heads, got {x.dtype} {tuple(x.shape)} with strides {x.stride()} on {x.device}")
+        return x.stride(0) if rows > 1 else c.num_kv_heads * c.head_dim
+
+    # -- calls -----------------------------------------------------------------------------------------------
+    def append(self, layer: int, seq_ids: Sequence[int], n_tokens: Sequence[int], k: torch.Tensor, v: torch.Tensor,
+               stream=None):
+        """Append n_tokens[i] tokens to each sequence; k, v: [sum(n_tokens)][Hkv][D], any stride between tokens."""
+        rows = sum(n_tokens)
+        ks, vs = self._tokens(k, rows, "k"), self._tokens(v, rows, "v")
+        _same_length(seq_ids, n_tokens)
+        with self._here():
+            K.kvarn_block_append(self.handle, layer, seq_ids, n_tokens, k, ks, v, vs, self._stream(stream))
+
+    def read(self, layer: int, seq_ids: Sequence[int], starts: Optional[Sequence[int]], counts: Sequence[int],
+             dtype: Optional[torch.dtype] = None, stream=None):
+        """(k, v) of tokens starts[i] .. starts[i] + counts[i] - 1 (starts None: from 0) of each sequence, back to
+        back, [sum(counts)][Hkv][D] of the cache's dtype or torch.float32."""
+        dtype = dtype or self.dtype
+        if dtype not in (self.dtype, torch.float32):
+            raise ValueError(f"dtype must be {self.dtype} or torch.float32, got {dtype}")
+        _same_length(seq_ids, counts)
+        if starts is not None:
+            _same_length(seq_ids, starts)
+        if any(n < 0 for n in counts):
+            raise ValueError("counts must not be negative")
+        shape = (sum(counts), self.cfg.num_kv_heads, self.cfg.head_dim)
+        k, v = self._empty(shape, dtype, stream), self._empty(shape, dtype, stream)
+        with self._here():
+            K.kvarn_block_read(self.handle, layer, seq_ids, starts, counts, k, v, dtype == torch.float32,
+                               self._stream(stream))
+        return k, v
+
+    def _attention(self, q, rows, out, stream):
+        self._dense(q, rows, self.cfg.num_q_heads, "q")
+        if out is None:
+            return self._empty(q.shape, q.dtype, stream)
+        return self._dense(out, rows, self.cfg.num_q_heads, "out")
+
+    def decode_attention(self, layer: int, seq_ids: Sequence[int], q: torch.Tensor, out: Optional[torch.Tensor] = None,
+                         scale: Optional[float] = None, stream=None) -> torch.Tensor:
+        """One query token per sequence over all its cached tokens; q, out: [len(seq_ids)][Hq][D]."""
+        out = self._attention(q, len(seq_ids), out, stream)
+        with self._here():
+            K.kvarn_block_decode_attention(self.handle, layer, seq_ids, q, out, self.scale if scale is None else scale,
+                                           self._stream(stream))
+        return out
+
+    def decode_step(self, layer: int, seq_ids: Sequence[int], k: torch.Tensor, v: torch.Tensor, q: torch.Tensor,
+                    out: Optional[torch.Tensor] = None, scale: Optional[float] = None, stream=None) -> torch.Tensor:
+        """Append one token per sequence and attend its query; k, v: [len(seq_ids)][Hkv][D]."""
+        n = len(seq_ids)
+        ks, vs = self._tokens(k, n, "k"), self._tokens(v, n, "v")
+        out = self._attention(q, n, out, stream)
+        with self._here():
+            K.kvarn_block_decode_step(self.handle, layer, seq_ids, k, ks, v, vs, q, out,
+                                      self.scale if scale is None else scale, self._stream(stream))
+        return out
+
+    def prefill_attention(self, layer: int, seq_ids: Sequence[int], q_lens: Sequence[int], q: torch.Tensor,
+                          out: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                          stream=None) -> torch.Tensor:
+        """Causal attention of the last q_lens[i] tokens of each sequence; q, out: [sum(q_lens)][Hq][D]."""
+        _same_length(seq_ids, q_lens)
+        out = self._attention(q, sum(q_lens), out, stream)
+        with self._here():
+            K.kvarn_block_prefill_attention(self.handle, layer, seq_ids, q_lens, q, out,
+                                            self.scale if scale is None else scale, self._stream(stream))
+        return out
+
+    def prefill(self, layer: int, seq_ids: Sequence[int], n_tokens: Sequence[int], k: torch.Tensor, v: torch.Tensor,
+                q: torch.Tensor, out: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                stream=None) -> torch.Tensor:
+        """Append a prompt chunk and attend its queries."""
+        _same_length(seq_ids, n_tokens)
+        rows = sum(n_tokens)
+        ks, vs = self._tokens(k, rows, "k"), self._tokens(v, rows, "v")
+        out = self._attention(q, rows, out, stream)
+        with self._here():
+            K.kvarn_block_prefill(self.handle, layer, seq_ids, n_tokens, k, ks, v, vs, q, out,
+                                  self.scale if scale is None else scale, self._stream(stream))
+        return out
+
+    def release(self, seq_ids: Union[int, Sequence[int]]):
+        """Drop sequences in every layer. A later append may reuse their blocks: it must follow, on the GPU, the
+        calls that still read them (issue both to one stream)."""
+        K.kvarn_block_release(self.handle, [seq_ids] if isinstance(seq_ids, int) else seq_ids)
+
+    def length(self, layer: int, seq_id: int) -> int:
+        return K.kvarn_block_length(self.handle, layer, seq_id)
+
+    def check_device_error(self, stream=None) -> int:
+        with self._here():
+            return K.kvarn_block_check_device_error(self.handle, self._stream(stream))
+
+
+def _same_length(seq_ids, counts):
+    if len(seq_ids) != len(counts):
+        raise ValueError(f"{len(seq_ids)} sequences, but {len(counts)} counts")

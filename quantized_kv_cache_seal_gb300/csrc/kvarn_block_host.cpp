@@ -1,0 +1,518 @@
+// Host side of the block cache and of the query/key norm + rotation: argument checks, the
+// host mirror of sequence lengths and pool slots, launch parameters, and the C ABI.
+#include <algorithm>
+#include <cmath>
+#include <cstdio>
+#include <cstring>
+#include <memory>
+#include <new>
+#include <vector>
+
+#include "../../include/kvarn.h"
+#include "kvarn_block.h"
+
+using namespace kvarn;
+
+struct kvarn_block_cache {
+    kvarn_block_config cfg;
+    BlockView view;
+    int r = 1;
+    std::vector<int32_t> len;         // [max_seqs][num_layers]
+    std::vector<int32_t> table;       // [max_seqs][num_layers][max_blocks]
+    std::vector<int32_t> free_slots;  // stack of free pool slots
+    std::vector<char> seen;           // scratch of check_ids, all zero between calls
+    bool initialized = false;
+    bool host_only = false;
+    int device = -1;
+    int sms = 152;
+
+    int32_t& L(int seq, int layer) { return len[(size_t)seq * cfg.num_layers + layer]; }
+    int32_t* T(int seq, int layer) { return &table[((size_t)seq * cfg.num_layers + layer) * view.max_blocks]; }
+};
+
+namespace {
+
+kvarn_status fail(kvarn_status st, const char* text) {
+    set_last_error(text);
+    return st;
+}
+
+kvarn_status cuda_fail(int rc, const char* what) {
+    char text[256];
+    std::snprintf(text, sizeof(text), "%s: %s (%d)", what, cuda_error_string(rc), rc);
+    return fail(KVARN_ECUDA, text);
+}
+
+bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+
+// Device layout of a cache; false if the sizes leave what an address can hold.
+bool make_view(const kvarn_block_config& c, BlockView* v) {
+    std::memset(v, 0, sizeof(*v));
+    v->hkv = c.num_kv_heads;
+    v->d = c.head_dim;
+    v->block = c.block_tokens;
+    v->log2_block = c.block_tokens == 32 ? 5 : c.block_tokens == 64 ? 6 : 7;
+    v->num_layers = c.num_layers;
+    v->max_blocks = std::max(1, c.max_seq_len / c.block_tokens);
+    v->int8 = c.code == KVARN_CODE_INT8;
+    v->bf16 = c.type == KVARN_TYPE_BF16;
+    v->slot_bytes = (int64_t)c.num_kv_heads * (c.block_tokens / kTileTokens) * tile_bytes(c.head_dim);
+    unsigned __int128 off = 0;
+    auto take = [&](unsigned __int128 n) {
+        const unsigned __int128 o = off;
+        off = (off + n + 255) / 256 * 256;
+        return (size_t)o;
+    };
+    typedef unsigned __int128 U;
+    const U seq_layers = (U)c.max_seqs * c.num_layers;
+    const U tail = seq_layers * c.num_kv_heads * c.block_tokens * c.head_dim * 2;
+    v->lay.err = take(16);
+    v->lay.table = take(seq_layers * v->max_blocks * 4);
+    v->lay.counters = take(kBlockMaxGrid * 4);
+    v->lay.partials = take((U)kBlockMaxGrid * 2 * kBlockMaxRatio * (c.head_dim + 2) * 4);
+    v->lay.tail_k = take(tail);
+    v->lay.tail_v = take(tail);
+    v->lay.pool = take((U)c.pool_blocks * (U)v->slot_bytes);
+    v->lay.total = (size_t)off;
+    return off < ((U)1 << 46);
+}
+
+kvarn_status check_config(const kvarn_block_config* c) {
+    if (!c) return fail(KVARN_EINVAL, "no configuration");
+    if (c->num_layers <= 0 || c->max_seqs <= 0 || c->num_kv_heads <= 0 || c->num_q_heads <= 0 || c->max_seq_len <= 0 ||
+        c->pool_blocks < 0)
+        return fail(KVARN_EINVAL, "sizes must be positive");
+    if (c->head_dim != 64 && c->head_dim != 128) return fail(KVARN_EINVAL, "head_dim must be 64 or 128");
+    if (c->block_tokens != 32 && c->block_tokens != 64 && c->block_tokens != 128)
+        return fail(KVARN_EINVAL, "block_tokens must be 32, 64 or 128");
+    if (c->code != KVARN_CODE_E4M3 && c->code != KVARN_CODE_INT8) return fail(KVARN_EINVAL, "unknown code");
+    if (c->type != KVARN_TYPE_F16 && c->type != KVARN_TYPE_BF16) return fail(KVARN_EINVAL, "unknown type");
+    if (c->num_q_heads % c->num_kv_heads || c->num_q_heads / c->num_kv_heads > kBlockMaxRatio)
+        return fail(KVARN_EINVAL, "num_q_heads must be 1 to 8 times num_kv_heads");
+    if ((c->flags & ~KVARN_FLAG_HOST_ONLY) != 0) return fail(KVARN_EINVAL, "unknown flag");
+    if ((int64_t)c->max_seqs * c->num_layers > (1ll << 31) - 1 || c->num_kv_heads > (1 << 16))
+        return fail(KVARN_EINVAL, "too many sequences, layers or heads");
+    return KVARN_OK;
+}
+
+// A call's layer and sequences; `changes`: the call moves the cache on, which a captured
+// graph would do again at each replay without the host's lengths following.
+kvarn_status check_call(kvarn_block_cache* c, int32_t layer, int32_t n, const int32_t* ids, void* stream, bool changes) {
+    if (!c) return fail(KVARN_EINVAL, "no cache");
+    if (layer < 0 || layer >= c->cfg.num_layers) return fail(KVARN_EINVAL, "no such layer");
+    if (n < 0 || (n > 0 && !ids)) return fail(KVARN_EINVAL, "bad sequence list");
+    if (n > kBlockMaxSeqs) return fail(KVARN_ECAPACITY, "more than 256 sequences in a call");
+    kvarn_status st = KVARN_OK;
+    int i = 0;
+    for (; i < n; ++i) {
+        if (ids[i] < 0 || ids[i] >= c->cfg.max_seqs || c->seen[ids[i]]) {
+            st = fail(KVARN_EINVAL, "a sequence id is out of range or given twice");
+            break;
+        }
+        c->seen[ids[i]] = 1;
+    }
+    for (int j = 0; j < i; ++j) c->seen[ids[j]] = 0;
+    if (st || c->host_only) return st;
+    int dev = -1;
+    int rc = current_device(&dev);
+    if (rc) return cuda_fail(rc, "current device");
+    if (dev != c->device) return fail(KVARN_EINVAL, "the current device is not the one that holds the cache");
+    if (changes || !c->initialized) {
+        int capturing = 0;
+        rc = stream_capturing(stream, &capturing);
+        if (rc) return cuda_fail(rc, "capture state");
+        if (capturing) return fail(KVARN_ESTATE, "a call that changes the cache (or is its first) cannot be captured");
+    }
+    return KVARN_OK;
+}
+
+kvarn_status ensure_init(kvarn_block_cache* c, void* stream) {
+    if (c->host_only || c->initialized) return KVARN_OK;
+    const int rc = launch_block_init(c->view, stream);
+    if (rc) return cuda_fail(rc, "cache init");
+    c->initialized = true;
+    return KVARN_OK;
+}
+
+kvarn_status check_append(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* ids, const int32_t* n_tokens,
+                          const void* k, const void* v, int64_t k_stride, int64_t v_stride) {
+    if (n_seqs > 0 && !n_tokens) return fail(KVARN_EINVAL, "no token counts");
+    const int bt = c->cfg.block_tokens;
+    int64_t total = 0, blocks = 0;
+    for (int i = 0; i < n_seqs; ++i) {
+        if (n_tokens[i] < 0) return fail(KVARN_EINVAL, "a token count is negative");
+        const int64_t n0 = c->L(ids[i], layer), n1 = n0 + n_tokens[i];
+        if (n1 > c->cfg.max_seq_len) return fail(KVARN_ECAPACITY, "a sequence would exceed max_seq_len");
+        total += n_tokens[i];
+        blocks += n1 / bt - n0 / bt;
+    }
+    if (total >= 1ll << 31) return fail(KVARN_ECAPACITY, "2^31 tokens or more in a call");
+    if ((size_t)blocks > c->free_slots.size()) return fail(KVARN_ECAPACITY, "the pool has too few free blocks");
+    if (total == 0) return KVARN_OK;
+    const int64_t row = (int64_t)c->cfg.num_kv_heads * c->cfg.head_dim;
+    if (!k || !v || !aligned16(k) || !aligned16(v)) return fail(KVARN_EINVAL, "k and v must be 16-byte aligned");
+    if (k_stride < row || v_stride < row || k_stride % 8 || v_stride % 8)
+        return fail(KVARN_EINVAL, "token strides must hold a token's heads and be multiples of 8 elements");
+    return KVARN_OK;
+}
+
+template <class P>
+kvarn_status launch_append(kvarn_block_cache* c, const P& p, void* stream) {
+    if (c->host_only || p.items == 0) return KVARN_OK;
+    const int rc = launch_block_append(p, stream);
+    return rc ? cuda_fail(rc, "append launch") : KVARN_OK;
+}
+
+// Append after its checks: launches of as many tokens as the parameters hold slots for. A
+// sequence may be cut between launches at any token (the result does not depend on it).
+template <class P>
+kvarn_status run_append(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* ids, const int32_t* n_tokens,
+                        const void* k, const void* v, int64_t k_stride, int64_t v_stride, void* stream, int max_slots) {
+    const int bt = c->cfg.block_tokens;
+    static thread_local P p;
+    p.c = c->view;
+    p.c.layer = layer;
+    p.k = (const uint16_t*)k;
+    p.v = (const uint16_t*)v;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.n_seqs = p.items = 0;
+    int slots = 0;
+    int64_t row = 0;
+    for (int i = 0; i < n_seqs; ++i) {
+        int32_t left = n_tokens[i];
+        while (left > 0) {
+            int32_t& n0 = c->L(ids[i], layer);
+            const int room = max_slots - slots;
+            // blocks and items that fit (items stay far below 2^31: max_slots * Hkv * 2)
+            const int32_t take = (int32_t)std::min<int64_t>(left, (int64_t)(n0 / bt + room) * bt + bt - 1 - n0);
+            BlockAppendSeq& e = p.seqs[p.n_seqs++];
+            e.seq = ids[i];
+            e.n_before = n0;
+            e.n_new = take;
+            e.n_blocks = (n0 + take) / bt - n0 / bt;
+            e.in_row = (int32_t)row;
+            e.item_begin = p.items;
+            e.slot_begin = slots;
+            int32_t* t = c->T(ids[i], layer) + n0 / bt;
+            for (int j = 0; j < e.n_blocks; ++j) {
+                p.slots[slots++] = t[j] = c->free_slots.back();
+                c->free_slots.pop_back();
+            }
+            p.items += std::max(e.n_blocks, 1) * c->cfg.num_kv_heads * 2;
+            n0 += take;
+            row += take;
+            left -= take;
+            if (left > 0) {  // the parameters are full
+                const kvarn_status st = launch_append(c, p, stream);
+                if (st) return st;
+                p.n_seqs = p.items = slots = 0;
+            }
+        }
+    }
+    return launch_append(c, p, stream);
+}
+
+kvarn_status append(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* ids, const int32_t* n_tokens,
+                    const void* k, const void* v, int64_t k_stride, int64_t v_stride, void* stream) {
+    kvarn_status st = ensure_init(c, stream);
+    if (st) return st;
+    const int bt = c->cfg.block_tokens;
+    int64_t blocks = 0;
+    for (int i = 0; i < n_seqs; ++i) {
+        const int64_t n0 = c->L(ids[i], layer);
+        blocks += (n0 + n_tokens[i]) / bt - n0 / bt;
+    }
+    if (n_seqs <= 16 && blocks <= 128)
+        return run_append<BlockAppendSmall>(c, layer, n_seqs, ids, n_tokens, k, v, k_stride, v_stride, stream, 128);
+    return run_append<BlockAppendLarge>(c, layer, n_seqs, ids, n_tokens, k, v, k_stride, v_stride, stream, 5000);
+}
+
+kvarn_status check_attention(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* ids, const int32_t* q_lens,
+                             const int32_t* added, const void* q, const void* out, float scale) {
+    if (!std::isfinite(scale)) return fail(KVARN_EINVAL, "softmax_scale must be finite");
+    int64_t rows = 0;
+    for (int i = 0; i < n_seqs; ++i) {
+        const int64_t n = c->L(ids[i], layer) + (added ? (int64_t)added[i] : 0);
+        const int64_t m = q_lens ? q_lens[i] : 1;
+        if (q_lens && (m < 0 || m > n)) return fail(KVARN_EINVAL, "a query count is negative or above the sequence's length");
+        rows += m;
+    }
+    if (rows * c->cfg.num_q_heads >= 1ll << 31) return fail(KVARN_ECAPACITY, "2^31 query rows or more in a call");
+    if (rows > 0 && (!q || !out || !aligned16(q) || !aligned16(out)))
+        return fail(KVARN_EINVAL, "q and out must be 16-byte aligned");
+    return KVARN_OK;
+}
+
+kvarn_status run_prefill(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* ids, const int32_t* q_lens,
+                         const void* q, void* out, float scale, void* stream) {
+    static thread_local BlockPrefillParams p;
+    p.c = c->view;
+    p.c.layer = layer;
+    p.q = (const uint16_t*)q;
+    p.out = (uint16_t*)out;
+    p.hq = c->cfg.num_q_heads;
+    p.r = c->r;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.n_seqs = p.grid = 0;
+    int64_t row = 0;
+    for (int i = 0; i < n_seqs; ++i) {
+        const int m = q_lens ? q_lens[i] : 1;
+        if (m > 0) {
+            BlockPrefillSeq& e = p.seqs[p.n_seqs++];
+            e.seq = ids[i];
+            e.n = c->L(ids[i], layer);
+            e.q_len = m;
+            e.q_row = (int32_t)row;
+            e.cta_begin = p.grid;
+            p.grid += m * p.hq;
+        }
+        row += m;
+    }
+    if (p.n_seqs == 0 || c->host_only) return KVARN_OK;
+    const kvarn_status st = ensure_init(c, stream);
+    if (st) return st;
+    const int rc = launch_block_prefill(p, stream);
+    return rc ? cuda_fail(rc, "prefill launch") : KVARN_OK;
+}
+
+kvarn_status run_decode(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* ids, const void* q, void* out,
+                        float scale, void* stream) {
+    return run_prefill(c, layer, n_seqs, ids, nullptr, q, out, scale, stream);
+}
+
+}  // namespace
+
+// Host allocations are made by kvarn_block_create alone; every other entry works in memory
+// that it reserved, so that no C++ exception can reach a C caller.
+extern "C" {
+
+kvarn_status kvarn_block_required_bytes(const kvarn_block_config* cfg, size_t* bytes) {
+    kvarn_status st = check_config(cfg);
+    if (st) return st;
+    if (!bytes) return fail(KVARN_EINVAL, "no place for the size");
+    BlockView v;
+    if (!make_view(*cfg, &v)) return fail(KVARN_EINVAL, "the cache is too large");
+    *bytes = v.lay.total;
+    return KVARN_OK;
+}
+
+kvarn_status kvarn_block_create(const kvarn_block_config* cfg, void* dev_mem, size_t bytes, kvarn_block_cache** out) {
+    kvarn_status st = check_config(cfg);
+    if (st) return st;
+    if (!out || !dev_mem || ((uintptr_t)dev_mem & 255)) return fail(KVARN_EINVAL, "dev_mem must be 256-byte aligned");
+    std::unique_ptr<kvarn_block_cache> c(new (std::nothrow) kvarn_block_cache());
+    if (!c) return fail(KVARN_ENOMEM, "out of host memory");
+    c->cfg = *cfg;
+    if (!make_view(*cfg, &c->view)) return fail(KVARN_EINVAL, "the cache is too large");
+    if (bytes < c->view.lay.total) return fail(KVARN_ENOMEM, "the device block is too small");
+    c->view.base = (uint8_t*)dev_mem;
+    c->r = cfg->num_q_heads / cfg->num_kv_heads;
+    c->host_only = (cfg->flags & KVARN_FLAG_HOST_ONLY) != 0;
+    try {
+        c->len.assign((size_t)cfg->max_seqs * cfg->num_layers, 0);
+        c->table.assign((size_t)cfg->max_seqs * cfg->num_layers * c->view.max_blocks, -1);
+        c->free_slots.resize(cfg->pool_blocks);
+        c->seen.assign(cfg->max_seqs, 0);
+    } catch (...) {
+        return fail(KVARN_ENOMEM, "out of host memory");
+    }
+    for (int i = 0; i < cfg->pool_blocks; ++i) c->free_slots[i] = cfg->pool_blocks - 1 - i;  // pop gives 0, 1, 2 ..
+    if (!c->host_only) {
+        c->sms = sm_count();
+        if (c->sms <= 0 || pointer_device(dev_mem, &c->device)) return fail(KVARN_ECUDA, "no CUDA device");
+    }
+    *out = c.release();
+    return KVARN_OK;
+}
+
+void kvarn_block_destroy(kvarn_block_cache* cache) { delete cache; }
+
+kvarn_status kvarn_block_append(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* seq_ids,
+                                const int32_t* n_tokens, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                                void* stream) {
+    kvarn_status st = check_call(c, layer, n_seqs, seq_ids, stream, true);
+    if (st) return st;
+    st = check_append(c, layer, n_seqs, seq_ids, n_tokens, k, v, k_stride, v_stride);
+    if (st) return st;
+    return append(c, layer, n_seqs, seq_ids, n_tokens, k, v, k_stride, v_stride, stream);
+}
+
+kvarn_status kvarn_block_read(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* seq_ids,
+                              const int32_t* starts, const int32_t* counts, void* k, void* v, int32_t out_fp32,
+                              void* stream) {
+    kvarn_status st = check_call(c, layer, n_seqs, seq_ids, stream, false);
+    if (st) return st;
+    if (n_seqs > 0 && !counts) return fail(KVARN_EINVAL, "no token counts");
+    static thread_local BlockReadParams p;
+    p.c = c->view;
+    p.c.layer = layer;
+    p.k = k;
+    p.v = v;
+    p.f32 = out_fp32 != 0;
+    p.n_seqs = 0;
+    int64_t row = 0, items = 0;
+    for (int i = 0; i < n_seqs; ++i) {
+        const int64_t n = c->L(seq_ids[i], layer), s = starts ? starts[i] : 0, m = counts[i];
+        if (s < 0 || m < 0 || s + m > n) return fail(KVARN_EINVAL, "a range is outside its sequence");
+        if (m > 0) {
+            BlockReadSeq& e = p.seqs[p.n_seqs++];
+            e.seq = seq_ids[i];
+            e.n = (int32_t)n;
+            e.start = (int32_t)s;
+            e.count = (int32_t)m;
+            e.out_row = (int32_t)row;
+            e.item_begin = (int32_t)items;
+            items += ((s + m - 1) / kTileTokens - s / kTileTokens + 1) * c->cfg.num_kv_heads * 2;
+        }
+        row += m;
+        if (row >= 1ll << 31 || items >= 1ll << 31) return fail(KVARN_ECAPACITY, "too many tokens in a call");
+    }
+    if (p.n_seqs == 0) return KVARN_OK;
+    if (!k || !v || !aligned16(k) || !aligned16(v)) return fail(KVARN_EINVAL, "k and v must be 16-byte aligned");
+    p.items = (int32_t)items;
+    if (c->host_only) return KVARN_OK;
+    const int rc = launch_block_read(p, stream);
+    return rc ? cuda_fail(rc, "read launch") : KVARN_OK;
+}
+
+kvarn_status kvarn_block_decode_attention(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* seq_ids,
+                                          const void* q, void* out, float softmax_scale, void* stream) {
+    kvarn_status st = check_call(c, layer, n_seqs, seq_ids, stream, false);
+    if (st) return st;
+    st = check_attention(c, layer, n_seqs, seq_ids, nullptr, nullptr, q, out, softmax_scale);
+    if (st || n_seqs == 0) return st;
+    return run_decode(c, layer, n_seqs, seq_ids, q, out, softmax_scale, stream);
+}
+
+kvarn_status kvarn_block_decode_step(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* seq_ids,
+                                     const void* k, int64_t k_stride, const void* v, int64_t v_stride, const void* q,
+                                     void* out, float softmax_scale, void* stream) {
+    kvarn_status st = check_call(c, layer, n_seqs, seq_ids, stream, true);
+    if (st) return st;
+    int32_t ones[kBlockMaxSeqs];
+    for (int i = 0; i < n_seqs; ++i) ones[i] = 1;
+    st = check_append(c, layer, n_seqs, seq_ids, ones, k, v, k_stride, v_stride);
+    if (st) return st;
+    st = check_attention(c, layer, n_seqs, seq_ids, nullptr, ones, q, out, softmax_scale);
+    if (st || n_seqs == 0) return st;
+    st = append(c, layer, n_seqs, seq_ids, ones, k, v, k_stride, v_stride, stream);
+    if (st) return st;
+    return run_decode(c, layer, n_seqs, seq_ids, q, out, softmax_scale, stream);
+}
+
+kvarn_status kvarn_block_prefill_attention(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* seq_ids,
+                                           const int32_t* q_lens, const void* q, void* out, float softmax_scale,
+                                           void* stream) {
+    kvarn_status st = check_call(c, layer, n_seqs, seq_ids, stream, false);
+    if (st) return st;
+    if (n_seqs > 0 && !q_lens) return fail(KVARN_EINVAL, "no query counts");
+    st = check_attention(c, layer, n_seqs, seq_ids, q_lens, nullptr, q, out, softmax_scale);
+    if (st || n_seqs == 0) return st;
+    return run_prefill(c, layer, n_seqs, seq_ids, q_lens, q, out, softmax_scale, stream);
+}
+
+kvarn_status kvarn_block_prefill(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* seq_ids,
+                                 const int32_t* n_tokens, const void* k, int64_t k_stride, const void* v,
+                                 int64_t v_stride, const void* q, void* out, float softmax_scale, void* stream) {
+    kvarn_status st = check_call(c, layer, n_seqs, seq_ids, stream, true);
+    if (st) return st;
+    st = check_append(c, layer, n_seqs, seq_ids, n_tokens, k, v, k_stride, v_stride);
+    if (st) return st;
+    st = check_attention(c, layer, n_seqs, seq_ids, n_tokens, n_tokens, q, out, softmax_scale);
+    if (st || n_seqs == 0) return st;
+    st = append(c, layer, n_seqs, seq_ids, n_tokens, k, v, k_stride, v_stride, stream);
+    if (st) return st;
+    return run_prefill(c, layer, n_seqs, seq_ids, n_tokens, q, out, softmax_scale, stream);
+}
+
+kvarn_status kvarn_block_release(kvarn_block_cache* c, int32_t n_seqs, const int32_t* seq_ids) {
+    if (!c || n_seqs < 0 || (n_seqs > 0 && !seq_ids)) return fail(KVARN_EINVAL, "bad sequence list");
+    for (int i = 0; i < n_seqs; ++i)
+        if (seq_ids[i] < 0 || seq_ids[i] >= c->cfg.max_seqs) return fail(KVARN_EINVAL, "no such sequence");
+    for (int i = 0; i < n_seqs; ++i)
+        for (int l = c->cfg.num_layers - 1; l >= 0; --l) {
+            int32_t* t = c->T(seq_ids[i], l);
+            // free_slots never holds more than pool_blocks entries: it was sized to that once
+            for (int b = c->L(seq_ids[i], l) / c->cfg.block_tokens - 1; b >= 0; --b) {
+                c->free_slots.push_back(t[b]);
+                t[b] = -1;
+            }
+            c->L(seq_ids[i], l) = 0;
+        }
+    return KVARN_OK;
+}
+
+kvarn_status kvarn_block_length(const kvarn_block_cache* c, int32_t layer, int32_t seq_id, int64_t* len) {
+    if (!c || !len || layer < 0 || layer >= c->cfg.num_layers || seq_id < 0 || seq_id >= c->cfg.max_seqs)
+        return fail(KVARN_EINVAL, "no such layer or sequence");
+    *len = c->len[(size_t)seq_id * c->cfg.num_layers + layer];
+    return KVARN_OK;
+}
+
+kvarn_status kvarn_block_check_device_error(kvarn_block_cache* c, void* stream) {
+    if (!c) return fail(KVARN_EINVAL, "no cache");
+    if (c->host_only || !c->initialized) return KVARN_OK;
+    int32_t err[4] = {0, 0, 0, 0};
+    int rc = memcpy_d2h_sync(err, c->view.base + c->view.lay.err, sizeof(err), stream);
+    if (rc) return cuda_fail(rc, "error word read");
+    const int32_t zero[4] = {0, 0, 0, 0};
+    rc = memcpy_h2d_async(c->view.base + c->view.lay.err, zero, sizeof(zero), stream);
+    if (rc) return cuda_fail(rc, "error word clear");
+    return err[0] & kErrTimeout ? KVARN_ETIMEOUT : err[0] ? KVARN_ESTATE : KVARN_OK;
+}
+
+kvarn_status kvarn_qk_norm_rope(const kvarn_qk_config* cfg, int64_t n_tokens, const void* q, int64_t q_stride, const void* k,
+                                int64_t k_stride, const float* q_weight, const float* k_weight, const int32_t* positions,
+                                const double* freqs, void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                                void* stream) {
+    if (!cfg) return fail(KVARN_EINVAL, "no configuration");
+    const int64_t hq = cfg->num_q_heads, hk = cfg->num_kv_heads, d = cfg->head_dim;
+    if (hq < 0 || hk < 0 || hq + hk < 1 || hq + hk > (1 << 16)) return fail(KVARN_EINVAL, "bad head counts");
+    if (d < 8 || d > 256 || d % 8) return fail(KVARN_EINVAL, "head_dim must be a multiple of 8 up to 256");
+    if (cfg->rot_dim < 0 || cfg->rot_dim > d || cfg->rot_dim % 8)
+        return fail(KVARN_EINVAL, "rot_dim must be a multiple of 8 up to head_dim");
+    if ((cfg->in_type != KVARN_TYPE_F16 && cfg->in_type != KVARN_TYPE_BF16) ||
+        (cfg->out_type != KVARN_TYPE_F16 && cfg->out_type != KVARN_TYPE_BF16))
+        return fail(KVARN_EINVAL, "unknown type");
+    if (!(cfg->eps >= 0.f) || !std::isfinite(cfg->eps)) return fail(KVARN_EINVAL, "eps must be finite and not negative");
+    if (n_tokens < 0 || n_tokens * (hq + hk) >= 1ll << 31) return fail(KVARN_EINVAL, "bad token count");
+    if (n_tokens == 0) return KVARN_OK;
+    struct Side { const void* in; const void* out; int64_t heads, in_stride, out_stride; };
+    for (const Side& s : {Side{q, q_out, hq, q_stride, q_out_stride}, Side{k, k_out, hk, k_stride, k_out_stride}}) {
+        if (s.heads == 0) continue;
+        if (!s.in || !s.out || !aligned16(s.in) || !aligned16(s.out))
+            return fail(KVARN_EINVAL, "q, k and their outputs must be 16-byte aligned");
+        if (s.in_stride < s.heads * d || s.out_stride < s.heads * d || s.in_stride % 8 || s.out_stride % 8)
+            return fail(KVARN_EINVAL, "token strides must hold a token's heads and be multiples of 8 elements");
+    }
+    if (cfg->rot_dim > 0 && (!positions || !freqs)) return fail(KVARN_EINVAL, "no positions or frequencies");
+    QkParams p;
+    p.q = (const uint16_t*)q;
+    p.k = (const uint16_t*)k;
+    p.q_out = (uint16_t*)q_out;
+    p.k_out = (uint16_t*)k_out;
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.q_out_stride = q_out_stride;
+    p.k_out_stride = k_out_stride;
+    p.q_weight = q_weight;
+    p.k_weight = k_weight;
+    p.positions = positions;
+    p.freqs = freqs;
+    p.n_tokens = n_tokens;
+    p.hq = (int32_t)hq;
+    p.hkv = (int32_t)hk;
+    p.d = (int32_t)d;
+    p.rot = cfg->rot_dim;
+    p.interleaved = cfg->interleaved != 0;
+    p.in_bf16 = cfg->in_type == KVARN_TYPE_BF16;
+    p.out_bf16 = cfg->out_type == KVARN_TYPE_BF16;
+    p.eps = cfg->eps;
+    p.heads_per_item = n_tokens * (hq + hk) <= 16384 ? 1 : 4;
+    p.items_per_token = (int32_t)((hq + hk + p.heads_per_item - 1) / p.heads_per_item);
+    const int rc = launch_qk_norm_rope(p, stream);
+    return rc ? cuda_fail(rc, "norm and rotation launch") : KVARN_OK;
+}
+
+}  // extern "C"

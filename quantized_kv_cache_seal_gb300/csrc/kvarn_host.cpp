@@ -15,6 +15,7 @@
 #include <vector>
 
 #include "../../include/kvarn.h"
+#include "kvarn_block.h"
 #include "kvarn_internal.h"
 
 using namespace kvarn;
@@ -48,6 +49,10 @@ bool pair_ok(int kb, int vb) {
 // fills (F = the tail floor in groups; 0 = the published design).
 int64_t groups_sealed(int64_t n, int F) { return n > kSink ? std::max<int64_t>(0, (n - kSink) / kGroup - F) : 0; }
 }  // namespace
+
+namespace kvarn {
+void set_last_error(const char* text) { std::snprintf(g_last_error, sizeof(g_last_error), "%s", text); }
+}  // namespace kvarn
 
 struct kvarn_cache {
     kvarn_config cfg;

@@ -18,6 +18,8 @@ STATUS = {0: "KVARN_OK", 1: "KVARN_EINVAL", 2: "KVARN_ENOMEM", 3: "KVARN_ECAPACI
           5: "KVARN_ESTATE", 6: "KVARN_ETIMEOUT"}
 KVARN_FLAG_HOST_ONLY = 1
 KVARN_FLAG_TEST_STALL = 2
+KVARN_TYPE_F16, KVARN_TYPE_BF16 = 0, 1
+KVARN_CODE_E4M3, KVARN_CODE_INT8 = 0, 1
 
 # every entry point declared in include/kvarn.h
 EXPORTS = [
@@ -27,6 +29,10 @@ EXPORTS = [
     "kvarn_cache_stats", "kvarn_seal_groups", "kvarn_check_device_error", "kvarn_status_string",
     "kvarn_last_error", "kvarn_partition_units", "kvarn_device_accessible", "kvarn_prefill_attention",
     "kvarn_prefill", "kvarn_snapshot_bytes", "kvarn_snapshot_save", "kvarn_snapshot_load",
+    "kvarn_block_required_bytes", "kvarn_block_create", "kvarn_block_destroy", "kvarn_block_append",
+    "kvarn_block_read", "kvarn_block_decode_attention", "kvarn_block_decode_step", "kvarn_block_prefill_attention",
+    "kvarn_block_prefill", "kvarn_block_release", "kvarn_block_length", "kvarn_block_check_device_error",
+    "kvarn_qk_norm_rope",
 ]
 
 
@@ -51,6 +57,18 @@ class kvarn_stats(ctypes.Structure):
         "pool_slots_used", "tokens_cached", "sealed_tokens", "exact_tokens", "sealed_bytes",
         "exact_bytes")] + [("body_bits_per_element", ctypes.c_double),
                            ("all_in_bits_per_element", ctypes.c_double)]
+
+
+class kvarn_block_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "num_layers", "max_seqs", "num_q_heads", "num_kv_heads", "head_dim", "block_tokens", "code", "type",
+        "max_seq_len", "pool_blocks", "flags")]
+
+
+class kvarn_qk_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "num_q_heads", "num_kv_heads", "head_dim", "rot_dim", "interleaved", "in_type", "out_type")] + [
+            ("eps", ctypes.c_float)]
 
 
 _lib = None
@@ -100,6 +118,21 @@ def load(build_if_missing: bool = True):
     L.kvarn_last_error.restype = ctypes.c_char_p
     L.kvarn_partition_units.argtypes = [I32, IP, IP, I32, I32, I32, I32, IP, IP]
     L.kvarn_device_accessible.argtypes = [P, IP]
+    BC = ctypes.POINTER(kvarn_block_config)
+    L.kvarn_block_required_bytes.argtypes = [BC, ctypes.POINTER(SZ)]
+    L.kvarn_block_create.argtypes = [BC, P, SZ, ctypes.POINTER(P)]
+    L.kvarn_block_destroy.argtypes = [P]
+    L.kvarn_block_destroy.restype = None
+    L.kvarn_block_append.argtypes = [P, I32, I32, IP, IP, P, I64, P, I64, P]
+    L.kvarn_block_read.argtypes = [P, I32, I32, IP, IP, IP, P, P, I32, P]
+    L.kvarn_block_decode_attention.argtypes = [P, I32, I32, IP, P, P, F, P]
+    L.kvarn_block_decode_step.argtypes = [P, I32, I32, IP, P, I64, P, I64, P, P, F, P]
+    L.kvarn_block_prefill_attention.argtypes = [P, I32, I32, IP, IP, P, P, F, P]
+    L.kvarn_block_prefill.argtypes = [P, I32, I32, IP, IP, P, I64, P, I64, P, P, F, P]
+    L.kvarn_block_release.argtypes = [P, I32, IP]
+    L.kvarn_block_length.argtypes = [P, I32, I32, ctypes.POINTER(I64)]
+    L.kvarn_block_check_device_error.argtypes = [P, P]
+    L.kvarn_qk_norm_rope.argtypes = [ctypes.POINTER(kvarn_qk_config), I64, P, I64, P, I64, P, P, P, P, P, I64, P, I64, P]
     for name in EXPORTS:
         fn = getattr(L, name)
         if fn.restype is ctypes.c_int:  # default: status enum
@@ -293,3 +326,84 @@ def kvarn_status_string(status: int) -> str:
 
 def kvarn_last_error() -> str:
     return load().kvarn_last_error().decode()
+
+
+def _check_why(rc: int, where: str):
+    """As _check, with the library's reason for any refusal (the block cache and norm calls set one)."""
+    if rc != 0:
+        raise KVarNError(rc, where, load().kvarn_last_error().decode())
+
+
+def kvarn_block_required_bytes(cfg: kvarn_block_config) -> int:
+    n = ctypes.c_size_t()
+    _check_why(load().kvarn_block_required_bytes(ctypes.byref(cfg), ctypes.byref(n)), "kvarn_block_required_bytes")
+    return n.value
+
+
+def kvarn_block_create(cfg: kvarn_block_config, dev_mem, nbytes: int) -> int:
+    h = ctypes.c_void_p()
+    _check_why(load().kvarn_block_create(ctypes.byref(cfg), _ptr(dev_mem), nbytes, ctypes.byref(h)),
+               "kvarn_block_create")
+    return h.value
+
+
+def kvarn_block_destroy(handle: int) -> None:
+    load().kvarn_block_destroy(handle)
+
+
+def kvarn_block_append(handle, layer, seq_ids, n_tokens, k, k_stride, v, v_stride, stream=None):
+    _check_why(load().kvarn_block_append(handle, layer, len(seq_ids), _ints(seq_ids), _ints(n_tokens), _ptr(k),
+                                         k_stride, _ptr(v), v_stride, _stream(stream)), "kvarn_block_append")
+
+
+def kvarn_block_read(handle, layer, seq_ids, starts, counts, k, v, out_fp32=False, stream=None):
+    _check_why(load().kvarn_block_read(handle, layer, len(seq_ids), _ints(seq_ids),
+                                       None if starts is None else _ints(starts), _ints(counts), _ptr(k), _ptr(v),
+                                       int(bool(out_fp32)), _stream(stream)), "kvarn_block_read")
+
+
+def kvarn_block_decode_attention(handle, layer, seq_ids, q, out, softmax_scale, stream=None):
+    _check_why(load().kvarn_block_decode_attention(handle, layer, len(seq_ids), _ints(seq_ids), _ptr(q), _ptr(out),
+                                                   float(softmax_scale), _stream(stream)),
+               "kvarn_block_decode_attention")
+
+
+def kvarn_block_decode_step(handle, layer, seq_ids, k, k_stride, v, v_stride, q, out, softmax_scale, stream=None):
+    _check_why(load().kvarn_block_decode_step(handle, layer, len(seq_ids), _ints(seq_ids), _ptr(k), k_stride, _ptr(v),
+                                              v_stride, _ptr(q), _ptr(out), float(softmax_scale), _stream(stream)),
+               "kvarn_block_decode_step")
+
+
+def kvarn_block_prefill_attention(handle, layer, seq_ids, q_lens, q, out, softmax_scale, stream=None):
+    _check_why(load().kvarn_block_prefill_attention(handle, layer, len(seq_ids), _ints(seq_ids), _ints(q_lens),
+                                                    _ptr(q), _ptr(out), float(softmax_scale), _stream(stream)),
+               "kvarn_block_prefill_attention")
+
+
+def kvarn_block_prefill(handle, layer, seq_ids, n_tokens, k, k_stride, v, v_stride, q, out, softmax_scale,
+                        stream=None):
+    _check_why(load().kvarn_block_prefill(handle, layer, len(seq_ids), _ints(seq_ids), _ints(n_tokens), _ptr(k),
+                                          k_stride, _ptr(v), v_stride, _ptr(q), _ptr(out), float(softmax_scale),
+                                          _stream(stream)), "kvarn_block_prefill")
+
+
+def kvarn_block_release(handle, seq_ids):
+    _check_why(load().kvarn_block_release(handle, len(seq_ids), _ints(seq_ids)), "kvarn_block_release")
+
+
+def kvarn_block_length(handle, layer, seq_id) -> int:
+    n = ctypes.c_int64()
+    _check_why(load().kvarn_block_length(handle, layer, seq_id, ctypes.byref(n)), "kvarn_block_length")
+    return n.value
+
+
+def kvarn_block_check_device_error(handle, stream=None) -> int:
+    return int(load().kvarn_block_check_device_error(handle, _stream(stream)))
+
+
+def kvarn_qk_norm_rope(cfg: kvarn_qk_config, n_tokens, q, q_stride, k, k_stride, q_weight, k_weight, positions, freqs,
+                       q_out, q_out_stride, k_out, k_out_stride, stream=None):
+    _check_why(load().kvarn_qk_norm_rope(ctypes.byref(cfg), n_tokens, _ptr(q), q_stride, _ptr(k), k_stride,
+                                         _ptr(q_weight), _ptr(k_weight), _ptr(positions), _ptr(freqs), _ptr(q_out),
+                                         q_out_stride, _ptr(k_out), k_out_stride, _stream(stream)),
+               "kvarn_qk_norm_rope")
