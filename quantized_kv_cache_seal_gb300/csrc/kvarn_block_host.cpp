@@ -278,7 +278,32 @@ kvarn_status run_prefill(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, co
 
 kvarn_status run_decode(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* ids, const void* q, void* out,
                         float scale, void* stream) {
-    return run_prefill(c, layer, n_seqs, ids, nullptr, q, out, scale, stream);
+    static thread_local BlockDecodeParams p;
+    p.c = c->view;
+    p.c.layer = layer;
+    p.q = (const uint16_t*)q;
+    p.out = (uint16_t*)out;
+    p.n_seqs = n_seqs;
+    p.hq = c->cfg.num_q_heads;
+    p.r = c->r;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    int64_t units = 0;
+    for (int i = 0; i < n_seqs; ++i) {
+        BlockDecodeSeq& e = p.seqs[i];
+        e.seq = ids[i];
+        e.n = c->L(ids[i], layer);
+        e.unit_begin = (int32_t)units;
+        e.units = std::max(1, (e.n + kTileTokens - 1) / kTileTokens);
+        units += (int64_t)e.units * c->cfg.num_kv_heads;
+        if (units >= 1ll << 31) return fail(KVARN_ECAPACITY, "2^31 tiles of 32 tokens or more in a call");
+    }
+    p.units = units;
+    p.grid = (int32_t)std::min<int64_t>(units, std::min(c->sms, kBlockMaxGrid));
+    if (c->host_only) return KVARN_OK;
+    const kvarn_status st = ensure_init(c, stream);
+    if (st) return st;
+    const int rc = launch_block_decode(p, stream);
+    return rc ? cuda_fail(rc, "decode launch") : KVARN_OK;
 }
 
 }  // namespace
