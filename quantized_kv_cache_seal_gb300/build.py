@@ -20,8 +20,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libkvarn.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["kvarn_host.cpp", "kvarn_seal.cu", "kvarn_decode.cu", "kvarn_prefill.cu", "kvarn_block_host.cpp",
-           "kvarn_block.cu", "kvarn_block_attn.cu", "kvarn_block_decode.cu", "kvarn_qk.cu"]
-HEADERS = ["kvarn_internal.h", "kvarn_dev.cuh", "kvarn_block.h", "kvarn_block_dev.cuh"]
+           "kvarn_block.cu", "kvarn_block_decode.cu", "kvarn_block_prefill.cu", "kvarn_qk.cu"]
+HEADERS = ["kvarn_internal.h", "kvarn_dev.cuh", "kvarn_block.h", "kvarn_block_dev.cuh", "kvarn_tc.cuh"]
 
 
 def _nvcc() -> str:

@@ -12,6 +12,7 @@ constexpr int kTileTokens = 32;      // tokens of a code tile; a block is 1, 2 o
 constexpr int kBlockMaxSeqs = 256;   // sequences per call (kernel parameter tables)
 constexpr int kBlockMaxRatio = 8;    // query heads per KV head
 constexpr int kBlockMaxGrid = 256;   // CTAs of a decode launch
+constexpr int kBlockPrefillGrid = 152;  // CTAs of a prefill launch that cuts segments: one a SM
 
 // One code tile: 32 tokens of one KV head, K and V, in the order in which a warp loads the
 // A operands of mma.m16n8k16 (16 bytes a lane, 512 contiguous bytes a load):
@@ -36,7 +37,8 @@ struct BlockLayout {
     size_t err;       // int32[4]
     size_t table;     // int32[max_seqs][num_layers][max_blocks]: pool slot of each sealed block
     size_t counters;  // int32[kBlockMaxGrid]: arrivals at a split (sequence, KV head), zero between calls
-    size_t partials;  // float[kBlockMaxGrid][2][8 (D + 2)]
+    size_t partials;  // float[kBlockMaxGrid][2][8 (D + 2)] of a decode call, or
+                      // float[kBlockPrefillGrid][2][256 (D + 2)] of a prefill call
     size_t tail_k;    // T[max_seqs][num_layers][Hkv][B][D]: exact rows of the partial block
     size_t tail_v;    // T[max_seqs][num_layers][Hkv][D][B]: the same for V, channel-major
     size_t pool;      // slots of Hkv * (B / 32) tiles
@@ -106,14 +108,19 @@ struct BlockDecodeParams {
 
 struct BlockPrefillSeq {
     int32_t seq, n, q_len, q_row;
-    int32_t cta_begin;
+    int32_t pairs;       // pairs of query tiles (256 / r query tokens at most)
+    int32_t cta_begin;   // prefix of pairs * Hkv
+    int32_t step_begin;  // prefix of Hkv * head_steps
+    int32_t head_steps;  // steps of 128 keys over the pairs of one KV head
 };
 struct BlockPrefillParams {
     BlockView c;
     const uint16_t* q;
     uint16_t* out;
     int32_t n_seqs, hq, r, grid;
-    float scale_log2;
+    int32_t line;        // 1: the steps of all segments are cut evenly over the CTAs; 0: a segment a CTA
+    int32_t steps;       // of the whole line
+    float scale_log2;    // softmax scale * log2(e)
     BlockPrefillSeq seqs[kBlockMaxSeqs];
 };
 

@@ -69,7 +69,7 @@ bool make_view(const kvarn_block_config& c, BlockView* v) {
     v->lay.err = take(16);
     v->lay.table = take(seq_layers * v->max_blocks * 4);
     v->lay.counters = take(kBlockMaxGrid * 4);
-    v->lay.partials = take((U)kBlockMaxGrid * 2 * kBlockMaxRatio * (c.head_dim + 2) * 4);
+    v->lay.partials = take((U)std::max(kBlockMaxGrid * kBlockMaxRatio, kBlockPrefillGrid * 256) * 2 * (c.head_dim + 2) * 4);
     v->lay.tail_k = take(tail);
     v->lay.tail_v = take(tail);
     v->lay.pool = take((U)c.pool_blocks * (U)v->slot_bytes);
@@ -254,22 +254,43 @@ kvarn_status run_prefill(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, co
     p.hq = c->cfg.num_q_heads;
     p.r = c->r;
     p.scale_log2 = scale * 1.4426950408889634f;
-    p.n_seqs = p.grid = 0;
+    p.n_seqs = 0;
+    const int hkv = c->cfg.num_kv_heads, pair_tokens = 2 * (128 / c->r);
     int64_t row = 0;
     for (int i = 0; i < n_seqs; ++i) {
-        const int m = q_lens ? q_lens[i] : 1;
-        if (m > 0) {
+        if (q_lens[i] > 0) {
             BlockPrefillSeq& e = p.seqs[p.n_seqs++];
             e.seq = ids[i];
             e.n = c->L(ids[i], layer);
-            e.q_len = m;
+            e.q_len = q_lens[i];
             e.q_row = (int32_t)row;
-            e.cta_begin = p.grid;
-            p.grid += m * p.hq;
         }
-        row += m;
+        row += q_lens[i];
     }
-    if (p.n_seqs == 0 || c->host_only) return KVARN_OK;
+    if (p.n_seqs == 0) return KVARN_OK;
+    // the longest sequences first: their segments are the longest
+    std::sort(p.seqs, p.seqs + p.n_seqs, [](const BlockPrefillSeq& a, const BlockPrefillSeq& b) { return a.n > b.n; });
+    int64_t ctas = 0, steps = 0;
+    for (int i = 0; i < p.n_seqs; ++i) {
+        BlockPrefillSeq& e = p.seqs[i];
+        e.pairs = (e.q_len + pair_tokens - 1) / pair_tokens;
+        e.cta_begin = (int32_t)ctas;
+        e.step_begin = (int32_t)steps;
+        int64_t head = 0;
+        for (int t = 1; t <= e.pairs; ++t)
+            head += (e.n - e.q_len + std::min<int64_t>((int64_t)t * pair_tokens, e.q_len) - 1) / 128 + 1;
+        e.head_steps = (int32_t)head;
+        ctas += (int64_t)e.pairs * hkv;
+        steps += head * hkv;
+        if (steps >= 1ll << 31) return fail(KVARN_ECAPACITY, "2^31 steps of 128 keys or more in a call");
+    }
+    // Enough segments to fill the SMs twice: one a CTA, the longest first. Fewer: the line of all
+    // steps is cut evenly.
+    const int sms = std::min(c->sms, kBlockPrefillGrid);
+    p.line = ctas < 2 * sms;
+    p.steps = (int32_t)steps;
+    p.grid = p.line ? (int32_t)std::min<int64_t>(sms, steps) : (int32_t)ctas;
+    if (c->host_only) return KVARN_OK;
     const kvarn_status st = ensure_init(c, stream);
     if (st) return st;
     const int rc = launch_block_prefill(p, stream);

@@ -64,7 +64,7 @@ def attend(q, k, v, scale, last):
         total = p.sum(-1, keepdim=True)
         p = torch.where(total > 0, p / total, torch.zeros_like(p))
         o[:, h] = p @ vh
-        off = (q[:, h].abs() @ kh.abs().T) * scale * (dim + 8) * 2.0 ** -24
+        off = (q[:, h].abs() @ kh.abs().T) * abs(scale) * (dim + 8) * 2.0 ** -24
         off = torch.where(seen, off, torch.zeros_like(off)).amax(-1, keepdim=True) if n else total
         mass = p @ vh.abs()
         small = n * 2.0 ** -24 * (p * vh.abs().amax(-1)[None]).amax(-1, keepdim=True) if n else total

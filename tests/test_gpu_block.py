@@ -252,6 +252,39 @@ def test_prefill_long(n, m):
     check(out[rows], want, tol, (n, m))
 
 
+def test_prefill_many_segments():
+    """More (sequence, KV head, query tile pair) segments than the SMs hold twice: one a thread block, no cuts."""
+    lens, qlens = [1500, 2100, 40], [1500, 1300, 33]
+    c = make(max_seqs=3, num_q_heads=32, num_kv_heads=4, block_tokens=128, code="int8", dtype=torch.bfloat16)
+    k, v = fill(c, lens, torch.bfloat16, 62)
+    q = tokens(sum(qlens), 32, 128, torch.bfloat16, 64, 0.3)
+    out = c.prefill_attention(0, [0, 1, 2], qlens, q)
+    at = 0
+    for s, (n, m) in enumerate(zip(lens, qlens)):
+        rows = sorted({0, 1, 31, 32, m // 2, m - 1} & set(range(m)))
+        want, tol = block_ref.attend(q[[at + t for t in rows]].cpu(), block_ref.hold(k[s], 128, "int8"),
+                                     block_ref.hold(v[s], 128, "int8"), 128 ** -0.5, [n - m + t for t in rows])
+        check(out[[at + t for t in rows]], want, tol, s)
+        at += m
+
+
+@pytest.mark.parametrize("scale", [-0.05, 0.0, 0.5])
+def test_other_scales(scale):
+    c = make(max_seqs=2, block_tokens=32)
+    lens = [150, 45]
+    k, v = fill(c, lens, torch.float16, 66)
+    q = tokens(50, 8, 128, torch.float16, 68, 0.3)
+    out = c.prefill_attention(0, [0, 1], [20, 30], q, scale=scale)
+    one = c.decode_attention(0, [0, 1], q[[19, 49]].contiguous(), scale=scale)
+    at = 0
+    for s, (n, m) in enumerate(zip(lens, [20, 30])):
+        held = [block_ref.hold(x[s], 32, "e4m3") for x in (k, v)]
+        want, tol = block_ref.attend(q[at:at + m].cpu(), *held, scale, list(range(n - m, n)))
+        check(out[at:at + m], want, tol, s)
+        check(one[s:s + 1], want[-1:], tol[-1:], s)
+        at += m
+
+
 @pytest.mark.parametrize("lens", [[20000], [9000, 40, 3000], [700] * 40])
 def test_decode_split(lens):
     """Long sequences cut over many thread blocks, and many sequences in one."""
