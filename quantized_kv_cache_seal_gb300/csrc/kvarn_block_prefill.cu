@@ -13,12 +13,11 @@
 // bf16 queries after an exact power of two per part or row (what that drops is 2^-39 of the
 // largest).
 //
-// Roles (640 threads): two softmax warpgroups, one a tile, a thread a row; a K and a V
-// warpgroup that turn codes into f16 tiles (K-major, 128-byte swizzle; warp w takes part w,
-// loads a step ahead, two stages); one thread that issues every MMA: PV and the next QK of
-// one tile run while the other tile's softmax does. Both tiles share each expanded K and V
-// tile, which halves the expansion a product costs. Bound by the tensor cores and, close
-// behind, by the softmax's issue slots.
+// Roles (512 threads): two softmax warpgroups, one a tile, a thread a row, its 128 logits in
+// registers; an expansion warpgroup that turns codes into f16 K and V tiles (K-major, 128-byte
+// swizzle, two stages; warp w takes part w of a step); a warp that issues every MMA: PV and the
+// next QK of one tile run while the other tile's softmax does. Both tiles share each
+// expanded K and V tile, which halves the expansion a product costs.
 // Tensor memory (512 columns): S0, S1 (128 each; weights over the first half), O0, O1.
 //
 // Work is laid out in one of two ways. With many segments a CTA takes one each, the longest
@@ -31,9 +30,9 @@
 namespace kvarn {
 namespace {
 
-constexpr int kThreads = 640;
-constexpr int kRegsLaunch = 96, kRegsSoftmax = 136, kRegsExpand = 88, kRegsIssue = 32;
-static_assert(2 * kRegsSoftmax + 2 * kRegsExpand + kRegsIssue <= 5 * kRegsLaunch, "register split");
+constexpr int kThreads = 512;
+constexpr int kRegsLaunch = 128, kRegsSoftmax = 184, kRegsExpand = 104, kRegsIssue = 40;
+static_assert(2 * kRegsSoftmax + kRegsExpand + kRegsIssue <= 4 * kRegsLaunch, "register split");
 constexpr uint32_t kColS = 0, kColO = 256;
 constexpr int kStep = 128;  // keys of a step
 #define kNegInf (-__int_as_float(0x7f800000))
@@ -91,6 +90,18 @@ __device__ __forceinline__ void tm_st16(uint32_t taddr, const uint32_t (&r)[16])
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
+}
+__device__ __forceinline__ void tm_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(ok));
+    return ok != 0;
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
@@ -177,27 +188,32 @@ __device__ __forceinline__ int warp_exponent(uint32_t top) {
     return bf16_exponent(top) - 14;
 }
 
-// ---- the MMA issuer (one thread) ----
+// ---- the MMA issuer ----
+// The whole warp walks and waits, so that addresses stay in uniform registers; one lane issues.
+// (With a single thread walking, each MMA took its operands through vector registers and
+// eight of them about 1,300 clocks to issue; they run in 512.)
 template <int D>
 __device__ __forceinline__ void issue_role(const BlockPrefillParams& p, uint32_t sbase, uint64_t* bars, uint32_t tmem,
                                            int32_t* err) {
     using Sh = Shape<D>;
+    const bool leader = elect_one();
     sbase >>= 4;  // (addresses stay under 2^18: descriptor fields)
     auto qk = [&](int b, int jj) {
         const uint32_t q = sbase + ((Sh::kQ + b * Sh::kTileQ) >> 4), k = sbase + ((Sh::kK + (jj & 1) * Sh::kTileQ) >> 4);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
             const uint32_t off = ((ks >> 2) * Sh::kAtom + (ks & 3) * 32) >> 4;
-            mma_ss(tmem + kColS + 128 * b, desc128(q + off), desc128(k + off), kIdesc<128>, ks > 0);
+            if (leader) mma_ss(tmem + kColS + 128 * b, desc128(q + off), desc128(k + off), kIdesc<128>, ks > 0);
         }
-        mma_commit(bars + kBarSFull + b);
+        if (leader) mma_commit(bars + kBarSFull + b);
     };
     auto pv = [&](int b, int jj, bool first) {
         const uint32_t v = sbase + ((Sh::kV + (jj & 1) * Sh::kTileV) >> 4);
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
-            mma_ts(tmem + kColO + 128 * b, tmem + kColS + 128 * b + 8 * ks,
-                   desc128(v + (((ks >> 2) * (D * 128) + (ks & 3) * 32) >> 4)), kIdesc<D>, (ks > 0 || !first) ? 1u : 0u);
+            if (leader)
+                mma_ts(tmem + kColO + 128 * b, tmem + kColS + 128 * b + 8 * ks,
+                       desc128(v + (((ks >> 2) * (D * 128) + (ks & 3) * 32) >> 4)), kIdesc<D>, (ks > 0 || !first) ? 1u : 0u);
     };
     int jj = 0;
     uint32_t segs = 0, steps = 0;  // bit b: phase of tile b's segments, steps
@@ -212,7 +228,7 @@ __device__ __forceinline__ void issue_role(const BlockPrefillParams& p, uint32_t
         tc_fence_after();
 #pragma unroll 1
         for (int b = 0; b < tiles; ++b) qk(b, jj);
-        mma_commit(bars + kBarKEmpty + (jj & 1));
+        if (leader) mma_commit(bars + kBarKEmpty + (jj & 1));
 #pragma unroll 1
         for (int j = w.j0; j < w.j1; ++j, ++jj) {
             mbar_wait(bars + kBarVFull + (jj & 3), (uint32_t)((jj >> 2) & 1), err);
@@ -223,20 +239,21 @@ __device__ __forceinline__ void issue_role(const BlockPrefillParams& p, uint32_t
                 steps ^= 1u << b;
                 tc_fence_after();
                 pv(b, jj, j == w.j0);
-                if (b == tiles - 1) mma_commit(bars + kBarVEmpty + (jj & 1));
+                if (b == tiles - 1 && leader) mma_commit(bars + kBarVEmpty + (jj & 1));
                 if (more) {
                     if (b == 0) {
                         mbar_wait(bars + kBarKFull + ((jj + 1) & 3), (uint32_t)(((jj + 1) >> 2) & 1), err);
                         tc_fence_after();
                     }
                     qk(b, jj + 1);
-                    if (b == tiles - 1) mma_commit(bars + kBarKEmpty + ((jj + 1) & 1));
-                } else {
+                    if (b == tiles - 1 && leader) mma_commit(bars + kBarKEmpty + ((jj + 1) & 1));
+                } else if (leader) {
                     mma_commit(bars + kBarOFull + b);
                 }
             }
         }
     }
+    if (leader) mma_commit(bars + kBarDrain);
 }
 
 // ---- expansion: one part (32 tokens) a warp ----
@@ -253,150 +270,201 @@ struct StepWalk {
     }
 };
 
-struct Part {
-    const uint8_t* rec;  // its record, or null: exact tokens or none
-    int i, kvh, tile;    // sequence entry, KV head, 32-token tile
-};
+// Non-finite 16-bit values of a word, as the bits of a pair (bit 0, bit 1).
+template <bool BF16>
+__device__ __forceinline__ uint32_t bad_pair(uint32_t w) {
+    constexpr uint32_t e = BF16 ? 0x7f80u : 0x7c00u;
+    return ((w & e) == e ? 1u : 0u) | ((w >> 16 & e) == e ? 2u : 0u);
+}
+// The word with its non-finite values made zero.
+template <bool BF16>
+__device__ __forceinline__ uint32_t finite_only(uint32_t w) {
+    const uint32_t b = bad_pair<BF16>(w);
+    return w & ((b & 1 ? 0u : 0xffffu) | (b & 2 ? 0u : 0xffff0000u));
+}
+template <bool BF16>
+__device__ __forceinline__ uint4 finite_only(uint4 w) {
+    return make_uint4(finite_only<BF16>(w.x), finite_only<BF16>(w.y), finite_only<BF16>(w.z), finite_only<BF16>(w.w));
+}
 
-template <int D, bool INT8, bool BF16, bool IS_V>
+// Exact tokens of a part (none: zeros) as its K or V tile rows. A later token's infinity or NaN
+// must not reach a query that does not see it through 0 x NaN: non-finite V enters as 0, and its
+// token is named in `bad` for the softmax to make visible weights NaN. K needs no such care (logits
+// of unseen tokens are replaced), but neither may set the part's power of two.
+// h: K scale, or log2 and reciprocal of the V scale.
+template <int D, bool BF16, bool IS_V>
+__device__ __forceinline__ void expand_exact(const BlockView& c, const BlockPrefillSeq& e, int kvh, int tile, int wp, int lane,
+                                             uint8_t* dst, float2& h, uint32_t& bad) {
+    const int g = lane >> 2, t = lane & 3;
+    const int first = (tile - (e.n >> c.log2_block << (c.log2_block - 5))) * kTileTokens;  // row of the tail
+    const int nv = min(kTileTokens, e.n - tile * kTileTokens);  // valid tokens, none if <= 0
+    h = IS_V ? make_float2(0.f, 1.f) : make_float2(1.f, 0.f);
+    bad = 0;
+    float f = 1.f;
+    if (IS_V) {
+        const uint16_t* v = tail_ptr(c, c.lay.tail_v, e.seq, kvh) + first;
+        uint32_t keep[4];
+#pragma unroll
+        for (int z = 0; z < 4; ++z)
+            keep[z] = (8 * t + 2 * z < nv ? 0xffffu : 0u) | (8 * t + 2 * z + 1 < nv ? 0xffff0000u : 0u);
+        auto row = [&](int ch) {
+            if (nv <= 0) return make_uint4(0, 0, 0, 0);
+            const uint4 r = *reinterpret_cast<const uint4*>(v + (size_t)ch * c.block + 8 * t);
+            return make_uint4(r.x & keep[0], r.y & keep[1], r.z & keep[2], r.w & keep[3]);
+        };
+        if (BF16) {
+            uint32_t top = 0;
+#pragma unroll 4
+            for (int i = 0; i < D / 8; ++i) top = max_of(top, finite_only<BF16>(row(8 * i + g)));
+            const int ex = warp_exponent(top);
+            f = power2(-ex);
+            h = make_float2((float)ex, f);
+        }
+        uint8_t* atom = dst + (wp >> 1) * (D * 128);
+#pragma unroll 4
+        for (int i = 0; i < D / 8; ++i) {
+            uint4 r = row(8 * i + g);
+            bad |= (bad_pair<BF16>(r.x) | bad_pair<BF16>(r.y) << 2 | bad_pair<BF16>(r.z) << 4 | bad_pair<BF16>(r.w) << 6) << (8 * t);
+            r = finite_only<BF16>(r);
+            if (BF16) r = scaled_f16(r, f);
+            *reinterpret_cast<uint4*>(atom + swz(8 * i + g, 4 * (wp & 1) + t)) = r;
+        }
+        bad = __reduce_or_sync(0xffffffffu, bad);
+    } else {
+        const uint16_t* k = tail_ptr(c, c.lay.tail_k, e.seq, kvh) + (ptrdiff_t)first * D;
+        auto piece = [&](int z) {  // 16 bytes z * 32 + lane of the part's 32 D values
+            const int y = z * 32 + lane, tok = y / (D / 8);
+            if (tok >= nv) return make_uint4(0, 0, 0, 0);
+            return *reinterpret_cast<const uint4*>(k + tok * D + y % (D / 8) * 8);
+        };
+        if (BF16) {
+            uint32_t top = 0;
+#pragma unroll 4
+            for (int z = 0; z < D / 8; ++z) top = max_of(top, finite_only<BF16>(piece(z)));
+            const int ex = warp_exponent(top);
+            f = power2(-ex);
+            h.x = power2(ex);
+        }
+#pragma unroll 4
+        for (int z = 0; z < D / 8; ++z) {
+            uint4 r = piece(z);
+            if (BF16) r = scaled_f16(r, f);
+            const int y = z * 32 + lane, ch8 = y % (D / 8);
+            *reinterpret_cast<uint4*>(dst + (ch8 >> 3) * Shape<D>::kAtom + swz(32 * wp + y / (D / 8), ch8 & 7)) = r;
+        }
+    }
+}
+
+// Warp wp turns part wp of every step into rows of the step's K tile, then of its V tile. Its 16
+// bytes a lane and chunk are reloaded in place: V codes while K's are converted, the next step's K
+// codes while V's are.
+template <int D, bool INT8, bool BF16>
 __device__ __forceinline__ void expand_role(const BlockPrefillParams& p, uint8_t* smem, uint64_t* bars, int32_t* err, int wp,
                                             int lane) {
     using Sh = Shape<D>;
     const BlockView& c = p.c;
     const int g = lane >> 2, t = lane & 3, sh = c.log2_block - 5;
-    constexpr int kChunks = D / 16;  // 512-byte chunks of a part
-    constexpr int kFull = IS_V ? kBarVFull : kBarKFull, kEmpty = IS_V ? kBarVEmpty : kBarKEmpty;
-    constexpr int kRecOff = 16 + (IS_V ? kTileTokens * D : 0);
+    constexpr int kChunks = D / 16;  // 512-byte chunks of a part's K or V
     StepWalk ahead(p, blockIdx.x);
+    // The part of a step: its sequence entry and KV head (head * 256 + entry, -1 behind the last
+    // step), its 32-token tile, with bit 31 set where the tile is exact or not there. The pool slot
+    // is loaded a step before its address is needed.
     int slot = 0;
-    // the part of the step at `ahead`, its slot on the way
-    auto look = [&](Part& x) {
-        x.i = -1;
-        x.rec = nullptr;
+    auto look = [&](int& who, uint32_t& tile) {
+        who = -1;
+        tile = 0x80000000u;
         if (!ahead.valid()) return;
         const BlockPrefillSeq& e = p.seqs[ahead.w.i];
-        x.i = ahead.w.i;
-        x.kvh = ahead.w.kvh;
-        x.tile = 4 * ahead.j + wp;
-        if (x.tile < e.n >> c.log2_block << sh) {
-            slot = __ldg(block_table(c, e.seq) + (x.tile >> sh));
-            x.rec = c.base;  // the address follows when the slot is here
-        }
+        who = ahead.w.kvh * 256 + ahead.w.i;
+        const int x = 4 * ahead.j + wp;
+        tile = (uint32_t)x;
+        if (x < e.n >> c.log2_block << sh) slot = __ldg(block_table(c, e.seq) + (x >> sh));
+        else tile |= 0x80000000u;
         ahead.next();
     };
-    auto address = [&](Part& x) {
-        if (x.rec) x.rec = tile_ptr(c, slot, x.kvh, x.tile & ((1 << sh) - 1));
+    auto address = [&](int who, uint32_t tile) -> const uint8_t* {
+        return tile >> 31 ? nullptr : tile_ptr(c, slot, who >> 8, (int)tile & ((1 << sh) - 1));
     };
+    auto load = [&](const uint8_t* rec, int i) { return __ldg(reinterpret_cast<const uint4*>(rec + 16 + i * 512) + lane); };
     uint4 x[kChunks];
-    float2 hd = make_float2(1.f, 1.f);  // K scale, or log2 and reciprocal of the V scale
-    auto scales = [&](const Part& s) {
-        return IS_V ? __ldg(reinterpret_cast<const float2*>(s.rec + 8)) : make_float2(__ldg(reinterpret_cast<const float*>(s.rec)), 0.f);
-    };
-    auto load = [&](const Part& s, int i) { return __ldg(reinterpret_cast<const uint4*>(s.rec + kRecOff + i * 512) + lane); };
-    Part cur, nxt;
-    look(cur);
-    address(cur);
-    if (cur.rec) {
+    float4 hd = make_float4(1.f, 0.f, 0.f, 1.f);
+    int who, who1;
+    uint32_t tile, tile1;
+    look(who, tile);
+    const uint8_t* rec = address(who, tile);
+    if (rec) {
 #pragma unroll
-        for (int i = 0; i < kChunks; ++i) x[i] = load(cur, i);
-        hd = scales(cur);
+        for (int i = 0; i < kChunks; ++i) x[i] = load(rec, i);
+        hd = __ldg(reinterpret_cast<const float4*>(rec));
     }
-    look(nxt);
-    for (int jj = 0; cur.i >= 0; ++jj) {
-        address(nxt);
-        Part nn;
-        look(nn);
-        if (jj >= 2) mbar_wait(bars + kEmpty + (jj & 1), (uint32_t)(((jj >> 1) - 1) & 1), err);
-        uint8_t* dst = smem + (IS_V ? Sh::kV + (jj & 1) * Sh::kTileV : Sh::kK + (jj & 1) * Sh::kTileQ);
-        float2 h = hd;
-        if (cur.rec) {
+    look(who1, tile1);
+#pragma unroll 1
+    for (int jj = 0; who >= 0; ++jj) {
+        float* head = reinterpret_cast<float*>(smem + Sh::kHdr) + ((jj & 3) * 4 + wp) * 4;
+        float2 h;
+        uint32_t bad = 0;
+        // K
+        if (jj >= 2) mbar_wait(bars + kBarKEmpty + (jj & 1), (uint32_t)(((jj >> 1) - 1) & 1), err);
+        uint8_t* dst = smem + Sh::kK + (jj & 1) * Sh::kTileQ;
+        if (rec) {
+            h = make_float2(hd.x, 0.f);
 #pragma unroll
             for (int i = 0; i < kChunks; ++i) {
                 const uint4 a = make_uint4(codes_lo<INT8>(x[i].x), codes_hi<INT8>(x[i].x), codes_lo<INT8>(x[i].y),
                                            codes_hi<INT8>(x[i].y));
                 const uint4 b = make_uint4(codes_lo<INT8>(x[i].z), codes_hi<INT8>(x[i].z), codes_lo<INT8>(x[i].w),
                                            codes_hi<INT8>(x[i].w));
-                if (nxt.rec) x[i] = load(nxt, i);
-                if (IS_V) {  // 8 tokens of channels 16 i + g and + 8
-                    uint8_t* atom = dst + (wp >> 1) * (D * 128);
-                    const int chunk = 4 * (wp & 1) + t;
-                    *reinterpret_cast<uint4*>(atom + swz(16 * i + g, chunk)) = a;
-                    *reinterpret_cast<uint4*>(atom + swz(16 * i + g + 8, chunk)) = b;
-                } else {  // 16 channels of one token
-                    const int s = i / (D / 32), cc = i / 2 % (D / 64), hh = i & 1;
-                    const int row = 32 * wp + 8 * (g >> 1) + 4 * s + 2 * hh + (g & 1);
-                    *reinterpret_cast<uint4*>(dst + cc * Sh::kAtom + swz(row, 2 * t)) = a;
-                    *reinterpret_cast<uint4*>(dst + cc * Sh::kAtom + swz(row, 2 * t + 1)) = b;
-                }
+                x[i] = load(rec, kChunks + i);
+                // 16 channels of one token
+                const int s = i / (D / 32), cc = i / 2 % (D / 64), hh = i & 1;
+                const int row = 32 * wp + 8 * (g >> 1) + 4 * s + 2 * hh + (g & 1);
+                *reinterpret_cast<uint4*>(dst + cc * Sh::kAtom + swz(row, 2 * t)) = a;
+                *reinterpret_cast<uint4*>(dst + cc * Sh::kAtom + swz(row, 2 * t + 1)) = b;
             }
-            if (nxt.rec) hd = scales(nxt);
         } else {
-            const BlockPrefillSeq& e = p.seqs[cur.i];
-            const int first = (cur.tile - (e.n >> c.log2_block << sh)) * kTileTokens;  // row of the tail
-            const int nv = min(kTileTokens, e.n - cur.tile * kTileTokens);             // valid tokens, none if <= 0
-            h = IS_V ? make_float2(0.f, 1.f) : make_float2(1.f, 0.f);
-            if (IS_V) {
-                const uint16_t* v = tail_ptr(c, c.lay.tail_v, e.seq, cur.kvh) + first;
-                uint32_t keep[4];
-#pragma unroll
-                for (int z = 0; z < 4; ++z)
-                    keep[z] = (8 * t + 2 * z < nv ? 0xffffu : 0u) | (8 * t + 2 * z + 1 < nv ? 0xffff0000u : 0u);
-                auto row = [&](int ch) {
-                    if (nv <= 0) return make_uint4(0, 0, 0, 0);
-                    const uint4 r = *reinterpret_cast<const uint4*>(v + (size_t)ch * c.block + 8 * t);
-                    return make_uint4(r.x & keep[0], r.y & keep[1], r.z & keep[2], r.w & keep[3]);
-                };
-                float f = 1.f;
-                if (BF16) {
-                    uint32_t top = 0;
-                    for (int i = 0; i < 2 * kChunks; ++i) top = max_of(top, row(8 * i + g));
-                    const int ex = warp_exponent(top);
-                    f = power2(-ex);
-                    h = make_float2((float)ex, f);
-                }
-                uint8_t* atom = dst + (wp >> 1) * (D * 128);
-                for (int i = 0; i < 2 * kChunks; ++i) {
-                    uint4 r = row(8 * i + g);
-                    if (BF16) r = scaled_f16(r, f);
-                    *reinterpret_cast<uint4*>(atom + swz(8 * i + g, 4 * (wp & 1) + t)) = r;
-                }
-            } else {
-                const uint16_t* k = tail_ptr(c, c.lay.tail_k, e.seq, cur.kvh) + (size_t)first * D;
-                auto piece = [&](int z) {  // 16 bytes z * 32 + lane of the part's 32 D values
-                    const int at = z * 32 + lane, tok = at / (D / 8);
-                    if (tok >= nv) return make_uint4(0, 0, 0, 0);
-                    return *reinterpret_cast<const uint4*>(k + (size_t)tok * D + at % (D / 8) * 8);
-                };
-                float f = 1.f;
-                if (BF16) {
-                    uint32_t top = 0;
-                    for (int z = 0; z < D / 8; ++z) top = max_of(top, piece(z));
-                    const int ex = warp_exponent(top);
-                    f = power2(-ex);
-                    h.x = power2(ex);
-                }
-                for (int z = 0; z < D / 8; ++z) {
-                    uint4 r = piece(z);
-                    if (BF16) r = scaled_f16(r, f);
-                    const int at = z * 32 + lane, ch8 = at % (D / 8);
-                    *reinterpret_cast<uint4*>(dst + (ch8 >> 3) * Sh::kAtom + swz(32 * wp + at / (D / 8), ch8 & 7)) = r;
-                }
-            }
-            if (nxt.rec) {
-#pragma unroll
-                for (int i = 0; i < kChunks; ++i) x[i] = load(nxt, i);
-                hd = scales(nxt);
-            }
+            expand_exact<D, BF16, false>(c, p.seqs[who & 255], who >> 8, (int)(tile & 0x7fffffffu), wp, lane, dst, h, bad);
         }
-        if (lane == 0) {
-            float* at = reinterpret_cast<float*>(smem + Sh::kHdr) + ((jj & 3) * 4 + wp) * 4;
-            if (IS_V) at[2] = h.x, at[3] = h.y;
-            else at[0] = h.x;
-        }
+        if (lane == 0) head[0] = h.x;
         fence_proxy_async_smem();
-        mbar_arrive(bars + kFull + (jj & 3));
-        cur = nxt;
-        nxt = nn;
+        mbar_arrive(bars + kBarKFull + (jj & 3));
+        // V
+        const uint8_t* rec1 = address(who1, tile1);
+        int who2;
+        uint32_t tile2;
+        look(who2, tile2);
+        if (jj >= 2) mbar_wait(bars + kBarVEmpty + (jj & 1), (uint32_t)(((jj >> 1) - 1) & 1), err);
+        dst = smem + Sh::kV + (jj & 1) * Sh::kTileV;
+        if (rec) {
+            h = make_float2(hd.z, hd.w);
+            uint8_t* atom = dst + (wp >> 1) * (D * 128);
+            const int chunk = 4 * (wp & 1) + t;
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i) {
+                const uint4 a = make_uint4(codes_lo<INT8>(x[i].x), codes_hi<INT8>(x[i].x), codes_lo<INT8>(x[i].y),
+                                           codes_hi<INT8>(x[i].y));
+                const uint4 b = make_uint4(codes_lo<INT8>(x[i].z), codes_hi<INT8>(x[i].z), codes_lo<INT8>(x[i].w),
+                                           codes_hi<INT8>(x[i].w));
+                if (rec1) x[i] = load(rec1, i);
+                // 8 tokens of channels 16 i + g and + 8
+                *reinterpret_cast<uint4*>(atom + swz(16 * i + g, chunk)) = a;
+                *reinterpret_cast<uint4*>(atom + swz(16 * i + g + 8, chunk)) = b;
+            }
+        } else {
+            expand_exact<D, BF16, true>(c, p.seqs[who & 255], who >> 8, (int)(tile & 0x7fffffffu), wp, lane, dst, h, bad);
+            if (rec1) {
+#pragma unroll
+                for (int i = 0; i < kChunks; ++i) x[i] = load(rec1, i);
+            }
+        }
+        if (rec1) hd = __ldg(reinterpret_cast<const float4*>(rec1));
+        if (lane == 0) head[1] = __uint_as_float(bad), head[2] = h.x, head[3] = h.y;
+        fence_proxy_async_smem();
+        mbar_arrive(bars + kBarVFull + (jj & 3));
+        who = who1;
+        tile = tile1;
+        rec = rec1;
+        who1 = who2;
+        tile1 = tile2;
     }
 }
 
@@ -409,7 +477,9 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, uint8_
     const int tpt = 128 / p.r, tok_in = et / p.r, head_in = et % p.r;
     const float4* hdr = reinterpret_cast<const float4*>(smem + Sh::kHdr);
     // a negative scale turns the query's sign, so that larger S is always a larger logit
-    const float scale = fabsf(p.scale_log2);
+    // (and a scale of 0 the query to zeros: every logit is 0)
+    const float scale = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
+    const bool zero = p.scale_log2 == 0.f;
     const uint32_t sign = p.scale_log2 < 0.f ? 0x80008000u : 0u;
     int jj = 0, step = 0, seg = 0;
     for (Walk w(p, blockIdx.x); w.valid(); w.next()) {
@@ -439,7 +509,7 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, uint8_
 #pragma unroll 4
             for (int i = 0; i < D / 8; ++i) {
                 uint4 r = make_uint4(0, 0, 0, 0);
-                if (valid) r = src[i];
+                if (valid && !zero) r = src[i];
                 if (BF16) r = scaled_f16(r, f);
                 r = make_uint4(r.x ^ sign, r.y ^ sign, r.z ^ sign, r.w ^ sign);
                 *reinterpret_cast<uint4*>(dst + (i >> 3) * Sh::kAtom + swz(et, i & 7)) = r;
@@ -456,32 +526,51 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, uint8_
             mbar_wait(bars + kBarVFull + (jj & 3), (uint32_t)((jj >> 2) & 1), err);
             tc_fence_after();
             const int lim = pos + 1 - j * kStep;  // visible columns
-            const bool all = __all_sync(0xffffffffu, lim >= kStep);
+            uint32_t r[4][32];
+#pragma unroll
+            for (int ch = 0; ch < 4; ++ch) tm_ld32(ts + 32 * ch, r[ch]);
+            // logit = S c[ch] (+ log2 of V's scale in the weight); c > 0 or NaN
+            float c[4], lv[4], iv[4];
+            uint32_t bad = 0;
+#pragma unroll
+            for (int ch = 0; ch < 4; ++ch) {
+                const float4 h = hdr[(jj & 3) * 4 + ch];
+                c[ch] = qs * h.x;
+                if (c[ch] < 1e-37f) c[ch] = 1e-37f;  // 0 would make -inf of a masked column NaN
+                lv[ch] = h.z;
+                iv[ch] = h.w;
+                bad |= __float_as_uint(h.y);
+            }
+            tm_wait_ld();
+            if (bad) {  // (a part's non-finite V tokens: their weights are NaN where seen)
+#pragma unroll
+                for (int ch = 0; ch < 4; ++ch) {
+                    const uint32_t y = __float_as_uint(hdr[(jj & 3) * 4 + ch].y);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        if (y >> k & 1) r[ch][k] = 0x7fc00000u;
+                }
+            }
+            if (__any_sync(0xffffffffu, lim < kStep)) {
+#pragma unroll
+                for (int ch = 0; ch < 4; ++ch) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        if (32 * ch + k >= lim) r[ch][k] = 0xff800000u;
+                    if (32 * ch >= lim) c[ch] = 1.f, lv[ch] = 0.f, iv[ch] = 1.f;  // nothing of a part that is not seen at all
+                }
+            }
             float mx = kNegInf;
 #pragma unroll
-            for (int ch = 0; ch < 4; ch += 2) {
-                uint32_t r[2][32];
-                tm_ld32(ts + 32 * ch, r[0]);
-                tm_ld32(ts + 32 * ch + 32, r[1]);
-                tm_wait_ld();
+            for (int ch = 0; ch < 4; ++ch) {
+                float a = __uint_as_float(r[ch][0]), a2 = __uint_as_float(r[ch][1]);
 #pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                    const float4 h = hdr[(jj & 3) * 4 + ch + z];
-                    float a = kNegInf, a2 = kNegInf;
-                    if (all) {
-#pragma unroll
-                        for (int k = 0; k < 32; k += 4) {
-                            a = max3(a, __uint_as_float(r[z][k]), __uint_as_float(r[z][k + 1]));
-                            a2 = max3(a2, __uint_as_float(r[z][k + 2]), __uint_as_float(r[z][k + 3]));
-                        }
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            if (32 * (ch + z) + k < lim) a = fmaxf(a, __uint_as_float(r[z][k]));
-                    }
-                    a = fmaxf(a, a2);
-                    if (a > kNegInf) mx = fmaxf(mx, fmaf(a, qs * h.x, h.z));
+                for (int k = 2; k < 30; k += 4) {
+                    a = max3(a, __uint_as_float(r[ch][k]), __uint_as_float(r[ch][k + 1]));
+                    a2 = max3(a2, __uint_as_float(r[ch][k + 2]), __uint_as_float(r[ch][k + 3]));
                 }
+                a = max3(a, __uint_as_float(r[ch][30]), __uint_as_float(r[ch][31]));
+                mx = fmaxf(mx, fmaf(fmaxf(a, a2), c[ch], lv[ch]));
             }
             const bool up = mx > m + 8.f;  // also from -inf
             if (__any_sync(0xffffffffu, up)) {
@@ -489,46 +578,37 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, uint8_
                 if (up) m = mx;
                 l *= f;
                 if (j > w.j0) {
+                    // O is rescaled 16 columns at a time: the 128 logits stay in registers
 #pragma unroll 1
-                    for (int ch = 0; ch < D / 32; ++ch) {
-                        uint32_t r[32];
-                        tm_ld32(to + 32 * ch, r);
+                    for (int ch = 0; ch < D / 16; ++ch) {
+                        uint32_t o[16];
+                        tm_ld16(to + 16 * ch, o);
                         tm_wait_ld();
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * f);
-                        tm_st32(to + 32 * ch, r);
+                        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                        tm_st16(to + 16 * ch, o);
                     }
                 }
             }
             const float mm = m == kNegInf ? 0.f : m;
 #pragma unroll
-            for (int ch = 0; ch < 4; ch += 2) {
-                uint32_t r[2][32];
-                tm_ld32(ts + 32 * ch, r[0]);
-                tm_ld32(ts + 32 * ch + 32, r[1]);
-                tm_wait_ld();
+            for (int ch = 0; ch < 4; ++ch) {
+                const float ad = lv[ch] - mm;
+                const float2 c2 = make_float2(c[ch], c[ch]), a2 = make_float2(ad, ad);
+                float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+                uint32_t o[16];
 #pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                    const float4 h = hdr[(jj & 3) * 4 + ch + z];
-                    const float cc = qs * h.x, ad = h.z - mm;
-                    const float2 c2 = make_float2(cc, cc), a2 = make_float2(ad, ad);
-                    float2 sum = make_float2(0.f, 0.f);
-                    uint32_t o[16];
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        const float2 x =
-                            __ffma2_rn(make_float2(__uint_as_float(r[z][2 * k]), __uint_as_float(r[z][2 * k + 1])), c2, a2);
-                        float2 y = make_float2(ex2f(x.x), ex2f(x.y));
-                        if (!all) {
-                            if (32 * (ch + z) + 2 * k >= lim) y.x = 0.f;
-                            if (32 * (ch + z) + 2 * k + 1 >= lim) y.y = 0.f;
-                        }
-                        sum = __fadd2_rn(sum, y);
-                        o[k] = h2u(__float22half2_rn(y));
-                    }
-                    l = fmaf(sum.x + sum.y, h.w, l);
-                    tm_st16(ts + 16 * (ch + z), o);
+                for (int k = 0; k < 16; ++k) {
+                    const float2 x =
+                        __ffma2_rn(make_float2(__uint_as_float(r[ch][2 * k]), __uint_as_float(r[ch][2 * k + 1])), c2, a2);
+                    const float2 y = make_float2(ex2f(x.x), ex2f(x.y));
+                    if (k & 1) s1 = __fadd2_rn(s1, y);
+                    else s0 = __fadd2_rn(s0, y);
+                    o[k] = h2u(__float22half2_rn(y));
                 }
+                s0 = __fadd2_rn(s0, s1);
+                l = fmaf(s0.x + s0.y, iv[ch], l);
+                tm_st16(ts + 16 * ch, o);
             }
             tm_wait_st();
             tc_fence_before();
@@ -603,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         mbar_init(bars + kBarDrain, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (w == 16) {
+    if (w == 12) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(smem + Sh::kTmem))
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -618,16 +698,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         softmax_role<D, BF16>(p, smem, bars, tmem, err, t & 127, wg, lane_off);
     } else if (wg == 2) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsExpand));
-        expand_role<D, INT8, BF16, false>(p, smem, bars, err, w & 3, lane);
-    } else if (wg == 3) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsExpand));
-        expand_role<D, INT8, BF16, true>(p, smem, bars, err, w & 3, lane);
+        expand_role<D, INT8, BF16>(p, smem, bars, err, w & 3, lane);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-        if (w == 16 && lane == 0) {
+        if (w == 12) {
             issue_role<D>(p, smem_addr(smem), bars, tmem, err);
             // every MMA has completed before tensor memory is released
-            mma_commit(bars + kBarDrain);
             const uint64_t t0 = global_ns();
             while (!mbar_try_wait(bars + kBarDrain, 0u) && global_ns() - t0 < kWaitLimitNs) {
             }
@@ -636,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (w == 16) {
+    if (w == 12) {
         __syncwarp();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     }

@@ -363,6 +363,37 @@ def test_nan_reaches_its_head_only(code):
         assert bool(torch.isfinite(out[2, :4]).all()) and bool(out[2, 4:].isnan().all())
 
 
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("at", [70, 190, 212])
+@pytest.mark.parametrize("side", ["k", "v"])
+def test_nan_of_a_later_token_stays_there(dtype, at, side):
+    """A NaN or infinity at position `at` (sealed blocks up to 191, then the tail): queries before its block, or
+    before the token itself where it is still exact, are as without it; later ones are NaN."""
+    dt = TYPES[dtype]
+    n, m = 220, 200
+    k, v = (tokens(n, 1, 128, dt, s) for s in (100, 101))
+    q = tokens(m, 4, 128, dt, 102, 0.3)
+    outs = []
+    for value in (None, float("nan"), float("inf")):
+        x, y = k.clone(), v.clone()
+        if value is not None:
+            (x if side == "k" else y)[at, 0, 3] = value
+        c = make(num_q_heads=4, num_kv_heads=1, block_tokens=64, dtype=dt, max_seqs=1)
+        c.append(0, [0], [n], x, y)
+        outs.append(c.prefill_attention(0, [0], [m], q))
+    first = at if at >= 192 else at // 64 * 64  # the first token that is not finite in the cache
+    rows = slice(0, first - (n - m))
+    want, tol = block_ref.attend(q[rows].cpu(), block_ref.hold(k[:first], 64, "e4m3"), block_ref.hold(v[:first], 64, "e4m3"),
+                                 128 ** -0.5, list(range(n - m, first)))
+    for out in outs:
+        check(out[rows], want, tol, (at, side))
+    assert bool(torch.isfinite(outs[0]).all())
+    channels = slice(0, 128) if side == "k" or at < 192 else slice(3, 4)
+    assert bool(outs[1][first - (n - m):, :, channels].isnan().all())
+    if at < 192:
+        assert bool(outs[2][first - (n - m):].isnan().all())
+
+
 def test_streams_and_graphs():
     """Calls on another stream; decode, prefill and read captured and replayed with new queries; calls that change
     the cache refused while capturing."""
