@@ -37,8 +37,9 @@ constexpr uint32_t kColS = 0, kColO = 256;
 constexpr int kStep = 128;  // keys of a step
 #define kNegInf (-__int_as_float(0x7f800000))
 
-constexpr int kBarKFull = 0, kBarVFull = 4, kBarKEmpty = 8, kBarVEmpty = 10, kBarSFull = 12, kBarPFull = 14, kBarOFull = 16,
-              kBarQFull = 18, kBarDrain = 20, kNumBars = 21;
+// p_full: by tile, two halves of 64 keys each (2 b + half)
+constexpr int kBarKFull = 0, kBarVFull = 4, kBarKEmpty = 8, kBarVEmpty = 10, kBarSFull = 12, kBarPFull = 14, kBarOFull = 18,
+              kBarQFull = 20, kBarDrain = 22, kNumBars = 23;
 
 template <int D>
 struct Shape {
@@ -102,6 +103,20 @@ __device__ __forceinline__ bool elect_one() {
     uint32_t ok;
     asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(ok));
     return ok != 0;
+}
+// mbar_wait for the waits that every step's latency goes through: polls without suspending first.
+__device__ __forceinline__ void mbar_spin(uint64_t* bar, uint32_t parity, int32_t* err) {
+    for (int i = 0; i < 1024; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n"
+            " selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok)
+            : "r"(smem_addr(bar)), "r"(parity)
+            : "memory");
+        if (ok) return;
+    }
+    mbar_wait(bar, parity, err);
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
@@ -207,13 +222,13 @@ __device__ __forceinline__ void issue_role(const BlockPrefillParams& p, uint32_t
         }
         if (leader) mma_commit(bars + kBarSFull + b);
     };
-    auto pv = [&](int b, int jj, bool first) {
-        const uint32_t v = sbase + ((Sh::kV + (jj & 1) * Sh::kTileV) >> 4);
+    auto pv = [&](int b, int jj, int half, uint32_t acc) {  // 64 keys
+        const uint32_t v = sbase + ((Sh::kV + (jj & 1) * Sh::kTileV + half * (D * 128)) >> 4);
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
+        for (int ks = 0; ks < 4; ++ks)
             if (leader)
-                mma_ts(tmem + kColO + 128 * b, tmem + kColS + 128 * b + 8 * ks,
-                       desc128(v + (((ks >> 2) * (D * 128) + (ks & 3) * 32) >> 4)), kIdesc<D>, (ks > 0 || !first) ? 1u : 0u);
+                mma_ts(tmem + kColO + 128 * b, tmem + kColS + 128 * b + 32 * half + 8 * ks, desc128(v + 2 * ks), kIdesc<D>,
+                       ks > 0 ? 1u : acc);
     };
     int jj = 0;
     uint32_t segs = 0, steps = 0;  // bit b: phase of tile b's segments, steps
@@ -235,10 +250,13 @@ __device__ __forceinline__ void issue_role(const BlockPrefillParams& p, uint32_t
             const bool more = j + 1 < w.j1;
 #pragma unroll 1
             for (int b = 0; b < tiles; ++b) {
-                mbar_wait(bars + kBarPFull + b, steps >> b & 1, err);
+                mbar_spin(bars + kBarPFull + 2 * b, steps >> b & 1, err);
+                tc_fence_after();
+                pv(b, jj, 0, j > w.j0 ? 1u : 0u);
+                mbar_spin(bars + kBarPFull + 2 * b + 1, steps >> b & 1, err);
                 steps ^= 1u << b;
                 tc_fence_after();
-                pv(b, jj, j == w.j0);
+                pv(b, jj, 1, 1u);
                 if (b == tiles - 1 && leader) mma_commit(bars + kBarVEmpty + (jj & 1));
                 if (more) {
                     if (b == 0) {
@@ -519,16 +537,12 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, uint8_
         mbar_arrive(bars + kBarQFull + b);
         float m = kNegInf, l = 0.f;
         for (int j = w.j0; j < w.j1; ++j, ++jj, ++step) {
-            // S first: a tile that sat out a segment may be whole phases ahead of the expansion,
-            // and once this step's QK is done both barriers are at this step's phase or the one before
-            mbar_wait(bars + kBarSFull + b, (uint32_t)(step & 1), err);
+            // A tile that sat out a segment may be whole phases ahead of the expansion; once its first
+            // step's QK is done both barriers are at that step's phase or the one before. Within a
+            // segment they are waited for first, and the headers read, while QK runs.
+            if (j == w.j0) mbar_wait(bars + kBarSFull + b, (uint32_t)(step & 1), err);
             mbar_wait(bars + kBarKFull + (jj & 3), (uint32_t)((jj >> 2) & 1), err);
             mbar_wait(bars + kBarVFull + (jj & 3), (uint32_t)((jj >> 2) & 1), err);
-            tc_fence_after();
-            const int lim = pos + 1 - j * kStep;  // visible columns
-            uint32_t r[4][32];
-#pragma unroll
-            for (int ch = 0; ch < 4; ++ch) tm_ld32(ts + 32 * ch, r[ch]);
             // logit = S c[ch] (+ log2 of V's scale in the weight); c > 0 or NaN
             float c[4], lv[4], iv[4];
             uint32_t bad = 0;
@@ -541,28 +555,12 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, uint8_
                 iv[ch] = h.w;
                 bad |= __float_as_uint(h.y);
             }
-            tm_wait_ld();
-            if (bad) {  // (a part's non-finite V tokens: their weights are NaN where seen)
-#pragma unroll
-                for (int ch = 0; ch < 4; ++ch) {
-                    const uint32_t y = __float_as_uint(hdr[(jj & 3) * 4 + ch].y);
-#pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        if (y >> k & 1) r[ch][k] = 0x7fc00000u;
-                }
-            }
-            if (__any_sync(0xffffffffu, lim < kStep)) {
-#pragma unroll
-                for (int ch = 0; ch < 4; ++ch) {
-#pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        if (32 * ch + k >= lim) r[ch][k] = 0xff800000u;
-                    if (32 * ch >= lim) c[ch] = 1.f, lv[ch] = 0.f, iv[ch] = 1.f;  // nothing of a part that is not seen at all
-                }
-            }
+            mbar_spin(bars + kBarSFull + b, (uint32_t)(step & 1), err);
+            tc_fence_after();
+            const int lim = pos + 1 - j * kStep;  // visible columns
+            uint32_t r[4][32];
             float mx = kNegInf;
-#pragma unroll
-            for (int ch = 0; ch < 4; ++ch) {
+            auto raise = [&](int ch) {
                 float a = __uint_as_float(r[ch][0]), a2 = __uint_as_float(r[ch][1]);
 #pragma unroll
                 for (int k = 2; k < 30; k += 4) {
@@ -571,6 +569,35 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, uint8_
                 }
                 a = max3(a, __uint_as_float(r[ch][30]), __uint_as_float(r[ch][31]));
                 mx = fmaxf(mx, fmaf(fmaxf(a, a2), c[ch], lv[ch]));
+            };
+            const bool plain = !bad && __all_sync(0xffffffffu, lim >= kStep);
+            tm_ld32(ts, r[0]);
+            tm_ld32(ts + 32, r[1]);
+            tm_wait_ld();
+            tm_ld32(ts + 64, r[2]);
+            tm_ld32(ts + 96, r[3]);
+            if (plain) {  // over the loads' latency
+                raise(0);
+                raise(1);
+            }
+            tm_wait_ld();
+            if (plain) {
+                raise(2);
+                raise(3);
+            } else {
+                // non-finite V tokens' weights become NaN where they are seen; then columns behind the
+                // row's position leave, with all of a part that is not seen at all
+#pragma unroll
+                for (int ch = 0; ch < 4; ++ch) {
+                    const uint32_t y = __float_as_uint(hdr[(jj & 3) * 4 + ch].y);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        if (y >> k & 1) r[ch][k] = 0x7fc00000u;
+                        if (32 * ch + k >= lim) r[ch][k] = 0xff800000u;
+                    }
+                    if (32 * ch >= lim) c[ch] = 1.f, lv[ch] = 0.f, iv[ch] = 1.f;
+                    raise(ch);
+                }
             }
             const bool up = mx > m + 8.f;  // also from -inf
             if (__any_sync(0xffffffffu, up)) {
@@ -609,10 +636,12 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, uint8_
                 s0 = __fadd2_rn(s0, s1);
                 l = fmaf(s0.x + s0.y, iv[ch], l);
                 tm_st16(ts + 16 * ch, o);
+                if (ch & 1) {  // 64 keys: their PV may start
+                    tm_wait_st();
+                    tc_fence_before();
+                    mbar_arrive(bars + kBarPFull + 2 * b + (ch >> 1));
+                }
             }
-            tm_wait_st();
-            tc_fence_before();
-            mbar_arrive(bars + kBarPFull + b);
         }
         mbar_wait(bars + kBarOFull + b, (uint32_t)(seg++ & 1), err);
         tc_fence_after();
@@ -677,6 +706,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             mbar_init(bars + kBarVEmpty + k, 1);
             mbar_init(bars + kBarSFull + k, 1);
             mbar_init(bars + kBarPFull + k, 128);
+            mbar_init(bars + kBarPFull + 2 + k, 128);
             mbar_init(bars + kBarOFull + k, 1);
             mbar_init(bars + kBarQFull + k, 128);
         }
