@@ -36,7 +36,8 @@ KVARN_HD inline int v_code_off(int d, int tok, int ch) {
 struct BlockLayout {
     size_t err;       // int32[4]
     size_t table;     // int32[max_seqs][num_layers][max_blocks]: pool slot of each sealed block
-    size_t counters;  // int32[kBlockMaxGrid]: arrivals at a split (sequence, KV head), zero between calls
+    size_t counters;  // int32[kBlockMaxGrid], zero between calls: arrivals at a split (sequence, KV head) of a
+                      // decode call; segments taken and CTAs done of a prefill call
     size_t partials;  // float[kBlockMaxGrid][2][8 (D + 2)] of a decode call, or
                       // float[kBlockPrefillGrid][2][256 (D + 2)] of a prefill call
     size_t tail_k;    // T[max_seqs][num_layers][Hkv][B][D]: exact rows of the partial block
@@ -109,7 +110,7 @@ struct BlockDecodeParams {
 struct BlockPrefillSeq {
     int32_t seq, n, q_len, q_row;
     int32_t pairs;       // pairs of query tiles (256 / r query tokens at most)
-    int32_t cta_begin;   // prefix of pairs * Hkv
+    int32_t seg_begin;   // prefix of pairs * Hkv: segments
     int32_t step_begin;  // prefix of Hkv * head_steps
     int32_t head_steps;  // steps of 128 keys over the pairs of one KV head
 };
@@ -118,8 +119,8 @@ struct BlockPrefillParams {
     const uint16_t* q;
     uint16_t* out;
     int32_t n_seqs, hq, r, grid;
-    int32_t line;        // 1: the steps of all segments are cut evenly over the CTAs; 0: a segment a CTA
-    int32_t steps;       // of the whole line
+    int32_t line;        // 1: the steps of all segments are cut evenly over the CTAs; 0: CTAs take whole segments
+    int32_t steps, segs; // of all sequences and KV heads
     float scale_log2;    // softmax scale * log2(e)
     BlockPrefillSeq seqs[kBlockMaxSeqs];
 };

@@ -79,6 +79,7 @@ struct Cursor {
     int i, h, begin, end;
     __device__ __forceinline__ void start(const BlockDecodeParams& p, int u) {
         int lo = 0;
+#pragma unroll 1
         for (int hi = p.n_seqs - 1; lo < hi;) {
             const int mid = (lo + hi + 1) / 2;
             if (p.seqs[mid].unit_begin <= u) lo = mid; else hi = mid - 1;
@@ -388,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
             const int tile = u - cur.begin;
             if (tile < sealed) {
                 const int s = done % Sh::kStages;
-                mbar_wait(bars + s, (uint32_t)(done / Sh::kStages & 1), err);
+                bar_wait(bars + s, (uint32_t)(done / Sh::kStages & 1), err);
                 sealed_unit<D, INT8>(st, ring + s * Sh::kTile, q, c0, c1, lane);
                 ++done;
                 __syncwarp();

@@ -69,6 +69,22 @@ __device__ __forceinline__ uint32_t codes_hi(uint32_t w) {
     return r;
 }
 
+// mbar_wait with its loop kept rolled: an unrolled one costs 2 KB of code at every place, and the
+// kernels here have to fit the instruction cache.
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, int32_t* err) {
+    if (__builtin_expect(mbar_try_wait(bar, parity), 1)) return true;
+    if (*reinterpret_cast<volatile int32_t*>(err) & kErrTimeout) return false;
+    const uint64_t t0 = global_ns();
+#pragma unroll 1
+    while (!mbar_try_wait(bar, parity)) {
+        if (global_ns() - t0 > kWaitLimitNs) {
+            atomicOr(err, kErrTimeout);
+            return false;
+        }
+    }
+    return true;
+}
+
 // Bytes of a 4 x 4 square: r[i] = row i; afterwards r[j] = column j.
 __device__ __forceinline__ void transpose4(uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
     const uint32_t a = __byte_perm(r0, r1, 0x5140), b = __byte_perm(r0, r1, 0x7362);

@@ -270,26 +270,27 @@ kvarn_status run_prefill(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, co
     if (p.n_seqs == 0) return KVARN_OK;
     // the longest sequences first: their segments are the longest
     std::sort(p.seqs, p.seqs + p.n_seqs, [](const BlockPrefillSeq& a, const BlockPrefillSeq& b) { return a.n > b.n; });
-    int64_t ctas = 0, steps = 0;
+    int64_t segs = 0, steps = 0;
     for (int i = 0; i < p.n_seqs; ++i) {
         BlockPrefillSeq& e = p.seqs[i];
         e.pairs = (e.q_len + pair_tokens - 1) / pair_tokens;
-        e.cta_begin = (int32_t)ctas;
+        e.seg_begin = (int32_t)segs;
         e.step_begin = (int32_t)steps;
         int64_t head = 0;
         for (int t = 1; t <= e.pairs; ++t)
             head += (e.n - e.q_len + std::min<int64_t>((int64_t)t * pair_tokens, e.q_len) - 1) / 128 + 1;
         e.head_steps = (int32_t)head;
-        ctas += (int64_t)e.pairs * hkv;
+        segs += (int64_t)e.pairs * hkv;
         steps += head * hkv;
         if (steps >= 1ll << 31) return fail(KVARN_ECAPACITY, "2^31 steps of 128 keys or more in a call");
     }
-    // Enough segments to fill the SMs twice: one a CTA, the longest first. Fewer: the line of all
-    // steps is cut evenly.
+    // Enough segments to fill the SMs twice: the CTAs take whole ones, the longest first. Fewer:
+    // the line of all steps is cut evenly.
     const int sms = std::min(c->sms, kBlockPrefillGrid);
-    p.line = ctas < 2 * sms;
+    p.line = segs < 2 * sms;
     p.steps = (int32_t)steps;
-    p.grid = p.line ? (int32_t)std::min<int64_t>(sms, steps) : (int32_t)ctas;
+    p.segs = (int32_t)segs;
+    p.grid = (int32_t)std::min<int64_t>(sms, steps);
     if (c->host_only) return KVARN_OK;
     const kvarn_status st = ensure_init(c, stream);
     if (st) return st;

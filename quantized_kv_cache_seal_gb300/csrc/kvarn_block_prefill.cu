@@ -16,13 +16,14 @@
 // Roles (512 threads): two softmax warpgroups, one a tile, a thread a row, its 128 logits in
 // registers; an expansion warpgroup that turns codes into f16 K and V tiles (K-major, 128-byte
 // swizzle, two stages; warp w takes part w of a step); a warp that issues every MMA: PV and the
-// next QK of one tile run while the other tile's softmax does. Both tiles share each
-// expanded K and V tile, which halves the expansion a product costs.
+// next QK of one tile run while the other tile's softmax does; one that hands out segments.
+// Both tiles share each expanded K and V tile, which halves the expansion a product costs.
 // Tensor memory (512 columns): S0, S1 (128 each; weights over the first half), O0, O1.
 //
-// Work is laid out in one of two ways. With many segments a CTA takes one each, the longest
-// first. With few, all steps form one line cut evenly over the CTAs; a segment that crosses
-// a cut leaves partial O, m, l in the workspace and a second kernel adds them in order.
+// Work is laid out in one of two ways, on one CTA a SM. With many segments the CTAs take whole
+// ones, the longest first, from a counter. With few, all steps form one line cut evenly over the
+// CTAs; a segment that crosses a cut leaves partial O, m, l in the workspace and a second kernel
+// adds them in order. Either way a CTA's expansion runs on into its next segment.
 // Every wait is bounded (2 s) and sets the error word when it gives up.
 #include "kvarn_block_dev.cuh"
 #include "kvarn_tc.cuh"
@@ -37,9 +38,11 @@ constexpr uint32_t kColS = 0, kColO = 256;
 constexpr int kStep = 128;  // keys of a step
 #define kNegInf (-__int_as_float(0x7f800000))
 
-// p_full: by tile, two halves of 64 keys each (2 b + half)
+// p_full: by tile, two halves of 64 keys each (2 b + half); feed: segments handed to the roles
+constexpr int kFeed = 8;
 constexpr int kBarKFull = 0, kBarVFull = 4, kBarKEmpty = 8, kBarVEmpty = 10, kBarSFull = 12, kBarPFull = 14, kBarOFull = 18,
-              kBarQFull = 20, kBarDrain = 22, kNumBars = 23;
+              kBarQFull = 20, kBarDrain = 22, kBarTake = 23, kBarFeedFull = 24, kBarFeedEmpty = kBarFeedFull + kFeed,
+              kNumBars = kBarFeedEmpty + kFeed;
 
 template <int D>
 struct Shape {
@@ -51,8 +54,10 @@ struct Shape {
     static constexpr int kTileV = 2 * D * 128;
     static constexpr int kHdr = kV + 2 * kTileV;        // float4[4][4]: by step % 4 and part
     static constexpr int kBars = kHdr + 4 * 4 * 16;
-    static constexpr int kTmem = kBars + 8 * kNumBars;
-    static constexpr int kSmem = kTmem + 16 + 1024;     // slack to start on 1024 bytes
+    static constexpr int kFeedAt = kBars + 8 * kNumBars;  // Seg[kFeed], where Walk looks for it
+    static constexpr int kTmem = kFeedAt + 32 * kFeed;
+    static_assert(kFeedAt % 16 == 0, "entries are read 16 bytes at a time");
+    static constexpr int kSmem = kTmem + 16;
     static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
 };
 
@@ -104,24 +109,20 @@ __device__ __forceinline__ bool elect_one() {
     asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(ok));
     return ok != 0;
 }
-// mbar_wait for the waits that every step's latency goes through: polls without suspending first.
-__device__ __forceinline__ void mbar_spin(uint64_t* bar, uint32_t parity, int32_t* err) {
-    for (int i = 0; i < 1024; ++i) {
-        uint32_t ok;
-        asm volatile(
-            "{\n .reg .pred p;\n mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n"
-            " selp.u32 %0, 1, 0, p;\n}\n"
-            : "=r"(ok)
-            : "r"(smem_addr(bar)), "r"(parity)
-            : "memory");
-        if (ok) return;
-    }
-    mbar_wait(bar, parity, err);
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
+}
+
+__device__ __forceinline__ float max32(const uint32_t (&r)[32]) {
+    float a = __uint_as_float(r[0]), b = __uint_as_float(r[1]);
+#pragma unroll
+    for (int k = 2; k < 30; k += 4) {
+        a = max3(a, __uint_as_float(r[k]), __uint_as_float(r[k + 1]));
+        b = max3(b, __uint_as_float(r[k + 2]), __uint_as_float(r[k + 3]));
+    }
+    return fmaxf(max3(a, __uint_as_float(r[30]), __uint_as_float(r[31])), b);
 }
 
 // ---- the line of steps ----
@@ -130,57 +131,112 @@ __device__ __forceinline__ int pair_steps(const BlockPrefillSeq& e, int pair, in
     return (e.n - e.q_len + min((pair + 1) * pair_tokens, e.q_len) - 1) / kStep + 1;
 }
 
-// The segments (steps [j0, j1) of each) of CTA b in order.
-struct Walk {
+// A segment: sequence entry, KV head, tile pair, its steps and the part [j0, j1) of them to take
+// (j1 = 0: no more); whether its second tile has rows.
+struct Seg {
+    int i, kvh, pair, steps, j0, j1, two, pad;
+};
+
+// The segments of CTA b's range of the line, in order.
+struct LineWalk {
     const BlockPrefillParams& p;
-    int pt, left;  // query tokens of a pair; steps of this CTA behind this segment's j0
-    int i, kvh, pair, steps, j0, j1;
-    __device__ __forceinline__ Walk(const BlockPrefillParams& p_, int b) : p(p_) {
-        pt = 2 * (128 / p.r);
-        int lo = 0, rel;
-        if (!p.line) {
-            for (int hi = p.n_seqs - 1; lo < hi;) {
-                const int mid = (lo + hi + 1) / 2;
-                if (p.seqs[mid].cta_begin <= b) lo = mid; else hi = mid - 1;
-            }
-            i = lo;
-            rel = b - p.seqs[i].cta_begin;
-            kvh = rel % p.c.hkv;
-            pair = p.seqs[i].pairs - 1 - rel / p.c.hkv;
-            steps = pair_steps(p.seqs[i], pair, pt);
-            j0 = 0;
-            j1 = left = steps;
-            return;
-        }
+    int pt, left;  // query tokens of a pair; steps of the range from this segment's j0 on
+    Seg s;
+    __device__ __forceinline__ void set() {
+        const BlockPrefillSeq& e = p.seqs[s.i];
+        s.steps = pair_steps(e, s.pair, pt);
+        s.j1 = left > 0 ? min(s.steps, s.j0 + left) : 0;
+        s.two = (2 * s.pair + 1) * (pt / 2) < e.q_len;
+    }
+    __device__ __forceinline__ LineWalk(const BlockPrefillParams& p_, int b) : p(p_), pt(2 * (128 / p_.r)) {
         const int u0 = (int)((int64_t)p.steps * b / p.grid), u1 = (int)((int64_t)p.steps * (b + 1) / p.grid);
-        for (int hi = p.n_seqs - 1; lo < hi;) {
-            const int mid = (lo + hi + 1) / 2;
-            if (p.seqs[mid].step_begin <= u0) lo = mid; else hi = mid - 1;
-        }
-        i = lo;
-        rel = u0 - p.seqs[i].step_begin;
-        kvh = rel / p.seqs[i].head_steps;
-        rel -= kvh * p.seqs[i].head_steps;
-        pair = p.seqs[i].pairs - 1;
-        while (rel >= (steps = pair_steps(p.seqs[i], pair, pt))) rel -= steps, --pair;
-        j0 = rel;
+        int i = 0;
+#pragma unroll 1
+        while (i + 1 < p.n_seqs && p.seqs[i + 1].step_begin <= u0) ++i;
+        const BlockPrefillSeq& e = p.seqs[i];
+        int rel = u0 - e.step_begin, n;
+        s.i = i;
+        s.kvh = rel / e.head_steps;
+        rel -= s.kvh * e.head_steps;
+        s.pair = e.pairs - 1;
+#pragma unroll 1
+        while (rel >= (n = pair_steps(e, s.pair, pt))) rel -= n, --s.pair;
+        s.j0 = rel;
         left = u1 - u0;
-        j1 = min(steps, j0 + left);
+        set();
     }
-    __device__ __forceinline__ bool valid() const { return left > 0; }
     __device__ __forceinline__ void next() {
-        left -= j1 - j0;
-        if (left <= 0) return;
-        if (--pair < 0) {
-            if (++kvh == p.c.hkv) kvh = 0, ++i;
-            pair = p.seqs[i].pairs - 1;
+        left -= s.j1 - s.j0;
+        s.j0 = 0;
+        if (left > 0 && --s.pair < 0) {
+            if (++s.kvh == p.c.hkv) s.kvh = 0, ++s.i;
+            s.pair = p.seqs[s.i].pairs - 1;
         }
-        steps = pair_steps(p.seqs[i], pair, pt);
-        j0 = 0;
-        j1 = min(steps, left);
+        if (left > 0) set();
+        else s.j1 = 0;
     }
-    __device__ __forceinline__ bool two() const { return (2 * pair + 1) * (pt / 2) < p.seqs[i].q_len; }  // the second tile has rows
-    __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == steps; }
+};
+
+// Hands out a CTA's segments to its roles: the line's, or whole ones, the longest first, as the CTAs
+// get to them (the first by the CTA's index, the next from a counter; the last CTA to run out sets
+// the counters back for the next call). One entry is made ahead of what the expansion has taken.
+__device__ __forceinline__ void feed_role(const BlockPrefillParams& p, uint64_t* bars, int32_t* err) {
+    int32_t* counters = reinterpret_cast<int32_t*>(p.c.base + p.c.lay.counters);
+    LineWalk line(p, p.line ? blockIdx.x : 0);
+    Seg* ring = reinterpret_cast<Seg*>(bars + kNumBars);
+    bool ok = true;
+#pragma unroll 1
+    for (int k = 0;; ++k) {
+        if (k >= kFeed) ok = bar_wait(bars + kBarFeedEmpty + (k & (kFeed - 1)), (uint32_t)((k / kFeed - 1) & 1), err) && ok;
+        if (k > 0) ok = bar_wait(bars + kBarTake, (uint32_t)((k - 1) & 1), err) && ok;
+        if (p.line) {
+            if (k > 0) line.next();
+        } else {
+            const int u = k == 0 ? (int)blockIdx.x : p.grid + atomicAdd(counters, 1);
+            line.left = 0;
+            if (u < p.segs) {
+                int i = 0;
+#pragma unroll 1
+                while (i + 1 < p.n_seqs && p.seqs[i + 1].seg_begin <= u) ++i;
+                const int rel = u - p.seqs[i].seg_begin;
+                line.s.i = i;
+                line.s.kvh = rel % p.c.hkv;
+                line.s.pair = p.seqs[i].pairs - 1 - rel / p.c.hkv;
+                line.s.j0 = 0;
+                line.left = 1 << 30;  // all of it
+            }
+            line.set();
+        }
+        if (!ok) line.s.j1 = 0;
+        ring[k & (kFeed - 1)] = line.s;
+        mbar_arrive(bars + kBarFeedFull + (k & (kFeed - 1)));
+        if (line.s.j1 == 0) break;
+    }
+    if (p.line) return;
+    __threadfence();
+    if (atomicAdd(counters + 1, 1) == p.grid - 1) {
+        counters[0] = 0;
+        counters[1] = 0;
+    }
+}
+
+// A warp's way through the segments; every warp that walks takes each entry once.
+struct Walk {
+    uint64_t* bars;
+    int k;
+    Seg s;
+    __device__ __forceinline__ explicit Walk(uint64_t* bars_) : bars(bars_), k(0) {}
+    __device__ __forceinline__ bool next(int32_t* err) {
+        if (!bar_wait(bars + kBarFeedFull + (k & (kFeed - 1)), (uint32_t)((k / kFeed) & 1), err)) return false;
+        const int4* at = reinterpret_cast<const int4*>(reinterpret_cast<const Seg*>(bars + kNumBars) + (k & (kFeed - 1)));
+        const int4 a = at[0], b = at[1];
+        s = Seg{a.x, a.y, a.z, a.w, b.x, b.y, b.z, 0};
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(bars + kBarFeedEmpty + (k & (kFeed - 1)));
+        ++k;
+        return s.j1 > 0;
+    }
+    __device__ __forceinline__ bool whole() const { return s.j0 == 0 && s.j1 == s.steps; }
 };
 
 __device__ __forceinline__ int bf16_exponent(uint32_t top) { return max((int)(top >> 7) - 127, -100); }
@@ -204,89 +260,79 @@ __device__ __forceinline__ int warp_exponent(uint32_t top) {
 }
 
 // ---- the MMA issuer ----
-// The whole warp walks and waits, so that addresses stay in uniform registers; one lane issues.
-// (With a single thread walking, each MMA took its operands through vector registers and
-// eight of them about 1,300 clocks to issue; they run in 512.)
+// An MMA of this size runs 64 clocks, but takes its warp about 30 turns at a scheduler that it shares
+// with two softmax warps and one of the expansion's, so that the issue, near 100 clocks an MMA, is
+// what bounds a step. The whole warp walks and each MMA is predicated by itself (with a single
+// thread walking, operands go through vector registers: 160 clocks), tiles and halves are unrolled,
+// and waits suspend (polling takes issue slots and shared-memory cycles from everyone). One warp
+// issues both tiles' MMAs in turn, which keeps the tiles half a step apart; with a warp a tile they
+// fall into step, both softmaxes run at once and then both tiles' MMAs.
 template <int D>
-__device__ __forceinline__ void issue_role(const BlockPrefillParams& p, uint32_t sbase, uint64_t* bars, uint32_t tmem,
-                                           int32_t* err) {
+__device__ __forceinline__ void issue_role(uint32_t sbase, uint64_t* bars, int32_t* err) {
     using Sh = Shape<D>;
     const bool leader = elect_one();
-    sbase >>= 4;  // (addresses stay under 2^18: descriptor fields)
-    auto qk = [&](int b, int jj) {
-        const uint32_t q = sbase + ((Sh::kQ + b * Sh::kTileQ) >> 4), k = sbase + ((Sh::kK + (jj & 1) * Sh::kTileQ) >> 4);
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t off = ((ks >> 2) * Sh::kAtom + (ks & 3) * 32) >> 4;
-            if (leader) mma_ss(tmem + kColS + 128 * b, desc128(q + off), desc128(k + off), kIdesc<128>, ks > 0);
-        }
-        if (leader) mma_commit(bars + kBarSFull + b);
-    };
-    auto pv = [&](int b, int jj, int half, uint32_t acc) {  // 64 keys
-        const uint32_t v = sbase + ((Sh::kV + (jj & 1) * Sh::kTileV + half * (D * 128)) >> 4);
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-            if (leader)
-                mma_ts(tmem + kColO + 128 * b, tmem + kColS + 128 * b + 32 * half + 8 * ks, desc128(v + 2 * ks), kIdesc<D>,
-                       ks > 0 ? 1u : acc);
-    };
+    const uint32_t base = sbase >> 4;  // (addresses stay under 2^18: descriptor fields)
     int jj = 0;
     uint32_t segs = 0, steps = 0;  // bit b: phase of tile b's segments, steps
-    for (Walk w(p, blockIdx.x); w.valid(); w.next()) {
-        const int tiles = w.two() ? 2 : 1;
+    Walk w(bars);
 #pragma unroll 1
-        for (int b = 0; b < tiles; ++b) {
-            mbar_wait(bars + kBarQFull + b, segs >> b & 1, err);
-            segs ^= 1u << b;
-        }
-        mbar_wait(bars + kBarKFull + (jj & 3), (uint32_t)((jj >> 2) & 1), err);
-        tc_fence_after();
+    while (w.next(err)) {
+        // broadcast from a lane, so that the loop is seen to be uniform
+        const int tiles = __shfl_sync(0xffffffffu, w.s.two, 0) ? 2 : 1, j0 = __shfl_sync(0xffffffffu, w.s.j0, 0),
+                  j1 = __shfl_sync(0xffffffffu, w.s.j1, 0);
+        // step j0 - 1 has no PV, step j1 - 1 no QK behind it
 #pragma unroll 1
-        for (int b = 0; b < tiles; ++b) qk(b, jj);
-        if (leader) mma_commit(bars + kBarKEmpty + (jj & 1));
-#pragma unroll 1
-        for (int j = w.j0; j < w.j1; ++j, ++jj) {
-            mbar_wait(bars + kBarVFull + (jj & 3), (uint32_t)((jj >> 2) & 1), err);
-            const bool more = j + 1 < w.j1;
-#pragma unroll 1
-            for (int b = 0; b < tiles; ++b) {
-                mbar_spin(bars + kBarPFull + 2 * b, steps >> b & 1, err);
-                tc_fence_after();
-                pv(b, jj, 0, j > w.j0 ? 1u : 0u);
-                mbar_spin(bars + kBarPFull + 2 * b + 1, steps >> b & 1, err);
-                steps ^= 1u << b;
-                tc_fence_after();
-                pv(b, jj, 1, 1u);
-                if (b == tiles - 1 && leader) mma_commit(bars + kBarVEmpty + (jj & 1));
-                if (more) {
-                    if (b == 0) {
-                        mbar_wait(bars + kBarKFull + ((jj + 1) & 3), (uint32_t)(((jj + 1) >> 2) & 1), err);
+        for (int j = j0 - 1; j < j1; ++j) {
+            const bool more = j + 1 < j1, any = j >= j0;
+            // jj: step j + 1. The expansion makes K(0) V(0) K(1) V(1) ..: the next K being there, so is this V
+            const int at = more ? kBarKFull + (jj & 3) : kBarVFull + ((jj - 1) & 3);
+            bar_wait(bars + at, (uint32_t)(((more ? jj : jj - 1) >> 2) & 1), err);
+            const uint32_t k = base + ((Sh::kK + (jj & 1) * Sh::kTileQ) >> 4), v = base + ((Sh::kV + (~jj & 1) * Sh::kTileV) >> 4);
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                if (b >= tiles) break;
+                if (any) {
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {  // 64 keys each
+                        bar_wait(bars + kBarPFull + 2 * b + half, steps >> b & 1, err);
                         tc_fence_after();
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            if (leader)
+                                mma_ts(kColO + 128 * b, kColS + 128 * b + 32 * half + 8 * ks,
+                                       desc128(v + ((half * (D * 128) + ks * 32) >> 4)), kIdesc<D>,
+                                       ks + half > 0 || j > j0 ? 1u : 0u);
                     }
-                    qk(b, jj + 1);
-                    if (b == tiles - 1 && leader) mma_commit(bars + kBarKEmpty + ((jj + 1) & 1));
+                    steps ^= 1u << b;
+                    if (leader && b == tiles - 1) mma_commit(bars + kBarVEmpty + (~jj & 1));
+                } else {
+                    bar_wait(bars + kBarQFull + b, segs >> b & 1, err);
+                    segs ^= 1u << b;
+                    tc_fence_after();
+                }
+                if (more) {
+                    const uint32_t q = base + ((Sh::kQ + b * Sh::kTileQ) >> 4);
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                        const uint32_t off = ((ks >> 2) * Sh::kAtom + (ks & 3) * 32) >> 4;
+                        if (leader) mma_ss(kColS + 128 * b, desc128(q + off), desc128(k + off), kIdesc<128>, ks > 0);
+                    }
+                    if (leader) mma_commit(bars + kBarSFull + b);
+                    if (leader && b == tiles - 1) mma_commit(bars + kBarKEmpty + (jj & 1));
                 } else if (leader) {
                     mma_commit(bars + kBarOFull + b);
                 }
             }
+            if (more) ++jj;
         }
     }
     if (leader) mma_commit(bars + kBarDrain);
-}
-
-// ---- expansion: one part (32 tokens) a warp ----
-// The steps of a CTA in order, for the expansion warps.
-struct StepWalk {
-    Walk w;
-    int j;
-    __device__ __forceinline__ StepWalk(const BlockPrefillParams& p, int b) : w(p, b), j(w.j0) {}
-    __device__ __forceinline__ bool valid() const { return w.valid(); }
-    __device__ __forceinline__ void next() {
-        if (++j < w.j1) return;
-        w.next();
-        j = w.j0;
+    // every MMA has completed before tensor memory is released
+    const uint64_t t0 = global_ns();
+#pragma unroll 1
+    while (!mbar_try_wait(bars + kBarDrain, 0u) && global_ns() - t0 < kWaitLimitNs) {
     }
-};
+}
 
 // Non-finite 16-bit values of a word, as the bits of a pair (bit 0, bit 1).
 template <bool BF16>
@@ -339,7 +385,7 @@ __device__ __forceinline__ void expand_exact(const BlockView& c, const BlockPref
             h = make_float2((float)ex, f);
         }
         uint8_t* atom = dst + (wp >> 1) * (D * 128);
-#pragma unroll 4
+#pragma unroll 2
         for (int i = 0; i < D / 8; ++i) {
             uint4 r = row(8 * i + g);
             bad |= (bad_pair<BF16>(r.x) | bad_pair<BF16>(r.y) << 2 | bad_pair<BF16>(r.z) << 4 | bad_pair<BF16>(r.w) << 6) << (8 * t);
@@ -357,13 +403,13 @@ __device__ __forceinline__ void expand_exact(const BlockView& c, const BlockPref
         };
         if (BF16) {
             uint32_t top = 0;
-#pragma unroll 4
+#pragma unroll 2
             for (int z = 0; z < D / 8; ++z) top = max_of(top, finite_only<BF16>(piece(z)));
             const int ex = warp_exponent(top);
             f = power2(-ex);
             h.x = power2(ex);
         }
-#pragma unroll 4
+#pragma unroll 2
         for (int z = 0; z < D / 8; ++z) {
             uint4 r = piece(z);
             if (BF16) r = scaled_f16(r, f);
@@ -373,111 +419,109 @@ __device__ __forceinline__ void expand_exact(const BlockView& c, const BlockPref
     }
 }
 
-// Warp wp turns part wp of every step into rows of the step's K tile, then of its V tile. Its 16
-// bytes a lane and chunk are reloaded in place: V codes while K's are converted, the next step's K
-// codes while V's are.
+// Warp wp turns part wp of every step into rows of the step's K tile, then of its V tile. A lane's 16
+// bytes of each chunk sit in registers and are reloaded in place: V codes while K's are converted,
+// the next step's K codes while V's are. (Staging the codes in shared memory instead cost
+// a third of the kernel's time: the MMAs' operand reads leave little of that bandwidth.) Lanes take
+// V's chunks in an order in which the stores of eight lanes meet eight different banks.
 template <int D, bool INT8, bool BF16>
 __device__ __forceinline__ void expand_role(const BlockPrefillParams& p, uint8_t* smem, uint64_t* bars, int32_t* err, int wp,
                                             int lane) {
     using Sh = Shape<D>;
     const BlockView& c = p.c;
-    const int g = lane >> 2, t = lane & 3, sh = c.log2_block - 5;
+    const int sh = c.log2_block - 5;
+    const int t = lane & 3, kg = lane >> 2, vg = (lane >> 3) + (lane & 4);
     constexpr int kChunks = D / 16;  // 512-byte chunks of a part's K or V
-    StepWalk ahead(p, blockIdx.x);
-    // The part of a step: its sequence entry and KV head (head * 256 + entry, -1 behind the last
-    // step), its 32-token tile, with bit 31 set where the tile is exact or not there. The pool slot
-    // is loaded a step before its address is needed.
-    int slot = 0;
-    auto look = [&](int& who, uint32_t& tile) {
-        who = -1;
-        tile = 0x80000000u;
-        if (!ahead.valid()) return;
-        const BlockPrefillSeq& e = p.seqs[ahead.w.i];
-        who = ahead.w.kvh * 256 + ahead.w.i;
-        const int x = 4 * ahead.j + wp;
-        tile = (uint32_t)x;
-        if (x < e.n >> c.log2_block << sh) slot = __ldg(block_table(c, e.seq) + (x >> sh));
-        else tile |= 0x80000000u;
-        ahead.next();
+    auto load_k = [&](const uint8_t* rec, int i) { return __ldg(reinterpret_cast<const uint4*>(rec + 16 + i * 512) + lane); };
+    auto load_v = [&](const uint8_t* rec, int i) {
+        return __ldg(reinterpret_cast<const uint4*>(rec + 16 + kTileTokens * D + i * 512) + 4 * vg + t);
     };
-    auto address = [&](int who, uint32_t tile) -> const uint8_t* {
-        return tile >> 31 ? nullptr : tile_ptr(c, slot, who >> 8, (int)tile & ((1 << sh) - 1));
+    auto halves = [&](uint32_t u, uint32_t v) {  // 8 codes
+        return make_uint4(codes_lo<INT8>(u), codes_hi<INT8>(u), codes_lo<INT8>(v), codes_hi<INT8>(v));
     };
-    auto load = [&](const uint8_t* rec, int i) { return __ldg(reinterpret_cast<const uint4*>(rec + 16 + i * 512) + lane); };
+    // The part of a step: its sequence entry and KV head (head * 256 + entry, -1 for none), its
+    // 32-token tile, with bit 31 set where the tile is exact or not there. A turn of the loop looks two
+    // steps ahead (so that the pool slot is there when its address is needed), loads one ahead and
+    // expands one.
+    Walk w(bars);
+    bool more = true;
+    int j = 0, end = 0, slot = 0;  // the next step to look at, and its segment's end
+    int who = -1, who1 = -1;
+    uint32_t tile = 0x80000000u, tile1 = 0x80000000u;
+    const uint8_t* rec = nullptr;
     uint4 x[kChunks];
     float4 hd = make_float4(1.f, 0.f, 0.f, 1.f);
-    int who, who1;
-    uint32_t tile, tile1;
-    look(who, tile);
-    const uint8_t* rec = address(who, tile);
-    if (rec) {
-#pragma unroll
-        for (int i = 0; i < kChunks; ++i) x[i] = load(rec, i);
-        hd = __ldg(reinterpret_cast<const float4*>(rec));
-    }
-    look(who1, tile1);
 #pragma unroll 1
-    for (int jj = 0; who >= 0; ++jj) {
-        float* head = reinterpret_cast<float*>(smem + Sh::kHdr) + ((jj & 3) * 4 + wp) * 4;
-        float2 h;
-        uint32_t bad = 0;
-        // K
-        if (jj >= 2) mbar_wait(bars + kBarKEmpty + (jj & 1), (uint32_t)(((jj >> 1) - 1) & 1), err);
-        uint8_t* dst = smem + Sh::kK + (jj & 1) * Sh::kTileQ;
-        if (rec) {
-            h = make_float2(hd.x, 0.f);
-#pragma unroll
-            for (int i = 0; i < kChunks; ++i) {
-                const uint4 a = make_uint4(codes_lo<INT8>(x[i].x), codes_hi<INT8>(x[i].x), codes_lo<INT8>(x[i].y),
-                                           codes_hi<INT8>(x[i].y));
-                const uint4 b = make_uint4(codes_lo<INT8>(x[i].z), codes_hi<INT8>(x[i].z), codes_lo<INT8>(x[i].w),
-                                           codes_hi<INT8>(x[i].w));
-                x[i] = load(rec, kChunks + i);
-                // 16 channels of one token
-                const int s = i / (D / 32), cc = i / 2 % (D / 64), hh = i & 1;
-                const int row = 32 * wp + 8 * (g >> 1) + 4 * s + 2 * hh + (g & 1);
-                *reinterpret_cast<uint4*>(dst + cc * Sh::kAtom + swz(row, 2 * t)) = a;
-                *reinterpret_cast<uint4*>(dst + cc * Sh::kAtom + swz(row, 2 * t + 1)) = b;
-            }
-        } else {
-            expand_exact<D, BF16, false>(c, p.seqs[who & 255], who >> 8, (int)(tile & 0x7fffffffu), wp, lane, dst, h, bad);
+    for (int jj = -2; jj < 0 || who >= 0; ++jj) {
+        const uint8_t* rec1 = tile1 >> 31 ? nullptr : tile_ptr(c, slot, who1 >> 8, (int)tile1 & ((1 << sh) - 1));
+        int who2 = -1;
+        uint32_t tile2 = 0x80000000u;
+        if (j == end && more) {
+            more = w.next(err);
+            j = w.s.j0;
+            end = w.s.j1;
+            if (lane == 0) mbar_arrive(bars + kBarTake);  // lets the feed make the next entry
         }
-        if (lane == 0) head[0] = h.x;
-        fence_proxy_async_smem();
-        mbar_arrive(bars + kBarKFull + (jj & 3));
-        // V
-        const uint8_t* rec1 = address(who1, tile1);
-        int who2;
-        uint32_t tile2;
-        look(who2, tile2);
-        if (jj >= 2) mbar_wait(bars + kBarVEmpty + (jj & 1), (uint32_t)(((jj >> 1) - 1) & 1), err);
-        dst = smem + Sh::kV + (jj & 1) * Sh::kTileV;
-        if (rec) {
-            h = make_float2(hd.z, hd.w);
-            uint8_t* atom = dst + (wp >> 1) * (D * 128);
-            const int chunk = 4 * (wp & 1) + t;
-#pragma unroll
-            for (int i = 0; i < kChunks; ++i) {
-                const uint4 a = make_uint4(codes_lo<INT8>(x[i].x), codes_hi<INT8>(x[i].x), codes_lo<INT8>(x[i].y),
-                                           codes_hi<INT8>(x[i].y));
-                const uint4 b = make_uint4(codes_lo<INT8>(x[i].z), codes_hi<INT8>(x[i].z), codes_lo<INT8>(x[i].w),
-                                           codes_hi<INT8>(x[i].w));
-                if (rec1) x[i] = load(rec1, i);
-                // 8 tokens of channels 16 i + g and + 8
-                *reinterpret_cast<uint4*>(atom + swz(16 * i + g, chunk)) = a;
-                *reinterpret_cast<uint4*>(atom + swz(16 * i + g + 8, chunk)) = b;
-            }
-        } else {
-            expand_exact<D, BF16, true>(c, p.seqs[who & 255], who >> 8, (int)(tile & 0x7fffffffu), wp, lane, dst, h, bad);
-            if (rec1) {
-#pragma unroll
-                for (int i = 0; i < kChunks; ++i) x[i] = load(rec1, i);
-            }
+        if (more) {
+            const BlockPrefillSeq& e = p.seqs[w.s.i];
+            who2 = w.s.kvh * 256 + w.s.i;
+            const int y = 4 * j++ + wp;
+            tile2 = (uint32_t)y;
+            if (y < e.n >> c.log2_block << sh) slot = __ldg(block_table(c, e.seq) + (y >> sh));
+            else tile2 |= 0x80000000u;
         }
-        if (rec1) hd = __ldg(reinterpret_cast<const float4*>(rec1));
-        if (lane == 0) head[1] = __uint_as_float(bad), head[2] = h.x, head[3] = h.y;
-        fence_proxy_async_smem();
-        mbar_arrive(bars + kBarVFull + (jj & 3));
+        if (jj >= 0) {
+            float* head = reinterpret_cast<float*>(smem + Sh::kHdr) + ((jj & 3) * 4 + wp) * 4;
+            float2 h;
+            uint32_t bad = 0;
+            // K
+            if (jj >= 2) bar_wait(bars + kBarKEmpty + (jj & 1), (uint32_t)(((jj >> 1) - 1) & 1), err);
+            uint8_t* dst = smem + Sh::kK + (jj & 1) * Sh::kTileQ;
+            if (rec) {
+                h = make_float2(hd.x, 0.f);
+                const int row0 = 32 * wp + 8 * (kg >> 1) + (kg & 1);
+#pragma unroll
+                for (int i = 0; i < kChunks; ++i) {
+                    const uint4 a = halves(x[i].x, x[i].y), b = halves(x[i].z, x[i].w);
+                    x[i] = load_v(rec, i);
+                    // 16 channels of one token
+                    const int s = i / (D / 32), cc = i / 2 % (D / 64), row = row0 + 4 * s + 2 * (i & 1);
+                    *reinterpret_cast<uint4*>(dst + cc * Sh::kAtom + swz(row, 2 * t)) = a;
+                    *reinterpret_cast<uint4*>(dst + cc * Sh::kAtom + swz(row, 2 * t + 1)) = b;
+                }
+            } else {
+                expand_exact<D, BF16, false>(c, p.seqs[who & 255], who >> 8, (int)(tile & 0x7fffffffu), wp, lane, dst, h, bad);
+            }
+            if (lane == 0) head[0] = h.x;
+            fence_proxy_async_smem();
+            mbar_arrive(bars + kBarKFull + (jj & 3));
+            // V
+            if (jj >= 2) bar_wait(bars + kBarVEmpty + (jj & 1), (uint32_t)(((jj >> 1) - 1) & 1), err);
+            dst = smem + Sh::kV + (jj & 1) * Sh::kTileV;
+            if (rec) {
+                h = make_float2(hd.z, hd.w);
+                uint8_t* to = dst + (wp >> 1) * (D * 128) + swz(vg, 4 * (wp & 1) + t);
+#pragma unroll
+                for (int i = 0; i < kChunks; ++i) {
+                    // 8 tokens of channels 16 i + vg and + 8
+                    *reinterpret_cast<uint4*>(to + i * 2048) = halves(x[i].x, x[i].y);
+                    *reinterpret_cast<uint4*>(to + i * 2048 + 1024) = halves(x[i].z, x[i].w);
+                    if (rec1) x[i] = load_k(rec1, i);
+                }
+            } else {
+                expand_exact<D, BF16, true>(c, p.seqs[who & 255], who >> 8, (int)(tile & 0x7fffffffu), wp, lane, dst, h, bad);
+            }
+            if (lane == 0) head[1] = __uint_as_float(bad), head[2] = h.x, head[3] = h.y;
+            fence_proxy_async_smem();
+            mbar_arrive(bars + kBarVFull + (jj & 3));
+        }
+        if (rec1) {
+            if (!rec) {  // nothing was reloaded in place
+#pragma unroll
+                for (int i = 0; i < kChunks; ++i) x[i] = load_k(rec1, i);
+            }
+            hd = __ldg(reinterpret_cast<const float4*>(rec1));
+        }
         who = who1;
         tile = tile1;
         rec = rec1;
@@ -492,57 +536,71 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, uint8_
                                              int32_t* err, int et, int b, uint32_t lane_off) {
     using Sh = Shape<D>;
     const uint32_t ts = tmem + kColS + 128 * b + lane_off, to = tmem + kColO + 128 * b + lane_off;
-    const int tpt = 128 / p.r, tok_in = et / p.r, head_in = et % p.r;
+    const int tpt = 128 / p.r, tok_in = et / p.r, head_in = et % p.r, lane = et & 31;
     const float4* hdr = reinterpret_cast<const float4*>(smem + Sh::kHdr);
+    // the warp's 32 rows of the tile's Q: query rows on the way in, output rows on the way out
+    uint8_t* rows = smem + Sh::kQ + b * Sh::kTileQ + (et & 96) * 128;
     // a negative scale turns the query's sign, so that larger S is always a larger logit
     // (and a scale of 0 the query to zeros: every logit is 0)
-    const float scale = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
     const bool zero = p.scale_log2 == 0.f;
+    const float scale = zero ? 1.f : fabsf(p.scale_log2);
     const uint32_t sign = p.scale_log2 < 0.f ? 0x80008000u : 0u;
     int jj = 0, step = 0, seg = 0;
-    for (Walk w(p, blockIdx.x); w.valid(); w.next()) {
-        if (b == 1 && !w.two()) {
-            jj += w.j1 - w.j0;
+    Walk w(bars);
+#pragma unroll 1
+    while (w.next(err)) {
+        if (b == 1 && !w.s.two) {
+            jj += w.s.j1 - w.s.j0;
             continue;
         }
-        const BlockPrefillSeq& e = p.seqs[w.i];
-        const int tok = (2 * w.pair + b) * tpt + tok_in;
+        const BlockPrefillSeq& e = p.seqs[w.s.i];
+        const int tok = (2 * w.s.pair + b) * tpt + tok_in;
         const bool valid = tok_in < tpt && tok < e.q_len;
-        const size_t row = ((size_t)(e.q_row + tok) * p.hq + w.kvh * p.r + head_in) * D;
+        const int row = valid ? (e.q_row + tok) * p.hq + w.s.kvh * p.r + head_in : -1;  // of q and out
         const int pos = valid ? e.n - e.q_len + tok : e.n - 1;
         float qs = scale;
         {
-            const uint4* src = reinterpret_cast<const uint4*>(p.q + (valid ? row : 0));
-            float f = 1.f;
-            if (BF16) {
-                uint32_t top = 0;
-#pragma unroll 4
-                for (int i = 0; i < D / 8; ++i)
-                    if (valid) top = max_of(top, src[i]);
-                const int ex = bf16_exponent(max(top & 0xffffu, top >> 16)) - 14;
-                f = power2(-ex);
-                qs *= power2(ex);
-            }
-            uint8_t* dst = smem + Sh::kQ + b * Sh::kTileQ;
-#pragma unroll 4
-            for (int i = 0; i < D / 8; ++i) {
-                uint4 r = make_uint4(0, 0, 0, 0);
-                if (valid && !zero) r = src[i];
-                if (BF16) r = scaled_f16(r, f);
-                r = make_uint4(r.x ^ sign, r.y ^ sign, r.z ^ sign, r.w ^ sign);
-                *reinterpret_cast<uint4*>(dst + (i >> 3) * Sh::kAtom + swz(et, i & 7)) = r;
+            // D / 8 lanes a row; loops stay short: this code runs once a segment, from a cold cache
+            constexpr int kLanes = D / 8, kRows = 32 / kLanes, kTurn = 4;
+#pragma unroll 1
+            for (int i0 = 0; i0 < kLanes; i0 += kTurn) {
+                uint4 x[kTurn];
+#pragma unroll
+                for (int z = 0; z < kTurn; ++z) {
+                    const int at = __shfl_sync(0xffffffffu, row, (i0 + z) * kRows + lane / kLanes);
+                    x[z] = make_uint4(0, 0, 0, 0);
+                    if (at >= 0 && !zero) x[z] = reinterpret_cast<const uint4*>(p.q + (size_t)at * D)[lane % kLanes];
+                }
+#pragma unroll
+                for (int z = 0; z < kTurn; ++z) {
+                    const int i = i0 + z;
+                    uint4 r = x[z];
+                    if (BF16) {
+                        uint32_t top = max_of(0, r);
+                        top = max(top & 0xffffu, top >> 16);
+#pragma unroll
+                        for (int d = kLanes / 2; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+                        const int ex = bf16_exponent(top) - 14;
+                        r = scaled_f16(r, power2(-ex));
+                        const int mine = __shfl_sync(0xffffffffu, ex, lane % kRows * kLanes);  // of row i kRows + lane % kRows
+                        if (lane / kRows == i) qs *= power2(mine);
+                    }
+                    r = make_uint4(r.x ^ sign, r.y ^ sign, r.z ^ sign, r.w ^ sign);
+                    *reinterpret_cast<uint4*>(rows + (lane % kLanes >> 3) * Sh::kAtom + swz(i * kRows + lane / kLanes, lane & 7)) = r;
+                }
             }
         }
         fence_proxy_async_smem();
         mbar_arrive(bars + kBarQFull + b);
         float m = kNegInf, l = 0.f;
-        for (int j = w.j0; j < w.j1; ++j, ++jj, ++step) {
+#pragma unroll 1
+        for (int j = w.s.j0; j < w.s.j1; ++j, ++jj, ++step) {
             // A tile that sat out a segment may be whole phases ahead of the expansion; once its first
             // step's QK is done both barriers are at that step's phase or the one before. Within a
             // segment they are waited for first, and the headers read, while QK runs.
-            if (j == w.j0) mbar_wait(bars + kBarSFull + b, (uint32_t)(step & 1), err);
-            mbar_wait(bars + kBarKFull + (jj & 3), (uint32_t)((jj >> 2) & 1), err);
-            mbar_wait(bars + kBarVFull + (jj & 3), (uint32_t)((jj >> 2) & 1), err);
+            if (j == w.s.j0) bar_wait(bars + kBarSFull + b, (uint32_t)(step & 1), err);
+            bar_wait(bars + kBarKFull + (jj & 3), (uint32_t)((jj >> 2) & 1), err);
+            bar_wait(bars + kBarVFull + (jj & 3), (uint32_t)((jj >> 2) & 1), err);
             // logit = S c[ch] (+ log2 of V's scale in the weight); c > 0 or NaN
             float c[4], lv[4], iv[4];
             uint32_t bad = 0;
@@ -555,35 +613,25 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, uint8_
                 iv[ch] = h.w;
                 bad |= __float_as_uint(h.y);
             }
-            mbar_spin(bars + kBarSFull + b, (uint32_t)(step & 1), err);
+            bar_wait(bars + kBarSFull + b, (uint32_t)(step & 1), err);
             tc_fence_after();
             const int lim = pos + 1 - j * kStep;  // visible columns
             uint32_t r[4][32];
             float mx = kNegInf;
-            auto raise = [&](int ch) {
-                float a = __uint_as_float(r[ch][0]), a2 = __uint_as_float(r[ch][1]);
-#pragma unroll
-                for (int k = 2; k < 30; k += 4) {
-                    a = max3(a, __uint_as_float(r[ch][k]), __uint_as_float(r[ch][k + 1]));
-                    a2 = max3(a2, __uint_as_float(r[ch][k + 2]), __uint_as_float(r[ch][k + 3]));
-                }
-                a = max3(a, __uint_as_float(r[ch][30]), __uint_as_float(r[ch][31]));
-                mx = fmaxf(mx, fmaf(fmaxf(a, a2), c[ch], lv[ch]));
-            };
             const bool plain = !bad && __all_sync(0xffffffffu, lim >= kStep);
             tm_ld32(ts, r[0]);
             tm_ld32(ts + 32, r[1]);
             tm_wait_ld();
             tm_ld32(ts + 64, r[2]);
             tm_ld32(ts + 96, r[3]);
-            if (plain) {  // over the loads' latency
-                raise(0);
-                raise(1);
+            if (__builtin_expect(plain, 1)) {  // over the loads' latency
+                mx = fmaxf(mx, fmaf(max32(r[0]), c[0], lv[0]));
+                mx = fmaxf(mx, fmaf(max32(r[1]), c[1], lv[1]));
             }
             tm_wait_ld();
-            if (plain) {
-                raise(2);
-                raise(3);
+            if (__builtin_expect(plain, 1)) {
+                mx = fmaxf(mx, fmaf(max32(r[2]), c[2], lv[2]));
+                mx = fmaxf(mx, fmaf(max32(r[3]), c[3], lv[3]));
             } else {
                 // non-finite V tokens' weights become NaN where they are seen; then columns behind the
                 // row's position leave, with all of a part that is not seen at all
@@ -596,7 +644,7 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, uint8_
                         if (32 * ch + k >= lim) r[ch][k] = 0xff800000u;
                     }
                     if (32 * ch >= lim) c[ch] = 1.f, lv[ch] = 0.f, iv[ch] = 1.f;
-                    raise(ch);
+                    mx = fmaxf(mx, fmaf(max32(r[ch]), c[ch], lv[ch]));
                 }
             }
             const bool up = mx > m + 8.f;  // also from -inf
@@ -604,7 +652,7 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, uint8_
                 const float f = up ? ex2f(m - mx) : 1.f;  // 0 from -inf
                 if (up) m = mx;
                 l *= f;
-                if (j > w.j0) {
+                if (j > w.s.j0) {
                     // O is rescaled 16 columns at a time: the 128 logits stay in registers
 #pragma unroll 1
                     for (int ch = 0; ch < D / 16; ++ch) {
@@ -643,47 +691,64 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, uint8_
                 }
             }
         }
-        mbar_wait(bars + kBarOFull + b, (uint32_t)(seg++ & 1), err);
+        bar_wait(bars + kBarOFull + b, (uint32_t)(seg++ & 1), err);
         tc_fence_after();
+        // out through the warp's Q rows (their MMAs are done), 128 bytes a row at a time, so that a row
+        // leaves in whole sectors
+        auto give = [&](int piece, const uint32_t (&o)[32]) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                *reinterpret_cast<uint4*>(rows + piece * Sh::kAtom + swz(lane, k)) =
+                    make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        };
+        auto take = [&](int piece, int k) {  // 16 bytes of row 4 k + lane / 8
+            return *reinterpret_cast<const uint4*>(rows + piece * Sh::kAtom + swz(4 * k + (lane >> 3), lane & 7));
+        };
         if (w.whole()) {
             const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
-            for (int ch = 0; ch < D / 32; ++ch) {
-                uint32_t r[32];
-                tm_ld32(to + 32 * ch, r);
+            for (int piece = 0; piece < D / 64; ++piece) {
+                uint32_t x[2][32], o[32];
+                tm_ld32(to + 64 * piece, x[0]);
+                tm_ld32(to + 64 * piece + 32, x[1]);
                 tm_wait_ld();
-                if (valid) {
-                    uint4* dst = reinterpret_cast<uint4*>(p.out + row + 32 * ch);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t o[4];
+                for (int k = 0; k < 32; ++k)
+                    o[k] = pack2<BF16>(__uint_as_float(x[k >> 4][2 * k & 31]) * inv, __uint_as_float(x[k >> 4][(2 * k & 31) + 1]) * inv);
+                give(piece, o);
+            }
+            __syncwarp();
+#pragma unroll 2
+            for (int k = 0; k < 8; ++k) {
+                const int at = __shfl_sync(0xffffffffu, row, 4 * k + (lane >> 3));
 #pragma unroll
-                        for (int z = 0; z < 4; ++z)
-                            o[z] = pack2<BF16>(__uint_as_float(r[8 * k + 2 * z]) * inv, __uint_as_float(r[8 * k + 2 * z + 1]) * inv);
-                        dst[k] = make_uint4(o[0], o[1], o[2], o[3]);
-                    }
+                for (int piece = 0; piece < D / 64; ++piece) {
+                    const uint4 x = take(piece, k);
+                    if (at >= 0) *reinterpret_cast<uint4*>(p.out + (size_t)at * D + 64 * piece + 8 * (lane & 7)) = x;
                 }
             }
         } else {
             float* part = reinterpret_cast<float*>(p.c.base + p.c.lay.partials) +
-                          (size_t)(2 * blockIdx.x + (w.j0 == 0 ? 1 : 0)) * (256 * (D + 2));
-            const int rr = 128 * b + et;
+                          (size_t)(2 * blockIdx.x + (w.s.j0 == 0 ? 1 : 0)) * (256 * (D + 2));
+            const int first = 128 * b + (et & 96);
 #pragma unroll 1
             for (int ch = 0; ch < D / 32; ++ch) {
-                uint32_t r[32];
-                tm_ld32(to + 32 * ch, r);
+                uint32_t x[32];
+                tm_ld32(to + 32 * ch, x);
                 tm_wait_ld();
-                float4* dst = reinterpret_cast<float4*>(part + (size_t)rr * D + 32 * ch);
-                if (valid) {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        dst[k] = make_float4(__uint_as_float(r[4 * k]), __uint_as_float(r[4 * k + 1]),
-                                             __uint_as_float(r[4 * k + 2]), __uint_as_float(r[4 * k + 3]));
+                give(0, x);
+                __syncwarp();
+#pragma unroll 4
+                for (int k = 0; k < 8; ++k) {
+                    const int rr = first + 4 * k + (lane >> 3);
+                    *reinterpret_cast<uint4*>(part + (size_t)rr * D + 32 * ch + 4 * (lane & 7)) = take(0, k);
                 }
+                __syncwarp();
             }
-            part[256 * D + rr] = m;
-            part[256 * D + 256 + rr] = l;
+            part[256 * D + 128 * b + et] = m;
+            part[256 * D + 256 + 128 * b + et] = l;
         }
+        __syncwarp();
         tc_fence_before();  // O has been read before this thread lets the next segment's PV start
     }
 }
@@ -691,8 +756,7 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, uint8_
 template <int D, bool INT8, bool BF16>
 __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_constant__ BlockPrefillParams p) {
     using Sh = Shape<D>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+    extern __shared__ __align__(1024) uint8_t smem[];
     const int t = threadIdx.x, w = t >> 5, lane = t & 31, wg = w >> 2;
     int32_t* err = reinterpret_cast<int32_t*>(p.c.base + p.c.lay.err);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Sh::kBars);
@@ -711,6 +775,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             mbar_init(bars + kBarQFull + k, 128);
         }
         mbar_init(bars + kBarDrain, 1);
+        mbar_init(bars + kBarTake, 4);  // the expansion's warps
+        for (int k = 0; k < kFeed; ++k) {
+            mbar_init(bars + kBarFeedFull + k, 1);
+            mbar_init(bars + kBarFeedEmpty + k, 13);  // the warps that walk: 8 softmax, 4 expansion, 1 issuer
+        }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (w == 12) {
@@ -721,9 +790,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + Sh::kTmem);
+    // All of tensor memory is this CTA's, so it starts at address 0, and shared memory on 1024 bytes;
+    // both are counted on below. Were it ever not so, the launch would do nothing but say so.
+    const bool placed = *reinterpret_cast<volatile uint32_t*>(smem + Sh::kTmem) == 0 && (smem_addr(smem) & 1023) == 0;
+    constexpr uint32_t tmem = 0;
+    if (!placed && t == 0) atomicOr(err, kErrBadSlot);
     const uint32_t lane_off = (uint32_t)(32 * (w & 3)) << 16;
-    if (wg < 2) {
+    if (!placed) {
+    } else if (wg < 2) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         softmax_role<D, BF16>(p, smem, bars, tmem, err, t & 127, wg, lane_off);
     } else if (wg == 2) {
@@ -731,60 +805,75 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         expand_role<D, INT8, BF16>(p, smem, bars, err, w & 3, lane);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-        if (w == 12) {
-            issue_role<D>(p, smem_addr(smem), bars, tmem, err);
-            // every MMA has completed before tensor memory is released
-            const uint64_t t0 = global_ns();
-            while (!mbar_try_wait(bars + kBarDrain, 0u) && global_ns() - t0 < kWaitLimitNs) {
-            }
-        }
+        if (w == 12) issue_role<D>(smem_addr(smem), bars, err);
+        else if (w == 13 && lane == 0) feed_role(p, bars, err);
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (w == 12) {
         __syncwarp();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(*reinterpret_cast<volatile uint32_t*>(smem + Sh::kTmem))
+                     : "memory");
     }
 }
 
 // Adds the partials of the segment that begins in CTA b's range and ends behind it, in the order
-// of the cuts. blockIdx.y: 32 of the pair's 256 rows; 4 channels a thread.
+// of the cuts. blockIdx.y: 32 of the pair's 256 rows; 4 channels of four rows a thread, whose loads
+// are all in flight for each part.
+constexpr int kCombineRows = 32;
 template <int D, bool BF16>
-__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ BlockPrefillParams p) {
+__global__ void __launch_bounds__(kCombineRows / 4 * (D / 4)) combine_kernel(const __grid_constant__ BlockPrefillParams p) {
     const int b = blockIdx.x;
     const int u0 = (int)((int64_t)p.steps * b / p.grid), u1 = (int)((int64_t)p.steps * (b + 1) / p.grid);
-    Walk w(p, b);
+    LineWalk w(p, b);
     int u = u0;
-    while (u + (w.j1 - w.j0) < u1) u += w.j1 - w.j0, w.next();
-    if (w.j0 > 0 || w.j1 == w.steps) return;  // no segment both begins here and goes on
-    const int last = (int)(((int64_t)(u + w.steps) * p.grid - 1) / p.steps);
-    const BlockPrefillSeq& e = p.seqs[w.i];
+#pragma unroll 1
+    while (u + (w.s.j1 - w.s.j0) < u1) u += w.s.j1 - w.s.j0, w.next();
+    if (w.s.j0 > 0 || w.s.j1 == w.s.steps) return;  // no segment both begins here and goes on
+    const int last = (int)(((int64_t)(u + w.s.steps) * p.grid - 1) / p.steps);
+    const BlockPrefillSeq& e = p.seqs[w.s.i];
     const int tpt = 128 / p.r;
-    const float* base = reinterpret_cast<const float*>(p.c.base + p.c.lay.partials);
+    const int r0 = blockIdx.y * kCombineRows + threadIdx.x / (D / 4), ch = threadIdx.x % (D / 4) * 4;
     constexpr size_t kPart = 256 * (D + 2);
-    for (int x = threadIdx.x; x < 32 * (D / 4); x += 256) {
-        const int rr = blockIdx.y * 32 + x / (D / 4), ch = x % (D / 4) * 4, et = rr & 127;
-        const int tok = (2 * w.pair + (rr >> 7)) * tpt + et / p.r;
-        if (et / p.r >= tpt || tok >= e.q_len) continue;
-        float big = kNegInf, l = 0.f;
-        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-        auto part = [&](int z) { return base + (size_t)(2 * z + (z == b ? 1 : 0)) * kPart; };
-        for (int z = b; z <= last; ++z) big = fmaxf(big, part(z)[256 * D + rr]);
-        for (int z = b; z <= last; ++z) {
-            const float* q = part(z);
-            const float mz = q[256 * D + rr], f = mz == kNegInf ? 1.f : ex2f(mz - big);  // -inf: zeros or NaN
-            const float4 o = *reinterpret_cast<const float4*>(q + (size_t)rr * D + ch);
-            sum.x = fmaf(o.x, f, sum.x);
-            sum.y = fmaf(o.y, f, sum.y);
-            sum.z = fmaf(o.z, f, sum.z);
-            sum.w = fmaf(o.w, f, sum.w);
-            l = fmaf(q[256 * D + 256 + rr], f, l);
+    const float* base = reinterpret_cast<const float*>(p.c.base + p.c.lay.partials);
+    float4 sum[4];
+    float big[4], l[4];
+#pragma unroll
+    for (int y = 0; y < 4; ++y) sum[y] = make_float4(0.f, 0.f, 0.f, 0.f), big[y] = kNegInf, l[y] = 0.f;
+#pragma unroll 1
+    for (int z = b; z <= last; ++z) {
+        const float* q = base + (size_t)(2 * z + (z == b ? 1 : 0)) * kPart;  // slot 1 where the segment begins
+        float4 o[4];
+        float m[4], n[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            const int rr = r0 + y * (kCombineRows / 4);
+            o[y] = *reinterpret_cast<const float4*>(q + (size_t)rr * D + ch);
+            m[y] = q[256 * D + rr];
+            n[y] = q[256 * D + 256 + rr];
         }
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        const size_t row = ((size_t)(e.q_row + tok) * p.hq + w.kvh * p.r + et % p.r) * D;
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            const float top = fmaxf(big[y], m[y]);
+            // -inf (no weight yet, or NaN): nothing to scale
+            const float f = big[y] == kNegInf ? 1.f : ex2f(big[y] - top), g = m[y] == kNegInf ? 1.f : ex2f(m[y] - top);
+            sum[y].x = fmaf(o[y].x, g, sum[y].x * f);
+            sum[y].y = fmaf(o[y].y, g, sum[y].y * f);
+            sum[y].z = fmaf(o[y].z, g, sum[y].z * f);
+            sum[y].w = fmaf(o[y].w, g, sum[y].w * f);
+            l[y] = fmaf(n[y], g, l[y] * f);
+            big[y] = top;
+        }
+    }
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+        const int rr = r0 + y * (kCombineRows / 4), et = rr & 127, tok = (2 * w.s.pair + (rr >> 7)) * tpt + et / p.r;
+        if (et / p.r >= tpt || tok >= e.q_len) continue;
+        const float inv = l[y] == 0.f ? 0.f : 1.f / l[y];
+        const size_t row = ((size_t)(e.q_row + tok) * p.hq + w.s.kvh * p.r + et % p.r) * D;
         *reinterpret_cast<uint2*>(p.out + row + ch) =
-            make_uint2(pack2<BF16>(sum.x * inv, sum.y * inv), pack2<BF16>(sum.z * inv, sum.w * inv));
+            make_uint2(pack2<BF16>(sum[y].x * inv, sum[y].y * inv), pack2<BF16>(sum[y].z * inv, sum[y].w * inv));
     }
 }
 
@@ -794,7 +883,7 @@ int launch(const BlockPrefillParams& p, cudaStream_t s) {
                                                Shape<D>::kSmem);
     if (e != cudaSuccess) return (int)e;
     prefill_kernel<D, INT8, BF16><<<p.grid, kThreads, Shape<D>::kSmem, s>>>(p);
-    if (p.line) combine_kernel<D, BF16><<<dim3(p.grid, 8), 256, 0, s>>>(p);
+    if (p.line) combine_kernel<D, BF16><<<dim3(p.grid, 256 / kCombineRows), kCombineRows / 4 * (D / 4), 0, s>>>(p);
     return (int)cudaGetLastError();
 }
 
