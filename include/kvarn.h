@@ -421,7 +421,8 @@ typedef struct {
 
 /* q: [n_tokens][num_q_heads][head_dim] with q_stride elements between tokens (at least
  * num_q_heads * head_dim, a multiple of 8; k, q_out, k_out likewise), so that q and k may be
- * parts of a packed projection; 16-byte aligned. q_weight, k_weight: f32 [head_dim] or NULL.
+ * parts of a packed projection; 16-byte aligned. q_weight, k_weight: f32 [head_dim], 16-byte
+ * aligned, or NULL.
  * positions: int32 [n_tokens]; freqs: f64 [rot_dim / 2], radians per position (both may be
  * NULL if rot_dim is 0). An output may be its own input (same address, stride and type);
  * any other overlap is not allowed. All pointers device. Can be captured. */

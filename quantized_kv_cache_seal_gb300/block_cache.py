@@ -2,7 +2,6 @@
 block with torch, checks tensors and forwards every call to libkvarn.so (``include/kvarn.h``, "Block cache")."""
 from __future__ import annotations
 
-import contextlib
 import math
 from typing import Optional, Sequence, Union
 
@@ -51,15 +50,12 @@ class BlockCache:
 
     # -- tensors, streams ------------------------------------------------------------------------------------
     def _here(self):
-        """The cache's device as the current one (nothing to do where it is)."""
-        if self.device.type != "cuda" or torch.cuda.current_device() == self.device.index:
-            return contextlib.nullcontext()
-        return torch.cuda.device(self.device)
+        return K.on_device(self.device)
 
     def _stream(self, stream):
         if stream is not None or self.device.type != "cuda":
             return stream
-        return torch.cuda.current_stream(self.device)
+        return K.current_stream(self.device)
 
     def _empty(self, shape, dtype, stream):
         """A result of a call on `stream`, allocated there: freed memory of another stream may still be in use."""
@@ -70,21 +66,23 @@ class BlockCache:
         with torch.cuda.stream(stream):
             return torch.empty(shape, dtype=dtype, device=self.device)
 
-    def _dense(self, x, rows, heads, name, dtype=None):
-        want = (rows, heads, self.cfg.head_dim)
-        if tuple(x.shape) != want or x.dtype != (dtype or self.dtype) or x.device != self.device or not x.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous {dtype or self.dtype} tensor {want} on {self.device}, got "
-                             f"{x.dtype} {tuple(x.shape)} with strides {x.stride()} on {x.device}")
-        return x
+    def _refuse(self, name, x, what):
+        raise ValueError(f"{name} must be {what} on {self.device}, got {x.dtype} {tuple(x.shape)} with strides "
+                         f"{x.stride()} on {x.device}")
+
+    def _dense(self, x, rows, name):
+        want = (rows, self.cfg.num_q_heads, self.cfg.head_dim)
+        if x.shape != want or x.dtype != self.dtype or x.device != self.device or not x.is_contiguous():
+            self._refuse(name, x, f"a contiguous {self.dtype} tensor {want}")
 
     def _tokens(self, x, rows, name):
         """Elements between the tokens of k or v; its heads and channels are dense."""
-        c = self.cfg
-        if (tuple(x.shape) != (rows, c.num_kv_heads, c.head_dim) or x.dtype != self.dtype or x.device != self.device
-                or (rows > 0 and (x.stride(2) != 1 or (c.num_kv_heads > 1 and x.stride(1) != c.head_dim)))):
-            raise ValueError(f"{name} must be a {self.dtype} tensor {(rows, c.num_kv_heads, c.head_dim)} on {self.device} "
-                             f"with dense heads, got {x.dtype} {tuple(x.shape)} with strides {x.stride()} on {x.device}")
-        return x.stride(0) if rows > 1 else c.num_kv_heads * c.head_dim
+        heads, dim = self.cfg.num_kv_heads, self.cfg.head_dim
+        stride = x.stride()
+        if (x.shape != (rows, heads, dim) or x.dtype != self.dtype or x.device != self.device
+                or (rows > 0 and (stride[2] != 1 or (heads > 1 and stride[1] != dim)))):
+            self._refuse(name, x, f"a {self.dtype} tensor {(rows, heads, dim)} with dense heads")
+        return stride[0] if rows > 1 else heads * dim
 
     # -- calls -----------------------------------------------------------------------------------------------
     def append(self, layer: int, seq_ids: Sequence[int], n_tokens: Sequence[int], k: torch.Tensor, v: torch.Tensor,
@@ -116,10 +114,11 @@ class BlockCache:
         return k, v
 
     def _attention(self, q, rows, out, stream):
-        self._dense(q, rows, self.cfg.num_q_heads, "q")
+        self._dense(q, rows, "q")
         if out is None:
             return self._empty(q.shape, q.dtype, stream)
-        return self._dense(out, rows, self.cfg.num_q_heads, "out")
+        self._dense(out, rows, "out")
+        return out
 
     def decode_attention(self, layer: int, seq_ids: Sequence[int], q: torch.Tensor, out: Optional[torch.Tensor] = None,
                          scale: Optional[float] = None, stream=None) -> torch.Tensor:

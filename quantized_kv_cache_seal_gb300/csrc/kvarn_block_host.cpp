@@ -534,6 +534,7 @@ kvarn_status kvarn_qk_norm_rope(const kvarn_qk_config* cfg, int64_t n_tokens, co
             return fail(KVARN_EINVAL, "token strides must hold a token's heads and be multiples of 8 elements");
     }
     if (cfg->rot_dim > 0 && (!positions || !freqs)) return fail(KVARN_EINVAL, "no positions or frequencies");
+    if (!aligned16(q_weight) || !aligned16(k_weight)) return fail(KVARN_EINVAL, "weights must be 16-byte aligned");
     QkParams p;
     p.q = (const uint16_t*)q;
     p.k = (const uint16_t*)k;
@@ -556,7 +557,11 @@ kvarn_status kvarn_qk_norm_rope(const kvarn_qk_config* cfg, int64_t n_tokens, co
     p.in_bf16 = cfg->in_type == KVARN_TYPE_BF16;
     p.out_bf16 = cfg->out_type == KVARN_TYPE_BF16;
     p.eps = cfg->eps;
-    p.heads_per_item = n_tokens * (hq + hk) <= 16384 ? 1 : 4;
+    // Heads an item: about 9,700 groups of 16 lanes are resident, so few rows go one a group; more go
+    // four (the rows in flight) and then as many as leave each group two items, up to 16, for the
+    // angle's sake.
+    const int64_t rows = n_tokens * (hq + hk);
+    p.heads_per_item = rows <= 9728 ? 1 : (int32_t)std::min<int64_t>(16, std::max<int64_t>(4, rows / (2 * 9728) / 4 * 4));
     p.items_per_token = (int32_t)((hq + hk + p.heads_per_item - 1) / p.heads_per_item);
     const int rc = launch_qk_norm_rope(p, stream);
     return rc ? cuda_fail(rc, "norm and rotation launch") : KVARN_OK;

@@ -38,10 +38,10 @@ constexpr uint32_t kColS = 0, kColO = 256;
 constexpr int kStep = 128;  // keys of a step
 #define kNegInf (-__int_as_float(0x7f800000))
 
-// p_full: by tile, two halves of 64 keys each (2 b + half); feed: segments handed to the roles
+// feed: segments handed to the roles
 constexpr int kFeed = 8;
-constexpr int kBarKFull = 0, kBarVFull = 4, kBarKEmpty = 8, kBarVEmpty = 10, kBarSFull = 12, kBarPFull = 14, kBarOFull = 18,
-              kBarQFull = 20, kBarDrain = 22, kBarTake = 23, kBarFeedFull = 24, kBarFeedEmpty = kBarFeedFull + kFeed,
+constexpr int kBarKFull = 0, kBarVFull = 4, kBarKEmpty = 8, kBarVEmpty = 10, kBarSFull = 12, kBarPFull = 14, kBarOFull = 16,
+              kBarQFull = 18, kBarDrain = 20, kBarTake = 21, kBarFeedFull = 22, kBarFeedEmpty = kBarFeedFull + kFeed,
               kNumBars = kBarFeedEmpty + kFeed;
 
 template <int D>
@@ -263,8 +263,8 @@ __device__ __forceinline__ int warp_exponent(uint32_t top) {
 // An MMA of this size runs 64 clocks, but takes its warp about 30 turns at a scheduler that it shares
 // with two softmax warps and one of the expansion's, so that the issue, near 100 clocks an MMA, is
 // what bounds a step. The whole warp walks and each MMA is predicated by itself (with a single
-// thread walking, operands go through vector registers: 160 clocks), tiles and halves are unrolled,
-// and waits suspend (polling takes issue slots and shared-memory cycles from everyone). One warp
+// thread walking, operands go through vector registers: 160 clocks), tiles are unrolled, and
+// waits suspend (polling takes issue slots and shared-memory cycles from everyone). One warp
 // issues both tiles' MMAs in turn, which keeps the tiles half a step apart; with a warp a tile they
 // fall into step, both softmaxes run at once and then both tiles' MMAs.
 template <int D>
@@ -292,17 +292,14 @@ __device__ __forceinline__ void issue_role(uint32_t sbase, uint64_t* bars, int32
             for (int b = 0; b < 2; ++b) {
                 if (b >= tiles) break;
                 if (any) {
+                    bar_wait(bars + kBarPFull + b, steps >> b & 1, err);
+                    tc_fence_after();
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {  // 64 keys each
-                        bar_wait(bars + kBarPFull + 2 * b + half, steps >> b & 1, err);
-                        tc_fence_after();
-#pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            if (leader)
-                                mma_ts(kColO + 128 * b, kColS + 128 * b + 32 * half + 8 * ks,
-                                       desc128(v + ((half * (D * 128) + ks * 32) >> 4)), kIdesc<D>,
-                                       ks + half > 0 || j > j0 ? 1u : 0u);
-                    }
+                    for (int ks = 0; ks < 8; ++ks)
+                        if (leader)
+                            mma_ts(kColO + 128 * b, kColS + 128 * b + 8 * ks,
+                                   desc128(v + (((ks >> 2) * (D * 128) + (ks & 3) * 32) >> 4)), kIdesc<D>,
+                                   ks > 0 || j > j0 ? 1u : 0u);
                     steps ^= 1u << b;
                     if (leader && b == tiles - 1) mma_commit(bars + kBarVEmpty + (~jj & 1));
                 } else {
@@ -619,17 +616,12 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, uint8_
             uint32_t r[4][32];
             float mx = kNegInf;
             const bool plain = !bad && __all_sync(0xffffffffu, lim >= kStep);
-            tm_ld32(ts, r[0]);
-            tm_ld32(ts + 32, r[1]);
-            tm_wait_ld();
-            tm_ld32(ts + 64, r[2]);
-            tm_ld32(ts + 96, r[3]);
-            if (__builtin_expect(plain, 1)) {  // over the loads' latency
-                mx = fmaxf(mx, fmaf(max32(r[0]), c[0], lv[0]));
-                mx = fmaxf(mx, fmaf(max32(r[1]), c[1], lv[1]));
-            }
+#pragma unroll
+            for (int ch = 0; ch < 4; ++ch) tm_ld32(ts + 32 * ch, r[ch]);
             tm_wait_ld();
             if (__builtin_expect(plain, 1)) {
+                mx = fmaxf(mx, fmaf(max32(r[0]), c[0], lv[0]));
+                mx = fmaxf(mx, fmaf(max32(r[1]), c[1], lv[1]));
                 mx = fmaxf(mx, fmaf(max32(r[2]), c[2], lv[2]));
                 mx = fmaxf(mx, fmaf(max32(r[3]), c[3], lv[3]));
             } else {
@@ -684,12 +676,10 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, uint8_
                 s0 = __fadd2_rn(s0, s1);
                 l = fmaf(s0.x + s0.y, iv[ch], l);
                 tm_st16(ts + 16 * ch, o);
-                if (ch & 1) {  // 64 keys: their PV may start
-                    tm_wait_st();
-                    tc_fence_before();
-                    mbar_arrive(bars + kBarPFull + 2 * b + (ch >> 1));
-                }
             }
+            tm_wait_st();
+            tc_fence_before();
+            mbar_arrive(bars + kBarPFull + b);
         }
         bar_wait(bars + kBarOFull + b, (uint32_t)(seg++ & 1), err);
         tc_fence_after();
@@ -770,7 +760,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             mbar_init(bars + kBarVEmpty + k, 1);
             mbar_init(bars + kBarSFull + k, 1);
             mbar_init(bars + kBarPFull + k, 128);
-            mbar_init(bars + kBarPFull + 2 + k, 128);
             mbar_init(bars + kBarOFull + k, 1);
             mbar_init(bars + kBarQFull + k, 128);
         }

@@ -4,11 +4,13 @@
 //   by position * freq_i; channels from R on pass through. fp32 throughout, one rounding.
 //
 // Bound by memory: each value is read once and written once. A group of 8, 16 or 32 lanes
-// takes one token and some of its heads, one head row at a time, 8 channels a lane, so
+// takes items (one token, some of its heads), one head row at a time, 8 channels a lane, so
 // that both halves of a pair sit in one lane and only the norm's sum crosses lanes; cos and
-// sin are computed once a token and reused for its heads. The angle is kept as a 64-bit
+// sin are computed once an item and reused for its heads. The angle is kept as a 64-bit
 // fraction of a turn: frac(freq / 2 pi) * 2^64 times the position, modulo 2^64, drops
-// whole turns exactly at any position; its top 32 bits then go to sincospi.
+// whole turns exactly at any position; its top 32 bits then go to sincospi. The fraction is
+// the only fp64 arithmetic (slow on this chip: done once an item it took twice the time of
+// the memory traffic), so groups stay and take items in turn, and it is done once a group.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -19,6 +21,7 @@ namespace kvarn {
 namespace {
 
 constexpr int kQkThreads = 128;
+constexpr int kQkMaxCtas = 152 * 8;  // as many as are resident
 
 template <bool BF16>
 __device__ __forceinline__ float2 unpack2(uint32_t w) {
@@ -38,108 +41,113 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 // Lane l of a group owns channels: interleaved, 8 l .. 8 l + 7; otherwise, for l < R / 8,
 // 4 l .. 4 l + 3 and R / 2 + 4 l .. + 3, and from R on 8 l .. 8 l + 7.
 template <bool IN_BF16, bool OUT_BF16, int LANES>
-__global__ void __launch_bounds__(kQkThreads) qk_kernel(const __grid_constant__ QkParams p) {
-    const int64_t item = ((int64_t)blockIdx.x * kQkThreads + threadIdx.x) / LANES;
+__global__ void __launch_bounds__(kQkThreads, 8) qk_kernel(const __grid_constant__ QkParams p) {
+    constexpr int kAhead = 4;  // rows in flight
     const int l = threadIdx.x % LANES;
-    const int64_t tok = item / p.items_per_token;
     const unsigned group = LANES == 32 ? 0xffffffffu : ((1u << LANES) - 1u) << ((threadIdx.x & 31) / LANES * LANES);
-    if (tok >= p.n_tokens) return;  // whole groups leave
-    const int h0 = (int)(item % p.items_per_token) * p.heads_per_item;
-    const int h1 = min(h0 + p.heads_per_item, p.hq + p.hkv);
     const bool live = 8 * l < p.d;
     const bool turned = 8 * l < p.rot;
     const bool halves = turned && !p.interleaved;
-    const int c0 = halves ? 4 * l : 8 * l;           // first four channels
+    const int c0 = halves ? 4 * l : 8 * l;                  // first four channels
     const int c1 = halves ? p.rot / 2 + 4 * l : 8 * l + 4;  // last four
-    float cs[4], sn[4];
-    if (turned) {
-        const int64_t pos = p.positions[tok];
+    uint64_t frac[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 4; ++i) {
+        frac[i] = 0;
+        if (turned) {
             double f = p.freqs[4 * l + i] * 0.15915494309189533577;  // turns a position
             f -= floor(f);
-            const uint64_t frac = (uint64_t)(f * 18446744073709551616.0);
-            const int32_t top = (int32_t)((frac * (uint64_t)pos) >> 32);
-            sincospif((float)top * 4.656612873077393e-10f, &sn[i], &cs[i]);  // top 2^-32 turns, 2 to a pi
+            frac[i] = (uint64_t)(f * 18446744073709551616.0);
         }
     }
-    float wq[8], wk[8];
-    if (p.q_weight && live && h0 < p.hq)
+    const int items = (int)(p.n_tokens * p.items_per_token), step = gridDim.x * (kQkThreads / LANES);
+    for (int item = (blockIdx.x * kQkThreads + threadIdx.x) / LANES; item < items; item += step) {  // whole groups
+        const int64_t tok = item / p.items_per_token;
+        const int h0 = item % p.items_per_token * p.heads_per_item, h1 = min(h0 + p.heads_per_item, p.hq + p.hkv);
+        const uint16_t* qr = p.q + tok * p.q_stride;
+        const uint16_t* kr = p.k + tok * p.k_stride;
+        uint16_t* qo = p.q_out + tok * p.q_out_stride;
+        uint16_t* ko = p.k_out + tok * p.k_out_stride;
+        float cs[4], sn[4];
+        for (int hb = h0; hb < h1; hb += kAhead) {
+            uint2 a[kAhead], b[kAhead];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) wq[i] = p.q_weight[(i < 4 ? c0 : c1 - 4) + i];
-    if (p.k_weight && live && h1 > p.hq)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) wk[i] = p.k_weight[(i < 4 ? c0 : c1 - 4) + i];
-    const uint16_t* qr = p.q + tok * p.q_stride;
-    const uint16_t* kr = p.k + tok * p.k_stride;
-    uint16_t* qo = p.q_out + tok * p.q_out_stride;
-    uint16_t* ko = p.k_out + tok * p.k_out_stride;
-    constexpr int kAhead = 4;  // rows in flight
-    for (int hb = h0; hb < h1; hb += kAhead) {
-        uint2 a[kAhead], b[kAhead];
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            const int h = hb + u;
-            a[u] = b[u] = make_uint2(0, 0);
-            if (h < h1 && live) {
-                const uint16_t* x = h < p.hq ? qr + (int64_t)h * p.d : kr + (int64_t)(h - p.hq) * p.d;
-                if (halves) {
-                    a[u] = *reinterpret_cast<const uint2*>(x + c0);
-                    b[u] = *reinterpret_cast<const uint2*>(x + c1);
-                } else {
-                    const uint4 w = *reinterpret_cast<const uint4*>(x + c0);
-                    a[u] = make_uint2(w.x, w.y);
-                    b[u] = make_uint2(w.z, w.w);
-                }
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            const int h = hb + u;
-            if (h >= h1) break;  // the same for the whole group
-            float y[8];
-            float2 f;
-            f = unpack2<IN_BF16>(a[u].x), y[0] = f.x, y[1] = f.y;
-            f = unpack2<IN_BF16>(a[u].y), y[2] = f.x, y[3] = f.y;
-            f = unpack2<IN_BF16>(b[u].x), y[4] = f.x, y[5] = f.y;
-            f = unpack2<IN_BF16>(b[u].y), y[6] = f.x, y[7] = f.y;
-            const bool is_q = h < p.hq;
-            if (is_q ? p.q_weight != nullptr : p.k_weight != nullptr) {
-                float ss = 0.f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) ss = fmaf(y[i], y[i], ss);
-#pragma unroll
-                for (int m = LANES / 2; m > 0; m >>= 1) ss += __shfl_xor_sync(group, ss, m);
-                const float rs = rsqrtf(ss / (float)p.d + p.eps);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] *= rs * (is_q ? wq[i] : wk[i]);
-            }
-            if (turned) {
-                if (p.interleaved) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float u0 = y[2 * i], u1 = y[2 * i + 1];
-                        y[2 * i] = u0 * cs[i] - u1 * sn[i];
-                        y[2 * i + 1] = u1 * cs[i] + u0 * sn[i];
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float u0 = y[i], u1 = y[4 + i];
-                        y[i] = u0 * cs[i] - u1 * sn[i];
-                        y[4 + i] = u1 * cs[i] + u0 * sn[i];
+            for (int u = 0; u < kAhead; ++u) {
+                const int h = hb + u;
+                a[u] = b[u] = make_uint2(0, 0);
+                if (h < h1 && live) {
+                    const uint16_t* x = h < p.hq ? qr + (int64_t)h * p.d : kr + (int64_t)(h - p.hq) * p.d;
+                    if (halves) {
+                        a[u] = *reinterpret_cast<const uint2*>(x + c0);
+                        b[u] = *reinterpret_cast<const uint2*>(x + c1);
+                    } else {
+                        const uint4 w = *reinterpret_cast<const uint4*>(x + c0);
+                        a[u] = make_uint2(w.x, w.y);
+                        b[u] = make_uint2(w.z, w.w);
                     }
                 }
             }
-            if (live) {
-                uint16_t* o = is_q ? qo + (int64_t)h * p.d : ko + (int64_t)(h - p.hq) * p.d;
-                const uint2 lo = make_uint2(pack2<OUT_BF16>(y[0], y[1]), pack2<OUT_BF16>(y[2], y[3]));
-                const uint2 hi = make_uint2(pack2<OUT_BF16>(y[4], y[5]), pack2<OUT_BF16>(y[6], y[7]));
-                if (halves) {
-                    *reinterpret_cast<uint2*>(o + c0) = lo;
-                    *reinterpret_cast<uint2*>(o + c1) = hi;
-                } else {
-                    *reinterpret_cast<uint4*>(o + c0) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+            if (hb == h0 && turned) {  // over the loads' latency
+                const int64_t pos = p.positions[tok];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int32_t top = (int32_t)((frac[i] * (uint64_t)pos) >> 32);
+                    sincospif((float)top * 4.656612873077393e-10f, &sn[i], &cs[i]);  // top 2^-32 turns, 2 to a pi
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int h = hb + u;
+                if (h >= h1) break;  // the same for the whole group
+                float y[8];
+                float2 f;
+                f = unpack2<IN_BF16>(a[u].x), y[0] = f.x, y[1] = f.y;
+                f = unpack2<IN_BF16>(a[u].y), y[2] = f.x, y[3] = f.y;
+                f = unpack2<IN_BF16>(b[u].x), y[4] = f.x, y[5] = f.y;
+                f = unpack2<IN_BF16>(b[u].y), y[6] = f.x, y[7] = f.y;
+                const bool is_q = h < p.hq;
+                const float* wt = is_q ? p.q_weight : p.k_weight;
+                if (wt) {
+                    float ss = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) ss = fmaf(y[i], y[i], ss);
+#pragma unroll
+                    for (int m = LANES / 2; m > 0; m >>= 1) ss += __shfl_xor_sync(group, ss, m);
+                    const float rs = rsqrtf(ss / (float)p.d + p.eps);
+                    if (live) {  // 1 KB at most: from the first cache
+                        const float4 w0 = __ldg(reinterpret_cast<const float4*>(wt + c0));
+                        const float4 w1 = __ldg(reinterpret_cast<const float4*>(wt + c1));
+                        y[0] *= rs * w0.x, y[1] *= rs * w0.y, y[2] *= rs * w0.z, y[3] *= rs * w0.w;
+                        y[4] *= rs * w1.x, y[5] *= rs * w1.y, y[6] *= rs * w1.z, y[7] *= rs * w1.w;
+                    }
+                }
+                if (turned) {
+                    if (p.interleaved) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float u0 = y[2 * i], u1 = y[2 * i + 1];
+                            y[2 * i] = u0 * cs[i] - u1 * sn[i];
+                            y[2 * i + 1] = u1 * cs[i] + u0 * sn[i];
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float u0 = y[i], u1 = y[4 + i];
+                            y[i] = u0 * cs[i] - u1 * sn[i];
+                            y[4 + i] = u1 * cs[i] + u0 * sn[i];
+                        }
+                    }
+                }
+                if (live) {
+                    uint16_t* o = is_q ? qo + (int64_t)h * p.d : ko + (int64_t)(h - p.hq) * p.d;
+                    const uint2 lo = make_uint2(pack2<OUT_BF16>(y[0], y[1]), pack2<OUT_BF16>(y[2], y[3]));
+                    const uint2 hi = make_uint2(pack2<OUT_BF16>(y[4], y[5]), pack2<OUT_BF16>(y[6], y[7]));
+                    if (halves) {
+                        *reinterpret_cast<uint2*>(o + c0) = lo;
+                        *reinterpret_cast<uint2*>(o + c1) = hi;
+                    } else {
+                        *reinterpret_cast<uint4*>(o + c0) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+                    }
                 }
             }
         }
@@ -149,9 +157,8 @@ __global__ void __launch_bounds__(kQkThreads) qk_kernel(const __grid_constant__ 
 template <bool I, bool O>
 int launch_qk(const QkParams& p, cudaStream_t s) {
     const int lanes = p.d <= 64 ? 8 : p.d <= 128 ? 16 : 32;
-    const int64_t items = p.n_tokens * p.items_per_token;
-    const int64_t ctas = (items * lanes + kQkThreads - 1) / kQkThreads;
-    const dim3 grid((unsigned)ctas);
+    const int64_t ctas = (p.n_tokens * p.items_per_token * lanes + kQkThreads - 1) / kQkThreads;
+    const unsigned grid = (unsigned)(ctas < kQkMaxCtas ? ctas : kQkMaxCtas);
     if (lanes == 8) qk_kernel<I, O, 8><<<grid, kQkThreads, 0, s>>>(p);
     else if (lanes == 16) qk_kernel<I, O, 16><<<grid, kQkThreads, 0, s>>>(p);
     else qk_kernel<I, O, 32><<<grid, kQkThreads, 0, s>>>(p);

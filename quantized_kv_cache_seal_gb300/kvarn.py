@@ -8,6 +8,7 @@ import of this module fails.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Sequence
@@ -328,6 +329,37 @@ def kvarn_last_error() -> str:
     return load().kvarn_last_error().decode()
 
 
+_HERE = contextlib.nullcontext()
+
+
+def on_device(device):
+    """`device` (a torch.device with an index) as the current one; nothing to do where it is."""
+    import torch
+
+    if device.type != "cuda" or torch.cuda.current_device() == device.index:
+        return _HERE
+    return torch.cuda.device(device)
+
+
+def current_stream(device) -> int:
+    """The current stream of a CUDA device, as an address."""
+    import torch
+
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _i32(xs):
+    """A host int32 array of a sequence of ints."""
+    n = len(xs)
+    kind = _ARRAYS.get(n)
+    if kind is None:
+        kind = _ARRAYS[n] = ctypes.c_int32 * n
+    return kind(*xs)
+
+
+_ARRAYS: dict = {}
+
+
 def _check_why(rc: int, where: str):
     """As _check, with the library's reason for any refusal (the block cache and norm calls set one)."""
     if rc != 0:
@@ -352,43 +384,43 @@ def kvarn_block_destroy(handle: int) -> None:
 
 
 def kvarn_block_append(handle, layer, seq_ids, n_tokens, k, k_stride, v, v_stride, stream=None):
-    _check_why(load().kvarn_block_append(handle, layer, len(seq_ids), _ints(seq_ids), _ints(n_tokens), _ptr(k),
+    _check_why(load().kvarn_block_append(handle, layer, len(seq_ids), _i32(seq_ids), _i32(n_tokens), _ptr(k),
                                          k_stride, _ptr(v), v_stride, _stream(stream)), "kvarn_block_append")
 
 
 def kvarn_block_read(handle, layer, seq_ids, starts, counts, k, v, out_fp32=False, stream=None):
-    _check_why(load().kvarn_block_read(handle, layer, len(seq_ids), _ints(seq_ids),
-                                       None if starts is None else _ints(starts), _ints(counts), _ptr(k), _ptr(v),
+    _check_why(load().kvarn_block_read(handle, layer, len(seq_ids), _i32(seq_ids),
+                                       None if starts is None else _i32(starts), _i32(counts), _ptr(k), _ptr(v),
                                        int(bool(out_fp32)), _stream(stream)), "kvarn_block_read")
 
 
 def kvarn_block_decode_attention(handle, layer, seq_ids, q, out, softmax_scale, stream=None):
-    _check_why(load().kvarn_block_decode_attention(handle, layer, len(seq_ids), _ints(seq_ids), _ptr(q), _ptr(out),
+    _check_why(load().kvarn_block_decode_attention(handle, layer, len(seq_ids), _i32(seq_ids), _ptr(q), _ptr(out),
                                                    float(softmax_scale), _stream(stream)),
                "kvarn_block_decode_attention")
 
 
 def kvarn_block_decode_step(handle, layer, seq_ids, k, k_stride, v, v_stride, q, out, softmax_scale, stream=None):
-    _check_why(load().kvarn_block_decode_step(handle, layer, len(seq_ids), _ints(seq_ids), _ptr(k), k_stride, _ptr(v),
+    _check_why(load().kvarn_block_decode_step(handle, layer, len(seq_ids), _i32(seq_ids), _ptr(k), k_stride, _ptr(v),
                                               v_stride, _ptr(q), _ptr(out), float(softmax_scale), _stream(stream)),
                "kvarn_block_decode_step")
 
 
 def kvarn_block_prefill_attention(handle, layer, seq_ids, q_lens, q, out, softmax_scale, stream=None):
-    _check_why(load().kvarn_block_prefill_attention(handle, layer, len(seq_ids), _ints(seq_ids), _ints(q_lens),
+    _check_why(load().kvarn_block_prefill_attention(handle, layer, len(seq_ids), _i32(seq_ids), _i32(q_lens),
                                                     _ptr(q), _ptr(out), float(softmax_scale), _stream(stream)),
                "kvarn_block_prefill_attention")
 
 
 def kvarn_block_prefill(handle, layer, seq_ids, n_tokens, k, k_stride, v, v_stride, q, out, softmax_scale,
                         stream=None):
-    _check_why(load().kvarn_block_prefill(handle, layer, len(seq_ids), _ints(seq_ids), _ints(n_tokens), _ptr(k),
+    _check_why(load().kvarn_block_prefill(handle, layer, len(seq_ids), _i32(seq_ids), _i32(n_tokens), _ptr(k),
                                           k_stride, _ptr(v), v_stride, _ptr(q), _ptr(out), float(softmax_scale),
                                           _stream(stream)), "kvarn_block_prefill")
 
 
 def kvarn_block_release(handle, seq_ids):
-    _check_why(load().kvarn_block_release(handle, len(seq_ids), _ints(seq_ids)), "kvarn_block_release")
+    _check_why(load().kvarn_block_release(handle, len(seq_ids), _i32(seq_ids)), "kvarn_block_release")
 
 
 def kvarn_block_length(handle, layer, seq_id) -> int:
