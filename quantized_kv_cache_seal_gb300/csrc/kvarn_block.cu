@@ -79,8 +79,8 @@ __global__ void __launch_bounds__(kWriteThreads) append_kernel(const __grid_cons
                 uint32_t w[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
-                    w[q] = (uint32_t)tail[(size_t)(8 * c8 + 2 * q) * bt + pos % bt] |
-                           ((uint32_t)tail[(size_t)(8 * c8 + 2 * q + 1) * bt + pos % bt] << 16);
+                    w[q] = (uint32_t)tail[tail_v_off(d, pos % bt, 8 * c8 + 2 * q)] |
+                           ((uint32_t)tail[tail_v_off(d, pos % bt, 8 * c8 + 2 * q + 1)] << 16);
                 x[u] = make_uint4(w[0], w[1], w[2], w[3]);
             }
         }
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kWriteThreads) append_kernel(const __grid_cons
                 const uint32_t v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                 for (int y = 0; y < 8; ++y)
-                    tail[(size_t)(ch + y) * bt + pos % bt] = (uint16_t)(v[y >> 1] >> (16 * (y & 1)));
+                    tail[tail_v_off(d, pos % bt, ch + y)] = (uint16_t)(v[y >> 1] >> (16 * (y & 1)));
             }
         }
     }
@@ -281,8 +281,8 @@ __global__ void __launch_bounds__(kWriteThreads) read_kernel(const __grid_consta
                 uint32_t v[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
-                    v[q] = (uint32_t)tail[(size_t)(8 * c8 + 2 * q) * c.block + (pos - sealed)] |
-                           ((uint32_t)tail[(size_t)(8 * c8 + 2 * q + 1) * c.block + (pos - sealed)] << 16);
+                    v[q] = (uint32_t)tail[tail_v_off(d, pos - sealed, 8 * c8 + 2 * q)] |
+                           ((uint32_t)tail[tail_v_off(d, pos - sealed, 8 * c8 + 2 * q + 1)] << 16);
                 w = make_uint4(v[0], v[1], v[2], v[3]);
             }
             const size_t o = ((size_t)e.out_row + (pos - e.start)) * row + at;

@@ -33,6 +33,9 @@ KVARN_HD inline int v_code_off(int d, int tok, int ch) {
     return 16 + kTileTokens * d + (ch >> 4) * 512 + ((ch & 7) * 4 + (tok >> 3)) * 16 + ((ch >> 3) & 1) * 8;
 }
 
+// element of the exact V of (row of the block, channel)
+KVARN_HD inline int tail_v_off(int d, int row, int ch) { return ((row >> 5) * d + ch) * kTileTokens + (row & 31); }
+
 struct BlockLayout {
     size_t err;       // int32[4]
     size_t table;     // int32[max_seqs][num_layers][max_blocks]: pool slot of each sealed block
@@ -41,7 +44,7 @@ struct BlockLayout {
     size_t partials;  // float[kBlockMaxGrid][2][8 (D + 2)] of a decode call, or
                       // float[kBlockPrefillGrid][2][256 (D + 2)] of a prefill call
     size_t tail_k;    // T[max_seqs][num_layers][Hkv][B][D]: exact rows of the partial block
-    size_t tail_v;    // T[max_seqs][num_layers][Hkv][D][B]: the same for V, channel-major
+    size_t tail_v;    // T[max_seqs][num_layers][Hkv][B / 32][D][32]: the same for V, channel rows of each 32 tokens
     size_t pool;      // slots of Hkv * (B / 32) tiles
     size_t total;
 };

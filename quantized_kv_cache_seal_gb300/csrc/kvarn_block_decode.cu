@@ -11,15 +11,16 @@
 //
 // Bound by memory: 4 r operations of a KV head's r query heads per 2 code bytes. All (sequence,
 // KV head) pairs form one line of 32-token tiles that is cut evenly over the CTAs, one a SM;
-// the warps of a CTA take its tiles in turn. A tile is one contiguous record that a warp
+// the warps of a CTA take its tiles in turn. A tile is one contiguous record (two where it is exact)
+// that a warp
 // fetches with one bulk copy into a ring of its own (three deep at head_dim 128: 197 KB in
 // flight a SM, which covers the latency four times), so that no barrier joins the warps but at
 // the end of a (sequence, KV head). Codes lie in the order of mma.m16n8k16's A operand:
 // K (tokens x channels) x q gives S^T, whose accumulators become the weights' B operand for
 // V^T (channels x tokens) by one movmatrix each; heads are the 8 columns, so up to 8 query
-// heads cost the same. Warps join in shared memory, CTAs that share a pair through a
-// workspace, added in the order of the cuts by whichever arrives last: results do not
-// depend on timing.
+// heads cost the same. Warps join in shared memory and CTAs that share a pair through a
+// workspace, each added in a fixed order by whichever comes last: results do not depend on
+// timing.
 #include "kvarn_block_dev.cuh"
 
 namespace kvarn {
@@ -30,16 +31,17 @@ constexpr int kWarps = 8, kThreads = 32 * kWarps;
 
 template <int D>
 struct Shape {
-    static constexpr int kTile = 16 + 2 * kTileTokens * D;
+    static constexpr int kTile = 16 + 2 * kTileTokens * D;  // a sealed tile; an exact one's K or V is 16 bytes less
     static constexpr int kStages = D == 128 ? 3 : 6;
     static constexpr int kHeadStride = D + 8;  // floats of a head in the join buffer: the two heads of a lane pair sit 16 banks apart
     static constexpr int kRing = kWarps * kStages * kTile;
     static constexpr int kJoin = kRing;                                    // float[warps][4][D + 8]
-    static constexpr int kM = kJoin + kWarps * 4 * kHeadStride * 4;        // float[warps][8]
-    static constexpr int kL = kM + kWarps * 8 * 4;
-    static constexpr int kBars = kL + kWarps * 8 * 4;
-    static constexpr int kFlag = kBars + kWarps * kStages * 8;
-    static constexpr int kSmem = kFlag + 16;
+    static constexpr int kM = kJoin + kWarps * 4 * kHeadStride * 4;        // float[warps][4]
+    static constexpr int kL = kM + kWarps * 4 * 4;
+    static constexpr int kBars = kL + kWarps * 4 * 4;
+    static constexpr int kFree = kBars + kWarps * kStages * 8;             // barrier: the join buffer may be written again
+    static constexpr int kCount = kFree + 8;                               // int: warps that have written it
+    static constexpr int kSmem = kCount + 8;
     static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
 };
 
@@ -185,10 +187,10 @@ __device__ __forceinline__ void sealed_unit(State<D>& st, const uint8_t* t, cons
     }
 }
 
-// 32 exact tokens (nv of them valid) from the tail: rows k, channel-major v (stride `block`). bf16
+// 32 exact tokens (nv of them valid) from the tail: rows k, channel rows v of 32 tokens. bf16
 // values become f16 after the tile's own exact powers of two, as the queries do.
 template <int D, bool BF16>
-__device__ __forceinline__ void exact_unit(State<D>& st, const uint16_t* k, const uint16_t* v, int block, int nv,
+__device__ __forceinline__ void exact_unit(State<D>& st, const uint16_t* k, const uint16_t* v, int nv,
                                            const uint32_t (&q)[D / 64][4][2], float c0, float c1, int lane) {
     const int g = lane >> 2, t = lane & 3;
     float ks = 1.f, vs = 1.f, lv = 0.f, ivs = 1.f;
@@ -206,7 +208,7 @@ __device__ __forceinline__ void exact_unit(State<D>& st, const uint16_t* k, cons
 #pragma unroll
                     for (int z = 0; z < 2; ++z) {
                         uint4 r = make_uint4(0, 0, 0, 0);
-                        if (tok < nv) r = *reinterpret_cast<const uint4*>(k + (size_t)tok * D + 64 * c + 16 * t + 8 * z);
+                        if (tok < nv) r = *reinterpret_cast<const uint4*>(k + tok * D + 64 * c + 16 * t + 8 * z);
                         x[a][c][b][z] = r;
                         if (BF16) top = max_of(top, r);
                     }
@@ -247,7 +249,7 @@ __device__ __forceinline__ void exact_unit(State<D>& st, const uint16_t* k, cons
     for (int i = 0; i < D / 16; ++i)
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-            uint4 r = *reinterpret_cast<const uint4*>(v + (size_t)(16 * i + g + 8 * b) * block + 8 * t);
+            uint4 r = *reinterpret_cast<const uint4*>(v + (16 * i + g + 8 * b) * kTileTokens + 8 * t);
             r = make_uint4(r.x & keep[0], r.y & keep[1], r.z & keep[2], r.w & keep[3]);
             y[i][b] = r;
             if (BF16) top = max_of(top, r);
@@ -278,6 +280,119 @@ __device__ __forceinline__ void exact_unit(State<D>& st, const uint16_t* k, cons
         }
 }
 
+// Heads h0 .. h0 + heads - 1 (four at most) of one (sequence, KV head) from the warps' states in the join
+// buffer, by one warp, a lane 4 channels (at head_dim 64 half the lanes). Where the CTA holds only a part of
+// the pair, the part goes to the workspace, and whichever part comes last adds them all in the order of the
+// cuts. out: first head of the pair.
+template <int D, bool BF16>
+__device__ void join_heads(const BlockDecodeParams& p, const uint8_t* smem, const Cursor& cur, bool whole, bool starts, int half,
+                           uint16_t* out, int lane) {
+    using Sh = Shape<D>;
+    const float* join = reinterpret_cast<const float*>(smem + Sh::kJoin);
+    const float* sm = reinterpret_cast<const float*>(smem + Sh::kM);
+    const float* sl = reinterpret_cast<const float*>(smem + Sh::kL);
+    const int heads = min(4, p.r - 4 * half), b = blockIdx.x;
+    const bool live = 4 * lane < D;
+    constexpr size_t kPart = 8 * (D + 2);  // floats: O [8][D], m [8], l [8]
+    float* partials = reinterpret_cast<float*>(p.c.base + p.c.lay.partials);
+    float* mine = partials + (size_t)(2 * b + (starts ? 1 : 0)) * kPart;
+    auto give = [&](int head, float4 o, float l) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        if (live)
+            *reinterpret_cast<uint2*>(out + (size_t)head * D + 4 * lane) =
+                make_uint2(pack2<BF16>(o.x * inv, o.y * inv), pack2<BF16>(o.z * inv, o.w * inv));
+    };
+#pragma unroll 1
+    for (int h = 0; h < heads; ++h) {
+        float big = kNegInf, l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int z = 0; z < kWarps; ++z) big = fmaxf(big, sm[z * 4 + h]);
+#pragma unroll
+        for (int z = 0; z < kWarps; ++z) {
+            const float mz = sm[z * 4 + h], f = mz == kNegInf ? 1.f : ex2(mz - big);  // -inf: zeros or NaN
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (live) x = *reinterpret_cast<const float4*>(join + (z * 4 + h) * Sh::kHeadStride + 4 * lane);
+            o.x = fmaf(x.x, f, o.x);
+            o.y = fmaf(x.y, f, o.y);
+            o.z = fmaf(x.z, f, o.z);
+            o.w = fmaf(x.w, f, o.w);
+            l = fmaf(sl[z * 4 + h], f, l);
+        }
+        if (whole) {
+            give(4 * half + h, o, l);
+        } else {
+            if (live) *reinterpret_cast<float4*>(mine + (4 * half + h) * D + 4 * lane) = o;
+            if (lane == 0) mine[8 * D + 4 * half + h] = big, mine[8 * D + 8 + 4 * half + h] = l;
+        }
+    }
+    if (whole || 4 * half + heads < p.r) return;
+    // CTAs first .. last share the pair; its first one's counter takes the arrivals
+    int32_t* counters = reinterpret_cast<int32_t*>(p.c.base + p.c.lay.counters);
+    const int first = (int)((((int64_t)cur.begin + 1) * p.grid - 1) / p.units);
+    const int last = (int)(((int64_t)cur.end * p.grid - 1) / p.units);
+    __threadfence();
+    __syncwarp();
+    int n = 0;
+    if (lane == 0) n = atomicAdd(counters + first, 1);
+    if (__shfl_sync(0xffffffffu, n, 0) != last - first) return;
+    if (lane == 0) counters[first] = 0;
+    __threadfence();
+    // part z of CTA first + z: slot 1 of the first, slot 0 of the others
+    auto part = [&](int z) { return partials + (size_t)(2 * (first + z) + (z == 0 ? 1 : 0)) * kPart; };
+#pragma unroll 1
+    for (int h0 = 0; h0 < p.r; h0 += 4) {
+        float big[4], l[4];
+        float4 o[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) big[y] = kNegInf, l[y] = 0.f, o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int z0 = 0; z0 <= last - first; z0 += 32) {  // 32 parts at a time, a lane their m and l
+            const int parts = min(32, last - first + 1 - z0);
+            float f[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const int h = min(h0 + y, p.r - 1);
+                float m = kNegInf, s = 0.f;
+                if (lane < parts) {
+                    m = __ldcg(part(z0 + lane) + 8 * D + h);
+                    s = __ldcg(part(z0 + lane) + 8 * D + 8 + h);
+                }
+                float top = m;
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                top = fmaxf(top, big[y]);
+                f[y] = m == kNegInf ? 1.f : ex2(m - top);
+                s *= f[y];
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+                const float g = big[y] == kNegInf ? 1.f : ex2(big[y] - top);
+                l[y] = fmaf(l[y], g, s);
+                o[y].x *= g, o[y].y *= g, o[y].z *= g, o[y].w *= g;
+                big[y] = top;
+            }
+#pragma unroll 4
+            for (int z = 0; z < parts; ++z) {
+                const float* at = part(z0 + z) + 4 * lane;
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const int h = min(h0 + y, p.r - 1);
+                    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (live) x = __ldcg(reinterpret_cast<const float4*>(at + h * D));
+                    const float w = __shfl_sync(0xffffffffu, f[y], z);
+                    o[y].x = fmaf(x.x, w, o[y].x);
+                    o[y].y = fmaf(x.y, w, o[y].y);
+                    o[y].z = fmaf(x.z, w, o[y].z);
+                    o[y].w = fmaf(x.w, w, o[y].w);
+                }
+            }
+        }
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+            if (h0 + y < p.r) give(h0 + y, o[y], l[y]);
+    }
+}
+
 template <int D, bool INT8, bool BF16>
 __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_constant__ BlockDecodeParams p) {
     using Sh = Shape<D>;
@@ -289,53 +404,64 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     float* join = reinterpret_cast<float*>(smem + Sh::kJoin);
     float* sm = reinterpret_cast<float*>(smem + Sh::kM);
     float* sl = reinterpret_cast<float*>(smem + Sh::kL);
-    int* flag = reinterpret_cast<int*>(smem + Sh::kFlag);
+    uint64_t* free_bar = reinterpret_cast<uint64_t*>(smem + Sh::kFree);
+    int* count = reinterpret_cast<int*>(smem + Sh::kCount);
     int32_t* err = reinterpret_cast<int32_t*>(c.base + c.lay.err);
-    int32_t* counters = reinterpret_cast<int32_t*>(c.base + c.lay.counters);
-    float* partials = reinterpret_cast<float*>(c.base + c.lay.partials);
     const int b = blockIdx.x;
     const int u0 = (int)(p.units * b / p.grid), u1 = (int)(p.units * (b + 1) / p.grid);
     if (lane < Sh::kStages) mbar_init(bars + lane, 1);
+    if (threadIdx.x == 0) {
+        mbar_init(free_bar, 1);
+        *count = 0;
+    }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    __syncwarp();
+    __syncthreads();
 
-    // copies run ahead of the work: the next sealed tile of this warp, and its slot
+    // Copies run ahead of the work: a sealed tile takes one ring entry, an exact one two (K rows, V
+    // channel rows), an empty sequence's unit none. The next tile's slot is loaded a step early.
     Cursor ahead;
-    int ua = u0 + w, slot = 0, issued = 0;
+    int ua = u0 + w, slot = 0, issued = 0, done = 0;  // issued, done: ring entries
     const int sh = c.log2_block - 5;
-    auto seek = [&]() {  // from ua on, the next sealed tile; its slot is loaded a step early
-        while (ua < u1) {
-            ahead.advance(p, ua);
-            const BlockDecodeSeq& e = p.seqs[ahead.i];
-            const int tile = ua - ahead.begin;
-            if (tile < e.n >> c.log2_block << sh) {
-                slot = __ldg(block_table(c, e.seq) + (tile >> sh));
-                return;
-            }
-            ua += kWarps;
-        }
-    };
-    auto fetch = [&]() {
+    auto seek = [&]() {
         if (ua >= u1) return;
+        ahead.advance(p, ua);
+        const BlockDecodeSeq& e = p.seqs[ahead.i];
+        const int tile = ua - ahead.begin;
+        slot = -1;
+        if (tile < e.n >> c.log2_block << sh) slot = __ldg(block_table(c, e.seq) + (tile >> sh));
+    };
+    auto entry = [&](const void* src, uint32_t bytes) {
         if (lane == 0) {
             const int st = issued % Sh::kStages;
-            const uint8_t* src = tile_ptr(c, slot, ahead.h, (ua - ahead.begin) & ((1 << sh) - 1));
-            mbar_arrive_expect_tx(bars + st, Sh::kTile);
-            bulk_g2s(ring + st * Sh::kTile, src, Sh::kTile, bars + st);
+            mbar_arrive_expect_tx(bars + st, bytes);
+            bulk_g2s(ring + st * Sh::kTile, src, bytes, bars + st);
         }
         ++issued;
-        ua += kWarps;
-        seek();
+    };
+    auto pump = [&]() {
+#pragma unroll 1
+        while (ua < u1 && issued - done + (slot < 0 ? 2 : 1) <= Sh::kStages) {
+            const BlockDecodeSeq& e = p.seqs[ahead.i];
+            const int tile = ua - ahead.begin, sealed = e.n >> c.log2_block << sh;
+            if (slot >= 0) {
+                entry(tile_ptr(c, slot, ahead.h, tile & ((1 << sh) - 1)), Sh::kTile);
+            } else if (tile * kTileTokens < e.n) {
+                constexpr uint32_t kSide = kTileTokens * D * 2;
+                const size_t at = (size_t)(tile - sealed) * (kTileTokens * D);
+                entry(tail_ptr(c, c.lay.tail_k, e.seq, ahead.h) + at, kSide);
+                entry(tail_ptr(c, c.lay.tail_v, e.seq, ahead.h) + at, kSide);
+            }
+            ua += kWarps;
+            seek();
+        }
     };
     Cursor cur;
     cur.start(p, u0);
     ahead = cur;
     seek();
-#pragma unroll 1
-    for (int i = 0; i < Sh::kStages; ++i) fetch();
+    pump();
 
-    int done = 0;  // sealed tiles taken from the ring
-    int u = u0 + w;
+    int u = u0 + w, joins = 0;
     for (int begin = u0; begin < u1; begin = min(cur.end, u1)) {
         cur.advance(p, begin);
         const BlockDecodeSeq& e = p.seqs[cur.i];
@@ -392,105 +518,60 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                 bar_wait(bars + s, (uint32_t)(done / Sh::kStages & 1), err);
                 sealed_unit<D, INT8>(st, ring + s * Sh::kTile, q, c0, c1, lane);
                 ++done;
-                __syncwarp();
-                fetch();
-            } else {
-                const int first = (tile - sealed) * kTileTokens;  // row of the tail
-                const int nv = min(kTileTokens, e.n - tile * kTileTokens);
-                if (nv > 0)
-                    exact_unit<D, BF16>(st, tail_ptr(c, c.lay.tail_k, e.seq, cur.h) + (size_t)first * D,
-                                        tail_ptr(c, c.lay.tail_v, e.seq, cur.h) + first, c.block, nv, q, c0, c1, lane);
+            } else if (const int nv = min(kTileTokens, e.n - tile * kTileTokens); nv > 0) {
+                const int s = done % Sh::kStages, s2 = (done + 1) % Sh::kStages;
+                bar_wait(bars + s, (uint32_t)(done / Sh::kStages & 1), err);
+                bar_wait(bars + s2, (uint32_t)((done + 1) / Sh::kStages & 1), err);
+                exact_unit<D, BF16>(st, reinterpret_cast<const uint16_t*>(ring + s * Sh::kTile),
+                                    reinterpret_cast<const uint16_t*>(ring + s2 * Sh::kTile), nv, q, c0, c1, lane);
+                done += 2;
             }
+            __syncwarp();
+            pump();
         }
-        // join the warps
+        // Join the warps, four heads at a time: each puts its state into the buffer and goes on; the last
+        // one to come adds them. (A barrier here left the memory idle at every pair's end.)
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) {
             st.l[0] += __shfl_xor_sync(0xffffffffu, st.l[0], d);
             st.l[1] += __shfl_xor_sync(0xffffffffu, st.l[1], d);
         }
-        if (g == 0) {
-            sm[w * 8 + 2 * t] = st.m[0];
-            sm[w * 8 + 2 * t + 1] = st.m[1];
-            sl[w * 8 + 2 * t] = st.l[0];
-            sl[w * 8 + 2 * t + 1] = st.l[1];
-        }
-        __syncthreads();
-        float big0 = kNegInf, big1 = kNegInf;
-#pragma unroll
-        for (int z = 0; z < kWarps; ++z) {
-            big0 = fmaxf(big0, sm[z * 8 + 2 * t]);
-            big1 = fmaxf(big1, sm[z * 8 + 2 * t + 1]);
-        }
-        const float f0 = st.m[0] == kNegInf ? (st.l[0] == 0.f ? 0.f : 1.f) : ex2(st.m[0] - big0);
-        const float f1 = st.m[1] == kNegInf ? (st.l[1] == 0.f ? 0.f : 1.f) : ex2(st.m[1] - big1);
         const bool whole = begin == cur.begin && end == cur.end;
-        float* part = partials + (size_t)(2 * b + (begin == cur.begin ? 1 : 0)) * (8 * (D + 2));
-        for (int half = 0; half < (p.r > 4 ? 2 : 1); ++half) {
-            if (half) __syncthreads();
+#pragma unroll 1
+        for (int half = 0; half < (p.r > 4 ? 2 : 1); ++half, ++joins) {
+            if (joins > 0) bar_wait(free_bar, (uint32_t)((joins - 1) & 1), err);
             if (t >> 1 == half) {
-                float* at = join + (w * 4 + 2 * (t & 1)) * Sh::kHeadStride + g;
+                const int h = 2 * (t & 1);
+                float* at = join + (w * 4 + h) * Sh::kHeadStride + g;
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
-                    at[16 * i] = st.o[i][0] * f0;
-                    at[16 * i + 8] = st.o[i][2] * f0;
-                    at[16 * i + Sh::kHeadStride] = st.o[i][1] * f1;
-                    at[16 * i + 8 + Sh::kHeadStride] = st.o[i][3] * f1;
+                    at[16 * i] = st.o[i][0];
+                    at[16 * i + 8] = st.o[i][2];
+                    at[16 * i + Sh::kHeadStride] = st.o[i][1];
+                    at[16 * i + 8 + Sh::kHeadStride] = st.o[i][3];
+                }
+                if (g == 0) {
+                    sm[w * 4 + h] = st.m[0];
+                    sm[w * 4 + h + 1] = st.m[1];
+                    sl[w * 4 + h] = st.l[0];
+                    sl[w * 4 + h + 1] = st.l[1];
                 }
             }
-            __syncthreads();
-            const int heads = min(4, p.r - 4 * half);
-            for (int x = threadIdx.x; x < heads * D; x += kThreads) {
-                const int hl = x / D, d = x % D, head = 4 * half + hl;
-                float big = kNegInf, sum = 0.f, l = 0.f;
-#pragma unroll
-                for (int z = 0; z < kWarps; ++z) big = fmaxf(big, sm[z * 8 + head]);
-#pragma unroll
-                for (int z = 0; z < kWarps; ++z) {
-                    sum += join[(z * 4 + hl) * Sh::kHeadStride + d];
-                    const float mz = sm[z * 8 + head], lz = sl[z * 8 + head];
-                    l += mz == kNegInf ? lz : lz * ex2(mz - big);  // -inf with a sum: NaN logits
-                }
-                if (whole) {
-                    p.out[((size_t)cur.i * p.hq + h0 + head) * D + d] = (uint16_t)pack2<BF16>(l == 0.f ? 0.f : sum / l, 0.f);
-                } else {
-                    part[head * (D + 2) + d] = sum;
-                    if (d == 0) part[head * (D + 2) + D] = big, part[head * (D + 2) + D + 1] = l;
-                }
-            }
-        }
-        if (!whole) {
-            // CTAs first .. last share the pair; its first one's counter takes the arrivals
-            const int first = (int)((((int64_t)cur.begin + 1) * p.grid - 1) / p.units);
-            const int last = (int)(((int64_t)cur.end * p.grid - 1) / p.units);
-            __threadfence();
-            __syncthreads();
-            if (threadIdx.x == 0) {
-                const int n = atomicAdd(counters + first, 1);
-                *flag = n == last - first;
-                if (*flag) counters[first] = 0;
-            }
-            __syncthreads();
-            if (*flag) {
-                __threadfence();
-                for (int x = threadIdx.x; x < p.r * D; x += kThreads) {
-                    const int head = x / D, d = x % D;
-                    const float* at = partials + (size_t)(2 * first + 1) * (8 * (D + 2)) + head * (D + 2);
-                    const size_t step = 2 * 8 * (D + 2);
-                    // part z of CTA first + z: slot 1 of the first, slot 0 of the others
-                    auto ptr = [&](int z) { return z ? at + z * step - step / 2 : at; };
-                    float big = kNegInf, sum = 0.f, l = 0.f;
-                    for (int z = 0; z <= last - first; ++z) big = fmaxf(big, __ldcg(ptr(z) + D));
-#pragma unroll 4
-                    for (int z = 0; z <= last - first; ++z) {
-                        const float mz = __ldcg(ptr(z) + D), f = mz == kNegInf ? 1.f : ex2(mz - big);
-                        sum += __ldcg(ptr(z) + d) * f;
-                        l += __ldcg(ptr(z) + D + 1) * f;
-                    }
-                    p.out[((size_t)cur.i * p.hq + h0 + head) * D + d] = (uint16_t)pack2<BF16>(l == 0.f ? 0.f : sum / l, 0.f);
+            __threadfence_block();
+            __syncwarp();
+            int n = 0;
+            if (lane == 0) n = atomicAdd(count, 1);
+            if (__shfl_sync(0xffffffffu, n, 0) == kWarps - 1) {
+                __threadfence_block();
+                join_heads<D, BF16>(p, smem, cur, whole, begin == cur.begin, half, p.out + ((size_t)cur.i * p.hq + h0) * D, lane);
+                __syncwarp();
+                if (lane == 0) {
+                    *count = 0;
+                    __threadfence_block();
+                    mbar_arrive(free_bar);
                 }
             }
         }
-        __syncthreads();  // before the next pair writes the join buffers
     }
 }
 

@@ -363,14 +363,14 @@ __device__ __forceinline__ void expand_exact(const BlockView& c, const BlockPref
     bad = 0;
     float f = 1.f;
     if (IS_V) {
-        const uint16_t* v = tail_ptr(c, c.lay.tail_v, e.seq, kvh) + first;
+        const uint16_t* v = tail_ptr(c, c.lay.tail_v, e.seq, kvh) + (ptrdiff_t)first * D;
         uint32_t keep[4];
 #pragma unroll
         for (int z = 0; z < 4; ++z)
             keep[z] = (8 * t + 2 * z < nv ? 0xffffu : 0u) | (8 * t + 2 * z + 1 < nv ? 0xffff0000u : 0u);
         auto row = [&](int ch) {
             if (nv <= 0) return make_uint4(0, 0, 0, 0);
-            const uint4 r = *reinterpret_cast<const uint4*>(v + (size_t)ch * c.block + 8 * t);
+            const uint4 r = *reinterpret_cast<const uint4*>(v + ch * kTileTokens + 8 * t);
             return make_uint4(r.x & keep[0], r.y & keep[1], r.z & keep[2], r.w & keep[3]);
         };
         if (BF16) {
