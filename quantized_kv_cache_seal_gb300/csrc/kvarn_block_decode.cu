@@ -4,8 +4,9 @@
 // Codes are exact in f16, so q . code runs on the tensor cores with fp32 sums (bf16 queries
 // enter as f16 after an exact power of two brings the head's largest value under 2^15: what
 // that drops is 2^-39 of it). V's scale is folded into the weight: w'_n = 2^(x_n + log2 s_V,n
-// - m'), m' the running maximum of x + log2 s_V, so that weights are at most 1 in f16
-// whatever V's range; the denominator adds w' / s_V in fp32. Rounding w' to f16 costs 2^-12
+// - m' + 15), m' the running maximum of x + log2 s_V, so that weights are at most 2^15 in f16
+// whatever V's range, and keep all its bits down to 2^-29 of the largest; the denominator adds
+// w' / s_V in fp32. Rounding w' to f16 costs 2^-12
 // of each weight on average less than the output's own rounding; bf16 would cost eight times
 // that.
 //
@@ -27,6 +28,7 @@ namespace kvarn {
 namespace {
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr float kShift = 15.f;  // weights are at most 2^15
 #define kNegInf (-__int_as_float(0x7f800000))
 
 template <int D>
@@ -61,19 +63,6 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
-}
-
-// Exponent (-100 at least) of a largest absolute value given as 16-bit bf16 pattern: values times
-// 2^(14 - e) stay under 2^15.
-__device__ __forceinline__ int bf16_exponent(uint32_t top) { return max((int)(top >> 7) - 127, -100); }
-__device__ __forceinline__ float power2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
-__device__ __forceinline__ uint32_t bf16_to_f16(uint32_t w, float f) {
-    const float2 a = unpack2<true>(w);
-    return pack2<false>(a.x * f, a.y * f);
-}
-__device__ __forceinline__ uint32_t max_of(uint32_t top, uint4 x) {
-    top = __vmaxu2(top, __vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu));
-    return __vmaxu2(top, __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
 }
 
 // A position on the line of tiles: the (sequence, KV head) that unit u belongs to.
@@ -145,7 +134,7 @@ __device__ __forceinline__ void weigh(State<D>& st, const float (&s)[2][4], floa
         }
     }
     // a head without a finite logit so far keeps m = -inf; its weights must not be 2^(inf - inf)
-    const float n0 = st.m[0] == kNegInf ? 0.f : st.m[0], n1 = st.m[1] == kNegInf ? 0.f : st.m[1];
+    const float n0 = st.m[0] == kNegInf ? 0.f : st.m[0] - kShift, n1 = st.m[1] == kNegInf ? 0.f : st.m[1] - kShift;
     float l0 = 0.f, l1 = 0.f;
 #pragma unroll
     for (int a = 0; a < 2; ++a)
@@ -193,7 +182,7 @@ template <int D, bool BF16>
 __device__ __forceinline__ void exact_unit(State<D>& st, const uint16_t* k, const uint16_t* v, int nv,
                                            const uint32_t (&q)[D / 64][4][2], float c0, float c1, int lane) {
     const int g = lane >> 2, t = lane & 3;
-    float ks = 1.f, vs = 1.f, lv = 0.f, ivs = 1.f;
+    float ks = 1.f;
     float s[2][4] = {};
     {
         uint4 x[2][D / 64][2][2];  // half, 64-channel part, rows g / g + 8, 16 channels
@@ -217,7 +206,7 @@ __device__ __forceinline__ void exact_unit(State<D>& st, const uint16_t* k, cons
         if (BF16) {
             top = max(top & 0xffffu, top >> 16);
             for (int d = 16; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-            const int e = bf16_exponent(top) - 14;
+            const int e = exponent_of<BF16>(top) - kExactK;
             f = power2(-e);
             ks = power2(e);
         }
@@ -234,7 +223,7 @@ __device__ __forceinline__ void exact_unit(State<D>& st, const uint16_t* k, cons
                         uint32_t r[4] = {lo[2 * j], hi[2 * j], lo[2 * j + 1], hi[2 * j + 1]};
                         if (BF16)
 #pragma unroll
-                            for (int y = 0; y < 4; ++y) r[y] = bf16_to_f16(r[y], f);
+                            for (int y = 0; y < 4; ++y) r[y] = scaled_f16<BF16>(r[y], f);
                         mma16816(s[a], r[0], r[1], r[2], r[3], q[c][2 * z + j][0], q[c][2 * z + j][1]);
                     }
                 }
@@ -252,30 +241,20 @@ __device__ __forceinline__ void exact_unit(State<D>& st, const uint16_t* k, cons
             uint4 r = *reinterpret_cast<const uint4*>(v + (16 * i + g + 8 * b) * kTileTokens + 8 * t);
             r = make_uint4(r.x & keep[0], r.y & keep[1], r.z & keep[2], r.w & keep[3]);
             y[i][b] = r;
-            if (BF16) top = max_of(top, r);
+            top = max_of(top, finite_only<BF16>(r));
         }
-    float f = 1.f;
-    if (BF16) {
-        top = max(top & 0xffffu, top >> 16);
-        for (int d = 16; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-        const int e = bf16_exponent(top) - 14;
-        f = power2(-e);
-        vs = power2(e);
-        lv = (float)e;
-        ivs = f;
-    }
-    (void)vs;
+    const int e = warp_exponent<BF16>(top) - kExactV;
+    const float f = power2(-e);
     uint32_t w[2][2];
-    weigh<D>(st, s, c0 * ks, c1 * ks, lv, ivs, nv, g, w);
+    weigh<D>(st, s, c0 * ks, c1 * ks, (float)e, f, nv, g, w);
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
 #pragma unroll
         for (int a = 0; a < 2; ++a) {
             uint32_t r[4] = {a ? y[i][0].z : y[i][0].x, a ? y[i][1].z : y[i][1].x, a ? y[i][0].w : y[i][0].y,
                              a ? y[i][1].w : y[i][1].y};
-            if (BF16)
 #pragma unroll
-                for (int z = 0; z < 4; ++z) r[z] = bf16_to_f16(r[z], f);
+            for (int z = 0; z < 4; ++z) r[z] = scaled_f16<BF16>(r[z], f);
             mma16816(st.o[i], r[0], r[1], r[2], r[3], w[a][0], w[a][1]);
         }
 }
@@ -490,14 +469,14 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                 top = max(top & 0xffffu, top >> 16);
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const int ex = bf16_exponent(top) - 14;
+                const int ex = exponent_of<BF16>(top) - kExactK;
                 const float f = power2(-ex);
 #pragma unroll
                 for (int a = 0; a < D / 64; ++a)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        q[a][j][0] = bf16_to_f16(q[a][j][0], f);
-                        q[a][j][1] = bf16_to_f16(q[a][j][1], f);
+                        q[a][j][0] = scaled_f16<BF16>(q[a][j][0], f);
+                        q[a][j][1] = scaled_f16<BF16>(q[a][j][1], f);
                     }
                 c0 *= power2(__shfl_sync(0xffffffffu, ex, 8 * t));
                 c1 *= power2(__shfl_sync(0xffffffffu, ex, 8 * t + 4));
@@ -577,10 +556,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
 
 template <int D, bool INT8, bool BF16>
 int launch(const BlockDecodeParams& p, cudaStream_t s) {
-    // a function attribute belongs to the device; setting it again is cheap
-    const cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, INT8, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               Shape<D>::kSmem);
-    if (e != cudaSuccess) return (int)e;
+    static SmemOnce once;
+    const int e = once.allow(reinterpret_cast<const void*>(decode_kernel<D, INT8, BF16>), Shape<D>::kSmem);
+    if (e) return e;
     decode_kernel<D, INT8, BF16><<<p.grid, kThreads, Shape<D>::kSmem, s>>>(p);
     return (int)cudaGetLastError();
 }

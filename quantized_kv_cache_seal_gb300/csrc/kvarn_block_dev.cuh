@@ -5,10 +5,26 @@
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "kvarn_block.h"
 #include "kvarn_dev.cuh"
 
 namespace kvarn {
+
+// A kernel's dynamic shared memory limit, raised once on each device (the attribute is the device's).
+struct SmemOnce {
+    std::atomic<uint64_t> done{0};
+    int allow(const void* kernel, int bytes) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        const uint64_t bit = 1ull << (dev & 63);
+        if (e != cudaSuccess || (dev < 64 && (done.load() & bit))) return (int)e;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess && dev < 64) done.fetch_or(bit);
+        return (int)e;
+    }
+};
 
 __device__ __forceinline__ const int32_t* block_table(const BlockView& c, int seq) {
     return reinterpret_cast<const int32_t*>(c.base + c.lay.table) + ((size_t)seq * c.num_layers + c.layer) * c.max_blocks;
@@ -84,6 +100,57 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, int32_t
     }
     return true;
 }
+
+// Exact 16-bit values enter the tensor cores as f16 after an exact power of two for 32 tokens or a
+// row. Exponent e (-100 at least) of the largest absolute value `top` (a 16-bit pattern without sign):
+// values times 2^(k - e) stay under 2^(k + 1).
+template <bool BF16>
+__device__ __forceinline__ int exponent_of(uint32_t top) {
+    return max((int)(__float_as_uint(unpack2<BF16>(top).x) >> 23) - 127, -100);
+}
+__device__ __forceinline__ float power2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+template <bool BF16>
+__device__ __forceinline__ uint32_t scaled_f16(uint32_t w, float f) {
+    const float2 a = unpack2<BF16>(w);
+    return pack2<false>(a.x * f, a.y * f);
+}
+template <bool BF16>
+__device__ __forceinline__ uint4 scaled_f16(uint4 w, float f) {
+    return make_uint4(scaled_f16<BF16>(w.x, f), scaled_f16<BF16>(w.y, f), scaled_f16<BF16>(w.z, f), scaled_f16<BF16>(w.w, f));
+}
+__device__ __forceinline__ uint32_t max_of(uint32_t top, uint4 x) {  // of two halves each, without sign
+    top = __vmaxu2(top, __vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu));
+    return __vmaxu2(top, __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+}
+template <bool BF16>
+__device__ __forceinline__ int warp_exponent(uint32_t top) {
+    top = max(top & 0xffffu, top >> 16);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+    return exponent_of<BF16>(top);
+}
+// Non-finite 16-bit values of a word, as the bits of a pair (bit 0, bit 1).
+template <bool BF16>
+__device__ __forceinline__ uint32_t bad_pair(uint32_t w) {
+    constexpr uint32_t e = BF16 ? 0x7f80u : 0x7c00u;
+    return ((w & e) == e ? 1u : 0u) | ((w >> 16 & e) == e ? 2u : 0u);
+}
+// The word with its non-finite values made zero.
+template <bool BF16>
+__device__ __forceinline__ uint32_t finite_only(uint32_t w) {
+    const uint32_t b = bad_pair<BF16>(w);
+    return w & ((b & 1 ? 0u : 0xffffu) | (b & 2 ? 0u : 0xffff0000u));
+}
+template <bool BF16>
+__device__ __forceinline__ uint4 finite_only(uint4 w) {
+    return make_uint4(finite_only<BF16>(w.x), finite_only<BF16>(w.y), finite_only<BF16>(w.z), finite_only<BF16>(w.w));
+}
+
+// Exact V values are brought to this power of two: near the largest codes (127, 448), so that the
+// weights, which carry V's scale, use f16's range alike for sealed and exact tokens.
+constexpr int kExactV = 8;
+// Exact K values and bf16 queries, whose products only go into fp32 sums, to the top of f16's range.
+constexpr int kExactK = 14;
 
 // Bytes of a 4 x 4 square: r[i] = row i; afterwards r[j] = column j.
 __device__ __forceinline__ void transpose4(uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {

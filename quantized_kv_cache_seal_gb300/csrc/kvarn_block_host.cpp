@@ -244,60 +244,6 @@ kvarn_status check_attention(kvarn_block_cache* c, int32_t layer, int32_t n_seqs
     return KVARN_OK;
 }
 
-kvarn_status run_prefill(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* ids, const int32_t* q_lens,
-                         const void* q, void* out, float scale, void* stream) {
-    static thread_local BlockPrefillParams p;
-    p.c = c->view;
-    p.c.layer = layer;
-    p.q = (const uint16_t*)q;
-    p.out = (uint16_t*)out;
-    p.hq = c->cfg.num_q_heads;
-    p.r = c->r;
-    p.scale_log2 = scale * 1.4426950408889634f;
-    p.n_seqs = 0;
-    const int hkv = c->cfg.num_kv_heads, pair_tokens = 2 * (128 / c->r);
-    int64_t row = 0;
-    for (int i = 0; i < n_seqs; ++i) {
-        if (q_lens[i] > 0) {
-            BlockPrefillSeq& e = p.seqs[p.n_seqs++];
-            e.seq = ids[i];
-            e.n = c->L(ids[i], layer);
-            e.q_len = q_lens[i];
-            e.q_row = (int32_t)row;
-        }
-        row += q_lens[i];
-    }
-    if (p.n_seqs == 0) return KVARN_OK;
-    // the longest sequences first: their segments are the longest
-    std::sort(p.seqs, p.seqs + p.n_seqs, [](const BlockPrefillSeq& a, const BlockPrefillSeq& b) { return a.n > b.n; });
-    int64_t segs = 0, steps = 0;
-    for (int i = 0; i < p.n_seqs; ++i) {
-        BlockPrefillSeq& e = p.seqs[i];
-        e.pairs = (e.q_len + pair_tokens - 1) / pair_tokens;
-        e.seg_begin = (int32_t)segs;
-        e.step_begin = (int32_t)steps;
-        int64_t head = 0;
-        for (int t = 1; t <= e.pairs; ++t)
-            head += (e.n - e.q_len + std::min<int64_t>((int64_t)t * pair_tokens, e.q_len) - 1) / 128 + 1;
-        e.head_steps = (int32_t)head;
-        segs += (int64_t)e.pairs * hkv;
-        steps += head * hkv;
-        if (steps >= 1ll << 31) return fail(KVARN_ECAPACITY, "2^31 steps of 128 keys or more in a call");
-    }
-    // Enough segments to fill the SMs twice: the CTAs take whole ones, the longest first. Fewer:
-    // the line of all steps is cut evenly.
-    const int sms = std::min(c->sms, kBlockPrefillGrid);
-    p.line = segs < 2 * sms;
-    p.steps = (int32_t)steps;
-    p.segs = (int32_t)segs;
-    p.grid = (int32_t)std::min<int64_t>(sms, steps);
-    if (c->host_only) return KVARN_OK;
-    const kvarn_status st = ensure_init(c, stream);
-    if (st) return st;
-    const int rc = launch_block_prefill(p, stream);
-    return rc ? cuda_fail(rc, "prefill launch") : KVARN_OK;
-}
-
 kvarn_status run_decode(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* ids, const void* q, void* out,
                         float scale, void* stream) {
     static thread_local BlockDecodeParams p;
@@ -326,6 +272,72 @@ kvarn_status run_decode(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, con
     if (st) return st;
     const int rc = launch_block_decode(p, stream);
     return rc ? cuda_fail(rc, "decode launch") : KVARN_OK;
+}
+
+kvarn_status run_prefill(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* ids, const int32_t* q_lens,
+                         const void* q, void* out, float scale, void* stream) {
+    // One query a sequence at most: the single-token kernel, whose rows are these queries.
+    if (std::all_of(q_lens, q_lens + n_seqs, [](int32_t m) { return m <= 1; })) {
+        int32_t one[kBlockMaxSeqs];
+        int32_t n = 0;
+        for (int i = 0; i < n_seqs; ++i)
+            if (q_lens[i] == 1) one[n++] = ids[i];
+        return n ? run_decode(c, layer, n, one, q, out, scale, stream) : KVARN_OK;
+    }
+    static thread_local BlockPrefillParams p;
+    p.c = c->view;
+    p.c.layer = layer;
+    p.q = (const uint16_t*)q;
+    p.out = (uint16_t*)out;
+    p.hq = c->cfg.num_q_heads;
+    p.r = c->r;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.n_seqs = 0;
+    const int hkv = c->cfg.num_kv_heads, pair_tokens = 2 * (128 / c->r);
+    int64_t row = 0;
+    for (int i = 0; i < n_seqs; ++i) {
+        if (q_lens[i] > 0) {
+            BlockPrefillSeq& e = p.seqs[p.n_seqs++];
+            e.seq = ids[i];
+            e.n = c->L(ids[i], layer);
+            e.q_len = q_lens[i];
+            e.q_row = (int32_t)row;
+        }
+        row += q_lens[i];
+    }
+    if (p.n_seqs == 0) return KVARN_OK;
+    // the longest sequences first: their segments are the longest
+    std::sort(p.seqs, p.seqs + p.n_seqs, [](const BlockPrefillSeq& a, const BlockPrefillSeq& b) { return a.n > b.n; });
+    int64_t segs = 0, steps = 0, longest = 0;
+    for (int i = 0; i < p.n_seqs; ++i) {
+        BlockPrefillSeq& e = p.seqs[i];
+        e.pairs = (e.q_len + pair_tokens - 1) / pair_tokens;
+        e.seg_begin = (int32_t)segs;
+        e.step_begin = (int32_t)steps;
+        int64_t head = 0;
+        for (int t = 1; t <= e.pairs; ++t)
+            head += (e.n - e.q_len + std::min<int64_t>((int64_t)t * pair_tokens, e.q_len) - 1) / 128 + 1;
+        e.head_steps = (int32_t)head;
+        longest = std::max<int64_t>(longest, (e.n - 1) / 128 + 1);
+        segs += (int64_t)e.pairs * hkv;
+        steps += head * hkv;
+        if (steps >= 1ll << 31) return fail(KVARN_ECAPACITY, "2^31 steps of 128 keys or more in a call");
+    }
+    // Whole segments, the longest first, end when the longest does or the SMs have shared out all;
+    // the line of all steps cut evenly ends a share of the steps later, and then costs about four more
+    // for the partial results and the kernel that adds them (6 us where a step takes 1.5).
+    const int64_t sms = std::min(c->sms, kBlockPrefillGrid);
+    const int64_t share = (steps + sms - 1) / sms;
+    const int64_t whole = segs >= 2 * sms ? share : std::max(share, longest * ((segs + sms - 1) / sms));
+    p.line = whole > share + 4;
+    p.steps = (int32_t)steps;
+    p.segs = (int32_t)segs;
+    p.grid = (int32_t)std::min<int64_t>(sms, p.line ? steps : segs);
+    if (c->host_only) return KVARN_OK;
+    const kvarn_status st = ensure_init(c, stream);
+    if (st) return st;
+    const int rc = launch_block_prefill(p, stream);
+    return rc ? cuda_fail(rc, "prefill launch") : KVARN_OK;
 }
 
 }  // namespace

@@ -4,14 +4,14 @@
 // head of the KV head's r), token-major, M = 128 of tcgen05.mma kind::f16. Keys come in steps
 // of 128 tokens:
 //   QK  S = Q code^T (f16 operands, exact codes, fp32 sums); logit x = S scale s_K.
-//   PV  O += W code, W = 2^(x + log2 s_V - m) in f16 with m the running maximum of x + log2 s_V
-//       (raised only when it grows by more than 8, with O and the sum rescaled then), so
-//       weights fit f16 whatever V's range; the denominator adds W / s_V in fp32. f16 weights
+//   PV  O += W code, W = 2^(x + log2 s_V - m + 7) in f16 with m the running maximum of
+//       x + log2 s_V (raised only when it grows by more than 8, with O and the sum rescaled
+//       then): weights fit f16 whatever V's range, at most 2^15, and keep all of f16's bits
+//       down to 2^-21 of the largest. The denominator adds W / s_V in fp32. f16 weights
 //       (rounded by 2^-12) are kept for bf16 caches too: bf16 would cost eight times that.
 // Scales belong to 32-token parts of a step (a part is sealed or exact as a whole), so each
-// is one constant for 32 columns. Exact fp16 values enter as they are; exact bf16 values and
-// bf16 queries after an exact power of two per part or row (what that drops is 2^-39 of the
-// largest).
+// is one constant for 32 columns. Exact values and bf16 queries enter after an exact power of two
+// per part or row (what f16 then drops is 2^-33 of the largest, 2^-39 for K and queries).
 //
 // Roles (512 threads): two softmax warpgroups, one a tile, a thread a row, its 128 logits in
 // registers; an expansion warpgroup that turns codes into f16 K and V tiles (K-major, 128-byte
@@ -36,6 +36,7 @@ constexpr int kRegsLaunch = 128, kRegsSoftmax = 184, kRegsExpand = 104, kRegsIss
 static_assert(2 * kRegsSoftmax + kRegsExpand + kRegsIssue <= 4 * kRegsLaunch, "register split");
 constexpr uint32_t kColS = 0, kColO = 256;
 constexpr int kStep = 128;  // keys of a step
+constexpr float kRaise = 8.f, kShift = 7.f;  // m is raised when it would grow by more; weights are at most 2^(both)
 #define kNegInf (-__int_as_float(0x7f800000))
 
 // feed: segments handed to the roles
@@ -96,13 +97,6 @@ __device__ __forceinline__ void tm_st16(uint32_t taddr, const uint32_t (&r)[16])
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
-}
-__device__ __forceinline__ void tm_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
 }
 __device__ __forceinline__ bool elect_one() {
     uint32_t ok;
@@ -239,26 +233,6 @@ struct Walk {
     __device__ __forceinline__ bool whole() const { return s.j0 == 0 && s.j1 == s.steps; }
 };
 
-__device__ __forceinline__ int bf16_exponent(uint32_t top) { return max((int)(top >> 7) - 127, -100); }
-__device__ __forceinline__ float power2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
-__device__ __forceinline__ uint32_t scaled_f16(uint32_t w, float f) {
-    const float2 a = unpack2<true>(w);
-    return pack2<false>(a.x * f, a.y * f);
-}
-__device__ __forceinline__ uint4 scaled_f16(uint4 w, float f) {
-    return make_uint4(scaled_f16(w.x, f), scaled_f16(w.y, f), scaled_f16(w.z, f), scaled_f16(w.w, f));
-}
-__device__ __forceinline__ uint32_t max_of(uint32_t top, uint4 x) {
-    top = __vmaxu2(top, __vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu));
-    return __vmaxu2(top, __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
-}
-__device__ __forceinline__ int warp_exponent(uint32_t top) {
-    top = max(top & 0xffffu, top >> 16);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-    return bf16_exponent(top) - 14;
-}
-
 // ---- the MMA issuer ----
 // An MMA of this size runs 64 clocks, but takes its warp about 30 turns at a scheduler that it shares
 // with two softmax warps and one of the expansion's, so that the issue, near 100 clocks an MMA, is
@@ -331,23 +305,6 @@ __device__ __forceinline__ void issue_role(uint32_t sbase, uint64_t* bars, int32
     }
 }
 
-// Non-finite 16-bit values of a word, as the bits of a pair (bit 0, bit 1).
-template <bool BF16>
-__device__ __forceinline__ uint32_t bad_pair(uint32_t w) {
-    constexpr uint32_t e = BF16 ? 0x7f80u : 0x7c00u;
-    return ((w & e) == e ? 1u : 0u) | ((w >> 16 & e) == e ? 2u : 0u);
-}
-// The word with its non-finite values made zero.
-template <bool BF16>
-__device__ __forceinline__ uint32_t finite_only(uint32_t w) {
-    const uint32_t b = bad_pair<BF16>(w);
-    return w & ((b & 1 ? 0u : 0xffffu) | (b & 2 ? 0u : 0xffff0000u));
-}
-template <bool BF16>
-__device__ __forceinline__ uint4 finite_only(uint4 w) {
-    return make_uint4(finite_only<BF16>(w.x), finite_only<BF16>(w.y), finite_only<BF16>(w.z), finite_only<BF16>(w.w));
-}
-
 // Exact tokens of a part (none: zeros) as its K or V tile rows. A later token's infinity or NaN
 // must not reach a query that does not see it through 0 x NaN: non-finite V enters as 0, and its
 // token is named in `bad` for the softmax to make visible weights NaN. K needs no such care (logits
@@ -373,21 +330,18 @@ __device__ __forceinline__ void expand_exact(const BlockView& c, const BlockPref
             const uint4 r = *reinterpret_cast<const uint4*>(v + ch * kTileTokens + 8 * t);
             return make_uint4(r.x & keep[0], r.y & keep[1], r.z & keep[2], r.w & keep[3]);
         };
-        if (BF16) {
-            uint32_t top = 0;
-#pragma unroll 4
-            for (int i = 0; i < D / 8; ++i) top = max_of(top, finite_only<BF16>(row(8 * i + g)));
-            const int ex = warp_exponent(top);
-            f = power2(-ex);
-            h = make_float2((float)ex, f);
-        }
+        uint32_t top = 0;
+#pragma unroll 2
+        for (int i = 0; i < D / 8; ++i) top = max_of(top, finite_only<BF16>(row(8 * i + g)));
+        const int ex = warp_exponent<BF16>(top) - kExactV;
+        f = power2(-ex);
+        h = make_float2((float)ex, f);
         uint8_t* atom = dst + (wp >> 1) * (D * 128);
 #pragma unroll 2
         for (int i = 0; i < D / 8; ++i) {
             uint4 r = row(8 * i + g);
             bad |= (bad_pair<BF16>(r.x) | bad_pair<BF16>(r.y) << 2 | bad_pair<BF16>(r.z) << 4 | bad_pair<BF16>(r.w) << 6) << (8 * t);
-            r = finite_only<BF16>(r);
-            if (BF16) r = scaled_f16(r, f);
+            r = scaled_f16<BF16>(finite_only<BF16>(r), f);
             *reinterpret_cast<uint4*>(atom + swz(8 * i + g, 4 * (wp & 1) + t)) = r;
         }
         bad = __reduce_or_sync(0xffffffffu, bad);
@@ -402,14 +356,14 @@ __device__ __forceinline__ void expand_exact(const BlockView& c, const BlockPref
             uint32_t top = 0;
 #pragma unroll 2
             for (int z = 0; z < D / 8; ++z) top = max_of(top, finite_only<BF16>(piece(z)));
-            const int ex = warp_exponent(top);
+            const int ex = warp_exponent<BF16>(top) - kExactK;
             f = power2(-ex);
             h.x = power2(ex);
         }
 #pragma unroll 2
         for (int z = 0; z < D / 8; ++z) {
             uint4 r = piece(z);
-            if (BF16) r = scaled_f16(r, f);
+            if (BF16) r = scaled_f16<BF16>(r, f);
             const int y = z * 32 + lane, ch8 = y % (D / 8);
             *reinterpret_cast<uint4*>(dst + (ch8 >> 3) * Shape<D>::kAtom + swz(32 * wp + y / (D / 8), ch8 & 7)) = r;
         }
@@ -577,8 +531,8 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, uint8_
                         top = max(top & 0xffffu, top >> 16);
 #pragma unroll
                         for (int d = kLanes / 2; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-                        const int ex = bf16_exponent(top) - 14;
-                        r = scaled_f16(r, power2(-ex));
+                        const int ex = exponent_of<BF16>(top) - kExactK;
+                        r = scaled_f16<BF16>(r, power2(-ex));
                         const int mine = __shfl_sync(0xffffffffu, ex, lane % kRows * kLanes);  // of row i kRows + lane % kRows
                         if (lane / kRows == i) qs *= power2(mine);
                     }
@@ -639,25 +593,12 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, uint8_
                     mx = fmaxf(mx, fmaf(max32(r[ch]), c[ch], lv[ch]));
                 }
             }
-            const bool up = mx > m + 8.f;  // also from -inf
-            if (__any_sync(0xffffffffu, up)) {
-                const float f = up ? ex2f(m - mx) : 1.f;  // 0 from -inf
-                if (up) m = mx;
-                l *= f;
-                if (j > w.s.j0) {
-                    // O is rescaled 16 columns at a time: the 128 logits stay in registers
-#pragma unroll 1
-                    for (int ch = 0; ch < D / 16; ++ch) {
-                        uint32_t o[16];
-                        tm_ld16(to + 16 * ch, o);
-                        tm_wait_ld();
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                        tm_st16(to + 16 * ch, o);
-                    }
-                }
-            }
-            const float mm = m == kNegInf ? 0.f : m;
+            const bool up = mx > m + kRaise;  // also from -inf
+            const bool rescale = __any_sync(0xffffffffu, up);
+            const float f = up ? ex2f(m - mx) : 1.f;  // 0 from -inf
+            if (up) m = mx;
+            l *= f;
+            const float mm = m == kNegInf ? 0.f : m - kShift;
 #pragma unroll
             for (int ch = 0; ch < 4; ++ch) {
                 const float ad = lv[ch] - mm;
@@ -676,6 +617,21 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, uint8_
                 s0 = __fadd2_rn(s0, s1);
                 l = fmaf(s0.x + s0.y, iv[ch], l);
                 tm_st16(ts + 16 * ch, o);
+            }
+            if (rescale && j > w.s.j0) {  // O, now that the logits' registers are free
+#pragma unroll 1
+                for (int ch = 0; ch < D / 64; ++ch) {
+                    uint32_t o[2][32];
+                    tm_ld32(to + 64 * ch, o[0]);
+                    tm_ld32(to + 64 * ch + 32, o[1]);
+                    tm_wait_ld();
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[z][k] = __float_as_uint(__uint_as_float(o[z][k]) * f);
+                        tm_st32(to + 64 * ch + 32 * z, o[z]);
+                    }
+                }
             }
             tm_wait_st();
             tc_fence_before();
@@ -721,22 +677,24 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, uint8_
             float* part = reinterpret_cast<float*>(p.c.base + p.c.lay.partials) +
                           (size_t)(2 * blockIdx.x + (w.s.j0 == 0 ? 1 : 0)) * (256 * (D + 2));
             const int first = 128 * b + (et & 96);
+            if (__any_sync(0xffffffffu, row >= 0)) {  // (rows without a query are not read back)
 #pragma unroll 1
-            for (int ch = 0; ch < D / 32; ++ch) {
-                uint32_t x[32];
-                tm_ld32(to + 32 * ch, x);
-                tm_wait_ld();
-                give(0, x);
-                __syncwarp();
+                for (int ch = 0; ch < D / 32; ++ch) {
+                    uint32_t x[32];
+                    tm_ld32(to + 32 * ch, x);
+                    tm_wait_ld();
+                    give(0, x);
+                    __syncwarp();
 #pragma unroll 4
-                for (int k = 0; k < 8; ++k) {
-                    const int rr = first + 4 * k + (lane >> 3);
-                    *reinterpret_cast<uint4*>(part + (size_t)rr * D + 32 * ch + 4 * (lane & 7)) = take(0, k);
+                    for (int k = 0; k < 8; ++k) {
+                        const int rr = first + 4 * k + (lane >> 3);
+                        *reinterpret_cast<uint4*>(part + (size_t)rr * D + 32 * ch + 4 * (lane & 7)) = take(0, k);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
+                part[256 * D + 128 * b + et] = m;
+                part[256 * D + 256 + 128 * b + et] = l;
             }
-            part[256 * D + 128 * b + et] = m;
-            part[256 * D + 256 + 128 * b + et] = l;
         }
         __syncwarp();
         tc_fence_before();  // O has been read before this thread lets the next segment's PV start
@@ -808,71 +766,75 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 }
 
 // Adds the partials of the segment that begins in CTA b's range and ends behind it, in the order
-// of the cuts. blockIdx.y: 32 of the pair's 256 rows; 4 channels of four rows a thread, whose loads
-// are all in flight for each part.
-constexpr int kCombineRows = 32;
+// of the cuts. A warp (half of one at head_dim 64) a row, 4 channels a lane; the parts' maxima and
+// sums 32 at a time, a lane each, then their rows eight at a time. blockIdx.y: kCombineRows rows.
+constexpr int kCombineThreads = 256;
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kCombineRows / 4 * (D / 4)) combine_kernel(const __grid_constant__ BlockPrefillParams p) {
-    const int b = blockIdx.x;
+__global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_constant__ BlockPrefillParams p) {
+    constexpr int kCombineRows = kCombineThreads / 32;
+    const int b = blockIdx.x, lane = threadIdx.x & 31;
     const int u0 = (int)((int64_t)p.steps * b / p.grid), u1 = (int)((int64_t)p.steps * (b + 1) / p.grid);
     LineWalk w(p, b);
     int u = u0;
 #pragma unroll 1
     while (u + (w.s.j1 - w.s.j0) < u1) u += w.s.j1 - w.s.j0, w.next();
     if (w.s.j0 > 0 || w.s.j1 == w.s.steps) return;  // no segment both begins here and goes on
-    const int last = (int)(((int64_t)(u + w.s.steps) * p.grid - 1) / p.steps);
     const BlockPrefillSeq& e = p.seqs[w.s.i];
-    const int tpt = 128 / p.r;
-    const int r0 = blockIdx.y * kCombineRows + threadIdx.x / (D / 4), ch = threadIdx.x % (D / 4) * 4;
+    const int tpt = 128 / p.r, rr = blockIdx.y * kCombineRows + threadIdx.x / 32, et = rr & 127;
+    const int tok = (2 * w.s.pair + (rr >> 7)) * tpt + et / p.r;
+    if (et / p.r >= tpt || tok >= e.q_len) return;
+    const int parts = (int)(((int64_t)(u + w.s.steps) * p.grid - 1) / p.steps) - b + 1;
+    const bool live = 4 * lane < D;
     constexpr size_t kPart = 256 * (D + 2);
     const float* base = reinterpret_cast<const float*>(p.c.base + p.c.lay.partials);
-    float4 sum[4];
-    float big[4], l[4];
-#pragma unroll
-    for (int y = 0; y < 4; ++y) sum[y] = make_float4(0.f, 0.f, 0.f, 0.f), big[y] = kNegInf, l[y] = 0.f;
+    // part z: slot 1 of the CTA where the segment begins, slot 0 of the others
+    auto part = [&](int z) { return base + (size_t)(2 * (b + z) + (z == 0 ? 1 : 0)) * kPart; };
+    float big = kNegInf, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-    for (int z = b; z <= last; ++z) {
-        const float* q = base + (size_t)(2 * z + (z == b ? 1 : 0)) * kPart;  // slot 1 where the segment begins
-        float4 o[4];
-        float m[4], n[4];
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-            const int rr = r0 + y * (kCombineRows / 4);
-            o[y] = *reinterpret_cast<const float4*>(q + (size_t)rr * D + ch);
-            m[y] = q[256 * D + rr];
-            n[y] = q[256 * D + 256 + rr];
+    for (int z0 = 0; z0 < parts; z0 += 32) {
+        const int n = min(32, parts - z0);
+        float m = kNegInf, s = 0.f;
+        if (lane < n) {
+            m = part(z0 + lane)[256 * D + rr];
+            s = part(z0 + lane)[256 * D + 256 + rr];
         }
+        float top = m;
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-            const float top = fmaxf(big[y], m[y]);
-            // -inf (no weight yet, or NaN): nothing to scale
-            const float f = big[y] == kNegInf ? 1.f : ex2f(big[y] - top), g = m[y] == kNegInf ? 1.f : ex2f(m[y] - top);
-            sum[y].x = fmaf(o[y].x, g, sum[y].x * f);
-            sum[y].y = fmaf(o[y].y, g, sum[y].y * f);
-            sum[y].z = fmaf(o[y].z, g, sum[y].z * f);
-            sum[y].w = fmaf(o[y].w, g, sum[y].w * f);
-            l[y] = fmaf(n[y], g, l[y] * f);
-            big[y] = top;
+        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        top = fmaxf(top, big);
+        const float f = m == kNegInf ? 1.f : ex2f(m - top), g = big == kNegInf ? 1.f : ex2f(big - top);  // -inf: zeros or NaN
+        s *= f;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+        l = fmaf(l, g, s);
+        o.x *= g, o.y *= g, o.z *= g, o.w *= g;
+        big = top;
+#pragma unroll 8
+        for (int z = 0; z < n; ++z) {
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (live) x = *reinterpret_cast<const float4*>(part(z0 + z) + (size_t)rr * D + 4 * lane);
+            const float y = __shfl_sync(0xffffffffu, f, z);
+            o.x = fmaf(x.x, y, o.x);
+            o.y = fmaf(x.y, y, o.y);
+            o.z = fmaf(x.z, y, o.z);
+            o.w = fmaf(x.w, y, o.w);
         }
     }
-#pragma unroll
-    for (int y = 0; y < 4; ++y) {
-        const int rr = r0 + y * (kCombineRows / 4), et = rr & 127, tok = (2 * w.s.pair + (rr >> 7)) * tpt + et / p.r;
-        if (et / p.r >= tpt || tok >= e.q_len) continue;
-        const float inv = l[y] == 0.f ? 0.f : 1.f / l[y];
-        const size_t row = ((size_t)(e.q_row + tok) * p.hq + w.s.kvh * p.r + et % p.r) * D;
-        *reinterpret_cast<uint2*>(p.out + row + ch) =
-            make_uint2(pack2<BF16>(sum[y].x * inv, sum[y].y * inv), pack2<BF16>(sum[y].z * inv, sum[y].w * inv));
-    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const size_t row = ((size_t)(e.q_row + tok) * p.hq + w.s.kvh * p.r + et % p.r) * D;
+    if (live)
+        *reinterpret_cast<uint2*>(p.out + row + 4 * lane) =
+            make_uint2(pack2<BF16>(o.x * inv, o.y * inv), pack2<BF16>(o.z * inv, o.w * inv));
 }
 
 template <int D, bool INT8, bool BF16>
 int launch(const BlockPrefillParams& p, cudaStream_t s) {
-    const cudaError_t e = cudaFuncSetAttribute(prefill_kernel<D, INT8, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               Shape<D>::kSmem);
-    if (e != cudaSuccess) return (int)e;
+    static SmemOnce once;
+    const int e = once.allow(reinterpret_cast<const void*>(prefill_kernel<D, INT8, BF16>), Shape<D>::kSmem);
+    if (e) return e;
     prefill_kernel<D, INT8, BF16><<<p.grid, kThreads, Shape<D>::kSmem, s>>>(p);
-    if (p.line) combine_kernel<D, BF16><<<dim3(p.grid, 256 / kCombineRows), kCombineRows / 4 * (D / 4), 0, s>>>(p);
+    if (p.line) combine_kernel<D, BF16><<<dim3(p.grid, 256 / (kCombineThreads / 32)), kCombineThreads, 0, s>>>(p);
     return (int)cudaGetLastError();
 }
 

@@ -345,7 +345,8 @@ def current_stream(device) -> int:
     """The current stream of a CUDA device, as an address."""
     import torch
 
-    return torch.cuda.current_stream(device).cuda_stream
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the same without building a Stream object
+    return raw(device.index) if raw else torch.cuda.current_stream(device).cuda_stream
 
 
 def _i32(xs):

@@ -44,10 +44,13 @@ def attend(q, k, v, scale, last):
     """o [rows][hq][dim] and a bound on a kernel's error. q [rows][hq][dim] in the inputs' type; k, v [n][hkv][dim] in
     64 bits; row i sees positions <= last[i].
 
-    The bound: weights rounded to f16 (2^-11 of each; what falls under f16's range is at most 2^-25 of the largest
-    weight times its block's largest value, which is at most twice what the largest code stands for), logits off by
-    (dim + 8) roundings of 2^-24 of sum |q k| scale (each changes a weight by that share, numerator and denominator),
-    sums and divisions a further 2^-16, and the output's own rounding."""
+    The bound: each weight is rounded to f16 (half a step: 2^-11 of it, or 2^-25 where it is under f16's normal
+    range); logits are off by (dim + 8) roundings of 2^-24 of sum |q k| scale (each changes a weight by that share,
+    numerator and denominator); sums and divisions a further 2^-16; and the output's own rounding. A weight stands
+    for p s (s: V's scale in its block) in units in which the largest of the row is at least 2^7, so 2^-25 is at
+    most 2^-32 max(p s), and its error meets a code of at most 512: over n tokens n 2^-32 512 max(p s). A block
+    whose largest |v| is a has 512 s <= 4.1 a (int8: s = a / 127; e4m3: s <= 2 a / 448; exact tokens: 512 s <= 2 a),
+    so with the largest |v| of all blocks for a: n 2^-29 max(p) max|v|."""
     dtype = q.dtype
     q = f64(q)
     rows, hq, dim = q.shape
@@ -67,7 +70,7 @@ def attend(q, k, v, scale, last):
         off = (q[:, h].abs() @ kh.abs().T) * abs(scale) * (dim + 8) * 2.0 ** -24
         off = torch.where(seen, off, torch.zeros_like(off)).amax(-1, keepdim=True) if n else total
         mass = p @ vh.abs()
-        small = n * 2.0 ** -24 * (p * vh.abs().amax(-1)[None]).amax(-1, keepdim=True) if n else total
+        small = n * 2.0 ** -29 * p.amax(-1, keepdim=True) * vh.abs().max() if n else total
         tol[:, h] = mass * (2.0 ** -11 + 2 * off + 2.0 ** -16) + small
     return o, tol + o.abs() * torch.finfo(dtype).eps / 2 + float(torch.finfo(dtype).smallest_normal) * 2.0 ** -7
 
