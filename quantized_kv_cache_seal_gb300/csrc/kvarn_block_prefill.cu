@@ -32,7 +32,7 @@ namespace kvarn {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kRegsLaunch = 128, kRegsSoftmax = 184, kRegsExpand = 104, kRegsIssue = 40;
+constexpr int kRegsLaunch = 128, kRegsSoftmax = 184, kRegsExpand = 112, kRegsIssue = 32;
 static_assert(2 * kRegsSoftmax + kRegsExpand + kRegsIssue <= 4 * kRegsLaunch, "register split");
 constexpr uint32_t kColS = 0, kColO = 256;
 constexpr int kStep = 128;  // keys of a step
@@ -309,63 +309,89 @@ __device__ __forceinline__ void issue_role(uint32_t sbase, uint64_t* bars, int32
 // must not reach a query that does not see it through 0 x NaN: non-finite V enters as 0, and its
 // token is named in `bad` for the softmax to make visible weights NaN. K needs no such care (logits
 // of unseen tokens are replaced), but neither may set the part's power of two.
-// h: K scale, or log2 and reciprocal of the V scale.
+// h: K scale, or log2 and reciprocal of the V scale. x: registers to use.
 template <int D, bool BF16, bool IS_V>
 __device__ __forceinline__ void expand_exact(const BlockView& c, const BlockPrefillSeq& e, int kvh, int tile, int wp, int lane,
-                                             uint8_t* dst, float2& h, uint32_t& bad) {
+                                             uint8_t* dst, float2& h, uint32_t& bad, uint4 (&x)[D / 16]) {
     const int g = lane >> 2, t = lane & 3;
     const int first = (tile - (e.n >> c.log2_block << (c.log2_block - 5))) * kTileTokens;  // row of the tail
     const int nv = min(kTileTokens, e.n - tile * kTileTokens);  // valid tokens, none if <= 0
     h = IS_V ? make_float2(0.f, 1.f) : make_float2(1.f, 0.f);
     bad = 0;
-    float f = 1.f;
-    if (IS_V) {
+    // D / 8 pieces of 16 bytes a lane, four at a time so that their loads overlap; twice, first for the largest
+    constexpr int kTurn = 4;
+    if (IS_V) {  // piece i: tokens 8 t .. of channel 8 i + g
         const uint16_t* v = tail_ptr(c, c.lay.tail_v, e.seq, kvh) + (ptrdiff_t)first * D;
         uint32_t keep[4];
 #pragma unroll
         for (int z = 0; z < 4; ++z)
             keep[z] = (8 * t + 2 * z < nv ? 0xffffu : 0u) | (8 * t + 2 * z + 1 < nv ? 0xffff0000u : 0u);
-        auto row = [&](int ch) {
-            if (nv <= 0) return make_uint4(0, 0, 0, 0);
-            const uint4 r = *reinterpret_cast<const uint4*>(v + ch * kTileTokens + 8 * t);
-            return make_uint4(r.x & keep[0], r.y & keep[1], r.z & keep[2], r.w & keep[3]);
+        auto load = [&](int i0) {
+#pragma unroll
+            for (int i = 0; i < kTurn; ++i) {
+                x[i] = make_uint4(0, 0, 0, 0);
+                if (nv > 0) x[i] = *reinterpret_cast<const uint4*>(v + (8 * (i0 + i) + g) * kTileTokens + 8 * t);
+            }
+#pragma unroll
+            for (int i = 0; i < kTurn; ++i)
+                x[i] = make_uint4(x[i].x & keep[0], x[i].y & keep[1], x[i].z & keep[2], x[i].w & keep[3]);
         };
         uint32_t top = 0;
-#pragma unroll 2
-        for (int i = 0; i < D / 8; ++i) top = max_of(top, finite_only<BF16>(row(8 * i + g)));
+#pragma unroll 1
+        for (int i0 = 0; i0 < D / 8; i0 += kTurn) {
+            load(i0);
+#pragma unroll
+            for (int i = 0; i < kTurn; ++i) top = max_of(top, finite_only<BF16>(x[i]));
+        }
         const int ex = warp_exponent<BF16>(top) - kExactV;
-        f = power2(-ex);
+        const float f = power2(-ex);
         h = make_float2((float)ex, f);
         uint8_t* atom = dst + (wp >> 1) * (D * 128);
-#pragma unroll 2
-        for (int i = 0; i < D / 8; ++i) {
-            uint4 r = row(8 * i + g);
-            bad |= (bad_pair<BF16>(r.x) | bad_pair<BF16>(r.y) << 2 | bad_pair<BF16>(r.z) << 4 | bad_pair<BF16>(r.w) << 6) << (8 * t);
-            r = scaled_f16<BF16>(finite_only<BF16>(r), f);
-            *reinterpret_cast<uint4*>(atom + swz(8 * i + g, 4 * (wp & 1) + t)) = r;
+#pragma unroll 1
+        for (int i0 = 0; i0 < D / 8; i0 += kTurn) {
+            load(i0);
+#pragma unroll
+            for (int i = 0; i < kTurn; ++i) {
+                const uint4 r = x[i];
+                bad |= (bad_pair<BF16>(r.x) | bad_pair<BF16>(r.y) << 2 | bad_pair<BF16>(r.z) << 4 | bad_pair<BF16>(r.w) << 6)
+                       << (8 * t);
+                *reinterpret_cast<uint4*>(atom + swz(8 * (i0 + i) + g, 4 * (wp & 1) + t)) =
+                    scaled_f16<BF16>(finite_only<BF16>(r), f);
+            }
         }
         bad = __reduce_or_sync(0xffffffffu, bad);
-    } else {
+    } else {  // piece i: bytes i * 512 + lane * 16 of the part's 32 D values
         const uint16_t* k = tail_ptr(c, c.lay.tail_k, e.seq, kvh) + (ptrdiff_t)first * D;
-        auto piece = [&](int z) {  // 16 bytes z * 32 + lane of the part's 32 D values
-            const int y = z * 32 + lane, tok = y / (D / 8);
-            if (tok >= nv) return make_uint4(0, 0, 0, 0);
-            return *reinterpret_cast<const uint4*>(k + tok * D + y % (D / 8) * 8);
+        auto load = [&](int i0) {
+#pragma unroll
+            for (int i = 0; i < kTurn; ++i) {
+                const int y = (i0 + i) * 32 + lane;
+                x[i] = make_uint4(0, 0, 0, 0);
+                if (y / (D / 8) < nv) x[i] = *reinterpret_cast<const uint4*>(k + y * 8);
+            }
         };
+        float f = 1.f;
         if (BF16) {
             uint32_t top = 0;
-#pragma unroll 2
-            for (int z = 0; z < D / 8; ++z) top = max_of(top, finite_only<BF16>(piece(z)));
+#pragma unroll 1
+            for (int i0 = 0; i0 < D / 8; i0 += kTurn) {
+                load(i0);
+#pragma unroll
+                for (int i = 0; i < kTurn; ++i) top = max_of(top, finite_only<BF16>(x[i]));
+            }
             const int ex = warp_exponent<BF16>(top) - kExactK;
             f = power2(-ex);
             h.x = power2(ex);
         }
-#pragma unroll 2
-        for (int z = 0; z < D / 8; ++z) {
-            uint4 r = piece(z);
-            if (BF16) r = scaled_f16<BF16>(r, f);
-            const int y = z * 32 + lane, ch8 = y % (D / 8);
-            *reinterpret_cast<uint4*>(dst + (ch8 >> 3) * Shape<D>::kAtom + swz(32 * wp + y / (D / 8), ch8 & 7)) = r;
+#pragma unroll 1
+        for (int i0 = 0; i0 < D / 8; i0 += kTurn) {
+            load(i0);
+#pragma unroll
+            for (int i = 0; i < kTurn; ++i) {
+                const int y = (i0 + i) * 32 + lane, ch8 = y % (D / 8);
+                *reinterpret_cast<uint4*>(dst + (ch8 >> 3) * Shape<D>::kAtom + swz(32 * wp + y / (D / 8), ch8 & 7)) =
+                    BF16 ? scaled_f16<BF16>(x[i], f) : x[i];
+            }
         }
     }
 }
@@ -441,7 +467,7 @@ __device__ __forceinline__ void expand_role(const BlockPrefillParams& p, uint8_t
                     *reinterpret_cast<uint4*>(dst + cc * Sh::kAtom + swz(row, 2 * t + 1)) = b;
                 }
             } else {
-                expand_exact<D, BF16, false>(c, p.seqs[who & 255], who >> 8, (int)(tile & 0x7fffffffu), wp, lane, dst, h, bad);
+                expand_exact<D, BF16, false>(c, p.seqs[who & 255], who >> 8, (int)(tile & 0x7fffffffu), wp, lane, dst, h, bad, x);
             }
             if (lane == 0) head[0] = h.x;
             fence_proxy_async_smem();
@@ -460,7 +486,7 @@ __device__ __forceinline__ void expand_role(const BlockPrefillParams& p, uint8_t
                     if (rec1) x[i] = load_k(rec1, i);
                 }
             } else {
-                expand_exact<D, BF16, true>(c, p.seqs[who & 255], who >> 8, (int)(tile & 0x7fffffffu), wp, lane, dst, h, bad);
+                expand_exact<D, BF16, true>(c, p.seqs[who & 255], who >> 8, (int)(tile & 0x7fffffffu), wp, lane, dst, h, bad, x);
             }
             if (lane == 0) head[1] = __uint_as_float(bad), head[2] = h.x, head[3] = h.y;
             fence_proxy_async_smem();
@@ -512,7 +538,7 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, uint8_
         float qs = scale;
         {
             // D / 8 lanes a row; loops stay short: this code runs once a segment, from a cold cache
-            constexpr int kLanes = D / 8, kRows = 32 / kLanes, kTurn = 4;
+            constexpr int kLanes = D / 8, kRows = 32 / kLanes, kTurn = 8;
 #pragma unroll 1
             for (int i0 = 0; i0 < kLanes; i0 += kTurn) {
                 uint4 x[kTurn];
@@ -581,15 +607,22 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, uint8_
             } else {
                 // non-finite V tokens' weights become NaN where they are seen; then columns behind the
                 // row's position leave, with all of a part that is not seen at all
+                if (bad) {
+#pragma unroll
+                    for (int ch = 0; ch < 4; ++ch) {
+                        const uint32_t y = __float_as_uint(hdr[(jj & 3) * 4 + ch].y);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (y >> k & 1) r[ch][k] = 0x7fc00000u;
+                    }
+                }
 #pragma unroll
                 for (int ch = 0; ch < 4; ++ch) {
-                    const uint32_t y = __float_as_uint(hdr[(jj & 3) * 4 + ch].y);
+                    const int left = lim - 32 * ch;  // visible columns from the part's first on
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        if (y >> k & 1) r[ch][k] = 0x7fc00000u;
-                        if (32 * ch + k >= lim) r[ch][k] = 0xff800000u;
-                    }
-                    if (32 * ch >= lim) c[ch] = 1.f, lv[ch] = 0.f, iv[ch] = 1.f;
+                    for (int k = 0; k < 32; ++k)
+                        if (k >= left) r[ch][k] = 0xff800000u;
+                    if (left <= 0) c[ch] = 1.f, lv[ch] = 0.f, iv[ch] = 1.f;
                     mx = fmaxf(mx, fmaf(max32(r[ch]), c[ch], lv[ch]));
                 }
             }
@@ -664,7 +697,7 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, uint8_
                 give(piece, o);
             }
             __syncwarp();
-#pragma unroll 2
+#pragma unroll 4
             for (int k = 0; k < 8; ++k) {
                 const int at = __shfl_sync(0xffffffffu, row, 4 * k + (lane >> 3));
 #pragma unroll
