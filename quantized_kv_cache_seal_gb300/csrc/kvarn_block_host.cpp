@@ -2,6 +2,7 @@
 // host mirror of sequence lengths and pool slots, launch parameters, and the C ABI.
 #include <algorithm>
 #include <cmath>
+#include <cstdint>
 #include <cstdio>
 #include <cstring>
 #include <memory>
@@ -266,7 +267,11 @@ kvarn_status run_decode(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, con
         if (units >= 1ll << 31) return fail(KVARN_ECAPACITY, "2^31 tiles of 32 tokens or more in a call");
     }
     p.units = units;
-    p.grid = (int32_t)std::min<int64_t>(units, std::min(c->sms, kBlockMaxGrid));
+    // One CTA a SM, each of its eight warps a unit at least. Equal short sequences: whole (sequence, KV
+    // head) pairs, so that nothing is joined across CTAs (which takes about as long as four rounds).
+    const int64_t pairs = (int64_t)n_seqs * c->cfg.num_kv_heads, most = std::min(c->sms, kBlockMaxGrid);
+    const bool equal = std::all_of(p.seqs, p.seqs + n_seqs, [](const BlockDecodeSeq& e) { return e.units == p.seqs[0].units; });
+    p.grid = (int32_t)(equal && p.seqs[0].units <= 32 && pairs <= most ? pairs : std::min((units + 7) / 8, most));
     if (c->host_only) return KVARN_OK;
     const kvarn_status st = ensure_init(c, stream);
     if (st) return st;
@@ -569,12 +574,23 @@ kvarn_status kvarn_qk_norm_rope(const kvarn_qk_config* cfg, int64_t n_tokens, co
     p.in_bf16 = cfg->in_type == KVARN_TYPE_BF16;
     p.out_bf16 = cfg->out_type == KVARN_TYPE_BF16;
     p.eps = cfg->eps;
-    // Heads an item: about 9,700 groups of 16 lanes are resident, so few rows go one a group; more go
-    // four (the rows in flight) and then as many as leave each group two items, up to 16, for the
-    // angle's sake.
-    const int64_t rows = n_tokens * (hq + hk);
-    p.heads_per_item = rows <= 9728 ? 1 : (int32_t)std::min<int64_t>(16, std::max<int64_t>(4, rows / (2 * 9728) / 4 * 4));
-    p.items_per_token = (int32_t)((hq + hk + p.heads_per_item - 1) / p.heads_per_item);
+    // Heads an item, by rounds of the groups that are resident (155,648 lanes): few rows go one a group;
+    // more, what ends soonest, an item counting as its rows (four in flight at a time) and eight more
+    // for the angle and the start. (Measured: 4096 tokens of 40 heads 24.9 us with the 20 that this
+    // gives, 27.0 with 8; 49157 of 50 204 us with all, 224 with 8; 20000 of 18 48.6 us with all, 57.5
+    // with 12.) And items a group in turn, for the phase's sake, while three rounds of groups are left.
+    const int64_t heads = hq + hk, resident = 155648 / (d <= 64 ? 8 : d <= 128 ? 16 : 32);
+    p.heads_per_item = 1;
+    if (n_tokens * heads > resident) {
+        int64_t best = INT64_MAX;
+        for (int64_t h = 4; h < std::min<int64_t>(heads, 64) + 4; h += 4) {
+            const int64_t items = n_tokens * ((heads + h - 1) / h), cost = (items + resident - 1) / resident * (h + 8);
+            if (cost < best) best = cost, p.heads_per_item = (int32_t)h;
+        }
+    }
+    p.items_per_token = (int32_t)((heads + p.heads_per_item - 1) / p.heads_per_item);
+    p.items_per_group = (int32_t)std::min<int64_t>(8, std::max<int64_t>(1, n_tokens * p.items_per_token / (3 * resident)));
+    p.inv_d = 1.f / (float)d;
     const int rc = launch_qk_norm_rope(p, stream);
     return rc ? cuda_fail(rc, "norm and rotation launch") : KVARN_OK;
 }

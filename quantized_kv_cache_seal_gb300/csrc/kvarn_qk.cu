@@ -10,7 +10,7 @@
 // fraction of a turn: frac(freq / 2 pi) * 2^64 times the position, modulo 2^64, drops
 // whole turns exactly at any position; its top 32 bits then go to sincospi. The fraction is
 // the only fp64 arithmetic (slow on this chip: done once an item it took twice the time of
-// the memory traffic), so groups stay and take items in turn, and it is done once a group.
+// the memory traffic), so in large calls a group takes several items and does it once.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -21,7 +21,6 @@ namespace kvarn {
 namespace {
 
 constexpr int kQkThreads = 128;
-constexpr int kQkMaxCtas = 152 * 8;  // as many as are resident
 
 template <bool BF16>
 __device__ __forceinline__ float2 unpack2(uint32_t w) {
@@ -60,8 +59,11 @@ __global__ void __launch_bounds__(kQkThreads, 8) qk_kernel(const __grid_constant
             frac[i] = (uint64_t)(f * 18446744073709551616.0);
         }
     }
-    const int items = (int)(p.n_tokens * p.items_per_token), step = gridDim.x * (kQkThreads / LANES);
-    for (int item = (blockIdx.x * kQkThreads + threadIdx.x) / LANES; item < items; item += step) {  // whole groups
+    // a CTA's items are consecutive, its groups take them in turn
+    constexpr int kGroups = kQkThreads / LANES;
+    const int items = (int)(p.n_tokens * p.items_per_token), first = blockIdx.x * kGroups * p.items_per_group;
+    const int end = min(items, first + kGroups * p.items_per_group);
+    for (int item = first + threadIdx.x / LANES; item < end; item += kGroups) {  // whole groups
         const int64_t tok = item / p.items_per_token;
         const int h0 = item % p.items_per_token * p.heads_per_item, h1 = min(h0 + p.heads_per_item, p.hq + p.hkv);
         const uint16_t* qr = p.q + tok * p.q_stride;
@@ -113,7 +115,7 @@ __global__ void __launch_bounds__(kQkThreads, 8) qk_kernel(const __grid_constant
                     for (int i = 0; i < 8; ++i) ss = fmaf(y[i], y[i], ss);
 #pragma unroll
                     for (int m = LANES / 2; m > 0; m >>= 1) ss += __shfl_xor_sync(group, ss, m);
-                    const float rs = rsqrtf(ss / (float)p.d + p.eps);
+                    const float rs = rsqrtf(ss * p.inv_d + p.eps);
                     if (live) {  // 1 KB at most: from the first cache
                         const float4 w0 = __ldg(reinterpret_cast<const float4*>(wt + c0));
                         const float4 w1 = __ldg(reinterpret_cast<const float4*>(wt + c1));
@@ -157,8 +159,8 @@ __global__ void __launch_bounds__(kQkThreads, 8) qk_kernel(const __grid_constant
 template <bool I, bool O>
 int launch_qk(const QkParams& p, cudaStream_t s) {
     const int lanes = p.d <= 64 ? 8 : p.d <= 128 ? 16 : 32;
-    const int64_t ctas = (p.n_tokens * p.items_per_token * lanes + kQkThreads - 1) / kQkThreads;
-    const unsigned grid = (unsigned)(ctas < kQkMaxCtas ? ctas : kQkMaxCtas);
+    const int64_t per_cta = (int64_t)(kQkThreads / lanes) * p.items_per_group;
+    const unsigned grid = (unsigned)((p.n_tokens * p.items_per_token + per_cta - 1) / per_cta);
     if (lanes == 8) qk_kernel<I, O, 8><<<grid, kQkThreads, 0, s>>>(p);
     else if (lanes == 16) qk_kernel<I, O, 16><<<grid, kQkThreads, 0, s>>>(p);
     else qk_kernel<I, O, 32><<<grid, kQkThreads, 0, s>>>(p);

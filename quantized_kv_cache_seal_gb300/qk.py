@@ -63,19 +63,23 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Te
     for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
         if w is not None and (w.dtype != torch.float32 or w.shape != (dim,) or w.device != device or not w.is_contiguous()):
             _refuse(name, w, f"a contiguous float32 tensor [{dim}] on {device}")
+    cfg = _config(hq, hkv, dim, 2 * freqs.shape[0], int(interleaved), _TYPES[in_type], _TYPES[out_type], eps)
     with K.on_device(device):
         if stream is None:
             stream = K.current_stream(device)
             where = _HERE
         else:  # results are allocated on the stream that writes them
             where = torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+        qos, kos = hq * dim, hkv * dim
         with where:
             if q_out is None:
                 q_out = torch.empty((tokens, hq, dim), dtype=out_type, device=device)
-            if k is not None and k_out is None:
-                k_out = torch.empty((tokens, hkv, dim), dtype=out_type, device=device)
-        qos = _stride(q_out, "q_out", out_type, device, tokens, hq, dim)
-        kos = 0 if k is None else _stride(k_out, "k_out", out_type, device, tokens, hkv, dim)
-        cfg = _config(hq, hkv, dim, 2 * freqs.shape[0], int(interleaved), _TYPES[in_type], _TYPES[out_type], eps)
+            else:
+                qos = _stride(q_out, "q_out", out_type, device, tokens, hq, dim)
+            if k is not None:
+                if k_out is None:
+                    k_out = torch.empty((tokens, hkv, dim), dtype=out_type, device=device)
+                else:
+                    kos = _stride(k_out, "k_out", out_type, device, tokens, hkv, dim)
         K.kvarn_qk_norm_rope(cfg, tokens, q, qs, k, ks, q_weight, k_weight, positions, freqs, q_out, qos, k_out, kos, stream)
     return q_out, k_out
