@@ -326,7 +326,9 @@ kvarn_status kvarn_device_accessible(const void* ptr, int32_t* accessible);
  *   - Calls that change a cache, and the first call on one, cannot be captured into a graph
  *     (KVARN_ESTATE): the host's lengths would not follow a replay. decode_attention,
  *     prefill_attention and read can; a replay sees the lengths of the capture, and the
- *     sequences must not have been released since.
+ *     sequences must not have been released since. A replay is a call: those of one cache stay
+ *     ordered on the GPU, since they share its workspace.
+ *   - q and out do not overlap.
  *   - kvarn_last_error says what a refused call was refused for. */
 #define KVARN_TYPE_F16 0
 #define KVARN_TYPE_BF16 1
@@ -344,7 +346,7 @@ typedef struct {
     int32_t block_tokens;   /* 32, 64 or 128 */
     int32_t code;           /* KVARN_CODE_* */
     int32_t type;           /* KVARN_TYPE_* of exact values, inputs and outputs */
-    int32_t max_seq_len;    /* longest sequence, tokens */
+    int32_t max_seq_len;    /* longest sequence, tokens, at most 2^30 */
     int32_t pool_blocks;    /* blocks in the pool; one holds one (sequence, layer, block) for all KV heads */
     int32_t flags;          /* 0 or KVARN_FLAG_HOST_ONLY */
 } kvarn_block_config;

@@ -323,6 +323,10 @@ int launch_block_init(const BlockView& c, void* stream) {
     return (int)cudaMemsetAsync(c.base + c.lay.err, 0, c.lay.partials - c.lay.err, (cudaStream_t)stream);
 }
 
+int launch_block_clear_counters(const BlockView& c, void* stream) {
+    return (int)cudaMemsetAsync(c.base + c.lay.counters, 0, kBlockMaxGrid * 4, (cudaStream_t)stream);
+}
+
 int stream_capturing(void* stream, int* capturing) {
     cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
     const cudaError_t e = cudaStreamIsCapturing((cudaStream_t)stream, &st);

@@ -91,8 +91,8 @@ kvarn_status check_config(const kvarn_block_config* c) {
     if (c->num_q_heads % c->num_kv_heads || c->num_q_heads / c->num_kv_heads > kBlockMaxRatio)
         return fail(KVARN_EINVAL, "num_q_heads must be 1 to 8 times num_kv_heads");
     if ((c->flags & ~KVARN_FLAG_HOST_ONLY) != 0) return fail(KVARN_EINVAL, "unknown flag");
-    if ((int64_t)c->max_seqs * c->num_layers > (1ll << 31) - 1 || c->num_kv_heads > (1 << 16))
-        return fail(KVARN_EINVAL, "too many sequences, layers or heads");
+    if ((int64_t)c->max_seqs * c->num_layers > (1ll << 31) - 1 || c->num_kv_heads > (1 << 16) || c->max_seq_len > (1 << 30))
+        return fail(KVARN_EINVAL, "too many sequences, layers or heads, or max_seq_len above 2^30");
     return KVARN_OK;
 }
 
@@ -523,7 +523,11 @@ kvarn_status kvarn_block_check_device_error(kvarn_block_cache* c, void* stream) 
     const int32_t zero[4] = {0, 0, 0, 0};
     rc = memcpy_h2d_async(c->view.base + c->view.lay.err, zero, sizeof(zero), stream);
     if (rc) return cuda_fail(rc, "error word clear");
-    return err[0] & kErrTimeout ? KVARN_ETIMEOUT : err[0] ? KVARN_ESTATE : KVARN_OK;
+    if (err[0] == 0) return KVARN_OK;
+    // a launch in which a wait gave up may have left its counters standing
+    rc = launch_block_clear_counters(c->view, stream);
+    if (rc) return cuda_fail(rc, "counter clear");
+    return err[0] & kErrTimeout ? KVARN_ETIMEOUT : KVARN_ESTATE;
 }
 
 kvarn_status kvarn_qk_norm_rope(const kvarn_qk_config* cfg, int64_t n_tokens, const void* q, int64_t q_stride, const void* k,

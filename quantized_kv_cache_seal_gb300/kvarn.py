@@ -8,6 +8,7 @@ import of this module fails.
 """
 from __future__ import annotations
 
+import array
 import contextlib
 import ctypes
 import os
@@ -350,12 +351,12 @@ def current_stream(device) -> int:
 
 
 def _i32(xs):
-    """A host int32 array of a sequence of ints."""
+    """A host int32 array of a sequence of ints (OverflowError where one does not fit)."""
     n = len(xs)
     kind = _ARRAYS.get(n)
     if kind is None:
         kind = _ARRAYS[n] = ctypes.c_int32 * n
-    return kind(*xs)
+    return kind.from_buffer(array.array("i", xs)) if n else kind()
 
 
 _ARRAYS: dict = {}

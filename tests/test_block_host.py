@@ -35,7 +35,7 @@ def refused(status, call, *args, **kw):
 @pytest.mark.parametrize("bad", [
     dict(head_dim=96), dict(head_dim=0), dict(block_tokens=16), dict(block_tokens=256), dict(code=2), dict(type=2),
     dict(num_q_heads=7), dict(num_q_heads=18), dict(num_kv_heads=0), dict(num_layers=0), dict(max_seqs=-1),
-    dict(max_seq_len=0), dict(pool_blocks=-1), dict(flags=2), dict(num_layers=2 ** 31 - 1, max_seqs=2 ** 31 - 1),
+    dict(max_seq_len=0), dict(max_seq_len=2 ** 30 + 1), dict(pool_blocks=-1), dict(flags=2), dict(num_layers=2 ** 31 - 1, max_seqs=2 ** 31 - 1),
     dict(num_layers=2 ** 30, max_seqs=1, max_seq_len=2 ** 31 - 1)])
 def test_bad_configurations(bad):
     refused(1, K.kvarn_block_required_bytes, config(**bad))
@@ -157,6 +157,21 @@ def test_read_and_attention_refusals():
     refused(1, K.kvarn_block_length, c, 0, 4)
     refused(1, K.kvarn_block_release, c, [4])
     assert K.kvarn_block_check_device_error(c) == 0
+    K.kvarn_block_destroy(c)
+
+
+def test_ids_that_do_not_fit():
+    """Numbers beyond 32 bits are refused, not cut."""
+    c = cache()
+    for bad in ([2 ** 32], [2 ** 31], [-2 ** 31 - 1]):
+        with pytest.raises(OverflowError):
+            K.kvarn_block_append(c, 0, bad, [1], FAKE, 256, FAKE, 256)
+        with pytest.raises(OverflowError):
+            K.kvarn_block_append(c, 0, [0], bad, FAKE, 256, FAKE, 256)
+        with pytest.raises(OverflowError):
+            K.kvarn_block_release(c, bad)
+    with pytest.raises(TypeError):
+        K.kvarn_block_append(c, 0, [0.5], [1], FAKE, 256, FAKE, 256)
     K.kvarn_block_destroy(c)
 
 

@@ -394,6 +394,52 @@ def test_nan_of_a_later_token_stays_there(dtype, at, side):
         assert bool(outs[2][first - (n - m):].isnan().all())
 
 
+def test_nothing_around_the_outputs_is_written():
+    """Outputs inside larger buffers: what stands before and behind stays, for every call that writes one."""
+    from quantized_kv_cache_seal_gb300.qk import qk_norm_rope
+    for dim, hkv, r in ((128, 2, 3), (64, 1, 8)):
+        hq = hkv * r
+        c = make(num_q_heads=hq, num_kv_heads=hkv, head_dim=dim, block_tokens=32)
+        lens = [100, 33, 7]
+        fill(c, lens, torch.float16, 110)
+        for ids, m in (([0, 1, 2], None), ([1, 0], [33, 50]), ([2], [1]), ([0, 2], [0, 7])):
+            rows = len(ids) if m is None else sum(m)
+            q = tokens(rows, hq, dim, torch.float16, 111)
+            big = torch.full((rows + 20, hq, dim), 7.0, dtype=torch.float16, device="cuda")
+            out = big[10:10 + rows]
+            if m is None:
+                c.decode_attention(0, ids, q, out=out)
+            else:
+                c.prefill_attention(0, ids, m, q, out=out)
+            assert bool((big[:10] == 7).all()) and bool((big[10 + rows:] == 7).all())
+            assert not bool((out == 7).all(dim=-1).any())
+    qkv = tokens(37, 10, 80, torch.bfloat16, 112)
+    big = torch.full((57, 10, 80), 7.0, dtype=torch.bfloat16, device="cuda")
+    pos, freqs = torch.arange(37, dtype=torch.int32, device="cuda"), torch.rand(20, dtype=torch.float64, device="cuda")
+    qk_norm_rope(qkv[:, :6], qkv[:, 6:8], pos, freqs, q_out=big[10:47, :6], k_out=big[10:47, 6:8])
+    assert bool((big[:10] == 7).all()) and bool((big[47:] == 7).all()) and bool((big[:, 8:] == 7).all())
+
+
+def test_two_caches_on_two_streams():
+    """Caches have workspaces of their own: calls on two of them may overlap."""
+    a, b = (make(max_seqs=2, block_tokens=32, max_seq_len=4000) for _ in range(2))
+    fill(a, [3000, 1000], torch.float16, 120)
+    fill(b, [2000, 3500], torch.float16, 122)
+    q = tokens(600, 8, 128, torch.float16, 124, 0.3)
+    want = [(c.decode_attention(0, [0, 1], q[:2]), c.prefill_attention(0, [0, 1], [400, 200], q)) for c in (a, b)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(5):
+        for i, c in enumerate((a, b)):
+            got[i].append((c.decode_attention(0, [0, 1], q[:2], stream=streams[i]),
+                           c.prefill_attention(0, [0, 1], [400, 200], q, stream=streams[i])))
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        for x in g:
+            assert torch.equal(x[0], w[0]) and torch.equal(x[1], w[1])
+
+
 def test_streams_and_graphs():
     """Calls on another stream; decode, prefill and read captured and replayed with new queries; calls that change
     the cache refused while capturing."""
