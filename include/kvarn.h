@@ -325,10 +325,13 @@ kvarn_status kvarn_device_accessible(const void* ptr, int32_t* accessible);
  *   - The current device must be the one that holds the cache (EINVAL otherwise).
  *   - Calls that change a cache, and the first call on one, cannot be captured into a graph
  *     (KVARN_ESTATE): the host's lengths would not follow a replay. decode_attention,
- *     prefill_attention and read can; a replay sees the lengths of the capture, and the
- *     sequences must not have been released since. A replay is a call: those of one cache stay
- *     ordered on the GPU, since they share its workspace.
+ *     prefill_attention and read can; a replay sees the lengths of the capture, so the
+ *     sequences must not have been released since, nor the block that was partial then have
+ *     filled (its exact tokens make room for the next block's). A replay is a call: those of
+ *     one cache stay ordered on the GPU, since they share its workspace.
  *   - q and out do not overlap.
+ *   - Attention tells a head's V scales apart up to a ratio of 2^100 (fp16 never leaves it):
+ *     tokens of bf16 blocks smaller than that against the largest can count for nothing.
  *   - kvarn_last_error says what a refused call was refused for. */
 #define KVARN_TYPE_F16 0
 #define KVARN_TYPE_BF16 1
@@ -425,9 +428,10 @@ typedef struct {
  * num_q_heads * head_dim, a multiple of 8; k, q_out, k_out likewise), so that q and k may be
  * parts of a packed projection; 16-byte aligned. q_weight, k_weight: f32 [head_dim], 16-byte
  * aligned, or NULL.
- * positions: int32 [n_tokens]; freqs: f64 [rot_dim / 2], radians per position (both may be
- * NULL if rot_dim is 0). An output may be its own input (same address, stride and type);
- * any other overlap is not allowed. All pointers device. Can be captured. */
+ * positions: int32 [n_tokens]; freqs: f64 [rot_dim / 2], finite, radians per position (both
+ * may be NULL if rot_dim is 0). n_tokens times all heads is at most 2^31 - 1024 (EINVAL). An
+ * output may be its own input (same address, stride and type); any other overlap is not
+ * allowed. All pointers device. Can be captured. */
 kvarn_status kvarn_qk_norm_rope(const kvarn_qk_config* cfg, int64_t n_tokens, const void* q, int64_t q_stride,
                                 const void* k, int64_t k_stride, const float* q_weight, const float* k_weight,
                                 const int32_t* positions, const double* freqs, void* q_out, int64_t q_out_stride,

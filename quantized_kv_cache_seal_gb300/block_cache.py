@@ -29,12 +29,14 @@ class BlockCache:
                                         _CODES[code], _TYPES[dtype], max_seq_len, pool_blocks, flags)
         self.handle = None
         self.dtype = dtype
+        self.heads, self.kv_heads, self.dim = num_q_heads, num_kv_heads, head_dim
         self.scale = 1.0 / math.sqrt(head_dim)
         self.nbytes = K.kvarn_block_required_bytes(self.cfg)
         self.mem = torch.empty(self.nbytes + 256, dtype=torch.uint8, device=device)
         self.device = self.mem.device
+        self.index = self.mem.get_device()  # -1: the CPU
         base = (self.mem.data_ptr() + 255) // 256 * 256
-        with self._here():
+        with K.on_device(self.device):
             self.handle = K.kvarn_block_create(self.cfg, base, self.nbytes)
 
     def close(self):
@@ -48,41 +50,26 @@ class BlockCache:
         except Exception:
             pass
 
-    # -- tensors, streams ------------------------------------------------------------------------------------
-    def _here(self):
-        return K.on_device(self.device)
-
-    def _stream(self, stream):
-        if stream is not None or self.device.type != "cuda":
-            return stream
-        return K.current_stream(self.device)
-
-    def _empty(self, shape, dtype, stream):
-        """A result of a call on `stream`, allocated there: freed memory of another stream may still be in use."""
-        if stream is None or self.device.type != "cuda":
-            return torch.empty(shape, dtype=dtype, device=self.device)
-        if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=self.device)
-        with torch.cuda.stream(stream):
-            return torch.empty(shape, dtype=dtype, device=self.device)
-
+    # -- tensors ---------------------------------------------------------------------------------------------
     def _refuse(self, name, x, what):
         raise ValueError(f"{name} must be {what} on {self.device}, got {x.dtype} {tuple(x.shape)} with strides "
                          f"{x.stride()} on {x.device}")
 
     def _dense(self, x, rows, name):
-        want = (rows, self.cfg.num_q_heads, self.cfg.head_dim)
-        if x.shape != want or x.dtype != self.dtype or x.device != self.device or not x.is_contiguous():
+        want = (rows, self.heads, self.dim)
+        if x.shape != want or x.dtype is not self.dtype or x.get_device() != self.index or not x.is_contiguous():
             self._refuse(name, x, f"a contiguous {self.dtype} tensor {want}")
 
     def _tokens(self, x, rows, name):
         """Elements between the tokens of k or v; its heads and channels are dense."""
-        heads, dim = self.cfg.num_kv_heads, self.cfg.head_dim
-        stride = x.stride()
-        if (x.shape != (rows, heads, dim) or x.dtype != self.dtype or x.device != self.device
-                or (rows > 0 and (stride[2] != 1 or (heads > 1 and stride[1] != dim)))):
-            self._refuse(name, x, f"a {self.dtype} tensor {(rows, heads, dim)} with dense heads")
-        return stride[0] if rows > 1 else heads * dim
+        heads, dim = self.kv_heads, self.dim
+        if x.shape == (rows, heads, dim) and x.dtype is self.dtype and x.get_device() == self.index:
+            if x.is_contiguous():
+                return heads * dim
+            between, head, channel = x.stride()
+            if channel == 1 and (heads == 1 or head == dim):
+                return between if rows > 1 else heads * dim
+        self._refuse(name, x, f"a {self.dtype} tensor {(rows, heads, dim)} with dense heads")
 
     # -- calls -----------------------------------------------------------------------------------------------
     def append(self, layer: int, seq_ids: Sequence[int], n_tokens: Sequence[int], k: torch.Tensor, v: torch.Tensor,
@@ -91,8 +78,8 @@ class BlockCache:
         rows = sum(n_tokens)
         ks, vs = self._tokens(k, rows, "k"), self._tokens(v, rows, "v")
         _same_length(seq_ids, n_tokens)
-        with self._here():
-            K.kvarn_block_append(self.handle, layer, seq_ids, n_tokens, k, ks, v, vs, self._stream(stream))
+        with K.on_device(self.device, stream) as stream:
+            K.kvarn_block_append(self.handle, layer, seq_ids, n_tokens, k, ks, v, vs, stream)
 
     def read(self, layer: int, seq_ids: Sequence[int], starts: Optional[Sequence[int]], counts: Sequence[int],
              dtype: Optional[torch.dtype] = None, stream=None):
@@ -106,27 +93,26 @@ class BlockCache:
             _same_length(seq_ids, starts)
         if any(n < 0 for n in counts):
             raise ValueError("counts must not be negative")
-        shape = (sum(counts), self.cfg.num_kv_heads, self.cfg.head_dim)
-        k, v = self._empty(shape, dtype, stream), self._empty(shape, dtype, stream)
-        with self._here():
-            K.kvarn_block_read(self.handle, layer, seq_ids, starts, counts, k, v, dtype == torch.float32,
-                               self._stream(stream))
+        shape = (sum(counts), self.kv_heads, self.dim)
+        with K.on_device(self.device, stream) as stream:
+            k, v = (torch.empty(shape, dtype=dtype, device=self.device) for _ in range(2))
+            K.kvarn_block_read(self.handle, layer, seq_ids, starts, counts, k, v, dtype is torch.float32, stream)
         return k, v
 
-    def _attention(self, q, rows, out, stream):
+    def _queries(self, q, rows, out):
         self._dense(q, rows, "q")
-        if out is None:
-            return self._empty(q.shape, q.dtype, stream)
-        self._dense(out, rows, "out")
-        return out
+        if out is not None:
+            self._dense(out, rows, "out")
 
     def decode_attention(self, layer: int, seq_ids: Sequence[int], q: torch.Tensor, out: Optional[torch.Tensor] = None,
                          scale: Optional[float] = None, stream=None) -> torch.Tensor:
         """One query token per sequence over all its cached tokens; q, out: [len(seq_ids)][Hq][D]."""
-        out = self._attention(q, len(seq_ids), out, stream)
-        with self._here():
+        self._queries(q, len(seq_ids), out)
+        with K.on_device(self.device, stream) as stream:
+            if out is None:
+                out = torch.empty_like(q)
             K.kvarn_block_decode_attention(self.handle, layer, seq_ids, q, out, self.scale if scale is None else scale,
-                                           self._stream(stream))
+                                           stream)
         return out
 
     def decode_step(self, layer: int, seq_ids: Sequence[int], k: torch.Tensor, v: torch.Tensor, q: torch.Tensor,
@@ -134,10 +120,12 @@ class BlockCache:
         """Append one token per sequence and attend its query; k, v: [len(seq_ids)][Hkv][D]."""
         n = len(seq_ids)
         ks, vs = self._tokens(k, n, "k"), self._tokens(v, n, "v")
-        out = self._attention(q, n, out, stream)
-        with self._here():
+        self._queries(q, n, out)
+        with K.on_device(self.device, stream) as stream:
+            if out is None:
+                out = torch.empty_like(q)
             K.kvarn_block_decode_step(self.handle, layer, seq_ids, k, ks, v, vs, q, out,
-                                      self.scale if scale is None else scale, self._stream(stream))
+                                      self.scale if scale is None else scale, stream)
         return out
 
     def prefill_attention(self, layer: int, seq_ids: Sequence[int], q_lens: Sequence[int], q: torch.Tensor,
@@ -145,10 +133,12 @@ class BlockCache:
                           stream=None) -> torch.Tensor:
         """Causal attention of the last q_lens[i] tokens of each sequence; q, out: [sum(q_lens)][Hq][D]."""
         _same_length(seq_ids, q_lens)
-        out = self._attention(q, sum(q_lens), out, stream)
-        with self._here():
+        self._queries(q, sum(q_lens), out)
+        with K.on_device(self.device, stream) as stream:
+            if out is None:
+                out = torch.empty_like(q)
             K.kvarn_block_prefill_attention(self.handle, layer, seq_ids, q_lens, q, out,
-                                            self.scale if scale is None else scale, self._stream(stream))
+                                            self.scale if scale is None else scale, stream)
         return out
 
     def prefill(self, layer: int, seq_ids: Sequence[int], n_tokens: Sequence[int], k: torch.Tensor, v: torch.Tensor,
@@ -158,10 +148,12 @@ class BlockCache:
         _same_length(seq_ids, n_tokens)
         rows = sum(n_tokens)
         ks, vs = self._tokens(k, rows, "k"), self._tokens(v, rows, "v")
-        out = self._attention(q, rows, out, stream)
-        with self._here():
+        self._queries(q, rows, out)
+        with K.on_device(self.device, stream) as stream:
+            if out is None:
+                out = torch.empty_like(q)
             K.kvarn_block_prefill(self.handle, layer, seq_ids, n_tokens, k, ks, v, vs, q, out,
-                                  self.scale if scale is None else scale, self._stream(stream))
+                                  self.scale if scale is None else scale, stream)
         return out
 
     def release(self, seq_ids: Union[int, Sequence[int]]):
@@ -173,8 +165,8 @@ class BlockCache:
         return K.kvarn_block_length(self.handle, layer, seq_id)
 
     def check_device_error(self, stream=None) -> int:
-        with self._here():
-            return K.kvarn_block_check_device_error(self.handle, self._stream(stream))
+        with K.on_device(self.device, stream) as stream:
+            return K.kvarn_block_check_device_error(self.handle, stream)
 
 
 def _same_length(seq_ids, counts):

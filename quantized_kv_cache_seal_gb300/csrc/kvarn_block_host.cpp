@@ -44,6 +44,8 @@ kvarn_status cuda_fail(int rc, const char* what) {
     return fail(KVARN_ECUDA, text);
 }
 
+constexpr float kLog2e = 1.4426950408889634f;
+
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
 // Device layout of a cache; false if the sizes leave what an address can hold.
@@ -231,7 +233,7 @@ kvarn_status append(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const i
 
 kvarn_status check_attention(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* ids, const int32_t* q_lens,
                              const int32_t* added, const void* q, const void* out, float scale) {
-    if (!std::isfinite(scale)) return fail(KVARN_EINVAL, "softmax_scale must be finite");
+    if (!std::isfinite(scale * kLog2e)) return fail(KVARN_EINVAL, "softmax_scale must be finite, below 2^127");
     int64_t rows = 0;
     for (int i = 0; i < n_seqs; ++i) {
         const int64_t n = c->L(ids[i], layer) + (added ? (int64_t)added[i] : 0);
@@ -255,7 +257,7 @@ kvarn_status run_decode(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, con
     p.n_seqs = n_seqs;
     p.hq = c->cfg.num_q_heads;
     p.r = c->r;
-    p.scale_log2 = scale * 1.4426950408889634f;
+    p.scale_log2 = scale * kLog2e;
     int64_t units = 0;
     for (int i = 0; i < n_seqs; ++i) {
         BlockDecodeSeq& e = p.seqs[i];
@@ -296,7 +298,7 @@ kvarn_status run_prefill(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, co
     p.out = (uint16_t*)out;
     p.hq = c->cfg.num_q_heads;
     p.r = c->r;
-    p.scale_log2 = scale * 1.4426950408889634f;
+    p.scale_log2 = scale * kLog2e;
     p.n_seqs = 0;
     const int hkv = c->cfg.num_kv_heads, pair_tokens = 2 * (128 / c->r);
     int64_t row = 0;
@@ -544,7 +546,8 @@ kvarn_status kvarn_qk_norm_rope(const kvarn_qk_config* cfg, int64_t n_tokens, co
         (cfg->out_type != KVARN_TYPE_F16 && cfg->out_type != KVARN_TYPE_BF16))
         return fail(KVARN_EINVAL, "unknown type");
     if (!(cfg->eps >= 0.f) || !std::isfinite(cfg->eps)) return fail(KVARN_EINVAL, "eps must be finite and not negative");
-    if (n_tokens < 0 || n_tokens * (hq + hk) >= 1ll << 31) return fail(KVARN_EINVAL, "bad token count");
+    // the kernel counts items in 32 bits, a CTA's (up to 128) beyond the last one among them
+    if (n_tokens < 0 || n_tokens > ((1ll << 31) - 1024) / (hq + hk)) return fail(KVARN_EINVAL, "bad token count");
     if (n_tokens == 0) return KVARN_OK;
     struct Side { const void* in; const void* out; int64_t heads, in_stride, out_stride; };
     for (const Side& s : {Side{q, q_out, hq, q_stride, q_out_stride}, Side{k, k_out, hk, k_stride, k_out_stride}}) {

@@ -330,16 +330,35 @@ def kvarn_last_error() -> str:
     return load().kvarn_last_error().decode()
 
 
-_HERE = contextlib.nullcontext()
+class on_device:
+    """`device` (a torch.device with an index) as the current one, and `stream` (None: the device's current one) as the
+    current stream, so that what is allocated inside belongs to the stream that will use it. Gives the stream to
+    pass on; on the CPU does nothing."""
 
+    __slots__ = ("device", "stream", "outer")
 
-def on_device(device):
-    """`device` (a torch.device with an index) as the current one; nothing to do where it is."""
-    import torch
+    def __init__(self, device, stream=None):
+        self.device, self.stream, self.outer = device, stream, None
 
-    if device.type != "cuda" or torch.cuda.current_device() == device.index:
-        return _HERE
-    return torch.cuda.device(device)
+    def __enter__(self):
+        import torch
+
+        if self.device.type != "cuda":
+            return self.stream
+        if self.stream is None and torch.cuda.current_device() == self.device.index:
+            return current_stream(self.device)
+        s = self.stream
+        if isinstance(s, int):  # an external stream of address 0 would be a new one
+            s = torch.cuda.ExternalStream(s, device=self.device) if s else torch.cuda.default_stream(self.device)
+        if s is not None and s.device != self.device:
+            raise ValueError(f"stream of {s.device}, tensors on {self.device}")
+        self.outer = contextlib.ExitStack()
+        self.outer.enter_context(torch.cuda.device(self.device) if s is None else torch.cuda.stream(s))
+        return current_stream(self.device)
+
+    def __exit__(self, *exc):
+        if self.outer is not None:
+            self.outer.close()
 
 
 def current_stream(device) -> int:

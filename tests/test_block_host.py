@@ -244,6 +244,22 @@ def test_norm_rope_refusals():
     K.kvarn_qk_norm_rope(qk(), 0, None, 0, None, 0, None, None, None, None, None, 0, None, 0)  # no tokens
 
 
+def test_norm_rope_token_counts_that_do_not_fit():
+    """Products of tokens and heads that leave 64 bits, or 32 bits together with a CTA's share behind the last token."""
+    big = 1 << 60  # times 16 heads: 0 modulo 2^64
+    refused(1, K.kvarn_qk_norm_rope, qk(num_q_heads=8, num_kv_heads=8), big, FAKE, 1024, FAKE, 1024, None, None, FAKE, FAKE,
+            FAKE, 1024, FAKE, 1024)
+    one = qk(num_q_heads=1, num_kv_heads=0, head_dim=8, rot_dim=8)
+    refused(1, K.kvarn_qk_norm_rope, one, (1 << 31) - 1, FAKE, 8, None, 0, None, None, FAKE, FAKE, FAKE, 8, None, 0)
+
+
+def test_scale_that_leaves_fp32():
+    c = cache()
+    refused(1, K.kvarn_block_decode_attention, c, 0, [0], FAKE, FAKE, 3e38)  # times log2 e
+    refused(1, K.kvarn_block_prefill_attention, c, 0, [0], [0], FAKE, FAKE, -3e38)
+    K.kvarn_block_destroy(c)
+
+
 def test_norm_rope_wrapper_wants_cuda_tensors():
     q = torch.zeros(3, 4, 64, dtype=torch.float16)
     with pytest.raises(ValueError):
