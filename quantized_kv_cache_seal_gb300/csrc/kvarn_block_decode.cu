@@ -246,7 +246,7 @@ __device__ __forceinline__ void exact_unit(State<D>& st, const uint16_t* k, cons
             y[i][b] = r;
             top = max_of(top, finite_only<BF16>(r));
         }
-    const int e = warp_exponent<BF16>(top) - kExactV;
+    const int e = warp_exponent_v<BF16>(top);
     const float f = power2(-e);
     uint32_t w[2][2];
     weigh<D>(st, s, c0 * ks, c1 * ks, (float)e, f, nv, g, w);

@@ -151,6 +151,16 @@ __device__ __forceinline__ uint4 finite_only(uint4 w) {
 constexpr int kExactV = 8;
 // Exact K values and bf16 queries, whose products only go into fp32 sums, to the top of f16's range.
 constexpr int kExactK = 14;
+// A V of nothing but zeros has no scale of its own, yet its weights (2^(x + log2 s), with 1 / s in the
+// denominator) stand beside the others': with this one they do not set the running maximum, which would
+// push the others out of f16, and do not leave fp32 in the denominator either, for other scales
+// between 2^-60 and 2^50.
+constexpr int kZeroV = -60;
+// Exponent of the power of two that stands for a part's V scale.
+template <bool BF16>
+__device__ __forceinline__ int warp_exponent_v(uint32_t top) {
+    return __any_sync(0xffffffffu, top != 0) ? warp_exponent<BF16>(top) - kExactV : kZeroV;
+}
 
 // Bytes of a 4 x 4 square: r[i] = row i; afterwards r[j] = column j.
 __device__ __forceinline__ void transpose4(uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {

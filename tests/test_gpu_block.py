@@ -329,6 +329,23 @@ def test_scales_of_very_different_size():
         check(out, want, tol, "scales")
 
 
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("power", [-40, -18, 0, 40])
+@pytest.mark.parametrize("where", ["sealed", "exact"])
+def test_values_of_zero_beside_others(where, power, code):
+    """Tokens whose V is zero (a whole block, the exact tokens) keep their weight, and the others their bits."""
+    c = make(num_q_heads=4, num_kv_heads=1, block_tokens=32, dtype=torch.bfloat16, code=code, max_seqs=1)
+    k, v, q = (tokens(n, h, 128, torch.bfloat16, s, 0.2) for n, h, s in ((106, 1, 31), (106, 1, 32), (106, 4, 33)))
+    v = v * 2.0 ** power
+    v[32:64 if where == "sealed" else 32] = 0
+    v[106 if where == "sealed" else 96:] = 0
+    c.append(0, [0], [106], k, v)
+    held = [block_ref.hold(x, 32, code) for x in (k, v)]
+    want, tol = block_ref.attend(q.cpu(), *held, 128 ** -0.5, list(range(106)))
+    check(c.prefill_attention(0, [0], [106], q), want, tol, "prefill")
+    check(c.decode_attention(0, [0], q[105:]), want[105:], tol[105:], "decode")
+
+
 def test_bf16_of_large_range():
     """bf16 queries, keys and values beyond f16's range (their products are not)."""
     c = make(num_q_heads=4, num_kv_heads=1, block_tokens=32, dtype=torch.bfloat16, max_seqs=1)
@@ -474,6 +491,39 @@ def test_streams_and_graphs():
         s.synchronize()
         assert torch.equal(got[0], w[0]) and torch.equal(got[1], w[1])
     assert torch.equal(back[0], c.read(0, [0], [90], [10])[0])
+
+
+def test_replay_after_the_cache_has_moved_on():
+    """A captured call sees the lengths of its capture while its partial block has not filled (or where it had none)."""
+    c = make(block_tokens=32, max_seqs=2)
+    k, v = (tokens(227, 2, 128, torch.float16, s) for s in (61, 62))
+    q = tokens(2, 8, 128, torch.float16, 63)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        c.append(0, [0, 1], [64, 40], k[:104], v[:104])
+        want = c.decode_attention(0, [0, 1], q), c.prefill_attention(0, [1], [2], q)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            got = c.decode_attention(0, [0, 1], q), c.prefill_attention(0, [1], [2], q)
+        c.append(0, [0, 1], [100, 23], k[104:], v[104:])
+        g.replay()
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_the_stream_that_a_call_names_owns_its_results():
+    from quantized_kv_cache_seal_gb300 import kvarn as K
+    device, side = torch.device("cuda", 0), torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        with K.on_device(device, 0) as s:  # the default stream by its address
+            assert s == 0 and torch.cuda.current_stream() == torch.cuda.default_stream()
+        with K.on_device(device) as s:
+            assert s == side.cuda_stream
+    for name in (side, side.cuda_stream):
+        with K.on_device(device, name) as s:
+            assert s == side.cuda_stream and torch.cuda.current_stream().cuda_stream == s
+    assert torch.cuda.current_stream() == torch.cuda.default_stream()
 
 
 def test_chain_as_a_layer_uses_it():
