@@ -137,7 +137,7 @@ struct QkParams {
     const double* freqs;
     int64_t n_tokens;
     int32_t hq, hkv, d, rot, interleaved, in_bf16, out_bf16;
-    int32_t heads_per_item, items_per_token, items_per_group;
+    int32_t heads_per_item, items_per_token;
     float eps, inv_d;
 };
 

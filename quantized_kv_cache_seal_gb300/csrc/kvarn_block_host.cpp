@@ -546,7 +546,7 @@ kvarn_status kvarn_qk_norm_rope(const kvarn_qk_config* cfg, int64_t n_tokens, co
         (cfg->out_type != KVARN_TYPE_F16 && cfg->out_type != KVARN_TYPE_BF16))
         return fail(KVARN_EINVAL, "unknown type");
     if (!(cfg->eps >= 0.f) || !std::isfinite(cfg->eps)) return fail(KVARN_EINVAL, "eps must be finite and not negative");
-    // the kernel counts items in 32 bits, a CTA's (up to 128) beyond the last one among them
+    // the kernel counts items in 32 bits, a CTA's beyond the last one among them
     if (n_tokens < 0 || n_tokens > ((1ll << 31) - 1024) / (hq + hk)) return fail(KVARN_EINVAL, "bad token count");
     if (n_tokens == 0) return KVARN_OK;
     struct Side { const void* in; const void* out; int64_t heads, in_stride, out_stride; };
@@ -581,22 +581,16 @@ kvarn_status kvarn_qk_norm_rope(const kvarn_qk_config* cfg, int64_t n_tokens, co
     p.in_bf16 = cfg->in_type == KVARN_TYPE_BF16;
     p.out_bf16 = cfg->out_type == KVARN_TYPE_BF16;
     p.eps = cfg->eps;
-    // Heads an item, by rounds of the groups that are resident (155,648 lanes): few rows go one a group;
-    // more, what ends soonest, an item counting as its rows (four in flight at a time) and eight more
-    // for the angle and the start. (Measured: 4096 tokens of 40 heads 24.9 us with the 20 that this
-    // gives, 27.0 with 8; 49157 of 50 204 us with all, 224 with 8; 20000 of 18 48.6 us with all, 57.5
-    // with 12.) And items a group in turn, for the phase's sake, while three rounds of groups are left.
-    const int64_t heads = hq + hk, resident = 155648 / (d <= 64 ? 8 : d <= 128 ? 16 : 32);
-    p.heads_per_item = 1;
-    if (n_tokens * heads > resident) {
-        int64_t best = INT64_MAX;
-        for (int64_t h = 4; h < std::min<int64_t>(heads, 64) + 4; h += 4) {
-            const int64_t items = n_tokens * ((heads + h - 1) / h), cost = (items + resident - 1) / resident * (h + 8);
-            if (cost < best) best = cost, p.heads_per_item = (int32_t)h;
-        }
-    }
+    // Heads an item, a group's work in turn. Where the rows are not many times the resident groups (97,280
+    // lanes): four, to have groups enough. Else all of a token's, so that its angles are made once a side; 32
+    // where tokens alone do not fill the machine or rows of very many heads would lie a power of two apart.
+    // (Measured, bf16 with weights, us: 1,000 tokens of 40 heads 10.3 by four, 12.3 by all; 4,096 29.7 by
+    // four, 20.8 by all; 4,000 of 72 43.0 by 32, 35.1 by all; 1,200 of 72 16.4 by 32, 19.8 by all; 4,000 of
+    // 128 50.3 by 32, 57.6 by all.)
+    const int64_t heads = hq + hk, resident = 97280 / (d <= 64 ? 8 : d <= 128 ? 16 : 32);
+    if (n_tokens * heads <= 8 * resident) p.heads_per_item = 4;
+    else p.heads_per_item = n_tokens >= resident / 4 && heads <= 80 ? (int32_t)heads : 32;
     p.items_per_token = (int32_t)((heads + p.heads_per_item - 1) / p.heads_per_item);
-    p.items_per_group = (int32_t)std::min<int64_t>(8, std::max<int64_t>(1, n_tokens * p.items_per_token / (3 * resident)));
     p.inv_d = 1.f / (float)d;
     const int rc = launch_qk_norm_rope(p, stream);
     return rc ? cuda_fail(rc, "norm and rotation launch") : KVARN_OK;

@@ -3,16 +3,19 @@
 //   y_d = x_d rsqrt(mean x^2 + eps) w_d;  pairs (y_i, y_{i+R/2}) or (y_2i, y_{2i+1}) turned
 //   by position * freq_i; channels from R on pass through. fp32 throughout, one rounding.
 //
+// Norm, weight and rotation are one linear map of a pair: out = rsqrt(..) (y c + partner s), with
+// c and s (cos, sin times the weights) made once for all heads of a token that an item holds.
+//
 // Bound by memory: each value is read once and written once. A group of 8, 16 or 32 lanes
-// takes items (one token, some of its heads), one head row at a time, 8 channels a lane, so
-// that both halves of a pair sit in one lane and only the norm's sum crosses lanes; cos and
-// sin are computed once an item and reused for its heads. The angle is kept as a 64-bit
-// fraction of a turn: frac(freq / 2 pi) * 2^64 times the position, modulo 2^64, drops
-// whole turns exactly at any position; its top 32 bits then go to sincospi. The fraction is
-// the only fp64 arithmetic (slow on this chip: done once an item it took twice the time of
-// the memory traffic), so in large calls a group takes several items and does it once.
-// Measured: 49,157 tokens of 40 + 10 heads of 128 in 204 us, 6.2 TB/s; 4,096 tokens of 32 + 8
-// in 26 us, 3.2 TB/s (a single round of groups: latency).
+// takes an item (one token, some of its heads), eight head rows in flight, 8 channels a lane, so
+// that both halves of a pair sit in one lane and only the norm's sums cross lanes, eight rows'
+// together. The angle is kept as a 64-bit fraction of a turn: frac(freq / 2 pi) * 2^64 times the
+// position, modulo 2^64, drops whole turns exactly at any position; its top 32 bits then go to
+// sincospi. No fp64 arithmetic is used: this chip has little, and the few operations that a lane
+// needed of it once an item took twice the time of the memory traffic.
+//
+// Measured: 49,157 tokens of 40 + 10 heads of 128 in 201 us, 6.3 TB/s (with weights 218 us); 4,096
+// tokens of 32 + 8 in 21 us, 4.0 TB/s (a single round of groups: latency).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -22,7 +25,9 @@
 namespace kvarn {
 namespace {
 
-constexpr int kQkThreads = 128;
+// 96 registers a thread, eight rows in flight: 4,096 tokens 20.8 us; 80 and four rows 22.6; with 64, which
+// do not hold four rows and the map, 34.
+constexpr int kQkThreads = 128, kQkCtas = 5, kAhead = 8;
 
 template <bool BF16>
 __device__ __forceinline__ float2 unpack2(uint32_t w) {
@@ -39,11 +44,21 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// frac(freq / 2 pi) * 2^64, from integers: with freq = M 2^(E - 1086), M of 64 bits, and C = 2^64 * 2 / pi
+// rounded, the high half of M C is turns * 2^(1024 - E), to 2^-63 of it (a double product: 2^-53).
+__device__ __forceinline__ uint64_t turns(double freq) {
+    const int64_t bits = __double_as_longlong(freq);
+    const int e = (int)(bits >> 52 & 0x7ff);
+    const uint64_t t = __umul64hi(((uint64_t)bits << 11) | 1ull << 63, 0xa2f9836e4e44152aull);
+    const int s = e - 1024;
+    const uint64_t f = s >= 0 ? (s < 64 ? t << s : 0) : (s > -64 ? t >> -s : 0);
+    return bits < 0 ? 0 - f : f;
+}
+
 // Lane l of a group owns channels: interleaved, 8 l .. 8 l + 7; otherwise, for l < R / 8,
 // 4 l .. 4 l + 3 and R / 2 + 4 l .. + 3, and from R on 8 l .. 8 l + 7.
 template <bool IN_BF16, bool OUT_BF16, int LANES>
-__global__ void __launch_bounds__(kQkThreads, 8) qk_kernel(const __grid_constant__ QkParams p) {
-    constexpr int kAhead = 4;  // rows in flight
+__global__ void __launch_bounds__(kQkThreads, kQkCtas) qk_kernel(const __grid_constant__ QkParams p) {
     const int l = threadIdx.x % LANES;
     const unsigned group = LANES == 32 ? 0xffffffffu : ((1u << LANES) - 1u) << ((threadIdx.x & 31) / LANES * LANES);
     const bool live = 8 * l < p.d;
@@ -51,36 +66,27 @@ __global__ void __launch_bounds__(kQkThreads, 8) qk_kernel(const __grid_constant
     const bool halves = turned && !p.interleaved;
     const int c0 = halves ? 4 * l : 8 * l;                  // first four channels
     const int c1 = halves ? p.rot / 2 + 4 * l : 8 * l + 4;  // last four
-    uint64_t frac[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        frac[i] = 0;
-        if (turned) {
-            double f = p.freqs[4 * l + i] * 0.15915494309189533577;  // turns a position
-            f -= floor(f);
-            frac[i] = (uint64_t)(f * 18446744073709551616.0);
-        }
-    }
-    // a CTA's items are consecutive, its groups take them in turn
-    constexpr int kGroups = kQkThreads / LANES;
-    const int items = (int)(p.n_tokens * p.items_per_token), first = blockIdx.x * kGroups * p.items_per_group;
-    const int end = min(items, first + kGroups * p.items_per_group);
-    for (int item = first + threadIdx.x / LANES; item < end; item += kGroups) {  // whole groups
-        const int64_t tok = item / p.items_per_token;
-        const int h0 = item % p.items_per_token * p.heads_per_item, h1 = min(h0 + p.heads_per_item, p.hq + p.hkv);
-        const uint16_t* qr = p.q + tok * p.q_stride;
-        const uint16_t* kr = p.k + tok * p.k_stride;
-        uint16_t* qo = p.q_out + tok * p.q_out_stride;
-        uint16_t* ko = p.k_out + tok * p.k_out_stride;
-        float cs[4], sn[4];
-        for (int hb = h0; hb < h1; hb += kAhead) {
+    const int item = blockIdx.x * (kQkThreads / LANES) + threadIdx.x / LANES;
+    const int64_t tok = item / p.items_per_token;
+    if (tok >= p.n_tokens) return;  // whole groups
+    const int h0 = item % p.items_per_token * p.heads_per_item, h1 = min(h0 + p.heads_per_item, p.hq + p.hkv);
+#pragma unroll 1
+    for (int side = 0; side < 2; ++side) {  // q, k
+        const int first = side ? max(h0 - p.hq, 0) : h0;
+        const int rows = (side ? h1 - p.hq : min(h1, p.hq)) - first;
+        if (rows <= 0) continue;
+        const uint16_t* in = (side ? p.k + tok * p.k_stride : p.q + tok * p.q_stride) + (int64_t)first * p.d;
+        uint16_t* out = (side ? p.k_out + tok * p.k_out_stride : p.q_out + tok * p.q_out_stride) + (int64_t)first * p.d;
+        const float* wt = side ? p.k_weight : p.q_weight;
+        float2 c[4], s[4];  // out = y c + partner s
+#pragma unroll 1
+        for (int hb = 0; hb < rows; hb += kAhead) {
             uint2 a[kAhead], b[kAhead];
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
-                const int h = hb + u;
                 a[u] = b[u] = make_uint2(0, 0);
-                if (h < h1 && live) {
-                    const uint16_t* x = h < p.hq ? qr + (int64_t)h * p.d : kr + (int64_t)(h - p.hq) * p.d;
+                if (hb + u < rows && live) {
+                    const uint16_t* x = in + u * p.d;
                     if (halves) {
                         a[u] = *reinterpret_cast<const uint2*>(x + c0);
                         b[u] = *reinterpret_cast<const uint2*>(x + c1);
@@ -91,77 +97,87 @@ __global__ void __launch_bounds__(kQkThreads, 8) qk_kernel(const __grid_constant
                     }
                 }
             }
-            if (hb == h0 && turned) {  // over the loads' latency
-                const int64_t pos = p.positions[tok];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int32_t top = (int32_t)((frac[i] * (uint64_t)pos) >> 32);
-                    sincospif((float)top * 4.656612873077393e-10f, &sn[i], &cs[i]);  // top 2^-32 turns, 2 to a pi
+            if (hb == 0) {  // over the loads' latency
+                float4 w0 = make_float4(1.f, 1.f, 1.f, 1.f), w1 = w0;
+                if (wt && live) {
+                    w0 = __ldg(reinterpret_cast<const float4*>(wt + c0));
+                    w1 = __ldg(reinterpret_cast<const float4*>(wt + c1));
                 }
+                float cs[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {};
+                if (turned) {
+                    const int64_t pos = p.positions[tok];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int32_t top = (int32_t)((turns(p.freqs[4 * l + i]) * (uint64_t)pos) >> 32);
+                        sincospif((float)top * 4.656612873077393e-10f, &sn[i], &cs[i]);  // top 2^-32 turns, 2 to a pi
+                    }
+                }
+                if (p.interleaved) {
+                    c[0] = make_float2(w0.x * cs[0], w0.y * cs[0]), s[0] = make_float2(-w0.y * sn[0], w0.x * sn[0]);
+                    c[1] = make_float2(w0.z * cs[1], w0.w * cs[1]), s[1] = make_float2(-w0.w * sn[1], w0.z * sn[1]);
+                    c[2] = make_float2(w1.x * cs[2], w1.y * cs[2]), s[2] = make_float2(-w1.y * sn[2], w1.x * sn[2]);
+                    c[3] = make_float2(w1.z * cs[3], w1.w * cs[3]), s[3] = make_float2(-w1.w * sn[3], w1.z * sn[3]);
+                } else {
+                    c[0] = make_float2(w0.x * cs[0], w0.y * cs[1]), s[0] = make_float2(-w1.x * sn[0], -w1.y * sn[1]);
+                    c[1] = make_float2(w0.z * cs[2], w0.w * cs[3]), s[1] = make_float2(-w1.z * sn[2], -w1.w * sn[3]);
+                    c[2] = make_float2(w1.x * cs[0], w1.y * cs[1]), s[2] = make_float2(w0.x * sn[0], w0.y * sn[1]);
+                    c[3] = make_float2(w1.z * cs[2], w1.w * cs[3]), s[3] = make_float2(w0.z * sn[2], w0.w * sn[3]);
+                }
+            }
+            float rs[kAhead];
+            if (wt) {  // the rows' sums cross the lanes together
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    float2 f = unpack2<IN_BF16>(a[u].x), g = __fmul2_rn(f, f);
+                    f = unpack2<IN_BF16>(a[u].y), g = __ffma2_rn(f, f, g);
+                    f = unpack2<IN_BF16>(b[u].x), g = __ffma2_rn(f, f, g);
+                    f = unpack2<IN_BF16>(b[u].y), g = __ffma2_rn(f, f, g);
+                    rs[u] = g.x + g.y;
+                }
+#pragma unroll
+                for (int m = LANES / 2; m > 0; m >>= 1)
+#pragma unroll
+                    for (int u = 0; u < kAhead; ++u) rs[u] += __shfl_xor_sync(group, rs[u], m);
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) rs[u] = rsqrtf(rs[u] * p.inv_d + p.eps);
             }
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
-                const int h = hb + u;
-                if (h >= h1) break;  // the same for the whole group
-                float y[8];
-                float2 f;
-                f = unpack2<IN_BF16>(a[u].x), y[0] = f.x, y[1] = f.y;
-                f = unpack2<IN_BF16>(a[u].y), y[2] = f.x, y[3] = f.y;
-                f = unpack2<IN_BF16>(b[u].x), y[4] = f.x, y[5] = f.y;
-                f = unpack2<IN_BF16>(b[u].y), y[6] = f.x, y[7] = f.y;
-                const bool is_q = h < p.hq;
-                const float* wt = is_q ? p.q_weight : p.k_weight;
-                if (wt) {
-                    float ss = 0.f;
+                if (hb + u >= rows || !live) break;
+                const float2 y[4] = {unpack2<IN_BF16>(a[u].x), unpack2<IN_BF16>(a[u].y), unpack2<IN_BF16>(b[u].x),
+                                     unpack2<IN_BF16>(b[u].y)};
+                float2 o[4];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) ss = fmaf(y[i], y[i], ss);
-#pragma unroll
-                    for (int m = LANES / 2; m > 0; m >>= 1) ss += __shfl_xor_sync(group, ss, m);
-                    const float rs = rsqrtf(ss * p.inv_d + p.eps);
-                    if (live) {  // 1 KB at most: from the first cache
-                        const float4 w0 = __ldg(reinterpret_cast<const float4*>(wt + c0));
-                        const float4 w1 = __ldg(reinterpret_cast<const float4*>(wt + c1));
-                        y[0] *= rs * w0.x, y[1] *= rs * w0.y, y[2] *= rs * w0.z, y[3] *= rs * w0.w;
-                        y[4] *= rs * w1.x, y[5] *= rs * w1.y, y[6] *= rs * w1.z, y[7] *= rs * w1.w;
-                    }
-                }
+                for (int i = 0; i < 4; ++i) o[i] = __fmul2_rn(y[i], c[i]);
                 if (turned) {
-                    if (p.interleaved) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float u0 = y[2 * i], u1 = y[2 * i + 1];
-                            y[2 * i] = u0 * cs[i] - u1 * sn[i];
-                            y[2 * i + 1] = u1 * cs[i] + u0 * sn[i];
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float u0 = y[i], u1 = y[4 + i];
-                            y[i] = u0 * cs[i] - u1 * sn[i];
-                            y[4 + i] = u1 * cs[i] + u0 * sn[i];
-                        }
-                    }
+                    for (int i = 0; i < 4; ++i)
+                        o[i] = __ffma2_rn(p.interleaved ? make_float2(y[i].y, y[i].x) : y[i ^ 2], s[i], o[i]);
                 }
-                if (live) {
-                    uint16_t* o = is_q ? qo + (int64_t)h * p.d : ko + (int64_t)(h - p.hq) * p.d;
-                    const uint2 lo = make_uint2(pack2<OUT_BF16>(y[0], y[1]), pack2<OUT_BF16>(y[2], y[3]));
-                    const uint2 hi = make_uint2(pack2<OUT_BF16>(y[4], y[5]), pack2<OUT_BF16>(y[6], y[7]));
-                    if (halves) {
-                        *reinterpret_cast<uint2*>(o + c0) = lo;
-                        *reinterpret_cast<uint2*>(o + c1) = hi;
-                    } else {
-                        *reinterpret_cast<uint4*>(o + c0) = make_uint4(lo.x, lo.y, hi.x, hi.y);
-                    }
+                if (wt) {
+                    const float2 r = make_float2(rs[u], rs[u]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[i] = __fmul2_rn(o[i], r);
+                }
+                const uint2 lo = make_uint2(pack2<OUT_BF16>(o[0].x, o[0].y), pack2<OUT_BF16>(o[1].x, o[1].y));
+                const uint2 hi = make_uint2(pack2<OUT_BF16>(o[2].x, o[2].y), pack2<OUT_BF16>(o[3].x, o[3].y));
+                uint16_t* z = out + u * p.d;
+                if (halves) {
+                    *reinterpret_cast<uint2*>(z + c0) = lo;
+                    *reinterpret_cast<uint2*>(z + c1) = hi;
+                } else {
+                    *reinterpret_cast<uint4*>(z + c0) = make_uint4(lo.x, lo.y, hi.x, hi.y);
                 }
             }
+            in += kAhead * p.d;
+            out += kAhead * p.d;
         }
     }
 }
 
 template <bool I, bool O>
 int launch_qk(const QkParams& p, cudaStream_t s) {
-    const int lanes = p.d <= 64 ? 8 : p.d <= 128 ? 16 : 32;
-    const int64_t per_cta = (int64_t)(kQkThreads / lanes) * p.items_per_group;
+    const int lanes = p.d <= 64 ? 8 : p.d <= 128 ? 16 : 32, per_cta = kQkThreads / lanes;
     const unsigned grid = (unsigned)((p.n_tokens * p.items_per_token + per_cta - 1) / per_cta);
     if (lanes == 8) qk_kernel<I, O, 8><<<grid, kQkThreads, 0, s>>>(p);
     else if (lanes == 16) qk_kernel<I, O, 16><<<grid, kQkThreads, 0, s>>>(p);

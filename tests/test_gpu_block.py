@@ -581,6 +581,40 @@ def test_norm_rope(dim, rot, interleaved, types):
         assert alone[1] is None
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_norm_rope_frequencies(interleaved):
+    """Frequencies of any sign and size: none, tiny, whole turns and many turns a position."""
+    from quantized_kv_cache_seal_gb300.qk import qk_norm_rope
+    freqs = torch.tensor([0.0, -0.0, 1e-300, 2.0 ** -1040, 2.0 ** -40, -2.0 ** -13, 0.5, -1.0, 2.0, 3.141592653589793,
+                          6.283185307179586, -6.283185307179587, 12.5, 1000.123, -123456.789, 1048577.0], dtype=torch.float64,
+                         device="cuda")
+    x = tokens(40, 3, 32, torch.float16, 5, 0.3)
+    pos = torch.arange(-20, 20, dtype=torch.int32, device="cuda") * 51
+    got, _ = qk_norm_rope(x, None, pos, freqs, interleaved=interleaved)
+    # the angle, up to 2^30 in 64 bits, is good to 2^-23 there
+    want, tol = block_ref.norm_rope(x, None, pos, freqs, interleaved, 0)
+    tol = tol + want.abs().amax(-1, keepdim=True) * 2 * 2.0 ** -23 + want.abs() * 2.0 ** -11 + 2.0 ** -24
+    assert float(((got.cpu().double() - want).abs() / tol).max()) <= 1
+
+
+@pytest.mark.parametrize("tokens_, hq, hkv, dim", [(1000, 40, 8, 128), (2100, 20, 3, 64), (1530, 32, 9, 128), (900, 70, 20, 128),
+                                                  (800, 17, 0, 256), (3, 0, 5, 256)])
+def test_norm_rope_by_items(tokens_, hq, hkv, dim):
+    """The ways in which heads are cut into items, with and without a side."""
+    from quantized_kv_cache_seal_gb300.qk import qk_norm_rope
+    x = tokens(tokens_, hq + hkv, dim, torch.bfloat16, 6, 0.3)
+    pos = torch.arange(tokens_, dtype=torch.int32, device="cuda")
+    freqs = 1e4 ** (-torch.arange(0, dim, 2, dtype=torch.float64, device="cuda") / dim)
+    w = torch.rand(dim, generator=torch.Generator().manual_seed(7)).cuda() + 0.5
+    q, k = (x[:, :hq], x[:, hq:]) if hkv else (x, None)
+    got = qk_norm_rope(q, k, pos, freqs, w if hq else None, w if hkv else None)
+    for part, y in zip((q, k), got):
+        if part is not None and part.shape[1]:
+            want, tol = block_ref.norm_rope(part, w, pos, freqs, False, 1e-6)
+            tol = tol + want.abs() * 2.0 ** -8 + 2.0 ** -126
+            assert float(((y.cpu().double() - want).abs() / tol).max()) <= 1
+
+
 def test_norm_rope_in_place_and_captured():
     from quantized_kv_cache_seal_gb300.qk import qk_norm_rope
     qkv = tokens(300, 12, 128, torch.float16, 5, 0.3)
