@@ -91,11 +91,12 @@ class BlockCache:
         _same_length(seq_ids, counts)
         if starts is not None:
             _same_length(seq_ids, starts)
-        if any(n < 0 for n in counts):
+        if len(counts) and min(counts) < 0:
             raise ValueError("counts must not be negative")
         shape = (sum(counts), self.kv_heads, self.dim)
         with K.on_device(self.device, stream) as stream:
-            k, v = (torch.empty(shape, dtype=dtype, device=self.device) for _ in range(2))
+            k = torch.empty(shape, dtype=dtype, device=self.device)
+            v = torch.empty_like(k)
             K.kvarn_block_read(self.handle, layer, seq_ids, starts, counts, k, v, dtype is torch.float32, stream)
         return k, v
 
