@@ -57,15 +57,19 @@ __device__ __forceinline__ uint64_t turns(double freq) {
 
 // Lane l of a group owns channels: interleaved, 8 l .. 8 l + 7; otherwise, for l < R / 8,
 // 4 l .. 4 l + 3 and R / 2 + 4 l .. + 3, and from R on 8 l .. 8 l + 7.
-template <bool IN_BF16, bool OUT_BF16, int LANES>
+enum { kAny, kFullHalves, kFullPairs };  // kAny: any head_dim, rot_dim and order; the others: both 8 * LANES
+
+template <bool IN_BF16, int LANES, int MODE>
 __global__ void __launch_bounds__(kQkThreads, kQkCtas) qk_kernel(const __grid_constant__ QkParams p) {
     const int l = threadIdx.x % LANES;
     const unsigned group = LANES == 32 ? 0xffffffffu : ((1u << LANES) - 1u) << ((threadIdx.x & 31) / LANES * LANES);
-    const bool live = 8 * l < p.d;
-    const bool turned = 8 * l < p.rot;
-    const bool halves = turned && !p.interleaved;
-    const int c0 = halves ? 4 * l : 8 * l;                  // first four channels
-    const int c1 = halves ? p.rot / 2 + 4 * l : 8 * l + 4;  // last four
+    const int d = MODE != kAny ? 8 * LANES : p.d;
+    const bool live = MODE != kAny || 8 * l < d;
+    const bool turned = MODE != kAny || 8 * l < p.rot;
+    const bool pairs = MODE == kAny ? p.interleaved : MODE == kFullPairs;
+    const bool halves = turned && !pairs;
+    const int c0 = halves ? 4 * l : 8 * l;                                                           // first four channels
+    const int c1 = halves ? (MODE != kAny ? 4 * LANES : p.rot / 2) + 4 * l : 8 * l + 4;  // last four
     const int item = blockIdx.x * (kQkThreads / LANES) + threadIdx.x / LANES;
     const int64_t tok = item / p.items_per_token;
     if (tok >= p.n_tokens) return;  // whole groups
@@ -75,8 +79,8 @@ __global__ void __launch_bounds__(kQkThreads, kQkCtas) qk_kernel(const __grid_co
         const int first = side ? max(h0 - p.hq, 0) : h0;
         const int rows = (side ? h1 - p.hq : min(h1, p.hq)) - first;
         if (rows <= 0) continue;
-        const uint16_t* in = (side ? p.k + tok * p.k_stride : p.q + tok * p.q_stride) + (int64_t)first * p.d;
-        uint16_t* out = (side ? p.k_out + tok * p.k_out_stride : p.q_out + tok * p.q_out_stride) + (int64_t)first * p.d;
+        const uint16_t* in = (side ? p.k + tok * p.k_stride : p.q + tok * p.q_stride) + (int64_t)first * d;
+        uint16_t* out = (side ? p.k_out + tok * p.k_out_stride : p.q_out + tok * p.q_out_stride) + (int64_t)first * d;
         const float* wt = side ? p.k_weight : p.q_weight;
         float2 c[4], s[4];  // out = y c + partner s
 #pragma unroll 1
@@ -86,7 +90,7 @@ __global__ void __launch_bounds__(kQkThreads, kQkCtas) qk_kernel(const __grid_co
             for (int u = 0; u < kAhead; ++u) {
                 a[u] = b[u] = make_uint2(0, 0);
                 if (hb + u < rows && live) {
-                    const uint16_t* x = in + u * p.d;
+                    const uint16_t* x = in + u * d;
                     if (halves) {
                         a[u] = *reinterpret_cast<const uint2*>(x + c0);
                         b[u] = *reinterpret_cast<const uint2*>(x + c1);
@@ -112,7 +116,7 @@ __global__ void __launch_bounds__(kQkThreads, kQkCtas) qk_kernel(const __grid_co
                         sincospif((float)top * 4.656612873077393e-10f, &sn[i], &cs[i]);  // top 2^-32 turns, 2 to a pi
                     }
                 }
-                if (p.interleaved) {
+                if (pairs) {
                     c[0] = make_float2(w0.x * cs[0], w0.y * cs[0]), s[0] = make_float2(-w0.y * sn[0], w0.x * sn[0]);
                     c[1] = make_float2(w0.z * cs[1], w0.w * cs[1]), s[1] = make_float2(-w0.w * sn[1], w0.z * sn[1]);
                     c[2] = make_float2(w1.x * cs[2], w1.y * cs[2]), s[2] = make_float2(-w1.y * sn[2], w1.x * sn[2]);
@@ -152,16 +156,22 @@ __global__ void __launch_bounds__(kQkThreads, kQkCtas) qk_kernel(const __grid_co
                 if (turned) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        o[i] = __ffma2_rn(p.interleaved ? make_float2(y[i].y, y[i].x) : y[i ^ 2], s[i], o[i]);
+                        o[i] = __ffma2_rn(pairs ? make_float2(y[i].y, y[i].x) : y[i ^ 2], s[i], o[i]);
                 }
                 if (wt) {
                     const float2 r = make_float2(rs[u], rs[u]);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) o[i] = __fmul2_rn(o[i], r);
                 }
-                const uint2 lo = make_uint2(pack2<OUT_BF16>(o[0].x, o[0].y), pack2<OUT_BF16>(o[1].x, o[1].y));
-                const uint2 hi = make_uint2(pack2<OUT_BF16>(o[2].x, o[2].y), pack2<OUT_BF16>(o[3].x, o[3].y));
-                uint16_t* z = out + u * p.d;
+                uint2 lo, hi;
+                if (p.out_bf16) {
+                    lo = make_uint2(pack2<true>(o[0].x, o[0].y), pack2<true>(o[1].x, o[1].y));
+                    hi = make_uint2(pack2<true>(o[2].x, o[2].y), pack2<true>(o[3].x, o[3].y));
+                } else {
+                    lo = make_uint2(pack2<false>(o[0].x, o[0].y), pack2<false>(o[1].x, o[1].y));
+                    hi = make_uint2(pack2<false>(o[2].x, o[2].y), pack2<false>(o[3].x, o[3].y));
+                }
+                uint16_t* z = out + u * d;
                 if (halves) {
                     *reinterpret_cast<uint2*>(z + c0) = lo;
                     *reinterpret_cast<uint2*>(z + c1) = hi;
@@ -169,28 +179,32 @@ __global__ void __launch_bounds__(kQkThreads, kQkCtas) qk_kernel(const __grid_co
                     *reinterpret_cast<uint4*>(z + c0) = make_uint4(lo.x, lo.y, hi.x, hi.y);
                 }
             }
-            in += kAhead * p.d;
-            out += kAhead * p.d;
+            in += kAhead * d;
+            out += kAhead * d;
         }
     }
 }
 
-template <bool I, bool O>
+template <bool I, int LANES>
 int launch_qk(const QkParams& p, cudaStream_t s) {
-    const int lanes = p.d <= 64 ? 8 : p.d <= 128 ? 16 : 32, per_cta = kQkThreads / lanes;
-    const unsigned grid = (unsigned)((p.n_tokens * p.items_per_token + per_cta - 1) / per_cta);
-    if (lanes == 8) qk_kernel<I, O, 8><<<grid, kQkThreads, 0, s>>>(p);
-    else if (lanes == 16) qk_kernel<I, O, 16><<<grid, kQkThreads, 0, s>>>(p);
-    else qk_kernel<I, O, 32><<<grid, kQkThreads, 0, s>>>(p);
+    constexpr int kPerCta = kQkThreads / LANES;
+    const unsigned grid = (unsigned)((p.n_tokens * p.items_per_token + kPerCta - 1) / kPerCta);
+    const bool full = p.d == 8 * LANES && p.rot == p.d;
+    if (!full) qk_kernel<I, LANES, kAny><<<grid, kQkThreads, 0, s>>>(p);
+    else if (p.interleaved) qk_kernel<I, LANES, kFullPairs><<<grid, kQkThreads, 0, s>>>(p);
+    else qk_kernel<I, LANES, kFullHalves><<<grid, kQkThreads, 0, s>>>(p);
     return (int)cudaGetLastError();
+}
+template <bool I>
+int launch_lanes(const QkParams& p, cudaStream_t s) {
+    return p.d <= 64 ? launch_qk<I, 8>(p, s) : p.d <= 128 ? launch_qk<I, 16>(p, s) : launch_qk<I, 32>(p, s);
 }
 
 }  // namespace
 
 int launch_qk_norm_rope(const QkParams& p, void* stream) {
     cudaStream_t s = (cudaStream_t)stream;
-    if (p.in_bf16) return p.out_bf16 ? launch_qk<true, true>(p, s) : launch_qk<true, false>(p, s);
-    return p.out_bf16 ? launch_qk<false, true>(p, s) : launch_qk<false, false>(p, s);
+    return p.in_bf16 ? launch_lanes<true>(p, s) : launch_lanes<false>(p, s);
 }
 
 }  // namespace kvarn
