@@ -582,14 +582,12 @@ kvarn_status kvarn_qk_norm_rope(const kvarn_qk_config* cfg, int64_t n_tokens, co
     p.out_bf16 = cfg->out_type == KVARN_TYPE_BF16;
     p.eps = cfg->eps;
     // Heads an item, a group's work in turn. Where the rows are not many times the resident groups (97,280
-    // lanes): four, to have groups enough. Else all of a token's, so that its angles are made once a side; 32
-    // where tokens alone do not fill the machine or rows of very many heads would lie a power of two apart.
-    // (Measured, bf16 with weights, us: 1,000 tokens of 40 heads 10.3 by four, 12.3 by all; 4,096 29.7 by
-    // four, 20.8 by all; 4,000 of 72 43.0 by 32, 35.1 by all; 1,200 of 72 16.4 by 32, 19.8 by all; 4,000 of
-    // 128 50.3 by 32, 57.6 by all.)
+    // lanes): four, to have groups enough, or 16 of few tokens. Else all of a token's, so that its angles are
+    // made once a side; 32 where a token's rows of very many heads would lie far apart.
+    // (Measured, bf16 with weights, us: 1,000 tokens of 40 heads 8.2 by four, 10.3 by all; 4,000 of 72 43.3 by
+    // four, 30.5 by all; 1,200 of 72 14.4 by four, 12.3 by 16, 16.4 by all; 2,000 of 128 26.7 by 32, 36.5 by all.)
     const int64_t heads = hq + hk, resident = 97280 / (d <= 64 ? 8 : d <= 128 ? 16 : 32);
-    if (n_tokens * heads <= 8 * resident) p.heads_per_item = 4;
-    else p.heads_per_item = n_tokens >= resident / 4 && heads <= 80 ? (int32_t)heads : 32;
+    p.heads_per_item = n_tokens * heads <= 8 * resident ? 4 : n_tokens < resident / 4 ? 16 : heads <= 80 ? (int32_t)heads : 32;
     p.items_per_token = (int32_t)((heads + p.heads_per_item - 1) / p.heads_per_item);
     p.inv_d = 1.f / (float)d;
     const int rc = launch_qk_norm_rope(p, stream);

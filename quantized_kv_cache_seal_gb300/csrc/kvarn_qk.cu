@@ -14,8 +14,8 @@
 // sincospi. No fp64 arithmetic is used: this chip has little, and the few operations that a lane
 // needed of it once an item took twice the time of the memory traffic.
 //
-// Measured: 49,157 tokens of 40 + 10 heads of 128 in 201 us, 6.3 TB/s (with weights 218 us); 4,096
-// tokens of 32 + 8 in 21 us, 4.0 TB/s (a single round of groups: latency).
+// Measured: 49,157 tokens of 40 + 10 heads of 128 in 188 us, 6.7 TB/s (with weights 192 us); 4,096
+// tokens of 32 + 8 with weights in 16.5 us, 5.1 TB/s.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -25,8 +25,8 @@
 namespace kvarn {
 namespace {
 
-// 96 registers a thread, eight rows in flight: 4,096 tokens 20.8 us; 80 and four rows 22.6; with 64, which
-// do not hold four rows and the map, 34.
+// 96 registers a thread, eight rows in flight (with runtime sizes, 4,096 tokens of 40 heads: 20.8 us; 80 and
+// four rows 22.6; with 64, which do not hold four rows and the map, 34; kAny needs 122).
 constexpr int kQkThreads = 128, kQkCtas = 5, kAhead = 8;
 
 template <bool BF16>
@@ -57,19 +57,23 @@ __device__ __forceinline__ uint64_t turns(double freq) {
 
 // Lane l of a group owns channels: interleaved, 8 l .. 8 l + 7; otherwise, for l < R / 8,
 // 4 l .. 4 l + 3 and R / 2 + 4 l .. + 3, and from R on 8 l .. 8 l + 7.
-enum { kAny, kFullHalves, kFullPairs };  // kAny: any head_dim, rot_dim and order; the others: both 8 * LANES
+// kAny: any head_dim and order; the others: head_dim 8 * LANES, and in the last two rot_dim too. (20,000 tokens
+// of 40 heads, rotated whole: 67.5 us as kFullHalves, 68.1 as kHalves; with rot_dim 64 of 128 68.7 as kHalves,
+// 89.5 as kAny.)
+enum { kAny, kHalves, kPairs, kFullHalves, kFullPairs };
 
 template <bool IN_BF16, int LANES, int MODE>
-__global__ void __launch_bounds__(kQkThreads, kQkCtas) qk_kernel(const __grid_constant__ QkParams p) {
+__global__ void __launch_bounds__(kQkThreads, MODE == kAny ? 4 : kQkCtas) qk_kernel(const __grid_constant__ QkParams p) {
     const int l = threadIdx.x % LANES;
     const unsigned group = LANES == 32 ? 0xffffffffu : ((1u << LANES) - 1u) << ((threadIdx.x & 31) / LANES * LANES);
     const int d = MODE != kAny ? 8 * LANES : p.d;
     const bool live = MODE != kAny || 8 * l < d;
-    const bool turned = MODE != kAny || 8 * l < p.rot;
-    const bool pairs = MODE == kAny ? p.interleaved : MODE == kFullPairs;
+    constexpr bool kFull = MODE >= kFullHalves, kTwo = MODE == kHalves || MODE == kFullHalves;  // kTwo: two pieces a row
+    const bool turned = kFull || 8 * l < p.rot;
+    const bool pairs = MODE == kAny ? p.interleaved : !kTwo;
     const bool halves = turned && !pairs;
-    const int c0 = halves ? 4 * l : 8 * l;                                                           // first four channels
-    const int c1 = halves ? (MODE != kAny ? 4 * LANES : p.rot / 2) + 4 * l : 8 * l + 4;  // last four
+    const int c0 = halves ? 4 * l : 8 * l;                  // first four channels
+    const int c1 = halves ? (kFull ? 4 * LANES : p.rot / 2) + 4 * l : 8 * l + 4;  // last four
     const int item = blockIdx.x * (kQkThreads / LANES) + threadIdx.x / LANES;
     const int64_t tok = item / p.items_per_token;
     if (tok >= p.n_tokens) return;  // whole groups
@@ -91,7 +95,7 @@ __global__ void __launch_bounds__(kQkThreads, kQkCtas) qk_kernel(const __grid_co
                 a[u] = b[u] = make_uint2(0, 0);
                 if (hb + u < rows && live) {
                     const uint16_t* x = in + u * d;
-                    if (halves) {
+                    if (kTwo || halves) {
                         a[u] = *reinterpret_cast<const uint2*>(x + c0);
                         b[u] = *reinterpret_cast<const uint2*>(x + c1);
                     } else {
@@ -172,7 +176,7 @@ __global__ void __launch_bounds__(kQkThreads, kQkCtas) qk_kernel(const __grid_co
                     hi = make_uint2(pack2<false>(o[2].x, o[2].y), pack2<false>(o[3].x, o[3].y));
                 }
                 uint16_t* z = out + u * d;
-                if (halves) {
+                if (kTwo || halves) {
                     *reinterpret_cast<uint2*>(z + c0) = lo;
                     *reinterpret_cast<uint2*>(z + c1) = hi;
                 } else {
@@ -189,10 +193,11 @@ template <bool I, int LANES>
 int launch_qk(const QkParams& p, cudaStream_t s) {
     constexpr int kPerCta = kQkThreads / LANES;
     const unsigned grid = (unsigned)((p.n_tokens * p.items_per_token + kPerCta - 1) / kPerCta);
-    const bool full = p.d == 8 * LANES && p.rot == p.d;
-    if (!full) qk_kernel<I, LANES, kAny><<<grid, kQkThreads, 0, s>>>(p);
-    else if (p.interleaved) qk_kernel<I, LANES, kFullPairs><<<grid, kQkThreads, 0, s>>>(p);
-    else qk_kernel<I, LANES, kFullHalves><<<grid, kQkThreads, 0, s>>>(p);
+    if (p.d != 8 * LANES) qk_kernel<I, LANES, kAny><<<grid, kQkThreads, 0, s>>>(p);
+    else if (p.interleaved && p.rot == p.d) qk_kernel<I, LANES, kFullPairs><<<grid, kQkThreads, 0, s>>>(p);
+    else if (p.interleaved) qk_kernel<I, LANES, kPairs><<<grid, kQkThreads, 0, s>>>(p);
+    else if (p.rot == p.d) qk_kernel<I, LANES, kFullHalves><<<grid, kQkThreads, 0, s>>>(p);
+    else qk_kernel<I, LANES, kHalves><<<grid, kQkThreads, 0, s>>>(p);
     return (int)cudaGetLastError();
 }
 template <bool I>

@@ -598,6 +598,7 @@ def test_norm_rope_frequencies(interleaved):
 
 
 @pytest.mark.parametrize("tokens_, hq, hkv, dim", [(1000, 40, 8, 128), (2100, 20, 3, 64), (1530, 32, 9, 128), (900, 70, 20, 128),
+                                                  (1600, 64, 30, 128),
                                                   (800, 17, 0, 256), (3, 0, 5, 256)])
 def test_norm_rope_by_items(tokens_, hq, hkv, dim):
     """The ways in which heads are cut into items, with and without a side."""
