@@ -66,8 +66,8 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
 // registers. The group of a sequence's first completed block also moves the tokens behind the
 // last block into the exact tail, after it has read the old tail: both use the same rows.
 // Bound by memory; the input is read once (16-byte loads, whole rows) and codes leave in
-// 32-byte sectors or larger. 64 sequences, ragged, written and read back (read_kernel): 1,620 us,
-// 5.8 TB/s together; smaller calls are bound by the two launches.
+// 32-byte sectors or larger. 64 sequences, ragged, written and read back (read_kernel), e4m3: 1,575
+// us, 6.0 TB/s together; smaller calls are bound by the two launches.
 template <int D, bool BF16, class P>
 __global__ void __launch_bounds__(kWriteThreads) append_kernel(const __grid_constant__ P p) {
     __shared__ uint32_t red[kWriteThreads / 32];
