@@ -202,7 +202,7 @@ __device__ __forceinline__ void exact_unit(State<D>& st, const uint16_t* k, cons
                         uint4 r = make_uint4(0, 0, 0, 0);
                         if (tok < nv) r = *reinterpret_cast<const uint4*>(k + tok * D + 64 * c + 16 * t + 8 * z);
                         x[a][c][b][z] = r;
-                        if (BF16) top = max_of(top, r);
+                        if (BF16) top = max_of(top, finite_only<BF16>(r));  // an infinity must not scale the others away
                     }
             }
         float f = 1.f;

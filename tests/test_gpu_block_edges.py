@@ -1,0 +1,36 @@
+"""GPU tests of the block cache at the edges of its number range and of its calls (include/kvarn.h), against the
+definition in 64 bits."""
+import pytest
+import torch
+
+from tests import block_ref
+from tests.test_gpu_block import TYPES, check, fill, make, tokens
+
+pytestmark = pytest.mark.gpu
+
+
+def held(x, block, code="e4m3"):
+    return block_ref.hold(x, block, code)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("at", [70, 100])
+def test_infinite_key_of_an_exact_token(dtype, dim, at):
+    """A key with an infinity whose logit is -inf takes its token out and leaves the other tokens' logits alone; where
+    the logit is +inf the output is NaN. Both attention kernels."""
+    dt, n = TYPES[dtype], 110  # exact from 64 on
+    k, v, q = (tokens(m, h, dim, dt, s, 0.3) for m, h, s in ((n, 1, 201), (n, 1, 202), (2, 4, 203)))
+    k[at, 0, 5] = float("inf")
+    q[:, :, 5] = torch.tensor([-1.0, -0.25, 1.0, 2.0], dtype=dt).cuda()  # by head
+    c = make(num_q_heads=4, num_kv_heads=1, head_dim=dim, block_tokens=64, dtype=dt, max_seqs=1)
+    c.append(0, [0], [n], k, v)
+    rest = [i for i in range(n) if i != at]
+    kk, vv = (held(x, 64)[rest] for x in (k, v))
+    want, tol = block_ref.attend(q[:, :2].contiguous().cpu(), kk, vv, dim ** -0.5, [n - 3, n - 2])
+    both = c.prefill_attention(0, [0], [2], q)
+    check(both[:, :2], want, tol, "prefill")
+    assert bool(both[:, 2:].isnan().all())
+    one = c.decode_attention(0, [0], q[1:])
+    check(one[:, :2], want[1:], tol[1:], "decode")
+    assert bool(one[:, 2:].isnan().all())
