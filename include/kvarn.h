@@ -329,6 +329,10 @@ kvarn_status kvarn_device_accessible(const void* ptr, int32_t* accessible);
  *     sequences must not have been released since, nor the block that was partial then have
  *     filled (its exact tokens make room for the next block's). A replay is a call: those of
  *     one cache stay ordered on the GPU, since they share its workspace.
+ *   - Infinities and NaN: a query sees those of the tokens at positions up to its own. In V of an
+ *     exact token they make their channel of the output non-finite (an infinity can come out as
+ *     NaN) and no other; in K they act through the token's logit. A query whose every logit is
+ *     -inf gives zeros.
  *   - q and out do not overlap.
  *   - Attention tells a head's V scales apart up to a ratio of 2^100 (fp16 never leaves it):
  *     tokens of bf16 blocks smaller than that against the largest can count for nothing.

@@ -310,8 +310,8 @@ __device__ __forceinline__ void issue_role(uint32_t sbase, uint64_t* bars, int32
 }
 
 // Exact tokens of a part (none: zeros) as its K or V tile rows. A later token's infinity or NaN
-// must not reach a query that does not see it through 0 x NaN: non-finite V enters as 0, and its
-// token is named in `bad` for the softmax to make visible weights NaN. K needs no such care (logits
+// must not reach a query that does not see it through 0 x NaN: non-finite V enters as 0, and `bad`
+// says that there is some, for add_non_finite at the segment's end. K needs no such care (logits
 // of unseen tokens are replaced), but neither may set the part's power of two.
 // h: K scale, or log2 and reciprocal of the V scale. x: registers to use.
 template <int D, bool BF16, bool IS_V>
@@ -357,8 +357,7 @@ __device__ __forceinline__ void expand_exact(const BlockView& c, const BlockPref
 #pragma unroll
             for (int i = 0; i < kTurn; ++i) {
                 const uint4 r = x[i];
-                bad |= (bad_pair<BF16>(r.x) | bad_pair<BF16>(r.y) << 2 | bad_pair<BF16>(r.z) << 4 | bad_pair<BF16>(r.w) << 6)
-                       << (8 * t);
+                bad |= bad_pair<BF16>(r.x) | bad_pair<BF16>(r.y) | bad_pair<BF16>(r.z) | bad_pair<BF16>(r.w);
                 *reinterpret_cast<uint4*>(atom + swz(8 * (i0 + i) + g, 4 * (wp & 1) + t)) =
                     scaled_f16<BF16>(finite_only<BF16>(r), f);
             }
@@ -511,6 +510,28 @@ __device__ __forceinline__ void expand_role(const BlockPrefillParams& p, uint8_t
     }
 }
 
+// Non-finite V of exact tokens went into the products as 0. Here a row takes those of the positions
+// [from, to) that it sees, each into its own channel: on top of the finished row `out`, or of the
+// partial one `part` (the other null).
+template <int D, bool BF16>
+__device__ __forceinline__ void add_non_finite(const BlockView& c, const BlockPrefillSeq& e, int kvh, int from, int to,
+                                               uint16_t* out, float* part) {
+    const int sealed = e.n & ~(c.block - 1);
+    const uint16_t* v = tail_ptr(c, c.lay.tail_v, e.seq, kvh);
+#pragma unroll 1
+    for (int ch = 0; ch < D; ++ch) {
+        float sum = 0.f;
+#pragma unroll 1
+        for (int pos = max(from, sealed); pos < to; ++pos) {
+            const uint32_t x = v[tail_v_off(D, pos - sealed, ch)];
+            if (bad_pair<BF16>(x)) sum += unpack2<BF16>(x).x;
+        }
+        if (sum == 0.f) continue;
+        if (out) out[ch] = (uint16_t)pack2<BF16>(unpack2<BF16>(out[ch]).x + sum, 0.f);
+        else part[ch] += sum;
+    }
+}
+
 // ---- softmax: thread et owns row et of tile b ----
 template <int D, bool BF16>
 __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, uint8_t* smem, uint64_t* bars, uint32_t tmem,
@@ -574,6 +595,7 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, uint8_
         fence_proxy_async_smem();
         mbar_arrive(bars + kBarQFull + b);
         float m = kNegInf, l = 0.f;
+        uint32_t bad = 0;  // non-finite V among the segment's exact tokens
 #pragma unroll 1
         for (int j = w.s.j0; j < w.s.j1; ++j, ++jj, ++step) {
             // A tile that sat out a segment may be whole phases ahead of the expansion; once its first
@@ -584,7 +606,6 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, uint8_
             bar_wait(bars + kBarVFull + (jj & 3), (uint32_t)((jj >> 2) & 1), err);
             // logit = S c[ch] (+ log2 of V's scale in the weight); c > 0 or NaN
             float c[4], lv[4], iv[4];
-            uint32_t bad = 0;
 #pragma unroll
             for (int ch = 0; ch < 4; ++ch) {
                 const float4 h = hdr[(jj & 3) * 4 + ch];
@@ -599,7 +620,7 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, uint8_
             const int lim = pos + 1 - j * kStep;  // visible columns
             uint32_t r[4][32];
             float mx = kNegInf;
-            const bool plain = !bad && __all_sync(0xffffffffu, lim >= kStep);
+            const bool plain = __all_sync(0xffffffffu, lim >= kStep);
 #pragma unroll
             for (int ch = 0; ch < 4; ++ch) tm_ld32(ts + 32 * ch, r[ch]);
             tm_wait_ld();
@@ -609,17 +630,7 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, uint8_
                 mx = fmaxf(mx, fmaf(max32(r[2]), c[2], lv[2]));
                 mx = fmaxf(mx, fmaf(max32(r[3]), c[3], lv[3]));
             } else {
-                // non-finite V tokens' weights become NaN where they are seen; then columns behind the
-                // row's position leave, with all of a part that is not seen at all
-                if (bad) {
-#pragma unroll
-                    for (int ch = 0; ch < 4; ++ch) {
-                        const uint32_t y = __float_as_uint(hdr[(jj & 3) * 4 + ch].y);
-#pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            if (y >> k & 1) r[ch][k] = 0x7fc00000u;
-                    }
-                }
+                // columns behind the row's position leave, with all of a part that is not seen at all
 #pragma unroll
                 for (int ch = 0; ch < 4; ++ch) {
                     const int left = lim - 32 * ch;  // visible columns from the part's first on
@@ -710,6 +721,10 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, uint8_
                     if (at >= 0) *reinterpret_cast<uint4*>(p.out + (size_t)at * D + 64 * piece + 8 * (lane & 7)) = x;
                 }
             }
+            if (__builtin_expect(bad, 0)) {
+                __syncwarp();  // the row is there
+                if (valid) add_non_finite<D, BF16>(p.c, e, w.s.kvh, 0, pos + 1, p.out + (size_t)row * D, nullptr);
+            }
         } else {
             float* part = reinterpret_cast<float*>(p.c.base + p.c.lay.partials) +
                           (size_t)(2 * blockIdx.x + (w.s.j0 == 0 ? 1 : 0)) * (256 * (D + 2));
@@ -729,6 +744,9 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, uint8_
                     }
                     __syncwarp();
                 }
+                if (__builtin_expect(bad, 0) && valid)
+                    add_non_finite<D, BF16>(p.c, e, w.s.kvh, w.s.j0 * kStep, min(pos + 1, w.s.j1 * kStep), nullptr,
+                                            part + (size_t)(128 * b + et) * D);
                 part[256 * D + 128 * b + et] = m;
                 part[256 * D + 256 + 128 * b + et] = l;
             }

@@ -34,3 +34,34 @@ def test_infinite_key_of_an_exact_token(dtype, dim, at):
     one = c.decode_attention(0, [0], q[1:])
     check(one[:, :2], want[1:], tol[1:], "decode")
     assert bool(one[:, 2:].isnan().all())
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("dim,r", [(64, 3), (128, 4)])
+@pytest.mark.parametrize("n,m", [(110, 60), (110, 1), (4090, 45), (4090, 1)])
+def test_non_finite_value_of_an_exact_token(dtype, dim, r, n, m):
+    """An infinity or NaN in V of an exact token reaches its own channel, of the queries that see it, and nothing else,
+    in both kernels and where work is cut between thread blocks (long sequences)."""
+    dt = TYPES[dtype]
+    k, v, q = (tokens(t, h, dim, dt, s, 0.3) for t, h, s in ((n, 1, 211), (n, 1, 212), (m, r, 213)))
+    bad = {(n - 40, 3): float("inf"), (n - 30, 9): float("-inf"), (n - 25, 3): float("inf"), (n - 20, 12): float("nan")}
+    first = {}  # channel: first position
+    for (t, ch), x in bad.items():
+        v[t, 0, ch] = x
+        first[ch] = min(t, first.get(ch, n))
+    block = 64
+    assert n - 40 >= n // block * block
+    c = make(num_q_heads=r, num_kv_heads=1, head_dim=dim, block_tokens=block, dtype=dt, max_seqs=1)
+    c.append(0, [0], [n], k, v)
+    out = c.prefill_attention(0, [0], [m], q).cpu()
+    clean = v.clone()
+    for t, ch in bad:
+        clean[t, 0, ch] = 0
+    want, tol = block_ref.attend(q.cpu(), held(k, block), held(clean, block), dim ** -0.5, list(range(n - m, n)))
+    pos = torch.arange(n - m, n)
+    for ch, t in first.items():
+        sees = pos >= t
+        assert bool((~torch.isfinite(out[sees][..., ch])).all()), ch
+        out[..., ch][sees] = 0
+        want[..., ch][sees] = 0
+    check(out, want, tol, (n, m))
