@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kWriteThreads) append_kernel(const __grid_cons
             } else {
                 hd[1] = s;
                 hd[2] = amax == 0.f ? (float)kZeroV : log2f(s);
-                hd[3] = amax == 0.f ? power2(-kZeroV) : inv;
+                hd[3] = (amax == 0.f ? power2(-kZeroV) : inv) * kDenomUnit;
             }
         }
         uint2 q[8];  // codes of token u, channel by channel

@@ -16,7 +16,7 @@ constexpr int kBlockPrefillGrid = 152;  // CTAs of a prefill launch that cuts se
 
 // One code tile: 32 tokens of one KV head, K and V, in the order in which a warp loads the
 // A operands of mma.m16n8k16 (16 bytes a lane, 512 contiguous bytes a load):
-//   [0,16)             f32 K scale, V scale, log2(V scale), 1 / V scale
+//   [0,16)             f32 K scale, V scale, log2(V scale), kDenomUnit / V scale
 //   [16, 16 + 32 D)    K codes: 512-byte chunk (s D/64 + c) 2 + h, lane 4 g + t: token
 //                      8 (g >> 1) + 4 s + 2 h + (g & 1), channels 64 c + 16 t .. + 15
 //   [16 + 32 D, ...)   V codes: 512-byte chunk m, lane 4 g + t: tokens 8 t .. 8 t + 7 of

@@ -6,7 +6,7 @@
 // that drops is 2^-39 of it). V's scale is folded into the weight: w'_n = 2^(x_n + log2 s_V,n
 // - m' + 15), m' the running maximum of x + log2 s_V, so that weights are at most 2^15 in f16
 // whatever V's range, and keep all its bits down to 2^-29 of the largest; the denominator adds
-// w' / s_V in fp32. Rounding w' to f16 is off by at most 2^-11 of each weight, less in sum than the
+// w' / s_V in fp32, in units of 2^12 (kDenomUnit). Rounding w' to f16 is off by at most 2^-11 of each weight, less in sum than the
 // output's own rounding; bf16 would cost eight times that.
 //
 // Bound by memory: 4 r operations of a KV head's r query heads per 2 code bytes. All (sequence,
@@ -249,7 +249,7 @@ __device__ __forceinline__ void exact_unit(State<D>& st, const uint16_t* k, cons
     const int e = warp_exponent_v<BF16>(top);
     const float f = power2(-e);
     uint32_t w[2][2];
-    weigh<D>(st, s, c0 * ks, c1 * ks, (float)e, f, nv, g, w);
+    weigh<D>(st, s, c0 * ks, c1 * ks, (float)e, f * kDenomUnit, nv, g, w);
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
 #pragma unroll
@@ -279,10 +279,10 @@ __device__ void join_heads(const BlockDecodeParams& p, const uint8_t* smem, cons
     float* partials = reinterpret_cast<float*>(p.c.base + p.c.lay.partials);
     float* mine = partials + (size_t)(2 * b + (starts ? 1 : 0)) * kPart;
     auto give = [&](int head, float4 o, float l) {
-        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const float inv = l == 0.f ? 0.f : 1.f / l, u = kDenomUnit;
         if (live)
             *reinterpret_cast<uint2*>(out + (size_t)head * D + 4 * lane) =
-                make_uint2(pack2<BF16>(o.x * inv, o.y * inv), pack2<BF16>(o.z * inv, o.w * inv));
+                make_uint2(pack2<BF16>(o.x * u * inv, o.y * u * inv), pack2<BF16>(o.z * u * inv, o.w * u * inv));
     };
 #pragma unroll 1
     for (int h = 0; h < heads; ++h) {

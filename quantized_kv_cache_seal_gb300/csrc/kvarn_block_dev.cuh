@@ -156,6 +156,10 @@ constexpr int kExactK = 14;
 // push the others out of f16, and do not leave fp32 in the denominator either, for other scales
 // between 2^-60 and 2^50.
 constexpr int kZeroV = -60;
+// Denominators count w / s in units of 2^12, times this: with weights of 2^15 at most (2^7 at least for a row's
+// largest) and scales from 2^-100 (exact values 2^-108) to 2^121, sums of up to 2^24 tokens and the least of them
+// stay in fp32's normal range. Without it 32 exact tokens of 2^-100 already made an infinity.
+constexpr float kDenomUnit = 1.f / 4096;
 // Exponent of the power of two that stands for a part's V scale.
 template <bool BF16>
 __device__ __forceinline__ int warp_exponent_v(uint32_t top) {

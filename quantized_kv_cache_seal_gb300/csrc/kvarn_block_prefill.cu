@@ -7,7 +7,7 @@
 //   PV  O += W code, W = 2^(x + log2 s_V - m + 7) in f16 with m the running maximum of
 //       x + log2 s_V (raised only when it grows by more than 8, with O and the sum rescaled
 //       then): weights fit f16 whatever V's range, at most 2^15, and keep all of f16's bits
-//       down to 2^-21 of the largest. The denominator adds W / s_V in fp32. f16 weights
+//       down to 2^-21 of the largest. The denominator adds W / s_V in fp32 (units of 2^12, kDenomUnit). f16 weights
 //       (rounded by 2^-12) are kept for bf16 caches too: bf16 would cost eight times that.
 // Scales belong to 32-token parts of a step (a part is sealed or exact as a whole), so each
 // is one constant for 32 columns. Exact values and bf16 queries enter after an exact power of two
@@ -313,7 +313,7 @@ __device__ __forceinline__ void issue_role(uint32_t sbase, uint64_t* bars, int32
 // must not reach a query that does not see it through 0 x NaN: non-finite V enters as 0, and `bad`
 // says that there is some, for add_non_finite at the segment's end. K needs no such care (logits
 // of unseen tokens are replaced), but neither may set the part's power of two.
-// h: K scale, or log2 and reciprocal of the V scale. x: registers to use.
+// h: K scale, or log2 of the V scale and kDenomUnit over it. x: registers to use.
 template <int D, bool BF16, bool IS_V>
 __device__ __forceinline__ void expand_exact(const BlockView& c, const BlockPrefillSeq& e, int kvh, int tile, int wp, int lane,
                                              uint8_t* dst, float2& h, uint32_t& bad, uint4 (&x)[D / 16]) {
@@ -349,7 +349,7 @@ __device__ __forceinline__ void expand_exact(const BlockView& c, const BlockPref
         }
         const int ex = warp_exponent_v<BF16>(top);
         const float f = power2(-ex);
-        h = make_float2((float)ex, f);
+        h = make_float2((float)ex, f * kDenomUnit);
         uint8_t* atom = dst + (wp >> 1) * (D * 128);
 #pragma unroll 1
         for (int i0 = 0; i0 < D / 8; i0 += kTurn) {
@@ -708,7 +708,8 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, uint8_
                 tm_wait_ld();
 #pragma unroll
                 for (int k = 0; k < 32; ++k)
-                    o[k] = pack2<BF16>(__uint_as_float(x[k >> 4][2 * k & 31]) * inv, __uint_as_float(x[k >> 4][(2 * k & 31) + 1]) * inv);
+                    o[k] = pack2<BF16>(__uint_as_float(x[k >> 4][2 * k & 31]) * kDenomUnit * inv,
+                                       __uint_as_float(x[k >> 4][(2 * k & 31) + 1]) * kDenomUnit * inv);
                 give(piece, o);
             }
             __syncwarp();
@@ -876,11 +877,11 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_c
             o.w = fmaf(x.w, y, o.w);
         }
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const float inv = l == 0.f ? 0.f : 1.f / l, y = kDenomUnit;
     const size_t row = ((size_t)(e.q_row + tok) * p.hq + w.s.kvh * p.r + et % p.r) * D;
     if (live)
         *reinterpret_cast<uint2*>(p.out + row + 4 * lane) =
-            make_uint2(pack2<BF16>(o.x * inv, o.y * inv), pack2<BF16>(o.z * inv, o.w * inv));
+            make_uint2(pack2<BF16>(o.x * y * inv, o.y * y * inv), pack2<BF16>(o.z * y * inv, o.w * y * inv));
 }
 
 template <int D, bool INT8, bool BF16>

@@ -65,3 +65,41 @@ def test_non_finite_value_of_an_exact_token(dtype, dim, r, n, m):
         out[..., ch][sees] = 0
         want[..., ch][sees] = 0
     check(out, want, tol, (n, m))
+
+
+TINY, HUGE = 2.0 ** -100, 2.0 ** 126
+
+
+def _one_size(n, dim, size, seed):
+    """Values of random sign, size to 1.98 times it."""
+    g = torch.Generator().manual_seed(seed)
+    x = (1 + torch.randint(0, 126, (n, 1, dim), generator=g) / 128.0) * size
+    return (x * (torch.randint(0, 2, (n, 1, dim), generator=g) * 2 - 1)).to(torch.bfloat16).cuda()
+
+
+# (tokens, size) of stretches of V. A block's e4m3 scale is 2^-8 of its size, an int8 one 2^-6, and 2^-100 at least.
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("parts", [
+    [(32, TINY)],                                 # 32 exact tokens of 2^-100
+    [(64, 2.0 ** -10), (32, TINY)],               # beside larger sealed ones
+    [(64, 2.0 ** -9), (63, 2.0 ** -92)],
+    [(16384, 2.0 ** -92)],                        # many sealed ones of the smallest scale
+    [(16384, 2.0 ** -92), (64, 1.0), (7, TINY)],
+    [(300, HUGE)],                                # the other end
+    [(64, HUGE), (64, 2.0 ** 40), (50, 2.0 ** 40)],
+], ids=str)
+def test_values_at_the_ends_of_bf16(parts, code):
+    """V at the ends of bf16's range, all tokens weighted alike and not: the denominator stays in fp32's range."""
+    dim, n = 64, sum(m for m, _ in parts)
+    v = torch.cat([_one_size(m, dim, size, i) for i, (m, size) in enumerate(parts)])
+    k = tokens(n, 1, dim, torch.bfloat16, 221, 0.3)
+    m = min(n, 40)
+    q = tokens(m, 2, dim, torch.bfloat16, 222, 0.3)
+    q[:, 0] = 0  # all tokens alike
+    c = make(num_q_heads=2, num_kv_heads=1, head_dim=dim, block_tokens=64, dtype=torch.bfloat16, max_seqs=1, code=code,
+             max_seq_len=n)
+    c.append(0, [0], [n], k, v)
+    kk, vv = (held(x, 64, code) for x in (k, v))
+    want, tol = block_ref.attend(q.cpu(), kk, vv, dim ** -0.5, list(range(n - m, n)))
+    check(c.decode_attention(0, [0], q[m - 1:]), want[m - 1:], tol[m - 1:], "decode")
+    check(c.prefill_attention(0, [0], [m], q), want, tol, "prefill")
