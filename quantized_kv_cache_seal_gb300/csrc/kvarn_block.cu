@@ -361,8 +361,10 @@ int launch_block_init(const BlockView& c, void* stream) {
     return (int)cudaMemsetAsync(c.base + c.lay.err, 0, c.lay.partials - c.lay.err, (cudaStream_t)stream);
 }
 
-int launch_block_clear_counters(const BlockView& c, void* stream) {
-    return (int)cudaMemsetAsync(c.base + c.lay.counters, 0, kBlockMaxGrid * 4, (cudaStream_t)stream);
+int launch_block_clear_errors(const BlockView& c, void* stream) {
+    cudaStream_t s = (cudaStream_t)stream;
+    const cudaError_t e = cudaMemsetAsync(c.base + c.lay.err, 0, 16, s);
+    return (int)(e != cudaSuccess ? e : cudaMemsetAsync(c.base + c.lay.counters, 0, kBlockMaxGrid * 4, s));
 }
 
 int stream_capturing(void* stream, int* capturing) {

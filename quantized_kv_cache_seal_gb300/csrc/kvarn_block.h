@@ -148,7 +148,7 @@ int launch_block_read(const BlockReadParams& p, void* stream);
 int launch_block_decode(const BlockDecodeParams& p, void* stream);
 int launch_block_prefill(const BlockPrefillParams& p, void* stream);
 int launch_block_init(const BlockView& c, void* stream);
-int launch_block_clear_counters(const BlockView& c, void* stream);
+int launch_block_clear_errors(const BlockView& c, void* stream);  // the error word and the counters
 int launch_qk_norm_rope(const QkParams& p, void* stream);
 int stream_capturing(void* stream, int* capturing);
 

@@ -522,13 +522,11 @@ kvarn_status kvarn_block_check_device_error(kvarn_block_cache* c, void* stream) 
     int32_t err[4] = {0, 0, 0, 0};
     int rc = memcpy_d2h_sync(err, c->view.base + c->view.lay.err, sizeof(err), stream);
     if (rc) return cuda_fail(rc, "error word read");
-    const int32_t zero[4] = {0, 0, 0, 0};
-    rc = memcpy_h2d_async(c->view.base + c->view.lay.err, zero, sizeof(zero), stream);
-    if (rc) return cuda_fail(rc, "error word clear");
     if (err[0] == 0) return KVARN_OK;
-    // a launch in which a wait gave up may have left its counters standing
-    rc = launch_block_clear_counters(c->view, stream);
-    if (rc) return cuda_fail(rc, "counter clear");
+    // (not by a copy from here: that may read this frame after the return) and the counters, which a
+    // launch in which a wait gave up may have left standing
+    rc = launch_block_clear_errors(c->view, stream);
+    if (rc) return cuda_fail(rc, "error word clear");
     return err[0] & kErrTimeout ? KVARN_ETIMEOUT : KVARN_ESTATE;
 }
 

@@ -103,3 +103,37 @@ def test_values_at_the_ends_of_bf16(parts, code):
     want, tol = block_ref.attend(q.cpu(), kk, vv, dim ** -0.5, list(range(n - m, n)))
     check(c.decode_attention(0, [0], q[m - 1:]), want[m - 1:], tol[m - 1:], "decode")
     check(c.prefill_attention(0, [0], [m], q), want, tol, "prefill")
+
+
+def _words(c, at, n):
+    """int32 words of the cache's device block from byte `at` on: the error word stands first, the counters behind
+    the block table."""
+    off = -c.mem.data_ptr() % 256 + at
+    return c.mem[off:off + 4 * n].view(torch.int32)
+
+
+def _round(n):
+    return (n + 255) // 256 * 256
+
+
+def _counters_at(c):
+    g = c.cfg
+    return 256 + _round(g.max_seqs * g.num_layers * max(1, g.max_seq_len // g.block_tokens) * 4)
+
+
+def test_a_reported_error_is_cleared_with_the_counters():
+    """What a launch in which a wait gave up leaves behind (error word, counters), written here by hand."""
+    c = make(max_seqs=2, block_tokens=32)
+    fill(c, [3000, 700], torch.float16, 231)
+    q = tokens(600, 8, 128, torch.float16, 233, 0.3)
+    want = c.decode_attention(0, [0, 1], q[:2]), c.prefill_attention(0, [0, 1], [400, 200], q)
+    assert not _words(c, _counters_at(c), 256).any()  # zero between calls
+    for word, status in ((1, 6), (2, 5)):
+        _words(c, 0, 1).fill_(word)
+        _words(c, _counters_at(c), 256).fill_(3)
+        assert c.check_device_error() == status
+        assert c.check_device_error() == 0
+        assert not _words(c, 0, 4).any() and not _words(c, _counters_at(c), 256).any()
+        got = c.decode_attention(0, [0, 1], q[:2]), c.prefill_attention(0, [0, 1], [400, 200], q)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert c.check_device_error() == 0
