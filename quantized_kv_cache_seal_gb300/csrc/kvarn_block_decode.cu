@@ -403,6 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     // channel rows), an empty sequence's unit none. The next tile's slot is loaded a step early.
     Cursor ahead;
     int ua = u0 + w, slot = 0, issued = 0, done = 0;  // issued, done: ring entries
+    bool ok = true;                                   // no wait for a copy has given up
     const int sh = c.log2_block - 5;
     auto seek = [&]() {
         if (ua >= u1) return;
@@ -422,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     };
     auto pump = [&]() {
 #pragma unroll 1
-        while (ua < u1 && issued - done + (slot < 0 ? 2 : 1) <= Sh::kStages) {
+        while (ok && ua < u1 && issued - done + (slot < 0 ? 2 : 1) <= Sh::kStages) {
             const BlockDecodeSeq& e = p.seqs[ahead.i];
             const int tile = ua - ahead.begin, sealed = e.n >> c.log2_block << sh;
             if (slot >= 0) {
@@ -494,21 +495,27 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
             for (int z = 0; z < 4; ++z) st.o[i][z] = 0.f;
         const int sealed = e.n >> c.log2_block << sh;  // tiles
         for (; u < end; u += kWarps) {
+            if (!ok) continue;
             const int tile = u - cur.begin;
+            bool landed = true;
+            int entries = 0;
             if (tile < sealed) {
                 const int s = done % Sh::kStages;
-                bar_wait(bars + s, (uint32_t)(done / Sh::kStages & 1), err);
+                landed = bar_wait(bars + s, (uint32_t)(done / Sh::kStages & 1), err);
                 sealed_unit<D, INT8>(st, ring + s * Sh::kTile, q, c0, c1, lane);
-                ++done;
+                entries = 1;
             } else if (const int nv = min(kTileTokens, e.n - tile * kTileTokens); nv > 0) {
                 const int s = done % Sh::kStages, s2 = (done + 1) % Sh::kStages;
-                bar_wait(bars + s, (uint32_t)(done / Sh::kStages & 1), err);
-                bar_wait(bars + s2, (uint32_t)((done + 1) / Sh::kStages & 1), err);
+                landed = bar_wait(bars + s, (uint32_t)(done / Sh::kStages & 1), err);
+                landed = bar_wait(bars + s2, (uint32_t)((done + 1) / Sh::kStages & 1), err) && landed;
                 exact_unit<D, BF16>(st, reinterpret_cast<const uint16_t*>(ring + s * Sh::kTile),
                                     reinterpret_cast<const uint16_t*>(ring + s2 * Sh::kTile), nv, q, c0, c1, lane);
-                done += 2;
+                entries = 2;
             }
-            __syncwarp();
+            // one answer for the warp, after the products that need not wait for it; also: all lanes have read
+            ok = __all_sync(0xffffffffu, landed);
+            if (!ok) continue;
+            done += entries;
             pump();
         }
         // Join the warps, four heads at a time: each puts its state into the buffer and goes on; the last
@@ -554,6 +561,15 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                 }
             }
         }
+    }
+    // Normally every copy was waited for above. After a wait that gave up nothing more was issued, and what is
+    // in flight lands (a bounded wait again) before the CTA's shared memory goes away.
+    if (!ok) {
+        const uint64_t t0 = global_ns();
+#pragma unroll 1
+        for (; done < issued; ++done)
+            while (!mbar_try_wait(bars + done % Sh::kStages, (uint32_t)(done / Sh::kStages & 1)) && global_ns() - t0 < kWaitLimitNs) {
+            }
     }
 }
 

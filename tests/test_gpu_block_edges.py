@@ -137,3 +137,22 @@ def test_a_reported_error_is_cleared_with_the_counters():
         got = c.decode_attention(0, [0, 1], q[:2]), c.prefill_attention(0, [0, 1], [400, 200], q)
         assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert c.check_device_error() == 0
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("dtype,code", [("fp16", "e4m3"), ("bf16", "int8")])
+def test_decode_after_a_wait_has_given_up(dtype, code, dim):
+    """With the timeout bit of the error word set, as by a wait of a launch before, every wait that would have to wait
+    gives up: the call ends at once, says so, and the next one after the check is right."""
+    dt = TYPES[dtype]
+    c = make(max_seqs=3, num_q_heads=16, head_dim=dim, block_tokens=128, dtype=dt, code=code)
+    fill(c, [4000, 127, 700], dt, 241)
+    q = tokens(3, 16, dim, dt, 243, 0.3)
+    want = c.decode_attention(0, [0, 1, 2], q)
+    for _ in range(10):
+        _words(c, 0, 1).fill_(1)
+        c.decode_attention(0, [0, 1, 2], q)
+        c.decode_attention(0, [0, 1, 2], q)
+        assert c.check_device_error() == 6
+        assert torch.equal(c.decode_attention(0, [0, 1, 2], q), want)
+        assert c.check_device_error() == 0
