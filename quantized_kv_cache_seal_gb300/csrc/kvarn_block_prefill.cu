@@ -225,7 +225,10 @@ struct Walk {
     Seg s;
     __device__ __forceinline__ explicit Walk(uint64_t* bars_) : bars(bars_), k(0) {}
     __device__ __forceinline__ bool next(int32_t* err) {
-        if (!bar_wait(bars + kBarFeedFull + (k & (kFeed - 1)), (uint32_t)((k / kFeed) & 1), err)) return false;
+        // one answer for the warp: a lane that gave up alone would leave for the kernel's end while the others
+        // wait for it at the next warp-wide instruction
+        if (!__all_sync(0xffffffffu, bar_wait(bars + kBarFeedFull + (k & (kFeed - 1)), (uint32_t)((k / kFeed) & 1), err)))
+            return false;
         const int4* at = reinterpret_cast<const int4*>(reinterpret_cast<const Seg*>(bars + kNumBars) + (k & (kFeed - 1)));
         const int4 a = at[0], b = at[1];
         s = Seg{a.x, a.y, a.z, a.w, b.x, b.y, b.z, 0};

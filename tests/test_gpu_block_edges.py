@@ -156,3 +156,20 @@ def test_decode_after_a_wait_has_given_up(dtype, code, dim):
         assert c.check_device_error() == 6
         assert torch.equal(c.decode_attention(0, [0, 1, 2], q), want)
         assert c.check_device_error() == 0
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("lens,qlens", [([4000, 300], [40, 300]), ([2000, 1500], [2000, 1500])])
+def test_prefill_after_a_wait_has_given_up(lens, qlens, dim):
+    """The same for prefill, with its work cut between thread blocks and in whole segments."""
+    c = make(max_seqs=2, num_q_heads=32, num_kv_heads=8, head_dim=dim, block_tokens=32)
+    fill(c, lens, torch.float16, 251)
+    q = tokens(sum(qlens), 32, dim, torch.float16, 253, 0.3)
+    want = c.prefill_attention(0, [0, 1], qlens, q)
+    for _ in range(5):
+        _words(c, 0, 1).fill_(1)
+        c.prefill_attention(0, [0, 1], qlens, q)
+        c.prefill_attention(0, [0, 1], qlens, q)
+        assert c.check_device_error() == 6
+        assert torch.equal(c.prefill_attention(0, [0, 1], qlens, q), want)
+        assert c.check_device_error() == 0
