@@ -231,17 +231,47 @@ kvarn_status append(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const i
     return run_append<BlockAppendLarge>(c, layer, n_seqs, ids, n_tokens, k, v, k_stride, v_stride, stream, 5000);
 }
 
+// The work of a sequence of n tokens in an attention launch: tiles of a KV head for the single-token kernel,
+// query tile pairs of a KV head and their steps of 128 keys for the many-query one.
+int32_t head_tiles(int64_t n) { return (int32_t)std::max<int64_t>(1, (n + kTileTokens - 1) / kTileTokens); }
+int64_t head_pairs(const kvarn_block_cache* c, int64_t q_len) {
+    const int pair_tokens = 2 * (128 / c->r);
+    return (q_len + pair_tokens - 1) / pair_tokens;
+}
+int64_t head_steps(const kvarn_block_cache* c, int64_t n, int64_t q_len) {
+    const int64_t pair_tokens = 2 * (128 / c->r);
+    int64_t steps = 0;
+    for (int64_t end = pair_tokens; end < q_len + pair_tokens; end += pair_tokens)
+        steps += (n - q_len + std::min(end, q_len) - 1) / 128 + 1;
+    return steps;
+}
+// One query a sequence at most: the single-token kernel, whose rows are these queries.
+bool single_queries(int32_t n_seqs, const int32_t* q_lens) {
+    return std::all_of(q_lens, q_lens + n_seqs, [](int32_t m) { return m <= 1; });
+}
+
 kvarn_status check_attention(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* ids, const int32_t* q_lens,
                              const int32_t* added, const void* q, const void* out, float scale) {
     if (!std::isfinite(scale * kLog2e)) return fail(KVARN_EINVAL, "softmax_scale must be finite, below 2^127");
-    int64_t rows = 0;
+    const bool single = !q_lens || single_queries(n_seqs, q_lens);
+    int64_t rows = 0, work = 0;  // work: tiles or steps of a KV head
     for (int i = 0; i < n_seqs; ++i) {
         const int64_t n = c->L(ids[i], layer) + (added ? (int64_t)added[i] : 0);
         const int64_t m = q_lens ? q_lens[i] : 1;
         if (q_lens && (m < 0 || m > n)) return fail(KVARN_EINVAL, "a query count is negative or above the sequence's length");
         rows += m;
+        if (single) work += m > 0 ? head_tiles(n) : 0;
+        else work += m > 0 ? head_pairs(c, m) * ((n - 1) / 128 + 1) : 0;
     }
     if (rows * c->cfg.num_q_heads >= 1ll << 31) return fail(KVARN_ECAPACITY, "2^31 query rows or more in a call");
+    if (!single && work * c->cfg.num_kv_heads >= 1ll << 31) {  // every pair counted as long as the last: now exactly
+        work = 0;
+        for (int i = 0; i < n_seqs; ++i)
+            work += head_steps(c, c->L(ids[i], layer) + (added ? (int64_t)added[i] : 0), q_lens[i]);
+    }
+    if (work * c->cfg.num_kv_heads >= 1ll << 31)
+        return fail(KVARN_ECAPACITY, single ? "2^31 tiles of 32 tokens or more in a call"
+                                            : "2^31 steps of 128 keys or more in a call");
     if (rows > 0 && (!q || !out || !aligned16(q) || !aligned16(out)))
         return fail(KVARN_EINVAL, "q and out must be 16-byte aligned");
     return KVARN_OK;
@@ -264,9 +294,8 @@ kvarn_status run_decode(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, con
         e.seq = ids[i];
         e.n = c->L(ids[i], layer);
         e.unit_begin = (int32_t)units;
-        e.units = std::max(1, (e.n + kTileTokens - 1) / kTileTokens);
+        e.units = head_tiles(e.n);
         units += (int64_t)e.units * c->cfg.num_kv_heads;
-        if (units >= 1ll << 31) return fail(KVARN_ECAPACITY, "2^31 tiles of 32 tokens or more in a call");
     }
     p.units = units;
     // One CTA a SM, each of its eight warps a unit at least. Equal short sequences: whole (sequence, KV
@@ -283,8 +312,7 @@ kvarn_status run_decode(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, con
 
 kvarn_status run_prefill(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* ids, const int32_t* q_lens,
                          const void* q, void* out, float scale, void* stream) {
-    // One query a sequence at most: the single-token kernel, whose rows are these queries.
-    if (std::all_of(q_lens, q_lens + n_seqs, [](int32_t m) { return m <= 1; })) {
+    if (single_queries(n_seqs, q_lens)) {
         int32_t one[kBlockMaxSeqs];
         int32_t n = 0;
         for (int i = 0; i < n_seqs; ++i)
@@ -300,7 +328,7 @@ kvarn_status run_prefill(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, co
     p.r = c->r;
     p.scale_log2 = scale * kLog2e;
     p.n_seqs = 0;
-    const int hkv = c->cfg.num_kv_heads, pair_tokens = 2 * (128 / c->r);
+    const int hkv = c->cfg.num_kv_heads;
     int64_t row = 0;
     for (int i = 0; i < n_seqs; ++i) {
         if (q_lens[i] > 0) {
@@ -318,17 +346,13 @@ kvarn_status run_prefill(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, co
     int64_t segs = 0, steps = 0, longest = 0;
     for (int i = 0; i < p.n_seqs; ++i) {
         BlockPrefillSeq& e = p.seqs[i];
-        e.pairs = (e.q_len + pair_tokens - 1) / pair_tokens;
+        e.pairs = (int32_t)head_pairs(c, e.q_len);
         e.seg_begin = (int32_t)segs;
         e.step_begin = (int32_t)steps;
-        int64_t head = 0;
-        for (int t = 1; t <= e.pairs; ++t)
-            head += (e.n - e.q_len + std::min<int64_t>((int64_t)t * pair_tokens, e.q_len) - 1) / 128 + 1;
-        e.head_steps = (int32_t)head;
+        e.head_steps = (int32_t)head_steps(c, e.n, e.q_len);
         longest = std::max<int64_t>(longest, (e.n - 1) / 128 + 1);
         segs += (int64_t)e.pairs * hkv;
-        steps += head * hkv;
-        if (steps >= 1ll << 31) return fail(KVARN_ECAPACITY, "2^31 steps of 128 keys or more in a call");
+        steps += (int64_t)e.head_steps * hkv;
     }
     // Whole segments, the longest first, end when the longest does or the SMs have shared out all;
     // the line of all steps cut evenly ends a share of the steps later, and then costs about four more

@@ -264,3 +264,31 @@ def test_norm_rope_wrapper_wants_cuda_tensors():
     q = torch.zeros(3, 4, 64, dtype=torch.float16)
     with pytest.raises(ValueError):
         qk_norm_rope(q, None, torch.zeros(3, dtype=torch.int32), torch.ones(32, dtype=torch.float64))
+
+
+def test_calls_of_too_much_work_change_nothing():
+    """A prefill of 2^31 steps, a decode step of 2^31 tiles: refused before anything is appended."""
+    n = (1 << 20) + 128  # 16 heads, 32 queries a pair of tiles: n / 32 pairs of n / 128 / 2 steps each, on average
+    c = cache(num_layers=1, num_q_heads=128, num_kv_heads=16, max_seq_len=n + 1, block_tokens=128, pool_blocks=n // 128)
+    refused(3, K.kvarn_block_prefill, c, 0, [2], [n], FAKE, 2048, FAKE, 2048, FAKE, 2 * FAKE, 1.0)
+    assert K.kvarn_block_length(c, 0, 2) == 0
+    K.kvarn_block_append(c, 0, [2], [n], FAKE, 2048, FAKE, 2048)  # every block of the pool was still free
+    refused(3, K.kvarn_block_prefill_attention, c, 0, [2], [n], FAKE, 2 * FAKE, 1.0)
+    K.kvarn_block_prefill_attention(c, 0, [2], [n // 2], FAKE, 2 * FAKE, 1.0)
+    K.kvarn_block_destroy(c)
+    n = 1 << 24  # 128 heads of 32 sequences of n tokens: 2^31 tiles of 32 tokens
+    c = cache(num_layers=1, max_seqs=32, num_q_heads=128, num_kv_heads=128, head_dim=64, max_seq_len=n + 1, block_tokens=128,
+              pool_blocks=32 * n // 128)
+    ids, kv = list(range(32)), (FAKE, 8192, FAKE, 8192)
+    K.kvarn_block_append(c, 0, ids, [n - 33] * 32, *kv)
+    K.kvarn_block_decode_step(c, 0, ids, *kv, FAKE, 2 * FAKE, 1.0)
+    for step in (K.kvarn_block_decode_step, K.kvarn_block_prefill):
+        counts = ([1] * 32,) if step is K.kvarn_block_prefill else ()
+        refused(3, step, c, 0, ids, *counts, *kv, FAKE, 2 * FAKE, 1.0)  # each at a new tile
+        assert [K.kvarn_block_length(c, 0, s) for s in ids] == [n - 32] * 32
+    K.kvarn_block_append(c, 0, ids, [1] * 32, *kv)
+    refused(3, K.kvarn_block_decode_attention, c, 0, ids, FAKE, 2 * FAKE, 1.0)
+    refused(3, K.kvarn_block_prefill_attention, c, 0, ids, [1] * 32, FAKE, 2 * FAKE, 1.0)
+    K.kvarn_block_prefill_attention(c, 0, ids, [1] * 31 + [0], FAKE, 2 * FAKE, 1.0)
+    K.kvarn_block_decode_attention(c, 0, ids[:31], FAKE, 2 * FAKE, 1.0)
+    K.kvarn_block_destroy(c)
