@@ -333,7 +333,7 @@ kvarn_status kvarn_device_accessible(const void* ptr, int32_t* accessible);
  *     exact token they make their channel of the output non-finite (an infinity can come out as
  *     NaN) and no other; in K they act through the token's logit. A query whose every logit is
  *     -inf gives zeros.
- *   - q and out do not overlap.
+ *   - out may be q itself; any other overlap of the two is refused.
  *   - Attention tells a head's V scales apart up to a ratio of 2^100 (fp16 never leaves it):
  *     tokens of bf16 blocks smaller than that against the largest can count for nothing.
  *   - kvarn_last_error says what a refused call was refused for. */

@@ -274,6 +274,10 @@ kvarn_status check_attention(kvarn_block_cache* c, int32_t layer, int32_t n_seqs
                                             : "2^31 steps of 128 keys or more in a call");
     if (rows > 0 && (!q || !out || !aligned16(q) || !aligned16(out)))
         return fail(KVARN_EINVAL, "q and out must be 16-byte aligned");
+    // A row of out is written once every reader of the same row of q is through with it, and only then.
+    const uint64_t bytes = (uint64_t)rows * c->cfg.num_q_heads * c->cfg.head_dim * 2;
+    if (q != out && (uintptr_t)q < (uintptr_t)out + bytes && (uintptr_t)out < (uintptr_t)q + bytes)
+        return fail(KVARN_EINVAL, "out overlaps q (it may only be q itself)");
     return KVARN_OK;
 }
 

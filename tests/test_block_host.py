@@ -10,6 +10,7 @@ from quantized_kv_cache_seal_gb300.block_cache import BlockCache
 from quantized_kv_cache_seal_gb300.qk import qk_norm_rope
 
 FAKE = 1 << 30  # a device address that is never dereferenced in host-only mode
+FAR = 1 << 45  # another, beyond any tensor at FAKE
 
 
 def config(**kw):
@@ -270,25 +271,45 @@ def test_calls_of_too_much_work_change_nothing():
     """A prefill of 2^31 steps, a decode step of 2^31 tiles: refused before anything is appended."""
     n = (1 << 20) + 128  # 16 heads, 32 queries a pair of tiles: n / 32 pairs of n / 128 / 2 steps each, on average
     c = cache(num_layers=1, num_q_heads=128, num_kv_heads=16, max_seq_len=n + 1, block_tokens=128, pool_blocks=n // 128)
-    refused(3, K.kvarn_block_prefill, c, 0, [2], [n], FAKE, 2048, FAKE, 2048, FAKE, 2 * FAKE, 1.0)
+    refused(3, K.kvarn_block_prefill, c, 0, [2], [n], FAKE, 2048, FAKE, 2048, FAKE, FAR, 1.0)
     assert K.kvarn_block_length(c, 0, 2) == 0
     K.kvarn_block_append(c, 0, [2], [n], FAKE, 2048, FAKE, 2048)  # every block of the pool was still free
-    refused(3, K.kvarn_block_prefill_attention, c, 0, [2], [n], FAKE, 2 * FAKE, 1.0)
-    K.kvarn_block_prefill_attention(c, 0, [2], [n // 2], FAKE, 2 * FAKE, 1.0)
+    refused(3, K.kvarn_block_prefill_attention, c, 0, [2], [n], FAKE, FAR, 1.0)
+    K.kvarn_block_prefill_attention(c, 0, [2], [n // 2], FAKE, FAR, 1.0)
     K.kvarn_block_destroy(c)
     n = 1 << 24  # 128 heads of 32 sequences of n tokens: 2^31 tiles of 32 tokens
     c = cache(num_layers=1, max_seqs=32, num_q_heads=128, num_kv_heads=128, head_dim=64, max_seq_len=n + 1, block_tokens=128,
               pool_blocks=32 * n // 128)
     ids, kv = list(range(32)), (FAKE, 8192, FAKE, 8192)
     K.kvarn_block_append(c, 0, ids, [n - 33] * 32, *kv)
-    K.kvarn_block_decode_step(c, 0, ids, *kv, FAKE, 2 * FAKE, 1.0)
+    K.kvarn_block_decode_step(c, 0, ids, *kv, FAKE, FAR, 1.0)
     for step in (K.kvarn_block_decode_step, K.kvarn_block_prefill):
         counts = ([1] * 32,) if step is K.kvarn_block_prefill else ()
-        refused(3, step, c, 0, ids, *counts, *kv, FAKE, 2 * FAKE, 1.0)  # each at a new tile
+        refused(3, step, c, 0, ids, *counts, *kv, FAKE, FAR, 1.0)  # each at a new tile
         assert [K.kvarn_block_length(c, 0, s) for s in ids] == [n - 32] * 32
     K.kvarn_block_append(c, 0, ids, [1] * 32, *kv)
-    refused(3, K.kvarn_block_decode_attention, c, 0, ids, FAKE, 2 * FAKE, 1.0)
-    refused(3, K.kvarn_block_prefill_attention, c, 0, ids, [1] * 32, FAKE, 2 * FAKE, 1.0)
-    K.kvarn_block_prefill_attention(c, 0, ids, [1] * 31 + [0], FAKE, 2 * FAKE, 1.0)
-    K.kvarn_block_decode_attention(c, 0, ids[:31], FAKE, 2 * FAKE, 1.0)
+    refused(3, K.kvarn_block_decode_attention, c, 0, ids, FAKE, FAR, 1.0)
+    refused(3, K.kvarn_block_prefill_attention, c, 0, ids, [1] * 32, FAKE, FAR, 1.0)
+    K.kvarn_block_prefill_attention(c, 0, ids, [1] * 31 + [0], FAKE, FAR, 1.0)
+    K.kvarn_block_decode_attention(c, 0, ids[:31], FAKE, FAR, 1.0)
+    K.kvarn_block_destroy(c)
+
+
+def test_outputs_that_overlap_the_queries():
+    """out is q itself or lies apart from it."""
+    c = cache()
+    K.kvarn_block_append(c, 0, [0], [100], FAKE, 256, FAKE, 256)
+    q, row = FAKE + (1 << 20), 8 * 128 * 2  # bytes of a row
+    for out in (q - row + 16, q - 16, q + 16, q + row - 16):
+        refused(1, K.kvarn_block_decode_attention, c, 0, [0], q, out, 1.0)
+        refused(1, K.kvarn_block_prefill_attention, c, 0, [0], [100], q, out, 1.0)
+        refused(1, K.kvarn_block_decode_step, c, 0, [0], FAKE, 256, FAKE, 256, q, out, 1.0)
+        refused(1, K.kvarn_block_prefill, c, 0, [0], [2], FAKE, 256, FAKE, 256, q, out, 1.0)
+    refused(1, K.kvarn_block_prefill_attention, c, 0, [0], [100], q, q + 99 * row, 1.0)
+    refused(1, K.kvarn_block_prefill_attention, c, 0, [0], [100], q, q - 99 * row, 1.0)
+    assert K.kvarn_block_length(c, 0, 0) == 100
+    for out in (q, q - row, q + row):
+        K.kvarn_block_decode_attention(c, 0, [0], q, out, 1.0)
+    for out in (q, q - 100 * row, q + 100 * row):
+        K.kvarn_block_prefill_attention(c, 0, [0], [100], q, out, 1.0)
     K.kvarn_block_destroy(c)

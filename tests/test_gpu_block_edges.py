@@ -173,3 +173,29 @@ def test_prefill_after_a_wait_has_given_up(lens, qlens, dim):
         assert c.check_device_error() == 6
         assert torch.equal(c.prefill_attention(0, [0, 1], qlens, q), want)
         assert c.check_device_error() == 0
+
+
+@pytest.mark.parametrize("hkv,r", [(8, 1), (2, 8), (3, 5)])
+@pytest.mark.parametrize("lens,qlens", [([4000, 300], [40, 300]), ([2500, 2400], [2500, 2400]), ([20, 0], [20, 0])])
+def test_output_over_the_queries(lens, qlens, hkv, r):
+    """out = q: the same bits as into a tensor of its own; an output that overlaps the queries otherwise is refused."""
+    from quantized_kv_cache_seal_gb300.kvarn import KVarNError
+    c = make(max_seqs=2, num_q_heads=hkv * r, num_kv_heads=hkv, block_tokens=32)
+    fill(c, lens, torch.float16, 261)
+    big = tokens(sum(qlens) + 4, hkv * r, 128, torch.float16, 263, 0.3)
+    q, keep = big[:sum(qlens)], big.clone()
+    want = c.prefill_attention(0, [0, 1], qlens, q), c.decode_attention(0, [0, 1], q[:2])
+    for call in (lambda out: c.prefill_attention(0, [0, 1], qlens, q, out=out),
+                 lambda out: c.prefill_attention(0, [0], [2], q[:2], out=out),
+                 lambda out: c.decode_attention(0, [0, 1], q[:2], out=out)):
+        rows = sum(qlens) if call(None).shape[0] > 2 else 2
+        for at in (1, 3):
+            if at < rows:
+                with pytest.raises(KVarNError):
+                    call(big[at:at + rows])
+    assert torch.equal(big, keep)
+    assert torch.equal(c.decode_attention(0, [0, 1], q[:2], out=q[:2]), want[1])
+    big.copy_(keep)
+    assert c.prefill_attention(0, [0, 1], qlens, q, out=q) is q
+    assert torch.equal(q, want[0])
+    assert torch.equal(big[sum(qlens):], keep[sum(qlens):])
