@@ -434,8 +434,8 @@ typedef struct {
  * aligned, or NULL.
  * positions: int32 [n_tokens]; freqs: f64 [rot_dim / 2], finite, radians per position (both
  * may be NULL if rot_dim is 0). n_tokens times all heads is at most 2^31 - 1024 (EINVAL). An
- * output may be its own input (same address, stride and type); any other overlap is not
- * allowed. All pointers device. Can be captured. */
+ * output may be its own input (same address, stride and type); any other overlap of outputs
+ * with inputs or one another is refused. All pointers device. Can be captured. */
 kvarn_status kvarn_qk_norm_rope(const kvarn_qk_config* cfg, int64_t n_tokens, const void* q, int64_t q_stride,
                                 const void* k, int64_t k_stride, const float* q_weight, const float* k_weight,
                                 const int32_t* positions, const double* freqs, void* q_out, int64_t q_out_stride,

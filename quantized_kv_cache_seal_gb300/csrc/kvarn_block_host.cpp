@@ -375,6 +375,30 @@ kvarn_status run_prefill(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, co
     return rc ? cuda_fail(rc, "prefill launch") : KVARN_OK;
 }
 
+// Do any of the n rows of `len` values at a, `stride` apart, touch one of b's? (Values of 16 bits.)
+struct Rows {
+    const void* at;
+    int64_t len, stride;
+};
+bool rows_meet(const Rows& a, const Rows& b, int64_t n) {
+    typedef __int128 I;
+    const I d = (I)(uintptr_t)b.at - (I)(uintptr_t)a.at;
+    const I sa = (I)a.stride * 2, sb = (I)b.stride * 2, la = a.len * 2, lb = b.len * 2;
+    if (d >= (n - 1) * sa + la || -d >= (n - 1) * sb + lb) return false;  // apart as a whole
+    if (n == 1) return true;
+    if (sa == sb) {  // where b's rows lie between two of a's
+        const I in = (d % sa + sa) % sa;
+        return in < la || in + lb > sa;
+    }
+    for (int64_t t = 0; t < n; ++t) {  // row t of a, and the rows of b that start before its end, the last one or two
+        const I from = t * sa - d, end = from + la;
+        if (end <= 0) continue;
+        const I u = (end - 1) / sb;
+        if (u < n ? u * sb + lb > from : (n - 1) * sb + lb > from) return true;
+    }
+    return false;
+}
+
 }  // namespace
 
 // Host allocations are made by kvarn_block_create alone; every other entry works in memory
@@ -583,6 +607,16 @@ kvarn_status kvarn_qk_norm_rope(const kvarn_qk_config* cfg, int64_t n_tokens, co
         if (s.in_stride < s.heads * d || s.out_stride < s.heads * d || s.in_stride % 8 || s.out_stride % 8)
             return fail(KVARN_EINVAL, "token strides must hold a token's heads and be multiples of 8 elements");
     }
+    const Rows in[2] = {{q, hq * d, q_stride}, {k, hk * d, k_stride}};
+    const Rows out[2] = {{q_out, hq * d, q_out_stride}, {k_out, hk * d, k_out_stride}};
+    for (int i = 0; i < 2; ++i)  // an output on its own input is turned row by row
+        for (int j = 0; j < 2; ++j) {
+            if (in[i].len == 0 || out[j].len == 0) continue;
+            if (i == j && in[i].at == out[i].at && (n_tokens == 1 || in[i].stride == out[i].stride)) continue;
+            if (rows_meet(in[i], out[j], n_tokens))
+                return fail(KVARN_EINVAL, "an output overlaps an input other than its own");
+        }
+    if (hq > 0 && hk > 0 && rows_meet(out[0], out[1], n_tokens)) return fail(KVARN_EINVAL, "the outputs overlap");
     if (cfg->rot_dim > 0 && (!positions || !freqs)) return fail(KVARN_EINVAL, "no positions or frequencies");
     if (!aligned16(q_weight) || !aligned16(k_weight)) return fail(KVARN_EINVAL, "weights must be 16-byte aligned");
     QkParams p;

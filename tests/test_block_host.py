@@ -313,3 +313,24 @@ def test_outputs_that_overlap_the_queries():
     for out in (q, q - 100 * row, q + 100 * row):
         K.kvarn_block_prefill_attention(c, 0, [0], [100], q, out, 1.0)
     K.kvarn_block_destroy(c)
+
+
+def test_norm_rope_outputs_that_overlap():
+    """An output is its own input or touches no other tensor: packed rows with and without gaps, different strides."""
+    b = 2  # bytes of a value
+
+    def call(n, q, qs, k, ks, qo, qos, ko, kos):
+        refused(1, K.kvarn_qk_norm_rope, qk(head_dim=64, rot_dim=64), n, q, qs, k, ks, None, None, FAR, FAR, qo, qos, ko, kos)
+
+    q, k, qo, ko = (FAKE + i * (1 << 24) for i in range(4))  # rows of 512 and 128 values
+    call(9, q, 512, k, 128, q + 16, 512, ko, 128)            # beside its input, not on it
+    call(9, q, 512, k, 128, q, 520, ko, 128)                 # on it with another stride
+    call(9, q, 512, k, 128, q + 8 * 512 * b, 512, ko, 128)   # on its last row
+    call(1, q, 512, k, 128, q - 511 * b + 14, 512, ko, 128)  # one row, eight values
+    call(9, q, 512, k, 128, k, 512, ko, 128)
+    call(9, q, 512, k, 128, qo, 512, q + 511 * b - 14, 512)
+    call(9, q, 512, k, 128, qo, 512, qo, 512)
+    call(9, q, 512, k, 128, qo, 1024, qo + 1016 * b, 1024)   # the end of a row in the next one's beginning
+    call(9, q, 512, k, 128, qo, 1024, qo + 504 * b, 1024)
+    call(9, q, 4096, k, 4096, qo, 512, q + 512 * b, 2040)    # strides that meet two rows on
+    call(1 << 27, q, 512, k, 128, FAR << 1, 512, q + (1 << 20), 128)
