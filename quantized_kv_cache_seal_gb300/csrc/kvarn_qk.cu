@@ -45,13 +45,21 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 }
 
 // frac(freq / 2 pi) * 2^64, from integers: with freq = M 2^(E - 1086), M of 64 bits, and C = 2^64 * 2 / pi
-// rounded, the high half of M C is turns * 2^(1024 - E), to 2^-63 of it (a double product: 2^-53).
+// rounded, the high half of M C is turns * 2^(1024 - E), to 2^-63 of it (a double product: 2^-53). From 4
+// radians on whole turns go out at the top and as many bits come in at the bottom: the next words of M times
+// 128 bits of 2 / pi, so that the fraction keeps 2^-64 up to 2^64 radians (and means little beyond 2^53).
 __device__ __forceinline__ uint64_t turns(double freq) {
     const int64_t bits = __double_as_longlong(freq);
-    const int e = (int)(bits >> 52 & 0x7ff);
-    const uint64_t t = __umul64hi(((uint64_t)bits << 11) | 1ull << 63, 0xa2f9836e4e44152aull);
-    const int s = e - 1024;
-    const uint64_t f = s >= 0 ? (s < 64 ? t << s : 0) : (s > -64 ? t >> -s : 0);
+    const int s = (int)(bits >> 52 & 0x7ff) - 1024;
+    const uint64_t m = ((uint64_t)bits << 11) | 1ull << 63;
+    uint64_t f;
+    if (s <= 0) {
+        f = s > -64 ? __umul64hi(m, 0xa2f9836e4e44152aull) >> -s : 0;
+    } else {
+        constexpr uint64_t c1 = 0xa2f9836e4e441529ull, c0 = 0xfc2757d1f534ddc0ull;
+        const uint64_t low = m * c1, next = low + __umul64hi(m, c0), top = __umul64hi(m, c1) + (next < low);
+        f = s < 64 ? top << s | next >> (64 - s) : s == 64 ? next : 0;
+    }
     return bits < 0 ? 0 - f : f;
 }
 

@@ -199,3 +199,42 @@ def test_output_over_the_queries(lens, qlens, hkv, r):
     assert c.prefill_attention(0, [0, 1], qlens, q, out=q) is q
     assert torch.equal(q, want[0])
     assert torch.equal(big[sum(qlens):], keep[sum(qlens):])
+
+
+def _two_pi(bits):
+    """2 pi * 2^bits, by Machin's formula in integers."""
+    def atan_inverse(x):
+        t = (1 << bits + 32) // x
+        total, k = t, 1
+        while t:
+            t //= -x * x
+            k += 2
+            total += t // k
+        return total
+    return 8 * (4 * atan_inverse(5) - atan_inverse(239)) >> 32
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dim", [32, 64])
+def test_norm_rope_large_frequencies_at_far_positions(interleaved, dim):
+    """Angles of many turns, against whole-number arithmetic: the fraction of a turn is right at any position."""
+    import math
+    from fractions import Fraction
+    from quantized_kv_cache_seal_gb300.qk import qk_norm_rope
+    freqs = [1.0, -3.999999, 4.0, 4.000001, 6.283185307179586, 7.7, -12345.678, 1048577.0, 1e9, -987654321.125, 2.0 ** 33 + 0.25,
+             1e13, 2.0 ** 53 - 1, -2.0 ** 60 * 1.1, 2.0 ** 63 * 1.7, 0.001]
+    positions = [0, 1, -1, 2 ** 31 - 1, -2 ** 31, 1234567891, -987654321, 131071, 2 ** 30]
+    x = torch.zeros(len(positions), 2, dim, dtype=torch.float16, device="cuda")
+    a, b = (slice(0, 32, 2), slice(1, 32, 2)) if interleaved else (slice(0, 16), slice(16, 32))
+    x[..., a] = 1  # (1, 0) turns to (cos, sin)
+    y, _ = qk_norm_rope(x, None, torch.tensor(positions, dtype=torch.int32, device="cuda"),
+                        torch.tensor(freqs, dtype=torch.float64, device="cuda"), interleaved=interleaved)
+    y = y.cpu().double()
+    circle = _two_pi(400)
+    for t, p in enumerate(positions):
+        for i, f in enumerate(freqs):
+            turn = Fraction(f) * p * (1 << 400) / circle
+            phi = float(turn - math.floor(turn)) * 2 * math.pi
+            for got, want in zip((y[t, 1, a][i], y[t, 1, b][i]), (math.cos(phi), math.sin(phi))):
+                # the angle to 2^-29 and fp32 (2^-22 with sincospi's 2 ulp), fp16's rounding
+                assert abs(float(got) - want) <= 2.0 ** -22 + 2.0 ** -11 * abs(want) + 2.0 ** -25, (p, f)
