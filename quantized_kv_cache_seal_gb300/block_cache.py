@@ -17,7 +17,11 @@ class BlockCache:
     """K and V of ``num_layers`` layers and ``max_seqs`` sequences in blocks of ``block_tokens`` (32, 64 or 128)
     tokens, sealed at 8 bits when full and exact until then. ``code``: "e4m3" (power-of-two scales; keeps small
     channels beside outliers) or "int8" (scale amax / 127; finer where values are alike). Tensors are ``dtype``
-    (fp16 or bf16) on ``device``; calls go to ``stream`` or the device's current stream and do not synchronise."""
+    (fp16 or bf16) on ``device``; calls go to ``stream`` or the device's current stream and do not synchronise.
+
+    A torch.cuda.Stream given as ``stream`` holds the memory of a call's tensors until it is through with them, and the
+    cache's own memory is held by every such or current stream that calls went to. A stream given by its address holds
+    nothing: keep the tensors and the cache until its work is done. Results belong to the stream that wrote them."""
 
     def __init__(self, num_layers=1, max_seqs=1, num_q_heads=32, num_kv_heads=8, head_dim=128, block_tokens=64,
                  code="e4m3", dtype=torch.float16, max_seq_len=32768, pool_blocks=None, device="cuda", flags=0):
@@ -35,6 +39,8 @@ class BlockCache:
         self.mem = torch.empty(self.nbytes + 256, dtype=torch.uint8, device=device)
         self.device = self.mem.device
         self.index = self.mem.get_device()  # -1: the CPU
+        # streams that hold the cache's memory: the one that it was allocated on, then others as they come
+        self._holders = {None if self.index < 0 else K.current_stream(self.device)}
         base = (self.mem.data_ptr() + 255) // 256 * 256
         with K.on_device(self.device):
             self.handle = K.kvarn_block_create(self.cfg, base, self.nbytes)
@@ -71,6 +77,14 @@ class BlockCache:
                 return between if rows > 1 else heads * dim
         self._refuse(name, x, f"a {self.dtype} tensor {(rows, heads, dim)} with dense heads")
 
+    def _used(self, given, stream, *tensors):
+        """A call went to `stream` (an address), which the caller gave as `given` (None: the current one)."""
+        if given is not None:
+            K.hold(given, *tensors)
+        if stream not in self._holders and not isinstance(given, int):
+            K.hold(given or torch.cuda.current_stream(self.device), self.mem)
+            self._holders.add(stream)
+
     # -- calls -----------------------------------------------------------------------------------------------
     def append(self, layer: int, seq_ids: Sequence[int], n_tokens: Sequence[int], k: torch.Tensor, v: torch.Tensor,
                stream=None):
@@ -78,8 +92,9 @@ class BlockCache:
         rows = sum(n_tokens)
         ks, vs = self._tokens(k, rows, "k"), self._tokens(v, rows, "v")
         _same_length(seq_ids, n_tokens)
-        with K.on_device(self.device, stream) as stream:
-            K.kvarn_block_append(self.handle, layer, seq_ids, n_tokens, k, ks, v, vs, stream)
+        with K.on_device(self.device, stream) as s:
+            K.kvarn_block_append(self.handle, layer, seq_ids, n_tokens, k, ks, v, vs, s)
+            self._used(stream, s, k, v)
 
     def read(self, layer: int, seq_ids: Sequence[int], starts: Optional[Sequence[int]], counts: Sequence[int],
              dtype: Optional[torch.dtype] = None, stream=None):
@@ -94,10 +109,11 @@ class BlockCache:
         if len(counts) and min(counts) < 0:
             raise ValueError("counts must not be negative")
         shape = (sum(counts), self.kv_heads, self.dim)
-        with K.on_device(self.device, stream) as stream:
+        with K.on_device(self.device, stream) as s:
             k = torch.empty(shape, dtype=dtype, device=self.device)
             v = torch.empty_like(k)
-            K.kvarn_block_read(self.handle, layer, seq_ids, starts, counts, k, v, dtype is torch.float32, stream)
+            K.kvarn_block_read(self.handle, layer, seq_ids, starts, counts, k, v, dtype is torch.float32, s)
+            self._used(stream, s)
         return k, v
 
     def _queries(self, q, rows, out):
@@ -109,11 +125,11 @@ class BlockCache:
                          scale: Optional[float] = None, stream=None) -> torch.Tensor:
         """One query token per sequence over all its cached tokens; q, out: [len(seq_ids)][Hq][D]."""
         self._queries(q, len(seq_ids), out)
-        with K.on_device(self.device, stream) as stream:
+        with K.on_device(self.device, stream) as s:
             if out is None:
                 out = torch.empty_like(q)
-            K.kvarn_block_decode_attention(self.handle, layer, seq_ids, q, out, self.scale if scale is None else scale,
-                                           stream)
+            K.kvarn_block_decode_attention(self.handle, layer, seq_ids, q, out, self.scale if scale is None else scale, s)
+            self._used(stream, s, q, out)
         return out
 
     def decode_step(self, layer: int, seq_ids: Sequence[int], k: torch.Tensor, v: torch.Tensor, q: torch.Tensor,
@@ -122,11 +138,12 @@ class BlockCache:
         n = len(seq_ids)
         ks, vs = self._tokens(k, n, "k"), self._tokens(v, n, "v")
         self._queries(q, n, out)
-        with K.on_device(self.device, stream) as stream:
+        with K.on_device(self.device, stream) as s:
             if out is None:
                 out = torch.empty_like(q)
             K.kvarn_block_decode_step(self.handle, layer, seq_ids, k, ks, v, vs, q, out,
-                                      self.scale if scale is None else scale, stream)
+                                      self.scale if scale is None else scale, s)
+            self._used(stream, s, k, v, q, out)
         return out
 
     def prefill_attention(self, layer: int, seq_ids: Sequence[int], q_lens: Sequence[int], q: torch.Tensor,
@@ -135,11 +152,12 @@ class BlockCache:
         """Causal attention of the last q_lens[i] tokens of each sequence; q, out: [sum(q_lens)][Hq][D]."""
         _same_length(seq_ids, q_lens)
         self._queries(q, sum(q_lens), out)
-        with K.on_device(self.device, stream) as stream:
+        with K.on_device(self.device, stream) as s:
             if out is None:
                 out = torch.empty_like(q)
             K.kvarn_block_prefill_attention(self.handle, layer, seq_ids, q_lens, q, out,
-                                            self.scale if scale is None else scale, stream)
+                                            self.scale if scale is None else scale, s)
+            self._used(stream, s, q, out)
         return out
 
     def prefill(self, layer: int, seq_ids: Sequence[int], n_tokens: Sequence[int], k: torch.Tensor, v: torch.Tensor,
@@ -150,11 +168,12 @@ class BlockCache:
         rows = sum(n_tokens)
         ks, vs = self._tokens(k, rows, "k"), self._tokens(v, rows, "v")
         self._queries(q, rows, out)
-        with K.on_device(self.device, stream) as stream:
+        with K.on_device(self.device, stream) as s:
             if out is None:
                 out = torch.empty_like(q)
             K.kvarn_block_prefill(self.handle, layer, seq_ids, n_tokens, k, ks, v, vs, q, out,
-                                  self.scale if scale is None else scale, stream)
+                                  self.scale if scale is None else scale, s)
+            self._used(stream, s, k, v, q, out)
         return out
 
     def release(self, seq_ids: Union[int, Sequence[int]]):
@@ -166,8 +185,9 @@ class BlockCache:
         return K.kvarn_block_length(self.handle, layer, seq_id)
 
     def check_device_error(self, stream=None) -> int:
-        with K.on_device(self.device, stream) as stream:
-            return K.kvarn_block_check_device_error(self.handle, stream)
+        with K.on_device(self.device, stream) as s:
+            self._used(stream, s)
+            return K.kvarn_block_check_device_error(self.handle, s)
 
 
 def _same_length(seq_ids, counts):

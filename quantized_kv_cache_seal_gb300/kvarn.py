@@ -361,6 +361,15 @@ class on_device:
             self.outer.close()
 
 
+def hold(stream, *tensors):
+    """Keep the allocator from handing the tensors' memory out again before the work queued on `stream` so far is done.
+    For a torch.cuda.Stream; an address says nothing of how long its stream lives, so nothing is noted for one."""
+    if hasattr(stream, "cuda_stream"):
+        for t in tensors:
+            if t is not None and t.is_cuda:
+                t.record_stream(stream)
+
+
 def current_stream(device) -> int:
     """The current stream of a CUDA device, as an address."""
     import torch

@@ -46,7 +46,8 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Te
     positions: int32 [T]; freqs: float64 [R / 2], radians per position, R <= D a multiple of 8 (channels from R on
     pass); weights: float32 [D]. q and k are fp16 or bf16 and may be parts of a packed projection (any stride between
     tokens). Results are ``dtype`` (default: the inputs'; fp16 for a KVarN cache) or go to q_out and k_out, which
-    may be q and k themselves. Returns (q, k)."""
+    may be q and k themselves. Returns (q, k); no gradient is recorded. A torch.cuda.Stream given as ``stream`` holds the
+    tensors' memory until it is through with them; one given by its address does not."""
     index = q.get_device()
     if q.dim() != 3 or (k is not None and k.dim() != 3) or index < 0 or q.dtype not in _TYPES:
         _refuse("q", q, "a CUDA tensor [tokens][heads][dim] of fp16 or bf16, as k")
@@ -70,10 +71,12 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Te
     qos = hq * dim if q_out is None else _stride(q_out, "q_out", out_type, index, tokens, hq, dim)
     kos = hkv * dim if k_out is None else _stride(k_out, "k_out", out_type, index, tokens, hkv, dim)
     cfg = _config(hq, hkv, dim, 2 * freqs.shape[0], int(interleaved), _TYPES[in_type], _TYPES[out_type], eps)
-    with K.on_device(q.device, stream) as stream:  # results are allocated on the stream that writes them
+    with K.on_device(q.device, stream) as s:  # results are allocated on the stream that writes them
         if q_out is None:
             q_out = torch.empty((tokens, hq, dim), dtype=out_type, device=q.device)
         if k is not None and k_out is None:
             k_out = torch.empty((tokens, hkv, dim), dtype=out_type, device=q.device)
-        K.kvarn_qk_norm_rope(cfg, tokens, q, qs, k, ks, q_weight, k_weight, positions, freqs, q_out, qos, k_out, kos, stream)
+        K.kvarn_qk_norm_rope(cfg, tokens, q, qs, k, ks, q_weight, k_weight, positions, freqs, q_out, qos, k_out, kos, s)
+        if stream is not None:
+            K.hold(stream, q, k, positions, freqs, q_weight, k_weight, q_out, k_out)
     return q_out, k_out

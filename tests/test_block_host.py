@@ -334,3 +334,22 @@ def test_norm_rope_outputs_that_overlap():
     call(9, q, 512, k, 128, qo, 1024, qo + 504 * b, 1024)
     call(9, q, 4096, k, 4096, qo, 512, q + 512 * b, 2040)    # strides that meet two rows on
     call(1 << 27, q, 512, k, 128, FAR << 1, 512, q + (1 << 20), 128)
+
+
+def test_streams_that_hold_memory():
+    """A Stream object is noted with each tensor of the GPU, an address with none."""
+    class Stream:
+        cuda_stream = 7
+
+    class Tensor:
+        def __init__(self, is_cuda):
+            self.is_cuda, self.noted = is_cuda, []
+
+        def record_stream(self, s):
+            self.noted.append(s)
+
+    a, b, s = Tensor(True), Tensor(False), Stream()
+    K.hold(s, a, None, b)
+    K.hold(7, a)
+    K.hold(None, a)
+    assert a.noted == [s] and b.noted == []

@@ -238,3 +238,56 @@ def test_norm_rope_large_frequencies_at_far_positions(interleaved, dim):
             for got, want in zip((y[t, 1, a][i], y[t, 1, b][i]), (math.cos(phi), math.sin(phi))):
                 # the angle to 2^-29 and fp32 (2^-22 with sincospi's 2 ulp), fp16's rounding
                 assert abs(float(got) - want) <= 2.0 ** -22 + 2.0 ** -11 * abs(want) + 2.0 ** -25, (p, f)
+
+
+def test_a_stream_that_a_call_names_holds_its_tensors():
+    """What the caller drops after a call on another stream is not handed out again before that stream is through."""
+    from quantized_kv_cache_seal_gb300.qk import qk_norm_rope
+    c = make(max_seqs=1, block_tokens=32)
+    c.append(0, [0], [100], *(tokens(100, 2, 128, torch.float16, s) for s in (271, 272)))
+    base = [tokens(500, h, 128, torch.float16, s) for h, s in ((2, 273), (2, 274), (8, 275))]
+    pos = torch.arange(500, dtype=torch.int32, device="cuda")
+    freqs = torch.rand(64, dtype=torch.float64, device="cuda")
+    other = make(max_seqs=1, block_tokens=32)
+    other.append(0, [0], [100], *(tokens(100, 2, 128, torch.float16, s) for s in (271, 272)))
+    want = other.prefill(0, [0], [500], *base), qk_norm_rope(base[2], base[0], pos, freqs)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+
+    def dropped(call, tensors):
+        at = {t.data_ptr(): t.nbytes for t in tensors}
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(100_000_000)  # some 50 ms
+        got = call(*tensors)
+        tensors.clear()
+        again = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for n in at.values() for _ in range(3)]
+        assert not {t.data_ptr() for t in again} & set(at)
+        side.synchronize()
+        return got
+
+    got = dropped(lambda k, v, q: c.prefill(0, [0], [500], k, v, q, stream=side), [x.clone() for x in base])
+    assert torch.equal(got, want[0])
+    got = dropped(lambda q, k, p, f: qk_norm_rope(q, k, p, f, stream=side), [base[2].clone(), base[0].clone(), pos.clone(),
+                                                                          freqs.clone()])
+    assert torch.equal(got[0], want[1][0]) and torch.equal(got[1], want[1][1])
+
+
+@pytest.mark.parametrize("named", [False, True])
+def test_the_streams_of_its_calls_hold_the_cache(named):
+    c = make(max_seqs=1, block_tokens=32)
+    c.append(0, [0], [100], *(tokens(100, 2, 128, torch.float16, s) for s in (281, 282)))
+    q = tokens(1, 8, 128, torch.float16, 283)
+    want = c.decode_attention(0, [0], q)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)
+        got = c.decode_attention(0, [0], q) if not named else None
+    if named:
+        got = c.decode_attention(0, [0], q, stream=side)
+    at, n = c.mem.data_ptr(), c.mem.nbytes
+    del c
+    again = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for _ in range(3)]
+    assert at not in {t.data_ptr() for t in again}
+    side.synchronize()
+    assert torch.equal(got, want)
