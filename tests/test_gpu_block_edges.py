@@ -291,3 +291,90 @@ def test_the_streams_of_its_calls_hold_the_cache(named):
     assert at not in {t.data_ptr() for t in again}
     side.synchronize()
     assert torch.equal(got, want)
+
+
+# ---------------------------------------------------------------------------------- the many-query kernel by itself
+def test_prefill_with_scales_of_very_different_size():
+    """V blocks whose scales differ by 2^20 and logits that favour the small one, for several queries of a sequence."""
+    c = make(num_q_heads=2, num_kv_heads=1, block_tokens=32, max_seqs=1)
+    g = torch.Generator().manual_seed(4)
+    k, v = (torch.randn(98, 1, 128, generator=g) for _ in range(2))
+    q = torch.randn(1, 2, 128, generator=g).expand(3, 2, 128).contiguous()
+    k[32:64] = q[0, :1] * 2.0  # these tokens take all the weight
+    v[:32] *= 1000.0
+    v[32:64] *= 2.0 ** -10
+    k, v, q = (x.half().cuda() for x in (k, v, q))
+    c.append(0, [0], [98], k, v)
+    want, tol = block_ref.attend(q.cpu(), held(k, 32), held(v, 32), 128 ** -0.5, [95, 96, 97])
+    check(c.prefill_attention(0, [0], [3], q), want, tol, "scales")
+
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_prefill_keeps_heads_and_unwritten_memory_apart(code, dtype):
+    """A NaN in one KV head shows in its query heads only; rows and channels never written show nowhere."""
+    dt = TYPES[dtype]
+    c = make(block_tokens=32, code=code, dtype=dt)
+    c.mem.fill_(0xff)  # whatever was there before the cache
+    lens, m = [45, 45, 50], [2, 3, 4]
+    k, v = (tokens(140, 2, 128, dt, s, 0.3) for s in (290, 291))
+    q = tokens(9, 8, 128, dt, 292, 0.3)
+    c.append(0, [0, 1, 2], lens, k, v)
+    out, at = c.prefill_attention(0, [0, 1, 2], m, q), 0
+    for s, (x, y) in enumerate(zip(k.split(lens), v.split(lens))):
+        want, tol = block_ref.attend(q[at:at + m[s]].cpu(), held(x, 32, code), held(y, 32, code), 128 ** -0.5,
+                                     list(range(lens[s] - m[s], lens[s])))
+        check(out[at:at + m[s]], want, tol, s)
+        at += m[s]
+    clean = out
+    c.release([0, 1, 2])
+    v[10, 1, 5] = float("nan")       # sequence 0, sealed block
+    v[45 + 44, 0, 7] = float("nan")  # sequence 1, its last token
+    k[90 + 48, 1, 0] = float("nan")  # sequence 2, its last but one
+    c.append(0, [0, 1, 2], lens, k, v)
+    out = c.prefill_attention(0, [0, 1, 2], m, q)
+    assert torch.equal(out[:2, :4], clean[:2, :4]) and bool(out[:2, 4:].isnan().all())
+    rest = [i for i in range(128) if i != 7]
+    assert torch.equal(out[2:4], clean[2:4]) and torch.equal(out[4, 4:], clean[4, 4:])
+    assert bool(out[4, :4, 7].isnan().all()) and torch.equal(out[4, :4][:, rest], clean[4, :4][:, rest])
+    assert torch.equal(out[5:, :4], clean[5:, :4]) and torch.equal(out[5:7], clean[5:7]) and bool(out[7:, 4:].isnan().all())
+
+
+@pytest.mark.parametrize("dtype,code,dim", [("fp16", "int8", 64), ("bf16", "e4m3", 128)])
+def test_layers_and_scattered_blocks(dtype, code, dim):
+    """Attention and read on other layers than the first, where appends to several sequences and layers in turn, with
+    releases between, have scattered each sequence's blocks over the pool."""
+    dt, layers, seqs = TYPES[dtype], 3, 3
+    c = make(num_layers=layers, max_seqs=seqs, head_dim=dim, block_tokens=32, dtype=dt, code=code, max_seq_len=700,
+             pool_blocks=130)
+    g = torch.Generator().manual_seed(5)
+    kept = {}
+    for turn in range(45):
+        layer, s = (int(torch.randint(0, n, (1,), generator=g)) for n in (layers, seqs))
+        if turn % 15 == 14 and turn < 40:
+            c.release(s)
+            kept = {at: x for at, x in kept.items() if at[1] != s}
+        n = int(torch.randint(1, 90, (1,), generator=g))
+        x = [tokens(n, 2, dim, dt, 300 + 2 * turn + i, 0.3) for i in (0, 1)]
+        if c.length(layer, s) + n > 700:
+            continue
+        c.append(layer, [s], [n], *x)
+        kept[layer, s] = [torch.cat(p) for p in zip(kept[layer, s], x)] if (layer, s) in kept else x
+    q = tokens(90, 8, dim, dt, 400, 0.3)
+    assert sum(layer > 0 for layer, _ in kept) >= 4
+    for layer in range(layers):
+        ids = [s for s in range(seqs) if (layer, s) in kept]
+        lens = [kept[layer, s][0].shape[0] for s in ids]
+        assert lens == [c.length(layer, s) for s in ids]
+        refs = [[held(x, 32, code) for x in kept[layer, s]] for s in ids]
+        m = [min(n, 30) for n in lens]
+        many, one, at = c.prefill_attention(layer, ids, m, q[:sum(m)]), c.decode_attention(layer, ids, q[:len(ids)]), 0
+        back = c.read(layer, ids, None, lens, dtype=torch.float32)
+        for i, (n, ref) in enumerate(zip(lens, refs)):
+            want, tol = block_ref.attend(q[at:at + m[i]].cpu(), *ref, dim ** -0.5, list(range(n - m[i], n)))
+            check(many[at:at + m[i]], want, tol, (layer, i))
+            want, tol = block_ref.attend(q[i:i + 1].cpu(), *ref, dim ** -0.5, [n - 1])
+            check(one[i:i + 1], want, tol, (layer, i))
+            for x, y in zip(back, ref):
+                assert torch.equal(x[sum(lens[:i]):sum(lens[:i + 1])].cpu(), y.float())
+            at += m[i]
