@@ -378,3 +378,16 @@ def test_layers_and_scattered_blocks(dtype, code, dim):
             for x, y in zip(back, ref):
                 assert torch.equal(x[sum(lens[:i]):sum(lens[:i + 1])].cpu(), y.float())
             at += m[i]
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_queries_whose_every_logit_is_minus_infinity(dtype):
+    """Zeros, as for an empty sequence; the other heads of the token are as without."""
+    dt = TYPES[dtype]
+    k, v, q = (tokens(m, h, 128, dt, s, 0.3) for m, h, s in ((20, 1, 501), (20, 1, 502), (3, 2, 503)))
+    k[:, 0, 5] = float("inf")
+    q[:, :, 5] = torch.tensor([-1.0, 0.5], dtype=dt).cuda()
+    c = make(num_q_heads=2, num_kv_heads=1, dtype=dt, max_seqs=1)
+    c.append(0, [0], [20], k, v)
+    for out in (c.decode_attention(0, [0], q[2:]), c.prefill_attention(0, [0], [3], q)):
+        assert not out[:, 0].any() and bool(out[:, 1].isnan().all())
