@@ -412,7 +412,8 @@ kvarn_status kvarn_block_check_device_error(kvarn_block_cache* cache, void* stre
 
 /* ---- RMS norm of query and key heads, with the position rotation in the same pass ----
  * What the caches take as post-rotation queries and keys. For each token and head, in fp32:
- *   y_j = x_j / sqrt(mean(x^2) + eps) * weight_j   (weight NULL: y = x), then for i < rot_dim / 2
+ *   y_j = x_j / sqrt(mean(x^2) + eps) * weight_j   (weight NULL: y = x; a sum of squares beyond
+ *   fp32, which takes bf16 values of 2^60 or more, gives zeros), then for i < rot_dim / 2
  *   with phi = position * freqs[i] (reduced to 2^-29 for any position and |freqs[i]| < 2^64, then fp32):
  *   (a, b) -> (a cos phi - b sin phi, b cos phi + a sin phi)
  *   on (y_i, y_{i + rot_dim / 2}), or on (y_2i, y_{2i + 1}) if interleaved; channels from

@@ -29,8 +29,8 @@ __device__ __forceinline__ int int8_code(float x, float s, float inv) {
 
 // Four codes + 128, as bytes. The nearest whole numbers come out of the low bits of a sum with 1.5 * 2^23
 // + 128; where every remainder is under half of s they are right, and only otherwise (ties among them)
-// taken one by one. |x / s| <= 127 (1 + 2^-22), so nothing needs a clamp. (131,072 tokens of 8 heads:
-// 186 us, one by one throughout 260; e4m3 148.)
+// taken one by one. |x / s| <= 127 (1 + 2^-22), so nothing needs a clamp. (131,072 tokens of 8 heads,
+// normal values: 168 us; one by one throughout 260; e4m3, without the remainders, 144.)
 __device__ __forceinline__ uint32_t int8x4(float a, float b, float c, float d, float s, float inv) {
     constexpr float kSum = 12582912.f + 128.f;
     const float2 inv2 = make_float2(inv, inv), less = make_float2(-s, -s);

@@ -6,8 +6,8 @@
 // that drops is 2^-39 of it). V's scale is folded into the weight: w'_n = 2^(x_n + log2 s_V,n
 // - m' + 15), m' the running maximum of x + log2 s_V, so that weights are at most 2^15 in f16
 // whatever V's range, and keep all its bits down to 2^-29 of the largest; the denominator adds
-// w' / s_V in fp32, in units of 2^12 (kDenomUnit). Rounding w' to f16 is off by at most 2^-11 of each weight, less in sum than the
-// output's own rounding; bf16 would cost eight times that.
+// w' / s_V in fp32, in units of 2^12 (kDenomUnit). Rounding w' to f16 is off by at most 2^-11 of
+// each weight, less in sum than the output's own rounding; bf16 would cost eight times that.
 //
 // Bound by memory: 4 r operations of a KV head's r query heads per 2 code bytes. All (sequence,
 // KV head) pairs form one line of 32-token tiles that is cut evenly over the CTAs, one a SM;
