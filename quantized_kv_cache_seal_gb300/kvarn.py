@@ -390,6 +390,13 @@ def _i32(xs):
 _ARRAYS: dict = {}
 
 
+def _counts(xs, seq_ids):
+    """_i32 of a list with one entry a sequence: the library reads as many as there are sequences."""
+    if len(xs) != len(seq_ids):
+        raise ValueError(f"{len(seq_ids)} sequences, but {len(xs)} counts")
+    return _i32(xs)
+
+
 def _check_why(rc: int, where: str):
     """As _check, with the library's reason for any refusal (the block cache and norm calls set one)."""
     if rc != 0:
@@ -414,14 +421,14 @@ def kvarn_block_destroy(handle: int) -> None:
 
 
 def kvarn_block_append(handle, layer, seq_ids, n_tokens, k, k_stride, v, v_stride, stream=None):
-    _check_why(load().kvarn_block_append(handle, layer, len(seq_ids), _i32(seq_ids), _i32(n_tokens), _ptr(k),
-                                         k_stride, _ptr(v), v_stride, _stream(stream)), "kvarn_block_append")
+    _check_why(load().kvarn_block_append(handle, layer, len(seq_ids), _i32(seq_ids), _counts(n_tokens, seq_ids),
+                                         _ptr(k), k_stride, _ptr(v), v_stride, _stream(stream)), "kvarn_block_append")
 
 
 def kvarn_block_read(handle, layer, seq_ids, starts, counts, k, v, out_fp32=False, stream=None):
     _check_why(load().kvarn_block_read(handle, layer, len(seq_ids), _i32(seq_ids),
-                                       None if starts is None else _i32(starts), _i32(counts), _ptr(k), _ptr(v),
-                                       int(bool(out_fp32)), _stream(stream)), "kvarn_block_read")
+                                       None if starts is None else _counts(starts, seq_ids), _counts(counts, seq_ids),
+                                       _ptr(k), _ptr(v), int(bool(out_fp32)), _stream(stream)), "kvarn_block_read")
 
 
 def kvarn_block_decode_attention(handle, layer, seq_ids, q, out, softmax_scale, stream=None):
@@ -437,16 +444,17 @@ def kvarn_block_decode_step(handle, layer, seq_ids, k, k_stride, v, v_stride, q,
 
 
 def kvarn_block_prefill_attention(handle, layer, seq_ids, q_lens, q, out, softmax_scale, stream=None):
-    _check_why(load().kvarn_block_prefill_attention(handle, layer, len(seq_ids), _i32(seq_ids), _i32(q_lens),
-                                                    _ptr(q), _ptr(out), float(softmax_scale), _stream(stream)),
+    _check_why(load().kvarn_block_prefill_attention(handle, layer, len(seq_ids), _i32(seq_ids),
+                                                    _counts(q_lens, seq_ids), _ptr(q), _ptr(out),
+                                                    float(softmax_scale), _stream(stream)),
                "kvarn_block_prefill_attention")
 
 
 def kvarn_block_prefill(handle, layer, seq_ids, n_tokens, k, k_stride, v, v_stride, q, out, softmax_scale,
                         stream=None):
-    _check_why(load().kvarn_block_prefill(handle, layer, len(seq_ids), _i32(seq_ids), _i32(n_tokens), _ptr(k),
-                                          k_stride, _ptr(v), v_stride, _ptr(q), _ptr(out), float(softmax_scale),
-                                          _stream(stream)), "kvarn_block_prefill")
+    _check_why(load().kvarn_block_prefill(handle, layer, len(seq_ids), _i32(seq_ids), _counts(n_tokens, seq_ids),
+                                          _ptr(k), k_stride, _ptr(v), v_stride, _ptr(q), _ptr(out),
+                                          float(softmax_scale), _stream(stream)), "kvarn_block_prefill")
 
 
 def kvarn_block_release(handle, seq_ids):

@@ -353,3 +353,18 @@ def test_streams_that_hold_memory():
     K.hold(7, a)
     K.hold(None, a)
     assert a.noted == [s] and b.noted == []
+
+
+def test_lists_of_different_lengths():
+    """The library reads one count a sequence: a shorter list never reaches it."""
+    c = cache()
+    kv = (FAKE, 256, FAKE, 256)
+    for counts in ([5], [5, 5, 5], []):
+        for call, args in ((K.kvarn_block_append, (counts, *kv)), (K.kvarn_block_read, (None, counts, FAKE, FAR)),
+                           (K.kvarn_block_read, (counts, [0, 0], FAKE, FAR)),
+                           (K.kvarn_block_prefill_attention, (counts, FAKE, FAR, 1.0)),
+                           (K.kvarn_block_prefill, (counts, *kv, FAKE, FAR, 1.0))):
+            with pytest.raises(ValueError):
+                call(c, 0, [0, 1], *args)
+    assert K.kvarn_block_length(c, 0, 0) == 0
+    K.kvarn_block_destroy(c)
