@@ -401,6 +401,62 @@ kvarn_status kvarn_block_prefill(kvarn_block_cache* cache, int32_t layer, int32_
                                  const int32_t* n_tokens, const void* k, int64_t k_stride, const void* v,
                                  int64_t v_stride, const void* q, void* out, float softmax_scale, void* stream);
 
+/* ---- prefixes that sequences share ----
+ * A prefix is a sequence of the cache like any other (written with kvarn_block_append, of any length). Where
+ * prefix_ids[i] is not -1, the queries of seq_ids[i] attend all tokens of that sequence, then those of their own
+ * (causally among themselves), under one softmax, as if the prefix stood in front of each sequence. Neighbours in the
+ * call with the same prefix are taken together: it is read once for all their queries. A prefix may not be a sequence
+ * of the call, and must not be released while calls on the GPU read it.
+ *
+ * ---- weights that blocks receive ----
+ * weights: f32 [max_seqs][num_kv_heads][max_seq_len / block_tokens + 1] of the layer, by sequence id; place b of a (sequence,
+ * KV head) belongs to its block b, the partial one included. A call adds to it, for every token of the block, the softmax
+ * weights that its queries give the token, over the query heads of the KV head. Rows whose denominator is not a finite
+ * number above 0 (NaN or infinite logits, or none) add nothing. Only sequences of the call are touched, none of
+ * their prefixes. Set a sequence's to 0 when it begins. Sums are fp32 in a fixed order: results repeat.
+ *
+ * Both want a workspace, 16-byte aligned, of the size that kvarn_block_attend_workspace gives; it belongs to the
+ * call until its work is done (a captured graph keeps it). */
+
+/* Bytes for a call with these arguments (counts: q_lens, or n_tokens if appended; NULL: one query each; weights != 0: with
+ * weights). For kvarn_block_window_weights: 8 * num_kv_heads * sum over sequences of ceil(length / 32) * (q_lens[i] *
+ * (num_q_heads / num_kv_heads) rounded up to a multiple of 8). */
+kvarn_status kvarn_block_attend_workspace(kvarn_block_cache* cache, int32_t layer, int32_t n_seqs, const int32_t* seq_ids,
+                                          const int32_t* prefix_ids, const int32_t* counts, int32_t appended,
+                                          int32_t weights, size_t* bytes);
+
+/* kvarn_block_prefill_attention (q_lens NULL: kvarn_block_decode_attention) with prefixes (NULL: none) and weights (NULL:
+ * none; with at most one query a sequence). Can be captured; lengths, prefixes' among them, are those of the capture. */
+kvarn_status kvarn_block_attend(kvarn_block_cache* cache, int32_t layer, int32_t n_seqs, const int32_t* seq_ids,
+                                const int32_t* prefix_ids, const int32_t* q_lens, const void* q, void* out,
+                                float softmax_scale, float* weights, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/* kvarn_block_append, then kvarn_block_attend with q_lens = n_tokens; the arguments of both are checked before
+ * anything is enqueued. */
+kvarn_status kvarn_block_append_attend(kvarn_block_cache* cache, int32_t layer, int32_t n_seqs, const int32_t* seq_ids,
+                                       const int32_t* prefix_ids, const int32_t* n_tokens, const void* k,
+                                       int64_t k_stride, const void* v, int64_t v_stride, const void* q, void* out,
+                                       float softmax_scale, float* weights, void* workspace, size_t workspace_bytes,
+                                       void* stream);
+
+/* Add the weights that the last q_lens[i] <= 128 tokens of each sequence give to its blocks, each over the tokens at
+ * positions up to its own: what the end of a prompt needs of it. q: [sum(q_lens)][num_q_heads][head_dim], their queries.
+ * Reads K alone. Can be captured. */
+kvarn_status kvarn_block_window_weights(kvarn_block_cache* cache, int32_t layer, int32_t n_seqs, const int32_t* seq_ids,
+                                        const int32_t* q_lens, const void* q, float softmax_scale, float* weights,
+                                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* Cut each sequence's full blocks in `layer` to `keep` where it has more: every KV head keeps its first `first` and last
+ * `last` blocks (first + last <= keep) and, of the others, those with the largest weights (ties: the lowest index; NaN below
+ * all), in their order. The partial block stays. Blocks move as they are: values held do not change. weights move with
+ * their blocks, with 0 behind the last; kept: int32 [n_seqs][num_kv_heads][keep], the number that each block had
+ * before (-1 behind the last of a sequence with fewer than keep). The sequence's length falls to keep * block_tokens plus
+ * its partial block, and its other pool blocks are free at once: a later append may use them and must follow on the
+ * GPU (issue both to one stream). Attention knows no positions: keys keep the rotation they came with. */
+kvarn_status kvarn_block_evict(kvarn_block_cache* cache, int32_t layer, int32_t n_seqs, const int32_t* seq_ids,
+                               int32_t keep, int32_t first, int32_t last, float* weights, int32_t* kept, void* stream);
+
 /* Drop sequences in every layer and return their pool blocks (an id may be given twice). */
 kvarn_status kvarn_block_release(kvarn_block_cache* cache, int32_t n_seqs, const int32_t* seq_ids);
 
@@ -441,6 +497,16 @@ kvarn_status kvarn_qk_norm_rope(const kvarn_qk_config* cfg, int64_t n_tokens, co
                                 const void* k, int64_t k_stride, const float* q_weight, const float* k_weight,
                                 const int32_t* positions, const double* freqs, void* q_out, int64_t q_out_stride,
                                 void* k_out, int64_t k_out_stride, void* stream);
+
+/* kvarn_qk_norm_rope with several axes of positions (an image's or a video's time, row and column): pair i turns by
+ * positions[axes[i] * axis_stride + token] * freqs[i]. positions: int32, n_axes rows of n_tokens, axis_stride elements
+ * apart (0: all the same one); n_axes 1 to 255; axes: HOST memory, rot_dim / 2 numbers below n_axes, read before the
+ * call returns (NULL with one axis: that one). A captured call keeps its axes and reads its positions at each replay. */
+kvarn_status kvarn_qk_norm_rope_axes(const kvarn_qk_config* cfg, int64_t n_tokens, const void* q, int64_t q_stride,
+                                     const void* k, int64_t k_stride, const float* q_weight, const float* k_weight,
+                                     const int32_t* positions, int64_t axis_stride, int32_t n_axes, const uint8_t* axes,
+                                     const double* freqs, void* q_out, int64_t q_out_stride, void* k_out,
+                                     int64_t k_out_stride, void* stream);
 
 /* Static text for a status code. */
 const char* kvarn_status_string(kvarn_status status);

@@ -21,7 +21,12 @@ class BlockCache:
 
     A torch.cuda.Stream given as ``stream`` holds the memory of a call's tensors until it is through with them, and the
     cache's own memory is held by every such or current stream that calls went to. A stream given by its address holds
-    nothing: keep the tensors and the cache until its work is done. Results belong to the stream that wrote them."""
+    nothing: keep the tensors and the cache until its work is done. Results belong to the stream that wrote them.
+
+    Attention takes ``prefix_ids``, one a sequence (None or -1: none): sequences of the cache whose tokens stand in front
+    of the sequence's own, read once for all neighbours in the call that name the same one. With ``weights``, a layer of
+    ``new_weights()``, single queries add up what each block receives of their softmax weights, ``window_weights`` adds
+    the last queries' of prompts, and ``evict`` keeps the blocks with the most."""
 
     def __init__(self, num_layers=1, max_seqs=1, num_q_heads=32, num_kv_heads=8, head_dim=128, block_tokens=64,
                  code="e4m3", dtype=torch.float16, max_seq_len=32768, pool_blocks=None, device="cuda", flags=0):
@@ -35,6 +40,8 @@ class BlockCache:
         self.dtype = dtype
         self.heads, self.kv_heads, self.dim = num_q_heads, num_kv_heads, head_dim
         self.scale = 1.0 / math.sqrt(head_dim)
+        # places of the blocks' weights in a layer
+        self.weights_shape = (max_seqs, num_kv_heads, max(1, max_seq_len // max(1, block_tokens)) + 1)
         self.nbytes = K.kvarn_block_required_bytes(self.cfg)
         self.mem = torch.empty(self.nbytes + 256, dtype=torch.uint8, device=device)
         self.device = self.mem.device
@@ -121,10 +128,46 @@ class BlockCache:
         if out is not None:
             self._dense(out, rows, "out")
 
+    def new_weights(self) -> torch.Tensor:
+        """float32 zeros [num_layers][max_seqs][Hkv][blocks]: the weights that blocks receive, by sequence id. Yours to
+        keep, one or more; calls take one layer of it. Zero a sequence's when it begins."""
+        return torch.zeros((self.cfg.num_layers,) + self.weights_shape, dtype=torch.float32, device=self.device)
+
+    def _weights(self, x):
+        if x.shape != self.weights_shape or x.dtype is not torch.float32 or x.get_device() != self.index or (
+                not x.is_contiguous()):
+            self._refuse("weights", x, f"a contiguous torch.float32 tensor {self.weights_shape}")
+
+    def _attend(self, layer, seq_ids, prefix_ids, counts, q, out, scale, weights, stream, k=None, ks=0, v=None, vs=0):
+        """The calls with prefixes or weights; counts: queries of each sequence (None: one), or tokens to append if k."""
+        if prefix_ids is not None:
+            _same_length(seq_ids, prefix_ids)
+            prefix_ids = [-1 if x is None else x for x in prefix_ids]
+        if weights is not None:
+            self._weights(weights)
+        with K.on_device(self.device, stream) as s:
+            if out is None:
+                out = torch.empty_like(q)
+            n = K.kvarn_block_attend_workspace(self.handle, layer, seq_ids, prefix_ids, counts, k is not None,
+                                               weights is not None)
+            # of this stream's memory: free for the stream's later work once the call is enqueued
+            space = torch.empty(n, dtype=torch.uint8, device=self.device) if n else None
+            scale = self.scale if scale is None else scale
+            if k is None:
+                K.kvarn_block_attend(self.handle, layer, seq_ids, prefix_ids, counts, q, out, scale, weights, space, n, s)
+            else:
+                K.kvarn_block_append_attend(self.handle, layer, seq_ids, prefix_ids, counts, k, ks, v, vs, q, out, scale,
+                                            weights, space, n, s)
+            self._used(stream, s, k, v, q, out, weights)
+        return out
+
     def decode_attention(self, layer: int, seq_ids: Sequence[int], q: torch.Tensor, out: Optional[torch.Tensor] = None,
-                         scale: Optional[float] = None, stream=None) -> torch.Tensor:
+                         scale: Optional[float] = None, stream=None, prefix_ids: Optional[Sequence[Optional[int]]] = None,
+                         weights: Optional[torch.Tensor] = None) -> torch.Tensor:
         """One query token per sequence over all its cached tokens; q, out: [len(seq_ids)][Hq][D]."""
         self._queries(q, len(seq_ids), out)
+        if prefix_ids is not None or weights is not None:
+            return self._attend(layer, seq_ids, prefix_ids, None, q, out, scale, weights, stream)
         with K.on_device(self.device, stream) as s:
             if out is None:
                 out = torch.empty_like(q)
@@ -133,11 +176,15 @@ class BlockCache:
         return out
 
     def decode_step(self, layer: int, seq_ids: Sequence[int], k: torch.Tensor, v: torch.Tensor, q: torch.Tensor,
-                    out: Optional[torch.Tensor] = None, scale: Optional[float] = None, stream=None) -> torch.Tensor:
+                    out: Optional[torch.Tensor] = None, scale: Optional[float] = None, stream=None,
+                    prefix_ids: Optional[Sequence[Optional[int]]] = None,
+                    weights: Optional[torch.Tensor] = None) -> torch.Tensor:
         """Append one token per sequence and attend its query; k, v: [len(seq_ids)][Hkv][D]."""
         n = len(seq_ids)
         ks, vs = self._tokens(k, n, "k"), self._tokens(v, n, "v")
         self._queries(q, n, out)
+        if prefix_ids is not None or weights is not None:
+            return self._attend(layer, seq_ids, prefix_ids, [1] * n, q, out, scale, weights, stream, k, ks, v, vs)
         with K.on_device(self.device, stream) as s:
             if out is None:
                 out = torch.empty_like(q)
@@ -147,11 +194,13 @@ class BlockCache:
         return out
 
     def prefill_attention(self, layer: int, seq_ids: Sequence[int], q_lens: Sequence[int], q: torch.Tensor,
-                          out: Optional[torch.Tensor] = None, scale: Optional[float] = None,
-                          stream=None) -> torch.Tensor:
+                          out: Optional[torch.Tensor] = None, scale: Optional[float] = None, stream=None,
+                          prefix_ids: Optional[Sequence[Optional[int]]] = None) -> torch.Tensor:
         """Causal attention of the last q_lens[i] tokens of each sequence; q, out: [sum(q_lens)][Hq][D]."""
         _same_length(seq_ids, q_lens)
         self._queries(q, sum(q_lens), out)
+        if prefix_ids is not None:
+            return self._attend(layer, seq_ids, prefix_ids, q_lens, q, out, scale, None, stream)
         with K.on_device(self.device, stream) as s:
             if out is None:
                 out = torch.empty_like(q)
@@ -161,13 +210,15 @@ class BlockCache:
         return out
 
     def prefill(self, layer: int, seq_ids: Sequence[int], n_tokens: Sequence[int], k: torch.Tensor, v: torch.Tensor,
-                q: torch.Tensor, out: Optional[torch.Tensor] = None, scale: Optional[float] = None,
-                stream=None) -> torch.Tensor:
+                q: torch.Tensor, out: Optional[torch.Tensor] = None, scale: Optional[float] = None, stream=None,
+                prefix_ids: Optional[Sequence[Optional[int]]] = None) -> torch.Tensor:
         """Append a prompt chunk and attend its queries."""
         _same_length(seq_ids, n_tokens)
         rows = sum(n_tokens)
         ks, vs = self._tokens(k, rows, "k"), self._tokens(v, rows, "v")
         self._queries(q, rows, out)
+        if prefix_ids is not None:
+            return self._attend(layer, seq_ids, prefix_ids, n_tokens, q, out, scale, None, stream, k, ks, v, vs)
         with K.on_device(self.device, stream) as s:
             if out is None:
                 out = torch.empty_like(q)
@@ -175,6 +226,37 @@ class BlockCache:
                                   self.scale if scale is None else scale, s)
             self._used(stream, s, k, v, q, out)
         return out
+
+    def window_weights(self, layer: int, seq_ids: Sequence[int], q_lens: Sequence[int], q: torch.Tensor,
+                       weights: torch.Tensor, scale: Optional[float] = None, stream=None):
+        """Add to ``weights`` what the last q_lens[i] (128 at most) tokens of each sequence give its blocks, each over
+        the tokens up to its own; q: [sum(q_lens)][Hq][D], their queries."""
+        _same_length(seq_ids, q_lens)
+        self._dense(q, sum(q_lens), "q")
+        self._weights(weights)
+        r = self.heads // self.kv_heads
+        with K.on_device(self.device, stream) as s:
+            n = 8 * self.kv_heads * sum(-(-K.kvarn_block_length(self.handle, layer, i) // 32) * (-(-m * r // 8) * 8)
+                                        for i, m in zip(seq_ids, q_lens))
+            space = torch.empty(n, dtype=torch.uint8, device=self.device) if n else None
+            K.kvarn_block_window_weights(self.handle, layer, seq_ids, q_lens, q, self.scale if scale is None else scale,
+                                         weights, space, n, s)
+            self._used(stream, s, q, weights)
+
+    def evict(self, layer: int, seq_ids: Sequence[int], weights: torch.Tensor, keep: int, first: int = 1, last: int = 1,
+              stream=None) -> torch.Tensor:
+        """Cut each sequence's full blocks in ``layer`` to ``keep`` where it has more: its first ``first``, its last
+        ``last`` and those of most weight, for each KV head its own, in their order; the partial block stays. Returns
+        int32 [len(seq_ids)][Hkv][keep]: the number that each block had before (-1: none). ``weights`` move along.
+        The blocks that leave are free at once: later appends go to the same stream, as after ``release``."""
+        self._weights(weights)
+        if not 0 <= keep < 1 << 31:
+            raise ValueError(f"keep must be a number of blocks, got {keep}")
+        with K.on_device(self.device, stream) as s:
+            kept = torch.empty((len(seq_ids), self.kv_heads, keep), dtype=torch.int32, device=self.device)
+            K.kvarn_block_evict(self.handle, layer, seq_ids, keep, first, last, weights, kept, s)
+            self._used(stream, s, weights, kept)
+        return kept
 
     def release(self, seq_ids: Union[int, Sequence[int]]):
         """Drop sequences in every layer. A later append may reuse their blocks: it must follow, on the GPU, the

@@ -4,6 +4,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <vector_types.h>
+
 #include "kvarn_internal.h"
 
 namespace kvarn {
@@ -99,6 +101,7 @@ struct BlockDecodeSeq {
     int32_t seq, n;
     int32_t unit_begin;        // prefix of Hkv * units; a unit is one tile
     int32_t units;             // of each KV head, at least 1
+    int32_t pre, pre_n;        // sequence whose pre_n tokens come before its own; pre_n = 0: none
 };
 struct BlockDecodeParams {
     BlockView c;
@@ -107,6 +110,9 @@ struct BlockDecodeParams {
     int32_t n_seqs, hq, r, grid;
     int64_t units;
     float scale_log2;          // softmax scale * log2(e)
+    float2* sums;              // [units][r] or null: maximum and sum of each tile's weights, by head
+    const float *pre_o, *pre_lse;  // rows finished over shared prefixes (pre_lse null: none), [rows][Hq][D] and [rows][Hq]
+    uint32_t merged[kBlockMaxSeqs / 32];  // bit i: sequence entry i takes its row from there
     BlockDecodeSeq seqs[kBlockMaxSeqs];
 };
 
@@ -125,7 +131,61 @@ struct BlockPrefillParams {
     int32_t line;        // 1: the steps of all segments are cut evenly over the CTAs; 0: CTAs take whole segments
     int32_t steps, segs; // of all sequences and KV heads
     float scale_log2;    // softmax scale * log2(e)
+    int32_t flat;        // 1: every query sees all of the entry's n tokens, and finished rows go to pre_o and pre_lse
+    float *pre_o, *pre_lse;  // f32 [rows][Hq][D], [rows][Hq]: written if flat; else added where merged says (null: nowhere)
+    uint32_t merged[kBlockMaxSeqs / 32];  // bit i: entry i
     BlockPrefillSeq seqs[kBlockMaxSeqs];
+};
+
+// Weights of the last queries of sequences (K alone is read).
+struct BlockWindowSeq {
+    int32_t seq, n, q_len, q_row;
+    int32_t rows;        // q_len * r
+    int32_t pad;         // rows rounded up to 8
+    int32_t chunks;      // of kWindowRows rows
+    int32_t tiles;       // of its tokens
+    int32_t unit_begin;  // prefix of Hkv * chunks * tiles
+    int32_t unused;
+    int64_t sum_begin;   // prefix of Hkv * tiles * pad
+};
+struct BlockWindowParams {
+    BlockView c;
+    const uint16_t* q;
+    float2* sums;        // of each sequence [Hkv][tiles][pad]: a tile's maximum and sum, by row
+    int32_t n_seqs, hq, r, grid, smem_rows;
+    int64_t units;
+    float scale_log2;
+    BlockWindowSeq seqs[kBlockMaxSeqs];
+};
+constexpr int kWindowRows = 512;
+
+// Adds the tiles' weights to what their blocks have received.
+struct BlockWeighSeq {
+    int32_t seq, rows, pad;   // rows of a KV head, and places for them in a tile's sums
+    int32_t before, tiles;    // tiles of a prefix in front, its own
+    int32_t lse_row;          // of pre_lse, -1 for none
+    int64_t sum_begin;
+};
+struct BlockWeighParams {
+    const float2* sums;
+    const float* pre_lse;     // [rows][Hq]
+    float* weights;           // [max_seqs][Hkv][cols]
+    float shift;              // of the maxima against log2 of the sums: 2^(m - shift) sum are the tile's 2^logits
+    int32_t n_seqs, hq, hkv, log2_tiles, cols;  // tiles of a block; places of a (sequence, KV head)
+    BlockWeighSeq seqs[kBlockMaxSeqs];
+};
+
+struct BlockEvictSeq {
+    int32_t seq, full;        // full blocks, more than keep
+    int32_t row;              // of kept
+};
+struct BlockEvictParams {
+    BlockView c;
+    float* weights;           // [max_seqs][Hkv][cols]
+    int32_t* kept;            // [sequences of the call][Hkv][keep]
+    int32_t keep, first, last, cols;
+    int32_t n_seqs, n_all;    // entries to cut; of all in the call, which come first in seqs
+    BlockEvictSeq seqs[kBlockMaxSeqs];
 };
 
 struct QkParams {
@@ -139,6 +199,9 @@ struct QkParams {
     int32_t hq, hkv, d, rot, interleaved, in_bf16, out_bf16;
     int32_t heads_per_item, items_per_token;
     float eps, inv_d;
+    int32_t several;      // 1: pair i turns by positions[axes[i] * axis_stride + token], axes a byte a pair
+    int64_t axis_stride;  // elements
+    uint32_t axes[32];
 };
 
 // Launchers: 0 on success, else a cudaError_t value.
@@ -147,6 +210,9 @@ int launch_block_append(const BlockAppendLarge& p, void* stream);
 int launch_block_read(const BlockReadParams& p, void* stream);
 int launch_block_decode(const BlockDecodeParams& p, void* stream);
 int launch_block_prefill(const BlockPrefillParams& p, void* stream);
+int launch_block_window(const BlockWindowParams& p, void* stream);
+int launch_block_weigh(const BlockWeighParams& p, void* stream);
+int launch_block_evict(const BlockEvictParams& p, void* stream);
 int launch_block_init(const BlockView& c, void* stream);
 int launch_block_clear_errors(const BlockView& c, void* stream);  // the error word and the counters
 int launch_qk_norm_rope(const QkParams& p, void* stream);

@@ -32,7 +32,6 @@ namespace {
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr float kShift = 15.f;  // weights are at most 2^15
-#define kNegInf (-__int_as_float(0x7f800000))
 
 template <int D>
 struct Shape {
@@ -92,6 +91,15 @@ struct Cursor {
     }
 };
 
+// Tile t of a sequence's line: of the prefix in front of it (where it has one here), then its own.
+struct TilePlace {
+    int seq, n, tile;
+};
+__device__ __forceinline__ TilePlace place_of(const BlockDecodeSeq& e, int t) {
+    const int before = (e.pre_n + kTileTokens - 1) / kTileTokens;
+    return t < before ? TilePlace{e.pre, e.pre_n, t} : TilePlace{e.seq, e.n, t - before};
+}
+
 // The warp's state for one (sequence, KV head); lane 4 g + t holds heads 2 t, 2 t + 1.
 template <int D>
 struct State {
@@ -100,9 +108,11 @@ struct State {
 };
 
 // Weights of 32 tokens from S^T (rows g, g + 8 of the two 16-token halves).
+// sums: where the tile's maximum and sum of each head go, or null.
 template <int D>
 __device__ __forceinline__ void weigh(State<D>& st, const float (&s)[2][4], float f0, float f1, float lv, float ivs, int nv,
-                                      int g, uint32_t (&w)[2][2]) {
+                                      int lane, int r, float2* sums, uint32_t (&w)[2][2]) {
+    const int g = lane >> 2;
     float x[2][4];
     float m0 = kNegInf, m1 = kNegInf;
 #pragma unroll
@@ -150,11 +160,21 @@ __device__ __forceinline__ void weigh(State<D>& st, const float (&s)[2][4], floa
         }
     st.l[0] = fmaf(l0, ivs, st.l[0]);
     st.l[1] = fmaf(l1, ivs, st.l[1]);
+    if (sums) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) {
+            l0 += __shfl_xor_sync(0xffffffffu, l0, d);
+            l1 += __shfl_xor_sync(0xffffffffu, l1, d);
+        }
+        const int h = 2 * (lane & 3);
+        if (g == 0 && h < r) sums[h] = make_float2(st.m[0], l0 * ivs);
+        if (g == 0 && h + 1 < r) sums[h + 1] = make_float2(st.m[1], l1 * ivs);
+    }
 }
 
 template <int D, bool INT8>
 __device__ __forceinline__ void sealed_unit(State<D>& st, const uint8_t* t, const uint32_t (&q)[D / 64][4][2], float c0, float c1,
-                                            int lane) {
+                                            int lane, int r, float2* sums) {
     const float4 hd = *reinterpret_cast<const float4*>(t);
     float s[2][4] = {};
 #pragma unroll
@@ -170,7 +190,7 @@ __device__ __forceinline__ void sealed_unit(State<D>& st, const uint8_t* t, cons
                          q[c][j][0], q[c][j][1]);
         }
     uint32_t w[2][2];
-    weigh<D>(st, s, c0 * hd.x, c1 * hd.x, hd.z, hd.w, kTileTokens, lane >> 2, w);
+    weigh<D>(st, s, c0 * hd.x, c1 * hd.x, hd.z, hd.w, kTileTokens, lane, r, sums, w);
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
         const uint4 x = *reinterpret_cast<const uint4*>(t + 16 + kTileTokens * D + i * 512 + lane * 16);
@@ -183,7 +203,8 @@ __device__ __forceinline__ void sealed_unit(State<D>& st, const uint8_t* t, cons
 // values become f16 after the tile's own exact powers of two, as the queries do.
 template <int D, bool BF16>
 __device__ __forceinline__ void exact_unit(State<D>& st, const uint16_t* k, const uint16_t* v, int nv,
-                                           const uint32_t (&q)[D / 64][4][2], float c0, float c1, int lane) {
+                                           const uint32_t (&q)[D / 64][4][2], float c0, float c1, int lane, int heads,
+                                           float2* sums) {
     const int g = lane >> 2, t = lane & 3;
     float ks = 1.f;
     float s[2][4] = {};
@@ -249,7 +270,7 @@ __device__ __forceinline__ void exact_unit(State<D>& st, const uint16_t* k, cons
     const int e = warp_exponent_v<BF16>(top);
     const float f = power2(-e);
     uint32_t w[2][2];
-    weigh<D>(st, s, c0 * ks, c1 * ks, (float)e, f * kDenomUnit, nv, g, w);
+    weigh<D>(st, s, c0 * ks, c1 * ks, (float)e, f * kDenomUnit, nv, lane, heads, sums, w);
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
 #pragma unroll
@@ -265,10 +286,10 @@ __device__ __forceinline__ void exact_unit(State<D>& st, const uint16_t* k, cons
 // Heads h0 .. h0 + heads - 1 (four at most) of one (sequence, KV head) from the warps' states in the join
 // buffer, by one warp, a lane 4 channels (at head_dim 64 half the lanes). Where the CTA holds only a part of
 // the pair, the part goes to the workspace, and whichever part comes last adds them all in the order of the
-// cuts. out: first head of the pair.
+// cuts. row: of the pair's first head in q and out.
 template <int D, bool BF16>
 __device__ void join_heads(const BlockDecodeParams& p, const uint8_t* smem, const Cursor& cur, bool whole, bool starts, int half,
-                           uint16_t* out, int lane) {
+                           size_t row, int lane) {
     using Sh = Shape<D>;
     const float* join = reinterpret_cast<const float*>(smem + Sh::kJoin);
     const float* sm = reinterpret_cast<const float*>(smem + Sh::kM);
@@ -278,11 +299,19 @@ __device__ void join_heads(const BlockDecodeParams& p, const uint8_t* smem, cons
     constexpr size_t kPart = 8 * (D + 2);  // floats: O [8][D], m [8], l [8]
     float* partials = reinterpret_cast<float*>(p.c.base + p.c.lay.partials);
     float* mine = partials + (size_t)(2 * b + (starts ? 1 : 0)) * kPart;
-    auto give = [&](int head, float4 o, float l) {
+    const bool merged = p.pre_lse && (p.merged[cur.i >> 5] >> (cur.i & 31) & 1);
+    auto give = [&](int head, float4 o, float m, float l) {
         const float inv = l == 0.f ? 0.f : 1.f / l, u = kDenomUnit;
+        float4 y = make_float4(o.x * u * inv, o.y * u * inv, o.z * u * inv, o.w * u * inv);
+        if (merged) {  // with the finished row over the shared prefix
+            const float2 f = merge_factors(lse_of(m, l, kShift), p.pre_lse[row + head]);
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (live) x = *reinterpret_cast<const float4*>(p.pre_o + (row + head) * D + 4 * lane);
+            y = make_float4(merge(y.x, x.x, f), merge(y.y, x.y, f), merge(y.z, x.z, f), merge(y.w, x.w, f));
+        }
         if (live)
-            *reinterpret_cast<uint2*>(out + (size_t)head * D + 4 * lane) =
-                make_uint2(pack2<BF16>(o.x * u * inv, o.y * u * inv), pack2<BF16>(o.z * u * inv, o.w * u * inv));
+            *reinterpret_cast<uint2*>(p.out + (row + head) * D + 4 * lane) =
+                make_uint2(pack2<BF16>(y.x, y.y), pack2<BF16>(y.z, y.w));
     };
 #pragma unroll 1
     for (int h = 0; h < heads; ++h) {
@@ -302,7 +331,7 @@ __device__ void join_heads(const BlockDecodeParams& p, const uint8_t* smem, cons
             l = fmaf(sl[z * 4 + h], f, l);
         }
         if (whole) {
-            give(4 * half + h, o, l);
+            give(4 * half + h, o, big, l);
         } else {
             if (live) *reinterpret_cast<float4*>(mine + (4 * half + h) * D + 4 * lane) = o;
             if (lane == 0) mine[8 * D + 4 * half + h] = big, mine[8 * D + 8 + 4 * half + h] = l;
@@ -371,7 +400,7 @@ __device__ void join_heads(const BlockDecodeParams& p, const uint8_t* smem, cons
         }
 #pragma unroll
         for (int y = 0; y < 4; ++y)
-            if (h0 + y < p.r) give(h0 + y, o[y], l[y]);
+            if (h0 + y < p.r) give(h0 + y, o[y], big[y], l[y]);
     }
 }
 
@@ -408,10 +437,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     auto seek = [&]() {
         if (ua >= u1) return;
         ahead.advance(p, ua);
-        const BlockDecodeSeq& e = p.seqs[ahead.i];
-        const int tile = ua - ahead.begin;
+        const TilePlace e = place_of(p.seqs[ahead.i], ua - ahead.begin);
         slot = -1;
-        if (tile < e.n >> c.log2_block << sh) slot = __ldg(block_table(c, e.seq) + (tile >> sh));
+        if (e.tile < e.n >> c.log2_block << sh) slot = __ldg(block_table(c, e.seq) + (e.tile >> sh));
     };
     auto entry = [&](const void* src, uint32_t bytes) {
         if (lane == 0) {
@@ -424,8 +452,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     auto pump = [&]() {
 #pragma unroll 1
         while (ok && ua < u1 && issued - done + (slot < 0 ? 2 : 1) <= Sh::kStages) {
-            const BlockDecodeSeq& e = p.seqs[ahead.i];
-            const int tile = ua - ahead.begin, sealed = e.n >> c.log2_block << sh;
+            const TilePlace e = place_of(p.seqs[ahead.i], ua - ahead.begin);
+            const int tile = e.tile, sealed = e.n >> c.log2_block << sh;
             if (slot >= 0) {
                 entry(tile_ptr(c, slot, ahead.h, tile & ((1 << sh) - 1)), Sh::kTile);
             } else if (tile * kTileTokens < e.n) {
@@ -447,7 +475,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     int u = u0 + w, joins = 0;
     for (int begin = u0; begin < u1; begin = min(cur.end, u1)) {
         cur.advance(p, begin);
-        const BlockDecodeSeq& e = p.seqs[cur.i];
         const int end = min(cur.end, u1);
         const int h0 = cur.h * p.r;
         // the queries of the pair's r heads as B operands: lane 4 g + t holds head g, channels
@@ -493,24 +520,27 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
         for (int i = 0; i < D / 16; ++i)
 #pragma unroll
             for (int z = 0; z < 4; ++z) st.o[i][z] = 0.f;
-        const int sealed = e.n >> c.log2_block << sh;  // tiles
         for (; u < end; u += kWarps) {
             if (!ok) continue;
-            const int tile = u - cur.begin;
+            const TilePlace e = place_of(p.seqs[cur.i], u - cur.begin);
+            const int tile = e.tile, sealed = e.n >> c.log2_block << sh;
+            float2* sums = p.sums ? p.sums + (size_t)u * p.r : nullptr;
             bool landed = true;
             int entries = 0;
             if (tile < sealed) {
                 const int s = done % Sh::kStages;
                 landed = bar_wait(bars + s, (uint32_t)(done / Sh::kStages & 1), err);
-                sealed_unit<D, INT8>(st, ring + s * Sh::kTile, q, c0, c1, lane);
+                sealed_unit<D, INT8>(st, ring + s * Sh::kTile, q, c0, c1, lane, p.r, sums);
                 entries = 1;
             } else if (const int nv = min(kTileTokens, e.n - tile * kTileTokens); nv > 0) {
                 const int s = done % Sh::kStages, s2 = (done + 1) % Sh::kStages;
                 landed = bar_wait(bars + s, (uint32_t)(done / Sh::kStages & 1), err);
                 landed = bar_wait(bars + s2, (uint32_t)((done + 1) / Sh::kStages & 1), err) && landed;
                 exact_unit<D, BF16>(st, reinterpret_cast<const uint16_t*>(ring + s * Sh::kTile),
-                                    reinterpret_cast<const uint16_t*>(ring + s2 * Sh::kTile), nv, q, c0, c1, lane);
+                                    reinterpret_cast<const uint16_t*>(ring + s2 * Sh::kTile), nv, q, c0, c1, lane, p.r, sums);
                 entries = 2;
+            } else if (sums && lane < p.r) {
+                sums[lane] = make_float2(kNegInf, 0.f);  // an empty sequence
             }
             // one answer for the warp, after the products that need not wait for it; also: all lanes have read
             ok = __all_sync(0xffffffffu, landed);
@@ -552,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
             if (lane == 0) n = atomicAdd(count, 1);
             if (__shfl_sync(0xffffffffu, n, 0) == kWarps - 1) {
                 __threadfence_block();
-                join_heads<D, BF16>(p, smem, cur, whole, begin == cur.begin, half, p.out + ((size_t)cur.i * p.hq + h0) * D, lane);
+                join_heads<D, BF16>(p, smem, cur, whole, begin == cur.begin, half, (size_t)cur.i * p.hq + h0, lane);
                 __syncwarp();
                 if (lane == 0) {
                     *count = 0;

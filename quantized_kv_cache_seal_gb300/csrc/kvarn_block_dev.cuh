@@ -166,6 +166,23 @@ __device__ __forceinline__ int warp_exponent_v(uint32_t top) {
     return __any_sync(0xffffffffu, top != 0) ? warp_exponent<BF16>(top) - kExactV : kZeroV;
 }
 
+#define kNegInf (-__int_as_float(0x7f800000))
+
+// log2 of the sum of 2^logit over a row's keys, from its running maximum m and its denominator l (weights are
+// 2^(x + log2 s_V - m + shift) and l adds weight kDenomUnit / s_V).
+__device__ __forceinline__ float lse_of(float m, float l, float shift) {
+    return l == 0.f ? kNegInf : log2f(l) + (m - shift + 12.f);
+}
+// A row over some keys and the row over others make the row over all of them: their shares, from the log2 of their
+// sums; zeros where there are no keys on either side. NaN stays.
+__device__ __forceinline__ float2 merge_factors(float a, float b) {
+    const float top = fmaxf(a, b);
+    if (top == kNegInf) return make_float2(0.f, 0.f);
+    const float x = exp2f(a - top), y = exp2f(b - top), inv = 1.f / (x + y);
+    return make_float2(x * inv, y * inv);
+}
+__device__ __forceinline__ float merge(float a, float b, float2 f) { return fmaf(a, f.x, b * f.y); }
+
 // Bytes of a 4 x 4 square: r[i] = row i; afterwards r[j] = column j.
 __device__ __forceinline__ void transpose4(uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
     const uint32_t a = __byte_perm(r0, r1, 0x5140), b = __byte_perm(r0, r1, 0x7362);

@@ -44,6 +44,8 @@ kvarn_status cuda_fail(int rc, const char* what) {
     return fail(KVARN_ECUDA, text);
 }
 
+constexpr float kDecodeShift = 3.f;  // of the decode kernel's tile maxima (2^(15 - 12))
+constexpr int kWindowTokens = 128;   // queries of a sequence in window_weights
 constexpr float kLog2e = 1.4426950408889634f;
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
@@ -233,6 +235,7 @@ kvarn_status append(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const i
 
 // The work of a sequence of n tokens in an attention launch: tiles of a KV head for the single-token kernel,
 // query tile pairs of a KV head and their steps of 128 keys for the many-query one.
+int32_t tiles_of(int64_t n) { return (int32_t)((n + kTileTokens - 1) / kTileTokens); }
 int32_t head_tiles(int64_t n) { return (int32_t)std::max<int64_t>(1, (n + kTileTokens - 1) / kTileTokens); }
 int64_t head_pairs(const kvarn_block_cache* c, int64_t q_len) {
     const int pair_tokens = 2 * (128 / c->r);
@@ -244,6 +247,11 @@ int64_t head_steps(const kvarn_block_cache* c, int64_t n, int64_t q_len) {
     for (int64_t end = pair_tokens; end < q_len + pair_tokens; end += pair_tokens)
         steps += (n - q_len + std::min(end, q_len) - 1) / 128 + 1;
     return steps;
+}
+// Flags as a mask of bits.
+void mark(uint32_t* mask, const uint8_t* flags, int n) {
+    std::memset(mask, 0, kBlockMaxSeqs / 8);
+    for (int i = 0; flags && i < n; ++i) mask[i / 32] |= (uint32_t)(flags[i] != 0) << i % 32;
 }
 // One query a sequence at most: the single-token kernel, whose rows are these queries.
 bool single_queries(int32_t n_seqs, const int32_t* q_lens) {
@@ -281,8 +289,28 @@ kvarn_status check_attention(kvarn_block_cache* c, int32_t layer, int32_t n_seqs
     return KVARN_OK;
 }
 
+// What an attention call may have beside its own tokens, sequence by sequence.
+struct Beside {
+    const int32_t* before = nullptr;   // decode: a prefix whose tokens come first in the sequence's line, -1 for none
+    const uint8_t* finished = nullptr; // 1: its rows over a prefix are in pre_o and pre_lse
+    float *pre_o = nullptr, *pre_lse = nullptr;
+    float2* sums = nullptr;            // decode: the tiles' sums
+    float* weights = nullptr;          // decode: what the blocks have received, added to
+};
+
+size_t columns(const kvarn_block_cache* c) { return (size_t)c->view.max_blocks + 1; }
+
+kvarn_status run_weigh(kvarn_block_cache* c, BlockWeighParams& p, void* stream) {
+    p.hq = c->cfg.num_q_heads;
+    p.hkv = c->cfg.num_kv_heads;
+    p.log2_tiles = c->view.log2_block - 5;
+    p.cols = (int32_t)columns(c);
+    const int rc = launch_block_weigh(p, stream);
+    return rc ? cuda_fail(rc, "weights launch") : KVARN_OK;
+}
+
 kvarn_status run_decode(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* ids, const void* q, void* out,
-                        float scale, void* stream) {
+                        float scale, void* stream, const Beside& beside = Beside()) {
     static thread_local BlockDecodeParams p;
     p.c = c->view;
     p.c.layer = layer;
@@ -298,10 +326,16 @@ kvarn_status run_decode(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, con
         e.seq = ids[i];
         e.n = c->L(ids[i], layer);
         e.unit_begin = (int32_t)units;
-        e.units = head_tiles(e.n);
+        e.pre = beside.before ? beside.before[i] : -1;
+        e.pre_n = e.pre >= 0 ? c->L(e.pre, layer) : 0;
+        e.units = e.pre_n > 0 ? tiles_of(e.pre_n) + tiles_of(e.n) : head_tiles(e.n);
         units += (int64_t)e.units * c->cfg.num_kv_heads;
     }
     p.units = units;
+    p.sums = beside.sums;
+    p.pre_o = beside.pre_o;
+    p.pre_lse = beside.pre_lse;
+    mark(p.merged, beside.finished, n_seqs);
     // One CTA a SM, each of its eight warps a unit at least. Equal short sequences: whole (sequence, KV
     // head) pairs, so that nothing is joined across CTAs (which takes about as long as four rounds).
     const int64_t pairs = (int64_t)n_seqs * c->cfg.num_kv_heads, most = std::min(c->sms, kBlockMaxGrid);
@@ -311,18 +345,65 @@ kvarn_status run_decode(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, con
     const kvarn_status st = ensure_init(c, stream);
     if (st) return st;
     const int rc = launch_block_decode(p, stream);
-    return rc ? cuda_fail(rc, "decode launch") : KVARN_OK;
+    if (rc) return cuda_fail(rc, "decode launch");
+    if (!beside.weights) return KVARN_OK;
+    static thread_local BlockWeighParams wp;
+    wp.sums = beside.sums;
+    wp.pre_lse = beside.pre_lse;
+    wp.weights = beside.weights;
+    wp.shift = kDecodeShift;
+    wp.n_seqs = n_seqs;
+    for (int i = 0; i < n_seqs; ++i) {
+        const BlockDecodeSeq& e = p.seqs[i];
+        BlockWeighSeq& s = wp.seqs[i];
+        s.seq = e.seq;
+        s.rows = s.pad = c->r;
+        s.before = tiles_of(e.pre_n);
+        s.tiles = e.units - s.before;
+        s.lse_row = beside.finished && beside.finished[i] ? i : -1;
+        s.sum_begin = (int64_t)e.unit_begin * c->r;
+    }
+    return run_weigh(c, wp, stream);
 }
 
+// Queries in rows of their own order, each entry's `q_len` of them over `n` tokens of sequence `seq`: all of them if
+// `flat` (rows go to pre_o and pre_lse), else causally.
+struct Entry {
+    int32_t seq, n, q_len, q_row;
+    uint8_t finished;
+};
+
+kvarn_status run_tiles(kvarn_block_cache* c, int32_t layer, int32_t n_entries, const Entry* entries, bool flat, const void* q,
+                       void* out, float scale, void* stream, const Beside& beside);
+
 kvarn_status run_prefill(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* ids, const int32_t* q_lens,
-                         const void* q, void* out, float scale, void* stream) {
+                         const void* q, void* out, float scale, void* stream, const Beside& beside = Beside()) {
     if (single_queries(n_seqs, q_lens)) {
-        int32_t one[kBlockMaxSeqs];
+        int32_t one[kBlockMaxSeqs], before[kBlockMaxSeqs];
+        uint8_t finished[kBlockMaxSeqs];
         int32_t n = 0;
         for (int i = 0; i < n_seqs; ++i)
-            if (q_lens[i] == 1) one[n++] = ids[i];
-        return n ? run_decode(c, layer, n, one, q, out, scale, stream) : KVARN_OK;
+            if (q_lens[i] == 1) {
+                if (beside.before) before[n] = beside.before[i];
+                if (beside.finished) finished[n] = beside.finished[i];
+                one[n++] = ids[i];
+            }
+        Beside b = beside;
+        if (b.before) b.before = before;
+        if (b.finished) b.finished = finished;
+        return n ? run_decode(c, layer, n, one, q, out, scale, stream, b) : KVARN_OK;
     }
+    Entry entries[kBlockMaxSeqs];
+    int64_t row = 0;
+    for (int i = 0; i < n_seqs; ++i) {
+        entries[i] = Entry{ids[i], c->L(ids[i], layer), q_lens[i], (int32_t)row, (uint8_t)(beside.finished && beside.finished[i])};
+        row += q_lens[i];
+    }
+    return run_tiles(c, layer, n_seqs, entries, false, q, out, scale, stream, beside);
+}
+
+kvarn_status run_tiles(kvarn_block_cache* c, int32_t layer, int32_t n_entries, const Entry* entries, bool flat, const void* q,
+                       void* out, float scale, void* stream, const Beside& beside) {
     static thread_local BlockPrefillParams p;
     p.c = c->view;
     p.c.layer = layer;
@@ -331,33 +412,37 @@ kvarn_status run_prefill(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, co
     p.hq = c->cfg.num_q_heads;
     p.r = c->r;
     p.scale_log2 = scale * kLog2e;
+    p.flat = flat;
+    p.pre_o = beside.pre_o;
+    p.pre_lse = beside.pre_lse;
     p.n_seqs = 0;
     const int hkv = c->cfg.num_kv_heads;
-    int64_t row = 0;
-    for (int i = 0; i < n_seqs; ++i) {
-        if (q_lens[i] > 0) {
-            BlockPrefillSeq& e = p.seqs[p.n_seqs++];
-            e.seq = ids[i];
-            e.n = c->L(ids[i], layer);
-            e.q_len = q_lens[i];
-            e.q_row = (int32_t)row;
-        }
-        row += q_lens[i];
+    for (int i = 0; i < n_entries; ++i) {
+        if (entries[i].q_len == 0) continue;
+        BlockPrefillSeq& e = p.seqs[p.n_seqs++];
+        e.seq = entries[i].seq;
+        e.n = entries[i].n;
+        e.q_len = entries[i].q_len;
+        e.q_row = entries[i].q_row;
+        e.pairs = entries[i].finished;  // (until they are counted below)
     }
     if (p.n_seqs == 0) return KVARN_OK;
     // the longest sequences first: their segments are the longest
     std::sort(p.seqs, p.seqs + p.n_seqs, [](const BlockPrefillSeq& a, const BlockPrefillSeq& b) { return a.n > b.n; });
+    uint8_t finished[kBlockMaxSeqs];
     int64_t segs = 0, steps = 0, longest = 0;
     for (int i = 0; i < p.n_seqs; ++i) {
         BlockPrefillSeq& e = p.seqs[i];
+        finished[i] = (uint8_t)e.pairs;
         e.pairs = (int32_t)head_pairs(c, e.q_len);
         e.seg_begin = (int32_t)segs;
         e.step_begin = (int32_t)steps;
-        e.head_steps = (int32_t)head_steps(c, e.n, e.q_len);
+        e.head_steps = flat ? e.pairs * ((e.n - 1) / 128 + 1) : (int32_t)head_steps(c, e.n, e.q_len);
         longest = std::max<int64_t>(longest, (e.n - 1) / 128 + 1);
         segs += (int64_t)e.pairs * hkv;
         steps += (int64_t)e.head_steps * hkv;
     }
+    mark(p.merged, finished, p.n_seqs);
     // Whole segments, the longest first, end when the longest does or the SMs have shared out all;
     // the line of all steps cut evenly ends a share of the steps later, and then costs about four more
     // for the partial results and the kernel that adds them (6 us where a step takes 1.5).
@@ -373,6 +458,155 @@ kvarn_status run_prefill(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, co
     if (st) return st;
     const int rc = launch_block_prefill(p, stream);
     return rc ? cuda_fail(rc, "prefill launch") : KVARN_OK;
+}
+
+// ---- prefixes and weights ----
+
+// The prefix of each sequence (-1 for none) and that none of them is a sequence of the call.
+kvarn_status check_prefixes(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* ids, const int32_t* prefix_ids,
+                            const int32_t* q_lens, const int32_t* added) {
+    if (!prefix_ids) return KVARN_OK;
+    kvarn_status st = KVARN_OK;
+    for (int i = 0; i < n_seqs; ++i) c->seen[ids[i]] = 1;
+    int64_t tiles = 0, steps = 0;
+    for (int i = 0; i < n_seqs && !st; ++i) {
+        const int32_t pre = prefix_ids[i];
+        if (pre < -1 || pre >= c->cfg.max_seqs) st = fail(KVARN_EINVAL, "no such prefix");
+        else if (pre >= 0 && c->seen[pre]) st = fail(KVARN_EINVAL, "a prefix is a sequence of the call");
+        if (st || pre < 0) continue;
+        const int64_t n = c->L(pre, layer), m = q_lens ? q_lens[i] : 1;
+        tiles += tiles_of(n) + head_tiles(c->L(ids[i], layer) + (added ? added[i] : 0));
+        steps += (m + 128 / c->r) * ((n + 127) / 128);  // more than there can be
+    }
+    for (int i = 0; i < n_seqs; ++i) c->seen[ids[i]] = 0;
+    if (!st && (tiles + n_seqs) * c->cfg.num_kv_heads >= 1ll << 31) st = fail(KVARN_ECAPACITY, "2^31 tiles of 32 tokens or more in a call");
+    if (!st && steps * c->cfg.num_kv_heads >= 1ll << 31) st = fail(KVARN_ECAPACITY, "2^31 steps of 128 keys or more in a call");
+    return st;
+}
+
+// The parts of an attention call's workspace.
+struct Workspace {
+    size_t pre_o = 0, pre_lse = 0, sums = 0, total = 0;
+};
+bool make_workspace(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* ids, const int32_t* prefix_ids,
+                    const int32_t* q_lens, const int32_t* added, bool weights, Workspace* w) {
+    unsigned __int128 rows = 0, tiles = 0, off = 0;
+    bool any = false;
+    for (int i = 0; i < n_seqs; ++i) {
+        const bool pre = prefix_ids && prefix_ids[i] >= 0;
+        any = any || pre;
+        rows += q_lens ? q_lens[i] : 1;
+        tiles += head_tiles(c->L(ids[i], layer) + (added ? added[i] : 0)) + (pre ? tiles_of(c->L(prefix_ids[i], layer)) : 0);
+    }
+    auto take = [&](unsigned __int128 n) {
+        const unsigned __int128 o = off;
+        off = (off + n + 255) / 256 * 256;
+        return (size_t)o;
+    };
+    w->pre_o = take(any ? rows * c->cfg.num_q_heads * c->cfg.head_dim * 4 : 0);
+    w->pre_lse = take(any ? rows * c->cfg.num_q_heads * 4 : 0);
+    w->sums = take(weights ? tiles * c->cfg.num_q_heads * 8 : 0);
+    w->total = (size_t)off;
+    return off < (unsigned __int128)1 << 46;
+}
+
+// Two ranges of memory that meet.
+bool meet(const void* a, size_t na, const void* b, size_t nb) {
+    return na && nb && (uintptr_t)a < (uintptr_t)b + nb && (uintptr_t)b < (uintptr_t)a + na;
+}
+
+// Arguments that attend, append_attend and window_weights share, once the sequences are known to be good.
+kvarn_status check_beside(kvarn_block_cache* c, int64_t rows, const void* q, const void* out, const float* weights,
+                          const void* workspace, size_t bytes, const Workspace& w) {
+    if (w.total > bytes || (w.total && !workspace)) return fail(KVARN_EINVAL, "the workspace is too small");
+    if (!aligned16(workspace)) return fail(KVARN_EINVAL, "the workspace must be 16-byte aligned");
+    const size_t io = (size_t)rows * c->cfg.num_q_heads * c->cfg.head_dim * 2;
+    const size_t held = weights ? (size_t)c->cfg.max_seqs * c->cfg.num_kv_heads * columns(c) * 4 : 0;
+    if (weights && ((uintptr_t)weights & 3)) return fail(KVARN_EINVAL, "weights must be 4-byte aligned");
+    if (meet(weights, held, q, io) || meet(weights, held, out, out ? io : 0) || meet(workspace, w.total, q, io) ||
+        meet(workspace, w.total, out, out ? io : 0) || meet(workspace, w.total, weights, held))
+        return fail(KVARN_EINVAL, "weights or workspace overlap another argument");
+    return KVARN_OK;
+}
+
+// All arguments of an attention call beyond check_call's, check_append's and check_attention's.
+kvarn_status check_attend(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* ids, const int32_t* prefix_ids,
+                          const int32_t* q_lens, const int32_t* added, const void* q, const void* out, const float* weights,
+                          const void* workspace, size_t bytes, Workspace* w) {
+    if (weights && q_lens && !single_queries(n_seqs, q_lens))
+        return fail(KVARN_EINVAL, "weights are noted for single queries (window_weights takes more)");
+    kvarn_status st = check_prefixes(c, layer, n_seqs, ids, prefix_ids, q_lens, added);
+    if (st) return st;
+    if (!make_workspace(c, layer, n_seqs, ids, prefix_ids, q_lens, added, weights != nullptr, w))
+        return fail(KVARN_ECAPACITY, "the workspace is too large");
+    int64_t rows = 0;
+    for (int i = 0; i < n_seqs; ++i) rows += q_lens ? q_lens[i] : 1;
+    return check_beside(c, rows, q, out, weights, workspace, bytes, *w);
+}
+
+// Is a prefix of a group of single queries better walked once, as tiles of 128 rows, than by each sequence?
+bool walked_once(const kvarn_block_cache* c, const Entry& g) {
+    const int64_t each = (int64_t)g.q_len * g.n, once = head_pairs(c, g.q_len) * (int64_t)g.n;
+    return each > 4 * once && each * c->cfg.num_kv_heads > 1 << 17;
+}
+
+kvarn_status run_attend(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* ids, const int32_t* prefix_ids,
+                        const int32_t* q_lens, const void* q, void* out, float scale, float* weights, void* workspace,
+                        const Workspace& w, void* stream) {
+    const bool single = !q_lens || single_queries(n_seqs, q_lens);
+    int32_t one[kBlockMaxSeqs], before[kBlockMaxSeqs], lens[kBlockMaxSeqs];
+    uint8_t finished[kBlockMaxSeqs];
+    Entry groups[kBlockMaxSeqs];
+    int32_t n = 0, n_groups = 0;
+    int64_t row = 0;
+    // Sequences without queries leave; runs of one prefix become groups of rows.
+    for (int i = 0; i < n_seqs; ++i) {
+        const int32_t m = q_lens ? q_lens[i] : 1;
+        if (m == 0) continue;
+        const int32_t pre = prefix_ids && prefix_ids[i] >= 0 && c->L(prefix_ids[i], layer) > 0 ? prefix_ids[i] : -1;
+        one[n] = ids[i];
+        before[n] = pre;
+        finished[n] = 0;
+        lens[n] = m;
+        if (pre >= 0) {
+            if (n == 0 || before[n - 1] != pre) groups[n_groups++] = Entry{pre, c->L(pre, layer), 0, (int32_t)row, 0};
+            groups[n_groups - 1].q_len += m;
+        }
+        ++n;
+        row += m;
+    }
+    if (n == 0) return KVARN_OK;
+    // Single queries can also walk a prefix each by itself, in the one launch that takes their own tokens. The groups whose
+    // prefix is better walked once are those where that takes longer than the tiles' steps.
+    int32_t n_once = 0;
+    for (int i = 0, g = -1, last = -1; i < n; ++i) {
+        if (before[i] < 0) {
+            last = -1;
+            continue;
+        }
+        if (before[i] != last) ++g;
+        last = before[i];
+        finished[i] = !single || walked_once(c, groups[g]);
+    }
+    for (int g = 0; g < n_groups; ++g)
+        if (!single || walked_once(c, groups[g])) groups[n_once++] = groups[g];
+    Beside b;
+    if (n_once > 0) {
+        b.pre_o = (float*)((uint8_t*)workspace + w.pre_o);
+        b.pre_lse = (float*)((uint8_t*)workspace + w.pre_lse);
+        const kvarn_status st = run_tiles(c, layer, n_once, groups, true, q, nullptr, scale, stream, b);
+        if (st) return st;
+    }
+    b.finished = finished;
+    for (int i = 0; i < n; ++i)
+        if (finished[i]) before[i] = -1;
+    if (!single) return run_prefill(c, layer, n, one, lens, q, out, scale, stream, b);
+    b.before = before;
+    if (weights) {
+        b.weights = weights;
+        b.sums = (float2*)((uint8_t*)workspace + w.sums);
+    }
+    return run_decode(c, layer, n, one, q, out, scale, stream, b);
 }
 
 // Do any of the n rows of `len` values at a, `stride` apart, touch one of b's? (Values of 16 bits.)
@@ -544,6 +778,170 @@ kvarn_status kvarn_block_prefill(kvarn_block_cache* c, int32_t layer, int32_t n_
     return run_prefill(c, layer, n_seqs, seq_ids, n_tokens, q, out, softmax_scale, stream);
 }
 
+kvarn_status kvarn_block_attend_workspace(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* seq_ids,
+                                          const int32_t* prefix_ids, const int32_t* counts, int32_t appended, int32_t weights,
+                                          size_t* bytes) {
+    if (!c || !bytes) return fail(KVARN_EINVAL, "no cache, or no place for the size");
+    if (layer < 0 || layer >= c->cfg.num_layers) return fail(KVARN_EINVAL, "no such layer");
+    if (n_seqs < 0 || (n_seqs > 0 && !seq_ids)) return fail(KVARN_EINVAL, "bad sequence list");
+    if (n_seqs > kBlockMaxSeqs) return fail(KVARN_ECAPACITY, "more than 256 sequences in a call");
+    if (appended && n_seqs > 0 && !counts) return fail(KVARN_EINVAL, "no token counts");
+    for (int i = 0; i < n_seqs; ++i) {
+        if (seq_ids[i] < 0 || seq_ids[i] >= c->cfg.max_seqs || (prefix_ids && (prefix_ids[i] < -1 || prefix_ids[i] >= c->cfg.max_seqs)))
+            return fail(KVARN_EINVAL, "a sequence id is out of range");
+        if (counts && counts[i] < 0) return fail(KVARN_EINVAL, "a count is negative");
+    }
+    Workspace w;
+    if (!make_workspace(c, layer, n_seqs, seq_ids, prefix_ids, counts, appended ? counts : nullptr, weights != 0, &w))
+        return fail(KVARN_ECAPACITY, "the workspace is too large");
+    *bytes = w.total;
+    return KVARN_OK;
+}
+
+kvarn_status kvarn_block_attend(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* seq_ids,
+                                const int32_t* prefix_ids, const int32_t* q_lens, const void* q, void* out,
+                                float softmax_scale, float* weights, void* workspace, size_t workspace_bytes, void* stream) {
+    kvarn_status st = check_call(c, layer, n_seqs, seq_ids, stream, false);
+    if (st) return st;
+    st = check_attention(c, layer, n_seqs, seq_ids, q_lens, nullptr, q, out, softmax_scale);
+    if (st) return st;
+    Workspace w;
+    st = check_attend(c, layer, n_seqs, seq_ids, prefix_ids, q_lens, nullptr, q, out, weights, workspace, workspace_bytes, &w);
+    if (st || n_seqs == 0) return st;
+    return run_attend(c, layer, n_seqs, seq_ids, prefix_ids, q_lens, q, out, softmax_scale, weights, workspace, w, stream);
+}
+
+kvarn_status kvarn_block_append_attend(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* seq_ids,
+                                       const int32_t* prefix_ids, const int32_t* n_tokens, const void* k, int64_t k_stride,
+                                       const void* v, int64_t v_stride, const void* q, void* out, float softmax_scale,
+                                       float* weights, void* workspace, size_t workspace_bytes, void* stream) {
+    kvarn_status st = check_call(c, layer, n_seqs, seq_ids, stream, true);
+    if (st) return st;
+    st = check_append(c, layer, n_seqs, seq_ids, n_tokens, k, v, k_stride, v_stride);
+    if (st) return st;
+    st = check_attention(c, layer, n_seqs, seq_ids, n_tokens, n_tokens, q, out, softmax_scale);
+    if (st) return st;
+    Workspace w;
+    st = check_attend(c, layer, n_seqs, seq_ids, prefix_ids, n_tokens, n_tokens, q, out, weights, workspace, workspace_bytes, &w);
+    if (st || n_seqs == 0) return st;
+    st = append(c, layer, n_seqs, seq_ids, n_tokens, k, v, k_stride, v_stride, stream);
+    if (st) return st;
+    return run_attend(c, layer, n_seqs, seq_ids, prefix_ids, n_tokens, q, out, softmax_scale, weights, workspace, w, stream);
+}
+
+kvarn_status kvarn_block_window_weights(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* seq_ids,
+                                        const int32_t* q_lens, const void* q, float softmax_scale, float* weights,
+                                        void* workspace, size_t workspace_bytes, void* stream) {
+    kvarn_status st = check_call(c, layer, n_seqs, seq_ids, stream, false);
+    if (st) return st;
+    if (!std::isfinite(softmax_scale * kLog2e)) return fail(KVARN_EINVAL, "softmax_scale must be finite, below 2^127");
+    if (n_seqs > 0 && !q_lens) return fail(KVARN_EINVAL, "no query counts");
+    static thread_local BlockWindowParams p;
+    static thread_local BlockWeighParams wp;
+    const int hkv = c->cfg.num_kv_heads;
+    int64_t rows = 0, units = 0, sums = 0;
+    p.n_seqs = p.smem_rows = 0;
+    for (int i = 0; i < n_seqs; ++i) {
+        const int64_t n = c->L(seq_ids[i], layer), m = q_lens[i];
+        if (m < 0 || m > n) return fail(KVARN_EINVAL, "a query count is negative or above the sequence's length");
+        if (m > kWindowTokens) return fail(KVARN_EINVAL, "more than 128 queries of a sequence");
+        if (m > 0) {
+            BlockWindowSeq& e = p.seqs[p.n_seqs];
+            BlockWeighSeq& s = wp.seqs[p.n_seqs++];
+            e.seq = s.seq = seq_ids[i];
+            e.n = (int32_t)n;
+            e.q_len = (int32_t)m;
+            e.q_row = (int32_t)rows;
+            e.rows = s.rows = (int32_t)m * c->r;
+            e.pad = s.pad = (e.rows + 7) / 8 * 8;
+            e.chunks = (e.rows + kWindowRows - 1) / kWindowRows;
+            e.tiles = s.tiles = tiles_of(n);
+            e.unit_begin = (int32_t)units;
+            e.unused = 0;
+            e.sum_begin = s.sum_begin = sums;
+            s.before = 0;
+            s.lse_row = -1;
+            p.smem_rows = std::max(p.smem_rows, std::min(kWindowRows, e.pad));
+            units += (int64_t)hkv * e.chunks * e.tiles;
+            sums += (int64_t)hkv * e.tiles * e.pad;
+        }
+        rows += m;
+        if (units >= 1ll << 31) return fail(KVARN_ECAPACITY, "2^31 tiles of 32 tokens or more in a call");
+    }
+    if (p.n_seqs == 0) return KVARN_OK;
+    if (!q || !aligned16(q)) return fail(KVARN_EINVAL, "q must be 16-byte aligned");
+    if (!weights) return fail(KVARN_EINVAL, "no weights");
+    Workspace w;
+    w.total = (size_t)sums * 8;
+    st = check_beside(c, rows, q, nullptr, weights, workspace, workspace_bytes, w);
+    if (st || c->host_only) return st;
+    p.c = c->view;
+    p.c.layer = layer;
+    p.q = (const uint16_t*)q;
+    p.sums = (float2*)workspace;
+    p.hq = c->cfg.num_q_heads;
+    p.r = c->r;
+    p.units = units;
+    p.grid = (int32_t)std::min<int64_t>(c->sms, (units + 11) / 12);
+    p.scale_log2 = softmax_scale * kLog2e;
+    const int rc = launch_block_window(p, stream);
+    if (rc) return cuda_fail(rc, "window launch");
+    wp.sums = p.sums;
+    wp.pre_lse = nullptr;
+    wp.weights = weights;
+    wp.shift = 0.f;
+    wp.n_seqs = p.n_seqs;
+    return run_weigh(c, wp, stream);
+}
+
+kvarn_status kvarn_block_evict(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* seq_ids, int32_t keep,
+                               int32_t first, int32_t last, float* weights, int32_t* kept, void* stream) {
+    kvarn_status st = check_call(c, layer, n_seqs, seq_ids, stream, true);
+    if (st) return st;
+    if (first < 0 || last < 0 || keep < 0 || (int64_t)first + last > keep)
+        return fail(KVARN_EINVAL, "keep must be at least first + last, none of them negative");
+    if (n_seqs == 0) return KVARN_OK;
+    if (!weights || ((uintptr_t)weights & 3) || (keep > 0 && (!kept || ((uintptr_t)kept & 3))))
+        return fail(KVARN_EINVAL, "weights and kept must be 4-byte aligned");
+    if (meet(weights, (size_t)c->cfg.max_seqs * c->cfg.num_kv_heads * columns(c) * 4, kept,
+             (size_t)n_seqs * c->cfg.num_kv_heads * keep * 4))
+        return fail(KVARN_EINVAL, "weights and kept overlap");
+    static thread_local BlockEvictParams p;
+    const int bt = c->cfg.block_tokens;
+    p.n_seqs = 0;
+    for (int cut = 1; cut >= 0; --cut)  // those to cut come first
+        for (int i = 0, n = cut ? 0 : p.n_seqs; i < n_seqs; ++i) {
+            const int32_t full = c->L(seq_ids[i], layer) / bt;
+            if ((full > keep) != (cut == 1)) continue;
+            p.seqs[n++] = BlockEvictSeq{seq_ids[i], full, i};
+            if (cut) p.n_seqs = n;
+        }
+    p.n_all = n_seqs;
+    st = ensure_init(c, stream);
+    if (st) return st;
+    if (!c->host_only) {
+        p.c = c->view;
+        p.c.layer = layer;
+        p.weights = weights;
+        p.kept = kept;
+        p.keep = keep;
+        p.first = first;
+        p.last = last;
+        p.cols = (int32_t)columns(c);
+        const int rc = launch_block_evict(p, stream);
+        if (rc) return cuda_fail(rc, "evict launch");
+    }
+    for (int i = 0; i < p.n_seqs; ++i) {
+        int32_t* t = c->T(p.seqs[i].seq, layer);
+        for (int b = p.seqs[i].full - 1; b >= keep; --b) {
+            c->free_slots.push_back(t[b]);
+            t[b] = -1;
+        }
+        c->L(p.seqs[i].seq, layer) -= (p.seqs[i].full - keep) * bt;
+    }
+    return KVARN_OK;
+}
+
 kvarn_status kvarn_block_release(kvarn_block_cache* c, int32_t n_seqs, const int32_t* seq_ids) {
     if (!c || n_seqs < 0 || (n_seqs > 0 && !seq_ids)) return fail(KVARN_EINVAL, "bad sequence list");
     for (int i = 0; i < n_seqs; ++i)
@@ -586,6 +984,15 @@ kvarn_status kvarn_qk_norm_rope(const kvarn_qk_config* cfg, int64_t n_tokens, co
                                 int64_t k_stride, const float* q_weight, const float* k_weight, const int32_t* positions,
                                 const double* freqs, void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride,
                                 void* stream) {
+    return kvarn_qk_norm_rope_axes(cfg, n_tokens, q, q_stride, k, k_stride, q_weight, k_weight, positions, 0, 1, nullptr,
+                                   freqs, q_out, q_out_stride, k_out, k_out_stride, stream);
+}
+
+kvarn_status kvarn_qk_norm_rope_axes(const kvarn_qk_config* cfg, int64_t n_tokens, const void* q, int64_t q_stride,
+                                     const void* k, int64_t k_stride, const float* q_weight, const float* k_weight,
+                                     const int32_t* positions, int64_t axis_stride, int32_t n_axes, const uint8_t* axes,
+                                     const double* freqs, void* q_out, int64_t q_out_stride, void* k_out,
+                                     int64_t k_out_stride, void* stream) {
     if (!cfg) return fail(KVARN_EINVAL, "no configuration");
     const int64_t hq = cfg->num_q_heads, hk = cfg->num_kv_heads, d = cfg->head_dim;
     if (hq < 0 || hk < 0 || hq + hk < 1 || hq + hk > (1 << 16)) return fail(KVARN_EINVAL, "bad head counts");
@@ -619,7 +1026,17 @@ kvarn_status kvarn_qk_norm_rope(const kvarn_qk_config* cfg, int64_t n_tokens, co
     if (hq > 0 && hk > 0 && rows_meet(out[0], out[1], n_tokens)) return fail(KVARN_EINVAL, "the outputs overlap");
     if (cfg->rot_dim > 0 && (!positions || !freqs)) return fail(KVARN_EINVAL, "no positions or frequencies");
     if (!aligned16(q_weight) || !aligned16(k_weight)) return fail(KVARN_EINVAL, "weights must be 16-byte aligned");
+    if (n_axes < 1 || n_axes > 255) return fail(KVARN_EINVAL, "1 to 255 axes of positions");
+    if (axis_stride < 0 || axis_stride > (1ll << 48)) return fail(KVARN_EINVAL, "bad stride between axes");
+    if (n_axes > 1 && cfg->rot_dim > 0 && !axes) return fail(KVARN_EINVAL, "several axes, but no axis for each pair");
     QkParams p;
+    p.several = axes && n_axes > 1;
+    p.axis_stride = axis_stride;
+    std::memset(p.axes, 0, sizeof(p.axes));
+    for (int i = 0; axes && i < cfg->rot_dim / 2; ++i) {
+        if (axes[i] >= n_axes) return fail(KVARN_EINVAL, "a pair's axis is out of range");
+        p.axes[i / 4] |= (uint32_t)axes[i] << 8 * (i % 4);
+    }
     p.q = (const uint16_t*)q;
     p.k = (const uint16_t*)k;
     p.q_out = (uint16_t*)q_out;

@@ -44,7 +44,6 @@ static_assert(2 * kRegsSoftmax + kRegsExpand + kRegsIssue <= 4 * kRegsLaunch, "r
 constexpr uint32_t kColS = 0, kColO = 256;
 constexpr int kStep = 128;  // keys of a step
 constexpr float kRaise = 8.f, kShift = 7.f;  // m is raised when it would grow by more; weights are at most 2^(both)
-#define kNegInf (-__int_as_float(0x7f800000))
 
 // feed: segments handed to the roles
 constexpr int kFeed = 8;
@@ -128,7 +127,8 @@ __device__ __forceinline__ float max32(const uint32_t (&r)[32]) {
 
 // ---- the line of steps ----
 // Steps of a query tile pair: up to the last position that its queries see.
-__device__ __forceinline__ int pair_steps(const BlockPrefillSeq& e, int pair, int pair_tokens) {
+__device__ __forceinline__ int pair_steps(const BlockPrefillParams& p, const BlockPrefillSeq& e, int pair, int pair_tokens) {
+    if (p.flat) return (e.n - 1) / kStep + 1;
     return (e.n - e.q_len + min((pair + 1) * pair_tokens, e.q_len) - 1) / kStep + 1;
 }
 
@@ -145,7 +145,7 @@ struct LineWalk {
     Seg s;
     __device__ __forceinline__ void set() {
         const BlockPrefillSeq& e = p.seqs[s.i];
-        s.steps = pair_steps(e, s.pair, pt);
+        s.steps = pair_steps(p, e, s.pair, pt);
         s.j1 = left > 0 ? min(s.steps, s.j0 + left) : 0;
         s.two = (2 * s.pair + 1) * (pt / 2) < e.q_len;
     }
@@ -161,7 +161,7 @@ struct LineWalk {
         rel -= s.kvh * e.head_steps;
         s.pair = e.pairs - 1;
 #pragma unroll 1
-        while (rel >= (n = pair_steps(e, s.pair, pt))) rel -= n, --s.pair;
+        while (rel >= (n = pair_steps(p, e, s.pair, pt))) rel -= n, --s.pair;
         s.j0 = rel;
         left = u1 - u0;
         set();
@@ -565,7 +565,7 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, uint8_
         const int tok = (2 * w.s.pair + b) * tpt + tok_in;
         const bool valid = tok_in < tpt && tok < e.q_len;
         const int row = valid ? (e.q_row + tok) * p.hq + w.s.kvh * p.r + head_in : -1;  // of q and out
-        const int pos = valid ? e.n - e.q_len + tok : e.n - 1;
+        const int pos = valid && !p.flat ? e.n - e.q_len + tok : e.n - 1;
         float qs = scale;
         {
             // D / 8 lanes a row; loops stay short: this code runs once a segment, from a cold cache
@@ -704,8 +704,33 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, uint8_
         auto take = [&](int piece, int k) {  // 16 bytes of row 4 k + lane / 8
             return *reinterpret_cast<const uint4*>(rows + piece * Sh::kAtom + swz(4 * k + (lane >> 3), lane & 7));
         };
-        if (w.whole()) {
-            const float inv = l == 0.f ? 0.f : 1.f / l;
+        const bool whole = w.whole();
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        if (whole && !p.flat) {
+            const bool merged = p.pre_lse && (p.merged[w.s.i >> 5] >> (w.s.i & 31) & 1);
+            if (merged) {  // the finished rows over the shared prefix, in units of O
+                float2 f = make_float2(1.f, 0.f);
+                if (valid) f = merge_factors(lse_of(m, l, kShift), p.pre_lse[row]);
+                const float scale_o = kDenomUnit * inv * f.x;
+#pragma unroll 1
+                for (int ch = 0; ch < D / 32; ++ch) {
+                    uint32_t x[32];
+                    tm_ld32(to + 32 * ch, x);
+                    tm_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (valid) y = *reinterpret_cast<const float4*>(p.pre_o + (size_t)row * D + 32 * ch + 4 * k);
+                        x[4 * k] = __float_as_uint(fmaf(__uint_as_float(x[4 * k]), scale_o, y.x * f.y));
+                        x[4 * k + 1] = __float_as_uint(fmaf(__uint_as_float(x[4 * k + 1]), scale_o, y.y * f.y));
+                        x[4 * k + 2] = __float_as_uint(fmaf(__uint_as_float(x[4 * k + 2]), scale_o, y.z * f.y));
+                        x[4 * k + 3] = __float_as_uint(fmaf(__uint_as_float(x[4 * k + 3]), scale_o, y.w * f.y));
+                    }
+                    tm_st32(to + 32 * ch, x);
+                }
+                tm_wait_st();
+            }
+            const float unit = merged ? 1.f : kDenomUnit, times = merged ? 1.f : inv;
 #pragma unroll 1
             for (int piece = 0; piece < D / 64; ++piece) {
                 uint32_t x[2][32], o[32];
@@ -714,8 +739,8 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, uint8_
                 tm_wait_ld();
 #pragma unroll
                 for (int k = 0; k < 32; ++k)
-                    o[k] = pack2<BF16>(__uint_as_float(x[k >> 4][2 * k & 31]) * kDenomUnit * inv,
-                                       __uint_as_float(x[k >> 4][(2 * k & 31) + 1]) * kDenomUnit * inv);
+                    o[k] = pack2<BF16>(__uint_as_float(x[k >> 4][2 * k & 31]) * unit * times,
+                                       __uint_as_float(x[k >> 4][(2 * k & 31) + 1]) * unit * times);
                 give(piece, o);
             }
             __syncwarp();
@@ -732,30 +757,38 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, uint8_
                 __syncwarp();  // the row is there
                 if (valid) add_non_finite<D, BF16>(p.c, e, w.s.kvh, 0, pos + 1, p.out + (size_t)row * D, nullptr);
             }
-        } else {
+        } else {  // fp32 rows: a part of the segment to the workspace, or a finished row over a shared prefix
             float* part = reinterpret_cast<float*>(p.c.base + p.c.lay.partials) +
                           (size_t)(2 * blockIdx.x + (w.s.j0 == 0 ? 1 : 0)) * (256 * (D + 2));
-            const int first = 128 * b + (et & 96);
-            if (__any_sync(0xffffffffu, row >= 0)) {  // (rows without a query are not read back)
+            const int to_row = whole ? row : 128 * b + et;  // -1: a row without a query (of a part it is not read back)
+            float* dst = whole ? p.pre_o : part;
+            const float times = whole ? kDenomUnit * inv : 1.f;
+            if (__any_sync(0xffffffffu, row >= 0)) {
 #pragma unroll 1
                 for (int ch = 0; ch < D / 32; ++ch) {
                     uint32_t x[32];
                     tm_ld32(to + 32 * ch, x);
                     tm_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * times);
                     give(0, x);
                     __syncwarp();
 #pragma unroll 4
                     for (int k = 0; k < 8; ++k) {
-                        const int rr = first + 4 * k + (lane >> 3);
-                        *reinterpret_cast<uint4*>(part + (size_t)rr * D + 32 * ch + 4 * (lane & 7)) = take(0, k);
+                        const int rr = __shfl_sync(0xffffffffu, to_row, 4 * k + (lane >> 3));
+                        if (rr >= 0) *reinterpret_cast<uint4*>(dst + (size_t)rr * D + 32 * ch + 4 * (lane & 7)) = take(0, k);
                     }
                     __syncwarp();
                 }
                 if (__builtin_expect(bad, 0) && valid)
                     add_non_finite<D, BF16>(p.c, e, w.s.kvh, w.s.j0 * kStep, min(pos + 1, w.s.j1 * kStep), nullptr,
-                                            part + (size_t)(128 * b + et) * D);
-                part[256 * D + 128 * b + et] = m;
-                part[256 * D + 256 + 128 * b + et] = l;
+                                            dst + (size_t)to_row * D);
+                if (!whole) {
+                    part[256 * D + 128 * b + et] = m;
+                    part[256 * D + 256 + 128 * b + et] = l;
+                } else if (valid) {
+                    p.pre_lse[row] = lse_of(m, l, kShift);
+                }
             }
         }
         __syncwarp();
@@ -884,10 +917,20 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_c
         }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l, y = kDenomUnit;
-    const size_t row = ((size_t)(e.q_row + tok) * p.hq + w.s.kvh * p.r + et % p.r) * D;
-    if (live)
-        *reinterpret_cast<uint2*>(p.out + row + 4 * lane) =
-            make_uint2(pack2<BF16>(o.x * y * inv, o.y * y * inv), pack2<BF16>(o.z * y * inv, o.w * y * inv));
+    const size_t at = (size_t)(e.q_row + tok) * p.hq + w.s.kvh * p.r + et % p.r, row = at * D;
+    o = make_float4(o.x * y * inv, o.y * y * inv, o.z * y * inv, o.w * y * inv);
+    if (p.flat) {
+        if (live) *reinterpret_cast<float4*>(p.pre_o + row + 4 * lane) = o;
+        if (lane == 0) p.pre_lse[at] = lse_of(big, l, kShift);
+        return;
+    }
+    if (p.pre_lse && (p.merged[w.s.i >> 5] >> (w.s.i & 31) & 1)) {
+        const float2 f = merge_factors(lse_of(big, l, kShift), p.pre_lse[at]);
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (live) x = *reinterpret_cast<const float4*>(p.pre_o + row + 4 * lane);
+        o = make_float4(merge(o.x, x.x, f), merge(o.y, x.y, f), merge(o.z, x.z, f), merge(o.w, x.w, f));
+    }
+    if (live) *reinterpret_cast<uint2*>(p.out + row + 4 * lane) = make_uint2(pack2<BF16>(o.x, o.y), pack2<BF16>(o.z, o.w));
 }
 
 template <int D, bool INT8, bool BF16>

@@ -2,6 +2,7 @@
 // pass (the cache takes post-rotation keys and queries).
 //   y_d = x_d rsqrt(mean x^2 + eps) w_d;  pairs (y_i, y_{i+R/2}) or (y_2i, y_{2i+1}) turned
 //   by position * freq_i; channels from R on pass through. fp32 throughout, one rounding.
+// With several axes of positions (time, height, width ..) pair i takes the position of its own axis.
 //
 // Norm, weight and rotation are one linear map of a pair: out = rsqrt(..) (y c + partner s), with
 // c and s (cos, sin times the weights) made once for all heads of a token that an item holds.
@@ -123,9 +124,11 @@ __global__ void __launch_bounds__(kQkThreads, MODE == kAny ? 4 : kQkCtas) qk_ker
                 }
                 float cs[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {};
                 if (turned) {
-                    const int64_t pos = p.positions[tok];
+                    int64_t pos = p.positions[tok];
+                    const uint32_t axes = p.several ? p.axes[l] : 0;  // of the lane's four pairs, a byte each
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
+                        if (p.several) pos = p.positions[tok + (int64_t)(axes >> 8 * i & 255) * p.axis_stride];
                         const int32_t top = (int32_t)((turns(p.freqs[4 * l + i]) * (uint64_t)pos) >> 32);
                         sincospif((float)top * 4.656612873077393e-10f, &sn[i], &cs[i]);  // top 2^-32 turns, 2 to a pi
                     }

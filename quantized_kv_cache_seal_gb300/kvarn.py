@@ -34,7 +34,8 @@ EXPORTS = [
     "kvarn_block_required_bytes", "kvarn_block_create", "kvarn_block_destroy", "kvarn_block_append",
     "kvarn_block_read", "kvarn_block_decode_attention", "kvarn_block_decode_step", "kvarn_block_prefill_attention",
     "kvarn_block_prefill", "kvarn_block_release", "kvarn_block_length", "kvarn_block_check_device_error",
-    "kvarn_qk_norm_rope",
+    "kvarn_qk_norm_rope", "kvarn_qk_norm_rope_axes", "kvarn_block_attend_workspace", "kvarn_block_attend",
+    "kvarn_block_append_attend", "kvarn_block_window_weights", "kvarn_block_evict",
 ]
 
 
@@ -135,6 +136,13 @@ def load(build_if_missing: bool = True):
     L.kvarn_block_length.argtypes = [P, I32, I32, ctypes.POINTER(I64)]
     L.kvarn_block_check_device_error.argtypes = [P, P]
     L.kvarn_qk_norm_rope.argtypes = [ctypes.POINTER(kvarn_qk_config), I64, P, I64, P, I64, P, P, P, P, P, I64, P, I64, P]
+    L.kvarn_qk_norm_rope_axes.argtypes = [ctypes.POINTER(kvarn_qk_config), I64, P, I64, P, I64, P, P, P, I64, I32,
+                                          ctypes.c_char_p, P, P, I64, P, I64, P]
+    L.kvarn_block_attend_workspace.argtypes = [P, I32, I32, IP, IP, IP, I32, I32, ctypes.POINTER(SZ)]
+    L.kvarn_block_attend.argtypes = [P, I32, I32, IP, IP, IP, P, P, F, P, P, SZ, P]
+    L.kvarn_block_append_attend.argtypes = [P, I32, I32, IP, IP, IP, P, I64, P, I64, P, P, F, P, P, SZ, P]
+    L.kvarn_block_window_weights.argtypes = [P, I32, I32, IP, IP, P, F, P, P, SZ, P]
+    L.kvarn_block_evict.argtypes = [P, I32, I32, IP, I32, I32, I32, P, P, P]
     for name in EXPORTS:
         fn = getattr(L, name)
         if fn.restype is ctypes.c_int:  # default: status enum
@@ -477,3 +485,56 @@ def kvarn_qk_norm_rope(cfg: kvarn_qk_config, n_tokens, q, q_stride, k, k_stride,
                                          _ptr(q_weight), _ptr(k_weight), _ptr(positions), _ptr(freqs), _ptr(q_out),
                                          q_out_stride, _ptr(k_out), k_out_stride, _stream(stream)),
                "kvarn_qk_norm_rope")
+
+
+def kvarn_qk_norm_rope_axes(cfg: kvarn_qk_config, n_tokens, q, q_stride, k, k_stride, q_weight, k_weight, positions,
+                            axis_stride, n_axes, axes, freqs, q_out, q_out_stride, k_out, k_out_stride, stream=None):
+    """axes: bytes, one a pair of channels."""
+    if axes is not None and len(axes) != cfg.rot_dim // 2:
+        raise ValueError(f"{cfg.rot_dim // 2} pairs, but {len(axes)} axes")
+    _check_why(load().kvarn_qk_norm_rope_axes(ctypes.byref(cfg), n_tokens, _ptr(q), q_stride, _ptr(k), k_stride,
+                                              _ptr(q_weight), _ptr(k_weight), _ptr(positions), axis_stride, n_axes, axes,
+                                              _ptr(freqs), _ptr(q_out), q_out_stride, _ptr(k_out), k_out_stride,
+                                              _stream(stream)), "kvarn_qk_norm_rope_axes")
+
+
+def _optional(xs, seq_ids):
+    return None if xs is None else _counts(xs, seq_ids)
+
+
+def kvarn_block_attend_workspace(handle, layer, seq_ids, prefix_ids, counts, appended=False, weights=False) -> int:
+    n = ctypes.c_size_t()
+    _check_why(load().kvarn_block_attend_workspace(handle, layer, len(seq_ids), _i32(seq_ids),
+                                                   _optional(prefix_ids, seq_ids), _optional(counts, seq_ids),
+                                                   int(bool(appended)), int(bool(weights)), ctypes.byref(n)),
+               "kvarn_block_attend_workspace")
+    return n.value
+
+
+def kvarn_block_attend(handle, layer, seq_ids, prefix_ids, q_lens, q, out, softmax_scale, weights, workspace,
+                       workspace_bytes, stream=None):
+    _check_why(load().kvarn_block_attend(handle, layer, len(seq_ids), _i32(seq_ids), _optional(prefix_ids, seq_ids),
+                                         _optional(q_lens, seq_ids), _ptr(q), _ptr(out), float(softmax_scale),
+                                         _ptr(weights), _ptr(workspace), workspace_bytes, _stream(stream)),
+               "kvarn_block_attend")
+
+
+def kvarn_block_append_attend(handle, layer, seq_ids, prefix_ids, n_tokens, k, k_stride, v, v_stride, q, out,
+                              softmax_scale, weights, workspace, workspace_bytes, stream=None):
+    _check_why(load().kvarn_block_append_attend(handle, layer, len(seq_ids), _i32(seq_ids),
+                                                _optional(prefix_ids, seq_ids), _counts(n_tokens, seq_ids), _ptr(k),
+                                                k_stride, _ptr(v), v_stride, _ptr(q), _ptr(out), float(softmax_scale),
+                                                _ptr(weights), _ptr(workspace), workspace_bytes, _stream(stream)),
+               "kvarn_block_append_attend")
+
+
+def kvarn_block_window_weights(handle, layer, seq_ids, q_lens, q, softmax_scale, weights, workspace, workspace_bytes,
+                               stream=None):
+    _check_why(load().kvarn_block_window_weights(handle, layer, len(seq_ids), _i32(seq_ids), _counts(q_lens, seq_ids),
+                                                 _ptr(q), float(softmax_scale), _ptr(weights), _ptr(workspace),
+                                                 workspace_bytes, _stream(stream)), "kvarn_block_window_weights")
+
+
+def kvarn_block_evict(handle, layer, seq_ids, keep, first, last, weights, kept, stream=None):
+    _check_why(load().kvarn_block_evict(handle, layer, len(seq_ids), _i32(seq_ids), keep, first, last, _ptr(weights),
+                                        _ptr(kept), _stream(stream)), "kvarn_block_evict")

@@ -3,7 +3,7 @@
 from __future__ import annotations
 
 import functools
-from typing import Optional
+from typing import Optional, Sequence
 
 import torch
 
@@ -37,14 +37,24 @@ def _config(hq, hkv, dim, rot, interleaved, in_type, out_type, eps):
     return K.kvarn_qk_config(hq, hkv, dim, rot, interleaved, in_type, out_type, eps)
 
 
+@functools.lru_cache(maxsize=64)
+def _axes(axes, pairs, count):
+    """One axis a pair, each below `count`, as the bytes that the library takes."""
+    if len(axes) != pairs or not all(0 <= a < count for a in axes) or not 1 <= count <= 255:
+        raise ValueError(f"axes must be {pairs} numbers from 0 to {count - 1} (1 to 255 axes), got {axes}")
+    return bytes(axes)
+
+
 def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, freqs: torch.Tensor,
                  q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
                  interleaved: bool = False, dtype: Optional[torch.dtype] = None, q_out: Optional[torch.Tensor] = None,
-                 k_out: Optional[torch.Tensor] = None, stream=None):
+                 k_out: Optional[torch.Tensor] = None, stream=None, axes: Optional[Sequence[int]] = None):
     """Normalise (where a weight is given) and rotate every head of q [T][Hq][D] and k [T][Hkv][D] (or None).
 
     positions: int32 [T]; freqs: float64 [R / 2], radians per position, R <= D a multiple of 8 (channels from R on
-    pass); weights: float32 [D]. q and k are fp16 or bf16 and may be parts of a packed projection (any stride between
+    pass); weights: float32 [D]. With ``axes`` (R / 2 ints, a tuple is quickest) positions are int32 [A][T], any
+    stride between the axes, and pair i turns by positions[axes[i]] freqs[i]: sections of an image's time, row and
+    column, or axes in turn, as the model has them. q and k are fp16 or bf16 and may be parts of a packed projection (any stride between
     tokens). Results are ``dtype`` (default: the inputs'; fp16 for a KVarN cache) or go to q_out and k_out, which
     may be q and k themselves. Returns (q, k); no gradient is recorded. A torch.cuda.Stream given as ``stream`` holds the
     tensors' memory until it is through with them; one given by its address does not."""
@@ -62,7 +72,13 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Te
         raise ValueError("k_out or k_weight without k")
     qs = _stride(q, "q", in_type, index, tokens, hq, dim)
     ks = 0 if k is None else _stride(k, "k", in_type, index, tokens, hkv, dim)
-    _table(positions, "positions", torch.int32, index, (tokens,))
+    if axes is None:
+        _table(positions, "positions", torch.int32, index, (tokens,))
+    else:
+        if positions.dim() != 2 or positions.shape[1] != tokens or positions.dtype is not torch.int32 or (
+                positions.get_device() != index or (tokens > 1 and positions.stride(1) != 1)):
+            _refuse("positions", positions, f"a torch.int32 tensor (axes, {tokens}) with dense rows on cuda:{index}")
+        axes = _axes(tuple(axes), freqs.numel(), positions.shape[0])
     _table(freqs, "freqs", torch.float64, index, (freqs.numel(),))
     if q_weight is not None:
         _table(q_weight, "q_weight", torch.float32, index, (dim,))
@@ -76,7 +92,11 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Te
             q_out = torch.empty((tokens, hq, dim), dtype=out_type, device=q.device)
         if k is not None and k_out is None:
             k_out = torch.empty((tokens, hkv, dim), dtype=out_type, device=q.device)
-        K.kvarn_qk_norm_rope(cfg, tokens, q, qs, k, ks, q_weight, k_weight, positions, freqs, q_out, qos, k_out, kos, s)
+        if axes is None:
+            K.kvarn_qk_norm_rope(cfg, tokens, q, qs, k, ks, q_weight, k_weight, positions, freqs, q_out, qos, k_out, kos, s)
+        else:
+            K.kvarn_qk_norm_rope_axes(cfg, tokens, q, qs, k, ks, q_weight, k_weight, positions, positions.stride(0),
+                                      positions.shape[0], axes, freqs, q_out, qos, k_out, kos, s)
         if stream is not None:
             K.hold(stream, q, k, positions, freqs, q_weight, k_weight, q_out, k_out)
     return q_out, k_out
