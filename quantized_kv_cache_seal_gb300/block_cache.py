@@ -41,7 +41,7 @@ class BlockCache:
         self.heads, self.kv_heads, self.dim = num_q_heads, num_kv_heads, head_dim
         self.scale = 1.0 / math.sqrt(head_dim)
         # places of the blocks' weights in a layer
-        self.weights_shape = (max_seqs, num_kv_heads, max(1, max_seq_len // max(1, block_tokens)) + 1)
+        self.weights_shape = (max_seqs, num_kv_heads, max_seq_len // max(1, block_tokens) + 1)
         self.nbytes = K.kvarn_block_required_bytes(self.cfg)
         self.mem = torch.empty(self.nbytes + 256, dtype=torch.uint8, device=device)
         self.device = self.mem.device

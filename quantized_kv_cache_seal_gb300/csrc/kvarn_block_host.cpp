@@ -298,7 +298,7 @@ struct Beside {
     float* weights = nullptr;          // decode: what the blocks have received, added to
 };
 
-size_t columns(const kvarn_block_cache* c) { return (size_t)c->view.max_blocks + 1; }
+size_t columns(const kvarn_block_cache* c) { return (size_t)(c->cfg.max_seq_len / c->cfg.block_tokens) + 1; }
 
 kvarn_status run_weigh(kvarn_block_cache* c, BlockWeighParams& p, void* stream) {
     p.hq = c->cfg.num_q_heads;

@@ -413,3 +413,19 @@ def test_other_streams():
     kept = c.evict(0, [0], want.clone(), 3, stream=torch.cuda.Stream())
     torch.cuda.synchronize()
     assert kept.shape == (1, 2, 3) and c.length(0, 0) == 3 * 32 + 12
+
+
+def test_sequences_shorter_than_a_block():
+    """One place of weights a (sequence, KV head) where no block can fill."""
+    c = make(max_seqs=2, block_tokens=128, max_seq_len=100)
+    k, _ = fill(c, [100, 33], torch.float16, 700)
+    q = tokens(4, 8, 128, torch.float16, 702, 0.3)
+    w = c.new_weights()[0]
+    assert w.shape == (2, 2, 1)
+    c.decode_attention(0, [0, 1], q[:2], weights=w)
+    assert bool(((w - 4).abs() < 2.0 ** -15).all())
+    c.window_weights(0, [0, 1], [2, 2], q, w)
+    assert bool(((w - 12).abs() < 2.0 ** -14).all())
+    before = w.clone()
+    assert not c.evict(0, [0, 1], w, 0, 0, 0).numel() and bool((c.evict(0, [0, 1], w, 2) == -1).all())
+    assert torch.equal(w, before) and c.length(0, 0) == 100
