@@ -415,12 +415,11 @@ kvarn_status kvarn_block_prefill(kvarn_block_cache* cache, int32_t layer, int32_
  * number above 0 (NaN or infinite logits, or none) add nothing. Only sequences of the call are touched, none of
  * their prefixes. Set a sequence's to 0 when it begins. Sums are fp32 in a fixed order: results repeat.
  *
- * Both want a workspace, 16-byte aligned, of the size that kvarn_block_attend_workspace gives; it belongs to the
+ * Both want a workspace, 16-byte aligned, of the size that a call of its own gives; it belongs to the
  * call until its work is done (a captured graph keeps it). */
 
 /* Bytes for a call with these arguments (counts: q_lens, or n_tokens if appended; NULL: one query each; weights != 0: with
- * weights). For kvarn_block_window_weights: 8 * num_kv_heads * sum over sequences of ceil(length / 32) * (q_lens[i] *
- * (num_q_heads / num_kv_heads) rounded up to a multiple of 8). */
+ * weights). */
 kvarn_status kvarn_block_attend_workspace(kvarn_block_cache* cache, int32_t layer, int32_t n_seqs, const int32_t* seq_ids,
                                           const int32_t* prefix_ids, const int32_t* counts, int32_t appended,
                                           int32_t weights, size_t* bytes);
@@ -439,6 +438,10 @@ kvarn_status kvarn_block_append_attend(kvarn_block_cache* cache, int32_t layer, 
                                        int64_t k_stride, const void* v, int64_t v_stride, const void* q, void* out,
                                        float softmax_scale, float* weights, void* workspace, size_t workspace_bytes,
                                        void* stream);
+
+/* Bytes for kvarn_block_window_weights with these arguments. */
+kvarn_status kvarn_block_window_workspace(kvarn_block_cache* cache, int32_t layer, int32_t n_seqs, const int32_t* seq_ids,
+                                          const int32_t* q_lens, size_t* bytes);
 
 /* Add the weights that the last q_lens[i] <= 128 tokens of each sequence give to its blocks, each over the tokens at
  * positions up to its own: what the end of a prompt needs of it. q: [sum(q_lens)][num_q_heads][head_dim], their queries.

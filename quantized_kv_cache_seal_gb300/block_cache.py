@@ -40,6 +40,7 @@ class BlockCache:
         self.dtype = dtype
         self.heads, self.kv_heads, self.dim = num_q_heads, num_kv_heads, head_dim
         self.scale = 1.0 / math.sqrt(head_dim)
+        self._tiles = (max_seq_len + 31) // 32
         # places of the blocks' weights in a layer
         self.weights_shape = (max_seqs, num_kv_heads, max_seq_len // max(1, block_tokens) + 1)
         self.nbytes = K.kvarn_block_required_bytes(self.cfg)
@@ -140,16 +141,20 @@ class BlockCache:
 
     def _attend(self, layer, seq_ids, prefix_ids, counts, q, out, scale, weights, stream, k=None, ks=0, v=None, vs=0):
         """The calls with prefixes or weights; counts: queries of each sequence (None: one), or tokens to append if k."""
-        if prefix_ids is not None:
-            _same_length(seq_ids, prefix_ids)
+        if prefix_ids is not None and None in prefix_ids:
             prefix_ids = [-1 if x is None else x for x in prefix_ids]
         if weights is not None:
             self._weights(weights)
+        # what the workspace takes at most; where that is much, what it takes
+        n = 0 if prefix_ids is None else 4 * q.numel() + 4 * self.heads * q.shape[0] + 512
+        if weights is not None:
+            n += 8 * self.heads * len(seq_ids) * (1 + self._tiles * (1 if prefix_ids is None else 2)) + 512
         with K.on_device(self.device, stream) as s:
             if out is None:
                 out = torch.empty_like(q)
-            n = K.kvarn_block_attend_workspace(self.handle, layer, seq_ids, prefix_ids, counts, k is not None,
-                                               weights is not None)
+            if n > 1 << 25:
+                n = K.kvarn_block_attend_workspace(self.handle, layer, seq_ids, prefix_ids, counts, k is not None,
+                                                   weights is not None)
             # of this stream's memory: free for the stream's later work once the call is enqueued
             space = torch.empty(n, dtype=torch.uint8, device=self.device) if n else None
             scale = self.scale if scale is None else scale
@@ -234,10 +239,8 @@ class BlockCache:
         _same_length(seq_ids, q_lens)
         self._dense(q, sum(q_lens), "q")
         self._weights(weights)
-        r = self.heads // self.kv_heads
         with K.on_device(self.device, stream) as s:
-            n = 8 * self.kv_heads * sum(-(-K.kvarn_block_length(self.handle, layer, i) // 32) * (-(-m * r // 8) * 8)
-                                        for i, m in zip(seq_ids, q_lens))
+            n = K.kvarn_block_window_workspace(self.handle, layer, seq_ids, q_lens)
             space = torch.empty(n, dtype=torch.uint8, device=self.device) if n else None
             K.kvarn_block_window_weights(self.handle, layer, seq_ids, q_lens, q, self.scale if scale is None else scale,
                                          weights, space, n, s)

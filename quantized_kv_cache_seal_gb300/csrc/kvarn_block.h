@@ -111,6 +111,7 @@ struct BlockDecodeParams {
     int64_t units;
     float scale_log2;          // softmax scale * log2(e)
     float2* sums;              // [units][r] or null: maximum and sum of each tile's weights, by head
+    float2* totals;            // [rows][Hq] (with sums): of each row over all its keys, a prefix's among them
     const float *pre_o, *pre_lse;  // rows finished over shared prefixes (pre_lse null: none), [rows][Hq][D] and [rows][Hq]
     uint32_t merged[kBlockMaxSeqs / 32];  // bit i: sequence entry i takes its row from there
     BlockDecodeSeq seqs[kBlockMaxSeqs];
@@ -142,36 +143,40 @@ struct BlockWindowSeq {
     int32_t seq, n, q_len, q_row;
     int32_t rows;        // q_len * r
     int32_t pad;         // rows rounded up to 8
-    int32_t chunks;      // of kWindowRows rows
-    int32_t tiles;       // of its tokens
-    int32_t unit_begin;  // prefix of Hkv * chunks * tiles
-    int32_t unused;
+    int32_t row_tiles;   // of 128 rows
+    int32_t steps;       // of 128 of its tokens
+    int32_t unit_begin;  // prefix of Hkv * row_tiles * steps
+    int32_t pair_begin;  // prefix of Hkv * row_tiles
     int64_t sum_begin;   // prefix of Hkv * tiles * pad
 };
 struct BlockWindowParams {
     BlockView c;
     const uint16_t* q;
     float2* sums;        // of each sequence [Hkv][tiles][pad]: a tile's maximum and sum, by row
-    int32_t n_seqs, hq, r, grid, smem_rows;
+    float2* totals;      // [pairs + grid][2][128]: a row's maximum and sum over part of its tokens
+    int32_t n_seqs, hq, r, grid;
     int64_t units;
     float scale_log2;
     BlockWindowSeq seqs[kBlockMaxSeqs];
 };
-constexpr int kWindowRows = 512;
 
 // Adds the tiles' weights to what their blocks have received.
 struct BlockWeighSeq {
     int32_t seq, rows, pad;   // rows of a KV head, and places for them in a tile's sums
     int32_t before, tiles;    // tiles of a prefix in front, its own
-    int32_t lse_row;          // of pre_lse, -1 for none
+    int32_t row;              // decode: of totals
+    int32_t unit_begin, pair_begin;  // window: as there
     int64_t sum_begin;
 };
 struct BlockWeighParams {
     const float2* sums;
-    const float* pre_lse;     // [rows][Hq]
+    const float2* totals;     // decode (grid 0): [rows][Hq]; window: as there
     float* weights;           // [max_seqs][Hkv][cols]
-    float shift;              // of the maxima against log2 of the sums: 2^(m - shift) sum are the tile's 2^logits
+    int64_t units;            // of the window's line
+    int32_t grid;
     int32_t n_seqs, hq, hkv, log2_tiles, cols;  // tiles of a block; places of a (sequence, KV head)
+    int32_t lanes, blocks;    // lanes that add up a block, blocks of a CTA
+    int32_t most;             // CTAs of a (sequence, KV head)
     BlockWeighSeq seqs[kBlockMaxSeqs];
 };
 

@@ -303,6 +303,11 @@ __device__ void join_heads(const BlockDecodeParams& p, const uint8_t* smem, cons
     auto give = [&](int head, float4 o, float m, float l) {
         const float inv = l == 0.f ? 0.f : 1.f / l, u = kDenomUnit;
         float4 y = make_float4(o.x * u * inv, o.y * u * inv, o.z * u * inv, o.w * u * inv);
+        if (p.totals && lane == 0) {  // a prefix's 2^lse in units of l
+            float2 t = make_float2(m, l);
+            if (merged) t = joined(t, make_float2(p.pre_lse[row + head] + (kShift - 12.f), 1.f));
+            p.totals[row + head] = t;
+        }
         if (merged) {  // with the finished row over the shared prefix
             const float2 f = merge_factors(lse_of(m, l, kShift), p.pre_lse[row + head]);
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);

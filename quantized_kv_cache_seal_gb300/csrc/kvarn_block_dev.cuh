@@ -183,6 +183,15 @@ __device__ __forceinline__ float2 merge_factors(float a, float b) {
 }
 __device__ __forceinline__ float merge(float a, float b, float2 f) { return fmaf(a, f.x, b * f.y); }
 
+// Sums as a maximum and what is over it, 2^x y: two of them as one. (With a maximum of -inf y is 0 or NaN.)
+__device__ __forceinline__ float2 joined(float2 a, float2 b) {
+    const float top = fmaxf(a.x, b.x);
+    float f, g;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(a.x - top));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(g) : "f"(b.x - top));
+    return make_float2(top, a.y * (a.x == kNegInf ? 1.f : f) + b.y * (b.x == kNegInf ? 1.f : g));
+}
+
 // Bytes of a 4 x 4 square: r[i] = row i; afterwards r[j] = column j.
 __device__ __forceinline__ void transpose4(uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
     const uint32_t a = __byte_perm(r0, r1, 0x5140), b = __byte_perm(r0, r1, 0x7362);

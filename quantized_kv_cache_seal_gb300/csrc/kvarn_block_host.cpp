@@ -44,7 +44,6 @@ kvarn_status cuda_fail(int rc, const char* what) {
     return fail(KVARN_ECUDA, text);
 }
 
-constexpr float kDecodeShift = 3.f;  // of the decode kernel's tile maxima (2^(15 - 12))
 constexpr int kWindowTokens = 128;   // queries of a sequence in window_weights
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -294,7 +293,7 @@ struct Beside {
     const int32_t* before = nullptr;   // decode: a prefix whose tokens come first in the sequence's line, -1 for none
     const uint8_t* finished = nullptr; // 1: its rows over a prefix are in pre_o and pre_lse
     float *pre_o = nullptr, *pre_lse = nullptr;
-    float2* sums = nullptr;            // decode: the tiles' sums
+    float2 *sums = nullptr, *totals = nullptr;  // decode: the tiles' sums, the rows'
     float* weights = nullptr;          // decode: what the blocks have received, added to
 };
 
@@ -305,6 +304,14 @@ kvarn_status run_weigh(kvarn_block_cache* c, BlockWeighParams& p, void* stream) 
     p.hkv = c->cfg.num_kv_heads;
     p.log2_tiles = c->view.log2_block - 5;
     p.cols = (int32_t)columns(c);
+    // Lanes enough for a block's sums two at a time; of blocks two rounds of 256 threads a CTA, so that there are many
+    // CTAs and the rows' totals are still shared by some blocks.
+    int32_t pad = 1, tiles = 1;
+    for (int i = 0; i < p.n_seqs; ++i) pad = std::max(pad, p.seqs[i].pad), tiles = std::max(tiles, p.seqs[i].tiles);
+    p.lanes = 1;
+    while (p.lanes < 32 && p.lanes * 2 < pad << p.log2_tiles) p.lanes *= 2;
+    p.blocks = 2 * 256 / p.lanes;
+    p.most = (((tiles - 1) >> p.log2_tiles) + p.blocks) / p.blocks;
     const int rc = launch_block_weigh(p, stream);
     return rc ? cuda_fail(rc, "weights launch") : KVARN_OK;
 }
@@ -333,6 +340,7 @@ kvarn_status run_decode(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, con
     }
     p.units = units;
     p.sums = beside.sums;
+    p.totals = beside.totals;
     p.pre_o = beside.pre_o;
     p.pre_lse = beside.pre_lse;
     mark(p.merged, beside.finished, n_seqs);
@@ -349,9 +357,9 @@ kvarn_status run_decode(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, con
     if (!beside.weights) return KVARN_OK;
     static thread_local BlockWeighParams wp;
     wp.sums = beside.sums;
-    wp.pre_lse = beside.pre_lse;
+    wp.totals = beside.totals;
     wp.weights = beside.weights;
-    wp.shift = kDecodeShift;
+    wp.units = wp.grid = 0;
     wp.n_seqs = n_seqs;
     for (int i = 0; i < n_seqs; ++i) {
         const BlockDecodeSeq& e = p.seqs[i];
@@ -360,7 +368,8 @@ kvarn_status run_decode(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, con
         s.rows = s.pad = c->r;
         s.before = tiles_of(e.pre_n);
         s.tiles = e.units - s.before;
-        s.lse_row = beside.finished && beside.finished[i] ? i : -1;
+        s.row = i;
+        s.unit_begin = s.pair_begin = 0;
         s.sum_begin = (int64_t)e.unit_begin * c->r;
     }
     return run_weigh(c, wp, stream);
@@ -486,7 +495,7 @@ kvarn_status check_prefixes(kvarn_block_cache* c, int32_t layer, int32_t n_seqs,
 
 // The parts of an attention call's workspace.
 struct Workspace {
-    size_t pre_o = 0, pre_lse = 0, sums = 0, total = 0;
+    size_t pre_o = 0, pre_lse = 0, sums = 0, totals = 0, total = 0;
 };
 bool make_workspace(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* ids, const int32_t* prefix_ids,
                     const int32_t* q_lens, const int32_t* added, bool weights, Workspace* w) {
@@ -506,6 +515,7 @@ bool make_workspace(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const i
     w->pre_o = take(any ? rows * c->cfg.num_q_heads * c->cfg.head_dim * 4 : 0);
     w->pre_lse = take(any ? rows * c->cfg.num_q_heads * 4 : 0);
     w->sums = take(weights ? tiles * c->cfg.num_q_heads * 8 : 0);
+    w->totals = take(weights ? rows * c->cfg.num_q_heads * 8 : 0);
     w->total = (size_t)off;
     return off < (unsigned __int128)1 << 46;
 }
@@ -542,6 +552,43 @@ kvarn_status check_attend(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, c
     int64_t rows = 0;
     for (int i = 0; i < n_seqs; ++i) rows += q_lens ? q_lens[i] : 1;
     return check_beside(c, rows, q, out, weights, workspace, bytes, *w);
+}
+
+// The line of a window_weights call and its workspace.
+kvarn_status plan_window(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* ids, const int32_t* q_lens,
+                         BlockWindowParams& p, Workspace* w) {
+    const int hkv = c->cfg.num_kv_heads;
+    int64_t rows = 0, units = 0, pairs = 0, sums = 0;
+    p.n_seqs = 0;
+    for (int i = 0; i < n_seqs; ++i) {
+        const int64_t n = c->L(ids[i], layer), m = q_lens[i];
+        if (m < 0 || m > n) return fail(KVARN_EINVAL, "a query count is negative or above the sequence's length");
+        if (m > kWindowTokens) return fail(KVARN_EINVAL, "more than 128 queries of a sequence");
+        if (m > 0) {
+            BlockWindowSeq& e = p.seqs[p.n_seqs++];
+            e.seq = ids[i];
+            e.n = (int32_t)n;
+            e.q_len = (int32_t)m;
+            e.q_row = (int32_t)rows;
+            e.rows = (int32_t)m * c->r;
+            e.pad = (e.rows + 7) / 8 * 8;
+            e.row_tiles = (e.rows + 127) / 128;
+            e.steps = (int32_t)((n + 127) / 128);
+            e.unit_begin = (int32_t)units;
+            e.pair_begin = (int32_t)pairs;
+            e.sum_begin = sums;
+            units += (int64_t)hkv * e.row_tiles * e.steps;
+            pairs += (int64_t)hkv * e.row_tiles;
+            sums += (int64_t)hkv * tiles_of(n) * e.pad;
+        }
+        rows += m;
+        if (units >= 1ll << 31) return fail(KVARN_ECAPACITY, "2^31 steps of 128 keys or more in a call");
+    }
+    p.units = units;
+    p.grid = (int32_t)std::min<int64_t>(c->sms, units);
+    w->totals = (size_t)(sums * 8 + 255) / 256 * 256;
+    w->total = p.n_seqs ? w->totals + (size_t)(pairs + p.grid) * 2 * 128 * 8 : 0;
+    return KVARN_OK;
 }
 
 // Is a prefix of a group of single queries better walked once, as tiles of 128 rows, than by each sequence?
@@ -605,6 +652,7 @@ kvarn_status run_attend(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, con
     if (weights) {
         b.weights = weights;
         b.sums = (float2*)((uint8_t*)workspace + w.sums);
+        b.totals = (float2*)((uint8_t*)workspace + w.totals);
     }
     return run_decode(c, layer, n, one, q, out, scale, stream, b);
 }
@@ -829,6 +877,21 @@ kvarn_status kvarn_block_append_attend(kvarn_block_cache* c, int32_t layer, int3
     return run_attend(c, layer, n_seqs, seq_ids, prefix_ids, n_tokens, q, out, softmax_scale, weights, workspace, w, stream);
 }
 
+kvarn_status kvarn_block_window_workspace(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* seq_ids,
+                                          const int32_t* q_lens, size_t* bytes) {
+    if (!c || !bytes) return fail(KVARN_EINVAL, "no cache, or no place for the size");
+    if (layer < 0 || layer >= c->cfg.num_layers) return fail(KVARN_EINVAL, "no such layer");
+    if (n_seqs < 0 || (n_seqs > 0 && (!seq_ids || !q_lens))) return fail(KVARN_EINVAL, "bad sequence list");
+    if (n_seqs > kBlockMaxSeqs) return fail(KVARN_ECAPACITY, "more than 256 sequences in a call");
+    for (int i = 0; i < n_seqs; ++i)
+        if (seq_ids[i] < 0 || seq_ids[i] >= c->cfg.max_seqs) return fail(KVARN_EINVAL, "a sequence id is out of range");
+    static thread_local BlockWindowParams p;
+    Workspace w;
+    const kvarn_status st = plan_window(c, layer, n_seqs, seq_ids, q_lens, p, &w);
+    if (st == KVARN_OK) *bytes = w.total;
+    return st;
+}
+
 kvarn_status kvarn_block_window_weights(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* seq_ids,
                                         const int32_t* q_lens, const void* q, float softmax_scale, float* weights,
                                         void* workspace, size_t workspace_bytes, void* stream) {
@@ -838,59 +901,34 @@ kvarn_status kvarn_block_window_weights(kvarn_block_cache* c, int32_t layer, int
     if (n_seqs > 0 && !q_lens) return fail(KVARN_EINVAL, "no query counts");
     static thread_local BlockWindowParams p;
     static thread_local BlockWeighParams wp;
-    const int hkv = c->cfg.num_kv_heads;
-    int64_t rows = 0, units = 0, sums = 0;
-    p.n_seqs = p.smem_rows = 0;
-    for (int i = 0; i < n_seqs; ++i) {
-        const int64_t n = c->L(seq_ids[i], layer), m = q_lens[i];
-        if (m < 0 || m > n) return fail(KVARN_EINVAL, "a query count is negative or above the sequence's length");
-        if (m > kWindowTokens) return fail(KVARN_EINVAL, "more than 128 queries of a sequence");
-        if (m > 0) {
-            BlockWindowSeq& e = p.seqs[p.n_seqs];
-            BlockWeighSeq& s = wp.seqs[p.n_seqs++];
-            e.seq = s.seq = seq_ids[i];
-            e.n = (int32_t)n;
-            e.q_len = (int32_t)m;
-            e.q_row = (int32_t)rows;
-            e.rows = s.rows = (int32_t)m * c->r;
-            e.pad = s.pad = (e.rows + 7) / 8 * 8;
-            e.chunks = (e.rows + kWindowRows - 1) / kWindowRows;
-            e.tiles = s.tiles = tiles_of(n);
-            e.unit_begin = (int32_t)units;
-            e.unused = 0;
-            e.sum_begin = s.sum_begin = sums;
-            s.before = 0;
-            s.lse_row = -1;
-            p.smem_rows = std::max(p.smem_rows, std::min(kWindowRows, e.pad));
-            units += (int64_t)hkv * e.chunks * e.tiles;
-            sums += (int64_t)hkv * e.tiles * e.pad;
-        }
-        rows += m;
-        if (units >= 1ll << 31) return fail(KVARN_ECAPACITY, "2^31 tiles of 32 tokens or more in a call");
-    }
-    if (p.n_seqs == 0) return KVARN_OK;
+    Workspace w;
+    st = plan_window(c, layer, n_seqs, seq_ids, q_lens, p, &w);
+    if (st || p.n_seqs == 0) return st;
     if (!q || !aligned16(q)) return fail(KVARN_EINVAL, "q must be 16-byte aligned");
     if (!weights) return fail(KVARN_EINVAL, "no weights");
-    Workspace w;
-    w.total = (size_t)sums * 8;
-    st = check_beside(c, rows, q, nullptr, weights, workspace, workspace_bytes, w);
+    const BlockWindowSeq& end = p.seqs[p.n_seqs - 1];
+    st = check_beside(c, (int64_t)end.q_row + end.q_len, q, nullptr, weights, workspace, workspace_bytes, w);
     if (st || c->host_only) return st;
     p.c = c->view;
     p.c.layer = layer;
     p.q = (const uint16_t*)q;
-    p.sums = (float2*)workspace;
+    p.sums = (float2*)((uint8_t*)workspace + w.sums);
+    p.totals = (float2*)((uint8_t*)workspace + w.totals);
     p.hq = c->cfg.num_q_heads;
     p.r = c->r;
-    p.units = units;
-    p.grid = (int32_t)std::min<int64_t>(c->sms, (units + 11) / 12);
     p.scale_log2 = softmax_scale * kLog2e;
     const int rc = launch_block_window(p, stream);
     if (rc) return cuda_fail(rc, "window launch");
     wp.sums = p.sums;
-    wp.pre_lse = nullptr;
+    wp.totals = p.totals;
     wp.weights = weights;
-    wp.shift = 0.f;
+    wp.units = p.units;
+    wp.grid = p.grid;
     wp.n_seqs = p.n_seqs;
+    for (int i = 0; i < p.n_seqs; ++i) {
+        const BlockWindowSeq& e = p.seqs[i];
+        wp.seqs[i] = BlockWeighSeq{e.seq, e.rows, e.pad, 0, tiles_of(e.n), 0, e.unit_begin, e.pair_begin, e.sum_begin};
+    }
     return run_weigh(c, wp, stream);
 }
 

@@ -32,8 +32,7 @@
 // of the causal products), 512 queries against 32,768 tokens 208 us (1,310 TFLOP/s). The prompt takes 110
 // us where its 75 MB stay in L2 from one call to the next, and 107 with normal values, on which no warp
 // ever rescales O (28 % of a warp's steps do with outlier channels and token norms of a wide spread).
-#include "kvarn_block_dev.cuh"
-#include "kvarn_tc.cuh"
+#include "kvarn_block_tc.cuh"
 
 namespace kvarn {
 namespace {
@@ -53,7 +52,6 @@ constexpr int kBarKFull = 0, kBarVFull = 4, kBarKEmpty = 8, kBarVEmpty = 10, kBa
 
 template <int D>
 struct Shape {
-    static constexpr int kAtom = 128 * 128;            // 128 rows of 64 f16
     static constexpr int kQ = 0;                        // 2 tiles of D / 64 atoms
     static constexpr int kTileQ = D / 64 * kAtom;
     static constexpr int kK = kQ + 2 * kTileQ;          // 2 stages of D / 64 atoms
@@ -68,28 +66,6 @@ struct Shape {
     static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
 };
 
-// K-major operand with 128-byte swizzle: rows of 128 bytes, 8-row groups 1024 bytes apart. Given
-// by its address / 16, to which offsets of a k-step are added.
-__device__ __forceinline__ uint64_t desc128(uint32_t addr16) {
-    constexpr uint32_t hi = (1024u >> 4) | (1u << 14) | (2u << 29);  // stride, version, swizzle
-    uint64_t d;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(addr16 | (1u << 16)), "n"(hi));
-    return d;
-}
-// byte of 16-byte chunk `chunk` of row `row` in such an atom
-__device__ __forceinline__ int swz(int row, int chunk) { return row * 128 + ((chunk ^ (row & 7)) << 4); }
-
-// instruction descriptor of kind::f16: f32 accumulator, f16 operands, both K-major, M = 128
-template <int N>
-constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((128u >> 4) << 24);
-
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(id), "r"(acc)
-        : "memory");
-}
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
     asm volatile(
         "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
@@ -104,27 +80,6 @@ __device__ __forceinline__ void tm_st16(uint32_t taddr, const uint32_t (&r)[16])
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
-__device__ __forceinline__ bool elect_one() {
-    uint32_t ok;
-    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(ok));
-    return ok != 0;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
-
-__device__ __forceinline__ float max32(const uint32_t (&r)[32]) {
-    float a = __uint_as_float(r[0]), b = __uint_as_float(r[1]);
-#pragma unroll
-    for (int k = 2; k < 30; k += 4) {
-        a = max3(a, __uint_as_float(r[k]), __uint_as_float(r[k + 1]));
-        b = max3(b, __uint_as_float(r[k + 2]), __uint_as_float(r[k + 3]));
-    }
-    return fmaxf(max3(a, __uint_as_float(r[30]), __uint_as_float(r[31])), b);
-}
-
 // ---- the line of steps ----
 // Steps of a query tile pair: up to the last position that its queries see.
 __device__ __forceinline__ int pair_steps(const BlockPrefillParams& p, const BlockPrefillSeq& e, int pair, int pair_tokens) {
@@ -295,7 +250,7 @@ __device__ __forceinline__ void issue_role(uint32_t sbase, uint64_t* bars, int32
                     const uint32_t q = base + ((Sh::kQ + b * Sh::kTileQ) >> 4);
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks) {
-                        const uint32_t off = ((ks >> 2) * Sh::kAtom + (ks & 3) * 32) >> 4;
+                        const uint32_t off = ((ks >> 2) * kAtom + (ks & 3) * 32) >> 4;
                         if (leader) mma_ss(kColS + 128 * b, desc128(q + off), desc128(k + off), kIdesc<128>, ks > 0);
                     }
                     if (leader) mma_commit(bars + kBarSFull + b);
@@ -312,96 +267,6 @@ __device__ __forceinline__ void issue_role(uint32_t sbase, uint64_t* bars, int32
     const uint64_t t0 = global_ns();
 #pragma unroll 1
     while (!mbar_try_wait(bars + kBarDrain, 0u) && global_ns() - t0 < kWaitLimitNs) {
-    }
-}
-
-// Exact tokens of a part (none: zeros) as its K or V tile rows. A later token's infinity or NaN
-// must not reach a query that does not see it through 0 x NaN: non-finite V enters as 0, and `bad`
-// says that there is some, for add_non_finite at the segment's end. K needs no such care (logits
-// of unseen tokens are replaced), but neither may set the part's power of two.
-// h: K scale, or log2 of the V scale and kDenomUnit over it. x: registers to use.
-template <int D, bool BF16, bool IS_V>
-__device__ __forceinline__ void expand_exact(const BlockView& c, const BlockPrefillSeq& e, int kvh, int tile, int wp, int lane,
-                                             uint8_t* dst, float2& h, uint32_t& bad, uint4 (&x)[D / 16]) {
-    const int g = lane >> 2, t = lane & 3;
-    const int first = (tile - (e.n >> c.log2_block << (c.log2_block - 5))) * kTileTokens;  // row of the tail
-    const int nv = min(kTileTokens, e.n - tile * kTileTokens);  // valid tokens, none if <= 0
-    h = IS_V ? make_float2(0.f, 1.f) : make_float2(1.f, 0.f);
-    bad = 0;
-    // D / 8 pieces of 16 bytes a lane, four at a time so that their loads overlap; twice, first for the largest
-    constexpr int kTurn = 4;
-    if (IS_V) {  // piece i: tokens 8 t .. of channel 8 i + g
-        const uint16_t* v = tail_ptr(c, c.lay.tail_v, e.seq, kvh) + (ptrdiff_t)first * D;
-        uint32_t keep[4];
-#pragma unroll
-        for (int z = 0; z < 4; ++z)
-            keep[z] = (8 * t + 2 * z < nv ? 0xffffu : 0u) | (8 * t + 2 * z + 1 < nv ? 0xffff0000u : 0u);
-        auto load = [&](int i0) {
-#pragma unroll
-            for (int i = 0; i < kTurn; ++i) {
-                x[i] = make_uint4(0, 0, 0, 0);
-                if (nv > 0) x[i] = *reinterpret_cast<const uint4*>(v + (8 * (i0 + i) + g) * kTileTokens + 8 * t);
-            }
-#pragma unroll
-            for (int i = 0; i < kTurn; ++i)
-                x[i] = make_uint4(x[i].x & keep[0], x[i].y & keep[1], x[i].z & keep[2], x[i].w & keep[3]);
-        };
-        uint32_t top = 0;
-#pragma unroll 1
-        for (int i0 = 0; i0 < D / 8; i0 += kTurn) {
-            load(i0);
-#pragma unroll
-            for (int i = 0; i < kTurn; ++i) top = max_of(top, finite_only<BF16>(x[i]));
-        }
-        const int ex = warp_exponent_v<BF16>(top);
-        const float f = power2(-ex);
-        h = make_float2((float)ex, f * kDenomUnit);
-        uint8_t* atom = dst + (wp >> 1) * (D * 128);
-#pragma unroll 1
-        for (int i0 = 0; i0 < D / 8; i0 += kTurn) {
-            load(i0);
-#pragma unroll
-            for (int i = 0; i < kTurn; ++i) {
-                const uint4 r = x[i];
-                bad |= bad_pair<BF16>(r.x) | bad_pair<BF16>(r.y) | bad_pair<BF16>(r.z) | bad_pair<BF16>(r.w);
-                *reinterpret_cast<uint4*>(atom + swz(8 * (i0 + i) + g, 4 * (wp & 1) + t)) =
-                    scaled_f16<BF16>(finite_only<BF16>(r), f);
-            }
-        }
-        bad = __reduce_or_sync(0xffffffffu, bad);
-    } else {  // piece i: bytes i * 512 + lane * 16 of the part's 32 D values
-        const uint16_t* k = tail_ptr(c, c.lay.tail_k, e.seq, kvh) + (ptrdiff_t)first * D;
-        auto load = [&](int i0) {
-#pragma unroll
-            for (int i = 0; i < kTurn; ++i) {
-                const int y = (i0 + i) * 32 + lane;
-                x[i] = make_uint4(0, 0, 0, 0);
-                if (y / (D / 8) < nv) x[i] = *reinterpret_cast<const uint4*>(k + y * 8);
-            }
-        };
-        float f = 1.f;
-        if (BF16) {
-            uint32_t top = 0;
-#pragma unroll 1
-            for (int i0 = 0; i0 < D / 8; i0 += kTurn) {
-                load(i0);
-#pragma unroll
-                for (int i = 0; i < kTurn; ++i) top = max_of(top, finite_only<BF16>(x[i]));
-            }
-            const int ex = warp_exponent<BF16>(top) - kExactK;
-            f = power2(-ex);
-            h.x = power2(ex);
-        }
-#pragma unroll 1
-        for (int i0 = 0; i0 < D / 8; i0 += kTurn) {
-            load(i0);
-#pragma unroll
-            for (int i = 0; i < kTurn; ++i) {
-                const int y = (i0 + i) * 32 + lane, ch8 = y % (D / 8);
-                *reinterpret_cast<uint4*>(dst + (ch8 >> 3) * Shape<D>::kAtom + swz(32 * wp + y / (D / 8), ch8 & 7)) =
-                    BF16 ? scaled_f16<BF16>(x[i], f) : x[i];
-            }
-        }
     }
 }
 
@@ -472,11 +337,11 @@ __device__ __forceinline__ void expand_role(const BlockPrefillParams& p, uint8_t
                     x[i] = load_v(rec, i);
                     // 16 channels of one token
                     const int s = i / (D / 32), cc = i / 2 % (D / 64), row = row0 + 4 * s + 2 * (i & 1);
-                    *reinterpret_cast<uint4*>(dst + cc * Sh::kAtom + swz(row, 2 * t)) = a;
-                    *reinterpret_cast<uint4*>(dst + cc * Sh::kAtom + swz(row, 2 * t + 1)) = b;
+                    *reinterpret_cast<uint4*>(dst + cc * kAtom + swz(row, 2 * t)) = a;
+                    *reinterpret_cast<uint4*>(dst + cc * kAtom + swz(row, 2 * t + 1)) = b;
                 }
             } else {
-                expand_exact<D, BF16, false>(c, p.seqs[who & 255], who >> 8, (int)(tile & 0x7fffffffu), wp, lane, dst, h, bad, x);
+                expand_exact<D, BF16, false>(c, p.seqs[who & 255].seq, p.seqs[who & 255].n, who >> 8, (int)(tile & 0x7fffffffu), wp, lane, dst, h, bad, x);
             }
             if (lane == 0) head[0] = h.x;
             fence_proxy_async_smem();
@@ -495,7 +360,7 @@ __device__ __forceinline__ void expand_role(const BlockPrefillParams& p, uint8_t
                     if (rec1) x[i] = load_k(rec1, i);
                 }
             } else {
-                expand_exact<D, BF16, true>(c, p.seqs[who & 255], who >> 8, (int)(tile & 0x7fffffffu), wp, lane, dst, h, bad, x);
+                expand_exact<D, BF16, true>(c, p.seqs[who & 255].seq, p.seqs[who & 255].n, who >> 8, (int)(tile & 0x7fffffffu), wp, lane, dst, h, bad, x);
             }
             if (lane == 0) head[1] = __uint_as_float(bad), head[2] = h.x, head[3] = h.y;
             fence_proxy_async_smem();
@@ -594,7 +459,7 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, uint8_
                         if (lane / kRows == i) qs *= power2(mine);
                     }
                     r = make_uint4(r.x ^ sign, r.y ^ sign, r.z ^ sign, r.w ^ sign);
-                    *reinterpret_cast<uint4*>(rows + (lane % kLanes >> 3) * Sh::kAtom + swz(i * kRows + lane / kLanes, lane & 7)) = r;
+                    *reinterpret_cast<uint4*>(rows + (lane % kLanes >> 3) * kAtom + swz(i * kRows + lane / kLanes, lane & 7)) = r;
                 }
             }
         }
@@ -698,11 +563,11 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, uint8_
         auto give = [&](int piece, const uint32_t (&o)[32]) {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-                *reinterpret_cast<uint4*>(rows + piece * Sh::kAtom + swz(lane, k)) =
+                *reinterpret_cast<uint4*>(rows + piece * kAtom + swz(lane, k)) =
                     make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
         };
         auto take = [&](int piece, int k) {  // 16 bytes of row 4 k + lane / 8
-            return *reinterpret_cast<const uint4*>(rows + piece * Sh::kAtom + swz(4 * k + (lane >> 3), lane & 7));
+            return *reinterpret_cast<const uint4*>(rows + piece * kAtom + swz(4 * k + (lane >> 3), lane & 7));
         };
         const bool whole = w.whole();
         const float inv = l == 0.f ? 0.f : 1.f / l;

@@ -4,273 +4,412 @@
 //   p_n = 2^(x_n) / sum 2^(x_n'), x_n = scale log2(e) (q . k_n), over the tokens that the row sees.
 // A row's denominator is known only behind its last key, so it goes in two steps: whoever makes the logits (decode
 // attention, or window_kernel for the last queries of a prompt, which reads K alone) leaves of every 32-token tile and row
-// the running maximum m and the tile's sum s of 2^(x - m), 8 bytes for 32 logits; weigh_kernel joins a row's tiles to the
-// denominator, and adds the tiles' shares to their blocks in a fixed order. Kept as a pair, no rounding
-// of a logit's size stands between a weight and its denominator (log2 of the sum in one word would be off by 2^-17 at 128).
-#include <limits.h>
-
-#include "kvarn_block_dev.cuh"
-#include "kvarn_tc.cuh"
+// a maximum m and the tile's sum s of 2^(x - m), 8 bytes for 32 logits, and of every row its total; weigh_kernel
+// adds the tiles' shares to their blocks in a fixed order. Kept as a pair, no rounding of a logit's size
+// stands between a weight and its denominator (log2 of the sum in one word would be off by 2^-17 at 128).
+#include "kvarn_block_tc.cuh"
 
 namespace kvarn {
 namespace {
 
 // ---- logits of the last queries ----
-// The pairs of a (sequence, KV head, chunk of kWindowRows rows) and its tiles form one line that is cut evenly over the
-// CTAs. A pair's rows lie in shared memory in the order of mma.m16n8k16's B operand; a warp takes a tile's codes as A
-// operands (the next tile's are on their way) and goes through the rows, eight at a time.
-constexpr int kWinWarps = 12, kWinThreads = 32 * kWinWarps;
+// S = Q code^T on tcgen05 (M = 128 rows, N = 128 tokens, f16 operands, exact codes, fp32 sums) as in prefill, and no more: a
+// unit of work is a step of 128 tokens for a tile of 128 rows of a (sequence, KV head), and the line of all units is cut evenly over
+// the CTAs, one a SM. Roles (608 threads): eight expansion warps that turn K codes into f16 tiles (a warp 32 tokens,
+// four warps every other step, four stages); one that issues the MMAs into four S buffers (all 512 columns of tensor
+// memory: no O is kept); two that load query rows, a tile ahead; two softmax warpgroups, every other step each, a thread a row. Every wait
+// is bounded and sets the error word when it gives up.
+constexpr int kWinThreads = 608, kWinStep = 128, kWinStages = 4, kWinRing = 8;
+constexpr int kWinSoftmax = 8, kWinExpand = 8;  // warps
+// barriers
+constexpr int kKFull = 0, kKEmpty = kKFull + kWinRing, kSFull = kKEmpty + kWinStages, kSEmpty = kSFull + 4, kQFull = kSEmpty + 4,
+              kQEmpty = kQFull + kWinRing, kDrain = kQEmpty + 2, kWinBars = kDrain + 1;
 
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+template <int D>
+struct WinShape {
+    static constexpr int kTile = D / 64 * kAtom;
+    static constexpr int kQ = 0;                                   // 2 tiles
+    static constexpr int kK = 2 * kTile;                           // kWinStages tiles
+    static constexpr int kScale = kK + kWinStages * kTile;         // float[kWinRing][4]: K scale of a step's parts
+    static constexpr int kFactor = kScale + kWinRing * 16;         // float[kWinRing][128]: of a segment's rows
+    static constexpr int kBars = kFactor + kWinRing * 512;
+    static constexpr int kTmem = kBars + 8 * kWinBars;
+    static constexpr int kSmem = kTmem + 16;
+    static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
+};
+
+// The segments (rows of 128, steps j0 .. j1 - 1) of a CTA's part of the line, in order.
+struct WinWalk {
+    const BlockWindowParams& p;
+    int64_t u, u1;
+    int i, h, tile, j0, j1, pair;
+    __device__ __forceinline__ explicit WinWalk(const BlockWindowParams& p_)
+        : p(p_), u(p_.units * blockIdx.x / p_.grid), u1(p_.units * (blockIdx.x + 1) / p_.grid), i(0) {}
+    __device__ __forceinline__ bool next() {
+        if (u >= u1) return false;
+#pragma unroll 1
+        while (i + 1 < p.n_seqs && p.seqs[i + 1].unit_begin <= u) ++i;
+        const BlockWindowSeq& e = p.seqs[i];
+        const int rel = (int)u - e.unit_begin;
+        pair = rel / e.steps;
+        j0 = rel - pair * e.steps;
+        j1 = (int)min((int64_t)e.steps, j0 + (u1 - u));
+        h = pair / e.row_tiles;
+        tile = pair - h * e.row_tiles;
+        u += j1 - j0;
+        return true;
+    }
+};
+
+// Warp wp (0 .. 3) of group `odd`: part wp of every other step. The next step's codes are on their way while one is expanded.
+template <int D, bool INT8, bool BF16>
+__device__ __forceinline__ void win_expand(const BlockWindowParams& p, uint8_t* smem, uint64_t* bars, int32_t* err, int odd,
+                                           int wp, int lane) {
+    using Sh = WinShape<D>;
+    const BlockView& c = p.c;
+    const int sh = c.log2_block - 5, t = lane & 3, kg = lane >> 2;
+    constexpr int kChunks = D / 16;
+    WinWalk w(p);
+    bool more = w.next();
+    int j = more ? w.j0 : 0, k = 0;  // the next step to look at
+    auto skip = [&]() {              // one step on
+        ++k;
+        if (more && ++j == w.j1) {
+            more = w.next();
+            if (more) j = w.j0;
+        }
+    };
+    if (odd) skip();
+    struct Part {
+        int step, seq, n, kvh, tile, slot;  // step -1: none
+    };
+    auto look = [&]() {
+        Part x = {-1, 0, 0, 0, 0, -1};
+        if (!more) return x;
+        const BlockWindowSeq& e = p.seqs[w.i];
+        x = Part{k, e.seq, e.n, w.h, 4 * j + wp, -1};
+        if (x.tile < e.n >> c.log2_block << sh) x.slot = __ldg(block_table(c, e.seq) + (x.tile >> sh));
+        skip();
+        skip();
+        return x;
+    };
+    uint4 x[kChunks];  // reloaded in place
+    float scale = 1.f;
+    auto record = [&](const Part& a) { return a.slot < 0 ? nullptr : tile_ptr(c, a.slot, a.kvh, a.tile & ((1 << sh) - 1)); };
+    auto load = [&](const uint8_t* rec, int i) { return __ldg(reinterpret_cast<const uint4*>(rec + 16 + i * 512) + lane); };
+    auto load_all = [&](const uint8_t* rec) {
+        if (!rec) return;
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) x[i] = load(rec, i);
+        scale = __ldg(reinterpret_cast<const float*>(rec));
+    };
+    Part now = look(), ahead = look();
+    load_all(record(now));
+#pragma unroll 1
+    while (now.step >= 0) {
+        const int s = now.step;
+        if (s >= kWinStages) bar_wait(bars + kKEmpty + s % kWinStages, (uint32_t)((s / kWinStages - 1) & 1), err);
+        uint8_t* dst = smem + Sh::kK + s % kWinStages * Sh::kTile;
+        float* head = reinterpret_cast<float*>(smem + Sh::kScale) + (s % kWinRing) * 4 + wp;
+        float f = scale;
+        const uint8_t* rec = record(ahead);
+        const Part then = look();
+        if (now.slot >= 0) {
+            const int row0 = 32 * wp + 8 * (kg >> 1) + (kg & 1);
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i) {  // 16 channels of one token
+                const int z = i / (D / 32), cc = i / 2 % (D / 64), row = row0 + 4 * z + 2 * (i & 1);
+                const uint4 a = make_uint4(codes_lo<INT8>(x[i].x), codes_hi<INT8>(x[i].x), codes_lo<INT8>(x[i].y), codes_hi<INT8>(x[i].y));
+                const uint4 b = make_uint4(codes_lo<INT8>(x[i].z), codes_hi<INT8>(x[i].z), codes_lo<INT8>(x[i].w), codes_hi<INT8>(x[i].w));
+                if (rec) x[i] = load(rec, i);
+                *reinterpret_cast<uint4*>(dst + cc * kAtom + swz(row, 2 * t)) = a;
+                *reinterpret_cast<uint4*>(dst + cc * kAtom + swz(row, 2 * t + 1)) = b;
+            }
+            if (rec) scale = __ldg(reinterpret_cast<const float*>(rec));
+        } else {
+            float2 hd;
+            uint32_t bad;
+            expand_exact<D, BF16, false>(c, now.seq, now.n, now.kvh, now.tile, wp, lane, dst, hd, bad, x);
+            f = hd.x;
+            load_all(rec);
+        }
+        if (lane == 0) *head = f;
+        fence_proxy_async_smem();
+        mbar_arrive(bars + kKFull + s % kWinRing);
+        now = ahead;
+        ahead = then;
+    }
+}
+
+template <int D>
+__device__ __forceinline__ void win_issue(const BlockWindowParams& p, uint32_t sbase, uint64_t* bars, int32_t* err) {
+    using Sh = WinShape<D>;
+    const bool leader = elect_one();
+    const uint32_t base = sbase >> 4;
+    int k = 0, seg = 0;
+    WinWalk w(p);
+#pragma unroll 1
+    for (; w.next(); ++seg) {
+        const int j1 = __shfl_sync(0xffffffffu, w.j1, 0), j0 = __shfl_sync(0xffffffffu, w.j0, 0);
+        bar_wait(bars + kQFull + seg % kWinRing, (uint32_t)(seg / kWinRing & 1), err);
+        const uint32_t q = base + ((Sh::kQ + (seg & 1) * Sh::kTile) >> 4);
+#pragma unroll 1
+        for (int j = j0; j < j1; ++j, ++k) {
+            bar_wait(bars + kKFull + k % kWinRing, (uint32_t)(k / kWinRing & 1), err);
+            if (k >= 4) bar_wait(bars + kSEmpty + (k & 3), (uint32_t)(((k >> 2) - 1) & 1), err);
+            __syncwarp();
+            tc_fence_after();
+            const uint32_t kt = base + ((Sh::kK + k % kWinStages * Sh::kTile) >> 4);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+                const uint32_t off = ((ks >> 2) * kAtom + (ks & 3) * 32) >> 4;
+                if (leader) mma_ss(128 * (k & 3), desc128(q + off), desc128(kt + off), kIdesc<128>, ks > 0);
+            }
+            if (leader) mma_commit(bars + kSFull + (k & 3));
+            if (leader) mma_commit(bars + kKEmpty + k % kWinStages);
+            if (leader && j == j1 - 1) mma_commit(bars + kQEmpty + (seg & 1));
+        }
+    }
+    if (leader) mma_commit(bars + kDrain);
+    // every MMA has completed before tensor memory is released
+    const uint64_t t0 = global_ns();
+#pragma unroll 1
+    while (!mbar_try_wait(bars + kDrain, 0u) && global_ns() - t0 < kWaitLimitNs) {
+    }
+}
+
+// Two warps: the rows of each segment as its Q tile, and the factors of their logits.
+template <int D, bool BF16>
+__device__ __forceinline__ void win_rows(const BlockWindowParams& p, uint8_t* smem, uint64_t* bars, int32_t* err, int half, int lane) {
+    using Sh = WinShape<D>;
+    // a negative scale turns the query's sign, so that larger S is always a larger logit (0: all logits are 0)
+    const bool zero = p.scale_log2 == 0.f;
+    const float scale = zero ? 1.f : fabsf(p.scale_log2);
+    const uint32_t sign = p.scale_log2 < 0.f ? 0x80008000u : 0u;
+    constexpr int kLanes = D / 8, kRows = 32 / kLanes, kTurn = 8;
+    int seg = 0;
+    WinWalk w(p);
+#pragma unroll 1
+    for (; w.next(); ++seg) {
+        if (seg >= 2) bar_wait(bars + kQEmpty + (seg & 1), (uint32_t)(((seg >> 1) - 1) & 1), err);
+        __syncwarp();
+        const BlockWindowSeq& e = p.seqs[w.i];
+        uint8_t* dst = smem + Sh::kQ + (seg & 1) * Sh::kTile;
+        float* factor = reinterpret_cast<float*>(smem + Sh::kFactor) + seg % kWinRing * 128;
+#pragma unroll 1
+        for (int r0 = 64 * half; r0 < 64 * half + 64; r0 += kTurn * kRows) {
+            uint4 x[kTurn];
+#pragma unroll
+            for (int z = 0; z < kTurn; ++z) {
+                const int row = r0 + z * kRows + lane / kLanes, all = w.tile * 128 + row;
+                x[z] = make_uint4(0, 0, 0, 0);
+                if (all < e.rows && !zero)
+                    x[z] = reinterpret_cast<const uint4*>(p.q + ((size_t)(e.q_row + all / p.r) * p.hq + w.h * p.r + all % p.r) * D)[lane % kLanes];
+            }
+#pragma unroll
+            for (int z = 0; z < kTurn; ++z) {
+                const int row = r0 + z * kRows + lane / kLanes;
+                float f = scale;
+                uint4 r = x[z];
+                if (BF16) {
+                    uint32_t top = max_of(0, r);
+                    top = max(top & 0xffffu, top >> 16);
+#pragma unroll
+                    for (int d = kLanes / 2; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+                    const int ex = exponent_of<BF16>(top) - kExactK;
+                    r = scaled_f16<BF16>(r, power2(-ex));
+                    f *= power2(ex);
+                }
+                r = make_uint4(r.x ^ sign, r.y ^ sign, r.z ^ sign, r.w ^ sign);
+                *reinterpret_cast<uint4*>(dst + (lane % kLanes >> 3) * kAtom + swz(row, lane & 7)) = r;
+                if (lane % kLanes == 0) factor[row] = f;
+            }
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(bars + kQFull + seg % kWinRing);
+    }
+}
+
+// Warpgroup b takes the steps of its parity; thread et owns row et.
+template <int D>
+__device__ __forceinline__ void win_softmax(const BlockWindowParams& p, uint8_t* smem, uint64_t* bars, int32_t* err, int et, int b,
+                                            uint32_t lane_off) {
+    using Sh = WinShape<D>;
+    int k = 0, seg = 0;
+    WinWalk w(p);
+#pragma unroll 1
+    for (; w.next(); ++seg) {
+        const BlockWindowSeq& e = p.seqs[w.i];
+        const int row = w.tile * 128 + et, tiles = (e.n + kTileTokens - 1) / kTileTokens;
+        const bool valid = row < e.rows;
+        const int pos = valid ? e.n - e.q_len + row / p.r : e.n - 1;
+        float2* out = p.sums + e.sum_begin + (int64_t)w.h * tiles * e.pad + row;
+        float2 total = make_float2(kNegInf, 0.f);
+        float qs = 1.f;
+        bool first = true;
+#pragma unroll 1
+        for (int j = w.j0; j < w.j1; ++j, ++k) {
+            if ((k & 1) != b) continue;
+            if (first) {
+                bar_wait(bars + kQFull + seg % kWinRing, (uint32_t)(seg / kWinRing & 1), err);
+                qs = reinterpret_cast<const float*>(smem + Sh::kFactor)[seg % kWinRing * 128 + et];
+                first = false;
+            }
+            bar_wait(bars + kKFull + k % kWinRing, (uint32_t)(k / kWinRing & 1), err);
+            const float4 hd = reinterpret_cast<const float4*>(smem + Sh::kScale)[k % kWinRing];
+            bar_wait(bars + kSFull + (k & 3), (uint32_t)(k >> 2 & 1), err);
+            __syncwarp();
+            tc_fence_after();
+            const int lim = pos + 1 - j * kWinStep;  // visible columns
+            const bool plain = __all_sync(0xffffffffu, lim >= kWinStep);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                uint32_t r[2][32];
+                tm_ld32(128 * (k & 3) + 64 * half + lane_off, r[0]);
+                tm_ld32(128 * (k & 3) + 64 * half + 32 + lane_off, r[1]);
+                tm_wait_ld();
+                if (half == 1) {  // S may be written again
+                    tc_fence_before();
+                    mbar_arrive(bars + kSEmpty + (k & 3));
+                }
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const int ch = 2 * half + y, left = lim - 32 * ch;
+                    float c = qs * (ch == 0 ? hd.x : ch == 1 ? hd.y : ch == 2 ? hd.z : hd.w);
+                    if (c < 1e-37f) c = 1e-37f;  // 0 would make -inf of a masked column NaN
+                    if (!plain) {
+#pragma unroll
+                        for (int z = 0; z < 32; ++z)
+                            if (z >= left) r[y][z] = 0xff800000u;
+                        if (left <= 0) c = 1.f;
+                    }
+                    const float m = max32(r[y]) * c, mm = m == kNegInf ? 0.f : m;
+                    const float2 c2 = make_float2(c, c), a2 = make_float2(-mm, -mm);
+                    float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+#pragma unroll
+                    for (int z = 0; z < 16; ++z) {
+                        const float2 x = __ffma2_rn(make_float2(__uint_as_float(r[y][2 * z]), __uint_as_float(r[y][2 * z + 1])), c2, a2);
+                        const float2 v = make_float2(ex2f(x.x), ex2f(x.y));
+                        if (z & 1) s1 = __fadd2_rn(s1, v);
+                        else s0 = __fadd2_rn(s0, v);
+                    }
+                    s0 = __fadd2_rn(s0, s1);
+                    const float2 part = make_float2(m, s0.x + s0.y);
+                    total = joined(total, part);
+                    if (valid && 4 * j + ch < tiles) out[(int64_t)(4 * j + ch) * e.pad] = part;
+                }
+            }
+        }
+        // of the pair's part in this CTA (a pair's first CTA is no sooner than the pair before's last)
+        p.totals[((int64_t)(e.pair_begin + w.pair + blockIdx.x) * 2 + b) * 128 + et] = total;
+    }
 }
 
 template <int D, bool INT8, bool BF16>
 __global__ void __launch_bounds__(kWinThreads, 1) window_kernel(const __grid_constant__ BlockWindowParams p) {
-    extern __shared__ __align__(128) uint8_t smem[];
-    const BlockView& c = p.c;
-    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    constexpr int kPieces = D / 32;  // 16-byte pieces of a lane for eight rows
-    uint4* rows = reinterpret_cast<uint4*>(smem);                                      // [row / 8][piece][lane]
-    float* factor = reinterpret_cast<float*>(smem + (size_t)p.smem_rows * (2 * D));    // of a row's logits
-    int* last = reinterpret_cast<int*>(factor + p.smem_rows);                          // the last position that it sees
-    int* down = last + p.smem_rows;                                                    // the power of two that its values lose
-    const int64_t u0 = p.units * blockIdx.x / p.grid, u1 = p.units * (blockIdx.x + 1) / p.grid;
-    const int sh = c.log2_block - 5;
-    int i = 0;
-    for (int64_t from = u0; from < u1;) {
-#pragma unroll 1
-        while (i + 1 < p.n_seqs && p.seqs[i + 1].unit_begin <= from) ++i;
-        const BlockWindowSeq& e = p.seqs[i];
-        const int pair = (int)((from - e.unit_begin) / e.tiles), kvh = pair / e.chunks, row0 = pair % e.chunks * kWindowRows;
-        const int64_t begin = e.unit_begin + (int64_t)pair * e.tiles;
-        const int tile0 = (int)(from - begin), tile1 = (int)min(u1 - begin, (int64_t)e.tiles);
-        const int count = min(kWindowRows, e.rows - row0), octets = (count + 7) / 8;
-        // the pair's rows
-        __syncthreads();
-        auto source = [&](int row) {
-            const int all = row0 + row;
-            return p.q + ((size_t)(e.q_row + all / p.r) * p.hq + kvh * p.r + all % p.r) * D;
-        };
-        for (int row = threadIdx.x; row < 8 * octets; row += kWinThreads) {
-            int ex = 0;
-            if (BF16 && row < count) {
-                uint32_t top = 0;
-                const uint4* at = reinterpret_cast<const uint4*>(source(row));
-#pragma unroll 4
-                for (int k = 0; k < D / 8; ++k) top = max_of(top, at[k]);
-                ex = exponent_of<BF16>(max(top & 0xffffu, top >> 16)) - kExactK;
-            }
-            down[row] = ex;
-            factor[row] = p.scale_log2 * power2(ex);
-            last[row] = e.n - e.q_len + min(row0 + row, e.rows - 1) / p.r;
+    using Sh = WinShape<D>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int t = threadIdx.x, w = t >> 5, lane = t & 31;
+    int32_t* err = reinterpret_cast<int32_t*>(p.c.base + p.c.lay.err);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Sh::kBars);
+    if (t == 0) {
+        for (int k = 0; k < kWinRing; ++k) {
+            mbar_init(bars + kKFull + k, 128);
+            mbar_init(bars + kQFull + k, 64);
         }
-        if (BF16) __syncthreads();
-        for (int k = threadIdx.x; k < octets * kPieces * 32; k += kWinThreads) {
-            const int l = k & 31, piece = k / 32 % kPieces, row = k / (32 * kPieces) * 8 + (l >> 2);
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (row < count) {
-                x = *reinterpret_cast<const uint4*>(source(row) + 64 * (piece >> 1) + 16 * (l & 3) + 8 * (piece & 1));
-                if (BF16) x = scaled_f16<BF16>(x, power2(-down[row]));
-            }
-            rows[k] = x;
+        for (int k = 0; k < kWinStages; ++k) mbar_init(bars + kKEmpty + k, 1);
+        for (int k = 0; k < 4; ++k) {
+            mbar_init(bars + kSFull + k, 1);
+            mbar_init(bars + kSEmpty + k, 128);
         }
-        __syncthreads();
-        float2* sums = p.sums + e.sum_begin + (int64_t)kvh * e.tiles * e.pad + row0;
-        const int32_t* table = block_table(c, e.seq);
-        const int sealed = e.n >> c.log2_block << sh;
-        // codes of the warp's next tile, 16 bytes a lane of each 512
-        uint4 next[D / 16];
-        float next_scale = 1.f;
-        auto fetch = [&](int tile) {
-            if (tile >= min(tile1, sealed)) return;
-            const uint8_t* rec = sealed_tile(c, table, kvh, tile);
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) next[k] = __ldg(reinterpret_cast<const uint4*>(rec + 16 + k * 512) + lane);
-            next_scale = __ldg(reinterpret_cast<const float*>(rec));
-        };
-        fetch(tile0 + w);
-        for (int tile = tile0 + w; tile < tile1; tile += kWinWarps) {
-            uint32_t a[2][D / 16][4];  // half of 16 tokens, 16 channels, registers of the A operand
-            float ks = 1.f;
-            if (tile < sealed) {
-                ks = next_scale;
-#pragma unroll
-                for (int z = 0; z < 2; ++z)
-#pragma unroll
-                    for (int y = 0; y < D / 64; ++y) {
-                        const uint4 u = next[(z * (D / 64) + y) * 2], v = next[(z * (D / 64) + y) * 2 + 1];
-                        const uint32_t x4[4] = {u.x, u.y, u.z, u.w}, y4[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            a[z][4 * y + j][0] = codes_lo<INT8>(x4[j]);
-                            a[z][4 * y + j][1] = codes_lo<INT8>(y4[j]);
-                            a[z][4 * y + j][2] = codes_hi<INT8>(x4[j]);
-                            a[z][4 * y + j][3] = codes_hi<INT8>(y4[j]);
-                        }
-                    }
-                fetch(tile + kWinWarps);
-            } else {  // exact rows
-                const uint16_t* k = tail_ptr(c, c.lay.tail_k, e.seq, kvh) + (size_t)(tile - sealed) * (kTileTokens * D);
-                const int nv = e.n - tile * kTileTokens;
-                uint32_t top = 0;
-#pragma unroll
-                for (int z = 0; z < 2; ++z)
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        const int tok = 8 * (g >> 1) + 4 * z + 2 * b + (g & 1);
-#pragma unroll
-                        for (int y = 0; y < D / 32; ++y) {
-                            uint4 x = make_uint4(0, 0, 0, 0);
-                            if (tok < nv) x = *reinterpret_cast<const uint4*>(k + tok * D + 64 * (y >> 1) + 16 * t + 8 * (y & 1));
-                            if (BF16) top = max_of(top, finite_only<BF16>(x));
-                            a[z][2 * y][b] = x.x;
-                            a[z][2 * y][2 + b] = x.y;
-                            a[z][2 * y + 1][b] = x.z;
-                            a[z][2 * y + 1][2 + b] = x.w;
-                        }
-                    }
-                if (BF16) {
-                    const int ex = warp_exponent<BF16>(top) - kExactK;
-                    ks = power2(ex);
-                    const float f = power2(-ex);
-#pragma unroll
-                    for (int z = 0; z < 2; ++z)
-#pragma unroll
-                        for (int y = 0; y < D / 16; ++y)
-#pragma unroll
-                            for (int x = 0; x < 4; ++x) a[z][y][x] = scaled_f16<BF16>(a[z][y][x], f);
-                }
-            }
-            const bool plain = (tile + 1) * kTileTokens <= e.n - e.q_len + row0 / p.r + 1;  // every row sees all of it
-            float2* out = sums + (int64_t)tile * e.pad;
-#pragma unroll 1
-            for (int o = 0; o < octets; ++o) {
-                float s[2][4] = {};
-#pragma unroll
-                for (int y = 0; y < kPieces; ++y) {
-                    const uint4 b = rows[(o * kPieces + y) * 32 + lane];
-#pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        mma16816(s[z], a[z][2 * y][0], a[z][2 * y][1], a[z][2 * y][2], a[z][2 * y][3], b.x, b.y);
-                        mma16816(s[z], a[z][2 * y + 1][0], a[z][2 * y + 1][1], a[z][2 * y + 1][2], a[z][2 * y + 1][3], b.z, b.w);
-                    }
-                }
-                const int r = 8 * o + 2 * t;
-                const float2 f = *reinterpret_cast<const float2*>(factor + r);
-                const float f0 = f.x * ks, f1 = f.y * ks;
-                int2 l = make_int2(INT_MAX, INT_MAX);
-                if (!plain) l = *reinterpret_cast<const int2*>(last + r);
-                const int pos = tile * kTileTokens + 8 * (g >> 1) + (g & 1);  // of a lane's first token; the others 4 z + 2 b on
-                float m0 = kNegInf, m1 = kNegInf;
-#pragma unroll
-                for (int z = 0; z < 2; ++z)
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        if (pos + 4 * z + 2 * b <= l.x) m0 = fmaxf(m0, s[z][2 * b] * f0);
-                        if (pos + 4 * z + 2 * b <= l.y) m1 = fmaxf(m1, s[z][2 * b + 1] * f1);
-                    }
-#pragma unroll
-                for (int d = 4; d < 32; d <<= 1) {
-                    m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, d));
-                    m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, d));
-                }
-                const float n0 = m0 == kNegInf ? 0.f : m0, n1 = m1 == kNegInf ? 0.f : m1;
-                float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-                for (int z = 0; z < 2; ++z)
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        if (pos + 4 * z + 2 * b <= l.x) l0 += ex2f(fmaf(s[z][2 * b], f0, -n0));
-                        if (pos + 4 * z + 2 * b <= l.y) l1 += ex2f(fmaf(s[z][2 * b + 1], f1, -n1));
-                    }
-#pragma unroll
-                for (int d = 4; d < 32; d <<= 1) {
-                    l0 += __shfl_xor_sync(0xffffffffu, l0, d);
-                    l1 += __shfl_xor_sync(0xffffffffu, l1, d);
-                }
-                if (g == 0) *reinterpret_cast<float4*>(out + r) = make_float4(m0, l0, m1, l1);
-            }
-        }
-        from = begin + tile1;
+        for (int k = 0; k < 2; ++k) mbar_init(bars + kQEmpty + k, 1);
+        mbar_init(bars + kDrain, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    constexpr int kIssuer = kWinSoftmax + kWinExpand;  // warp
+    if (w == kIssuer) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(smem + Sh::kTmem))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    // All of tensor memory is this CTA's, so it starts at address 0, and shared memory on 1024 bytes; both are counted on.
+    // Were it ever not so, the launch would do nothing but say so.
+    const bool placed = *reinterpret_cast<volatile uint32_t*>(smem + Sh::kTmem) == 0 && (smem_addr(smem) & 1023) == 0;
+    if (!placed && t == 0) atomicOr(err, kErrBadSlot);
+    if (!placed) {
+    } else if (w < kWinSoftmax) {
+        win_softmax<D>(p, smem, bars, err, t & 127, w >> 2, (uint32_t)(32 * (w & 3)) << 16);
+    } else if (w < kIssuer) {
+        win_expand<D, INT8, BF16>(p, smem, bars, err, (w >> 2) & 1, w & 3, lane);
+    } else if (w == kIssuer) {
+        win_issue<D>(p, smem_addr(smem), bars, err);
+    } else {
+        win_rows<D, BF16>(p, smem, bars, err, w - kIssuer - 1, lane);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (w == kIssuer) {
+        __syncwarp();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(*reinterpret_cast<volatile uint32_t*>(smem + Sh::kTmem))
+                     : "memory");
     }
 }
 
 // ---- shares of the blocks ----
-constexpr int kWeighWarps = 16, kWeighThreads = 32 * kWeighWarps;
+constexpr int kWeighThreads = 256;
 constexpr int kWeighRows = 128 * kBlockMaxRatio;  // rows of a KV head
 
-struct Sum {
-    float m, l;  // 2^m l
-    __device__ __forceinline__ void add(float om, float ol) {
-        const float top = fmaxf(m, om);
-        const float f = m == kNegInf ? 1.f : ex2f(m - top), of = om == kNegInf ? 1.f : ex2f(om - top);  // -inf: 0 or NaN
-        l = l * f + ol * of;
-        m = top;
-    }
-};
-
-// A CTA a (KV head, sequence). The rows' denominators first, a lane a row and the warps in turns of tiles; then the
-// blocks, a warp each.
+// A CTA some blocks of a (KV head, sequence): its rows' totals first, then p.lanes lanes a block.
 __global__ void __launch_bounds__(kWeighThreads) weigh_kernel(const __grid_constant__ BlockWeighParams p) {
-    __shared__ float top[kWeighRows], share[kWeighRows];  // of a row: its maximum, 1 / denominator (0: adds nothing)
-    __shared__ Sum part[kWeighWarps][32];
-    const BlockWeighSeq& e = p.seqs[blockIdx.y];
-    const int h = blockIdx.x, w = threadIdx.x >> 5, lane = threadIdx.x & 31, tiles = e.before + e.tiles;
-    const float2* sums = p.sums + e.sum_begin + (int64_t)h * tiles * e.pad;
-    int span = 1;  // lanes of a tile
-    while (span < min(e.rows, 32)) span *= 2;
-    for (int row0 = 0; row0 < e.rows; row0 += span) {
-        const int row = row0 + lane % span, step = 32 / span;
-        Sum s = {kNegInf, 0.f};
-        if (row < e.rows) {
-#pragma unroll 4
-            for (int k = w * step + lane / span; k < tiles; k += kWeighWarps * step) {
-                const float2 x = sums[(int64_t)k * e.pad + row];
-                s.add(x.x, x.y);
-            }
+    __shared__ float2 of[kWeighRows];  // of a row: its maximum, 1 / denominator (0: adds nothing)
+    const BlockWeighSeq& e = p.seqs[blockIdx.z];
+    const int h = blockIdx.y, t = threadIdx.x, blocks = (e.tiles + (1 << p.log2_tiles) - 1) >> p.log2_tiles;
+    const int first = blockIdx.x * p.blocks;
+    if (first >= blocks) return;
+    for (int row = t; row < e.rows; row += kWeighThreads) {
+        float2 s = make_float2(kNegInf, 0.f);
+        if (p.grid == 0) {
+            s = p.totals[(int64_t)e.row * p.hq + h * e.rows + row];
+        } else {  // the parts of the row's pair, of the CTAs that share it
+            const int steps = (e.tiles + 3) / 4, pair = h * ((e.rows + 127) / 128) + row / 128;
+            const int64_t u = e.unit_begin + (int64_t)pair * steps;
+            const int b0 = (int)(((u + 1) * p.grid - 1) / p.units), b1 = (int)(((u + steps) * p.grid - 1) / p.units);
+            for (int b = 2 * b0; b < 2 * b1 + 2; ++b)
+                s = joined(s, p.totals[((int64_t)(e.pair_begin + pair) * 2 + b) * 128 + row % 128]);
         }
-        for (int d = span; d < 32; d *= 2) s.add(__shfl_xor_sync(0xffffffffu, s.m, d), __shfl_xor_sync(0xffffffffu, s.l, d));
-        part[w][lane] = s;
-        __syncthreads();
-        if (w == 0 && lane < span && row < e.rows) {
-#pragma unroll
-            for (int z = 1; z < kWeighWarps; ++z) s.add(part[z][lane].m, part[z][lane].l);
-            if (e.lse_row >= 0) s.add(p.pre_lse[(int64_t)e.lse_row * p.hq + h * e.rows + row] + p.shift, 1.f);
-            top[row] = s.m;
-            share[row] = s.l > 0.f && s.l < -kNegInf ? 1.f / s.l : 0.f;
-        }
-        __syncthreads();
+        of[row] = make_float2(s.x, s.y > 0.f && s.y < -kNegInf ? 1.f / s.y : 0.f);
     }
-    const int blocks = (e.tiles + (1 << p.log2_tiles) - 1) >> p.log2_tiles;
+    __syncthreads();
+    const float2* sums = p.sums + e.sum_begin + ((int64_t)h * (e.before + e.tiles) + e.before) * e.pad;
     float* to = p.weights + ((int64_t)e.seq * p.hkv + h) * p.cols;
-    for (int b = w; b < blocks; b += kWeighWarps) {
-        const int t0 = b << p.log2_tiles, t1 = min(t0 + (1 << p.log2_tiles), e.tiles);
-        const float2* at = sums + (int64_t)(e.before + t0) * e.pad;
+    const int lane = t % p.lanes;
+    for (int b = first + t / p.lanes; b < first + p.blocks; b += kWeighThreads / p.lanes) {  // whole warps
+        const int t0 = b << p.log2_tiles, count = (min(t0 + (1 << p.log2_tiles), e.tiles) - t0) * e.pad;  // negative: none
+        const float2* at = sums + (int64_t)t0 * e.pad;
         float sum = 0.f;
+        int row = lane % e.pad;
 #pragma unroll 4
-        for (int k = lane; k < (t1 - t0) * e.pad; k += 32) {
-            const int row = k % e.pad;
-            if (row >= e.rows || share[row] == 0.f) continue;
-            const float2 x = at[k];
-            if (x.x != kNegInf) sum += x.y * ex2f(x.x - top[row]) * share[row];
+        for (int k = lane; k < count; k += p.lanes) {
+            const float2 x = at[k], f = row < e.rows ? of[row] : make_float2(0.f, 0.f);
+            if (f.y != 0.f && x.x != kNegInf) sum += x.y * ex2f(x.x - f.x) * f.y;
+            row += p.lanes;
+            if (row >= e.pad) row %= e.pad;
         }
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        if (lane == 0) to[b] += sum;
+        for (int d = p.lanes / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        if (lane == 0 && b < blocks) to[b] += sum;
     }
 }
 
 template <int D, bool INT8, bool BF16>
 int launch(const BlockWindowParams& p, cudaStream_t s) {
     static SmemOnce once;
-    const int e = once.allow(reinterpret_cast<const void*>(window_kernel<D, INT8, BF16>), kWindowRows * (2 * D + 12));
+    const int e = once.allow(reinterpret_cast<const void*>(window_kernel<D, INT8, BF16>), WinShape<D>::kSmem);
     if (e) return e;
-    window_kernel<D, INT8, BF16><<<p.grid, kWinThreads, (size_t)p.smem_rows * (2 * D + 12), s>>>(p);
+    window_kernel<D, INT8, BF16><<<p.grid, kWinThreads, WinShape<D>::kSmem, s>>>(p);
     return (int)cudaGetLastError();
 }
 
@@ -291,7 +430,7 @@ int launch_block_window(const BlockWindowParams& p, void* stream) {
 }
 
 int launch_block_weigh(const BlockWeighParams& p, void* stream) {
-    weigh_kernel<<<dim3(p.hkv, p.n_seqs), kWeighThreads, 0, (cudaStream_t)stream>>>(p);
+    weigh_kernel<<<dim3(p.most, p.hkv, p.n_seqs), kWeighThreads, 0, (cudaStream_t)stream>>>(p);
     return (int)cudaGetLastError();
 }
 

@@ -80,10 +80,11 @@ def test_workspace_sizes():
     assert size([0, 1], [5, -1], None) == up(rows * 128 * 4) + up(rows * 4)
     assert size([0, 1], [5, 5], [100, 3]) == up(103 * 8 * 128 * 4) + up(103 * 8 * 4)
     # tiles of 32 tokens, heads, 8 bytes
-    assert size([0, 1], None, None, False, True) == up((4 + 3) * 8 * 8)
-    assert size([2], None, None, False, True) == up(8 * 8)  # an empty sequence has one
-    assert size([0], None, [29], True, True) == up(5 * 8 * 8)
-    assert size([0], [5], None, False, True) == up(8 * 128 * 4) + up(8 * 4) + up((4 + 10) * 8 * 8)
+    # and a row's totals
+    assert size([0, 1], None, None, False, True) == up((4 + 3) * 8 * 8) + up(2 * 8 * 8)
+    assert size([2], None, None, False, True) == up(8 * 8) + up(8 * 8)  # an empty sequence has one
+    assert size([0], None, [29], True, True) == up(5 * 8 * 8) + up(29 * 8 * 8)
+    assert size([0], [5], None, False, True) == up(8 * 128 * 4) + up(8 * 4) + up((4 + 10) * 8 * 8) + up(8 * 8)
     for bad in (([6], None, None), ([0], [6], None), ([0], None, [-1])):
         refused(1, size, *bad)
     refused(1, K.kvarn_block_attend_workspace, c, 2, [0], None, None)
@@ -109,7 +110,12 @@ def test_window_refusals():
     refused(1, call, [0], [1], FAKE, W, None)
     refused(1, call, [0], [1], FAKE, W, SPACE + 8)
     refused(1, call, [0], [1], scale=float("inf"))
-    need = 8 * 2 * 4 * 16  # 4 tiles, 3 x 4 rows up to 16
+    size = lambda *a: K.kvarn_block_window_workspace(c, 0, *a)
+    # sums of 2 heads, 4 tiles, 3 x 4 rows up to 16; rows of 2 (pairs) + 2 (thread blocks), twice
+    need = 8 * 2 * 4 * 16 + (2 + 2) * 2 * 128 * 8
+    assert size([0], [3]) == need and size([2], [0]) == 0
+    for bad in (([6], [1]), ([0], [101]), ([0], [-1]), ([5], [129])):
+        refused(1, size, *bad)
     call([0], [3], n=need)
     refused(1, call, [0], [3], n=need - 1)
     refused(1, call, [0, 0], [1, 1])
@@ -215,6 +221,7 @@ def test_null_arguments():
     assert L.kvarn_block_attend_workspace(None, 0, 0, None, None, None, 0, 0, ctypes.byref(n)) == 1
     assert L.kvarn_block_attend(None, 0, 0, None, None, None, None, None, 1.0, None, None, 0, None) == 1
     assert L.kvarn_block_append_attend(None, 0, 0, None, None, None, None, 0, None, 0, None, None, 1.0, None, None, 0, None) == 1
+    assert L.kvarn_block_window_workspace(None, 0, 0, None, None, ctypes.byref(n)) == 1
     assert L.kvarn_block_window_weights(None, 0, 0, None, None, None, 1.0, None, None, 0, None) == 1
     assert L.kvarn_block_evict(None, 0, 0, None, 0, 0, 0, None, None, None) == 1
     c = cache()

@@ -189,7 +189,8 @@ def test_window_leaves_the_rest_of_its_workspace():
     fill(c, [300, 33], torch.float16, 600)
     q = tokens(10, 10, 128, torch.float16, 601, 0.3)
     w = torch.zeros(c.weights_shape, device="cuda")
-    n = 8 * 2 * (10 * 40 + 2 * 16)  # 7 x 5 and 3 x 5 rows, up to 8s
+    n = K.kvarn_block_window_workspace(c.handle, 0, [0, 1], [7, 3])
+    assert n > 0
     space = torch.full((n + 1024,), 0xa5, dtype=torch.uint8, device="cuda")
     base = (space.data_ptr() + 255) // 256 * 256 + 256
     K.kvarn_block_window_weights(c.handle, 0, [0, 1], [7, 3], q, 0.1, w, base, n, torch.cuda.current_stream().cuda_stream)
