@@ -138,6 +138,7 @@ struct BlockPrefillParams {
     BlockPrefillSeq seqs[kBlockMaxSeqs];
 };
 
+constexpr int kWindowParts = 4;  // softmax warpgroups of a window_weights launch
 // Weights of the last queries of sequences (K alone is read).
 struct BlockWindowSeq {
     int32_t seq, n, q_len, q_row;
@@ -153,7 +154,7 @@ struct BlockWindowParams {
     BlockView c;
     const uint16_t* q;
     float2* sums;        // of each sequence [Hkv][tiles][pad]: a tile's maximum and sum, by row
-    float2* totals;      // [pairs + grid][2][128]: a row's maximum and sum over part of its tokens
+    float2* totals;      // [pairs + grid][kWindowParts][128]: a row's maximum and sum over part of its tokens
     int32_t n_seqs, hq, r, grid;
     int64_t units;
     float scale_log2;

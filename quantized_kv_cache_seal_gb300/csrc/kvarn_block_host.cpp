@@ -587,7 +587,7 @@ kvarn_status plan_window(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, co
     p.units = units;
     p.grid = (int32_t)std::min<int64_t>(c->sms, units);
     w->totals = (size_t)(sums * 8 + 255) / 256 * 256;
-    w->total = p.n_seqs ? w->totals + (size_t)(pairs + p.grid) * 2 * 128 * 8 : 0;
+    w->total = p.n_seqs ? w->totals + (size_t)(pairs + p.grid) * kWindowParts * 128 * 8 : 0;
     return KVARN_OK;
 }
 

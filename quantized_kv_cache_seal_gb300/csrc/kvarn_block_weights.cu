@@ -15,22 +15,24 @@ namespace {
 // ---- logits of the last queries ----
 // S = Q code^T on tcgen05 (M = 128 rows, N = 128 tokens, f16 operands, exact codes, fp32 sums) as in prefill, and no more: a
 // unit of work is a step of 128 tokens for a tile of 128 rows of a (sequence, KV head), and the line of all units is cut evenly over
-// the CTAs, one a SM. Roles (608 threads): eight expansion warps that turn K codes into f16 tiles (a warp 32 tokens,
-// four warps every other step, four stages); one that issues the MMAs into four S buffers (all 512 columns of tensor
-// memory: no O is kept); two that load query rows, a tile ahead; two softmax warpgroups, every other step each, a thread a row. Every wait
+// the CTAs, one a SM. Roles (864 threads): eight expansion warps that turn K codes into f16 tiles (a warp 32 tokens,
+// four warps every other step); one that issues the MMAs into four S buffers (all 512 columns of tensor
+// memory: no O is kept); two that load query rows, a tile ahead; four softmax warpgroups, every fourth step each, a thread a row. Every wait
 // is bounded and sets the error word when it gives up.
-constexpr int kWinThreads = 608, kWinStep = 128, kWinStages = 4, kWinRing = 8;
-constexpr int kWinSoftmax = 8, kWinExpand = 8;  // warps
+constexpr int kWinThreads = 864, kWinStep = 128, kWinStages = 2, kWinRing = 8, kWinAhead = 2;
+constexpr int kWinSoftmax = 4 * kWindowParts, kWinExpand = 8;  // warps
 // barriers
 constexpr int kKFull = 0, kKEmpty = kKFull + kWinRing, kSFull = kKEmpty + kWinStages, kSEmpty = kSFull + 4, kQFull = kSEmpty + 4,
-              kQEmpty = kQFull + kWinRing, kDrain = kQEmpty + 2, kWinBars = kDrain + 1;
+              kQEmpty = kQFull + kWinRing, kDrain = kQEmpty + 2, kRawFull = kDrain + 1, kWinBars = kRawFull + kWinExpand * kWinAhead;
 
 template <int D>
 struct WinShape {
     static constexpr int kTile = D / 64 * kAtom;
     static constexpr int kQ = 0;                                   // 2 tiles
     static constexpr int kK = 2 * kTile;                           // kWinStages tiles
-    static constexpr int kScale = kK + kWinStages * kTile;         // float[kWinRing][4]: K scale of a step's parts
+    static constexpr int kRec = 16 + kTileTokens * D;              // scales and K codes of a tile
+    static constexpr int kRaw = kK + kWinStages * kTile;           // kWinAhead of an expansion warp
+    static constexpr int kScale = kRaw + kWinExpand * kWinAhead * kRec;  // float[kWinRing][4]: K scale of a step's parts
     static constexpr int kFactor = kScale + kWinRing * 16;         // float[kWinRing][128]: of a segment's rows
     static constexpr int kBars = kFactor + kWinRing * 512;
     static constexpr int kTmem = kBars + 8 * kWinBars;
@@ -61,7 +63,8 @@ struct WinWalk {
     }
 };
 
-// Warp wp (0 .. 3) of group `odd`: part wp of every other step. The next step's codes are on their way while one is expanded.
+// Warp wp (0 .. 3) of group `odd`: part wp of every other step. Codes come by bulk copies into a ring of the warp's own, two parts
+// ahead of the one that is expanded (one part ahead in registers, 32 KB in flight a SM, left the memory waiting), pool slots a part earlier.
 template <int D, bool INT8, bool BF16>
 __device__ __forceinline__ void win_expand(const BlockWindowParams& p, uint8_t* smem, uint64_t* bars, int32_t* err, int odd,
                                            int wp, int lane) {
@@ -81,7 +84,7 @@ __device__ __forceinline__ void win_expand(const BlockWindowParams& p, uint8_t* 
     };
     if (odd) skip();
     struct Part {
-        int step, seq, n, kvh, tile, slot;  // step -1: none
+        int step, seq, n, kvh, tile, slot;  // step -1: none; slot -1: exact tokens, or none
     };
     auto look = [&]() {
         Part x = {-1, 0, 0, 0, 0, -1};
@@ -93,51 +96,70 @@ __device__ __forceinline__ void win_expand(const BlockWindowParams& p, uint8_t* 
         skip();
         return x;
     };
-    uint4 x[kChunks];  // reloaded in place
-    float scale = 1.f;
-    auto record = [&](const Part& a) { return a.slot < 0 ? nullptr : tile_ptr(c, a.slot, a.kvh, a.tile & ((1 << sh) - 1)); };
-    auto load = [&](const uint8_t* rec, int i) { return __ldg(reinterpret_cast<const uint4*>(rec + 16 + i * 512) + lane); };
-    auto load_all = [&](const uint8_t* rec) {
-        if (!rec) return;
-#pragma unroll
-        for (int i = 0; i < kChunks; ++i) x[i] = load(rec, i);
-        scale = __ldg(reinterpret_cast<const float*>(rec));
+    uint8_t* ring = smem + Sh::kRaw + (4 * odd + wp) * kWinAhead * Sh::kRec;
+    uint64_t* landed = bars + kRawFull + (4 * odd + wp) * kWinAhead;
+    int issued = 0, done = 0;  // ring entries
+    bool ok = true;
+    auto fetch = [&](const Part& a) {
+        if (a.slot < 0 || !ok) return;
+        if (lane == 0) {
+            const int e = issued % kWinAhead;
+            mbar_arrive_expect_tx(landed + e, Sh::kRec);
+            bulk_g2s(ring + e * Sh::kRec, tile_ptr(c, a.slot, a.kvh, a.tile & ((1 << sh) - 1)), Sh::kRec, landed + e);
+        }
+        ++issued;
     };
-    Part now = look(), ahead = look();
-    load_all(record(now));
+    static_assert(kWinAhead == 2, "parts in hand");
+    Part now = look(), next = look(), then = look();
+    fetch(now);
+    fetch(next);
 #pragma unroll 1
     while (now.step >= 0) {
         const int s = now.step;
-        if (s >= kWinStages) bar_wait(bars + kKEmpty + s % kWinStages, (uint32_t)((s / kWinStages - 1) & 1), err);
+        bool here = true;
+        if (s >= kWinStages) here = bar_wait(bars + kKEmpty + s % kWinStages, (uint32_t)((s / kWinStages - 1) & 1), err);
         uint8_t* dst = smem + Sh::kK + s % kWinStages * Sh::kTile;
         float* head = reinterpret_cast<float*>(smem + Sh::kScale) + (s % kWinRing) * 4 + wp;
-        float f = scale;
-        const uint8_t* rec = record(ahead);
-        const Part then = look();
-        if (now.slot >= 0) {
+        float f = 1.f;
+        if (now.slot >= 0 && ok) {
+            const uint8_t* rec = ring + done % kWinAhead * Sh::kRec;
+            here = bar_wait(landed + done % kWinAhead, (uint32_t)(done / kWinAhead & 1), err) && here;
+            f = *reinterpret_cast<const float*>(rec);
             const int row0 = 32 * wp + 8 * (kg >> 1) + (kg & 1);
 #pragma unroll
             for (int i = 0; i < kChunks; ++i) {  // 16 channels of one token
+                const uint4 x = *reinterpret_cast<const uint4*>(rec + 16 + i * 512 + lane * 16);
                 const int z = i / (D / 32), cc = i / 2 % (D / 64), row = row0 + 4 * z + 2 * (i & 1);
-                const uint4 a = make_uint4(codes_lo<INT8>(x[i].x), codes_hi<INT8>(x[i].x), codes_lo<INT8>(x[i].y), codes_hi<INT8>(x[i].y));
-                const uint4 b = make_uint4(codes_lo<INT8>(x[i].z), codes_hi<INT8>(x[i].z), codes_lo<INT8>(x[i].w), codes_hi<INT8>(x[i].w));
-                if (rec) x[i] = load(rec, i);
-                *reinterpret_cast<uint4*>(dst + cc * kAtom + swz(row, 2 * t)) = a;
-                *reinterpret_cast<uint4*>(dst + cc * kAtom + swz(row, 2 * t + 1)) = b;
+                *reinterpret_cast<uint4*>(dst + cc * kAtom + swz(row, 2 * t)) =
+                    make_uint4(codes_lo<INT8>(x.x), codes_hi<INT8>(x.x), codes_lo<INT8>(x.y), codes_hi<INT8>(x.y));
+                *reinterpret_cast<uint4*>(dst + cc * kAtom + swz(row, 2 * t + 1)) =
+                    make_uint4(codes_lo<INT8>(x.z), codes_hi<INT8>(x.z), codes_lo<INT8>(x.w), codes_hi<INT8>(x.w));
             }
-            if (rec) scale = __ldg(reinterpret_cast<const float*>(rec));
-        } else {
+        } else if (now.slot < 0) {
             float2 hd;
             uint32_t bad;
+            uint4 x[kChunks];
             expand_exact<D, BF16, false>(c, now.seq, now.n, now.kvh, now.tile, wp, lane, dst, hd, bad, x);
             f = hd.x;
-            load_all(rec);
         }
+        ok = __all_sync(0xffffffffu, here) && ok;  // one answer for the warp; also: all lanes have read
+        if (now.slot >= 0 && ok) ++done;
         if (lane == 0) *head = f;
         fence_proxy_async_smem();
         mbar_arrive(bars + kKFull + s % kWinRing);
-        now = ahead;
-        ahead = then;
+        fetch(then);
+        now = next;
+        next = then;
+        then = look();
+    }
+    // Normally every copy was waited for above. After a wait that gave up nothing more was issued, and what is in flight
+    // lands (a bounded wait again) before the CTA's shared memory goes away.
+    if (!ok) {
+        const uint64_t t0 = global_ns();
+#pragma unroll 1
+        for (; done < issued; ++done)
+            while (!mbar_try_wait(landed + done % kWinAhead, (uint32_t)(done / kWinAhead & 1)) && global_ns() - t0 < kWaitLimitNs) {
+            }
     }
 }
 
@@ -230,78 +252,82 @@ __device__ __forceinline__ void win_rows(const BlockWindowParams& p, uint8_t* sm
     }
 }
 
-// Warpgroup b takes the steps of its parity; thread et owns row et.
+// Warpgroup b takes every fourth step, in its own S buffer; thread et owns row et.
 template <int D>
 __device__ __forceinline__ void win_softmax(const BlockWindowParams& p, uint8_t* smem, uint64_t* bars, int32_t* err, int et, int b,
                                             uint32_t lane_off) {
     using Sh = WinShape<D>;
+    const uint32_t ts = 128 * b + lane_off;
     int k = 0, seg = 0;
     WinWalk w(p);
 #pragma unroll 1
     for (; w.next(); ++seg) {
         const BlockWindowSeq& e = p.seqs[w.i];
-        const int row = w.tile * 128 + et, tiles = (e.n + kTileTokens - 1) / kTileTokens;
+        const int row = w.tile * 128 + et, tiles = (e.n + kTileTokens - 1) / kTileTokens, pad = e.pad;
         const bool valid = row < e.rows;
         const int pos = valid ? e.n - e.q_len + row / p.r : e.n - 1;
-        float2* out = p.sums + e.sum_begin + (int64_t)w.h * tiles * e.pad + row;
+        float2* out = p.sums + e.sum_begin + (int64_t)w.h * tiles * pad + row;
         float2 total = make_float2(kNegInf, 0.f);
         float qs = 1.f;
         bool first = true;
+        const int j0 = w.j0 + ((b - k) & 3);
+        k += w.j1 - w.j0;
 #pragma unroll 1
-        for (int j = w.j0; j < w.j1; ++j, ++k) {
-            if ((k & 1) != b) continue;
+        for (int j = j0, kk = k - (w.j1 - j0); j < w.j1; j += 4, kk += 4) {
             if (first) {
                 bar_wait(bars + kQFull + seg % kWinRing, (uint32_t)(seg / kWinRing & 1), err);
                 qs = reinterpret_cast<const float*>(smem + Sh::kFactor)[seg % kWinRing * 128 + et];
                 first = false;
             }
-            bar_wait(bars + kKFull + k % kWinRing, (uint32_t)(k / kWinRing & 1), err);
-            const float4 hd = reinterpret_cast<const float4*>(smem + Sh::kScale)[k % kWinRing];
-            bar_wait(bars + kSFull + (k & 3), (uint32_t)(k >> 2 & 1), err);
+            bar_wait(bars + kKFull + kk % kWinRing, (uint32_t)(kk / kWinRing & 1), err);
+            const float4 hd = reinterpret_cast<const float4*>(smem + Sh::kScale)[kk % kWinRing];
+            bar_wait(bars + kSFull + b, (uint32_t)(kk >> 2 & 1), err);
             __syncwarp();
             tc_fence_after();
             const int lim = pos + 1 - j * kWinStep;  // visible columns
             const bool plain = __all_sync(0xffffffffu, lim >= kWinStep);
+            float m[4], l[4];
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                uint32_t r[2][32];
-                tm_ld32(128 * (k & 3) + 64 * half + lane_off, r[0]);
-                tm_ld32(128 * (k & 3) + 64 * half + 32 + lane_off, r[1]);
+            for (int ch = 0; ch < 4; ++ch) {
+                uint32_t r[32];
+                tm_ld32(ts + 32 * ch, r);
                 tm_wait_ld();
-                if (half == 1) {  // S may be written again
+                if (ch == 3) {  // S may be written again
                     tc_fence_before();
-                    mbar_arrive(bars + kSEmpty + (k & 3));
+                    mbar_arrive(bars + kSEmpty + b);
                 }
+                const int left = lim - 32 * ch;
+                float c = qs * (ch == 0 ? hd.x : ch == 1 ? hd.y : ch == 2 ? hd.z : hd.w);
+                if (c < 1e-37f) c = 1e-37f;  // 0 would make -inf of a masked column NaN
+                if (!plain) {
 #pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    const int ch = 2 * half + y, left = lim - 32 * ch;
-                    float c = qs * (ch == 0 ? hd.x : ch == 1 ? hd.y : ch == 2 ? hd.z : hd.w);
-                    if (c < 1e-37f) c = 1e-37f;  // 0 would make -inf of a masked column NaN
-                    if (!plain) {
-#pragma unroll
-                        for (int z = 0; z < 32; ++z)
-                            if (z >= left) r[y][z] = 0xff800000u;
-                        if (left <= 0) c = 1.f;
-                    }
-                    const float m = max32(r[y]) * c, mm = m == kNegInf ? 0.f : m;
-                    const float2 c2 = make_float2(c, c), a2 = make_float2(-mm, -mm);
-                    float2 s0 = make_float2(0.f, 0.f), s1 = s0;
-#pragma unroll
-                    for (int z = 0; z < 16; ++z) {
-                        const float2 x = __ffma2_rn(make_float2(__uint_as_float(r[y][2 * z]), __uint_as_float(r[y][2 * z + 1])), c2, a2);
-                        const float2 v = make_float2(ex2f(x.x), ex2f(x.y));
-                        if (z & 1) s1 = __fadd2_rn(s1, v);
-                        else s0 = __fadd2_rn(s0, v);
-                    }
-                    s0 = __fadd2_rn(s0, s1);
-                    const float2 part = make_float2(m, s0.x + s0.y);
-                    total = joined(total, part);
-                    if (valid && 4 * j + ch < tiles) out[(int64_t)(4 * j + ch) * e.pad] = part;
+                    for (int z = 0; z < 32; ++z)
+                        if (z >= left) r[z] = 0xff800000u;
+                    if (left <= 0) c = 1.f;
                 }
+                m[ch] = max32(r) * c;
+                const float mm = m[ch] == kNegInf ? 0.f : m[ch];
+                const float2 c2 = make_float2(c, c), a2 = make_float2(-mm, -mm);
+                float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+#pragma unroll
+                for (int z = 0; z < 16; ++z) {
+                    const float2 x = __ffma2_rn(make_float2(__uint_as_float(r[2 * z]), __uint_as_float(r[2 * z + 1])), c2, a2);
+                    const float2 v = make_float2(ex2f(x.x), ex2f(x.y));
+                    if (z & 1) s1 = __fadd2_rn(s1, v);
+                    else s0 = __fadd2_rn(s0, v);
+                }
+                s0 = __fadd2_rn(s0, s1);
+                l[ch] = s0.x + s0.y;
+                if (valid && 4 * j + ch < tiles) out[(int64_t)(4 * j + ch) * pad] = make_float2(m[ch], l[ch]);
             }
+            const float top = fmaxf(max3(m[0], m[1], m[2]), fmaxf(m[3], total.x));
+            float sum = total.y * (total.x == kNegInf ? 1.f : ex2f(total.x - top));
+#pragma unroll
+            for (int ch = 0; ch < 4; ++ch) sum = fmaf(l[ch], m[ch] == kNegInf ? 1.f : ex2f(m[ch] - top), sum);
+            total = make_float2(top, sum);
         }
         // of the pair's part in this CTA (a pair's first CTA is no sooner than the pair before's last)
-        p.totals[((int64_t)(e.pair_begin + w.pair + blockIdx.x) * 2 + b) * 128 + et] = total;
+        p.totals[((int64_t)(e.pair_begin + w.pair + blockIdx.x) * kWindowParts + b) * 128 + et] = total;
     }
 }
 
@@ -324,6 +350,7 @@ __global__ void __launch_bounds__(kWinThreads, 1) window_kernel(const __grid_con
         }
         for (int k = 0; k < 2; ++k) mbar_init(bars + kQEmpty + k, 1);
         mbar_init(bars + kDrain, 1);
+        for (int k = 0; k < kWinExpand * kWinAhead; ++k) mbar_init(bars + kRawFull + k, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     constexpr int kIssuer = kWinSoftmax + kWinExpand;  // warp
@@ -378,8 +405,8 @@ __global__ void __launch_bounds__(kWeighThreads) weigh_kernel(const __grid_const
             const int steps = (e.tiles + 3) / 4, pair = h * ((e.rows + 127) / 128) + row / 128;
             const int64_t u = e.unit_begin + (int64_t)pair * steps;
             const int b0 = (int)(((u + 1) * p.grid - 1) / p.units), b1 = (int)(((u + steps) * p.grid - 1) / p.units);
-            for (int b = 2 * b0; b < 2 * b1 + 2; ++b)
-                s = joined(s, p.totals[((int64_t)(e.pair_begin + pair) * 2 + b) * 128 + row % 128]);
+            for (int b = kWindowParts * b0; b < kWindowParts * (b1 + 1); ++b)
+                s = joined(s, p.totals[((int64_t)(e.pair_begin + pair) * kWindowParts + b) * 128 + row % 128]);
         }
         of[row] = make_float2(s.x, s.y > 0.f && s.y < -kNegInf ? 1.f / s.y : 0.f);
     }
