@@ -101,7 +101,6 @@ struct BlockDecodeSeq {
     int32_t seq, n;
     int32_t unit_begin;        // prefix of Hkv * units; a unit is one tile
     int32_t units;             // of each KV head, at least 1
-    int32_t pre, pre_n;        // sequence whose pre_n tokens come before its own; pre_n = 0: none
 };
 struct BlockDecodeParams {
     BlockView c;
@@ -110,11 +109,15 @@ struct BlockDecodeParams {
     int32_t n_seqs, hq, r, grid;
     int64_t units;
     float scale_log2;          // softmax scale * log2(e)
+    BlockDecodeSeq seqs[kBlockMaxSeqs];
+};
+// What a decode launch with prefixes or weights has beside.
+struct BlockDecodeMore {
     float2* sums;              // [units][r] or null: maximum and sum of each tile's weights, by head
     float2* totals;            // [rows][Hq] (with sums): of each row over all its keys, a prefix's among them
     const float *pre_o, *pre_lse;  // rows finished over shared prefixes (pre_lse null: none), [rows][Hq][D] and [rows][Hq]
     uint32_t merged[kBlockMaxSeqs / 32];  // bit i: sequence entry i takes its row from there
-    BlockDecodeSeq seqs[kBlockMaxSeqs];
+    int32_t pre[kBlockMaxSeqs], pre_n[kBlockMaxSeqs];  // sequence whose pre_n tokens come before entry i's own (0: none)
 };
 
 struct BlockPrefillSeq {
@@ -132,10 +135,13 @@ struct BlockPrefillParams {
     int32_t line;        // 1: the steps of all segments are cut evenly over the CTAs; 0: CTAs take whole segments
     int32_t steps, segs; // of all sequences and KV heads
     float scale_log2;    // softmax scale * log2(e)
-    int32_t flat;        // 1: every query sees all of the entry's n tokens, and finished rows go to pre_o and pre_lse
-    float *pre_o, *pre_lse;  // f32 [rows][Hq][D], [rows][Hq]: written if flat; else added where merged says (null: nowhere)
-    uint32_t merged[kBlockMaxSeqs / 32];  // bit i: entry i
     BlockPrefillSeq seqs[kBlockMaxSeqs];
+};
+// What a prefill launch with prefixes has beside.
+struct BlockPrefillMore {
+    int32_t flat;        // 1: every query sees all of the entry's n tokens, and finished rows go to pre_o and pre_lse
+    float *pre_o, *pre_lse;  // f32 [rows][Hq][D], [rows][Hq]: written if flat; else added where merged says
+    uint32_t merged[kBlockMaxSeqs / 32];  // bit i: entry i
 };
 
 constexpr int kWindowParts = 4;  // softmax warpgroups of a window_weights launch
@@ -215,7 +221,9 @@ int launch_block_append(const BlockAppendSmall& p, void* stream);
 int launch_block_append(const BlockAppendLarge& p, void* stream);
 int launch_block_read(const BlockReadParams& p, void* stream);
 int launch_block_decode(const BlockDecodeParams& p, void* stream);
+int launch_block_decode(const BlockDecodeParams& p, const BlockDecodeMore& more, void* stream);
 int launch_block_prefill(const BlockPrefillParams& p, void* stream);
+int launch_block_prefill(const BlockPrefillParams& p, const BlockPrefillMore& more, void* stream);
 int launch_block_window(const BlockWindowParams& p, void* stream);
 int launch_block_weigh(const BlockWeighParams& p, void* stream);
 int launch_block_evict(const BlockEvictParams& p, void* stream);

@@ -25,10 +25,30 @@
 //
 // 16 sequences of 32k tokens, 32 / 8 heads, e4m3: 176 us, 6.1 TB/s of code bytes, 0.90 of a plain
 // copy's rate; 64 ragged sequences of 1k..16k, 40 / 10 heads, int8, bf16: 262 us, 5.7 TB/s.
+//
+// KVARN_BLOCK_MORE: the variant with prefixes and weights, a translation unit of its own (kvarn_block_decode_more.cu), so that
+// calls without them keep their code. A prefix's tiles stand in front of a sequence's own in its line, or its row over a
+// prefix walked once for many sequences is joined at the end; each tile's maximum and sum of weights go to `sums`.
 #include "kvarn_block_dev.cuh"
 
 namespace kvarn {
 namespace {
+
+#ifdef KVARN_BLOCK_MORE
+constexpr bool kMore = true;
+#define KVARN_MORE_PARAM , const __grid_constant__ BlockDecodeMore x
+typedef BlockDecodeMore More;
+#else
+constexpr bool kMore = false;
+#define KVARN_MORE_PARAM
+// (nothing of it is read)
+struct More {
+    float2 *sums, *totals;
+    const float *pre_o, *pre_lse;
+    uint32_t merged[1];
+    int32_t pre[1], pre_n[1];
+};
+#endif
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr float kShift = 15.f;  // weights are at most 2^15
@@ -91,21 +111,23 @@ struct Cursor {
     }
 };
 
-// Tile t of a sequence's line: of the prefix in front of it (where it has one here), then its own.
-struct TilePlace {
-    int seq, n, tile;
-};
-__device__ __forceinline__ TilePlace place_of(const BlockDecodeSeq& e, int t) {
-    const int before = (e.pre_n + kTileTokens - 1) / kTileTokens;
-    return t < before ? TilePlace{e.pre, e.pre_n, t} : TilePlace{e.seq, e.n, t - before};
-}
-
 // The warp's state for one (sequence, KV head); lane 4 g + t holds heads 2 t, 2 t + 1.
 template <int D>
 struct State {
     float m[2], l[2];
     float o[D / 16][4];  // O^T: channels 16 i + g (+ 8), heads 2 t, 2 t + 1
 };
+
+// Tile t of a sequence's line: of the prefix in front of it (where it has one here), then its own.
+struct TilePlace {
+    int seq, n, tile;
+};
+__device__ __forceinline__ TilePlace place_of(const BlockDecodeParams& p, const More& x, int i, int t) {
+    const BlockDecodeSeq& e = p.seqs[i];
+    if (!kMore) return TilePlace{e.seq, e.n, t};
+    const int before = (x.pre_n[i] + kTileTokens - 1) / kTileTokens;
+    return t < before ? TilePlace{x.pre[i], x.pre_n[i], t} : TilePlace{e.seq, e.n, t - before};
+}
 
 // Weights of 32 tokens from S^T (rows g, g + 8 of the two 16-token halves).
 // sums: where the tile's maximum and sum of each head go, or null.
@@ -160,7 +182,7 @@ __device__ __forceinline__ void weigh(State<D>& st, const float (&s)[2][4], floa
         }
     st.l[0] = fmaf(l0, ivs, st.l[0]);
     st.l[1] = fmaf(l1, ivs, st.l[1]);
-    if (sums) {
+    if (kMore && sums) {
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) {
             l0 += __shfl_xor_sync(0xffffffffu, l0, d);
@@ -288,8 +310,8 @@ __device__ __forceinline__ void exact_unit(State<D>& st, const uint16_t* k, cons
 // the pair, the part goes to the workspace, and whichever part comes last adds them all in the order of the
 // cuts. row: of the pair's first head in q and out.
 template <int D, bool BF16>
-__device__ void join_heads(const BlockDecodeParams& p, const uint8_t* smem, const Cursor& cur, bool whole, bool starts, int half,
-                           size_t row, int lane) {
+__device__ void join_heads(const BlockDecodeParams& p, const More& x, const uint8_t* smem, const Cursor& cur, bool whole,
+                           bool starts, int half, size_t row, int lane) {
     using Sh = Shape<D>;
     const float* join = reinterpret_cast<const float*>(smem + Sh::kJoin);
     const float* sm = reinterpret_cast<const float*>(smem + Sh::kM);
@@ -299,20 +321,20 @@ __device__ void join_heads(const BlockDecodeParams& p, const uint8_t* smem, cons
     constexpr size_t kPart = 8 * (D + 2);  // floats: O [8][D], m [8], l [8]
     float* partials = reinterpret_cast<float*>(p.c.base + p.c.lay.partials);
     float* mine = partials + (size_t)(2 * b + (starts ? 1 : 0)) * kPart;
-    const bool merged = p.pre_lse && (p.merged[cur.i >> 5] >> (cur.i & 31) & 1);
+    const bool merged = kMore && x.pre_lse && (x.merged[cur.i >> 5] >> (cur.i & 31) & 1);
     auto give = [&](int head, float4 o, float m, float l) {
         const float inv = l == 0.f ? 0.f : 1.f / l, u = kDenomUnit;
         float4 y = make_float4(o.x * u * inv, o.y * u * inv, o.z * u * inv, o.w * u * inv);
-        if (p.totals && lane == 0) {  // a prefix's 2^lse in units of l
+        if (kMore && x.totals && lane == 0) {  // a prefix's 2^lse in units of l
             float2 t = make_float2(m, l);
-            if (merged) t = joined(t, make_float2(p.pre_lse[row + head] + (kShift - 12.f), 1.f));
-            p.totals[row + head] = t;
+            if (merged) t = joined(t, make_float2(x.pre_lse[row + head] + (kShift - 12.f), 1.f));
+            x.totals[row + head] = t;
         }
-        if (merged) {  // with the finished row over the shared prefix
-            const float2 f = merge_factors(lse_of(m, l, kShift), p.pre_lse[row + head]);
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (live) x = *reinterpret_cast<const float4*>(p.pre_o + (row + head) * D + 4 * lane);
-            y = make_float4(merge(y.x, x.x, f), merge(y.y, x.y, f), merge(y.z, x.z, f), merge(y.w, x.w, f));
+        if (kMore && merged) {  // with the finished row over the shared prefix
+            const float2 f = merge_factors(lse_of(m, l, kShift), x.pre_lse[row + head]);
+            float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (live) z = *reinterpret_cast<const float4*>(x.pre_o + (row + head) * D + 4 * lane);
+            y = make_float4(merge(y.x, z.x, f), merge(y.y, z.y, f), merge(y.z, z.z, f), merge(y.w, z.w, f));
         }
         if (live)
             *reinterpret_cast<uint2*>(p.out + (row + head) * D + 4 * lane) =
@@ -410,8 +432,11 @@ __device__ void join_heads(const BlockDecodeParams& p, const uint8_t* smem, cons
 }
 
 template <int D, bool INT8, bool BF16>
-__global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_constant__ BlockDecodeParams p) {
+__global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_constant__ BlockDecodeParams p KVARN_MORE_PARAM) {
     using Sh = Shape<D>;
+#ifndef KVARN_BLOCK_MORE
+    const More x = {};
+#endif
     extern __shared__ __align__(128) uint8_t smem[];
     const BlockView& c = p.c;
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -442,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     auto seek = [&]() {
         if (ua >= u1) return;
         ahead.advance(p, ua);
-        const TilePlace e = place_of(p.seqs[ahead.i], ua - ahead.begin);
+        const TilePlace e = place_of(p, x, ahead.i, ua - ahead.begin);
         slot = -1;
         if (e.tile < e.n >> c.log2_block << sh) slot = __ldg(block_table(c, e.seq) + (e.tile >> sh));
     };
@@ -457,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     auto pump = [&]() {
 #pragma unroll 1
         while (ok && ua < u1 && issued - done + (slot < 0 ? 2 : 1) <= Sh::kStages) {
-            const TilePlace e = place_of(p.seqs[ahead.i], ua - ahead.begin);
+            const TilePlace e = place_of(p, x, ahead.i, ua - ahead.begin);
             const int tile = e.tile, sealed = e.n >> c.log2_block << sh;
             if (slot >= 0) {
                 entry(tile_ptr(c, slot, ahead.h, tile & ((1 << sh) - 1)), Sh::kTile);
@@ -527,9 +552,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
             for (int z = 0; z < 4; ++z) st.o[i][z] = 0.f;
         for (; u < end; u += kWarps) {
             if (!ok) continue;
-            const TilePlace e = place_of(p.seqs[cur.i], u - cur.begin);
+            const TilePlace e = place_of(p, x, cur.i, u - cur.begin);
             const int tile = e.tile, sealed = e.n >> c.log2_block << sh;
-            float2* sums = p.sums ? p.sums + (size_t)u * p.r : nullptr;
+            float2* sums = kMore && x.sums ? x.sums + (size_t)u * p.r : nullptr;
             bool landed = true;
             int entries = 0;
             if (tile < sealed) {
@@ -544,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                 exact_unit<D, BF16>(st, reinterpret_cast<const uint16_t*>(ring + s * Sh::kTile),
                                     reinterpret_cast<const uint16_t*>(ring + s2 * Sh::kTile), nv, q, c0, c1, lane, p.r, sums);
                 entries = 2;
-            } else if (sums && lane < p.r) {
+            } else if (kMore && sums && lane < p.r) {
                 sums[lane] = make_float2(kNegInf, 0.f);  // an empty sequence
             }
             // one answer for the warp, after the products that need not wait for it; also: all lanes have read
@@ -587,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
             if (lane == 0) n = atomicAdd(count, 1);
             if (__shfl_sync(0xffffffffu, n, 0) == kWarps - 1) {
                 __threadfence_block();
-                join_heads<D, BF16>(p, smem, cur, whole, begin == cur.begin, half, (size_t)cur.i * p.hq + h0, lane);
+                join_heads<D, BF16>(p, x, smem, cur, whole, begin == cur.begin, half, (size_t)cur.i * p.hq + h0, lane);
                 __syncwarp();
                 if (lane == 0) {
                     *count = 0;
@@ -608,28 +633,36 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     }
 }
 
+#ifdef KVARN_BLOCK_MORE
+#define KVARN_ARGS p, x
+#define KVARN_PARAMS const BlockDecodeParams &p, const BlockDecodeMore &x
+#else
+#define KVARN_ARGS p
+#define KVARN_PARAMS const BlockDecodeParams& p
+#endif
+
 template <int D, bool INT8, bool BF16>
-int launch(const BlockDecodeParams& p, cudaStream_t s) {
+int launch(KVARN_PARAMS, cudaStream_t s) {
     static SmemOnce once;
     const int e = once.allow(reinterpret_cast<const void*>(decode_kernel<D, INT8, BF16>), Shape<D>::kSmem);
     if (e) return e;
-    decode_kernel<D, INT8, BF16><<<p.grid, kThreads, Shape<D>::kSmem, s>>>(p);
+    decode_kernel<D, INT8, BF16><<<p.grid, kThreads, Shape<D>::kSmem, s>>>(KVARN_ARGS);
     return (int)cudaGetLastError();
 }
 
 }  // namespace
 
-int launch_block_decode(const BlockDecodeParams& p, void* stream) {
+int launch_block_decode(KVARN_PARAMS, void* stream) {
     cudaStream_t s = (cudaStream_t)stream;
     switch ((p.c.d == 128 ? 4 : 0) + (p.c.int8 ? 2 : 0) + (p.c.bf16 ? 1 : 0)) {
-        case 0: return launch<64, false, false>(p, s);
-        case 1: return launch<64, false, true>(p, s);
-        case 2: return launch<64, true, false>(p, s);
-        case 3: return launch<64, true, true>(p, s);
-        case 4: return launch<128, false, false>(p, s);
-        case 5: return launch<128, false, true>(p, s);
-        case 6: return launch<128, true, false>(p, s);
-        default: return launch<128, true, true>(p, s);
+        case 0: return launch<64, false, false>(KVARN_ARGS, s);
+        case 1: return launch<64, false, true>(KVARN_ARGS, s);
+        case 2: return launch<64, true, false>(KVARN_ARGS, s);
+        case 3: return launch<64, true, true>(KVARN_ARGS, s);
+        case 4: return launch<128, false, false>(KVARN_ARGS, s);
+        case 5: return launch<128, false, true>(KVARN_ARGS, s);
+        case 6: return launch<128, true, false>(KVARN_ARGS, s);
+        default: return launch<128, true, true>(KVARN_ARGS, s);
     }
 }
 

@@ -304,13 +304,19 @@ kvarn_status run_weigh(kvarn_block_cache* c, BlockWeighParams& p, void* stream) 
     p.hkv = c->cfg.num_kv_heads;
     p.log2_tiles = c->view.log2_block - 5;
     p.cols = (int32_t)columns(c);
-    // Lanes enough for a block's sums two at a time; of blocks two rounds of 256 threads a CTA, so that there are many
-    // CTAs and the rows' totals are still shared by some blocks.
+    // Lanes enough for a block's sums two at a time; a CTA one round of blocks, or more where that still makes eight CTAs
+    // a SM: every CTA looks its rows' totals up.
     int32_t pad = 1, tiles = 1;
-    for (int i = 0; i < p.n_seqs; ++i) pad = std::max(pad, p.seqs[i].pad), tiles = std::max(tiles, p.seqs[i].tiles);
+    int64_t blocks = 0;
+    for (int i = 0; i < p.n_seqs; ++i) {
+        pad = std::max(pad, p.seqs[i].pad);
+        tiles = std::max(tiles, p.seqs[i].tiles);
+        blocks += (int64_t)p.hkv * (((p.seqs[i].tiles - 1) >> p.log2_tiles) + 1);
+    }
     p.lanes = 1;
     while (p.lanes < 32 && p.lanes * 2 < pad << p.log2_tiles) p.lanes *= 2;
-    p.blocks = 2 * 256 / p.lanes;
+    p.blocks = 256 / p.lanes;
+    while (p.blocks < 8 * 256 / p.lanes && blocks / (2 * p.blocks) > 8 * c->sms) p.blocks *= 2;
     p.most = (((tiles - 1) >> p.log2_tiles) + p.blocks) / p.blocks;
     const int rc = launch_block_weigh(p, stream);
     return rc ? cuda_fail(rc, "weights launch") : KVARN_OK;
@@ -319,6 +325,8 @@ kvarn_status run_weigh(kvarn_block_cache* c, BlockWeighParams& p, void* stream) 
 kvarn_status run_decode(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* ids, const void* q, void* out,
                         float scale, void* stream, const Beside& beside = Beside()) {
     static thread_local BlockDecodeParams p;
+    static thread_local BlockDecodeMore x;
+    const bool more = beside.before || beside.finished || beside.sums;
     p.c = c->view;
     p.c.layer = layer;
     p.q = (const uint16_t*)q;
@@ -333,17 +341,22 @@ kvarn_status run_decode(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, con
         e.seq = ids[i];
         e.n = c->L(ids[i], layer);
         e.unit_begin = (int32_t)units;
-        e.pre = beside.before ? beside.before[i] : -1;
-        e.pre_n = e.pre >= 0 ? c->L(e.pre, layer) : 0;
-        e.units = e.pre_n > 0 ? tiles_of(e.pre_n) + tiles_of(e.n) : head_tiles(e.n);
+        e.units = head_tiles(e.n);
+        if (more) {
+            x.pre[i] = beside.before ? beside.before[i] : -1;
+            x.pre_n[i] = x.pre[i] >= 0 ? c->L(x.pre[i], layer) : 0;
+            if (x.pre_n[i] > 0) e.units = tiles_of(x.pre_n[i]) + tiles_of(e.n);
+        }
         units += (int64_t)e.units * c->cfg.num_kv_heads;
     }
     p.units = units;
-    p.sums = beside.sums;
-    p.totals = beside.totals;
-    p.pre_o = beside.pre_o;
-    p.pre_lse = beside.pre_lse;
-    mark(p.merged, beside.finished, n_seqs);
+    if (more) {
+        x.sums = beside.sums;
+        x.totals = beside.totals;
+        x.pre_o = beside.pre_o;
+        x.pre_lse = beside.pre_lse;
+        mark(x.merged, beside.finished, n_seqs);
+    }
     // One CTA a SM, each of its eight warps a unit at least. Equal short sequences: whole (sequence, KV
     // head) pairs, so that nothing is joined across CTAs (which takes about as long as four rounds).
     const int64_t pairs = (int64_t)n_seqs * c->cfg.num_kv_heads, most = std::min(c->sms, kBlockMaxGrid);
@@ -352,7 +365,7 @@ kvarn_status run_decode(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, con
     if (c->host_only) return KVARN_OK;
     const kvarn_status st = ensure_init(c, stream);
     if (st) return st;
-    const int rc = launch_block_decode(p, stream);
+    const int rc = more ? launch_block_decode(p, x, stream) : launch_block_decode(p, stream);
     if (rc) return cuda_fail(rc, "decode launch");
     if (!beside.weights) return KVARN_OK;
     static thread_local BlockWeighParams wp;
@@ -366,7 +379,7 @@ kvarn_status run_decode(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, con
         BlockWeighSeq& s = wp.seqs[i];
         s.seq = e.seq;
         s.rows = s.pad = c->r;
-        s.before = tiles_of(e.pre_n);
+        s.before = tiles_of(x.pre_n[i]);
         s.tiles = e.units - s.before;
         s.row = i;
         s.unit_begin = s.pair_begin = 0;
@@ -414,6 +427,7 @@ kvarn_status run_prefill(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, co
 kvarn_status run_tiles(kvarn_block_cache* c, int32_t layer, int32_t n_entries, const Entry* entries, bool flat, const void* q,
                        void* out, float scale, void* stream, const Beside& beside) {
     static thread_local BlockPrefillParams p;
+    static thread_local BlockPrefillMore x;
     p.c = c->view;
     p.c.layer = layer;
     p.q = (const uint16_t*)q;
@@ -421,9 +435,6 @@ kvarn_status run_tiles(kvarn_block_cache* c, int32_t layer, int32_t n_entries, c
     p.hq = c->cfg.num_q_heads;
     p.r = c->r;
     p.scale_log2 = scale * kLog2e;
-    p.flat = flat;
-    p.pre_o = beside.pre_o;
-    p.pre_lse = beside.pre_lse;
     p.n_seqs = 0;
     const int hkv = c->cfg.num_kv_heads;
     for (int i = 0; i < n_entries; ++i) {
@@ -451,7 +462,10 @@ kvarn_status run_tiles(kvarn_block_cache* c, int32_t layer, int32_t n_entries, c
         segs += (int64_t)e.pairs * hkv;
         steps += (int64_t)e.head_steps * hkv;
     }
-    mark(p.merged, finished, p.n_seqs);
+    x.flat = flat;
+    x.pre_o = beside.pre_o;
+    x.pre_lse = beside.pre_lse;
+    mark(x.merged, finished, p.n_seqs);
     // Whole segments, the longest first, end when the longest does or the SMs have shared out all;
     // the line of all steps cut evenly ends a share of the steps later, and then costs about four more
     // for the partial results and the kernel that adds them (6 us where a step takes 1.5).
@@ -465,7 +479,7 @@ kvarn_status run_tiles(kvarn_block_cache* c, int32_t layer, int32_t n_entries, c
     if (c->host_only) return KVARN_OK;
     const kvarn_status st = ensure_init(c, stream);
     if (st) return st;
-    const int rc = launch_block_prefill(p, stream);
+    const int rc = beside.pre_lse ? launch_block_prefill(p, x, stream) : launch_block_prefill(p, stream);
     return rc ? cuda_fail(rc, "prefill launch") : KVARN_OK;
 }
 

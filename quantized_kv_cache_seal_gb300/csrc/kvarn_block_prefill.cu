@@ -32,10 +32,29 @@
 // of the causal products), 512 queries against 32,768 tokens 208 us (1,310 TFLOP/s). The prompt takes 110
 // us where its 75 MB stay in L2 from one call to the next, and 107 with normal values, on which no warp
 // ever rescales O (28 % of a warp's steps do with outlier channels and token norms of a wide spread).
+//
+// KVARN_BLOCK_MORE: the variant with prefixes, a translation unit of its own (kvarn_block_prefill_more.cu), so that calls
+// without them keep their code. `flat`: a segment's rows are queries of many sequences and see all of a prefix; their
+// finished rows go to fp32. Otherwise rows take their share of such rows at the end.
 #include "kvarn_block_tc.cuh"
 
 namespace kvarn {
 namespace {
+
+#ifdef KVARN_BLOCK_MORE
+constexpr bool kMore = true;
+#define KVARN_MORE_PARAM , const __grid_constant__ BlockPrefillMore x
+typedef BlockPrefillMore More;
+#else
+constexpr bool kMore = false;
+#define KVARN_MORE_PARAM
+// (nothing of it is read)
+struct More {
+    int32_t flat;
+    float *pre_o, *pre_lse;
+    uint32_t merged[1];
+};
+#endif
 
 constexpr int kThreads = 512;
 constexpr int kRegsLaunch = 128, kRegsSoftmax = 184, kRegsExpand = 112, kRegsIssue = 32;
@@ -82,8 +101,8 @@ __device__ __forceinline__ void tm_st16(uint32_t taddr, const uint32_t (&r)[16])
 }
 // ---- the line of steps ----
 // Steps of a query tile pair: up to the last position that its queries see.
-__device__ __forceinline__ int pair_steps(const BlockPrefillParams& p, const BlockPrefillSeq& e, int pair, int pair_tokens) {
-    if (p.flat) return (e.n - 1) / kStep + 1;
+__device__ __forceinline__ int pair_steps(const More& x, const BlockPrefillSeq& e, int pair, int pair_tokens) {
+    if (kMore && x.flat) return (e.n - 1) / kStep + 1;
     return (e.n - e.q_len + min((pair + 1) * pair_tokens, e.q_len) - 1) / kStep + 1;
 }
 
@@ -96,15 +115,16 @@ struct Seg {
 // The segments of CTA b's range of the line, in order.
 struct LineWalk {
     const BlockPrefillParams& p;
+    const More& x;
     int pt, left;  // query tokens of a pair; steps of the range from this segment's j0 on
     Seg s;
     __device__ __forceinline__ void set() {
         const BlockPrefillSeq& e = p.seqs[s.i];
-        s.steps = pair_steps(p, e, s.pair, pt);
+        s.steps = pair_steps(x, e, s.pair, pt);
         s.j1 = left > 0 ? min(s.steps, s.j0 + left) : 0;
         s.two = (2 * s.pair + 1) * (pt / 2) < e.q_len;
     }
-    __device__ __forceinline__ LineWalk(const BlockPrefillParams& p_, int b) : p(p_), pt(2 * (128 / p_.r)) {
+    __device__ __forceinline__ LineWalk(const BlockPrefillParams& p_, const More& x_, int b) : p(p_), x(x_), pt(2 * (128 / p_.r)) {
         const int u0 = (int)((int64_t)p.steps * b / p.grid), u1 = (int)((int64_t)p.steps * (b + 1) / p.grid);
         int i = 0;
 #pragma unroll 1
@@ -116,7 +136,7 @@ struct LineWalk {
         rel -= s.kvh * e.head_steps;
         s.pair = e.pairs - 1;
 #pragma unroll 1
-        while (rel >= (n = pair_steps(p, e, s.pair, pt))) rel -= n, --s.pair;
+        while (rel >= (n = pair_steps(x, e, s.pair, pt))) rel -= n, --s.pair;
         s.j0 = rel;
         left = u1 - u0;
         set();
@@ -136,9 +156,9 @@ struct LineWalk {
 // Hands out a CTA's segments to its roles: the line's, or whole ones, the longest first, as the CTAs
 // get to them (the first by the CTA's index, the next from a counter; the last CTA to run out sets
 // the counters back for the next call). One entry is made ahead of what the expansion has taken.
-__device__ __forceinline__ void feed_role(const BlockPrefillParams& p, uint64_t* bars, int32_t* err) {
+__device__ __forceinline__ void feed_role(const BlockPrefillParams& p, const More& x, uint64_t* bars, int32_t* err) {
     int32_t* counters = reinterpret_cast<int32_t*>(p.c.base + p.c.lay.counters);
-    LineWalk line(p, p.line ? blockIdx.x : 0);
+    LineWalk line(p, x, p.line ? blockIdx.x : 0);
     Seg* ring = reinterpret_cast<Seg*>(bars + kNumBars);
     bool ok = true;
 #pragma unroll 1
@@ -405,7 +425,7 @@ __device__ __forceinline__ void add_non_finite(const BlockView& c, const BlockPr
 
 // ---- softmax: thread et owns row et of tile b ----
 template <int D, bool BF16>
-__device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, uint8_t* smem, uint64_t* bars, uint32_t tmem,
+__device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, const More& x, uint8_t* smem, uint64_t* bars, uint32_t tmem,
                                              int32_t* err, int et, int b, uint32_t lane_off) {
     using Sh = Shape<D>;
     const uint32_t ts = tmem + kColS + 128 * b + lane_off, to = tmem + kColO + 128 * b + lane_off;
@@ -430,7 +450,7 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, uint8_
         const int tok = (2 * w.s.pair + b) * tpt + tok_in;
         const bool valid = tok_in < tpt && tok < e.q_len;
         const int row = valid ? (e.q_row + tok) * p.hq + w.s.kvh * p.r + head_in : -1;  // of q and out
-        const int pos = valid && !p.flat ? e.n - e.q_len + tok : e.n - 1;
+        const int pos = valid && !(kMore && x.flat) ? e.n - e.q_len + tok : e.n - 1;
         float qs = scale;
         {
             // D / 8 lanes a row; loops stay short: this code runs once a segment, from a cold cache
@@ -569,33 +589,33 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, uint8_
         auto take = [&](int piece, int k) {  // 16 bytes of row 4 k + lane / 8
             return *reinterpret_cast<const uint4*>(rows + piece * kAtom + swz(4 * k + (lane >> 3), lane & 7));
         };
-        const bool whole = w.whole();
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        if (whole && !p.flat) {
-            const bool merged = p.pre_lse && (p.merged[w.s.i >> 5] >> (w.s.i & 31) & 1);
-            if (merged) {  // the finished rows over the shared prefix, in units of O
-                float2 f = make_float2(1.f, 0.f);
-                if (valid) f = merge_factors(lse_of(m, l, kShift), p.pre_lse[row]);
-                const float scale_o = kDenomUnit * inv * f.x;
+        if (kMore && x.pre_lse && !x.flat && w.whole() && (x.merged[w.s.i >> 5] >> (w.s.i & 31) & 1)) {
+            // the finished rows over the shared prefix, in units of O
+            float2 f = make_float2(1.f, 0.f);
+            if (valid) f = merge_factors(lse_of(m, l, kShift), x.pre_lse[row]);
+            f.x *= l == 0.f ? 0.f : 1.f / l;
+            f.y *= 1.f / kDenomUnit;
+            l = 1.f;
 #pragma unroll 1
-                for (int ch = 0; ch < D / 32; ++ch) {
-                    uint32_t x[32];
-                    tm_ld32(to + 32 * ch, x);
-                    tm_wait_ld();
+            for (int ch = 0; ch < D / 32; ++ch) {
+                uint32_t o[32];
+                tm_ld32(to + 32 * ch, o);
+                tm_wait_ld();
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (valid) y = *reinterpret_cast<const float4*>(p.pre_o + (size_t)row * D + 32 * ch + 4 * k);
-                        x[4 * k] = __float_as_uint(fmaf(__uint_as_float(x[4 * k]), scale_o, y.x * f.y));
-                        x[4 * k + 1] = __float_as_uint(fmaf(__uint_as_float(x[4 * k + 1]), scale_o, y.y * f.y));
-                        x[4 * k + 2] = __float_as_uint(fmaf(__uint_as_float(x[4 * k + 2]), scale_o, y.z * f.y));
-                        x[4 * k + 3] = __float_as_uint(fmaf(__uint_as_float(x[4 * k + 3]), scale_o, y.w * f.y));
-                    }
-                    tm_st32(to + 32 * ch, x);
+                for (int k = 0; k < 8; ++k) {
+                    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (valid) y = *reinterpret_cast<const float4*>(x.pre_o + (size_t)row * D + 32 * ch + 4 * k);
+                    o[4 * k] = __float_as_uint(merge(__uint_as_float(o[4 * k]), y.x, f));
+                    o[4 * k + 1] = __float_as_uint(merge(__uint_as_float(o[4 * k + 1]), y.y, f));
+                    o[4 * k + 2] = __float_as_uint(merge(__uint_as_float(o[4 * k + 2]), y.z, f));
+                    o[4 * k + 3] = __float_as_uint(merge(__uint_as_float(o[4 * k + 3]), y.w, f));
                 }
-                tm_wait_st();
+                tm_st32(to + 32 * ch, o);
             }
-            const float unit = merged ? 1.f : kDenomUnit, times = merged ? 1.f : inv;
+            tm_wait_st();
+        }
+        if (w.whole() && !(kMore && x.flat)) {
+            const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
             for (int piece = 0; piece < D / 64; ++piece) {
                 uint32_t x[2][32], o[32];
@@ -604,8 +624,8 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, uint8_
                 tm_wait_ld();
 #pragma unroll
                 for (int k = 0; k < 32; ++k)
-                    o[k] = pack2<BF16>(__uint_as_float(x[k >> 4][2 * k & 31]) * unit * times,
-                                       __uint_as_float(x[k >> 4][(2 * k & 31) + 1]) * unit * times);
+                    o[k] = pack2<BF16>(__uint_as_float(x[k >> 4][2 * k & 31]) * kDenomUnit * inv,
+                                       __uint_as_float(x[k >> 4][(2 * k & 31) + 1]) * kDenomUnit * inv);
                 give(piece, o);
             }
             __syncwarp();
@@ -622,38 +642,52 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, uint8_
                 __syncwarp();  // the row is there
                 if (valid) add_non_finite<D, BF16>(p.c, e, w.s.kvh, 0, pos + 1, p.out + (size_t)row * D, nullptr);
             }
-        } else {  // fp32 rows: a part of the segment to the workspace, or a finished row over a shared prefix
+        } else if (kMore && w.whole()) {  // a finished row over a shared prefix, in fp32
+            const float inv = kDenomUnit * (l == 0.f ? 0.f : 1.f / l);
+#pragma unroll 1
+            for (int ch = 0; ch < D / 32; ++ch) {
+                uint32_t o[32];
+                tm_ld32(to + 32 * ch, o);
+                tm_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * inv);
+                give(0, o);
+                __syncwarp();
+#pragma unroll 4
+                for (int k = 0; k < 8; ++k) {
+                    const int at = __shfl_sync(0xffffffffu, row, 4 * k + (lane >> 3));
+                    const uint4 y = take(0, k);
+                    if (at >= 0) *reinterpret_cast<uint4*>(x.pre_o + (size_t)at * D + 32 * ch + 4 * (lane & 7)) = y;
+                }
+                __syncwarp();
+            }
+            if (__builtin_expect(bad, 0) && valid)
+                add_non_finite<D, BF16>(p.c, e, w.s.kvh, 0, pos + 1, nullptr, x.pre_o + (size_t)row * D);
+            if (valid) x.pre_lse[row] = lse_of(m, l, kShift);
+        } else {
             float* part = reinterpret_cast<float*>(p.c.base + p.c.lay.partials) +
                           (size_t)(2 * blockIdx.x + (w.s.j0 == 0 ? 1 : 0)) * (256 * (D + 2));
-            const int to_row = whole ? row : 128 * b + et;  // -1: a row without a query (of a part it is not read back)
-            float* dst = whole ? p.pre_o : part;
-            const float times = whole ? kDenomUnit * inv : 1.f;
-            if (__any_sync(0xffffffffu, row >= 0)) {
+            const int first = 128 * b + (et & 96);
+            if (__any_sync(0xffffffffu, row >= 0)) {  // (rows without a query are not read back)
 #pragma unroll 1
                 for (int ch = 0; ch < D / 32; ++ch) {
                     uint32_t x[32];
                     tm_ld32(to + 32 * ch, x);
                     tm_wait_ld();
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * times);
                     give(0, x);
                     __syncwarp();
 #pragma unroll 4
                     for (int k = 0; k < 8; ++k) {
-                        const int rr = __shfl_sync(0xffffffffu, to_row, 4 * k + (lane >> 3));
-                        if (rr >= 0) *reinterpret_cast<uint4*>(dst + (size_t)rr * D + 32 * ch + 4 * (lane & 7)) = take(0, k);
+                        const int rr = first + 4 * k + (lane >> 3);
+                        *reinterpret_cast<uint4*>(part + (size_t)rr * D + 32 * ch + 4 * (lane & 7)) = take(0, k);
                     }
                     __syncwarp();
                 }
                 if (__builtin_expect(bad, 0) && valid)
                     add_non_finite<D, BF16>(p.c, e, w.s.kvh, w.s.j0 * kStep, min(pos + 1, w.s.j1 * kStep), nullptr,
-                                            dst + (size_t)to_row * D);
-                if (!whole) {
-                    part[256 * D + 128 * b + et] = m;
-                    part[256 * D + 256 + 128 * b + et] = l;
-                } else if (valid) {
-                    p.pre_lse[row] = lse_of(m, l, kShift);
-                }
+                                            part + (size_t)(128 * b + et) * D);
+                part[256 * D + 128 * b + et] = m;
+                part[256 * D + 256 + 128 * b + et] = l;
             }
         }
         __syncwarp();
@@ -662,7 +696,10 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, uint8_
 }
 
 template <int D, bool INT8, bool BF16>
-__global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_constant__ BlockPrefillParams p) {
+__global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_constant__ BlockPrefillParams p KVARN_MORE_PARAM) {
+#ifndef KVARN_BLOCK_MORE
+    const More x = {};
+#endif
     using Sh = Shape<D>;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int t = threadIdx.x, w = t >> 5, lane = t & 31, wg = w >> 2;
@@ -706,14 +743,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     if (!placed) {
     } else if (wg < 2) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-        softmax_role<D, BF16>(p, smem, bars, tmem, err, t & 127, wg, lane_off);
+        softmax_role<D, BF16>(p, x, smem, bars, tmem, err, t & 127, wg, lane_off);
     } else if (wg == 2) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsExpand));
         expand_role<D, INT8, BF16>(p, smem, bars, err, w & 3, lane);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
         if (w == 12) issue_role<D>(smem_addr(smem), bars, err);
-        else if (w == 13 && lane == 0) feed_role(p, bars, err);
+        else if (w == 13 && lane == 0) feed_role(p, x, bars, err);
     }
     tc_fence_before();
     __syncthreads();
@@ -730,11 +767,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 // sums 32 at a time, a lane each, then their rows eight at a time. blockIdx.y: kCombineRows rows.
 constexpr int kCombineThreads = 256;
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_constant__ BlockPrefillParams p) {
+__global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_constant__ BlockPrefillParams p KVARN_MORE_PARAM) {
+#ifndef KVARN_BLOCK_MORE
+    const More x = {};
+#endif
     constexpr int kCombineRows = kCombineThreads / 32;
     const int b = blockIdx.x, lane = threadIdx.x & 31;
     const int u0 = (int)((int64_t)p.steps * b / p.grid), u1 = (int)((int64_t)p.steps * (b + 1) / p.grid);
-    LineWalk w(p, b);
+    LineWalk w(p, x, b);
     int u = u0;
 #pragma unroll 1
     while (u + (w.s.j1 - w.s.j0) < u1) u += w.s.j1 - w.s.j0, w.next();
@@ -782,45 +822,60 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_c
         }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l, y = kDenomUnit;
-    const size_t at = (size_t)(e.q_row + tok) * p.hq + w.s.kvh * p.r + et % p.r, row = at * D;
-    o = make_float4(o.x * y * inv, o.y * y * inv, o.z * y * inv, o.w * y * inv);
-    if (p.flat) {
-        if (live) *reinterpret_cast<float4*>(p.pre_o + row + 4 * lane) = o;
-        if (lane == 0) p.pre_lse[at] = lse_of(big, l, kShift);
+    const size_t row = ((size_t)(e.q_row + tok) * p.hq + w.s.kvh * p.r + et % p.r) * D;
+    if (kMore) {
+        const size_t at = row / D;
+        o = make_float4(o.x * y * inv, o.y * y * inv, o.z * y * inv, o.w * y * inv);
+        if (x.flat) {
+            if (live) *reinterpret_cast<float4*>(x.pre_o + row + 4 * lane) = o;
+            if (lane == 0) x.pre_lse[at] = lse_of(big, l, kShift);
+            return;
+        }
+        if (x.pre_lse && (x.merged[w.s.i >> 5] >> (w.s.i & 31) & 1)) {
+            const float2 f = merge_factors(lse_of(big, l, kShift), x.pre_lse[at]);
+            float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (live) z = *reinterpret_cast<const float4*>(x.pre_o + row + 4 * lane);
+            o = make_float4(merge(o.x, z.x, f), merge(o.y, z.y, f), merge(o.z, z.z, f), merge(o.w, z.w, f));
+        }
+        if (live) *reinterpret_cast<uint2*>(p.out + row + 4 * lane) = make_uint2(pack2<BF16>(o.x, o.y), pack2<BF16>(o.z, o.w));
         return;
     }
-    if (p.pre_lse && (p.merged[w.s.i >> 5] >> (w.s.i & 31) & 1)) {
-        const float2 f = merge_factors(lse_of(big, l, kShift), p.pre_lse[at]);
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (live) x = *reinterpret_cast<const float4*>(p.pre_o + row + 4 * lane);
-        o = make_float4(merge(o.x, x.x, f), merge(o.y, x.y, f), merge(o.z, x.z, f), merge(o.w, x.w, f));
-    }
-    if (live) *reinterpret_cast<uint2*>(p.out + row + 4 * lane) = make_uint2(pack2<BF16>(o.x, o.y), pack2<BF16>(o.z, o.w));
+    if (live)
+        *reinterpret_cast<uint2*>(p.out + row + 4 * lane) =
+            make_uint2(pack2<BF16>(o.x * y * inv, o.y * y * inv), pack2<BF16>(o.z * y * inv, o.w * y * inv));
 }
 
+#ifdef KVARN_BLOCK_MORE
+#define KVARN_ARGS p, x
+#define KVARN_PARAMS const BlockPrefillParams &p, const BlockPrefillMore &x
+#else
+#define KVARN_ARGS p
+#define KVARN_PARAMS const BlockPrefillParams& p
+#endif
+
 template <int D, bool INT8, bool BF16>
-int launch(const BlockPrefillParams& p, cudaStream_t s) {
+int launch(KVARN_PARAMS, cudaStream_t s) {
     static SmemOnce once;
     const int e = once.allow(reinterpret_cast<const void*>(prefill_kernel<D, INT8, BF16>), Shape<D>::kSmem);
     if (e) return e;
-    prefill_kernel<D, INT8, BF16><<<p.grid, kThreads, Shape<D>::kSmem, s>>>(p);
-    if (p.line) combine_kernel<D, BF16><<<dim3(p.grid, 256 / (kCombineThreads / 32)), kCombineThreads, 0, s>>>(p);
+    prefill_kernel<D, INT8, BF16><<<p.grid, kThreads, Shape<D>::kSmem, s>>>(KVARN_ARGS);
+    if (p.line) combine_kernel<D, BF16><<<dim3(p.grid, 256 / (kCombineThreads / 32)), kCombineThreads, 0, s>>>(KVARN_ARGS);
     return (int)cudaGetLastError();
 }
 
 }  // namespace
 
-int launch_block_prefill(const BlockPrefillParams& p, void* stream) {
+int launch_block_prefill(KVARN_PARAMS, void* stream) {
     cudaStream_t s = (cudaStream_t)stream;
     switch ((p.c.d == 128 ? 4 : 0) + (p.c.int8 ? 2 : 0) + (p.c.bf16 ? 1 : 0)) {
-        case 0: return launch<64, false, false>(p, s);
-        case 1: return launch<64, false, true>(p, s);
-        case 2: return launch<64, true, false>(p, s);
-        case 3: return launch<64, true, true>(p, s);
-        case 4: return launch<128, false, false>(p, s);
-        case 5: return launch<128, false, true>(p, s);
-        case 6: return launch<128, true, false>(p, s);
-        default: return launch<128, true, true>(p, s);
+        case 0: return launch<64, false, false>(KVARN_ARGS, s);
+        case 1: return launch<64, false, true>(KVARN_ARGS, s);
+        case 2: return launch<64, true, false>(KVARN_ARGS, s);
+        case 3: return launch<64, true, true>(KVARN_ARGS, s);
+        case 4: return launch<128, false, false>(KVARN_ARGS, s);
+        case 5: return launch<128, false, true>(KVARN_ARGS, s);
+        case 6: return launch<128, true, false>(KVARN_ARGS, s);
+        default: return launch<128, true, true>(KVARN_ARGS, s);
     }
 }
 

@@ -7,7 +7,7 @@
 // a maximum m and the tile's sum s of 2^(x - m), 8 bytes for 32 logits, and of every row its total; weigh_kernel
 // adds the tiles' shares to their blocks in a fixed order. Kept as a pair, no rounding of a logit's size
 // stands between a weight and its denominator (log2 of the sum in one word would be off by 2^-17 at 128).
-#include "kvarn_block_tc.cuh"
+#include "kvarn_block_ring.cuh"
 
 namespace kvarn {
 namespace {
@@ -19,149 +19,27 @@ namespace {
 // four warps every other step); one that issues the MMAs into four S buffers (all 512 columns of tensor
 // memory: no O is kept); two that load query rows, a tile ahead; four softmax warpgroups, every fourth step each, a thread a row. Every wait
 // is bounded and sets the error word when it gives up.
-constexpr int kWinThreads = 864, kWinStep = 128, kWinStages = 2, kWinRing = 8, kWinAhead = 2;
+constexpr int kWinThreads = 864, kWinStep = 128, kWinStages = 3, kWinRing = 8;
 constexpr int kWinSoftmax = 4 * kWindowParts, kWinExpand = 8;  // warps
 // barriers
 constexpr int kKFull = 0, kKEmpty = kKFull + kWinRing, kSFull = kKEmpty + kWinStages, kSEmpty = kSFull + 4, kQFull = kSEmpty + 4,
-              kQEmpty = kQFull + kWinRing, kDrain = kQEmpty + 2, kRawFull = kDrain + 1, kWinBars = kRawFull + kWinExpand * kWinAhead;
+              kQEmpty = kQFull + kWinRing, kDrain = kQEmpty + 2, kRawFull = kDrain + 1, kWinBars = kRawFull + kWinExpand * 2;
 
 template <int D>
 struct WinShape {
     static constexpr int kTile = D / 64 * kAtom;
     static constexpr int kQ = 0;                                   // 2 tiles
     static constexpr int kK = 2 * kTile;                           // kWinStages tiles
-    static constexpr int kRec = 16 + kTileTokens * D;              // scales and K codes of a tile
-    static constexpr int kRaw = kK + kWinStages * kTile;           // kWinAhead of an expansion warp
-    static constexpr int kScale = kRaw + kWinExpand * kWinAhead * kRec;  // float[kWinRing][4]: K scale of a step's parts
-    static constexpr int kFactor = kScale + kWinRing * 16;         // float[kWinRing][128]: of a segment's rows
-    static constexpr int kBars = kFactor + kWinRing * 512;
+    static constexpr int kRaw = kK + kWinStages * kTile;           // two ring entries of an expansion warp
+    static constexpr int kScale = kRaw + kWinExpand * 2 * kRingEntry<D>;  // float[kWinRing][4]: K scale of a step's parts
+    static constexpr int kPower = kScale + kWinRing * 16;          // int8[kWinRing][128]: of a segment's rows
+    static constexpr int kBars = kPower + kWinRing * 128;
     static constexpr int kTmem = kBars + 8 * kWinBars;
     static constexpr int kSmem = kTmem + 16;
     static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
 };
 
-// The segments (rows of 128, steps j0 .. j1 - 1) of a CTA's part of the line, in order.
-struct WinWalk {
-    const BlockWindowParams& p;
-    int64_t u, u1;
-    int i, h, tile, j0, j1, pair;
-    __device__ __forceinline__ explicit WinWalk(const BlockWindowParams& p_)
-        : p(p_), u(p_.units * blockIdx.x / p_.grid), u1(p_.units * (blockIdx.x + 1) / p_.grid), i(0) {}
-    __device__ __forceinline__ bool next() {
-        if (u >= u1) return false;
-#pragma unroll 1
-        while (i + 1 < p.n_seqs && p.seqs[i + 1].unit_begin <= u) ++i;
-        const BlockWindowSeq& e = p.seqs[i];
-        const int rel = (int)u - e.unit_begin;
-        pair = rel / e.steps;
-        j0 = rel - pair * e.steps;
-        j1 = (int)min((int64_t)e.steps, j0 + (u1 - u));
-        h = pair / e.row_tiles;
-        tile = pair - h * e.row_tiles;
-        u += j1 - j0;
-        return true;
-    }
-};
-
-// Warp wp (0 .. 3) of group `odd`: part wp of every other step. Codes come by bulk copies into a ring of the warp's own, two parts
-// ahead of the one that is expanded (one part ahead in registers, 32 KB in flight a SM, left the memory waiting), pool slots a part earlier.
-template <int D, bool INT8, bool BF16>
-__device__ __forceinline__ void win_expand(const BlockWindowParams& p, uint8_t* smem, uint64_t* bars, int32_t* err, int odd,
-                                           int wp, int lane) {
-    using Sh = WinShape<D>;
-    const BlockView& c = p.c;
-    const int sh = c.log2_block - 5, t = lane & 3, kg = lane >> 2;
-    constexpr int kChunks = D / 16;
-    WinWalk w(p);
-    bool more = w.next();
-    int j = more ? w.j0 : 0, k = 0;  // the next step to look at
-    auto skip = [&]() {              // one step on
-        ++k;
-        if (more && ++j == w.j1) {
-            more = w.next();
-            if (more) j = w.j0;
-        }
-    };
-    if (odd) skip();
-    struct Part {
-        int step, seq, n, kvh, tile, slot;  // step -1: none; slot -1: exact tokens, or none
-    };
-    auto look = [&]() {
-        Part x = {-1, 0, 0, 0, 0, -1};
-        if (!more) return x;
-        const BlockWindowSeq& e = p.seqs[w.i];
-        x = Part{k, e.seq, e.n, w.h, 4 * j + wp, -1};
-        if (x.tile < e.n >> c.log2_block << sh) x.slot = __ldg(block_table(c, e.seq) + (x.tile >> sh));
-        skip();
-        skip();
-        return x;
-    };
-    uint8_t* ring = smem + Sh::kRaw + (4 * odd + wp) * kWinAhead * Sh::kRec;
-    uint64_t* landed = bars + kRawFull + (4 * odd + wp) * kWinAhead;
-    int issued = 0, done = 0;  // ring entries
-    bool ok = true;
-    auto fetch = [&](const Part& a) {
-        if (a.slot < 0 || !ok) return;
-        if (lane == 0) {
-            const int e = issued % kWinAhead;
-            mbar_arrive_expect_tx(landed + e, Sh::kRec);
-            bulk_g2s(ring + e * Sh::kRec, tile_ptr(c, a.slot, a.kvh, a.tile & ((1 << sh) - 1)), Sh::kRec, landed + e);
-        }
-        ++issued;
-    };
-    static_assert(kWinAhead == 2, "parts in hand");
-    Part now = look(), next = look(), then = look();
-    fetch(now);
-    fetch(next);
-#pragma unroll 1
-    while (now.step >= 0) {
-        const int s = now.step;
-        bool here = true;
-        if (s >= kWinStages) here = bar_wait(bars + kKEmpty + s % kWinStages, (uint32_t)((s / kWinStages - 1) & 1), err);
-        uint8_t* dst = smem + Sh::kK + s % kWinStages * Sh::kTile;
-        float* head = reinterpret_cast<float*>(smem + Sh::kScale) + (s % kWinRing) * 4 + wp;
-        float f = 1.f;
-        if (now.slot >= 0 && ok) {
-            const uint8_t* rec = ring + done % kWinAhead * Sh::kRec;
-            here = bar_wait(landed + done % kWinAhead, (uint32_t)(done / kWinAhead & 1), err) && here;
-            f = *reinterpret_cast<const float*>(rec);
-            const int row0 = 32 * wp + 8 * (kg >> 1) + (kg & 1);
-#pragma unroll
-            for (int i = 0; i < kChunks; ++i) {  // 16 channels of one token
-                const uint4 x = *reinterpret_cast<const uint4*>(rec + 16 + i * 512 + lane * 16);
-                const int z = i / (D / 32), cc = i / 2 % (D / 64), row = row0 + 4 * z + 2 * (i & 1);
-                *reinterpret_cast<uint4*>(dst + cc * kAtom + swz(row, 2 * t)) =
-                    make_uint4(codes_lo<INT8>(x.x), codes_hi<INT8>(x.x), codes_lo<INT8>(x.y), codes_hi<INT8>(x.y));
-                *reinterpret_cast<uint4*>(dst + cc * kAtom + swz(row, 2 * t + 1)) =
-                    make_uint4(codes_lo<INT8>(x.z), codes_hi<INT8>(x.z), codes_lo<INT8>(x.w), codes_hi<INT8>(x.w));
-            }
-        } else if (now.slot < 0) {
-            float2 hd;
-            uint32_t bad;
-            uint4 x[kChunks];
-            expand_exact<D, BF16, false>(c, now.seq, now.n, now.kvh, now.tile, wp, lane, dst, hd, bad, x);
-            f = hd.x;
-        }
-        ok = __all_sync(0xffffffffu, here) && ok;  // one answer for the warp; also: all lanes have read
-        if (now.slot >= 0 && ok) ++done;
-        if (lane == 0) *head = f;
-        fence_proxy_async_smem();
-        mbar_arrive(bars + kKFull + s % kWinRing);
-        fetch(then);
-        now = next;
-        next = then;
-        then = look();
-    }
-    // Normally every copy was waited for above. After a wait that gave up nothing more was issued, and what is in flight
-    // lands (a bounded wait again) before the CTA's shared memory goes away.
-    if (!ok) {
-        const uint64_t t0 = global_ns();
-#pragma unroll 1
-        for (; done < issued; ++done)
-            while (!mbar_try_wait(landed + done % kWinAhead, (uint32_t)(done / kWinAhead & 1)) && global_ns() - t0 < kWaitLimitNs) {
-            }
-    }
-}
+typedef RowWalk<BlockWindowParams> WinWalk;
 
 template <int D>
 __device__ __forceinline__ void win_issue(const BlockWindowParams& p, uint32_t sbase, uint64_t* bars, int32_t* err) {
@@ -200,58 +78,6 @@ __device__ __forceinline__ void win_issue(const BlockWindowParams& p, uint32_t s
     }
 }
 
-// Two warps: the rows of each segment as its Q tile, and the factors of their logits.
-template <int D, bool BF16>
-__device__ __forceinline__ void win_rows(const BlockWindowParams& p, uint8_t* smem, uint64_t* bars, int32_t* err, int half, int lane) {
-    using Sh = WinShape<D>;
-    // a negative scale turns the query's sign, so that larger S is always a larger logit (0: all logits are 0)
-    const bool zero = p.scale_log2 == 0.f;
-    const float scale = zero ? 1.f : fabsf(p.scale_log2);
-    const uint32_t sign = p.scale_log2 < 0.f ? 0x80008000u : 0u;
-    constexpr int kLanes = D / 8, kRows = 32 / kLanes, kTurn = 8;
-    int seg = 0;
-    WinWalk w(p);
-#pragma unroll 1
-    for (; w.next(); ++seg) {
-        if (seg >= 2) bar_wait(bars + kQEmpty + (seg & 1), (uint32_t)(((seg >> 1) - 1) & 1), err);
-        __syncwarp();
-        const BlockWindowSeq& e = p.seqs[w.i];
-        uint8_t* dst = smem + Sh::kQ + (seg & 1) * Sh::kTile;
-        float* factor = reinterpret_cast<float*>(smem + Sh::kFactor) + seg % kWinRing * 128;
-#pragma unroll 1
-        for (int r0 = 64 * half; r0 < 64 * half + 64; r0 += kTurn * kRows) {
-            uint4 x[kTurn];
-#pragma unroll
-            for (int z = 0; z < kTurn; ++z) {
-                const int row = r0 + z * kRows + lane / kLanes, all = w.tile * 128 + row;
-                x[z] = make_uint4(0, 0, 0, 0);
-                if (all < e.rows && !zero)
-                    x[z] = reinterpret_cast<const uint4*>(p.q + ((size_t)(e.q_row + all / p.r) * p.hq + w.h * p.r + all % p.r) * D)[lane % kLanes];
-            }
-#pragma unroll
-            for (int z = 0; z < kTurn; ++z) {
-                const int row = r0 + z * kRows + lane / kLanes;
-                float f = scale;
-                uint4 r = x[z];
-                if (BF16) {
-                    uint32_t top = max_of(0, r);
-                    top = max(top & 0xffffu, top >> 16);
-#pragma unroll
-                    for (int d = kLanes / 2; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-                    const int ex = exponent_of<BF16>(top) - kExactK;
-                    r = scaled_f16<BF16>(r, power2(-ex));
-                    f *= power2(ex);
-                }
-                r = make_uint4(r.x ^ sign, r.y ^ sign, r.z ^ sign, r.w ^ sign);
-                *reinterpret_cast<uint4*>(dst + (lane % kLanes >> 3) * kAtom + swz(row, lane & 7)) = r;
-                if (lane % kLanes == 0) factor[row] = f;
-            }
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(bars + kQFull + seg % kWinRing);
-    }
-}
-
 // Warpgroup b takes every fourth step, in its own S buffer; thread et owns row et.
 template <int D>
 __device__ __forceinline__ void win_softmax(const BlockWindowParams& p, uint8_t* smem, uint64_t* bars, int32_t* err, int et, int b,
@@ -276,7 +102,7 @@ __device__ __forceinline__ void win_softmax(const BlockWindowParams& p, uint8_t*
         for (int j = j0, kk = k - (w.j1 - j0); j < w.j1; j += 4, kk += 4) {
             if (first) {
                 bar_wait(bars + kQFull + seg % kWinRing, (uint32_t)(seg / kWinRing & 1), err);
-                qs = reinterpret_cast<const float*>(smem + Sh::kFactor)[seg % kWinRing * 128 + et];
+                qs = row_factor(p.scale_log2, reinterpret_cast<const int8_t*>(smem + Sh::kPower)[seg % kWinRing * 128 + et]);
                 first = false;
             }
             bar_wait(bars + kKFull + kk % kWinRing, (uint32_t)(kk / kWinRing & 1), err);
@@ -350,7 +176,7 @@ __global__ void __launch_bounds__(kWinThreads, 1) window_kernel(const __grid_con
         }
         for (int k = 0; k < 2; ++k) mbar_init(bars + kQEmpty + k, 1);
         mbar_init(bars + kDrain, 1);
-        for (int k = 0; k < kWinExpand * kWinAhead; ++k) mbar_init(bars + kRawFull + k, 1);
+        for (int k = 0; k < kWinExpand * 2; ++k) mbar_init(bars + kRawFull + k, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     constexpr int kIssuer = kWinSoftmax + kWinExpand;  // warp
@@ -370,11 +196,28 @@ __global__ void __launch_bounds__(kWinThreads, 1) window_kernel(const __grid_con
     } else if (w < kWinSoftmax) {
         win_softmax<D>(p, smem, bars, err, t & 127, w >> 2, (uint32_t)(32 * (w & 3)) << 16);
     } else if (w < kIssuer) {
-        win_expand<D, INT8, BF16>(p, smem, bars, err, (w >> 2) & 1, w & 3, lane);
+        const int x = w - kWinSoftmax, odd = x >> 2, wp = x & 3;
+        expand_line<D, INT8, BF16, false, 2>(
+            p, smem + Sh::kRaw + x * 2 * kRingEntry<D>, bars + kRawFull + 2 * x, err, odd, wp, lane,
+            [&](int k) -> uint8_t* {
+                if (k >= kWinStages && !bar_wait(bars + kKEmpty + k % kWinStages, (uint32_t)((k / kWinStages - 1) & 1), err)) return nullptr;
+                return smem + Sh::kK + k % kWinStages * Sh::kTile;
+            },
+            [&](int k, float2 h, uint32_t) {
+                if (lane == 0) reinterpret_cast<float*>(smem + Sh::kScale)[k % kWinRing * 4 + wp] = h.x;
+                mbar_arrive(bars + kKFull + k % kWinRing);
+            });
     } else if (w == kIssuer) {
         win_issue<D>(p, smem_addr(smem), bars, err);
     } else {
-        win_rows<D, BF16>(p, smem, bars, err, w - kIssuer - 1, lane);
+        int seg = 0;
+        for (WinWalk x(p); x.next(); ++seg) {
+            if (seg >= 2) bar_wait(bars + kQEmpty + (seg & 1), (uint32_t)(((seg >> 1) - 1) & 1), err);
+            __syncwarp();
+            make_rows<D, BF16, 2>(p, x, smem + Sh::kQ + (seg & 1) * Sh::kTile,
+                                  reinterpret_cast<int8_t*>(smem + Sh::kPower) + seg % kWinRing * 128, w - kIssuer - 1, lane);
+            mbar_arrive(bars + kQFull + seg % kWinRing);
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -393,22 +236,34 @@ constexpr int kWeighRows = 128 * kBlockMaxRatio;  // rows of a KV head
 // A CTA some blocks of a (KV head, sequence): its rows' totals first, then p.lanes lanes a block.
 __global__ void __launch_bounds__(kWeighThreads) weigh_kernel(const __grid_constant__ BlockWeighParams p) {
     __shared__ float2 of[kWeighRows];  // of a row: its maximum, 1 / denominator (0: adds nothing)
+    __shared__ float2 some[kWeighThreads];
     const BlockWeighSeq& e = p.seqs[blockIdx.z];
     const int h = blockIdx.y, t = threadIdx.x, blocks = (e.tiles + (1 << p.log2_tiles) - 1) >> p.log2_tiles;
     const int first = blockIdx.x * p.blocks;
     if (first >= blocks) return;
-    for (int row = t; row < e.rows; row += kWeighThreads) {
+    int span = 32;  // rows at a time; as many threads as there are to a row, each some of its parts
+    while (span < kWeighThreads && span < e.rows) span *= 2;
+    for (int row0 = 0; row0 < e.rows; row0 += span) {
+        const int row = row0 + t % span, turn = t / span, turns = kWeighThreads / span;
         float2 s = make_float2(kNegInf, 0.f);
-        if (p.grid == 0) {
-            s = p.totals[(int64_t)e.row * p.hq + h * e.rows + row];
+        if (row >= e.rows) {
+        } else if (p.grid == 0) {
+            if (turn == 0) s = p.totals[(int64_t)e.row * p.hq + h * e.rows + row];
         } else {  // the parts of the row's pair, of the CTAs that share it
             const int steps = (e.tiles + 3) / 4, pair = h * ((e.rows + 127) / 128) + row / 128;
             const int64_t u = e.unit_begin + (int64_t)pair * steps;
             const int b0 = (int)(((u + 1) * p.grid - 1) / p.units), b1 = (int)(((u + steps) * p.grid - 1) / p.units);
-            for (int b = kWindowParts * b0; b < kWindowParts * (b1 + 1); ++b)
-                s = joined(s, p.totals[((int64_t)(e.pair_begin + pair) * kWindowParts + b) * 128 + row % 128]);
+            const float2* at = p.totals + (int64_t)(e.pair_begin + pair) * kWindowParts * 128 + row % 128;
+#pragma unroll 4
+            for (int b = kWindowParts * b0 + turn; b < kWindowParts * (b1 + 1); b += turns) s = joined(s, at[(int64_t)b * 128]);
         }
-        of[row] = make_float2(s.x, s.y > 0.f && s.y < -kNegInf ? 1.f / s.y : 0.f);
+        if (turns > 1) {
+            some[t] = s;
+            __syncthreads();
+            for (int z = 1; turn == 0 && z < turns; ++z) s = joined(s, some[z * span + t]);
+            __syncthreads();
+        }
+        if (turn == 0 && row < e.rows) of[row] = make_float2(s.x, s.y > 0.f && s.y < -kNegInf ? 1.f / s.y : 0.f);
     }
     __syncthreads();
     const float2* sums = p.sums + e.sum_begin + ((int64_t)h * (e.before + e.tiles) + e.before) * e.pad;
