@@ -21,7 +21,7 @@ LIB = os.path.join(BUILD, "libkvarn.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["kvarn_host.cpp", "kvarn_seal.cu", "kvarn_decode.cu", "kvarn_prefill.cu", "kvarn_block_host.cpp",
            "kvarn_block.cu", "kvarn_block_decode.cu", "kvarn_block_prefill.cu", "kvarn_block_decode_more.cu",
-           "kvarn_block_prefill_more.cu", "kvarn_block_weights.cu",
+           "kvarn_block_prefill_more.cu", "kvarn_block_flat.cu", "kvarn_block_weights.cu",
            "kvarn_block_evict.cu", "kvarn_qk.cu"]
 HEADERS = ["kvarn_internal.h", "kvarn_dev.cuh", "kvarn_block.h", "kvarn_block_dev.cuh", "kvarn_block_tc.cuh", "kvarn_block_ring.cuh",
            "kvarn_tc.cuh"]

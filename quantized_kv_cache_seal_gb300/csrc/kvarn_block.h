@@ -144,18 +144,33 @@ struct BlockPrefillMore {
     uint32_t merged[kBlockMaxSeqs / 32];  // bit i: entry i
 };
 
-constexpr int kWindowParts = 4;  // softmax warpgroups of a window_weights launch
-// Weights of the last queries of sequences (K alone is read).
-struct BlockWindowSeq {
+// Queries as tiles of 128 rows (query, head of a KV head) over a sequence in steps of 128 tokens, for each KV head.
+struct BlockRowsSeq {
     int32_t seq, n, q_len, q_row;
     int32_t rows;        // q_len * r
-    int32_t pad;         // rows rounded up to 8
+    int32_t pad;         // rows rounded up to 8 (window)
     int32_t row_tiles;   // of 128 rows
     int32_t steps;       // of 128 of its tokens
     int32_t unit_begin;  // prefix of Hkv * row_tiles * steps
     int32_t pair_begin;  // prefix of Hkv * row_tiles
-    int64_t sum_begin;   // prefix of Hkv * tiles * pad
+    int64_t sum_begin;   // prefix of Hkv * tiles * pad (window)
 };
+
+// Queries of all sequences behind a shared prefix, which see all of it.
+struct BlockFlatParams {
+    BlockView c;
+    const uint16_t* q;
+    float* parts;            // [pairs + grid][2][128 (D + 3)]
+    float *pre_o, *pre_lse;  // f32 [rows][Hq][D], [rows][Hq]
+    int32_t n_seqs, hq, r, grid;
+    int64_t units;           // steps of all sequences, KV heads and row tiles
+    float scale_log2;
+    BlockRowsSeq seqs[kBlockMaxSeqs];
+};
+inline size_t flat_part_floats(int d) { return 128 * ((size_t)d + 3); }
+
+// Weights of the last queries of sequences (K alone is read).
+constexpr int kWindowParts = 3;  // softmax warpgroups of a launch
 struct BlockWindowParams {
     BlockView c;
     const uint16_t* q;
@@ -164,7 +179,7 @@ struct BlockWindowParams {
     int32_t n_seqs, hq, r, grid;
     int64_t units;
     float scale_log2;
-    BlockWindowSeq seqs[kBlockMaxSeqs];
+    BlockRowsSeq seqs[kBlockMaxSeqs];
 };
 
 // Adds the tiles' weights to what their blocks have received.
@@ -224,6 +239,7 @@ int launch_block_decode(const BlockDecodeParams& p, void* stream);
 int launch_block_decode(const BlockDecodeParams& p, const BlockDecodeMore& more, void* stream);
 int launch_block_prefill(const BlockPrefillParams& p, void* stream);
 int launch_block_prefill(const BlockPrefillParams& p, const BlockPrefillMore& more, void* stream);
+int launch_block_flat(const BlockFlatParams& p, int pairs, void* stream);
 int launch_block_window(const BlockWindowParams& p, void* stream);
 int launch_block_weigh(const BlockWeighParams& p, void* stream);
 int launch_block_evict(const BlockEvictParams& p, void* stream);

@@ -424,8 +424,50 @@ kvarn_status run_prefill(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, co
     return run_tiles(c, layer, n_seqs, entries, false, q, out, scale, stream, beside);
 }
 
+// The prefixes' pass on single row tiles, where its parts have room; `done` says so.
+kvarn_status run_flat(kvarn_block_cache* c, int32_t layer, int32_t n_entries, const Entry* entries, const void* q, float scale,
+                      void* stream, const Beside& beside, bool* done) {
+    static thread_local BlockFlatParams p;
+    const int hkv = c->cfg.num_kv_heads;
+    int64_t units = 0, pairs = 0;
+    for (int i = 0; i < n_entries; ++i) {
+        BlockRowsSeq& e = p.seqs[i];
+        const int64_t rows = (int64_t)entries[i].q_len * c->r, tiles = (rows + 127) / 128, steps = ((int64_t)entries[i].n + 127) / 128;
+        e = BlockRowsSeq{entries[i].seq, entries[i].n, entries[i].q_len, entries[i].q_row, (int32_t)rows, 0, (int32_t)tiles,
+                         (int32_t)steps, (int32_t)units, (int32_t)pairs, 0};
+        units += hkv * tiles * steps;
+        pairs += hkv * tiles;
+        if (units >= 1ll << 31 || pairs > kBlockPrefillGrid) return KVARN_OK;
+    }
+    p.grid = (int32_t)std::min<int64_t>(std::min(c->sms, kBlockPrefillGrid), units);
+    const size_t room = (size_t)kBlockPrefillGrid * 2 * 256 * (c->cfg.head_dim + 2);
+    if ((size_t)(pairs + p.grid) * 2 * flat_part_floats(c->cfg.head_dim) > room) return KVARN_OK;
+    *done = true;
+    if (c->host_only) return KVARN_OK;
+    const kvarn_status st = ensure_init(c, stream);
+    if (st) return st;
+    p.c = c->view;
+    p.c.layer = layer;
+    p.q = (const uint16_t*)q;
+    p.parts = (float*)(c->view.base + c->view.lay.partials);
+    p.pre_o = beside.pre_o;
+    p.pre_lse = beside.pre_lse;
+    p.n_seqs = n_entries;
+    p.hq = c->cfg.num_q_heads;
+    p.r = c->r;
+    p.units = units;
+    p.scale_log2 = scale * kLog2e;
+    const int rc = launch_block_flat(p, (int)pairs, stream);
+    return rc ? cuda_fail(rc, "prefix launch") : KVARN_OK;
+}
+
 kvarn_status run_tiles(kvarn_block_cache* c, int32_t layer, int32_t n_entries, const Entry* entries, bool flat, const void* q,
                        void* out, float scale, void* stream, const Beside& beside) {
+    if (flat) {
+        bool done = false;
+        const kvarn_status st = run_flat(c, layer, n_entries, entries, q, scale, stream, beside, &done);
+        if (st || done) return st;
+    }
     static thread_local BlockPrefillParams p;
     static thread_local BlockPrefillMore x;
     p.c = c->view;
@@ -579,7 +621,7 @@ kvarn_status plan_window(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, co
         if (m < 0 || m > n) return fail(KVARN_EINVAL, "a query count is negative or above the sequence's length");
         if (m > kWindowTokens) return fail(KVARN_EINVAL, "more than 128 queries of a sequence");
         if (m > 0) {
-            BlockWindowSeq& e = p.seqs[p.n_seqs++];
+            BlockRowsSeq& e = p.seqs[p.n_seqs++];
             e.seq = ids[i];
             e.n = (int32_t)n;
             e.q_len = (int32_t)m;
@@ -920,7 +962,7 @@ kvarn_status kvarn_block_window_weights(kvarn_block_cache* c, int32_t layer, int
     if (st || p.n_seqs == 0) return st;
     if (!q || !aligned16(q)) return fail(KVARN_EINVAL, "q must be 16-byte aligned");
     if (!weights) return fail(KVARN_EINVAL, "no weights");
-    const BlockWindowSeq& end = p.seqs[p.n_seqs - 1];
+    const BlockRowsSeq& end = p.seqs[p.n_seqs - 1];
     st = check_beside(c, (int64_t)end.q_row + end.q_len, q, nullptr, weights, workspace, workspace_bytes, w);
     if (st || c->host_only) return st;
     p.c = c->view;
@@ -940,7 +982,7 @@ kvarn_status kvarn_block_window_weights(kvarn_block_cache* c, int32_t layer, int
     wp.grid = p.grid;
     wp.n_seqs = p.n_seqs;
     for (int i = 0; i < p.n_seqs; ++i) {
-        const BlockWindowSeq& e = p.seqs[i];
+        const BlockRowsSeq& e = p.seqs[i];
         wp.seqs[i] = BlockWeighSeq{e.seq, e.rows, e.pad, 0, tiles_of(e.n), 0, e.unit_begin, e.pair_begin, e.sum_begin};
     }
     return run_weigh(c, wp, stream);

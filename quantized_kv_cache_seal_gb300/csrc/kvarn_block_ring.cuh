@@ -97,7 +97,7 @@ __device__ __forceinline__ void expand_codes(const uint8_t* rec, uint8_t* dst, i
     if (IS_V) {  // lanes take the chunks in an order in which the stores of eight meet eight different banks
         const int g = (lane >> 3) + (lane & 4);
         uint8_t* to = dst + (wp >> 1) * (D * 128) + swz(g, 4 * (wp & 1) + t);
-#pragma unroll
+#pragma unroll 2
         for (int i = 0; i < D / 16; ++i) {  // 8 tokens of channels 16 i + g and + 8
             const uint4 x = *reinterpret_cast<const uint4*>(rec + 16 + i * 512 + (4 * g + t) * 16);
             *reinterpret_cast<uint4*>(to + i * 2048) = halves(x.x, x.y);
@@ -105,12 +105,16 @@ __device__ __forceinline__ void expand_codes(const uint8_t* rec, uint8_t* dst, i
         }
     } else {
         const int g = lane >> 2, row0 = 32 * wp + 8 * (g >> 1) + (g & 1);
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {  // 16 channels of one token
+        // 16 channels of one token: chunk i holds token 4 (i / (D / 32)) + 2 (i & 1), channels 64 (i / 2 % (D / 64)) on. The row's place in
+        // its group of eight turns the 16-byte chunks' places by an exclusive or.
+#pragma unroll 2
+        for (int i = 0; i < D / 16; ++i) {
             const uint4 x = *reinterpret_cast<const uint4*>(rec + 16 + i * 512 + lane * 16);
-            const int z = i / (D / 32), cc = i / 2 % (D / 64), row = row0 + 4 * z + 2 * (i & 1);
-            *reinterpret_cast<uint4*>(dst + cc * kAtom + swz(row, 2 * t)) = halves(x.x, x.y);
-            *reinterpret_cast<uint4*>(dst + cc * kAtom + swz(row, 2 * t + 1)) = halves(x.z, x.w);
+            const int row = row0 + 4 * (i / (D / 32)) + 2 * (i & 1);
+            uint8_t* to = dst + i / 2 % (D / 64) * kAtom + row * 128;
+            const int at = (2 * t) ^ (row & 7);
+            *reinterpret_cast<uint4*>(to + (at << 4)) = halves(x.x, x.y);
+            *reinterpret_cast<uint4*>(to + ((at ^ 1) << 4)) = halves(x.z, x.w);
         }
     }
 }
@@ -134,13 +138,13 @@ __device__ __forceinline__ void expand_rows(const uint8_t* src, int nv, uint8_t*
             return make_uint4(x.x & keep[0], x.y & keep[1], x.z & keep[2], x.w & keep[3]);
         };
         uint32_t top = 0;
-#pragma unroll 4
+#pragma unroll 2
         for (int i = 0; i < kPieces; ++i) top = max_of(top, finite_only<BF16>(piece(i)));
         const int ex = warp_exponent_v<BF16>(top);
         const float f = power2(-ex);
         h = make_float2((float)ex, f * kDenomUnit);
         uint8_t* atom = dst + (wp >> 1) * (D * 128);
-#pragma unroll 4
+#pragma unroll 2
         for (int i = 0; i < kPieces; ++i) {
             const uint4 r = piece(i);
             bad |= bad_pair<BF16>(r.x) | bad_pair<BF16>(r.y) | bad_pair<BF16>(r.z) | bad_pair<BF16>(r.w);
@@ -156,13 +160,13 @@ __device__ __forceinline__ void expand_rows(const uint8_t* src, int nv, uint8_t*
         float f = 1.f;
         if (BF16) {
             uint32_t top = 0;
-#pragma unroll 4
+#pragma unroll 2
             for (int i = 0; i < kPieces; ++i) top = max_of(top, finite_only<BF16>(piece(i)));
             const int ex = warp_exponent<BF16>(top) - kExactK;
             f = power2(-ex);
             h.x = power2(ex);
         }
-#pragma unroll 4
+#pragma unroll 2
         for (int i = 0; i < kPieces; ++i) {
             const int y = i * 32 + lane, ch8 = y % kPieces;
             const uint4 x = piece(i);

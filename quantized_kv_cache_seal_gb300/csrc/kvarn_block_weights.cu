@@ -15,11 +15,11 @@ namespace {
 // ---- logits of the last queries ----
 // S = Q code^T on tcgen05 (M = 128 rows, N = 128 tokens, f16 operands, exact codes, fp32 sums) as in prefill, and no more: a
 // unit of work is a step of 128 tokens for a tile of 128 rows of a (sequence, KV head), and the line of all units is cut evenly over
-// the CTAs, one a SM. Roles (864 threads): eight expansion warps that turn K codes into f16 tiles (a warp 32 tokens,
+// the CTAs, one a SM. Roles (736 threads): eight expansion warps that turn K codes into f16 tiles (a warp 32 tokens,
 // four warps every other step); one that issues the MMAs into four S buffers (all 512 columns of tensor
-// memory: no O is kept); two that load query rows, a tile ahead; four softmax warpgroups, every fourth step each, a thread a row. Every wait
+// memory: no O is kept); two that load query rows, a tile ahead; three softmax warpgroups, every third step each, a thread a row. Every wait
 // is bounded and sets the error word when it gives up.
-constexpr int kWinThreads = 864, kWinStep = 128, kWinStages = 3, kWinRing = 8;
+constexpr int kWinThreads = 736, kWinStep = 128, kWinStages = 3, kWinRing = 8;
 constexpr int kWinSoftmax = 4 * kWindowParts, kWinExpand = 8;  // warps
 // barriers
 constexpr int kKFull = 0, kKEmpty = kKFull + kWinRing, kSFull = kKEmpty + kWinStages, kSEmpty = kSFull + 4, kQFull = kSEmpty + 4,
@@ -78,17 +78,17 @@ __device__ __forceinline__ void win_issue(const BlockWindowParams& p, uint32_t s
     }
 }
 
-// Warpgroup b takes every fourth step, in its own S buffer; thread et owns row et.
+// Warpgroup b takes every third step; thread et owns row et. (Two of them take 72 us where three take 60; four, with an S buffer
+// each that the next MMAs wait for, 79.)
 template <int D>
 __device__ __forceinline__ void win_softmax(const BlockWindowParams& p, uint8_t* smem, uint64_t* bars, int32_t* err, int et, int b,
                                             uint32_t lane_off) {
     using Sh = WinShape<D>;
-    const uint32_t ts = 128 * b + lane_off;
     int k = 0, seg = 0;
     WinWalk w(p);
 #pragma unroll 1
     for (; w.next(); ++seg) {
-        const BlockWindowSeq& e = p.seqs[w.i];
+        const BlockRowsSeq& e = p.seqs[w.i];
         const int row = w.tile * 128 + et, tiles = (e.n + kTileTokens - 1) / kTileTokens, pad = e.pad;
         const bool valid = row < e.rows;
         const int pos = valid ? e.n - e.q_len + row / p.r : e.n - 1;
@@ -96,43 +96,42 @@ __device__ __forceinline__ void win_softmax(const BlockWindowParams& p, uint8_t*
         float2 total = make_float2(kNegInf, 0.f);
         float qs = 1.f;
         bool first = true;
-        const int j0 = w.j0 + ((b - k) & 3);
+        const int j0 = w.j0 + (b + kWindowParts - k % kWindowParts) % kWindowParts;
         k += w.j1 - w.j0;
 #pragma unroll 1
-        for (int j = j0, kk = k - (w.j1 - j0); j < w.j1; j += 4, kk += 4) {
+        for (int j = j0, kk = k - (w.j1 - j0); j < w.j1; j += kWindowParts, kk += kWindowParts) {
             if (first) {
                 bar_wait(bars + kQFull + seg % kWinRing, (uint32_t)(seg / kWinRing & 1), err);
                 qs = row_factor(p.scale_log2, reinterpret_cast<const int8_t*>(smem + Sh::kPower)[seg % kWinRing * 128 + et]);
                 first = false;
             }
             bar_wait(bars + kKFull + kk % kWinRing, (uint32_t)(kk / kWinRing & 1), err);
-            const float4 hd = reinterpret_cast<const float4*>(smem + Sh::kScale)[kk % kWinRing];
-            bar_wait(bars + kSFull + b, (uint32_t)(kk >> 2 & 1), err);
+            const float* hd = reinterpret_cast<const float*>(smem + Sh::kScale) + kk % kWinRing * 4;
+            bar_wait(bars + kSFull + (kk & 3), (uint32_t)(kk >> 2 & 1), err);
             __syncwarp();
             tc_fence_after();
             const int lim = pos + 1 - j * kWinStep;  // visible columns
             const bool plain = __all_sync(0xffffffffu, lim >= kWinStep);
-            float m[4], l[4];
-#pragma unroll
+            // (rolled: unrolled, the roles together would not fit the instruction cache)
+#pragma unroll 1
             for (int ch = 0; ch < 4; ++ch) {
                 uint32_t r[32];
-                tm_ld32(ts + 32 * ch, r);
+                tm_ld32(128 * (kk & 3) + 32 * ch + lane_off, r);
+                float c = qs * hd[ch];
+                if (c < 1e-37f) c = 1e-37f;  // 0 would make -inf of a masked column NaN
                 tm_wait_ld();
                 if (ch == 3) {  // S may be written again
                     tc_fence_before();
-                    mbar_arrive(bars + kSEmpty + b);
+                    mbar_arrive(bars + kSEmpty + (kk & 3));
                 }
                 const int left = lim - 32 * ch;
-                float c = qs * (ch == 0 ? hd.x : ch == 1 ? hd.y : ch == 2 ? hd.z : hd.w);
-                if (c < 1e-37f) c = 1e-37f;  // 0 would make -inf of a masked column NaN
                 if (!plain) {
 #pragma unroll
                     for (int z = 0; z < 32; ++z)
                         if (z >= left) r[z] = 0xff800000u;
                     if (left <= 0) c = 1.f;
                 }
-                m[ch] = max32(r) * c;
-                const float mm = m[ch] == kNegInf ? 0.f : m[ch];
+                const float m = max32(r) * c, mm = m == kNegInf ? 0.f : m;
                 const float2 c2 = make_float2(c, c), a2 = make_float2(-mm, -mm);
                 float2 s0 = make_float2(0.f, 0.f), s1 = s0;
 #pragma unroll
@@ -143,14 +142,10 @@ __device__ __forceinline__ void win_softmax(const BlockWindowParams& p, uint8_t*
                     else s0 = __fadd2_rn(s0, v);
                 }
                 s0 = __fadd2_rn(s0, s1);
-                l[ch] = s0.x + s0.y;
-                if (valid && 4 * j + ch < tiles) out[(int64_t)(4 * j + ch) * pad] = make_float2(m[ch], l[ch]);
+                const float2 part = make_float2(m, s0.x + s0.y);
+                if (valid && 4 * j + ch < tiles) out[(int64_t)(4 * j + ch) * pad] = part;
+                total = joined(total, part);
             }
-            const float top = fmaxf(max3(m[0], m[1], m[2]), fmaxf(m[3], total.x));
-            float sum = total.y * (total.x == kNegInf ? 1.f : ex2f(total.x - top));
-#pragma unroll
-            for (int ch = 0; ch < 4; ++ch) sum = fmaf(l[ch], m[ch] == kNegInf ? 1.f : ex2f(m[ch] - top), sum);
-            total = make_float2(top, sum);
         }
         // of the pair's part in this CTA (a pair's first CTA is no sooner than the pair before's last)
         p.totals[((int64_t)(e.pair_begin + w.pair + blockIdx.x) * kWindowParts + b) * 128 + et] = total;

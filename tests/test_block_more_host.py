@@ -111,8 +111,8 @@ def test_window_refusals():
     refused(1, call, [0], [1], FAKE, W, SPACE + 8)
     refused(1, call, [0], [1], scale=float("inf"))
     size = lambda *a: K.kvarn_block_window_workspace(c, 0, *a)
-    # sums of 2 heads, 4 tiles, 3 x 4 rows up to 16; rows of 2 (pairs) + 2 (thread blocks), in four parts
-    need = 8 * 2 * 4 * 16 + (2 + 2) * 4 * 128 * 8
+    # sums of 2 heads, 4 tiles, 3 x 4 rows up to 16; rows of 2 (pairs) + 2 (thread blocks), in three parts
+    need = 8 * 2 * 4 * 16 + (2 + 2) * 3 * 128 * 8
     assert size([0], [3]) == need and size([2], [0]) == 0
     for bad in (([6], [1]), ([0], [101]), ([0], [-1]), ([5], [129])):
         refused(1, size, *bad)
