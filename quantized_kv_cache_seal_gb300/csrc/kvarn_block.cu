@@ -364,7 +364,7 @@ int launch_block_init(const BlockView& c, void* stream) {
 int launch_block_clear_errors(const BlockView& c, void* stream) {
     cudaStream_t s = (cudaStream_t)stream;
     const cudaError_t e = cudaMemsetAsync(c.base + c.lay.err, 0, 16, s);
-    return (int)(e != cudaSuccess ? e : cudaMemsetAsync(c.base + c.lay.counters, 0, kBlockMaxGrid * 4, s));
+    return (int)(e != cudaSuccess ? e : cudaMemsetAsync(c.base + c.lay.counters, 0, c.lay.partials - c.lay.counters, s));
 }
 
 int stream_capturing(void* stream, int* capturing) {

@@ -43,6 +43,7 @@ struct BlockLayout {
     size_t table;     // int32[max_seqs][num_layers][max_blocks]: pool slot of each sealed block
     size_t counters;  // int32[kBlockMaxGrid], zero between calls: arrivals at a split (sequence, KV head) of a
                       // decode call; segments taken and CTAs done of a prefill call
+    size_t warp_counters;  // int32[kBlockMaxGrid * 8]: the same of a decode call that cuts the line over warps
     size_t partials;  // float[kBlockMaxGrid][2][8 (D + 2)] of a decode call, or
                       // float[kBlockPrefillGrid][2][256 (D + 2)] of a prefill call
     size_t tail_k;    // T[max_seqs][num_layers][Hkv][B][D]: exact rows of the partial block
@@ -113,6 +114,7 @@ struct BlockDecodeParams {
 };
 // What a decode launch with prefixes or weights has beside.
 struct BlockDecodeMore {
+    int32_t alone;             // 1: the line is cut over the warps
     float2* sums;              // [units][r] or null: maximum and sum of each tile's weights, by head
     float2* totals;            // [rows][Hq] (with sums): of each row over all its keys, a prefix's among them
     const float *pre_o, *pre_lse;  // rows finished over shared prefixes (pre_lse null: none), [rows][Hq][D] and [rows][Hq]

@@ -309,14 +309,16 @@ __device__ __forceinline__ void exact_unit(State<D>& st, const uint16_t* k, cons
 // buffer, by one warp, a lane 4 channels (at head_dim 64 half the lanes). Where the CTA holds only a part of
 // the pair, the part goes to the workspace, and whichever part comes last adds them all in the order of the
 // cuts. row: of the pair's first head in q and out.
-template <int D, bool BF16>
+// ALONE: a warp's own state instead (w: this one), and parts of the warps' own.
+template <int D, bool BF16, bool ALONE>
 __device__ void join_heads(const BlockDecodeParams& p, const More& x, const uint8_t* smem, const Cursor& cur, bool whole,
-                           bool starts, int half, size_t row, int lane) {
+                           bool starts, int half, size_t row, int w, int lane) {
     using Sh = Shape<D>;
     const float* join = reinterpret_cast<const float*>(smem + Sh::kJoin);
     const float* sm = reinterpret_cast<const float*>(smem + Sh::kM);
     const float* sl = reinterpret_cast<const float*>(smem + Sh::kL);
-    const int heads = min(4, p.r - 4 * half), b = blockIdx.x;
+    const int heads = min(4, p.r - 4 * half), b = ALONE ? blockIdx.x * kWarps + w : blockIdx.x, workers = ALONE ? p.grid * kWarps : p.grid;
+    const int z0 = ALONE ? w : 0, z1 = ALONE ? w + 1 : kWarps;
     const bool live = 4 * lane < D;
     constexpr size_t kPart = 8 * (D + 2);  // floats: O [8][D], m [8], l [8]
     float* partials = reinterpret_cast<float*>(p.c.base + p.c.lay.partials);
@@ -345,9 +347,9 @@ __device__ void join_heads(const BlockDecodeParams& p, const More& x, const uint
         float big = kNegInf, l = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int z = 0; z < kWarps; ++z) big = fmaxf(big, sm[z * 4 + h]);
+        for (int z = z0; z < z1; ++z) big = fmaxf(big, sm[z * 4 + h]);
 #pragma unroll
-        for (int z = 0; z < kWarps; ++z) {
+        for (int z = z0; z < z1; ++z) {
             const float mz = sm[z * 4 + h], f = mz == kNegInf ? 1.f : ex2(mz - big);  // -inf: zeros or NaN
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
             if (live) x = *reinterpret_cast<const float4*>(join + (z * 4 + h) * Sh::kHeadStride + 4 * lane);
@@ -366,9 +368,9 @@ __device__ void join_heads(const BlockDecodeParams& p, const More& x, const uint
     }
     if (whole || 4 * half + heads < p.r) return;
     // CTAs first .. last share the pair; its first one's counter takes the arrivals
-    int32_t* counters = reinterpret_cast<int32_t*>(p.c.base + p.c.lay.counters);
-    const int first = (int)((((int64_t)cur.begin + 1) * p.grid - 1) / p.units);
-    const int last = (int)(((int64_t)cur.end * p.grid - 1) / p.units);
+    int32_t* counters = reinterpret_cast<int32_t*>(p.c.base + (ALONE ? p.c.lay.warp_counters : p.c.lay.counters));
+    const int first = (int)((((int64_t)cur.begin + 1) * workers - 1) / p.units);
+    const int last = (int)(((int64_t)cur.end * workers - 1) / p.units);
     __threadfence();
     __syncwarp();
     int n = 0;
@@ -431,7 +433,9 @@ __device__ void join_heads(const BlockDecodeParams& p, const More& x, const uint
     }
 }
 
-template <int D, bool INT8, bool BF16>
+// ALONE: the line is cut over the warps, not over the CTAs, and a warp ends its pairs by itself: where pairs are short, eight
+// warps would spend more time on joining than on their few tiles each.
+template <int D, bool INT8, bool BF16, bool ALONE>
 __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_constant__ BlockDecodeParams p KVARN_MORE_PARAM) {
     using Sh = Shape<D>;
 #ifndef KVARN_BLOCK_MORE
@@ -448,8 +452,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     uint64_t* free_bar = reinterpret_cast<uint64_t*>(smem + Sh::kFree);
     int* count = reinterpret_cast<int*>(smem + Sh::kCount);
     int32_t* err = reinterpret_cast<int32_t*>(c.base + c.lay.err);
-    const int b = blockIdx.x;
-    const int u0 = (int)(p.units * b / p.grid), u1 = (int)(p.units * (b + 1) / p.grid);
+    const int b = ALONE ? blockIdx.x * kWarps + w : blockIdx.x, workers = ALONE ? p.grid * kWarps : p.grid;
+    constexpr int kTurn = ALONE ? 1 : kWarps;
+    const int mine = ALONE ? 0 : w;
+    const int u0 = (int)(p.units * b / workers), u1 = (int)(p.units * (b + 1) / workers);
     if (lane < Sh::kStages) mbar_init(bars + lane, 1);
     if (threadIdx.x == 0) {
         mbar_init(free_bar, 1);
@@ -461,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     // Copies run ahead of the work: a sealed tile takes one ring entry, an exact one two (K rows, V
     // channel rows), an empty sequence's unit none. The next tile's slot is loaded a step early.
     Cursor ahead;
-    int ua = u0 + w, slot = 0, issued = 0, done = 0;  // issued, done: ring entries
+    int ua = u0 + mine, slot = 0, issued = 0, done = 0;  // issued, done: ring entries
     bool ok = true;                                   // no wait for a copy has given up
     const int sh = c.log2_block - 5;
     auto seek = [&]() {
@@ -492,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                 entry(tail_ptr(c, c.lay.tail_k, e.seq, ahead.h) + at, kSide);
                 entry(tail_ptr(c, c.lay.tail_v, e.seq, ahead.h) + at, kSide);
             }
-            ua += kWarps;
+            ua += kTurn;
             seek();
         }
     };
@@ -502,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     seek();
     pump();
 
-    int u = u0 + w, joins = 0;
+    int u = u0 + mine, joins = 0;
     for (int begin = u0; begin < u1; begin = min(cur.end, u1)) {
         cur.advance(p, begin);
         const int end = min(cur.end, u1);
@@ -550,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
         for (int i = 0; i < D / 16; ++i)
 #pragma unroll
             for (int z = 0; z < 4; ++z) st.o[i][z] = 0.f;
-        for (; u < end; u += kWarps) {
+        for (; u < end; u += kTurn) {
             if (!ok) continue;
             const TilePlace e = place_of(p, x, cur.i, u - cur.begin);
             const int tile = e.tile, sealed = e.n >> c.log2_block << sh;
@@ -588,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
         const bool whole = begin == cur.begin && end == cur.end;
 #pragma unroll 1
         for (int half = 0; half < (p.r > 4 ? 2 : 1); ++half, ++joins) {
-            if (joins > 0) bar_wait(free_bar, (uint32_t)((joins - 1) & 1), err);
+            if (!ALONE && joins > 0) bar_wait(free_bar, (uint32_t)((joins - 1) & 1), err);
             if (t >> 1 == half) {
                 const int h = 2 * (t & 1);
                 float* at = join + (w * 4 + h) * Sh::kHeadStride + g;
@@ -606,13 +612,19 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                     sl[w * 4 + h + 1] = st.l[1];
                 }
             }
+            if (ALONE) {
+                __syncwarp();
+                join_heads<D, BF16, ALONE>(p, x, smem, cur, whole, begin == cur.begin, half, (size_t)cur.i * p.hq + h0, w, lane);
+                __syncwarp();
+                continue;
+            }
             __threadfence_block();
             __syncwarp();
             int n = 0;
             if (lane == 0) n = atomicAdd(count, 1);
             if (__shfl_sync(0xffffffffu, n, 0) == kWarps - 1) {
                 __threadfence_block();
-                join_heads<D, BF16>(p, x, smem, cur, whole, begin == cur.begin, half, (size_t)cur.i * p.hq + h0, lane);
+                join_heads<D, BF16, ALONE>(p, x, smem, cur, whole, begin == cur.begin, half, (size_t)cur.i * p.hq + h0, w, lane);
                 __syncwarp();
                 if (lane == 0) {
                     *count = 0;
@@ -641,12 +653,15 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
 #define KVARN_PARAMS const BlockDecodeParams& p
 #endif
 
-template <int D, bool INT8, bool BF16>
+template <int D, bool INT8, bool BF16, bool ALONE = false>
 int launch(KVARN_PARAMS, cudaStream_t s) {
+#ifdef KVARN_BLOCK_MORE
+    if (!ALONE && x.alone) return launch<D, INT8, BF16, true>(p, x, s);
+#endif
     static SmemOnce once;
-    const int e = once.allow(reinterpret_cast<const void*>(decode_kernel<D, INT8, BF16>), Shape<D>::kSmem);
+    const int e = once.allow(reinterpret_cast<const void*>(decode_kernel<D, INT8, BF16, ALONE>), Shape<D>::kSmem);
     if (e) return e;
-    decode_kernel<D, INT8, BF16><<<p.grid, kThreads, Shape<D>::kSmem, s>>>(KVARN_ARGS);
+    decode_kernel<D, INT8, BF16, ALONE><<<p.grid, kThreads, Shape<D>::kSmem, s>>>(KVARN_ARGS);
     return (int)cudaGetLastError();
 }
 

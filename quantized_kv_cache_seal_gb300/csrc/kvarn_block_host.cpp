@@ -73,6 +73,7 @@ bool make_view(const kvarn_block_config& c, BlockView* v) {
     v->lay.err = take(16);
     v->lay.table = take(seq_layers * v->max_blocks * 4);
     v->lay.counters = take(kBlockMaxGrid * 4);
+    v->lay.warp_counters = take(kBlockMaxGrid * 8 * 4);
     v->lay.partials = take((U)std::max(kBlockMaxGrid * kBlockMaxRatio, kBlockPrefillGrid * 256) * 2 * (c.head_dim + 2) * 4);
     v->lay.tail_k = take(tail);
     v->lay.tail_v = take(tail);
@@ -362,6 +363,8 @@ kvarn_status run_decode(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, con
     const int64_t pairs = (int64_t)n_seqs * c->cfg.num_kv_heads, most = std::min(c->sms, kBlockMaxGrid);
     const bool equal = std::all_of(p.seqs, p.seqs + n_seqs, [](const BlockDecodeSeq& e) { return e.units == p.seqs[0].units; });
     p.grid = (int32_t)(equal && p.seqs[0].units <= 32 && pairs <= most ? pairs : std::min((units + 7) / 8, most));
+    // Short pairs, four tiles a warp at least: the line is cut over the warps.
+    x.alone = units >= 4 * 8 * most && units < 64 * pairs;
     if (c->host_only) return KVARN_OK;
     const kvarn_status st = ensure_init(c, stream);
     if (st) return st;

@@ -242,12 +242,14 @@ __device__ __forceinline__ void expand_line(const P& p, uint8_t* ring, uint64_t*
         return true;
     };
     RowPart now = look(), next = look(), then = look();
-    int ahead = 0;  // of these, on their way
-#pragma unroll 1
-    while (now.step >= 0) {
+    int ahead = 0;  // of the first two, on their way
+    auto pump = [&]() {
         if (ahead == 0 && fetch(now)) ahead = 1;
         if (ahead == 1 && fetch(next)) ahead = 2;
-        if (ahead == 2 && fetch(then)) ahead = 3;
+    };
+    pump();
+#pragma unroll 1
+    while (now.step >= 0) {
         uint8_t* dst = place(now.step);
         bool here = __all_sync(0xffffffffu, dst != nullptr);  // (the expansion of exact rows is warp-wide)
         float2 h = make_float2(1.f, 1.f);
@@ -275,8 +277,9 @@ __device__ __forceinline__ void expand_line(const P& p, uint8_t* ring, uint64_t*
         publish(now.step, h, bad);
         now = next;
         next = then;
-        then = look();
         ahead = max(ahead - 1, 0);
+        pump();
+        then = look();  // its slot is there by the time it is fetched, a turn from now
     }
     // Normally every copy was waited for above. After a wait that gave up nothing more was issued, and what is in flight
     // lands (a bounded wait again) before the CTA's shared memory goes away.

@@ -292,3 +292,34 @@ def test_after_a_wait_has_given_up():
         assert c.check_device_error() == 6
         assert all(torch.equal(f(), w) for f, w in zip(calls, want))
         assert c.check_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype,code,dim,block", [("fp16", "e4m3", 128, 64), ("bf16", "int8", 64, 32)])
+@pytest.mark.parametrize("hkv,r", [(8, 4), (10, 1), (7, 5), (8, 8)])
+def test_many_short_sequences(dtype, code, dim, block, hkv, r):
+    """Short pairs whose line is cut over warps: with a long prefix, walked once, and with weights."""
+    from tests.test_gpu_block_evict import near, received, some_weights
+    dt, seqs, n = TYPES[dtype], 200, 1500
+    lens = [(131 * i) % 700 for i in range(seqs)] + [n]
+    c = make(max_seqs=seqs + 1, num_q_heads=hkv * r, num_kv_heads=hkv, head_dim=dim, block_tokens=block, code=code, dtype=dt,
+             max_seq_len=1600, pool_blocks=sum(x // block for x in lens))
+    k, v = fill(c, lens, dt, 480)
+    q = tokens(seqs, hkv * r, dim, dt, 482, 0.3)
+    ids = list(range(seqs))
+    for pre in ([seqs] * seqs, None):
+        w = some_weights(c, 483)
+        before = w.clone()
+        out = c.decode_attention(0, ids, q, prefix_ids=pre, weights=w)
+        again = before.clone()
+        assert torch.equal(out, c.decode_attention(0, ids, q, prefix_ids=pre, weights=again)) and torch.equal(w, again)
+        for s in (0, 1, 2, 77, seqs - 1):  # 0 has no tokens of its own
+            if pre is None and s == 0:
+                assert not out[s].any()
+                continue
+            want, tol = want_of(q, s, k, v, None if pre is None else seqs, s, lens[s], 1, block, code, dim)
+            check(out[s:s + 1], want, tol, s)
+            first = 0 if pre is None else n
+            parts = ([block_ref.hold(k[seqs], block, code)] if pre else []) + [block_ref.hold(k[s], block, code)]
+            want, tol = received(q[s:s + 1], torch.cat(parts), dim ** -0.5, [first + lens[s] - 1], block, first)
+            near(w[s], before[s], want, tol, s)
+    assert c.check_device_error() == 0
