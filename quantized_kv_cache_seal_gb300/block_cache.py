@@ -148,7 +148,7 @@ class BlockCache:
         # what the workspace takes at most; where that is much, what it takes
         n = 0 if prefix_ids is None else 4 * q.numel() + 4 * self.heads * q.shape[0] + 512
         if weights is not None:
-            n += 8 * self.heads * len(seq_ids) * (1 + self._tiles * (1 if prefix_ids is None else 2)) + 512
+            n += 8 * self.heads * len(seq_ids) * (5 + self._tiles * (1 if prefix_ids is None else 2)) + 512
         with K.on_device(self.device, stream) as s:
             if out is None:
                 out = torch.empty_like(q)

@@ -112,6 +112,8 @@ struct BlockDecodeParams {
     float scale_log2;          // softmax scale * log2(e)
     BlockDecodeSeq seqs[kBlockMaxSeqs];
 };
+// Units that a (sequence, KV head) counts beside its tiles where the line is cut over warps: its end, in tiles.
+constexpr int kPairCost = 4;
 // What a decode launch with prefixes or weights has beside.
 struct BlockDecodeMore {
     int32_t alone;             // 1: the line is cut over the warps
@@ -188,6 +190,7 @@ struct BlockWindowParams {
 struct BlockWeighSeq {
     int32_t seq, rows, pad;   // rows of a KV head, and places for them in a tile's sums
     int32_t before, tiles;    // tiles of a prefix in front, its own
+    int32_t stride;           // places for them
     int32_t row;              // decode: of totals
     int32_t unit_begin, pair_begin;  // window: as there
     int64_t sum_begin;

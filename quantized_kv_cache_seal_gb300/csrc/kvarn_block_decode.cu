@@ -342,8 +342,10 @@ __device__ void join_heads(const BlockDecodeParams& p, const More& x, const uint
             *reinterpret_cast<uint2*>(p.out + (row + head) * D + 4 * lane) =
                 make_uint2(pack2<BF16>(y.x, y.y), pack2<BF16>(y.z, y.w));
     };
-#pragma unroll 1
-    for (int h = 0; h < heads; ++h) {
+    // (alone there is nothing else to do while a head's loads are on their way)
+#pragma unroll(ALONE ? 4 : 1)
+    for (int h = 0; h < (ALONE ? 4 : heads); ++h) {
+        if (ALONE && h >= heads) break;
         float big = kNegInf, l = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -370,7 +372,7 @@ __device__ void join_heads(const BlockDecodeParams& p, const More& x, const uint
     // CTAs first .. last share the pair; its first one's counter takes the arrivals
     int32_t* counters = reinterpret_cast<int32_t*>(p.c.base + (ALONE ? p.c.lay.warp_counters : p.c.lay.counters));
     const int first = (int)((((int64_t)cur.begin + 1) * workers - 1) / p.units);
-    const int last = (int)(((int64_t)cur.end * workers - 1) / p.units);
+    const int last = (int)(((int64_t)(cur.end - (ALONE ? kPairCost : 0)) * workers - 1) / p.units);
     __threadfence();
     __syncwarp();
     int n = 0;
@@ -511,7 +513,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     int u = u0 + mine, joins = 0;
     for (int begin = u0; begin < u1; begin = min(cur.end, u1)) {
         cur.advance(p, begin);
-        const int end = min(cur.end, u1);
+        const int tiles_end = cur.end - (ALONE ? kPairCost : 0);
+        if (ALONE && begin >= tiles_end) {  // of the pair nothing but its cost
+            u = min(cur.end, u1);
+            continue;
+        }
+        const int end = min(tiles_end, u1);
         const int h0 = cur.h * p.r;
         // the queries of the pair's r heads as B operands: lane 4 g + t holds head g, channels
         // 64 c + 16 t + 4 j + {0, 1} and {2, 3}
@@ -591,7 +598,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
             st.l[0] += __shfl_xor_sync(0xffffffffu, st.l[0], d);
             st.l[1] += __shfl_xor_sync(0xffffffffu, st.l[1], d);
         }
-        const bool whole = begin == cur.begin && end == cur.end;
+        const bool whole = begin == cur.begin && end == tiles_end;
+        if (ALONE) u = min(cur.end, u1);
 #pragma unroll 1
         for (int half = 0; half < (p.r > 4 ? 2 : 1); ++half, ++joins) {
             if (!ALONE && joins > 0) bar_wait(free_bar, (uint32_t)((joins - 1) & 1), err);

@@ -364,7 +364,17 @@ kvarn_status run_decode(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, con
     const bool equal = std::all_of(p.seqs, p.seqs + n_seqs, [](const BlockDecodeSeq& e) { return e.units == p.seqs[0].units; });
     p.grid = (int32_t)(equal && p.seqs[0].units <= 32 && pairs <= most ? pairs : std::min((units + 7) / 8, most));
     // Short pairs, four tiles a warp at least: the line is cut over the warps.
-    x.alone = units >= 4 * 8 * most && units < 64 * pairs;
+    x.alone = more && units >= 4 * 8 * most && units < 64 * pairs;
+    if (x.alone) {
+        units = 0;
+        for (int i = 0; i < n_seqs; ++i) {
+            p.seqs[i].unit_begin = (int32_t)units;
+            p.seqs[i].units += kPairCost;
+            units += (int64_t)p.seqs[i].units * c->cfg.num_kv_heads;
+        }
+        p.units = units;
+        p.grid = (int32_t)most;
+    }
     if (c->host_only) return KVARN_OK;
     const kvarn_status st = ensure_init(c, stream);
     if (st) return st;
@@ -383,7 +393,8 @@ kvarn_status run_decode(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, con
         s.seq = e.seq;
         s.rows = s.pad = c->r;
         s.before = tiles_of(x.pre_n[i]);
-        s.tiles = e.units - s.before;
+        s.tiles = e.units - s.before - (x.alone ? kPairCost : 0);
+        s.stride = e.units;
         s.row = i;
         s.unit_begin = s.pair_begin = 0;
         s.sum_begin = (int64_t)e.unit_begin * c->r;
@@ -547,7 +558,7 @@ kvarn_status check_prefixes(kvarn_block_cache* c, int32_t layer, int32_t n_seqs,
         steps += (m + 128 / c->r) * ((n + 127) / 128);  // more than there can be
     }
     for (int i = 0; i < n_seqs; ++i) c->seen[ids[i]] = 0;
-    if (!st && (tiles + n_seqs) * c->cfg.num_kv_heads >= 1ll << 31) st = fail(KVARN_ECAPACITY, "2^31 tiles of 32 tokens or more in a call");
+    if (!st && (tiles + n_seqs * (1 + kPairCost)) * c->cfg.num_kv_heads >= 1ll << 31) st = fail(KVARN_ECAPACITY, "2^31 tiles of 32 tokens or more in a call");
     if (!st && steps * c->cfg.num_kv_heads >= 1ll << 31) st = fail(KVARN_ECAPACITY, "2^31 steps of 128 keys or more in a call");
     return st;
 }
@@ -564,7 +575,7 @@ bool make_workspace(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const i
         const bool pre = prefix_ids && prefix_ids[i] >= 0;
         any = any || pre;
         rows += q_lens ? q_lens[i] : 1;
-        tiles += head_tiles(c->L(ids[i], layer) + (added ? added[i] : 0)) + (pre ? tiles_of(c->L(prefix_ids[i], layer)) : 0);
+        tiles += head_tiles(c->L(ids[i], layer) + (added ? added[i] : 0)) + (pre ? tiles_of(c->L(prefix_ids[i], layer)) : 0) + kPairCost;
     }
     auto take = [&](unsigned __int128 n) {
         const unsigned __int128 o = off;
@@ -986,7 +997,7 @@ kvarn_status kvarn_block_window_weights(kvarn_block_cache* c, int32_t layer, int
     wp.n_seqs = p.n_seqs;
     for (int i = 0; i < p.n_seqs; ++i) {
         const BlockRowsSeq& e = p.seqs[i];
-        wp.seqs[i] = BlockWeighSeq{e.seq, e.rows, e.pad, 0, tiles_of(e.n), 0, e.unit_begin, e.pair_begin, e.sum_begin};
+        wp.seqs[i] = BlockWeighSeq{e.seq, e.rows, e.pad, 0, tiles_of(e.n), tiles_of(e.n), 0, e.unit_begin, e.pair_begin, e.sum_begin};
     }
     return run_weigh(c, wp, stream);
 }

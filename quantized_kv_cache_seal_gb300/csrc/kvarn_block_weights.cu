@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kWeighThreads) weigh_kernel(const __grid_const
         if (turn == 0 && row < e.rows) of[row] = make_float2(s.x, s.y > 0.f && s.y < -kNegInf ? 1.f / s.y : 0.f);
     }
     __syncthreads();
-    const float2* sums = p.sums + e.sum_begin + ((int64_t)h * (e.before + e.tiles) + e.before) * e.pad;
+    const float2* sums = p.sums + e.sum_begin + ((int64_t)h * e.stride + e.before) * e.pad;
     float* to = p.weights + ((int64_t)e.seq * p.hkv + h) * p.cols;
     const int lane = t % p.lanes;
     for (int b = first + t / p.lanes; b < first + p.blocks; b += kWeighThreads / p.lanes) {  // whole warps

@@ -79,12 +79,12 @@ def test_workspace_sizes():
     rows = 2 * 8
     assert size([0, 1], [5, -1], None) == up(rows * 128 * 4) + up(rows * 4)
     assert size([0, 1], [5, 5], [100, 3]) == up(103 * 8 * 128 * 4) + up(103 * 8 * 4)
-    # tiles of 32 tokens, heads, 8 bytes
+    # tiles of 32 tokens and four more a sequence, heads, 8 bytes
     # and a row's totals
-    assert size([0, 1], None, None, False, True) == up((4 + 3) * 8 * 8) + up(2 * 8 * 8)
-    assert size([2], None, None, False, True) == up(8 * 8) + up(8 * 8)  # an empty sequence has one
-    assert size([0], None, [29], True, True) == up(5 * 8 * 8) + up(29 * 8 * 8)
-    assert size([0], [5], None, False, True) == up(8 * 128 * 4) + up(8 * 4) + up((4 + 10) * 8 * 8) + up(8 * 8)
+    assert size([0, 1], None, None, False, True) == up((4 + 3 + 2 * 4) * 8 * 8) + up(2 * 8 * 8)
+    assert size([2], None, None, False, True) == up((1 + 4) * 8 * 8) + up(8 * 8)  # an empty sequence has one
+    assert size([0], None, [29], True, True) == up((5 + 4) * 8 * 8) + up(29 * 8 * 8)
+    assert size([0], [5], None, False, True) == up(8 * 128 * 4) + up(8 * 4) + up((4 + 10 + 4) * 8 * 8) + up(8 * 8)
     for bad in (([6], None, None), ([0], [6], None), ([0], None, [-1])):
         refused(1, size, *bad)
     refused(1, K.kvarn_block_attend_workspace, c, 2, [0], None, None)
