@@ -13,14 +13,19 @@
 namespace kvarn {
 namespace {
 
-constexpr int kSoftWarps = 8, kExpWarps = 8, kIssuer = kSoftWarps + kExpWarps, kThreads = 32 * (kIssuer + 3);
+// Warps: two softmax warpgroups, then the first of each four the issuer, the one that fills the rings and an idle one, the others
+// expansion warps.
+// The issuer's scheduler has no expansion warp: an MMA takes its warp about 30 turns there (140 clocks an MMA with two, 00 without).
+constexpr int kSoftWarps = 8, kExpWarps = 8, kIssuer = kSoftWarps, kThreads = 32 * (kSoftWarps + kExpWarps + 3);
+__device__ __forceinline__ int expansion_warp(int w) { return (w - kSoftWarps) / 4 * 3 + (w & 3) - 1; }  // 0 .. 7, of w & 3 > 0
+static_assert(kSoftWarps % 4 == 0 && kExpWarps == 8, "warps by scheduler");
 constexpr int kStep = 128, kRing = 8;
 constexpr float kRaise = 8.f, kShift = 7.f;  // m is raised when it would grow by more; weights are at most 2^(both)
 constexpr uint32_t kColS = 0, kColO = 256;
 // barriers
 constexpr int kKFull = 0, kVFull = kKFull + kRing, kQFull = kVFull + kRing, kKEmpty = kQFull + kRing, kVEmpty = kKEmpty + 2,
               kSFull = kVEmpty + 2, kPFull = kSFull + 2, kOFull = kPFull + 2, kOEmpty = kOFull + 2, kQEmpty = kOEmpty + 2,
-              kDrain = kQEmpty + 1, kLanded = kDrain + 1, kNumBars = kLanded + 2 * kExpWarps;
+              kDrain = kQEmpty + 1, kRaw = kDrain + 1, kNumBars = kRaw + 2 * kExpWarps + 2;
 
 template <int D>
 struct Shape {
@@ -28,12 +33,13 @@ struct Shape {
     static constexpr int kQ = 0;
     static constexpr int kK = kTileK;                            // 2 stages
     static constexpr int kV = kK + 2 * kTileK;                   // 2 stages
-    static constexpr int kRaw = kV + 2 * kTileV;                 // two ring entries of an expansion warp
-    static constexpr int kHeadV = kRaw + kExpWarps * 2 * kRingEntry<D>;  // float4[kRing][4]: log2 of V's scale, kDenomUnit over it, non-finite
+    static constexpr int kRings = kV + 2 * kTileV;
+    static constexpr int kHeadV = kRings + Rings<D>::kBytes;     // float4[kRing][4]: log2 of V's scale, kDenomUnit over it, non-finite
     static constexpr int kHeadK = kHeadV + kRing * 64;           // float[kRing][4]: K's scale
     static constexpr int kPower = kHeadK + kRing * 16;           // int8[kRing][128]
     static constexpr int kBars = kPower + kRing * 128;
-    static constexpr int kTmem = kBars + 8 * kNumBars;
+    static constexpr int kWhat = kBars + 8 * kNumBars;           // int[8][2]
+    static constexpr int kTmem = kWhat + 64;
     static constexpr int kSmem = kTmem + 16;
     static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
 };
@@ -75,11 +81,12 @@ __device__ __forceinline__ void issue_role(const BlockFlatParams& p, uint32_t sb
                 bar_wait(bars + kKFull + k % kRing, (uint32_t)(k / kRing & 1), err);
                 __syncwarp();
                 tc_fence_after();
-                const uint32_t q = base + (Sh::kQ >> 4), kt = base + ((Sh::kK + (k & 1) * Sh::kTileK) >> 4);
+                const int b = __shfl_sync(0xffffffffu, k & 1, 0);  // seen to be uniform
+                const uint32_t q = base + (Sh::kQ >> 4), kt = base + ((Sh::kK + b * Sh::kTileK) >> 4);
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
                     const uint32_t off = ((ks >> 2) * kAtom + (ks & 3) * 32) >> 4;
-                    if (leader) mma_ss(kColS + 128 * (k & 1), desc128(q + off), desc128(kt + off), kIdesc<128>, ks > 0);
+                    if (leader) mma_ss(kColS + 128 * b, desc128(q + off), desc128(kt + off), kIdesc<128>, ks > 0);
                 }
                 if (leader) mma_commit(bars + kSFull + (k & 1));
                 if (leader) mma_commit(bars + kKEmpty + (k & 1));
@@ -87,18 +94,19 @@ __device__ __forceinline__ void issue_role(const BlockFlatParams& p, uint32_t sb
                 ++k;
             }
             if (i > 0) {
-                const int at = i < n ? k - 2 : k - 1, b = at & 1;
+                const int at = i < n ? k - 2 : k - 1, b = __shfl_sync(0xffffffffu, at & 1, 0);
                 if (seg > 0 && i <= 2) bar_wait(bars + kOEmpty + b, (uint32_t)((seg - 1) & 1), err);  // the last segment's sums are out
                 bar_wait(bars + kVFull + at % kRing, (uint32_t)(at / kRing & 1), err);
                 bar_wait(bars + kPFull + b, (uint32_t)(at >> 1 & 1), err);
                 __syncwarp();
                 tc_fence_after();
+                const uint32_t more = __shfl_sync(0xffffffffu, i > 2 ? 1u : 0u, 0);
                 const uint32_t v = base + ((Sh::kV + b * Sh::kTileV) >> 4);
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks)
                     if (leader)
                         mma_ts(kColO + 128 * b, kColS + 128 * b + 8 * ks, desc128(v + (((ks >> 2) * (D * 128) + (ks & 3) * 32) >> 4)),
-                               kIdesc<D>, ks > 0 || i > 2 ? 1u : 0u);
+                               kIdesc<D>, ks > 0 ? 1u : more);
                 if (leader) mma_commit(bars + kVEmpty + b);
             }
         }
@@ -118,15 +126,26 @@ template <int D>
 constexpr int kPart = 128 * (D + 3);
 
 // Warpgroup b has tile b; thread et owns row et.
-template <int D>
+template <int D, bool BF16>
 __device__ __forceinline__ void softmax_role(const BlockFlatParams& p, uint8_t* smem, uint64_t* bars, int32_t* err, int et, int b,
                                              uint32_t lane_off) {
     using Sh = Shape<D>;
     const uint32_t ts = kColS + 128 * b + lane_off, to = kColO + 128 * b + lane_off;
+    // The rows of the next segment are on their way while this one's sums are written.
+    const Rows<D, kSoftWarps> rows(smem + Sh::kQ, 4 * b + (et >> 5), et & 31);
+    auto ready = [&](int s) {
+        rows.template finish<BF16>(p.scale_log2, reinterpret_cast<int8_t*>(smem + Sh::kPower) + s % kRing * 128);
+        mbar_arrive(bars + kQFull + s % kRing);
+    };
     int k = 0, seg = 0;
     Walk w(p);
+    bool more = w.next();
+    if (more) {
+        rows.fetch(p, w);
+        ready(0);
+    }
 #pragma unroll 1
-    for (; w.next(); ++seg) {
+    for (; more; ++seg) {
         const int n = p.seqs[w.i].n;
         const int begin = w.j0 + ((b ^ k) & 1);
         float m = kNegInf, l = 0.f, qs = 1.f;
@@ -216,12 +235,18 @@ __device__ __forceinline__ void softmax_role(const BlockFlatParams& p, uint8_t* 
             tc_fence_before();
             mbar_arrive(bars + kPFull + b);
         }
-        bar_wait(bars + kOFull + b, (uint32_t)(seg & 1), err);
-        __syncwarp();
-        tc_fence_after();
         // of the pair's part in this CTA (a pair's first CTA is no sooner than the pair before's last)
         float* part = p.parts + (size_t)((p.seqs[w.i].pair_begin + w.pair + blockIdx.x) * 2 + b) * kPart<D>;
         const bool some = begin < w.j1;
+        more = w.next();
+        if (more) {
+            bar_wait(bars + kQEmpty, (uint32_t)(seg & 1), err);
+            __syncwarp();
+            rows.fetch(p, w);
+        }
+        bar_wait(bars + kOFull + b, (uint32_t)(seg & 1), err);
+        __syncwarp();
+        tc_fence_after();
 #pragma unroll 1
         for (int ch = 0; ch < D / 32; ++ch) {
             uint32_t o[32];
@@ -237,6 +262,7 @@ __device__ __forceinline__ void softmax_role(const BlockFlatParams& p, uint8_t* 
         part[128 * D + 256 + et] = __uint_as_float(bad);
         tc_fence_before();
         mbar_arrive(bars + kOEmpty + b);
+        if (more) ready(seg + 1);
     }
 }
 
@@ -251,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1) flat_kernel(const __grid_constant
         for (int k = 0; k < kRing; ++k) {
             mbar_init(bars + kKFull + k, 128);
             mbar_init(bars + kVFull + k, 128);
-            mbar_init(bars + kQFull + k, 64);
+            mbar_init(bars + kQFull + k, 32 * kSoftWarps);
         }
         for (int k = 0; k < 2; ++k) {
             mbar_init(bars + kKEmpty + k, 1);
@@ -263,7 +289,8 @@ __global__ void __launch_bounds__(kThreads, 1) flat_kernel(const __grid_constant
         }
         mbar_init(bars + kQEmpty, 1);
         mbar_init(bars + kDrain, 1);
-        for (int k = 0; k < 2 * kExpWarps; ++k) mbar_init(bars + kLanded + k, 1);
+        for (int k = 0; k < 2 * kExpWarps; ++k) mbar_init(bars + kRaw + k, 1);
+        for (int k = 0; k < 2; ++k) mbar_init(bars + kRaw + 2 * kExpWarps + k, kExpWarps);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (w == kIssuer) {
@@ -278,17 +305,18 @@ __global__ void __launch_bounds__(kThreads, 1) flat_kernel(const __grid_constant
     // Were it ever not so, the launch would do nothing but say so.
     const bool placed = *reinterpret_cast<volatile uint32_t*>(smem + Sh::kTmem) == 0 && (smem_addr(smem) & 1023) == 0;
     if (!placed && t == 0) atomicOr(err, kErrBadSlot);
+    const Rings<D> rings = {smem + Sh::kRings, bars + kRaw, bars + kRaw + 2 * kExpWarps, reinterpret_cast<int32_t*>(smem + Sh::kWhat)};
+    const int steps = (int)(p.units * (blockIdx.x + 1) / p.grid - p.units * blockIdx.x / p.grid);
     if (!placed) {
     } else if (w < kSoftWarps) {
-        softmax_role<D>(p, smem, bars, err, t & 127, w >> 2, (uint32_t)(32 * (w & 3)) << 16);
-    } else if (w < kIssuer) {
-        const int x = w - kSoftWarps, wp = x & 3;
-        uint8_t* ring = smem + Sh::kRaw + x * 2 * kRingEntry<D>;
+        softmax_role<D, BF16>(p, smem, bars, err, t & 127, w >> 2, (uint32_t)(32 * (w & 3)) << 16);
+    } else if (w & 3) {
+        const int x = expansion_warp(w), wp = x & 3;
         if (x < 4)
-            expand_line<D, INT8, BF16, false, 1>(
-                p, ring, bars + kLanded + 2 * x, err, 0, wp, lane,
-                [&](int k) -> uint8_t* {
-                    if (k >= 2 && !bar_wait(bars + kKEmpty + (k & 1), (uint32_t)(((k >> 1) - 1) & 1), err)) return nullptr;
+            expand_steps<D, INT8, BF16, false, 1>(
+                rings, x, 0, steps, err, lane,
+                [&](int k) {
+                    if (k >= 2) bar_wait(bars + kKEmpty + (k & 1), (uint32_t)(((k >> 1) - 1) & 1), err);
                     return smem + Sh::kK + (k & 1) * Sh::kTileK;
                 },
                 [&](int k, float2 h, uint32_t) {
@@ -296,10 +324,10 @@ __global__ void __launch_bounds__(kThreads, 1) flat_kernel(const __grid_constant
                     mbar_arrive(bars + kKFull + k % kRing);
                 });
         else
-            expand_line<D, INT8, BF16, true, 1>(
-                p, ring, bars + kLanded + 2 * x, err, 0, wp, lane,
-                [&](int k) -> uint8_t* {
-                    if (k >= 2 && !bar_wait(bars + kVEmpty + (k & 1), (uint32_t)(((k >> 1) - 1) & 1), err)) return nullptr;
+            expand_steps<D, INT8, BF16, true, 1>(
+                rings, x, 0, steps, err, lane,
+                [&](int k) {
+                    if (k >= 2) bar_wait(bars + kVEmpty + (k & 1), (uint32_t)(((k >> 1) - 1) & 1), err);
                     return smem + Sh::kV + (k & 1) * Sh::kTileV;
                 },
                 [&](int k, float2 h, uint32_t bad) {
@@ -309,15 +337,8 @@ __global__ void __launch_bounds__(kThreads, 1) flat_kernel(const __grid_constant
                 });
     } else if (w == kIssuer) {
         issue_role<D>(p, smem_addr(smem), bars, err);
-    } else {
-        int seg = 0;
-        for (Walk x(p); x.next(); ++seg) {
-            if (seg > 0) bar_wait(bars + kQEmpty, (uint32_t)((seg - 1) & 1), err);
-            __syncwarp();
-            make_rows<D, BF16, 2>(p, x, smem + Sh::kQ, reinterpret_cast<int8_t*>(smem + Sh::kPower) + seg % kRing * 128,
-                                  w - kIssuer - 1, lane);
-            mbar_arrive(bars + kQFull + seg % kRing);
-        }
+    } else if (w == kIssuer + 4) {
+        fill_rings<D, true>(p, rings, steps, err, lane);
     }
     tc_fence_before();
     __syncthreads();
@@ -329,8 +350,8 @@ __global__ void __launch_bounds__(kThreads, 1) flat_kernel(const __grid_constant
     }
 }
 
-// The parts of a pair (blockIdx.x), 32 rows of it (blockIdx.y), in the order of the cuts: a lane a row, the warps in turns of parts for the
-// maxima and sums, then of four channels.
+// The parts of a pair (blockIdx.x) for 32 rows of it (blockIdx.y) and 32 channels (blockIdx.z), in the order of the cuts: a lane a row,
+// the warps in turns of parts for the maxima and sums, then four channels each.
 constexpr int kJoinWarps = 8, kMostParts = 2 * kBlockPrefillGrid;
 template <int D, bool BF16>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ BlockFlatParams p) {
@@ -379,10 +400,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
     const int all = tile * 128 + row;
     if (all >= e.rows) return;
     const size_t out = (size_t)(e.q_row + all / p.r) * p.hq + h * p.r + all % p.r;
-    if (w == 0) p.pre_lse[out] = lse_of(m, l, kShift);
+    if (w == 0 && blockIdx.z == 0) p.pre_lse[out] = lse_of(m, l, kShift);
     const float inv = kDenomUnit * (l == 0.f ? 0.f : 1.f / l);
-#pragma unroll 1
-    for (int c = w; c < D / 4; c += kJoinWarps) {
+    {
+        static_assert(kJoinWarps * 4 == 32, "channels of a CTA");
+        const int c = blockIdx.z * kJoinWarps + w;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
         for (int z = 0; z < parts; ++z) {
@@ -412,7 +434,7 @@ int launch(const BlockFlatParams& p, int pairs, cudaStream_t s) {
     const int e = once.allow(reinterpret_cast<const void*>(flat_kernel<D, INT8, BF16>), Shape<D>::kSmem);
     if (e) return e;
     flat_kernel<D, INT8, BF16><<<p.grid, kThreads, Shape<D>::kSmem, s>>>(p);
-    join_kernel<D, BF16><<<dim3(pairs, 4), 32 * kJoinWarps, 0, s>>>(p);
+    join_kernel<D, BF16><<<dim3(pairs, 4, D / 32), 32 * kJoinWarps, 0, s>>>(p);
     return (int)cudaGetLastError();
 }
 

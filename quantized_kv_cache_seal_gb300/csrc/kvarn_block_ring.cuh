@@ -31,58 +31,61 @@ struct RowWalk {
 
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// WARPS warps write a segment's rows as its Q tile (K-major, 128-byte swizzle) and the exponents of the powers of two
-// that they stand for; warp w.
-// All of a warp's rows are on their way together; bf16 values and a scale below 0 (which turns the query's sign, so
-// that larger S is always a larger logit) take a second look. A scale of 0 makes the queries zeros: all logits are 0.
-template <int D, bool BF16, int WARPS, class P>
-__device__ __forceinline__ void make_rows(const P& p, const RowWalk<P>& s, uint8_t* dst, int8_t* power, int w, int lane) {
-    const bool zero = p.scale_log2 == 0.f;
-    const uint32_t sign = p.scale_log2 < 0.f ? 0x80008000u : 0u;
-    constexpr int kLanes = D / 8, kRows = 32 / kLanes, kTurns = 128 / kRows / WARPS;
-    const auto& e = p.seqs[s.i];
-    const int first = w * (128 / WARPS) + lane / kLanes;
-    auto at = [&](int z) { return dst + (lane % kLanes >> 3) * kAtom + swz(first + z * kRows, lane & 7); };
+// WARPS warps write a segment's rows as its Q tile (K-major, 128-byte swizzle) and the exponents of the powers of two that they
+// stand for; warp w of them. All of a warp's rows are on their way together; bf16 values and a scale below 0 (which turns
+// the query's sign, so that larger S is always a larger logit) take a second look. A scale of 0 makes the queries zeros: all
+// logits are 0.
+template <int D, int WARPS>
+struct Rows {
+    static constexpr int kLanes = D / 8, kRows = 32 / kLanes, kTurns = 128 / kRows / WARPS;
+    uint8_t* dst;
+    int first, lane;
+    __device__ __forceinline__ Rows(uint8_t* dst_, int w, int lane_)
+        : dst(dst_), first(w * (128 / WARPS) + lane_ / kLanes), lane(lane_) {}
+    __device__ __forceinline__ uint8_t* at(int z) const { return dst + (lane % kLanes >> 3) * kAtom + swz(first + z * kRows, lane & 7); }
+    template <class P>
+    __device__ __forceinline__ void fetch(const P& p, const RowWalk<P>& s) const {
+        const auto& e = p.seqs[s.i];
+        const int tok0 = s.tile * 128 / p.r, in0 = s.tile * 128 - tok0 * p.r, inv = 65536 / p.r + 1;
+        const uint4* q = reinterpret_cast<const uint4*>(p.q + ((size_t)(e.q_row + tok0) * p.hq + s.h * p.r) * D) + lane % kLanes;
 #pragma unroll 4
-    for (int z = 0; z < kTurns; ++z) {
-        const int all = s.tile * 128 + first + z * kRows;
-        if (all < e.rows && !zero)
-            cp_async_16(at(z), reinterpret_cast<const uint4*>(p.q + ((size_t)(e.q_row + all / p.r) * p.hq + s.h * p.r + all % p.r) * D) +
-                                   lane % kLanes);
-        else
-            *reinterpret_cast<uint4*>(at(z)) = make_uint4(0, 0, 0, 0);
-    }
-    cp_async_wait_all();
-#pragma unroll 4
-    for (int z = 0; z < kTurns; ++z) {
-        int ex = 0;  // -114 to 113
-        if (BF16 || sign) {
-            uint4 r = *reinterpret_cast<const uint4*>(at(z));
-            if (BF16) {
-                uint32_t top = max_of(0, r);
-                top = max(top & 0xffffu, top >> 16);
-#pragma unroll
-                for (int d = kLanes / 2; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-                ex = exponent_of<BF16>(top) - kExactK;
-                r = scaled_f16<BF16>(r, power2(-ex));
-            }
-            *reinterpret_cast<uint4*>(at(z)) = make_uint4(r.x ^ sign, r.y ^ sign, r.z ^ sign, r.w ^ sign);
+        for (int z = 0; z < kTurns; ++z) {
+            const int row = first + z * kRows, in = in0 + row, tok = in * inv >> 16;  // in / r: in < 136, r <= 8
+            if (s.tile * 128 + row < e.rows && p.scale_log2 != 0.f)
+                cp_async_16(at(z), q + ((size_t)tok * p.hq + in - tok * p.r) * kLanes);
+            else
+                *reinterpret_cast<uint4*>(at(z)) = make_uint4(0, 0, 0, 0);
         }
-        if (lane % kLanes == 0) power[first + z * kRows] = (int8_t)ex;
     }
-    fence_proxy_async_smem();
-}
+    template <bool BF16>
+    __device__ __forceinline__ void finish(float scale_log2, int8_t* power) const {
+        const uint32_t sign = scale_log2 < 0.f ? 0x80008000u : 0u;
+        cp_async_wait_all();
+#pragma unroll 4
+        for (int z = 0; z < kTurns; ++z) {
+            int ex = 0;  // -114 to 113
+            if (BF16 || sign) {
+                uint4 r = *reinterpret_cast<const uint4*>(at(z));
+                if (BF16) {
+                    uint32_t top = max_of(0, r);
+                    top = max(top & 0xffffu, top >> 16);
+#pragma unroll
+                    for (int d = kLanes / 2; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+                    ex = exponent_of<BF16>(top) - kExactK;
+                    r = scaled_f16<BF16>(r, power2(-ex));
+                }
+                *reinterpret_cast<uint4*>(at(z)) = make_uint4(r.x ^ sign, r.y ^ sign, r.z ^ sign, r.w ^ sign);
+            }
+            if (lane % kLanes == 0) power[first + z * kRows] = (int8_t)ex;
+        }
+        fence_proxy_async_smem();
+    }
+};
 
 // What a row's S is multiplied with, beside K's scale, for its logits.
 __device__ __forceinline__ float row_factor(float scale_log2, int power) {
     return (scale_log2 == 0.f ? 1.f : fabsf(scale_log2)) * power2(power);
 }
-
-// A 32-token part of a step: of sequence `seq` with n tokens. step -1: none; slot -1: exact tokens, or none.
-struct RowPart {
-    int step, seq, n, kvh, tile, slot;
-    __device__ __forceinline__ int exact() const { return slot < 0 ? n - tile * kTileTokens : 0; }  // tokens, none if <= 0
-};
 
 template <int D>
 constexpr int kRingEntry = 16 + kTileTokens * D;  // scales and codes of one side of a tile; two hold an exact part
@@ -175,120 +178,128 @@ __device__ __forceinline__ void expand_rows(const uint8_t* src, int nv, uint8_t*
     }
 }
 
-// One expansion warp: part wp of every STRIDE-th step from `first` on, K or V. Codes come by bulk copies into a ring of the warp's own (two
-// entries at `ring`, a barrier each), two parts ahead of the one that is expanded, pool slots a part earlier; an exact
-// part takes both entries. place(step): the tile to write, once it is free (null: the wait gave up); publish(step, h, bad):
-// the tile is there.
-template <int D, bool INT8, bool BF16, bool IS_V, int STRIDE, class P, class Place, class Publish>
-__device__ __forceinline__ void expand_line(const P& p, uint8_t* ring, uint64_t* landed, int32_t* err, int first, int wp, int lane,
-                                            Place place, Publish publish) {
+// Eight rings of two entries each, one of every expansion warp x: part x & 3 (32 tokens) of every step, K for x < 4 and V
+// for the others (SIDES), or K of every other step, the odd ones for x >= 4. The rings go in step: turn t (step t, or steps 2 t and
+// 2 t + 1) is entry t & 1 of each. An exact part takes both entries, so a turn with one waits for the turn before to be through,
+// and the turn behind it for it.
+template <int D>
+struct Rings {
+    static constexpr int kCount = 8;
+    static constexpr int kBytes = kCount * 2 * kRingEntry<D>;
+    uint8_t* data;     // [kCount][2][kRingEntry]
+    uint64_t* full;    // barriers [kCount][2]
+    uint64_t* empty;   // barriers [2], of all rings
+    int32_t* what;     // [kCount][2]: kCodes, or exact tokens, none if 0
+    static constexpr int kCodes = -1;
+};
+
+// One warp fills the rings, a lane each (the way along the line is the same for all, and costs an expansion warp as much as the
+// conversion). Pool slots are looked up a turn earlier.
+template <int D, bool SIDES, class P>
+__device__ __forceinline__ void fill_rings(const P& p, const Rings<D>& rings, int steps, int32_t* err, int lane) {
     const BlockView& c = p.c;
-    const int sh = c.log2_block - 5;
+    const int sh = c.log2_block - 5, wp = lane & 3, x = lane & 7;
+    const bool v = SIDES && x >= 4;
+    uint8_t* data = rings.data + x * 2 * kRingEntry<D>;
+    uint64_t* full = rings.full + 2 * x;
+    volatile int32_t* what = rings.what + 2 * x;
+    struct Part {
+        int seq, n, kvh, tile, slot;  // seq -1: no more; slot -1: exact tokens, or none
+    };
     RowWalk<P> w(p);
     bool more = w.next();
-    int j = w.j0, k = 0;  // the next step to look at
+    int j = w.j0;
     auto skip = [&]() {
-        ++k;
         if (more && ++j == w.j1) {
             more = w.next();
             if (more) j = w.j0;
         }
     };
-    if (first) skip();
+    if (!SIDES && x >= 4) skip();
     auto look = [&]() {
-        RowPart x = {-1, 0, 0, 0, 0, -1};
-        if (!more) return x;
+        Part a = {-1, 0, 0, 0, -1};
+        if (!more) return a;
         const auto& e = p.seqs[w.i];
-        x = RowPart{k, e.seq, e.n, w.h, 4 * j + wp, -1};
-        if (x.tile < e.n >> c.log2_block << sh) x.slot = __ldg(block_table(c, e.seq) + (x.tile >> sh));
-#pragma unroll
-        for (int z = 0; z < STRIDE; ++z) skip();
-        return x;
+        a = Part{e.seq, e.n, w.h, 4 * j + wp, -1};
+        if (a.tile < e.n >> c.log2_block << sh) a.slot = __ldg(block_table(c, e.seq) + (a.tile >> sh));
+        skip();
+        if (!SIDES) skip();
+        return a;
     };
-    int issued = 0, done = 0;  // entries; entry x is place x & 1, phase x >> 1 of its barrier
-    bool ok = true;            // no wait has given up
-    // the part's copy, where there is room for it
-    auto fetch = [&](const RowPart& a) {
-        if (!ok) return false;
-        if (a.slot >= 0) {
-            if (issued - done >= 2) return false;
-            if (lane == 0) {
-                const uint8_t* rec = tile_ptr(c, a.slot, a.kvh, a.tile & ((1 << sh) - 1));
-                uint8_t* to = ring + (issued & 1) * kRingEntry<D>;
-                mbar_arrive_expect_tx(landed + (issued & 1), kRingEntry<D>);
-                if (IS_V) {
-                    bulk_g2s(to, rec, 16, landed + (issued & 1));
-                    bulk_g2s(to + 16, rec + 16 + kTileTokens * D, kTileTokens * D, landed + (issued & 1));
-                } else {
-                    bulk_g2s(to, rec, kRingEntry<D>, landed + (issued & 1));
-                }
-            }
-            ++issued;
-        } else if (a.exact() > 0) {
-            if (issued != done) return false;
-            const bool odd = issued & 1;
-            if (lane == 0) {
-                if (odd) mbar_arrive(landed + 1);  // from the ring's start on
+    const int turns = SIDES ? steps : (steps + 1) / 2;
+    bool ok = true, alone = false;  // alone: the turn before has the rings for itself
+    Part now = look(), next = look();
+    int t = 0;
+#pragma unroll 1
+    for (; t < turns; ++t) {
+        const int y = t & 1, exact = now.slot < 0 && now.seq >= 0 ? max(now.n - now.tile * kTileTokens, 0) : 0;
+        const bool was = alone;
+        alone = __any_sync(0xffffffffu, exact > 0);
+        bool here = t < 2 || bar_wait(rings.empty + y, (uint32_t)(((t >> 1) - 1) & 1), err);
+        if (t > 0 && (was || alone)) here = bar_wait(rings.empty + (y ^ 1), (uint32_t)(((t - 1) >> 1) & 1), err) && here;
+        ok = __all_sync(0xffffffffu, here);
+        if (!ok) break;
+        if (lane < Rings<D>::kCount) {
+            if (now.slot >= 0) {
+                const uint8_t* rec = tile_ptr(c, now.slot, now.kvh, now.tile & ((1 << sh) - 1));
+                uint8_t* to = data + y * kRingEntry<D>;
+                what[y] = Rings<D>::kCodes;
+                mbar_arrive_expect_tx(full + y, kRingEntry<D>);
+                // scales, and K's codes behind them, or V's
+                bulk_g2s(to, rec, 16, full + y);
+                bulk_g2s(to + 16, rec + 16 + (v ? kTileTokens * D : 0), kTileTokens * D, full + y);
+            } else if (exact) {
                 constexpr int kBytes = kTileTokens * D * 2;
                 static_assert(kBytes <= 2 * kRingEntry<D>, "room for an exact part");
-                mbar_arrive_expect_tx(landed, kBytes);
-                bulk_g2s(ring, tail_ptr(c, IS_V ? c.lay.tail_v : c.lay.tail_k, a.seq, a.kvh) +
-                                   (size_t)(a.tile - (a.n >> c.log2_block << sh)) * (kTileTokens * D), kBytes, landed);
-                mbar_arrive(landed + 1);
-            }
-            if (odd) ++issued, ++done;
-            issued += 2;
-        }
-        return true;
-    };
-    RowPart now = look(), next = look(), then = look();
-    int ahead = 0;  // of the first two, on their way
-    auto pump = [&]() {
-        if (ahead == 0 && fetch(now)) ahead = 1;
-        if (ahead == 1 && fetch(next)) ahead = 2;
-    };
-    pump();
-#pragma unroll 1
-    while (now.step >= 0) {
-        uint8_t* dst = place(now.step);
-        bool here = __all_sync(0xffffffffu, dst != nullptr);  // (the expansion of exact rows is warp-wide)
-        float2 h = make_float2(1.f, 1.f);
-        uint32_t bad = 0;
-        int used = 0;
-        if (here && ok) {
-            if (now.slot >= 0) {
-                here = bar_wait(landed + (done & 1), (uint32_t)(done >> 1 & 1), err);
-                const uint8_t* rec = ring + (done & 1) * kRingEntry<D>;
-                const float4 hd = *reinterpret_cast<const float4*>(rec);
-                h = IS_V ? make_float2(hd.z, hd.w) : make_float2(hd.x, 0.f);
-                expand_codes<D, INT8, IS_V>(rec, dst, wp, lane);
-                used = 1;
+                what[y] = min(exact, kTileTokens);
+                mbar_arrive_expect_tx(full + y, kBytes);
+                bulk_g2s(data, tail_ptr(c, v ? c.lay.tail_v : c.lay.tail_k, now.seq, now.kvh) +
+                                   (size_t)(now.tile - (now.n >> c.log2_block << sh)) * (kTileTokens * D), kBytes, full + y);
             } else {
-                if (now.exact() > 0) {
-                    here = __all_sync(0xffffffffu, bar_wait(landed, (uint32_t)(done >> 1 & 1), err));
-                    used = 2;
-                }
-                expand_rows<D, BF16, IS_V>(ring, now.exact(), dst, wp, lane, h, bad);
+                what[y] = 0;
+                mbar_arrive(full + y);
             }
         }
-        ok = __all_sync(0xffffffffu, here) && ok;  // one answer for the warp; also: all lanes have read
-        if (ok) done += used;
-        fence_proxy_async_smem();
-        publish(now.step, h, bad);
+        __syncwarp();
         now = next;
-        next = then;
-        ahead = max(ahead - 1, 0);
-        pump();
-        then = look();  // its slot is there by the time it is fetched, a turn from now
+        next = look();
     }
-    // Normally every copy was waited for above. After a wait that gave up nothing more was issued, and what is in flight
-    // lands (a bounded wait again) before the CTA's shared memory goes away.
-    if (!ok) {
-        const uint64_t t0 = global_ns();
+    // What is in flight lands (which a wait that gave up did not see to) before the CTA's shared memory goes away.
+    const uint64_t t0 = global_ns();
 #pragma unroll 1
-        for (; done < issued; ++done)
-            while (!mbar_try_wait(landed + (done & 1), (uint32_t)(done >> 1 & 1)) && global_ns() - t0 < kWaitLimitNs) {
-            }
+    for (int z = max(t - 2, 0); z < t; ++z)
+        while (!mbar_try_wait(full + (z & 1), (uint32_t)(z >> 1 & 1)) && global_ns() - t0 < kWaitLimitNs) {
+        }
+}
+
+// Expansion warp x: its part of steps first, first + STRIDE .. of the CTA's `steps`. place(step): the tile to write, once it is
+// free; publish(step, h, bad): the tile is there.
+template <int D, bool INT8, bool BF16, bool IS_V, int STRIDE, class Place, class Publish>
+__device__ __forceinline__ void expand_steps(const Rings<D>& rings, int x, int first, int steps, int32_t* err, int lane, Place place,
+                                             Publish publish) {
+    const uint8_t* data = rings.data + x * 2 * kRingEntry<D>;
+    const volatile int32_t* what = rings.what + 2 * x;
+    int t = 0;
+#pragma unroll 1
+    for (int k = first; k < steps; k += STRIDE, ++t) {
+        const int y = t & 1;
+        uint8_t* dst = place(k);
+        bar_wait(rings.full + 2 * x + y, (uint32_t)(t >> 1 & 1), err);
+        const int is = __shfl_sync(0xffffffffu, what[y], 0);  // one answer for the warp, also after a wait that gave up
+        float2 h;
+        uint32_t bad = 0;
+        if (is < 0) {
+            const uint8_t* rec = data + y * kRingEntry<D>;
+            const float4 hd = *reinterpret_cast<const float4*>(rec);
+            h = IS_V ? make_float2(hd.z, hd.w) : make_float2(hd.x, 0.f);
+            expand_codes<D, INT8, IS_V>(rec, dst, x & 3, lane);
+        } else {
+            expand_rows<D, BF16, IS_V>(data, is, dst, x & 3, lane, h, bad);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(rings.empty + y);
+        fence_proxy_async_smem();
+        publish(k, h, bad);
     }
 }
 

@@ -20,21 +20,25 @@ namespace {
 // memory: no O is kept); two that load query rows, a tile ahead; three softmax warpgroups, every third step each, a thread a row. Every wait
 // is bounded and sets the error word when it gives up.
 constexpr int kWinThreads = 736, kWinStep = 128, kWinStages = 3, kWinRing = 8;
-constexpr int kWinSoftmax = 4 * kWindowParts, kWinExpand = 8;  // warps
+// warps; behind the softmax ones in turn of four the issuer and the two that load rows, and three expansion warps, so that the issuer's
+// scheduler has none of those
+constexpr int kWinSoftmax = 4 * kWindowParts, kWinExpand = 8, kWinIssuer = kWinSoftmax;
+static_assert(kWinThreads == 32 * (kWinSoftmax + kWinExpand + 3), "warps");
 // barriers
 constexpr int kKFull = 0, kKEmpty = kKFull + kWinRing, kSFull = kKEmpty + kWinStages, kSEmpty = kSFull + 4, kQFull = kSEmpty + 4,
-              kQEmpty = kQFull + kWinRing, kDrain = kQEmpty + 2, kRawFull = kDrain + 1, kWinBars = kRawFull + kWinExpand * 2;
+              kQEmpty = kQFull + kWinRing, kDrain = kQEmpty + 2, kRaw = kDrain + 1, kWinBars = kRaw + kWinExpand * 2 + 2;
 
 template <int D>
 struct WinShape {
     static constexpr int kTile = D / 64 * kAtom;
     static constexpr int kQ = 0;                                   // 2 tiles
     static constexpr int kK = 2 * kTile;                           // kWinStages tiles
-    static constexpr int kRaw = kK + kWinStages * kTile;           // two ring entries of an expansion warp
-    static constexpr int kScale = kRaw + kWinExpand * 2 * kRingEntry<D>;  // float[kWinRing][4]: K scale of a step's parts
+    static constexpr int kRings = kK + kWinStages * kTile;
+    static constexpr int kScale = kRings + Rings<D>::kBytes;       // float[kWinRing][4]: K scale of a step's parts
     static constexpr int kPower = kScale + kWinRing * 16;          // int8[kWinRing][128]: of a segment's rows
     static constexpr int kBars = kPower + kWinRing * 128;
-    static constexpr int kTmem = kBars + 8 * kWinBars;
+    static constexpr int kWhat = kBars + 8 * kWinBars;             // int[8][2]
+    static constexpr int kTmem = kWhat + 64;
     static constexpr int kSmem = kTmem + 16;
     static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
 };
@@ -52,18 +56,19 @@ __device__ __forceinline__ void win_issue(const BlockWindowParams& p, uint32_t s
     for (; w.next(); ++seg) {
         const int j1 = __shfl_sync(0xffffffffu, w.j1, 0), j0 = __shfl_sync(0xffffffffu, w.j0, 0);
         bar_wait(bars + kQFull + seg % kWinRing, (uint32_t)(seg / kWinRing & 1), err);
-        const uint32_t q = base + ((Sh::kQ + (seg & 1) * Sh::kTile) >> 4);
+        const uint32_t q = base + ((Sh::kQ + __shfl_sync(0xffffffffu, seg & 1, 0) * Sh::kTile) >> 4);
 #pragma unroll 1
         for (int j = j0; j < j1; ++j, ++k) {
             bar_wait(bars + kKFull + k % kWinRing, (uint32_t)(k / kWinRing & 1), err);
             if (k >= 4) bar_wait(bars + kSEmpty + (k & 3), (uint32_t)(((k >> 2) - 1) & 1), err);
             __syncwarp();
             tc_fence_after();
-            const uint32_t kt = base + ((Sh::kK + k % kWinStages * Sh::kTile) >> 4);
+            const int stage = __shfl_sync(0xffffffffu, k % kWinStages, 0), buf = __shfl_sync(0xffffffffu, k & 3, 0);  // seen to be uniform
+            const uint32_t kt = base + ((Sh::kK + stage * Sh::kTile) >> 4);
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks) {
                 const uint32_t off = ((ks >> 2) * kAtom + (ks & 3) * 32) >> 4;
-                if (leader) mma_ss(128 * (k & 3), desc128(q + off), desc128(kt + off), kIdesc<128>, ks > 0);
+                if (leader) mma_ss(128 * buf, desc128(q + off), desc128(kt + off), kIdesc<128>, ks > 0);
             }
             if (leader) mma_commit(bars + kSFull + (k & 3));
             if (leader) mma_commit(bars + kKEmpty + k % kWinStages);
@@ -162,7 +167,7 @@ __global__ void __launch_bounds__(kWinThreads, 1) window_kernel(const __grid_con
     if (t == 0) {
         for (int k = 0; k < kWinRing; ++k) {
             mbar_init(bars + kKFull + k, 128);
-            mbar_init(bars + kQFull + k, 64);
+            mbar_init(bars + kQFull + k, 32);
         }
         for (int k = 0; k < kWinStages; ++k) mbar_init(bars + kKEmpty + k, 1);
         for (int k = 0; k < 4; ++k) {
@@ -171,11 +176,11 @@ __global__ void __launch_bounds__(kWinThreads, 1) window_kernel(const __grid_con
         }
         for (int k = 0; k < 2; ++k) mbar_init(bars + kQEmpty + k, 1);
         mbar_init(bars + kDrain, 1);
-        for (int k = 0; k < kWinExpand * 2; ++k) mbar_init(bars + kRawFull + k, 1);
+        for (int k = 0; k < kWinExpand * 2; ++k) mbar_init(bars + kRaw + k, 1);
+        for (int k = 0; k < 2; ++k) mbar_init(bars + kRaw + 2 * kWinExpand + k, kWinExpand);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    constexpr int kIssuer = kWinSoftmax + kWinExpand;  // warp
-    if (w == kIssuer) {
+    if (w == kWinIssuer) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(smem + Sh::kTmem))
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -187,37 +192,42 @@ __global__ void __launch_bounds__(kWinThreads, 1) window_kernel(const __grid_con
     // Were it ever not so, the launch would do nothing but say so.
     const bool placed = *reinterpret_cast<volatile uint32_t*>(smem + Sh::kTmem) == 0 && (smem_addr(smem) & 1023) == 0;
     if (!placed && t == 0) atomicOr(err, kErrBadSlot);
+    const Rings<D> rings = {smem + Sh::kRings, bars + kRaw, bars + kRaw + 2 * kWinExpand, reinterpret_cast<int32_t*>(smem + Sh::kWhat)};
+    const int steps = (int)(p.units * (blockIdx.x + 1) / p.grid - p.units * blockIdx.x / p.grid);
     if (!placed) {
     } else if (w < kWinSoftmax) {
         win_softmax<D>(p, smem, bars, err, t & 127, w >> 2, (uint32_t)(32 * (w & 3)) << 16);
-    } else if (w < kIssuer) {
-        const int x = w - kWinSoftmax, odd = x >> 2, wp = x & 3;
-        expand_line<D, INT8, BF16, false, 2>(
-            p, smem + Sh::kRaw + x * 2 * kRingEntry<D>, bars + kRawFull + 2 * x, err, odd, wp, lane,
-            [&](int k) -> uint8_t* {
-                if (k >= kWinStages && !bar_wait(bars + kKEmpty + k % kWinStages, (uint32_t)((k / kWinStages - 1) & 1), err)) return nullptr;
+    } else if (w & 3) {
+        const int x = (w - kWinSoftmax) / 4 * 3 + (w & 3) - 1, odd = x >> 2, wp = x & 3;
+        expand_steps<D, INT8, BF16, false, 2>(
+            rings, x, odd, steps, err, lane,
+            [&](int k) {
+                if (k >= kWinStages) bar_wait(bars + kKEmpty + k % kWinStages, (uint32_t)((k / kWinStages - 1) & 1), err);
                 return smem + Sh::kK + k % kWinStages * Sh::kTile;
             },
             [&](int k, float2 h, uint32_t) {
                 if (lane == 0) reinterpret_cast<float*>(smem + Sh::kScale)[k % kWinRing * 4 + wp] = h.x;
                 mbar_arrive(bars + kKFull + k % kWinRing);
             });
-    } else if (w == kIssuer) {
+    } else if (w == kWinIssuer) {
         win_issue<D>(p, smem_addr(smem), bars, err);
-    } else {
+    } else if (w == kWinIssuer + 4) {
         int seg = 0;
         for (WinWalk x(p); x.next(); ++seg) {
             if (seg >= 2) bar_wait(bars + kQEmpty + (seg & 1), (uint32_t)(((seg >> 1) - 1) & 1), err);
             __syncwarp();
-            make_rows<D, BF16, 2>(p, x, smem + Sh::kQ + (seg & 1) * Sh::kTile,
-                                  reinterpret_cast<int8_t*>(smem + Sh::kPower) + seg % kWinRing * 128, w - kIssuer - 1, lane);
+            const Rows<D, 1> rows(smem + Sh::kQ + (seg & 1) * Sh::kTile, 0, lane);
+            rows.fetch(p, x);
+            rows.template finish<BF16>(p.scale_log2, reinterpret_cast<int8_t*>(smem + Sh::kPower) + seg % kWinRing * 128);
             mbar_arrive(bars + kQFull + seg % kWinRing);
         }
+    } else {
+        fill_rings<D, false>(p, rings, steps, err, lane);
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (w == kIssuer) {
+    if (w == kWinIssuer) {
         __syncwarp();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(*reinterpret_cast<volatile uint32_t*>(smem + Sh::kTmem))
                      : "memory");
