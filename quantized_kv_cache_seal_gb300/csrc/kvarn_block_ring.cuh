@@ -11,6 +11,10 @@ struct RowWalk {
     const P& p;
     int64_t u, u1;
     int i, h, tile, j0, j1, pair;
+    __device__ __forceinline__ RowWalk& operator=(const RowWalk& o) {  // (of the same p)
+        u = o.u, u1 = o.u1, i = o.i, h = o.h, tile = o.tile, j0 = o.j0, j1 = o.j1, pair = o.pair;
+        return *this;
+    }
     __device__ __forceinline__ explicit RowWalk(const P& p_)
         : p(p_), u(p_.units * blockIdx.x / p_.grid), u1(p_.units * (blockIdx.x + 1) / p_.grid), i(0), j0(0), j1(0) {}
     __device__ __forceinline__ bool next() {

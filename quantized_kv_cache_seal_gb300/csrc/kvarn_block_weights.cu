@@ -17,10 +17,10 @@ namespace {
 // unit of work is a step of 128 tokens for a tile of 128 rows of a (sequence, KV head), and the line of all units is cut evenly over
 // the CTAs, one a SM. Roles (736 threads): eight expansion warps that turn K codes into f16 tiles (a warp 32 tokens,
 // four warps every other step); one that issues the MMAs into four S buffers (all 512 columns of tensor
-// memory: no O is kept); two that load query rows, a tile ahead; three softmax warpgroups, every third step each, a thread a row. Every wait
+// memory: no O is kept); one that fills the code rings; three softmax warpgroups, every third step each, a thread a row. Every wait
 // is bounded and sets the error word when it gives up.
 constexpr int kWinThreads = 736, kWinStep = 128, kWinStages = 3, kWinRing = 8;
-// warps; behind the softmax ones in turn of four the issuer and the two that load rows, and three expansion warps, so that the issuer's
+// warps; behind the softmax ones in turn of four the issuer, the one that fills the rings and an idle one, and three expansion warps, so that the issuer's
 // scheduler has none of those
 constexpr int kWinSoftmax = 4 * kWindowParts, kWinExpand = 8, kWinIssuer = kWinSoftmax;
 static_assert(kWinThreads == 32 * (kWinSoftmax + kWinExpand + 3), "warps");
@@ -85,14 +85,39 @@ __device__ __forceinline__ void win_issue(const BlockWindowParams& p, uint32_t s
 
 // Warpgroup b takes every third step; thread et owns row et. (Two of them take 72 us where three take 60; four, with an S buffer
 // each that the next MMAs wait for, 79.)
-template <int D>
+template <int D, bool BF16>
 __device__ __forceinline__ void win_softmax(const BlockWindowParams& p, uint8_t* smem, uint64_t* bars, int32_t* err, int et, int b,
                                             uint32_t lane_off) {
     using Sh = WinShape<D>;
+    // The first two warpgroups also bring the next segment's rows, which are on their way during a step. (One warp of its own took
+    // 13 us to bring the first.)
     int k = 0, seg = 0;
-    WinWalk w(p);
+    WinWalk w(p), then(p);
+    bool more = then.next(), coming = false;
+    auto fetch = [&](int s) {
+        const Rows<D, 8> rows(smem + Sh::kQ + (s & 1) * Sh::kTile, 4 * b + (et >> 5), et & 31);
+        rows.fetch(p, then);
+        coming = true;
+    };
+    auto ready = [&](int s) {
+        const Rows<D, 8> rows(smem + Sh::kQ + (s & 1) * Sh::kTile, 4 * b + (et >> 5), et & 31);
+        rows.template finish<BF16>(p.scale_log2, reinterpret_cast<int8_t*>(smem + Sh::kPower) + s % kWinRing * 128);
+        mbar_arrive(bars + kQFull + s % kWinRing);
+        coming = false;
+    };
+    if (more && b < 2) {
+        fetch(0);
+        ready(0);
+    }
 #pragma unroll 1
-    for (; w.next(); ++seg) {
+    for (; more; ++seg) {
+        w = then;
+        more = then.next();
+        if (more && b < 2) {
+            if (seg > 0) bar_wait(bars + kQEmpty + ((seg - 1) & 1), (uint32_t)(((seg - 1) >> 1) & 1), err);
+            __syncwarp();
+            fetch(seg + 1);
+        }
         const BlockRowsSeq& e = p.seqs[w.i];
         const int row = w.tile * 128 + et, tiles = (e.n + kTileTokens - 1) / kTileTokens, pad = e.pad;
         const bool valid = row < e.rows;
@@ -151,7 +176,9 @@ __device__ __forceinline__ void win_softmax(const BlockWindowParams& p, uint8_t*
                 if (valid && 4 * j + ch < tiles) out[(int64_t)(4 * j + ch) * pad] = part;
                 total = joined(total, part);
             }
+            if (coming) ready(seg + 1);
         }
+        if (coming) ready(seg + 1);
         // of the pair's part in this CTA (a pair's first CTA is no sooner than the pair before's last)
         p.totals[((int64_t)(e.pair_begin + w.pair + blockIdx.x) * kWindowParts + b) * 128 + et] = total;
     }
@@ -167,7 +194,7 @@ __global__ void __launch_bounds__(kWinThreads, 1) window_kernel(const __grid_con
     if (t == 0) {
         for (int k = 0; k < kWinRing; ++k) {
             mbar_init(bars + kKFull + k, 128);
-            mbar_init(bars + kQFull + k, 32);
+            mbar_init(bars + kQFull + k, 256);
         }
         for (int k = 0; k < kWinStages; ++k) mbar_init(bars + kKEmpty + k, 1);
         for (int k = 0; k < 4; ++k) {
@@ -196,7 +223,7 @@ __global__ void __launch_bounds__(kWinThreads, 1) window_kernel(const __grid_con
     const int steps = (int)(p.units * (blockIdx.x + 1) / p.grid - p.units * blockIdx.x / p.grid);
     if (!placed) {
     } else if (w < kWinSoftmax) {
-        win_softmax<D>(p, smem, bars, err, t & 127, w >> 2, (uint32_t)(32 * (w & 3)) << 16);
+        win_softmax<D, BF16>(p, smem, bars, err, t & 127, w >> 2, (uint32_t)(32 * (w & 3)) << 16);
     } else if (w & 3) {
         const int x = (w - kWinSoftmax) / 4 * 3 + (w & 3) - 1, odd = x >> 2, wp = x & 3;
         expand_steps<D, INT8, BF16, false, 2>(
@@ -212,16 +239,6 @@ __global__ void __launch_bounds__(kWinThreads, 1) window_kernel(const __grid_con
     } else if (w == kWinIssuer) {
         win_issue<D>(p, smem_addr(smem), bars, err);
     } else if (w == kWinIssuer + 4) {
-        int seg = 0;
-        for (WinWalk x(p); x.next(); ++seg) {
-            if (seg >= 2) bar_wait(bars + kQEmpty + (seg & 1), (uint32_t)(((seg >> 1) - 1) & 1), err);
-            __syncwarp();
-            const Rows<D, 1> rows(smem + Sh::kQ + (seg & 1) * Sh::kTile, 0, lane);
-            rows.fetch(p, x);
-            rows.template finish<BF16>(p.scale_log2, reinterpret_cast<int8_t*>(smem + Sh::kPower) + seg % kWinRing * 128);
-            mbar_arrive(bars + kQFull + seg % kWinRing);
-        }
-    } else {
         fill_rings<D, false>(p, rings, steps, err, lane);
     }
     tc_fence_before();
