@@ -259,10 +259,20 @@ constexpr int kWeighRows = 128 * kBlockMaxRatio;  // rows of a KV head
 __global__ void __launch_bounds__(kWeighThreads) weigh_kernel(const __grid_constant__ BlockWeighParams p) {
     __shared__ float2 of[kWeighRows];  // of a row: its maximum, 1 / denominator (0: adds nothing)
     __shared__ float2 some[kWeighThreads];
+    __shared__ int2 ctas[kWeighRows / 128];
     const BlockWeighSeq& e = p.seqs[blockIdx.z];
     const int h = blockIdx.y, t = threadIdx.x, blocks = (e.tiles + (1 << p.log2_tiles) - 1) >> p.log2_tiles;
     const int first = blockIdx.x * p.blocks;
     if (first >= blocks) return;
+    if (p.grid > 0) {  // the CTAs that share each row tile's pair
+        const int steps = (e.tiles + 3) / 4;
+        if (t < (e.rows + 127) / 128) {
+            const int64_t u = e.unit_begin + (int64_t)(h * ((e.rows + 127) / 128) + t) * steps;
+            ctas[t] = make_int2((int)(((u + 1) * p.grid - 1) / p.units), (int)(((u + steps) * p.grid - 1) / p.units));
+        }
+        __syncthreads();
+    }
+    for (int row = e.rows + t; row < e.pad; row += kWeighThreads) of[row] = make_float2(0.f, 0.f);
     int span = 32;  // rows at a time; as many threads as there are to a row, each some of its parts
     while (span < kWeighThreads && span < e.rows) span *= 2;
     for (int row0 = 0; row0 < e.rows; row0 += span) {
@@ -272,9 +282,7 @@ __global__ void __launch_bounds__(kWeighThreads) weigh_kernel(const __grid_const
         } else if (p.grid == 0) {
             if (turn == 0) s = p.totals[(int64_t)e.row * p.hq + h * e.rows + row];
         } else {  // the parts of the row's pair, of the CTAs that share it
-            const int steps = (e.tiles + 3) / 4, pair = h * ((e.rows + 127) / 128) + row / 128;
-            const int64_t u = e.unit_begin + (int64_t)pair * steps;
-            const int b0 = (int)(((u + 1) * p.grid - 1) / p.units), b1 = (int)(((u + steps) * p.grid - 1) / p.units);
+            const int pair = h * ((e.rows + 127) / 128) + row / 128, b0 = ctas[row / 128].x, b1 = ctas[row / 128].y;
             const float2* at = p.totals + (int64_t)(e.pair_begin + pair) * kWindowParts * 128 + row % 128;
 #pragma unroll 4
             for (int b = kWindowParts * b0 + turn; b < kWindowParts * (b1 + 1); b += turns) s = joined(s, at[(int64_t)b * 128]);
@@ -290,18 +298,18 @@ __global__ void __launch_bounds__(kWeighThreads) weigh_kernel(const __grid_const
     __syncthreads();
     const float2* sums = p.sums + e.sum_begin + ((int64_t)h * e.stride + e.before) * e.pad;
     float* to = p.weights + ((int64_t)e.seq * p.hkv + h) * p.cols;
-    const int lane = t % p.lanes;
+    const int lane = t % p.lanes, lane0 = lane % e.pad, step = p.lanes % e.pad;
     for (int b = first + t / p.lanes; b < first + p.blocks; b += kWeighThreads / p.lanes) {  // whole warps
         const int t0 = b << p.log2_tiles, count = (min(t0 + (1 << p.log2_tiles), e.tiles) - t0) * e.pad;  // negative: none
         const float2* at = sums + (int64_t)t0 * e.pad;
         float sum = 0.f;
-        int row = lane % e.pad;
+        int row = lane0;
 #pragma unroll 4
         for (int k = lane; k < count; k += p.lanes) {
-            const float2 x = at[k], f = row < e.rows ? of[row] : make_float2(0.f, 0.f);
-            if (f.y != 0.f && x.x != kNegInf) sum += x.y * ex2f(x.x - f.x) * f.y;
-            row += p.lanes;
-            if (row >= e.pad) row %= e.pad;
+            const float2 x = at[k], f = of[row];
+            if (f.y != 0.f) sum = fmaf(x.y * ex2f(x.x - f.x), f.y, sum);  // (a tile out of sight: -inf, 0)
+            row += step;
+            if (row >= e.pad) row -= e.pad;
         }
         for (int d = p.lanes / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
         if (lane == 0 && b < blocks) to[b] += sum;
