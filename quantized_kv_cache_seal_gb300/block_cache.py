@@ -40,13 +40,13 @@ class BlockCache:
         self.dtype = dtype
         self.heads, self.kv_heads, self.dim = num_q_heads, num_kv_heads, head_dim
         self.scale = 1.0 / math.sqrt(head_dim)
-        self._tiles = (max_seq_len + 31) // 32
         # places of the blocks' weights in a layer
         self.weights_shape = (max_seqs, num_kv_heads, max_seq_len // max(1, block_tokens) + 1)
         self.nbytes = K.kvarn_block_required_bytes(self.cfg)
         self.mem = torch.empty(self.nbytes + 256, dtype=torch.uint8, device=device)
         self.device = self.mem.device
         self.index = self.mem.get_device()  # -1: the CPU
+        self._spaces = [torch.empty(1 << 20, dtype=torch.uint8, device=device)]  # workspaces of calls that want one, the last in use
         # streams that hold the cache's memory: the one that it was allocated on, then others as they come
         self._holders = {None if self.index < 0 else K.current_stream(self.device)}
         base = (self.mem.data_ptr() + 255) // 256 * 256
@@ -90,7 +90,7 @@ class BlockCache:
         if given is not None:
             K.hold(given, *tensors)
         if stream not in self._holders and not isinstance(given, int):
-            K.hold(given or torch.cuda.current_stream(self.device), self.mem)
+            K.hold(given or torch.cuda.current_stream(self.device), self.mem, *self._spaces)
             self._holders.add(stream)
 
     # -- calls -----------------------------------------------------------------------------------------------
@@ -145,26 +145,48 @@ class BlockCache:
             prefix_ids = [-1 if x is None else x for x in prefix_ids]
         if weights is not None:
             self._weights(weights)
-        # what the workspace takes at most; where that is much, what it takes
-        n = 0 if prefix_ids is None else 4 * q.numel() + 4 * self.heads * q.shape[0] + 512
-        if weights is not None:
-            n += 8 * self.heads * len(seq_ids) * (5 + self._tiles * (1 if prefix_ids is None else 2)) + 512
         with K.on_device(self.device, stream) as s:
             if out is None:
                 out = torch.empty_like(q)
-            if n > 1 << 25:
-                n = K.kvarn_block_attend_workspace(self.handle, layer, seq_ids, prefix_ids, counts, k is not None,
-                                                   weights is not None)
-            # of this stream's memory: free for the stream's later work once the call is enqueued
-            space = torch.empty(n, dtype=torch.uint8, device=self.device) if n else None
             scale = self.scale if scale is None else scale
-            if k is None:
-                K.kvarn_block_attend(self.handle, layer, seq_ids, prefix_ids, counts, q, out, scale, weights, space, n, s)
-            else:
-                K.kvarn_block_append_attend(self.handle, layer, seq_ids, prefix_ids, counts, k, ks, v, vs, q, out, scale,
-                                            weights, space, n, s)
+
+            def call(space, n):
+                if k is None:
+                    K.kvarn_block_attend(self.handle, layer, seq_ids, prefix_ids, counts, q, out, scale, weights, space, n, s)
+                else:
+                    K.kvarn_block_append_attend(self.handle, layer, seq_ids, prefix_ids, counts, k, ks, v, vs, q, out, scale,
+                                                weights, space, n, s)
+
+            self._in_space(call, lambda: K.kvarn_block_attend_workspace(self.handle, layer, seq_ids, prefix_ids, counts,
+                                                                        k is not None, weights is not None))
             self._used(stream, s, k, v, q, out, weights)
         return out
+
+    def _in_space(self, call, need):
+        """call(workspace, bytes) with the cache's own, which grows where need() says that it is too small. Calls of one
+        cache are ordered on the GPU, so that they can share it. Spaces that were outgrown stay: captured graphs use them."""
+        space = self._spaces[-1]
+        try:
+            return call(space, space.numel())
+        except K.KVarNError as e:
+            if e.status != 1:
+                raise
+            try:
+                n = need()
+            except K.KVarNError:
+                raise e from None
+            if n <= space.numel():
+                raise
+        # while a stream captures, memory belongs to its graph: for this call alone
+        capturing = self.index >= 0 and torch.cuda.is_current_stream_capturing()
+        space = torch.empty(n if capturing else max(n, 2 * space.numel()), dtype=torch.uint8, device=self.device)
+        if not capturing:
+            self._spaces.append(space)
+            # held anew by the streams that calls go to, but for the one that it was allocated on
+            self._holders = {None if self.index < 0 else K.current_stream(self.device)}
+            if self.index >= 0:
+                self.mem.record_stream(torch.cuda.current_stream(self.device))
+        return call(space, space.numel())
 
     def decode_attention(self, layer: int, seq_ids: Sequence[int], q: torch.Tensor, out: Optional[torch.Tensor] = None,
                          scale: Optional[float] = None, stream=None, prefix_ids: Optional[Sequence[Optional[int]]] = None,
@@ -240,10 +262,10 @@ class BlockCache:
         self._dense(q, sum(q_lens), "q")
         self._weights(weights)
         with K.on_device(self.device, stream) as s:
-            n = K.kvarn_block_window_workspace(self.handle, layer, seq_ids, q_lens)
-            space = torch.empty(n, dtype=torch.uint8, device=self.device) if n else None
-            K.kvarn_block_window_weights(self.handle, layer, seq_ids, q_lens, q, self.scale if scale is None else scale,
-                                         weights, space, n, s)
+            scale = self.scale if scale is None else scale
+            self._in_space(lambda space, n: K.kvarn_block_window_weights(self.handle, layer, seq_ids, q_lens, q, scale, weights,
+                                                                         space, n, s),
+                           lambda: K.kvarn_block_window_workspace(self.handle, layer, seq_ids, q_lens))
             self._used(stream, s, q, weights)
 
     def evict(self, layer: int, seq_ids: Sequence[int], weights: torch.Tensor, keep: int, first: int = 1, last: int = 1,

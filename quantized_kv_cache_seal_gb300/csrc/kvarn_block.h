@@ -195,7 +195,7 @@ struct BlockWeighSeq {
     int32_t unit_begin, pair_begin;  // window: as there
     int64_t sum_begin;
 };
-struct BlockWeighParams {
+struct BlockWeighHead {
     const float2* sums;
     const float2* totals;     // decode (grid 0): [rows][Hq]; window: as there
     float* weights;           // [max_seqs][Hkv][cols]
@@ -204,8 +204,13 @@ struct BlockWeighParams {
     int32_t n_seqs, hq, hkv, log2_tiles, cols;  // tiles of a block; places of a (sequence, KV head)
     int32_t lanes, blocks;    // lanes that add up a block, blocks of a CTA
     int32_t most;             // CTAs of a (sequence, KV head)
-    BlockWeighSeq seqs[kBlockMaxSeqs];
 };
+template <int SEQS>
+struct BlockWeighArgs : BlockWeighHead {
+    BlockWeighSeq seqs[SEQS];
+};
+// (parameters are copied at every launch: few sequences pass a small form)
+using BlockWeighParams = BlockWeighArgs<kBlockMaxSeqs>;
 
 struct BlockEvictSeq {
     int32_t seq, full;        // full blocks, more than keep

@@ -256,7 +256,8 @@ constexpr int kWeighThreads = 256;
 constexpr int kWeighRows = 128 * kBlockMaxRatio;  // rows of a KV head
 
 // A CTA some blocks of a (KV head, sequence): its rows' totals first, then p.lanes lanes a block.
-__global__ void __launch_bounds__(kWeighThreads) weigh_kernel(const __grid_constant__ BlockWeighParams p) {
+template <int SEQS>
+__global__ void __launch_bounds__(kWeighThreads) weigh_kernel(const __grid_constant__ BlockWeighArgs<SEQS> p) {
     __shared__ float2 of[kWeighRows];  // of a row: its maximum, 1 / denominator (0: adds nothing)
     __shared__ float2 some[kWeighThreads];
     __shared__ int2 ctas[kWeighRows / 128];
@@ -342,7 +343,15 @@ int launch_block_window(const BlockWindowParams& p, void* stream) {
 }
 
 int launch_block_weigh(const BlockWeighParams& p, void* stream) {
-    weigh_kernel<<<dim3(p.most, p.hkv, p.n_seqs), kWeighThreads, 0, (cudaStream_t)stream>>>(p);
+    const dim3 grid(p.most, p.hkv, p.n_seqs);
+    if (p.n_seqs <= 16) {
+        BlockWeighArgs<16> few;
+        static_cast<BlockWeighHead&>(few) = p;
+        for (int i = 0; i < p.n_seqs; ++i) few.seqs[i] = p.seqs[i];
+        weigh_kernel<16><<<grid, kWeighThreads, 0, (cudaStream_t)stream>>>(few);
+    } else {
+        weigh_kernel<kBlockMaxSeqs><<<grid, kWeighThreads, 0, (cudaStream_t)stream>>>(p);
+    }
     return (int)cudaGetLastError();
 }
 
