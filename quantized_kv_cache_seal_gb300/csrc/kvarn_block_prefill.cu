@@ -767,10 +767,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 // sums 32 at a time, a lane each, then their rows eight at a time. blockIdx.y: kCombineRows rows.
 constexpr int kCombineThreads = 256;
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_constant__ BlockPrefillParams p KVARN_MORE_PARAM) {
-#ifndef KVARN_BLOCK_MORE
+__global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_constant__ BlockPrefillParams p) {
     const More x = {};
-#endif
     constexpr int kCombineRows = kCombineThreads / 32;
     const int b = blockIdx.x, lane = threadIdx.x & 31;
     const int u0 = (int)((int64_t)p.steps * b / p.grid), u1 = (int)((int64_t)p.steps * (b + 1) / p.grid);
@@ -823,29 +821,107 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_c
     }
     const float inv = l == 0.f ? 0.f : 1.f / l, y = kDenomUnit;
     const size_t row = ((size_t)(e.q_row + tok) * p.hq + w.s.kvh * p.r + et % p.r) * D;
-    if (kMore) {
-        const size_t at = row / D;
-        o = make_float4(o.x * y * inv, o.y * y * inv, o.z * y * inv, o.w * y * inv);
-        if (x.flat) {
-            if (live) *reinterpret_cast<float4*>(x.pre_o + row + 4 * lane) = o;
-            if (lane == 0) x.pre_lse[at] = lse_of(big, l, kShift);
-            return;
-        }
-        if (x.pre_lse && (x.merged[w.s.i >> 5] >> (w.s.i & 31) & 1)) {
-            const float2 f = merge_factors(lse_of(big, l, kShift), x.pre_lse[at]);
-            float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (live) z = *reinterpret_cast<const float4*>(x.pre_o + row + 4 * lane);
-            o = make_float4(merge(o.x, z.x, f), merge(o.y, z.y, f), merge(o.z, z.z, f), merge(o.w, z.w, f));
-        }
-        if (live) *reinterpret_cast<uint2*>(p.out + row + 4 * lane) = make_uint2(pack2<BF16>(o.x, o.y), pack2<BF16>(o.z, o.w));
-        return;
-    }
     if (live)
         *reinterpret_cast<uint2*>(p.out + row + 4 * lane) =
             make_uint2(pack2<BF16>(o.x * y * inv, o.y * y * inv), pack2<BF16>(o.z * y * inv, o.w * y * inv));
 }
 
 #ifdef KVARN_BLOCK_MORE
+// combine_kernel for both uses of prefixes; a warp four rows at a time, whose loads are on their way together (one row a warp
+// takes four rounds of thread blocks: 20 us for 3,500 query rows of 2,048 tokens, where this takes 00).
+constexpr int kMoreRows = 4;
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kCombineThreads) combine_more_kernel(const __grid_constant__ BlockPrefillParams p KVARN_MORE_PARAM) {
+    constexpr int R = kMoreRows;
+    const int b = blockIdx.x, lane = threadIdx.x & 31;
+    const int u0 = (int)((int64_t)p.steps * b / p.grid), u1 = (int)((int64_t)p.steps * (b + 1) / p.grid);
+    LineWalk w(p, x, b);
+    int u = u0;
+#pragma unroll 1
+    while (u + (w.s.j1 - w.s.j0) < u1) u += w.s.j1 - w.s.j0, w.next();
+    if (w.s.j0 > 0 || w.s.j1 == w.s.steps) return;  // no segment both begins here and goes on
+    const BlockPrefillSeq& e = p.seqs[w.s.i];
+    const int tpt = 128 / p.r, rr = (blockIdx.y * (kCombineThreads / 32) + threadIdx.x / 32) * R;
+    int64_t row[R];  // of q, -1 for none
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int et = rr + i & 127, tok = (2 * w.s.pair + (rr >> 7)) * tpt + et / p.r;
+        const bool valid = et / p.r < tpt && tok < e.q_len;
+        row[i] = valid ? (int64_t)(e.q_row + tok) * p.hq + w.s.kvh * p.r + et % p.r : -1;
+        any = any || valid;
+    }
+    if (!any) return;
+    const int parts = (int)(((int64_t)(u + w.s.steps) * p.grid - 1) / p.steps) - b + 1;
+    const bool live = 4 * lane < D;
+    constexpr size_t kPart = 256 * (D + 2);
+    const float* base = reinterpret_cast<const float*>(p.c.base + p.c.lay.partials);
+    // part z: slot 1 of the CTA where the segment begins, slot 0 of the others
+    auto part = [&](int z) { return base + (size_t)(2 * (b + z) + (z == 0 ? 1 : 0)) * kPart; };
+    float big[R], l[R];
+    float4 o[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) big[i] = kNegInf, l[i] = 0.f, o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int z0 = 0; z0 < parts; z0 += 32) {
+        const int n = min(32, parts - z0);
+        float f[R], s[R];
+        // (rows without a query are not written: what is read there goes nowhere)
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            f[i] = kNegInf;
+            s[i] = 0.f;
+            if (lane < n && row[i] >= 0) {
+                f[i] = part(z0 + lane)[256 * D + rr + i];
+                s[i] = part(z0 + lane)[256 * D + 256 + rr + i];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            float top = f[i];
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            top = fmaxf(top, big[i]);
+            f[i] = f[i] == kNegInf ? 1.f : ex2f(f[i] - top);  // -inf: zeros or NaN
+            const float g = big[i] == kNegInf ? 1.f : ex2f(big[i] - top);
+            s[i] *= f[i];
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) s[i] += __shfl_xor_sync(0xffffffffu, s[i], d);
+            l[i] = fmaf(l[i], g, s[i]);
+            o[i] = make_float4(o[i].x * g, o[i].y * g, o[i].z * g, o[i].w * g);
+            big[i] = top;
+        }
+#pragma unroll 2
+        for (int z = 0; z < n; ++z)
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (live && row[i] >= 0) v = *reinterpret_cast<const float4*>(part(z0 + z) + (size_t)(rr + i) * D + 4 * lane);
+                const float y = __shfl_sync(0xffffffffu, f[i], z);
+                o[i] = make_float4(fmaf(v.x, y, o[i].x), fmaf(v.y, y, o[i].y), fmaf(v.z, y, o[i].z), fmaf(v.w, y, o[i].w));
+            }
+    }
+    const bool merged = !x.flat && x.pre_lse && (x.merged[w.s.i >> 5] >> (w.s.i & 31) & 1);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        if (row[i] < 0) continue;
+        const float inv = kDenomUnit * (l[i] == 0.f ? 0.f : 1.f / l[i]), lse = lse_of(big[i], l[i], kShift);
+        float4 v = make_float4(o[i].x * inv, o[i].y * inv, o[i].z * inv, o[i].w * inv);
+        if (x.flat) {
+            if (live) *reinterpret_cast<float4*>(x.pre_o + row[i] * D + 4 * lane) = v;
+            if (lane == 0) x.pre_lse[row[i]] = lse;
+            continue;
+        }
+        if (merged) {
+            const float2 f = merge_factors(lse, x.pre_lse[row[i]]);
+            float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (live) z = *reinterpret_cast<const float4*>(x.pre_o + row[i] * D + 4 * lane);
+            v = make_float4(merge(v.x, z.x, f), merge(v.y, z.y, f), merge(v.z, z.z, f), merge(v.w, z.w, f));
+        }
+        if (live) *reinterpret_cast<uint2*>(p.out + row[i] * D + 4 * lane) = make_uint2(pack2<BF16>(v.x, v.y), pack2<BF16>(v.z, v.w));
+    }
+}
+
 #define KVARN_ARGS p, x
 #define KVARN_PARAMS const BlockPrefillParams &p, const BlockPrefillMore &x
 #else
@@ -859,7 +935,11 @@ int launch(KVARN_PARAMS, cudaStream_t s) {
     const int e = once.allow(reinterpret_cast<const void*>(prefill_kernel<D, INT8, BF16>), Shape<D>::kSmem);
     if (e) return e;
     prefill_kernel<D, INT8, BF16><<<p.grid, kThreads, Shape<D>::kSmem, s>>>(KVARN_ARGS);
-    if (p.line) combine_kernel<D, BF16><<<dim3(p.grid, 256 / (kCombineThreads / 32)), kCombineThreads, 0, s>>>(KVARN_ARGS);
+#ifdef KVARN_BLOCK_MORE
+    if (p.line) combine_more_kernel<D, BF16><<<dim3(p.grid, 256 / (kCombineThreads / 32 * kMoreRows)), kCombineThreads, 0, s>>>(p, x);
+#else
+    if (p.line) combine_kernel<D, BF16><<<dim3(p.grid, 256 / (kCombineThreads / 32)), kCombineThreads, 0, s>>>(p);
+#endif
     return (int)cudaGetLastError();
 }
 
