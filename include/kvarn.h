@@ -326,7 +326,7 @@ kvarn_status kvarn_device_accessible(const void* ptr, int32_t* accessible);
  *   - Calls that change a cache, and the first call on one, cannot be captured into a graph
  *     (KVARN_ESTATE): the host's lengths would not follow a replay. decode_attention,
  *     prefill_attention and read can; a replay sees the lengths of the capture, so the
- *     sequences must not have been released since, nor the block that was partial then have
+ *     sequences must not have been released or cut since, nor the block that was partial then have
  *     filled (its exact tokens make room for the next block's). A replay is a call: those of
  *     one cache stay ordered on the GPU, since they share its workspace.
  *   - Infinities and NaN: a query sees those of the tokens at positions up to its own. In V of an

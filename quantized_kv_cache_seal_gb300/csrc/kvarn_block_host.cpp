@@ -363,8 +363,10 @@ kvarn_status run_decode(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, con
     const int64_t pairs = (int64_t)n_seqs * c->cfg.num_kv_heads, most = std::min(c->sms, kBlockMaxGrid);
     const bool equal = std::all_of(p.seqs, p.seqs + n_seqs, [](const BlockDecodeSeq& e) { return e.units == p.seqs[0].units; });
     p.grid = (int32_t)(equal && p.seqs[0].units <= 32 && pairs <= most ? pairs : std::min((units + 7) / 8, most));
-    // Short pairs, four tiles a warp at least: the line is cut over the warps.
-    x.alone = more && units >= 4 * 8 * most && units < 64 * pairs;
+    // Short pairs, four tiles a warp at least: the line is cut over the warps. (Measured with weights, 32 / 8 heads of 128, us
+    // over warps and over CTAs: 64 ragged sequences of up to 1,024 tokens 28 and 87, of up to 256 20 and 44; 64 of 2,048 59 and 59; 8 of
+    // 4,096 22 and 23; 16 of 8,192 59 and 58, of 32,768 195 and 182.)
+    x.alone = more && units >= 4 * 8 * most && units < 128 * pairs;
     if (x.alone) {
         units = 0;
         for (int i = 0; i < n_seqs; ++i) {
@@ -661,10 +663,13 @@ kvarn_status plan_window(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, co
     return KVARN_OK;
 }
 
-// Is a prefix of a group of single queries better walked once, as tiles of 128 rows, than by each sequence?
+// Is a prefix of a group of single queries better walked once, as tiles of 128 rows (two more launches), than by each
+// sequence? (Measured, 32 / 8 heads of 128, us once and each: 4 sequences behind 32k 42 and 45; 8 behind 8k 30 and 28, behind
+// 32k 42 and 79; 16 behind 2k 24 and 20, behind 8k 31 and 45; 64 behind 512 41 and 28, behind 2k 47 and 52, behind 32k 83 and 543. With
+// 16 / 2 heads: 32 behind 8k 35 and 32, 64 behind 8k 34 and 49.)
 bool walked_once(const kvarn_block_cache* c, const Entry& g) {
     const int64_t each = (int64_t)g.q_len * g.n, once = head_pairs(c, g.q_len) * (int64_t)g.n;
-    return each > 4 * once && each * c->cfg.num_kv_heads > 1 << 17;
+    return each >= 4 * once && each * c->cfg.num_kv_heads > 600000;
 }
 
 kvarn_status run_attend(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* ids, const int32_t* prefix_ids,

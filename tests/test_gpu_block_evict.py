@@ -430,3 +430,60 @@ def test_sequences_shorter_than_a_block():
     before = w.clone()
     assert not c.evict(0, [0, 1], w, 0, 0, 0).numel() and bool((c.evict(0, [0, 1], w, 2) == -1).all())
     assert torch.equal(w, before) and c.length(0, 0) == 100
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_after_a_wait_has_given_up(dim):
+    """With the timeout bit set, as by a wait of a launch before, calls end at once and say so; then all is right again."""
+    from tests.test_gpu_block_edges import _words
+    c = make(max_seqs=60, num_q_heads=16, head_dim=dim, block_tokens=32, dtype=torch.bfloat16, code="int8")
+    fill(c, [33 + 9 * i for i in range(58)] + [4000, 700], torch.bfloat16, 710)
+    ids = list(range(60))
+    q = tokens(20 * 60, 16, dim, torch.bfloat16, 712, 0.3)
+
+    def both():
+        w = torch.zeros(c.weights_shape, device="cuda")
+        out = c.decode_attention(0, ids, q[:60], weights=w)
+        c.window_weights(0, ids, [20] * 60, q, w)
+        return out, w
+
+    want = both()
+    for _ in range(5):
+        _words(c, 0, 1).fill_(1)
+        both()
+        assert c.check_device_error() == 6
+        got = both()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        assert c.check_device_error() == 0
+
+
+def test_a_pool_of_more_than_4_gb():
+    """Slots whose bytes 32 bits cannot count: eviction, prefixes and weights of what lies there."""
+    c = make(max_seqs=4, num_q_heads=64, num_kv_heads=64, block_tokens=128, max_seq_len=1 << 20, pool_blocks=2400)
+    filler = torch.zeros(1 << 16, 64, 128, dtype=torch.float16, device="cuda")
+    for _ in range(4):
+        c.append(0, [0], [1 << 16], filler, filler)
+    del filler
+    lens = [1500, 300]
+    k, v = (tokens(sum(lens), 64, 128, torch.float16, s, 0.3) for s in (720, 721))
+    c.append(0, [1, 2], lens, k, v)
+    k, v = ([None] + list(torch.split(x, lens)) for x in (k, v))
+    w = some_weights(c, 722)
+    kept = c.evict(0, [1], w, 5)
+    assert c.length(0, 1) == 5 * 128 + 1500 % 128
+    got = c.read(0, [1], None, [c.length(0, 1)], dtype=torch.float32)
+    sides = []
+    for x, g in zip((k, v), got):
+        held = block_ref.hold(x[1][:, :2], 128, "e4m3")
+        pick = [[b * 128 + t for b in kept[0, h].tolist() for t in range(128)] + list(range(1500 // 128 * 128, 1500)) for h in (0, 1)]
+        sides.append(torch.stack([held[pick[h], h] for h in (0, 1)], 1))
+        assert same(g[:, :2], sides[-1].float())
+    q = tokens(1, 64, 128, torch.float16, 723, 0.3)
+    before = w.clone()
+    out = c.decode_attention(0, [2], q, prefix_ids=[1], weights=w)
+    parts = [torch.cat([a, block_ref.hold(x[2][:, :2], 128, "e4m3")]) for a, x in zip(sides, (k, v))]
+    n = parts[0].shape[0]
+    want, tol = block_ref.attend(q[:, :2].cpu(), *parts, 128 ** -0.5, [n - 1])
+    check(out[:, :2], want, tol, "prefix")
+    share, off = received(q[:, :2], parts[0], 128 ** -0.5, [n - 1], 128, n - 300)
+    near(w[2, :2], before[2, :2], share, off, "weights")

@@ -53,8 +53,8 @@ def test_decode(dtype, code, block, dim, hkv, r):
 
 
 @pytest.mark.parametrize("dtype,code", [("fp16", "e4m3"), ("bf16", "int8"), ("fp16", "int8"), ("bf16", "e4m3")])
-@pytest.mark.parametrize("block,dim,hkv,r,seqs,n", [(32, 64, 2, 1, 40, 3001), (64, 128, 2, 4, 20, 4000), (128, 128, 1, 8, 40, 4096),
-                                                    (64, 64, 1, 7, 70, 2500), (64, 128, 8, 4, 9, 2049), (32, 128, 3, 5, 150, 1025)])
+@pytest.mark.parametrize("block,dim,hkv,r,seqs,n", [(32, 64, 2, 1, 120, 3001), (64, 128, 2, 4, 80, 4000), (128, 128, 1, 8, 160, 4096),
+                                                    (64, 64, 1, 7, 250, 2500), (64, 128, 8, 4, 39, 2049), (32, 128, 3, 5, 200, 1025)])
 def test_decode_walked_once(dtype, code, block, dim, hkv, r, seqs, n):
     """A long prefix of many sequences, walked once as tiles of rows, one walked by its only sequence, and none."""
     dt = TYPES[dtype]
@@ -210,9 +210,9 @@ def test_output_over_the_queries_and_layers():
     c = make(max_seqs=41, num_layers=2, num_q_heads=32, num_kv_heads=8, block_tokens=64, max_seq_len=2048)
     sides = []
     for layer in (0, 1):
-        k, v = (tokens(40 * 30 + 1500, 8, 128, torch.float16, 440 + 2 * layer + s) for s in (0, 1))
-        c.append(layer, list(range(41)), [30] * 40 + [1500 - layer], k[:2700 - layer], v[:2700 - layer])
-        sides.append([[x[30 * i:30 * i + 30] for i in range(40)] + [x[1200:2700 - layer]] for x in (k, v)])
+        k, v = (tokens(40 * 30 + 2000, 8, 128, torch.float16, 440 + 2 * layer + s) for s in (0, 1))
+        c.append(layer, list(range(41)), [30] * 40 + [2000 - layer], k[:3200 - layer], v[:3200 - layer])
+        sides.append([[x[30 * i:30 * i + 30] for i in range(40)] + [x[1200:3200 - layer]] for x in (k, v)])
     for layer in (0, 1):
         q = tokens(80, 32, 128, torch.float16, 446 + layer, 0.3)
         for qlens in (None, [2] * 40):
