@@ -13,7 +13,7 @@
 namespace kvarn {
 namespace {
 
-// Warps: two softmax warpgroups, then the first of each four the issuer, the one that fills the rings and an idle one, the others
+// Warps: two softmax warpgroups, then the first of each four the issuer and the two that fill the rings, the others
 // expansion warps.
 // The issuer's scheduler has no expansion warp: an MMA takes its warp about 30 turns there (140 clocks an MMA with two, 00 without).
 constexpr int kSoftWarps = 8, kExpWarps = 8, kIssuer = kSoftWarps, kThreads = 32 * (kSoftWarps + kExpWarps + 3);
@@ -23,9 +23,9 @@ constexpr int kStep = 128, kRing = 8;
 constexpr float kRaise = 8.f, kShift = 7.f;  // m is raised when it would grow by more; weights are at most 2^(both)
 constexpr uint32_t kColS = 0, kColO = 256;
 // barriers
-constexpr int kKFull = 0, kVFull = kKFull + kRing, kQFull = kVFull + kRing, kKEmpty = kQFull + kRing, kVEmpty = kKEmpty + 2,
+constexpr int kKFull = 0, kVFull = kKFull + kRing, kVHead = kVFull + kRing, kQFull = kVHead + kRing, kKEmpty = kQFull + kRing, kVEmpty = kKEmpty + 2,
               kSFull = kVEmpty + 2, kPFull = kSFull + 2, kOFull = kPFull + 2, kOEmpty = kOFull + 2, kQEmpty = kOEmpty + 2,
-              kDrain = kQEmpty + 1, kRaw = kDrain + 1, kNumBars = kRaw + 2 * kExpWarps + 2;
+              kDrain = kQEmpty + 1, kRaw = kDrain + 1, kNumBars = kRaw + 2 * kExpWarps + 4;
 
 template <int D>
 struct Shape {
@@ -158,7 +158,7 @@ __device__ __forceinline__ void softmax_role(const BlockFlatParams& p, uint8_t* 
                 qs = row_factor(p.scale_log2, reinterpret_cast<const int8_t*>(smem + Sh::kPower)[seg % kRing * 128 + et]);
             }
             bar_wait(bars + kKFull + kk % kRing, (uint32_t)(kk / kRing & 1), err);
-            bar_wait(bars + kVFull + kk % kRing, (uint32_t)(kk / kRing & 1), err);
+            bar_wait(bars + kVHead + kk % kRing, (uint32_t)(kk / kRing & 1), err);
             const float* hk = reinterpret_cast<const float*>(smem + Sh::kHeadK) + kk % kRing * 4;
             const float4* hv = reinterpret_cast<const float4*>(smem + Sh::kHeadV) + kk % kRing * 4;
             bar_wait(bars + kSFull + b, (uint32_t)(kk >> 1 & 1), err);
@@ -277,6 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1) flat_kernel(const __grid_constant
         for (int k = 0; k < kRing; ++k) {
             mbar_init(bars + kKFull + k, 128);
             mbar_init(bars + kVFull + k, 128);
+            mbar_init(bars + kVHead + k, 4);
             mbar_init(bars + kQFull + k, 32 * kSoftWarps);
         }
         for (int k = 0; k < 2; ++k) {
@@ -290,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1) flat_kernel(const __grid_constant
         mbar_init(bars + kQEmpty, 1);
         mbar_init(bars + kDrain, 1);
         for (int k = 0; k < 2 * kExpWarps; ++k) mbar_init(bars + kRaw + k, 1);
-        for (int k = 0; k < 2; ++k) mbar_init(bars + kRaw + 2 * kExpWarps + k, kExpWarps);
+        for (int k = 0; k < 4; ++k) mbar_init(bars + kRaw + 2 * kExpWarps + k, 4);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (w == kIssuer) {
@@ -315,30 +316,32 @@ __global__ void __launch_bounds__(kThreads, 1) flat_kernel(const __grid_constant
         if (x < 4)
             expand_steps<D, INT8, BF16, false, 1>(
                 rings, x, 0, steps, err, lane,
+                [&](int k, float2 h, uint32_t) {
+                    if (lane == 0) reinterpret_cast<float*>(smem + Sh::kHeadK)[k % kRing * 4 + wp] = h.x;
+                },
                 [&](int k) {
                     if (k >= 2) bar_wait(bars + kKEmpty + (k & 1), (uint32_t)(((k >> 1) - 1) & 1), err);
                     return smem + Sh::kK + (k & 1) * Sh::kTileK;
                 },
-                [&](int k, float2 h, uint32_t) {
-                    if (lane == 0) reinterpret_cast<float*>(smem + Sh::kHeadK)[k % kRing * 4 + wp] = h.x;
-                    mbar_arrive(bars + kKFull + k % kRing);
-                });
+                [&](int k) { mbar_arrive(bars + kKFull + k % kRing); });
         else
             expand_steps<D, INT8, BF16, true, 1>(
                 rings, x, 0, steps, err, lane,
+                [&](int k, float2 h, uint32_t bad) {  // the weights need no more of V: they are made while its tile waits for a place
+                    if (lane == 0) {
+                        reinterpret_cast<float4*>(smem + Sh::kHeadV)[k % kRing * 4 + wp] = make_float4(h.x, h.y, __uint_as_float(bad), 0.f);
+                        mbar_arrive(bars + kVHead + k % kRing);
+                    }
+                },
                 [&](int k) {
                     if (k >= 2) bar_wait(bars + kVEmpty + (k & 1), (uint32_t)(((k >> 1) - 1) & 1), err);
                     return smem + Sh::kV + (k & 1) * Sh::kTileV;
                 },
-                [&](int k, float2 h, uint32_t bad) {
-                    if (lane == 0)
-                        reinterpret_cast<float4*>(smem + Sh::kHeadV)[k % kRing * 4 + wp] = make_float4(h.x, h.y, __uint_as_float(bad), 0.f);
-                    mbar_arrive(bars + kVFull + k % kRing);
-                });
+                [&](int k) { mbar_arrive(bars + kVFull + k % kRing); });
     } else if (w == kIssuer) {
         issue_role<D>(p, smem_addr(smem), bars, err);
-    } else if (w == kIssuer + 4) {
-        fill_rings<D, true>(p, rings, steps, err, lane);
+    } else {
+        fill_rings<D, true>(p, rings, (w - kIssuer) / 4 - 1, steps, err, lane);
     }
     tc_fence_before();
     __syncthreads();

@@ -126,84 +126,84 @@ __device__ __forceinline__ void expand_codes(const uint8_t* rec, uint8_t* dst, i
     }
 }
 
-// Exact tokens (nv of them; none: zeros, and `src` is not read) as the same. Non-finite V enters as 0, and `bad` says that there is
-// some; neither side's sets the part's power of two. h: K scale, or log2 of the V scale and kDenomUnit over it.
-template <int D, bool BF16, bool IS_V>
-__device__ __forceinline__ void expand_rows(const uint8_t* src, int nv, uint8_t* dst, int wp, int lane, float2& h, uint32_t& bad) {
-    const int g = lane >> 2, t = lane & 3;
-    constexpr int kPieces = D / 8;
-    h = IS_V ? make_float2(0.f, 1.f) : make_float2(1.f, 0.f);
-    bad = 0;
-    if (IS_V) {  // piece i: tokens 8 t .. of channel 8 i + g
+// 16 bytes of exact tokens (nv of them; none: zeros, and `src` is not read): of V tokens 8 t .. of channel 8 i + g, of K
+// bytes i * 512 + lane * 16 of the part's rows.
+template <int D, bool IS_V>
+__device__ __forceinline__ uint4 exact_piece(const uint8_t* src, int nv, int i, int lane) {
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (IS_V) {
+        const int g = lane >> 2, t = lane & 3;
+        if (8 * t < nv) x = *reinterpret_cast<const uint4*>(src + (8 * i + g) * 64 + 16 * t);
+        const int left = nv - 8 * t;
         uint32_t keep[4];
 #pragma unroll
-        for (int z = 0; z < 4; ++z)
-            keep[z] = (8 * t + 2 * z < nv ? 0xffffu : 0u) | (8 * t + 2 * z + 1 < nv ? 0xffff0000u : 0u);
-        auto piece = [&](int i) {
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (nv > 0) x = *reinterpret_cast<const uint4*>(src + (8 * i + g) * 64 + 16 * t);
-            return make_uint4(x.x & keep[0], x.y & keep[1], x.z & keep[2], x.w & keep[3]);
-        };
-        uint32_t top = 0;
+        for (int z = 0; z < 4; ++z) keep[z] = (2 * z < left ? 0xffffu : 0u) | (2 * z + 1 < left ? 0xffff0000u : 0u);
+        return make_uint4(x.x & keep[0], x.y & keep[1], x.z & keep[2], x.w & keep[3]);
+    }
+    if ((i * 32 + lane) / (D / 8) < nv) x = *reinterpret_cast<const uint4*>(src + (i * 32 + lane) * 16);
+    return x;
+}
+// What a part of exact tokens stands for: K's scale, or log2 of V's and kDenomUnit over it; `bad`: non-finite V, which enters as
+// 0. Neither side's non-finite values set the power of two.
+template <int D, bool BF16, bool IS_V>
+__device__ __forceinline__ float2 exact_head(const uint8_t* src, int nv, int lane, uint32_t& bad) {
+    bad = 0;
+    if (!IS_V && !BF16) return make_float2(1.f, 0.f);
+    uint32_t top = 0;
 #pragma unroll 2
-        for (int i = 0; i < kPieces; ++i) top = max_of(top, finite_only<BF16>(piece(i)));
-        const int ex = warp_exponent_v<BF16>(top);
-        const float f = power2(-ex);
-        h = make_float2((float)ex, f * kDenomUnit);
-        uint8_t* atom = dst + (wp >> 1) * (D * 128);
+    for (int i = 0; i < D / 8; ++i) {
+        const uint4 r = exact_piece<D, IS_V>(src, nv, i, lane);
+        top = max_of(top, finite_only<BF16>(r));
+        if (IS_V) bad |= bad_pair<BF16>(r.x) | bad_pair<BF16>(r.y) | bad_pair<BF16>(r.z) | bad_pair<BF16>(r.w);
+    }
+    if (!IS_V) return make_float2(power2(warp_exponent<BF16>(top) - kExactK), 0.f);
+    bad = __reduce_or_sync(0xffffffffu, bad);
+    const int ex = warp_exponent_v<BF16>(top);
+    return make_float2((float)ex, power2(-ex) * kDenomUnit);
+}
+// The tokens as rows of a K tile, or columns of a V tile. h: exact_head's.
+template <int D, bool BF16, bool IS_V>
+__device__ __forceinline__ void expand_rows(const uint8_t* src, int nv, uint8_t* dst, int wp, int lane, float2 h) {
+    const float f = IS_V ? power2(-(int)h.x) : 1.f / h.x;
 #pragma unroll 2
-        for (int i = 0; i < kPieces; ++i) {
-            const uint4 r = piece(i);
-            bad |= bad_pair<BF16>(r.x) | bad_pair<BF16>(r.y) | bad_pair<BF16>(r.z) | bad_pair<BF16>(r.w);
-            *reinterpret_cast<uint4*>(atom + swz(8 * i + g, 4 * (wp & 1) + t)) = scaled_f16<BF16>(finite_only<BF16>(r), f);
-        }
-        bad = __reduce_or_sync(0xffffffffu, bad);
-    } else {  // piece i: bytes i * 512 + lane * 16 of the part's rows
-        auto piece = [&](int i) {
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if ((i * 32 + lane) / kPieces < nv) x = *reinterpret_cast<const uint4*>(src + (i * 32 + lane) * 16);
-            return x;
-        };
-        float f = 1.f;
-        if (BF16) {
-            uint32_t top = 0;
-#pragma unroll 2
-            for (int i = 0; i < kPieces; ++i) top = max_of(top, finite_only<BF16>(piece(i)));
-            const int ex = warp_exponent<BF16>(top) - kExactK;
-            f = power2(-ex);
-            h.x = power2(ex);
-        }
-#pragma unroll 2
-        for (int i = 0; i < kPieces; ++i) {
-            const int y = i * 32 + lane, ch8 = y % kPieces;
-            const uint4 x = piece(i);
-            *reinterpret_cast<uint4*>(dst + (ch8 >> 3) * kAtom + swz(32 * wp + y / kPieces, ch8 & 7)) = BF16 ? scaled_f16<BF16>(x, f) : x;
+    for (int i = 0; i < D / 8; ++i) {
+        const uint4 r = exact_piece<D, IS_V>(src, nv, i, lane);
+        if (IS_V) {
+            uint8_t* atom = dst + (wp >> 1) * (D * 128);
+            *reinterpret_cast<uint4*>(atom + swz(8 * i + (lane >> 2), 4 * (wp & 1) + (lane & 3))) =
+                scaled_f16<BF16>(finite_only<BF16>(r), f);
+        } else {
+            const int y = i * 32 + lane, ch8 = y % (D / 8);
+            *reinterpret_cast<uint4*>(dst + (ch8 >> 3) * kAtom + swz(32 * wp + y / (D / 8), ch8 & 7)) =
+                BF16 ? scaled_f16<BF16>(r, f) : r;
         }
     }
 }
 
 // Eight rings of two entries each, one of every expansion warp x: part x & 3 (32 tokens) of every step, K for x < 4 and V
-// for the others (SIDES), or K of every other step, the odd ones for x >= 4. The rings go in step: turn t (step t, or steps 2 t and
-// 2 t + 1) is entry t & 1 of each. An exact part takes both entries, so a turn with one waits for the turn before to be through,
-// and the turn behind it for it.
+// for the others (SIDES), or K of every other step, the odd ones for x >= 4. The four rings of such a group go in step: turn t is entry
+// t & 1 of each. An exact part takes both entries, so a turn with one waits for the turn before to be through, and the turn
+// behind it for it.
 template <int D>
 struct Rings {
     static constexpr int kCount = 8;
     static constexpr int kBytes = kCount * 2 * kRingEntry<D>;
     uint8_t* data;     // [kCount][2][kRingEntry]
     uint64_t* full;    // barriers [kCount][2]
-    uint64_t* empty;   // barriers [2], of all rings
+    uint64_t* empty;   // barriers [2 groups][2]
     int32_t* what;     // [kCount][2]: kCodes, or exact tokens, none if 0
     static constexpr int kCodes = -1;
 };
 
-// One warp fills the rings, a lane each (the way along the line is the same for all, and costs an expansion warp as much as the
-// conversion). Pool slots are looked up a turn earlier.
+// A warp fills a group's rings, a lane each (the way along the line is the same for all, and costs an expansion warp as much as the
+// conversion). Pool slots are looked up a turn earlier. (One warp for both groups held K back until V was through too: the same
+// 60 us as long as softmax waited for V's tiles, 00 against 00 since.)
 template <int D, bool SIDES, class P>
-__device__ __forceinline__ void fill_rings(const P& p, const Rings<D>& rings, int steps, int32_t* err, int lane) {
+__device__ __forceinline__ void fill_rings(const P& p, const Rings<D>& rings, int group, int steps, int32_t* err, int lane) {
     const BlockView& c = p.c;
-    const int sh = c.log2_block - 5, wp = lane & 3, x = lane & 7;
-    const bool v = SIDES && x >= 4;
+    const int sh = c.log2_block - 5, wp = lane & 3, x = 4 * group + wp;
+    const bool v = SIDES && group == 1;
+    uint64_t* empty = rings.empty + 2 * group;
     uint8_t* data = rings.data + x * 2 * kRingEntry<D>;
     uint64_t* full = rings.full + 2 * x;
     volatile int32_t* what = rings.what + 2 * x;
@@ -219,7 +219,7 @@ __device__ __forceinline__ void fill_rings(const P& p, const Rings<D>& rings, in
             if (more) j = w.j0;
         }
     };
-    if (!SIDES && x >= 4) skip();
+    if (!SIDES && group == 1) skip();
     auto look = [&]() {
         Part a = {-1, 0, 0, 0, -1};
         if (!more) return a;
@@ -230,7 +230,7 @@ __device__ __forceinline__ void fill_rings(const P& p, const Rings<D>& rings, in
         if (!SIDES) skip();
         return a;
     };
-    const int turns = SIDES ? steps : (steps + 1) / 2;
+    const int turns = SIDES ? steps : (steps + 1 - group) / 2;
     bool ok = true, alone = false;  // alone: the turn before has the rings for itself
     Part now = look(), next = look();
     int t = 0;
@@ -239,11 +239,11 @@ __device__ __forceinline__ void fill_rings(const P& p, const Rings<D>& rings, in
         const int y = t & 1, exact = now.slot < 0 && now.seq >= 0 ? max(now.n - now.tile * kTileTokens, 0) : 0;
         const bool was = alone;
         alone = __any_sync(0xffffffffu, exact > 0);
-        bool here = t < 2 || bar_wait(rings.empty + y, (uint32_t)(((t >> 1) - 1) & 1), err);
-        if (t > 0 && (was || alone)) here = bar_wait(rings.empty + (y ^ 1), (uint32_t)(((t - 1) >> 1) & 1), err) && here;
+        bool here = t < 2 || bar_wait(empty + y, (uint32_t)(((t >> 1) - 1) & 1), err);
+        if (t > 0 && (was || alone)) here = bar_wait(empty + (y ^ 1), (uint32_t)(((t - 1) >> 1) & 1), err) && here;
         ok = __all_sync(0xffffffffu, here);
         if (!ok) break;
-        if (lane < Rings<D>::kCount) {
+        if (lane < 4) {
             if (now.slot >= 0) {
                 const uint8_t* rec = tile_ptr(c, now.slot, now.kvh, now.tile & ((1 << sh) - 1));
                 uint8_t* to = data + y * kRingEntry<D>;
@@ -276,34 +276,36 @@ __device__ __forceinline__ void fill_rings(const P& p, const Rings<D>& rings, in
         }
 }
 
-// Expansion warp x: its part of steps first, first + STRIDE .. of the CTA's `steps`. place(step): the tile to write, once it is
-// free; publish(step, h, bad): the tile is there.
-template <int D, bool INT8, bool BF16, bool IS_V, int STRIDE, class Place, class Publish>
-__device__ __forceinline__ void expand_steps(const Rings<D>& rings, int x, int first, int steps, int32_t* err, int lane, Place place,
-                                             Publish publish) {
+// Expansion warp x: its part of steps first, first + STRIDE .. of the CTA's `steps`. head(step, h, bad): what the part stands for, known
+// before there is a place for it; place(step): the tile to write, once it is free; publish(step): the tile is there.
+template <int D, bool INT8, bool BF16, bool IS_V, int STRIDE, class Head, class Place, class Publish>
+__device__ __forceinline__ void expand_steps(const Rings<D>& rings, int x, int first, int steps, int32_t* err, int lane, Head head,
+                                             Place place, Publish publish) {
     const uint8_t* data = rings.data + x * 2 * kRingEntry<D>;
     const volatile int32_t* what = rings.what + 2 * x;
     int t = 0;
 #pragma unroll 1
     for (int k = first; k < steps; k += STRIDE, ++t) {
         const int y = t & 1;
-        uint8_t* dst = place(k);
         bar_wait(rings.full + 2 * x + y, (uint32_t)(t >> 1 & 1), err);
         const int is = __shfl_sync(0xffffffffu, what[y], 0);  // one answer for the warp, also after a wait that gave up
+        const uint8_t* rec = data + y * kRingEntry<D>;
         float2 h;
         uint32_t bad = 0;
         if (is < 0) {
-            const uint8_t* rec = data + y * kRingEntry<D>;
             const float4 hd = *reinterpret_cast<const float4*>(rec);
             h = IS_V ? make_float2(hd.z, hd.w) : make_float2(hd.x, 0.f);
-            expand_codes<D, INT8, IS_V>(rec, dst, x & 3, lane);
         } else {
-            expand_rows<D, BF16, IS_V>(data, is, dst, x & 3, lane, h, bad);
+            h = exact_head<D, BF16, IS_V>(data, is, lane, bad);
         }
+        head(k, h, bad);
+        uint8_t* dst = place(k);
+        if (is < 0) expand_codes<D, INT8, IS_V>(rec, dst, x & 3, lane);
+        else expand_rows<D, BF16, IS_V>(data, is, dst, x & 3, lane, h);
         __syncwarp();
-        if (lane == 0) mbar_arrive(rings.empty + y);
+        if (lane == 0) mbar_arrive(rings.empty + (x >> 2) * 2 + y);
         fence_proxy_async_smem();
-        publish(k, h, bad);
+        publish(k);
     }
 }
 

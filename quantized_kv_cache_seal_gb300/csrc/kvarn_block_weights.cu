@@ -17,16 +17,16 @@ namespace {
 // unit of work is a step of 128 tokens for a tile of 128 rows of a (sequence, KV head), and the line of all units is cut evenly over
 // the CTAs, one a SM. Roles (736 threads): eight expansion warps that turn K codes into f16 tiles (a warp 32 tokens,
 // four warps every other step); one that issues the MMAs into four S buffers (all 512 columns of tensor
-// memory: no O is kept); one that fills the code rings; three softmax warpgroups, every third step each, a thread a row. Every wait
+// memory: no O is kept); two that fill the code rings; three softmax warpgroups, every third step each, a thread a row. Every wait
 // is bounded and sets the error word when it gives up.
 constexpr int kWinThreads = 736, kWinStep = 128, kWinStages = 3, kWinRing = 8;
-// warps; behind the softmax ones in turn of four the issuer, the one that fills the rings and an idle one, and three expansion warps, so that the issuer's
+// warps; behind the softmax ones in turn of four the issuer and the two that fill the rings, and three expansion warps, so that the issuer's
 // scheduler has none of those
 constexpr int kWinSoftmax = 4 * kWindowParts, kWinExpand = 8, kWinIssuer = kWinSoftmax;
 static_assert(kWinThreads == 32 * (kWinSoftmax + kWinExpand + 3), "warps");
 // barriers
 constexpr int kKFull = 0, kKEmpty = kKFull + kWinRing, kSFull = kKEmpty + kWinStages, kSEmpty = kSFull + 4, kQFull = kSEmpty + 4,
-              kQEmpty = kQFull + kWinRing, kDrain = kQEmpty + 2, kRaw = kDrain + 1, kWinBars = kRaw + kWinExpand * 2 + 2;
+              kQEmpty = kQFull + kWinRing, kDrain = kQEmpty + 2, kRaw = kDrain + 1, kWinBars = kRaw + kWinExpand * 2 + 4;
 
 template <int D>
 struct WinShape {
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kWinThreads, 1) window_kernel(const __grid_con
         for (int k = 0; k < 2; ++k) mbar_init(bars + kQEmpty + k, 1);
         mbar_init(bars + kDrain, 1);
         for (int k = 0; k < kWinExpand * 2; ++k) mbar_init(bars + kRaw + k, 1);
-        for (int k = 0; k < 2; ++k) mbar_init(bars + kRaw + 2 * kWinExpand + k, kWinExpand);
+        for (int k = 0; k < 4; ++k) mbar_init(bars + kRaw + 2 * kWinExpand + k, 4);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (w == kWinIssuer) {
@@ -228,18 +228,18 @@ __global__ void __launch_bounds__(kWinThreads, 1) window_kernel(const __grid_con
         const int x = (w - kWinSoftmax) / 4 * 3 + (w & 3) - 1, odd = x >> 2, wp = x & 3;
         expand_steps<D, INT8, BF16, false, 2>(
             rings, x, odd, steps, err, lane,
+            [&](int k, float2 h, uint32_t) {
+                if (lane == 0) reinterpret_cast<float*>(smem + Sh::kScale)[k % kWinRing * 4 + wp] = h.x;
+            },
             [&](int k) {
                 if (k >= kWinStages) bar_wait(bars + kKEmpty + k % kWinStages, (uint32_t)((k / kWinStages - 1) & 1), err);
                 return smem + Sh::kK + k % kWinStages * Sh::kTile;
             },
-            [&](int k, float2 h, uint32_t) {
-                if (lane == 0) reinterpret_cast<float*>(smem + Sh::kScale)[k % kWinRing * 4 + wp] = h.x;
-                mbar_arrive(bars + kKFull + k % kWinRing);
-            });
+            [&](int k) { mbar_arrive(bars + kKFull + k % kWinRing); });
     } else if (w == kWinIssuer) {
         win_issue<D>(p, smem_addr(smem), bars, err);
-    } else if (w == kWinIssuer + 4) {
-        fill_rings<D, false>(p, rings, steps, err, lane);
+    } else {
+        fill_rings<D, false>(p, rings, (w - kWinIssuer) / 4 - 1, steps, err, lane);
     }
     tc_fence_before();
     __syncthreads();
