@@ -305,7 +305,7 @@ kvarn_status run_weigh(kvarn_block_cache* c, BlockWeighParams& p, void* stream) 
     p.hkv = c->cfg.num_kv_heads;
     p.log2_tiles = c->view.log2_block - 5;
     p.cols = (int32_t)columns(c);
-    // Lanes enough for a block's sums two at a time; a CTA one round of blocks, or more where that still makes eight CTAs
+    // Lanes enough for a block's sums two at a time; a CTA one round of blocks, or more where that still makes four CTAs
     // a SM: every CTA looks its rows' totals up.
     int32_t pad = 1, tiles = 1;
     int64_t blocks = 0;
@@ -317,7 +317,7 @@ kvarn_status run_weigh(kvarn_block_cache* c, BlockWeighParams& p, void* stream) 
     p.lanes = 1;
     while (p.lanes < 32 && p.lanes * 2 < pad << p.log2_tiles) p.lanes *= 2;
     p.blocks = 256 / p.lanes;
-    while (p.blocks < 8 * 256 / p.lanes && blocks / (2 * p.blocks) > 8 * c->sms) p.blocks *= 2;
+    while (p.blocks < 8 * 256 / p.lanes && blocks / (2 * p.blocks) > 4 * c->sms) p.blocks *= 2;
     p.most = (((tiles - 1) >> p.log2_tiles) + p.blocks) / p.blocks;
     const int rc = launch_block_weigh(p, stream);
     return rc ? cuda_fail(rc, "weights launch") : KVARN_OK;

@@ -828,7 +828,8 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_c
 
 #ifdef KVARN_BLOCK_MORE
 // combine_kernel for both uses of prefixes; a warp four rows at a time, whose loads are on their way together (one row a warp
-// takes four rounds of thread blocks: 20 us for 3,500 query rows of 2,048 tokens, where this takes 00).
+// takes four rounds of thread blocks: 20 us for the 3,500 query rows of eight questions over 2,048 tokens, where
+// this takes 15).
 constexpr int kMoreRows = 4;
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kCombineThreads) combine_more_kernel(const __grid_constant__ BlockPrefillParams p KVARN_MORE_PARAM) {

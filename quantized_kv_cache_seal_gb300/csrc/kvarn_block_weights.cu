@@ -7,6 +7,10 @@
 // a maximum m and the tile's sum s of 2^(x - m), 8 bytes for 32 logits, and of every row its total; weigh_kernel
 // adds the tiles' shares to their blocks in a fixed order. Kept as a pair, no rounding of a logit's size
 // stands between a weight and its denominator (log2 of the sum in one word would be off by 2^-17 at 128).
+//
+// Measured: beside decode (16 sequences of 32k, 32 / 8 heads) the pairs cost nothing that shows, 178 us as without, and weigh_kernel
+// 6.4 us. 32 queries of 16 ragged prompts of 1k to 16k, 40 / 10 heads, bf16 (178 MB of codes, 45 MB of pairs written and read): window_kernel 60 us,
+// weigh_kernel 14; the former bound by issue slots (61 % busy; a third of them the weights), the latter by its loads' latency.
 #include "kvarn_block_ring.cuh"
 
 namespace kvarn {
@@ -83,8 +87,8 @@ __device__ __forceinline__ void win_issue(const BlockWindowParams& p, uint32_t s
     }
 }
 
-// Warpgroup b takes every third step; thread et owns row et. (Two of them take 72 us where three take 60; four, with an S buffer
-// each that the next MMAs wait for, 79.)
+// Warpgroup b takes every third step; thread et owns row et. (32 queries of 16 ragged prompts: two of them 74 us, three
+// 72, four, with an S buffer each that the next MMAs wait for, 79; three with rows that several warps bring 60.)
 template <int D, bool BF16>
 __device__ __forceinline__ void win_softmax(const BlockWindowParams& p, uint8_t* smem, uint64_t* bars, int32_t* err, int et, int b,
                                             uint32_t lane_off) {
@@ -255,12 +259,21 @@ __global__ void __launch_bounds__(kWinThreads, 1) window_kernel(const __grid_con
 constexpr int kWeighThreads = 256;
 constexpr int kWeighRows = 128 * kBlockMaxRatio;  // rows of a KV head
 
-// A CTA some blocks of a (KV head, sequence): its rows' totals first, then p.lanes lanes a block.
-template <int SEQS>
+// The CTA that takes unit u: the last b with units b / grid <= u, that is units b < (u + 1) grid. (No division of 64 bits.)
+__device__ __forceinline__ int cta_of(int64_t u, int64_t units, int grid) {
+    int64_t b = (int64_t)((float)u / (float)units * (float)grid);
+    while (units * b >= (u + 1) * grid) --b;
+    while (units * (b + 1) < (u + 1) * grid) ++b;
+    return (int)b;
+}
+
+// A CTA some blocks of a (KV head, sequence): its rows' totals first, then p.lanes lanes (WIDE: 32) a block.
+template <int SEQS, bool WIDE>
 __global__ void __launch_bounds__(kWeighThreads) weigh_kernel(const __grid_constant__ BlockWeighArgs<SEQS> p) {
     __shared__ float2 of[kWeighRows];  // of a row: its maximum, 1 / denominator (0: adds nothing)
     __shared__ float2 some[kWeighThreads];
     __shared__ int2 ctas[kWeighRows / 128];
+    __shared__ float got[WIDE ? 8 * kWeighThreads / 32 : 8 * kWeighThreads];  // of a block
     const BlockWeighSeq& e = p.seqs[blockIdx.z];
     const int h = blockIdx.y, t = threadIdx.x, blocks = (e.tiles + (1 << p.log2_tiles) - 1) >> p.log2_tiles;
     const int first = blockIdx.x * p.blocks;
@@ -269,7 +282,7 @@ __global__ void __launch_bounds__(kWeighThreads) weigh_kernel(const __grid_const
         const int steps = (e.tiles + 3) / 4;
         if (t < (e.rows + 127) / 128) {
             const int64_t u = e.unit_begin + (int64_t)(h * ((e.rows + 127) / 128) + t) * steps;
-            ctas[t] = make_int2((int)(((u + 1) * p.grid - 1) / p.units), (int)(((u + steps) * p.grid - 1) / p.units));
+            ctas[t] = make_int2(cta_of(u, p.units, p.grid), cta_of(u + steps - 1, p.units, p.grid));
         }
         __syncthreads();
     }
@@ -298,23 +311,56 @@ __global__ void __launch_bounds__(kWeighThreads) weigh_kernel(const __grid_const
     }
     __syncthreads();
     const float2* sums = p.sums + e.sum_begin + ((int64_t)h * e.stride + e.before) * e.pad;
-    float* to = p.weights + ((int64_t)e.seq * p.hkv + h) * p.cols;
-    const int lane = t % p.lanes, lane0 = lane % e.pad, step = p.lanes % e.pad;
-    for (int b = first + t / p.lanes; b < first + p.blocks; b += kWeighThreads / p.lanes) {  // whole warps
-        const int t0 = b << p.log2_tiles, count = (min(t0 + (1 << p.log2_tiles), e.tiles) - t0) * e.pad;  // negative: none
-        const float2* at = sums + (int64_t)t0 * e.pad;
-        float sum = 0.f;
-        int row = lane0;
-#pragma unroll 4
-        for (int k = lane; k < count; k += p.lanes) {
-            const float2 x = at[k], f = of[row];
-            if (f.y != 0.f) sum = fmaf(x.y * ex2f(x.x - f.x), f.y, sum);  // (a tile out of sight: -inf, 0)
-            row += step;
-            if (row >= e.pad) row -= e.pad;
+    float* to = p.weights + ((int64_t)e.seq * p.hkv + h) * p.cols + first;
+    const int count = min(p.blocks, blocks - first);
+    auto share = [](float2 x, float2 f) {  // (a tile out of sight: -inf, 0)
+        const float y = x.y * ex2f(x.x - f.x);
+        return f.y != 0.f ? y * f.y : 0.f;
+    };
+    if (WIDE) {
+        // A warp a block, 128 rows at a time, four a lane, whose totals stay in registers (looked up row by row, 21 us where this
+        // takes 14 for 32 queries of 16 ragged prompts).
+        const int w = t >> 5, lane = t & 31;
+        for (int r0 = 0; r0 < e.pad; r0 += 128) {
+            float2 f[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = r0 + 32 * i + lane < e.pad ? of[r0 + 32 * i + lane] : make_float2(0.f, 0.f);
+            for (int b = w; b < count; b += kWeighThreads / 32) {
+                const int t0 = (first + b) << p.log2_tiles, t1 = min(t0 + (1 << p.log2_tiles), e.tiles);
+                const float2* at = sums + (int64_t)t0 * e.pad + r0 + lane;
+                float sum = 0.f;
+#pragma unroll 2
+                for (int k = t0; k < t1; ++k, at += e.pad) {
+                    float2 x[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[i] = r0 + 32 * i + lane < e.pad ? at[32 * i] : make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sum += share(x[i], f[i]);
+                }
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                if (lane == 0) got[b] = r0 == 0 ? sum : got[b] + sum;
+            }
         }
-        for (int d = p.lanes / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        if (lane == 0 && b < blocks) to[b] += sum;
+    } else {
+        const int lane = t % p.lanes, lane0 = lane % e.pad, step = p.lanes % e.pad;
+        for (int b = t / p.lanes; b < p.blocks; b += kWeighThreads / p.lanes) {  // whole warps
+            const int t0 = (first + b) << p.log2_tiles, n = (min(t0 + (1 << p.log2_tiles), e.tiles) - t0) * e.pad;  // negative: none
+            const float2* at = sums + (int64_t)t0 * e.pad;
+            float sum = 0.f;
+            int row = lane0;
+#pragma unroll 4
+            for (int k = lane; k < n; k += p.lanes) {
+                sum += share(at[k], of[row]);
+                row += step;
+                row -= row >= e.pad ? e.pad : 0;
+            }
+            for (int d = p.lanes / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            if (lane == 0) got[b] = sum;
+        }
     }
+    __syncthreads();
+    for (int b = t; b < count; b += kWeighThreads) to[b] += got[b];
 }
 
 template <int D, bool INT8, bool BF16>
@@ -344,13 +390,17 @@ int launch_block_window(const BlockWindowParams& p, void* stream) {
 
 int launch_block_weigh(const BlockWeighParams& p, void* stream) {
     const dim3 grid(p.most, p.hkv, p.n_seqs);
+    cudaStream_t t = (cudaStream_t)stream;
     if (p.n_seqs <= 16) {
         BlockWeighArgs<16> few;
         static_cast<BlockWeighHead&>(few) = p;
         for (int i = 0; i < p.n_seqs; ++i) few.seqs[i] = p.seqs[i];
-        weigh_kernel<16><<<grid, kWeighThreads, 0, (cudaStream_t)stream>>>(few);
+        if (p.lanes == 32) weigh_kernel<16, true><<<grid, kWeighThreads, 0, t>>>(few);
+        else weigh_kernel<16, false><<<grid, kWeighThreads, 0, t>>>(few);
+    } else if (p.lanes == 32) {
+        weigh_kernel<kBlockMaxSeqs, true><<<grid, kWeighThreads, 0, t>>>(p);
     } else {
-        weigh_kernel<kBlockMaxSeqs><<<grid, kWeighThreads, 0, (cudaStream_t)stream>>>(p);
+        weigh_kernel<kBlockMaxSeqs, false><<<grid, kWeighThreads, 0, t>>>(p);
     }
     return (int)cudaGetLastError();
 }
