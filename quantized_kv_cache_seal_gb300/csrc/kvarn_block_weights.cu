@@ -24,6 +24,9 @@ namespace {
 // memory: no O is kept); two that fill the code rings; three softmax warpgroups, every third step each, a thread a row. Every wait
 // is bounded and sets the error word when it gives up.
 constexpr int kWinThreads = 736, kWinStep = 128, kWinStages = 3, kWinRing = 8;
+// A step's scales are written before its tile has a place, when the QK of five steps before has been issued and so the softmax of nine
+// before is through: eight places would not do.
+constexpr int kWinScales = 16;
 // warps; behind the softmax ones in turn of four the issuer and the two that fill the rings, and three expansion warps, so that the issuer's
 // scheduler has none of those
 constexpr int kWinSoftmax = 4 * kWindowParts, kWinExpand = 8, kWinIssuer = kWinSoftmax;
@@ -38,8 +41,8 @@ struct WinShape {
     static constexpr int kQ = 0;                                   // 2 tiles
     static constexpr int kK = 2 * kTile;                           // kWinStages tiles
     static constexpr int kRings = kK + kWinStages * kTile;
-    static constexpr int kScale = kRings + Rings<D>::kBytes;       // float[kWinRing][4]: K scale of a step's parts
-    static constexpr int kPower = kScale + kWinRing * 16;          // int8[kWinRing][128]: of a segment's rows
+    static constexpr int kScale = kRings + Rings<D>::kBytes;       // float[kWinScales][4]: K scale of a step's parts
+    static constexpr int kPower = kScale + kWinScales * 16;         // int8[kWinRing][128]: of a segment's rows
     static constexpr int kBars = kPower + kWinRing * 128;
     static constexpr int kWhat = kBars + 8 * kWinBars;             // int[8][2]
     static constexpr int kTmem = kWhat + 64;
@@ -140,7 +143,7 @@ __device__ __forceinline__ void win_softmax(const BlockWindowParams& p, uint8_t*
                 first = false;
             }
             bar_wait(bars + kKFull + kk % kWinRing, (uint32_t)(kk / kWinRing & 1), err);
-            const float* hd = reinterpret_cast<const float*>(smem + Sh::kScale) + kk % kWinRing * 4;
+            const float* hd = reinterpret_cast<const float*>(smem + Sh::kScale) + kk % kWinScales * 4;
             bar_wait(bars + kSFull + (kk & 3), (uint32_t)(kk >> 2 & 1), err);
             __syncwarp();
             tc_fence_after();
@@ -233,7 +236,7 @@ __global__ void __launch_bounds__(kWinThreads, 1) window_kernel(const __grid_con
         expand_steps<D, INT8, BF16, false, 2>(
             rings, x, odd, steps, err, lane,
             [&](int k, float2 h, uint32_t) {
-                if (lane == 0) reinterpret_cast<float*>(smem + Sh::kScale)[k % kWinRing * 4 + wp] = h.x;
+                if (lane == 0) reinterpret_cast<float*>(smem + Sh::kScale)[k % kWinScales * 4 + wp] = h.x;
             },
             [&](int k) {
                 if (k >= kWinStages) bar_wait(bars + kKEmpty + k % kWinStages, (uint32_t)((k / kWinStages - 1) & 1), err);

@@ -487,3 +487,27 @@ def test_a_pool_of_more_than_4_gb():
     check(out[:, :2], want, tol, "prefix")
     share, off = received(q[:, :2], parts[0], 128 ** -0.5, [n - 1], 128, n - 300)
     near(w[2, :2], before[2, :2], share, off, "weights")
+
+
+def test_window_of_long_prompts_repeats():
+    """Many steps a thread block, on every SM: the same bits each time, and right."""
+    lens = [9000, 5762, 8000, 7531, 4464, 3220, 9001, 2356]
+    c = make(max_seqs=8, num_q_heads=40, num_kv_heads=10, block_tokens=32, dtype=torch.bfloat16, max_seq_len=9001,
+             pool_blocks=sum(n // 32 for n in lens))
+    k, _ = fill(c, lens, torch.bfloat16, 730)
+    ids = list(range(8))
+    q = tokens(32 * 8, 40, 128, torch.bfloat16, 732, 0.3)
+    first = torch.zeros(c.weights_shape, device="cuda")
+    c.window_weights(0, ids, [32] * 8, q, first)
+    for _ in range(40):
+        w = torch.zeros_like(first)
+        c.window_weights(0, ids, [32] * 8, q, w)
+        assert torch.equal(w, first)
+    # the mass that blocks receive: 32 queries of 4 heads
+    assert bool(((first.double().sum(-1) - 128).abs() < 128 * 2.0 ** -12).all())
+    for s in (0, 7):
+        held = block_ref.hold(k[s][:, :1], 32, "e4m3")
+        want, tol = received(q[32 * s:32 * s + 32, :4], held, 128 ** -0.5, list(range(lens[s] - 32, lens[s])), 32)
+        # received()'s bound is for 2^12 tokens; sums of 2^14 in turn add as many roundings four times
+        near(first[s, :1], torch.zeros_like(first[s, :1]), want, tol + want * 2.0 ** -14, s)
+    assert c.check_device_error() == 0
