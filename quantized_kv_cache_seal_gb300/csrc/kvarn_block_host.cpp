@@ -363,10 +363,10 @@ kvarn_status run_decode(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, con
     const int64_t pairs = (int64_t)n_seqs * c->cfg.num_kv_heads, most = std::min(c->sms, kBlockMaxGrid);
     const bool equal = std::all_of(p.seqs, p.seqs + n_seqs, [](const BlockDecodeSeq& e) { return e.units == p.seqs[0].units; });
     p.grid = (int32_t)(equal && p.seqs[0].units <= 32 && pairs <= most ? pairs : std::min((units + 7) / 8, most));
-    // Short pairs, four tiles a warp at least: the line is cut over the warps. (Measured with weights, 32 / 8 heads of 128, us
-    // over warps and over CTAs: 64 ragged sequences of up to 1,024 tokens 28 and 87, of up to 256 20 and 44; 64 of 2,048 59 and 59; 8 of
-    // 4,096 22 and 23; 16 of 8,192 59 and 58, of 32,768 195 and 182.)
-    x.alone = more && units >= 4 * 8 * most && units < 128 * pairs;
+    // Short pairs, a tile a warp at least: the line is cut over the warps. (Measured with weights, 32 / 8 heads of 128, us
+    // over warps and over CTAs: 64 ragged sequences of up to 1,024 tokens 28 and 87, of up to 256 21 and 44; 200 of up to 40 26 and 42;
+    // 64 of 2,048 57 and 59; 8 of 4,096 22 and 23; 16 of 8,192 59 and 58, of 32,768 195 and 182.)
+    x.alone = more && units >= 8 * most && units < 128 * pairs;
     if (x.alone) {
         units = 0;
         for (int i = 0; i < n_seqs; ++i) {
@@ -605,6 +605,7 @@ kvarn_status check_beside(kvarn_block_cache* c, int64_t rows, const void* q, con
     const size_t io = (size_t)rows * c->cfg.num_q_heads * c->cfg.head_dim * 2;
     const size_t held = weights ? (size_t)c->cfg.max_seqs * c->cfg.num_kv_heads * columns(c) * 4 : 0;
     if (weights && ((uintptr_t)weights & 3)) return fail(KVARN_EINVAL, "weights must be 4-byte aligned");
+    if (weights && c->cfg.num_kv_heads > 65535) return fail(KVARN_ECAPACITY, "weights of more than 65,535 KV heads");
     if (meet(weights, held, q, io) || meet(weights, held, out, out ? io : 0) || meet(workspace, w.total, q, io) ||
         meet(workspace, w.total, out, out ? io : 0) || meet(workspace, w.total, weights, held))
         return fail(KVARN_EINVAL, "weights or workspace overlap another argument");

@@ -79,12 +79,12 @@ def test_workspace_sizes():
     rows = 2 * 8
     assert size([0, 1], [5, -1], None) == up(rows * 128 * 4) + up(rows * 4)
     assert size([0, 1], [5, 5], [100, 3]) == up(103 * 8 * 128 * 4) + up(103 * 8 * 4)
-    # tiles of 32 tokens and four more a sequence, heads, 8 bytes
+    # tiles of 32 tokens and eight more a sequence, heads, 8 bytes
     # and a row's totals
-    assert size([0, 1], None, None, False, True) == up((4 + 3 + 2 * 4) * 8 * 8) + up(2 * 8 * 8)
-    assert size([2], None, None, False, True) == up((1 + 4) * 8 * 8) + up(8 * 8)  # an empty sequence has one
-    assert size([0], None, [29], True, True) == up((5 + 4) * 8 * 8) + up(29 * 8 * 8)
-    assert size([0], [5], None, False, True) == up(8 * 128 * 4) + up(8 * 4) + up((4 + 10 + 4) * 8 * 8) + up(8 * 8)
+    assert size([0, 1], None, None, False, True) == up((4 + 3 + 2 * 8) * 8 * 8) + up(2 * 8 * 8)
+    assert size([2], None, None, False, True) == up((1 + 8) * 8 * 8) + up(8 * 8)  # an empty sequence has one
+    assert size([0], None, [29], True, True) == up((5 + 8) * 8 * 8) + up(29 * 8 * 8)
+    assert size([0], [5], None, False, True) == up(8 * 128 * 4) + up(8 * 4) + up((4 + 10 + 8) * 8 * 8) + up(8 * 8)
     for bad in (([6], None, None), ([0], [6], None), ([0], None, [-1])):
         refused(1, size, *bad)
     refused(1, K.kvarn_block_attend_workspace, c, 2, [0], None, None)
@@ -228,4 +228,11 @@ def test_null_arguments():
     assert L.kvarn_block_attend_workspace(c, 0, 0, None, None, None, 0, 0, None) == 1
     assert L.kvarn_block_window_weights(c, 0, 1, K._i32([0]), None, FAKE, 1.0, W, SPACE, 1 << 30, None) == 1
     assert L.kvarn_block_append_attend(c, 0, 1, K._i32([0]), None, None, FAKE, 256, FAKE, 256, FAKE, FAKE, 1.0, None, None, 0, None) == 1
+    K.kvarn_block_destroy(c)
+
+
+def test_weights_of_too_many_heads():
+    c = cache(num_q_heads=65536, num_kv_heads=65536, head_dim=64, block_tokens=32, max_seqs=2, pool_blocks=0, num_layers=1)
+    refused(3, attend, c, [0], None, None, weights=W)
+    attend(c, [0], [1], None)
     K.kvarn_block_destroy(c)

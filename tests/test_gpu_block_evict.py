@@ -511,3 +511,63 @@ def test_window_of_long_prompts_repeats():
         # received()'s bound is for 2^12 tokens; sums of 2^14 in turn add as many roundings four times
         near(first[s, :1], torch.zeros_like(first[s, :1]), want, tol + want * 2.0 ** -14, s)
     assert c.check_device_error() == 0
+
+
+def test_two_caches_at_once():
+    """Two caches' calls on two streams, interleaved: each as alone."""
+    caches, want, w, q = [], [], [], []
+    for i in range(2):
+        c = make(max_seqs=41, num_q_heads=32, num_kv_heads=8, block_tokens=32, max_seq_len=3000)
+        fill(c, [50 + 3 * j for j in range(40)] + [2300], torch.float16, 740 + 10 * i)
+        caches.append(c)
+        q.append(tokens(160, 32, 128, torch.float16, 760 + i, 0.3))
+    ids, pre = list(range(40)), [40] * 40
+
+    def run(i, weights):
+        c = caches[i]
+        a = c.decode_attention(0, ids, q[i][:40], prefix_ids=pre, weights=weights)
+        c.window_weights(0, ids, [4] * 40, q[i], weights)
+        return a, c.prefill_attention(0, ids, [4] * 40, q[i], prefix_ids=pre), weights
+
+    for i in range(2):
+        want.append(run(i, torch.zeros(caches[i].weights_shape, device="cuda")))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        got = []
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got.append(run(i, torch.zeros(caches[i].weights_shape, device="cuda")))
+        torch.cuda.synchronize()
+        for g, x in zip(got, want):
+            assert all(torch.equal(a, b) for a, b in zip(g, x))
+
+
+def test_a_space_that_grows_under_a_graph():
+    """A captured call keeps its workspace when later calls need a larger one, and one captured when it has to grow works too."""
+    c = make(max_seqs=64, num_q_heads=64, num_kv_heads=64, block_tokens=32, max_seq_len=2000, pool_blocks=64 * 20)
+    fill(c, [600] * 64, torch.float16, 780)
+    q = tokens(64 * 8, 64, 128, torch.float16, 782, 0.3)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        w, g, big = torch.zeros(c.weights_shape, device="cuda"), torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+        c.decode_attention(0, [0], q[:1], weights=torch.zeros_like(w))
+        size = c._spaces[-1].numel()
+        with torch.cuda.graph(g, stream=s):
+            c.decode_attention(0, [0, 1], q[:2], weights=w)
+        with torch.cuda.graph(big, stream=s):
+            c.window_weights(0, list(range(64)), [8] * 64, q, w)
+        assert c._spaces[-1].numel() == size  # the graph's own
+        want = torch.zeros_like(w)
+        c.decode_attention(0, [0, 1], q[:2], weights=want)
+        c.window_weights(0, list(range(64)), [8] * 64, q, want)
+        assert c._spaces[-1].numel() > size
+        junk = [torch.full((size,), 0xff, dtype=torch.uint8, device="cuda") for _ in range(8)]
+        for _ in range(2):
+            w.zero_()
+            g.replay()
+            big.replay()
+            s.synchronize()
+            assert torch.equal(w, want)
+    del junk
