@@ -526,11 +526,12 @@ kvarn_status run_tiles(kvarn_block_cache* c, int32_t layer, int32_t n_entries, c
     mark(x.merged, finished, p.n_seqs);
     // Whole segments, the longest first, end when the longest does or the SMs have shared out all;
     // the line of all steps cut evenly ends a share of the steps later, and then costs about four more
-    // for the partial results and the kernel that adds them (6 us where a step takes 1.5).
+    // for the partial results and the kernel that adds them (6 us where a step takes 1.5); eight with prefixes, whose
+    // rows are fp32 or are joined (15 to 20 us where it takes 1.9).
     const int64_t sms = std::min(c->sms, kBlockPrefillGrid);
     const int64_t share = (steps + sms - 1) / sms;
     const int64_t whole = segs >= 2 * sms ? share : std::max(share, longest * ((segs + sms - 1) / sms));
-    p.line = whole > share + 4;
+    p.line = whole > share + (beside.pre_lse ? 8 : 4);
     p.steps = (int32_t)steps;
     p.segs = (int32_t)segs;
     p.grid = (int32_t)std::min<int64_t>(sms, p.line ? steps : segs);
