@@ -157,12 +157,12 @@ class BlockCache:
                     K.kvarn_block_append_attend(self.handle, layer, seq_ids, prefix_ids, counts, k, ks, v, vs, q, out, scale,
                                                 weights, space, n, s)
 
-            self._in_space(call, lambda: K.kvarn_block_attend_workspace(self.handle, layer, seq_ids, prefix_ids, counts,
-                                                                        k is not None, weights is not None))
+            self._in_space(stream, call, lambda: K.kvarn_block_attend_workspace(self.handle, layer, seq_ids, prefix_ids, counts,
+                                                                                k is not None, weights is not None))
             self._used(stream, s, k, v, q, out, weights)
         return out
 
-    def _in_space(self, call, need):
+    def _in_space(self, given, call, need):
         """call(workspace, bytes) with the cache's own, which grows where need() says that it is too small. Calls of one
         cache are ordered on the GPU, so that they can share it. Spaces that were outgrown stay: captured graphs use them."""
         space = self._spaces[-1]
@@ -182,10 +182,13 @@ class BlockCache:
         space = torch.empty(n if capturing else max(n, 2 * space.numel()), dtype=torch.uint8, device=self.device)
         if not capturing:
             self._spaces.append(space)
-            # held anew by the streams that calls go to, but for the one that it was allocated on
-            self._holders = {None if self.index < 0 else K.current_stream(self.device)}
-            if self.index >= 0:
-                self.mem.record_stream(torch.cuda.current_stream(self.device))
+            # held anew by the streams that calls go to, but for the one that it was allocated on (one given by its
+            # address holds nothing)
+            self._holders = set()
+            if not isinstance(given, int):
+                self._holders.add(None if self.index < 0 else K.current_stream(self.device))
+                if self.index >= 0:
+                    self.mem.record_stream(torch.cuda.current_stream(self.device))
         return call(space, space.numel())
 
     def decode_attention(self, layer: int, seq_ids: Sequence[int], q: torch.Tensor, out: Optional[torch.Tensor] = None,
@@ -263,8 +266,8 @@ class BlockCache:
         self._weights(weights)
         with K.on_device(self.device, stream) as s:
             scale = self.scale if scale is None else scale
-            self._in_space(lambda space, n: K.kvarn_block_window_weights(self.handle, layer, seq_ids, q_lens, q, scale, weights,
-                                                                         space, n, s),
+            self._in_space(stream, lambda space, n: K.kvarn_block_window_weights(self.handle, layer, seq_ids, q_lens, q, scale,
+                                                                                 weights, space, n, s),
                            lambda: K.kvarn_block_window_workspace(self.handle, layer, seq_ids, q_lens))
             self._used(stream, s, q, weights)
 

@@ -323,3 +323,29 @@ def test_many_short_sequences(dtype, code, dim, block, hkv, r):
             want, tol = received(q[s:s + 1], torch.cat(parts), dim ** -0.5, [first + lens[s] - 1], block, first)
             near(w[s], before[s], want, tol, s)
     assert c.check_device_error() == 0
+
+
+def test_streams_that_hold_a_workspace_that_grows(monkeypatch):
+    """A stream given by its address holds nothing, also where a call lets the workspace grow; the next Stream object that
+    a call names holds the cache's memory and every workspace."""
+    held = []
+    record = torch.Tensor.record_stream
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda x, s: (held.append(x.data_ptr()), record(x, s))[1])
+    hq, hkv, dim, m = 32, 8, 128, 200
+    c = make(max_seqs=2, num_q_heads=hq, num_kv_heads=hkv)
+    k, v = fill(c, [m, 65], torch.float16, 900)
+    q = tokens(m, hq, dim, torch.float16, 910, 0.3)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    del held[:]
+    out = c.prefill_attention(0, [0], [m], q, stream=s.cuda_stream, prefix_ids=[1])
+    assert len(c._spaces) == 2 and not held
+    s.synchronize()
+    again = c.prefill_attention(0, [0], [m], q, stream=s, prefix_ids=[1])
+    assert {c.mem.data_ptr(), *(x.data_ptr() for x in c._spaces)} <= set(held)
+    s.synchronize()
+    assert torch.equal(out, again)
+    for t in (0, 64, m - 1):
+        want, tol = want_of(q, 0, k, v, 1, 0, m, m, 64, "e4m3", dim)
+        check(out[t:t + 1], want[t:t + 1], tol[t:t + 1], t)
+    assert c.check_device_error() == 0
