@@ -555,9 +555,11 @@ kvarn_status check_prefixes(kvarn_block_cache* c, int32_t layer, int32_t n_seqs,
         const int32_t pre = prefix_ids[i];
         if (pre < -1 || pre >= c->cfg.max_seqs) st = fail(KVARN_EINVAL, "no such prefix");
         else if (pre >= 0 && c->seen[pre]) st = fail(KVARN_EINVAL, "a prefix is a sequence of the call");
-        if (st || pre < 0) continue;
+        if (st) break;
+        tiles += head_tiles(c->L(ids[i], layer) + (added ? added[i] : 0));
+        if (pre < 0) continue;
         const int64_t n = c->L(pre, layer), m = q_lens ? q_lens[i] : 1;
-        tiles += tiles_of(n) + head_tiles(c->L(ids[i], layer) + (added ? added[i] : 0));
+        tiles += tiles_of(n);
         steps += (m + 128 / c->r) * ((n + 127) / 128);  // more than there can be
     }
     for (int i = 0; i < n_seqs; ++i) c->seen[ids[i]] = 0;
