@@ -405,7 +405,7 @@ kvarn_status kvarn_block_prefill(kvarn_block_cache* cache, int32_t layer, int32_
  * A prefix is a sequence of the cache like any other (written with kvarn_block_append, of any length). Where
  * prefix_ids[i] is not -1, the queries of seq_ids[i] attend all tokens of that sequence, then those of their own
  * (causally among themselves), under one softmax, as if the prefix stood in front of each sequence. Neighbours in the
- * call with the same prefix are taken together: it is read once for all their queries. A prefix may not be a sequence
+ * call with the same prefix are taken together: where that is quicker it is read once for all of them. A prefix may not be a sequence
  * of the call, and must not be released while calls on the GPU read it.
  *
  * ---- weights that blocks receive ----

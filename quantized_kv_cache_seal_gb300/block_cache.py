@@ -24,7 +24,7 @@ class BlockCache:
     nothing: keep the tensors and the cache until its work is done. Results belong to the stream that wrote them.
 
     Attention takes ``prefix_ids``, one a sequence (None or -1: none): sequences of the cache whose tokens stand in front
-    of the sequence's own, read once for all neighbours in the call that name the same one. With ``weights``, a layer of
+    of the sequence's own; neighbours in the call that name the same one share its reading where that is quicker. With ``weights``, a layer of
     ``new_weights()``, single queries add up what each block receives of their softmax weights, ``window_weights`` adds
     the last queries' of prompts, and ``evict`` keeps the blocks with the most."""
 

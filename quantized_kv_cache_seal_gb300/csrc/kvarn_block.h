@@ -147,6 +147,8 @@ struct BlockPrefillMore {
     int32_t flat;        // 1: every query sees all of the entry's n tokens, and finished rows go to pre_o and pre_lse
     float *pre_o, *pre_lse;  // f32 [rows][Hq][D], [rows][Hq]: written if flat; else added where merged says
     uint32_t merged[kBlockMaxSeqs / 32];  // bit i: entry i
+    int32_t pre[kBlockMaxSeqs];    // a prefix whose steps come first in the segments of entry i (not if flat)
+    int32_t pre_n[kBlockMaxSeqs];  // its tokens, 0: none
 };
 
 // Queries as tiles of 128 rows (query, head of a KV head) over a sequence in steps of 128 tokens, for each KV head.

@@ -45,6 +45,8 @@ kvarn_status cuda_fail(int rc, const char* what) {
 }
 
 constexpr int kWindowTokens = 128;   // queries of a sequence in window_weights
+constexpr int kOwnSteps = 18;        // of each SM: what a pass over the prefixes takes beside its steps
+constexpr int kChangeSteps = 4;      // of an SM: what a change of segment takes
 constexpr float kLog2e = 1.4426950408889634f;
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
@@ -237,6 +239,7 @@ kvarn_status append(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const i
 // query tile pairs of a KV head and their steps of 128 keys for the many-query one.
 int32_t tiles_of(int64_t n) { return (int32_t)((n + kTileTokens - 1) / kTileTokens); }
 int32_t head_tiles(int64_t n) { return (int32_t)std::max<int64_t>(1, (n + kTileTokens - 1) / kTileTokens); }
+int64_t key_steps(int64_t n) { return (n + 127) / 128; }
 int64_t head_pairs(const kvarn_block_cache* c, int64_t q_len) {
     const int pair_tokens = 2 * (128 / c->r);
     return (q_len + pair_tokens - 1) / pair_tokens;
@@ -291,7 +294,7 @@ kvarn_status check_attention(kvarn_block_cache* c, int32_t layer, int32_t n_seqs
 
 // What an attention call may have beside its own tokens, sequence by sequence.
 struct Beside {
-    const int32_t* before = nullptr;   // decode: a prefix whose tokens come first in the sequence's line, -1 for none
+    const int32_t* before = nullptr;   // a prefix whose tokens come first in the sequence's line, -1 for none
     const uint8_t* finished = nullptr; // 1: its rows over a prefix are in pre_o and pre_lse
     float *pre_o = nullptr, *pre_lse = nullptr;
     float2 *sums = nullptr, *totals = nullptr;  // decode: the tiles' sums, the rows'
@@ -408,6 +411,7 @@ kvarn_status run_decode(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, con
 // `flat` (rows go to pre_o and pre_lse), else causally.
 struct Entry {
     int32_t seq, n, q_len, q_row;
+    int32_t before;  // as Beside's
     uint8_t finished;
 };
 
@@ -434,7 +438,8 @@ kvarn_status run_prefill(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, co
     Entry entries[kBlockMaxSeqs];
     int64_t row = 0;
     for (int i = 0; i < n_seqs; ++i) {
-        entries[i] = Entry{ids[i], c->L(ids[i], layer), q_lens[i], (int32_t)row, (uint8_t)(beside.finished && beside.finished[i])};
+        entries[i] = Entry{ids[i], c->L(ids[i], layer), q_lens[i], (int32_t)row, beside.before ? beside.before[i] : -1,
+                           (uint8_t)(beside.finished && beside.finished[i])};
         row += q_lens[i];
     }
     return run_tiles(c, layer, n_seqs, entries, false, q, out, scale, stream, beside);
@@ -502,23 +507,33 @@ kvarn_status run_tiles(kvarn_block_cache* c, int32_t layer, int32_t n_entries, c
         e.n = entries[i].n;
         e.q_len = entries[i].q_len;
         e.q_row = entries[i].q_row;
-        e.pairs = entries[i].finished;  // (until they are counted below)
+        // (until they are counted below)
+        e.pairs = entries[i].finished;
+        e.seg_begin = flat ? -1 : entries[i].before;
+        e.step_begin = e.seg_begin >= 0 ? c->L(e.seg_begin, layer) : 0;
     }
     if (p.n_seqs == 0) return KVARN_OK;
     // the longest sequences first: their segments are the longest
-    std::sort(p.seqs, p.seqs + p.n_seqs, [](const BlockPrefillSeq& a, const BlockPrefillSeq& b) { return a.n > b.n; });
+    std::sort(p.seqs, p.seqs + p.n_seqs, [](const BlockPrefillSeq& a, const BlockPrefillSeq& b) {
+        return (int64_t)a.n + a.step_begin > (int64_t)b.n + b.step_begin;
+    });
+    const bool more = beside.pre_lse || beside.before;
     uint8_t finished[kBlockMaxSeqs];
-    int64_t segs = 0, steps = 0, longest = 0;
+    int64_t segs = 0, steps = 0, longest = 0, n_long = 0;
     for (int i = 0; i < p.n_seqs; ++i) {
         BlockPrefillSeq& e = p.seqs[i];
         finished[i] = (uint8_t)e.pairs;
+        x.pre[i] = e.seg_begin;
+        x.pre_n[i] = e.step_begin;
+        const int32_t before = (e.step_begin + 127) / 128;
         e.pairs = (int32_t)head_pairs(c, e.q_len);
         e.seg_begin = (int32_t)segs;
         e.step_begin = (int32_t)steps;
-        e.head_steps = flat ? e.pairs * ((e.n - 1) / 128 + 1) : (int32_t)head_steps(c, e.n, e.q_len);
-        longest = std::max<int64_t>(longest, (e.n - 1) / 128 + 1);
+        e.head_steps = flat ? e.pairs * ((e.n - 1) / 128 + 1) : (int32_t)head_steps(c, e.n, e.q_len) + e.pairs * before;
+        longest = std::max<int64_t>(longest, before + (e.n - 1) / 128 + 1);
         segs += (int64_t)e.pairs * hkv;
         steps += (int64_t)e.head_steps * hkv;
+        if (2 * (e.head_steps / e.pairs) > longest) n_long += (int64_t)e.pairs * hkv;  // (the longest come first)
     }
     x.flat = flat;
     x.pre_o = beside.pre_o;
@@ -530,15 +545,28 @@ kvarn_status run_tiles(kvarn_block_cache* c, int32_t layer, int32_t n_entries, c
     // rows are fp32 or are joined (15 to 20 us where it takes 1.9).
     const int64_t sms = std::min(c->sms, kBlockPrefillGrid);
     const int64_t share = (steps + sms - 1) / sms;
-    const int64_t whole = segs >= 2 * sms ? share : std::max(share, longest * ((segs + sms - 1) / sms));
-    p.line = whole > share + (beside.pre_lse ? 8 : 4);
+    if (more) {
+        // Segments can be of very different length here, where some sequences have a prefix in front: changes of segment count as well,
+        // as many as the line's last CTA has, whose are the shortest, and of whole ones only those that cannot share an SM count as the longest.
+        // (16 sequences, half of them behind a prefix of 8k: 493 us by the rule below.)
+        int64_t left = share, last = 0;
+        for (int i = p.n_seqs - 1; i >= 0 && left > 0; left -= (int64_t)p.seqs[i--].head_steps * hkv) {
+            const BlockPrefillSeq& e = p.seqs[i];
+            last += std::min<int64_t>((int64_t)e.pairs * hkv, left / std::max(1, e.head_steps / e.pairs) + 1);
+        }
+        const int64_t whole = std::max(share, longest * ((n_long + sms - 1) / sms)) + kChangeSteps * (segs / sms);
+        p.line = whole > share + 8 + kChangeSteps * last;
+    } else {
+        const int64_t whole = segs >= 2 * sms ? share : std::max(share, longest * ((segs + sms - 1) / sms));
+        p.line = whole > share + 4;
+    }
     p.steps = (int32_t)steps;
     p.segs = (int32_t)segs;
     p.grid = (int32_t)std::min<int64_t>(sms, p.line ? steps : segs);
     if (c->host_only) return KVARN_OK;
     const kvarn_status st = ensure_init(c, stream);
     if (st) return st;
-    const int rc = beside.pre_lse ? launch_block_prefill(p, x, stream) : launch_block_prefill(p, stream);
+    const int rc = more ? launch_block_prefill(p, x, stream) : launch_block_prefill(p, stream);
     return rc ? cuda_fail(rc, "prefill launch") : KVARN_OK;
 }
 
@@ -556,11 +584,13 @@ kvarn_status check_prefixes(kvarn_block_cache* c, int32_t layer, int32_t n_seqs,
         if (pre < -1 || pre >= c->cfg.max_seqs) st = fail(KVARN_EINVAL, "no such prefix");
         else if (pre >= 0 && c->seen[pre]) st = fail(KVARN_EINVAL, "a prefix is a sequence of the call");
         if (st) break;
-        tiles += head_tiles(c->L(ids[i], layer) + (added ? added[i] : 0));
+        const int64_t own = c->L(ids[i], layer) + (added ? (int64_t)added[i] : 0), most_pairs = head_pairs(c, q_lens ? q_lens[i] : 1);
+        tiles += head_tiles(own);
+        steps += most_pairs * ((own + 127) / 128);
         if (pre < 0) continue;
-        const int64_t n = c->L(pre, layer), m = q_lens ? q_lens[i] : 1;
+        const int64_t n = c->L(pre, layer);
         tiles += tiles_of(n);
-        steps += (m + 128 / c->r) * ((n + 127) / 128);  // more than there can be
+        steps += most_pairs * ((n + 127) / 128);
     }
     for (int i = 0; i < n_seqs; ++i) c->seen[ids[i]] = 0;
     if (!st && (tiles + n_seqs * (1 + kPairCost)) * c->cfg.num_kv_heads >= 1ll << 31) st = fail(KVARN_ECAPACITY, "2^31 tiles of 32 tokens or more in a call");
@@ -676,6 +706,13 @@ bool walked_once(const kvarn_block_cache* c, const Entry& g) {
     return each >= 4 * once && each * c->cfg.num_kv_heads > 600000;
 }
 
+// The same for more queries, whose row tiles are filled by each sequence's own: `extra` steps of all KV heads are what the prefixes
+// take more that way. Walked once they take a launch of their own and fp32 rows that are joined. (Measured, 32 / 8 heads of 128, us once
+// and each: 8 sequences of 17 to 200 queries behind 2k, 2.5 extra steps a SM, 57 and 42; 4 of 400 to 700 behind 16k, 6.7, 421 and
+// 398; 32 of 2 to 16 behind 1k, 11.4, 60 and 43; 8 of 30 to 100 behind 8k, 16.8, 123 and 114; 8 of 2 to 16 behind 8k, 20.2, 54 and 63;
+// 16 of 40 to 64 behind 16k, 20.2, 197 and 225; 64 behind four of 2k, 22.7, 137 and 154.)
+bool stacked(const kvarn_block_cache* c, int64_t extra) { return extra > (int64_t)kOwnSteps * c->sms; }
+
 kvarn_status run_attend(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* ids, const int32_t* prefix_ids,
                         const int32_t* q_lens, const void* q, void* out, float scale, float* weights, void* workspace,
                         const Workspace& w, void* stream) {
@@ -683,6 +720,7 @@ kvarn_status run_attend(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, con
     int32_t one[kBlockMaxSeqs], before[kBlockMaxSeqs], lens[kBlockMaxSeqs];
     uint8_t finished[kBlockMaxSeqs];
     Entry groups[kBlockMaxSeqs];
+    int64_t extra = 0;
     int32_t n = 0, n_groups = 0;
     int64_t row = 0;
     // Sequences without queries leave; runs of one prefix become groups of rows.
@@ -695,15 +733,19 @@ kvarn_status run_attend(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, con
         finished[n] = 0;
         lens[n] = m;
         if (pre >= 0) {
-            if (n == 0 || before[n - 1] != pre) groups[n_groups++] = Entry{pre, c->L(pre, layer), 0, (int32_t)row, 0};
+            if (n == 0 || before[n - 1] != pre) groups[n_groups++] = Entry{pre, c->L(pre, layer), 0, (int32_t)row, -1, 0};
             groups[n_groups - 1].q_len += m;
+            extra += head_pairs(c, m) * key_steps(c->L(pre, layer));
         }
         ++n;
         row += m;
     }
     if (n == 0) return KVARN_OK;
-    // Single queries can also walk a prefix each by itself, in the one launch that takes their own tokens. The groups whose
+    // Sequences can also walk a prefix each by itself, in the one launch that takes their own tokens. The groups whose
     // prefix is better walked once are those where that takes longer than the tiles' steps.
+    for (int g = 0; g < n_groups; ++g) extra -= head_pairs(c, groups[g].q_len) * key_steps(groups[g].n);
+    const bool together = stacked(c, extra * c->cfg.num_kv_heads);
+    auto walked = [&](int g) { return single ? walked_once(c, groups[g]) : together; };
     int32_t n_once = 0;
     for (int i = 0, g = -1, last = -1; i < n; ++i) {
         if (before[i] < 0) {
@@ -712,10 +754,10 @@ kvarn_status run_attend(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, con
         }
         if (before[i] != last) ++g;
         last = before[i];
-        finished[i] = !single || walked_once(c, groups[g]);
+        finished[i] = walked(g);
     }
     for (int g = 0; g < n_groups; ++g)
-        if (!single || walked_once(c, groups[g])) groups[n_once++] = groups[g];
+        if (walked(g)) groups[n_once++] = groups[g];
     Beside b;
     if (n_once > 0) {
         b.pre_o = (float*)((uint8_t*)workspace + w.pre_o);
@@ -726,8 +768,8 @@ kvarn_status run_attend(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, con
     b.finished = finished;
     for (int i = 0; i < n; ++i)
         if (finished[i]) before[i] = -1;
+    if (std::any_of(before, before + n, [](int32_t pre) { return pre >= 0; }) || single) b.before = before;
     if (!single) return run_prefill(c, layer, n, one, lens, q, out, scale, stream, b);
-    b.before = before;
     if (weights) {
         b.weights = weights;
         b.sums = (float2*)((uint8_t*)workspace + w.sums);

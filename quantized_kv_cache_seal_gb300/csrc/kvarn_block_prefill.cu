@@ -35,7 +35,8 @@
 //
 // KVARN_BLOCK_MORE: the variant with prefixes, a translation unit of its own (kvarn_block_prefill_more.cu), so that calls
 // without them keep their code. `flat`: a segment's rows are queries of many sequences and see all of a prefix; their
-// finished rows go to fp32. Otherwise rows take their share of such rows at the end.
+// finished rows go to fp32. Otherwise rows take their share of such rows at the end, or a prefix's steps stand in front of the
+// sequence's own, all of them seen.
 #include "kvarn_block_tc.cuh"
 
 namespace kvarn {
@@ -53,6 +54,7 @@ struct More {
     int32_t flat;
     float *pre_o, *pre_lse;
     uint32_t merged[1];
+    int32_t pre[1], pre_n[1];
 };
 #endif
 
@@ -100,10 +102,13 @@ __device__ __forceinline__ void tm_st16(uint32_t taddr, const uint32_t (&r)[16])
         : "memory");
 }
 // ---- the line of steps ----
-// Steps of a query tile pair: up to the last position that its queries see.
-__device__ __forceinline__ int pair_steps(const More& x, const BlockPrefillSeq& e, int pair, int pair_tokens) {
+// Steps of the prefix in front of entry i's own tokens.
+__device__ __forceinline__ int steps_before(const More& x, int i) { return kMore ? (x.pre_n[i] + kStep - 1) / kStep : 0; }
+// Steps of a query tile pair of entry i: up to the last position that its queries see.
+__device__ __forceinline__ int pair_steps(const BlockPrefillParams& p, const More& x, int i, int pair, int pair_tokens) {
+    const BlockPrefillSeq& e = p.seqs[i];
     if (kMore && x.flat) return (e.n - 1) / kStep + 1;
-    return (e.n - e.q_len + min((pair + 1) * pair_tokens, e.q_len) - 1) / kStep + 1;
+    return steps_before(x, i) + (e.n - e.q_len + min((pair + 1) * pair_tokens, e.q_len) - 1) / kStep + 1;
 }
 
 // A segment: sequence entry, KV head, tile pair, its steps and the part [j0, j1) of them to take
@@ -120,7 +125,7 @@ struct LineWalk {
     Seg s;
     __device__ __forceinline__ void set() {
         const BlockPrefillSeq& e = p.seqs[s.i];
-        s.steps = pair_steps(x, e, s.pair, pt);
+        s.steps = pair_steps(p, x, s.i, s.pair, pt);
         s.j1 = left > 0 ? min(s.steps, s.j0 + left) : 0;
         s.two = (2 * s.pair + 1) * (pt / 2) < e.q_len;
     }
@@ -136,7 +141,7 @@ struct LineWalk {
         rel -= s.kvh * e.head_steps;
         s.pair = e.pairs - 1;
 #pragma unroll 1
-        while (rel >= (n = pair_steps(x, e, s.pair, pt))) rel -= n, --s.pair;
+        while (rel >= (n = pair_steps(p, x, i, s.pair, pt))) rel -= n, --s.pair;
         s.j0 = rel;
         left = u1 - u0;
         set();
@@ -296,7 +301,7 @@ __device__ __forceinline__ void issue_role(uint32_t sbase, uint64_t* bars, int32
 // 9 to 14 % more time.) Lanes take V's chunks in an order in which the stores of eight lanes meet
 // eight different banks.
 template <int D, bool INT8, bool BF16>
-__device__ __forceinline__ void expand_role(const BlockPrefillParams& p, uint8_t* smem, uint64_t* bars, int32_t* err, int wp,
+__device__ __forceinline__ void expand_role(const BlockPrefillParams& p, const More& x_, uint8_t* smem, uint64_t* bars, int32_t* err, int wp,
                                             int lane) {
     using Sh = Shape<D>;
     const BlockView& c = p.c;
@@ -310,7 +315,10 @@ __device__ __forceinline__ void expand_role(const BlockPrefillParams& p, uint8_t
     auto halves = [&](uint32_t u, uint32_t v) {  // 8 codes
         return make_uint4(codes_lo<INT8>(u), codes_hi<INT8>(u), codes_lo<INT8>(v), codes_hi<INT8>(v));
     };
-    // The part of a step: its sequence entry and KV head (head * 256 + entry, -1 for none), its
+    auto head_of = [](int who) { return kMore ? who >> 8 & 0x3fffff : who >> 8; };
+    auto seq_of = [&](int who) { return kMore && who >> 30 ? x_.pre[who & 255] : p.seqs[who & 255].seq; };
+    auto n_of = [&](int who) { return kMore && who >> 30 ? x_.pre_n[who & 255] : p.seqs[who & 255].n; };
+    // The part of a step: its sequence entry and KV head (head * 256 + entry, -1 for none; bit 30: of its prefix), its
     // 32-token tile, with bit 31 set where the tile is exact or not there. A turn of the loop looks two
     // steps ahead (so that the pool slot is there when its address is needed), loads one ahead and
     // expands one.
@@ -324,7 +332,7 @@ __device__ __forceinline__ void expand_role(const BlockPrefillParams& p, uint8_t
     float4 hd = make_float4(1.f, 0.f, 0.f, 1.f);
 #pragma unroll 1
     for (int jj = -2; jj < 0 || who >= 0; ++jj) {
-        const uint8_t* rec1 = tile1 >> 31 ? nullptr : tile_ptr(c, slot, who1 >> 8, (int)tile1 & ((1 << sh) - 1));
+        const uint8_t* rec1 = tile1 >> 31 ? nullptr : tile_ptr(c, slot, head_of(who1), (int)tile1 & ((1 << sh) - 1));
         int who2 = -1;
         uint32_t tile2 = 0x80000000u;
         if (j == end && more) {
@@ -334,11 +342,15 @@ __device__ __forceinline__ void expand_role(const BlockPrefillParams& p, uint8_t
             if (lane == 0) mbar_arrive(bars + kBarTake);  // lets the feed make the next entry
         }
         if (more) {
-            const BlockPrefillSeq& e = p.seqs[w.s.i];
             who2 = w.s.kvh * 256 + w.s.i;
-            const int y = 4 * j++ + wp;
+            int y = 4 * j++ + wp;
+            if (kMore) {
+                const int before = 4 * steps_before(x_, w.s.i);
+                if (y < before) who2 |= 1 << 30;
+                else y -= before;
+            }
             tile2 = (uint32_t)y;
-            if (y < e.n >> c.log2_block << sh) slot = __ldg(block_table(c, e.seq) + (y >> sh));
+            if (y < n_of(who2) >> c.log2_block << sh) slot = __ldg(block_table(c, seq_of(who2)) + (y >> sh));
             else tile2 |= 0x80000000u;
         }
         if (jj >= 0) {
@@ -361,7 +373,7 @@ __device__ __forceinline__ void expand_role(const BlockPrefillParams& p, uint8_t
                     *reinterpret_cast<uint4*>(dst + cc * kAtom + swz(row, 2 * t + 1)) = b;
                 }
             } else {
-                expand_exact<D, BF16, false>(c, p.seqs[who & 255].seq, p.seqs[who & 255].n, who >> 8, (int)(tile & 0x7fffffffu), wp, lane, dst, h, bad, x);
+                expand_exact<D, BF16, false>(c, seq_of(who), n_of(who), head_of(who), (int)(tile & 0x7fffffffu), wp, lane, dst, h, bad, x);
             }
             if (lane == 0) head[0] = h.x;
             fence_proxy_async_smem();
@@ -380,7 +392,7 @@ __device__ __forceinline__ void expand_role(const BlockPrefillParams& p, uint8_t
                     if (rec1) x[i] = load_k(rec1, i);
                 }
             } else {
-                expand_exact<D, BF16, true>(c, p.seqs[who & 255].seq, p.seqs[who & 255].n, who >> 8, (int)(tile & 0x7fffffffu), wp, lane, dst, h, bad, x);
+                expand_exact<D, BF16, true>(c, seq_of(who), n_of(who), head_of(who), (int)(tile & 0x7fffffffu), wp, lane, dst, h, bad, x);
             }
             if (lane == 0) head[1] = __uint_as_float(bad), head[2] = h.x, head[3] = h.y;
             fence_proxy_async_smem();
@@ -405,10 +417,10 @@ __device__ __forceinline__ void expand_role(const BlockPrefillParams& p, uint8_t
 // [from, to) that it sees, each into its own channel: on top of the finished row `out`, or of the
 // partial one `part` (the other null).
 template <int D, bool BF16>
-__device__ __forceinline__ void add_non_finite(const BlockView& c, const BlockPrefillSeq& e, int kvh, int from, int to,
+__device__ __forceinline__ void add_non_finite(const BlockView& c, int seq, int n, int kvh, int from, int to,
                                                uint16_t* out, float* part) {
-    const int sealed = e.n & ~(c.block - 1);
-    const uint16_t* v = tail_ptr(c, c.lay.tail_v, e.seq, kvh);
+    const int sealed = n & ~(c.block - 1);
+    const uint16_t* v = tail_ptr(c, c.lay.tail_v, seq, kvh);
 #pragma unroll 1
     for (int ch = 0; ch < D; ++ch) {
         float sum = 0.f;
@@ -451,6 +463,7 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, const 
         const bool valid = tok_in < tpt && tok < e.q_len;
         const int row = valid ? (e.q_row + tok) * p.hq + w.s.kvh * p.r + head_in : -1;  // of q and out
         const int pos = valid && !(kMore && x.flat) ? e.n - e.q_len + tok : e.n - 1;
+        const int before = steps_before(x, w.s.i);
         float qs = scale;
         {
             // D / 8 lanes a row; loops stay short: this code runs once a segment, from a cold cache
@@ -508,7 +521,8 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, const 
             }
             bar_wait(bars + kBarSFull + b, (uint32_t)(step & 1), err);
             tc_fence_after();
-            const int lim = pos + 1 - j * kStep;  // visible columns
+            // visible columns
+            const int lim = kMore && j < before ? x.pre_n[w.s.i] - j * kStep : pos + 1 - (j - before) * kStep;
             uint32_t r[4][32];
             float mx = kNegInf;
             const bool plain = __all_sync(0xffffffffu, lim >= kStep);
@@ -640,7 +654,9 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, const 
             }
             if (__builtin_expect(bad, 0)) {
                 __syncwarp();  // the row is there
-                if (valid) add_non_finite<D, BF16>(p.c, e, w.s.kvh, 0, pos + 1, p.out + (size_t)row * D, nullptr);
+                if (kMore && valid && before > 0)
+                    add_non_finite<D, BF16>(p.c, x.pre[w.s.i], x.pre_n[w.s.i], w.s.kvh, 0, x.pre_n[w.s.i], p.out + (size_t)row * D, nullptr);
+                if (valid) add_non_finite<D, BF16>(p.c, e.seq, e.n, w.s.kvh, 0, pos + 1, p.out + (size_t)row * D, nullptr);
             }
         } else if (kMore && w.whole()) {  // a finished row over a shared prefix, in fp32
             const float inv = kDenomUnit * (l == 0.f ? 0.f : 1.f / l);
@@ -662,7 +678,7 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, const 
                 __syncwarp();
             }
             if (__builtin_expect(bad, 0) && valid)
-                add_non_finite<D, BF16>(p.c, e, w.s.kvh, 0, pos + 1, nullptr, x.pre_o + (size_t)row * D);
+                add_non_finite<D, BF16>(p.c, e.seq, e.n, w.s.kvh, 0, pos + 1, nullptr, x.pre_o + (size_t)row * D);
             if (valid) x.pre_lse[row] = lse_of(m, l, kShift);
         } else {
             float* part = reinterpret_cast<float*>(p.c.base + p.c.lay.partials) +
@@ -683,9 +699,14 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, const 
                     }
                     __syncwarp();
                 }
-                if (__builtin_expect(bad, 0) && valid)
-                    add_non_finite<D, BF16>(p.c, e, w.s.kvh, w.s.j0 * kStep, min(pos + 1, w.s.j1 * kStep), nullptr,
-                                            part + (size_t)(128 * b + et) * D);
+                if (__builtin_expect(bad, 0) && valid) {
+                    float* to = part + (size_t)(128 * b + et) * D;
+                    if (kMore && before > 0)
+                        add_non_finite<D, BF16>(p.c, x.pre[w.s.i], x.pre_n[w.s.i], w.s.kvh, w.s.j0 * kStep,
+                                                min(x.pre_n[w.s.i], w.s.j1 * kStep), nullptr, to);
+                    add_non_finite<D, BF16>(p.c, e.seq, e.n, w.s.kvh, (w.s.j0 - before) * kStep, min(pos + 1, (w.s.j1 - before) * kStep),
+                                            nullptr, to);
+                }
                 part[256 * D + 128 * b + et] = m;
                 part[256 * D + 256 + 128 * b + et] = l;
             }
@@ -746,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         softmax_role<D, BF16>(p, x, smem, bars, tmem, err, t & 127, wg, lane_off);
     } else if (wg == 2) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsExpand));
-        expand_role<D, INT8, BF16>(p, smem, bars, err, w & 3, lane);
+        expand_role<D, INT8, BF16>(p, x, smem, bars, err, w & 3, lane);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
         if (w == 12) issue_role<D>(smem_addr(smem), bars, err);

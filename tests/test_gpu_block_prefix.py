@@ -349,3 +349,72 @@ def test_streams_that_hold_a_workspace_that_grows(monkeypatch):
         want, tol = want_of(q, 0, k, v, 1, 0, m, m, 64, "e4m3", dim)
         check(out[t:t + 1], want[t:t + 1], tol[t:t + 1], t)
     assert c.check_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype,code", [("fp16", "e4m3"), ("bf16", "int8")])
+@pytest.mark.parametrize("block,dim,hkv,r,seqs,n", [(64, 128, 4, 4, 60, 4001), (32, 64, 2, 1, 90, 4090), (64, 128, 8, 4, 150, 700),
+                                                    (128, 128, 8, 7, 120, 1024), (64, 64, 5, 8, 130, 1300)])
+def test_prefill_walked_once(dtype, code, block, dim, hkv, r, seqs, n):
+    """Many sequences of few queries, whose rows stand together over the prefix: of tiles by themselves, and of so many that they
+    go in pairs; with a second prefix and sequences without one."""
+    dt = TYPES[dtype]
+    lens = [9 + (37 * i) % 90 for i in range(seqs)] + [n, 333, 45]
+    qlens = [2 + i % 7 for i in range(seqs)] + [1]
+    c = make(max_seqs=seqs + 3, num_q_heads=hkv * r, num_kv_heads=hkv, head_dim=dim, block_tokens=block, code=code, dtype=dt,
+             max_seq_len=4096, pool_blocks=(sum(lens) // block))
+    k, v = fill(c, lens, dt, 920)
+    ids = list(range(seqs)) + [seqs + 2]
+    pre = [seqs] * (seqs - 2) + [seqs + 1] * 2 + [None]
+    q = tokens(sum(qlens), hkv * r, dim, dt, 930, 0.3)
+    out = c.prefill_attention(0, ids, qlens, q, prefix_ids=pre)
+    at = [sum(qlens[:i]) for i in range(len(ids))]
+    for i in (0, 1, seqs // 2, seqs - 3, seqs - 2, seqs - 1, seqs):
+        want, tol = want_of(q, at[i], k, v, pre[i], ids[i], lens[ids[i]], qlens[i], block, code, dim)
+        check(out[at[i]:at[i] + qlens[i]], want, tol, i)
+    assert torch.equal(out, c.prefill_attention(0, ids, qlens, q, prefix_ids=pre))
+    assert c.check_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype,code", [("fp16", "e4m3"), ("bf16", "int8"), ("fp16", "int8"), ("bf16", "e4m3")])
+@pytest.mark.parametrize("block,dim,hkv,r,n", [(64, 128, 2, 4, 3001), (128, 128, 1, 8, 1024), (32, 64, 3, 5, 515), (64, 64, 40, 1, 129),
+                                               (64, 128, 40, 2, 127), (128, 128, 2, 3, 1)])
+def test_prefill_with_the_prefix_in_front(dtype, code, block, dim, hkv, r, n):
+    """Prefixes in front of the sequences' own tokens, steps of both cut over thread blocks and segments taken whole, beside
+    sequences without one, for prompts whose last tokens only ask as well."""
+    dt = TYPES[dtype]
+    lens = [150, 61, 200, 33, 300, n, 95]
+    qlens = [150, 45, 7, 33, 129]
+    pre = [5, 5, None, 6, 5]
+    c = make(max_seqs=7, num_q_heads=hkv * r, num_kv_heads=hkv, head_dim=dim, block_tokens=block, code=code, dtype=dt)
+    k, v = fill(c, lens, dt, 940)
+    q = tokens(sum(qlens), hkv * r, dim, dt, 950, 0.3)
+    out = c.prefill_attention(0, range(5), qlens, q, prefix_ids=pre)
+    at = 0
+    for s in range(5):
+        rows = sorted({0, 1, qlens[s] // 2, qlens[s] - 2, qlens[s] - 1})
+        want, tol = want_of(q, at, k, v, pre[s], s, lens[s], qlens[s], block, code, dim)
+        check(out[at:at + qlens[s]][rows], want[rows], tol[rows], s)
+        at += qlens[s]
+    assert torch.equal(out, c.prefill_attention(0, range(5), qlens, q, prefix_ids=pre))
+    assert c.check_device_error() == 0
+
+
+@pytest.mark.parametrize("hkv", [2, 80])
+def test_non_finite_values_on_both_sides(hkv):
+    """Infinities in V of the prefix's last exact token, of an own token that only later queries see, and of another sequence's:
+    each in its channel of the rows that see it. Few segments, cut over thread blocks, and many, taken whole."""
+    c = make(max_seqs=3, num_q_heads=hkv, num_kv_heads=hkv, block_tokens=64)
+    lens = [150, 40, 700]  # two sequences, their prefix
+    k, v = (tokens(sum(lens), hkv, 128, torch.float16, s, 0.3) for s in (961, 962))
+    v[140, 1, 5] = float("inf")   # own position 140
+    v[155, 0, 9] = float("-inf")  # the other's own position 5
+    v[-1, 1, 77] = float("inf")
+    c.append(0, [0, 1, 2], lens, k, v)
+    q = tokens(160, hkv, 128, torch.float16, 963, 0.3)
+    out = c.prefill_attention(0, [0, 1], [150, 10], q, prefix_ids=[2, 2])
+    want = torch.zeros_like(out, dtype=torch.bool)
+    want[:, 1, 77] = True
+    want[140:150, 1, 5] = True
+    want[150:, 0, 9] = True
+    assert torch.equal(~torch.isfinite(out), want)
+    assert c.check_device_error() == 0
