@@ -465,6 +465,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     __syncthreads();
+    if (kMore) {
+        before_done();
+        start_next();
+    }
 
     // Copies run ahead of the work: a sealed tile takes one ring entry, an exact one two (K rows, V
     // channel rows), an empty sequence's unit none. The next tile's slot is loaded a step early.
@@ -477,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
         ahead.advance(p, ua);
         const TilePlace e = place_of(p, x, ahead.i, ua - ahead.begin);
         slot = -1;
-        if (e.tile < e.n >> c.log2_block << sh) slot = __ldg(block_table(c, e.seq) + (e.tile >> sh));
+        if (e.tile < e.n >> c.log2_block << sh) slot = read<kMore>(block_table(c, e.seq) + (e.tile >> sh));
     };
     auto entry = [&](const void* src, uint32_t bytes) {
         if (lane == 0) {
@@ -669,8 +673,12 @@ int launch(KVARN_PARAMS, cudaStream_t s) {
     static SmemOnce once;
     const int e = once.allow(reinterpret_cast<const void*>(decode_kernel<D, INT8, BF16, ALONE>), Shape<D>::kSmem);
     if (e) return e;
-    decode_kernel<D, INT8, BF16, ALONE><<<p.grid, kThreads, Shape<D>::kSmem, s>>>(KVARN_ARGS);
+#ifdef KVARN_BLOCK_MORE
+    return launch_behind(decode_kernel<D, INT8, BF16, ALONE>, p.grid, kThreads, Shape<D>::kSmem, s, p, x);
+#else
+    decode_kernel<D, INT8, BF16, ALONE><<<p.grid, kThreads, Shape<D>::kSmem, s>>>(p);
     return (int)cudaGetLastError();
+#endif
 }
 
 }  // namespace

@@ -26,6 +26,32 @@ struct SmemOnce {
     }
 };
 
+// A launch that may begin while the stream's kernel before it still runs: its thread blocks take the SMs as they get free and wait
+// (before_done) ahead of their first access to global memory, for the other to be complete and seen. All threads of all
+// thread blocks call it, so that a kernel behind finds every kernel before complete as well. start_next: from here on the next
+// kernel's thread blocks may come. What a kernel before may have written is read by plain loads (read<true>), since it is not
+// read-only for as long as this one runs.
+__device__ __forceinline__ void before_done() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void start_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+template <bool BEHIND, class T>
+__device__ __forceinline__ T read(const T* p) {
+    return BEHIND ? *p : __ldg(p);
+}
+template <class... Args>
+int launch_behind(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t s, const Args&... args) {
+    cudaLaunchAttribute early = {};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t config = {};
+    config.gridDim = grid;
+    config.blockDim = dim3(threads);
+    config.dynamicSmemBytes = smem;
+    config.stream = s;
+    config.attrs = &early;
+    config.numAttrs = 1;
+    return (int)cudaLaunchKernelEx(&config, kernel, args...);
+}
+
 __device__ __forceinline__ const int32_t* block_table(const BlockView& c, int seq) {
     return reinterpret_cast<const int32_t*>(c.base + c.lay.table) + ((size_t)seq * c.num_layers + c.layer) * c.max_blocks;
 }

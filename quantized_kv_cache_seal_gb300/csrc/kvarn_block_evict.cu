@@ -29,6 +29,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
     __shared__ int counts[kSelWarps][256];
     __shared__ int found[2];
     __shared__ int warp_sum[2][kSelWarps];
+    start_next();
     const BlockEvictSeq& e = p.seqs[blockIdx.y];
     const int h = blockIdx.x, t = threadIdx.x, w = t >> 5, lane = t & 31, full = e.full;
     int32_t* kept = p.kept + ((int64_t)e.row * p.c.hkv + h) * p.keep;
@@ -124,6 +125,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
 }
 
 __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constant__ BlockEvictParams p) {
+    before_done();
     const BlockEvictSeq& e = p.seqs[blockIdx.y];
     const int per = (p.c.block / kTileTokens) * tile_bytes(p.c.d) / 16;  // pieces of a head's record
     const int piece = blockIdx.x * kMoveThreads + threadIdx.x;
@@ -138,7 +140,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constan
         bool moves[kMoveAhead];
 #pragma unroll
         for (int z = 0; z < kMoveAhead; ++z) {
-            const int from = j0 + z < p.keep ? __ldg(kept + j0 + z) : j0 + z;
+            const int from = j0 + z < p.keep ? kept[j0 + z] : j0 + z;
             moves[z] = from != j0 + z;
             if (moves[z]) x[z] = pool[__ldg(table + from) * slot];
         }
@@ -155,7 +157,8 @@ int launch_block_evict(const BlockEvictParams& p, void* stream) {
     select_kernel<<<dim3(p.c.hkv, p.n_all), kSelThreads, 0, s>>>(p);
     if (p.n_seqs > 0) {
         const int pieces = p.c.hkv * ((p.c.block / kTileTokens) * tile_bytes(p.c.d) / 16);
-        move_kernel<<<dim3((pieces + kMoveThreads - 1) / kMoveThreads, p.n_seqs), kMoveThreads, 0, s>>>(p);
+        const int rc = (int)cudaGetLastError();
+        return rc ? rc : launch_behind(move_kernel, dim3((pieces + kMoveThreads - 1) / kMoveThreads, p.n_seqs), kMoveThreads, 0, s, p);
     }
     return (int)cudaGetLastError();
 }

@@ -308,6 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1) flat_kernel(const __grid_constant
     tc_fence_after();
     // All of tensor memory is this CTA's, so it starts at address 0, and shared memory on 1024 bytes; both are counted on.
     // Were it ever not so, the launch would do nothing but say so.
+    start_next();
     const bool placed = *reinterpret_cast<volatile uint32_t*>(smem + Sh::kTmem) == 0 && (smem_addr(smem) & 1023) == 0;
     if (!placed && t == 0) atomicOr(err, kErrBadSlot);
     const Rings<D> rings = {smem + Sh::kRings, bars + kRaw, bars + kRaw + 2 * kExpWarps, reinterpret_cast<int32_t*>(smem + Sh::kWhat)};
@@ -365,6 +366,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
     __shared__ float factor[kMostParts][32];
     __shared__ float red[kJoinWarps][32];
     __shared__ uint32_t flags[kJoinWarps];
+    before_done();
+    start_next();
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, row = blockIdx.y * 32 + lane;
     int i = 0;
 #pragma unroll 1
@@ -441,8 +444,8 @@ int launch(const BlockFlatParams& p, int pairs, cudaStream_t s) {
     const int e = once.allow(reinterpret_cast<const void*>(flat_kernel<D, INT8, BF16>), Shape<D>::kSmem);
     if (e) return e;
     flat_kernel<D, INT8, BF16><<<p.grid, kThreads, Shape<D>::kSmem, s>>>(p);
-    join_kernel<D, BF16><<<dim3(pairs, 4, D / 32), 32 * kJoinWarps, 0, s>>>(p);
-    return (int)cudaGetLastError();
+    const int rc = (int)cudaGetLastError();
+    return rc ? rc : launch_behind(join_kernel<D, BF16>, dim3(pairs, 4, D / 32), 32 * kJoinWarps, 0, s, p);
 }
 
 }  // namespace

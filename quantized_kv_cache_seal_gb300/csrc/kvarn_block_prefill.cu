@@ -308,9 +308,9 @@ __device__ __forceinline__ void expand_role(const BlockPrefillParams& p, const M
     const int sh = c.log2_block - 5;
     const int t = lane & 3, kg = lane >> 2, vg = (lane >> 3) + (lane & 4);
     constexpr int kChunks = D / 16;  // 512-byte chunks of a part's K or V
-    auto load_k = [&](const uint8_t* rec, int i) { return __ldg(reinterpret_cast<const uint4*>(rec + 16 + i * 512) + lane); };
+    auto load_k = [&](const uint8_t* rec, int i) { return read<kMore>(reinterpret_cast<const uint4*>(rec + 16 + i * 512) + lane); };
     auto load_v = [&](const uint8_t* rec, int i) {
-        return __ldg(reinterpret_cast<const uint4*>(rec + 16 + kTileTokens * D + i * 512) + 4 * vg + t);
+        return read<kMore>(reinterpret_cast<const uint4*>(rec + 16 + kTileTokens * D + i * 512) + 4 * vg + t);
     };
     auto halves = [&](uint32_t u, uint32_t v) {  // 8 codes
         return make_uint4(codes_lo<INT8>(u), codes_hi<INT8>(u), codes_lo<INT8>(v), codes_hi<INT8>(v));
@@ -350,7 +350,7 @@ __device__ __forceinline__ void expand_role(const BlockPrefillParams& p, const M
                 else y -= before;
             }
             tile2 = (uint32_t)y;
-            if (y < n_of(who2) >> c.log2_block << sh) slot = __ldg(block_table(c, seq_of(who2)) + (y >> sh));
+            if (y < n_of(who2) >> c.log2_block << sh) slot = read<kMore>(block_table(c, seq_of(who2)) + (y >> sh));
             else tile2 |= 0x80000000u;
         }
         if (jj >= 0) {
@@ -403,7 +403,7 @@ __device__ __forceinline__ void expand_role(const BlockPrefillParams& p, const M
 #pragma unroll
                 for (int i = 0; i < kChunks; ++i) x[i] = load_k(rec1, i);
             }
-            hd = __ldg(reinterpret_cast<const float4*>(rec1));
+            hd = read<kMore>(reinterpret_cast<const float4*>(rec1));
         }
         who = who1;
         tile = tile1;
@@ -726,6 +726,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     const int t = threadIdx.x, w = t >> 5, lane = t & 31, wg = w >> 2;
     int32_t* err = reinterpret_cast<int32_t*>(p.c.base + p.c.lay.err);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Sh::kBars);
+    if (kMore) {  // (ahead of tensor memory, which the kernel before may hold)
+        before_done();
+        start_next();
+    }
     if (t == 0) {
         for (int k = 0; k < 4; ++k) {
             mbar_init(bars + kBarKFull + k, 128);
@@ -855,6 +859,8 @@ constexpr int kMoreRows = 4;
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kCombineThreads) combine_more_kernel(const __grid_constant__ BlockPrefillParams p KVARN_MORE_PARAM) {
     constexpr int R = kMoreRows;
+    before_done();
+    start_next();
     const int b = blockIdx.x, lane = threadIdx.x & 31;
     const int u0 = (int)((int64_t)p.steps * b / p.grid), u1 = (int)((int64_t)p.steps * (b + 1) / p.grid);
     LineWalk w(p, x, b);
@@ -956,13 +962,15 @@ int launch(KVARN_PARAMS, cudaStream_t s) {
     static SmemOnce once;
     const int e = once.allow(reinterpret_cast<const void*>(prefill_kernel<D, INT8, BF16>), Shape<D>::kSmem);
     if (e) return e;
-    prefill_kernel<D, INT8, BF16><<<p.grid, kThreads, Shape<D>::kSmem, s>>>(KVARN_ARGS);
 #ifdef KVARN_BLOCK_MORE
-    if (p.line) combine_more_kernel<D, BF16><<<dim3(p.grid, 256 / (kCombineThreads / 32 * kMoreRows)), kCombineThreads, 0, s>>>(p, x);
+    const int rc = launch_behind(prefill_kernel<D, INT8, BF16>, p.grid, kThreads, Shape<D>::kSmem, s, p, x);
+    if (rc || !p.line) return rc;
+    return launch_behind(combine_more_kernel<D, BF16>, dim3(p.grid, 256 / (kCombineThreads / 32 * kMoreRows)), kCombineThreads, 0, s, p, x);
 #else
+    prefill_kernel<D, INT8, BF16><<<p.grid, kThreads, Shape<D>::kSmem, s>>>(p);
     if (p.line) combine_kernel<D, BF16><<<dim3(p.grid, 256 / (kCombineThreads / 32)), kCombineThreads, 0, s>>>(p);
-#endif
     return (int)cudaGetLastError();
+#endif
 }
 
 }  // namespace

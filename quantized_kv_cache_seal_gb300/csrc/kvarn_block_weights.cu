@@ -224,6 +224,7 @@ __global__ void __launch_bounds__(kWinThreads, 1) window_kernel(const __grid_con
     tc_fence_after();
     // All of tensor memory is this CTA's, so it starts at address 0, and shared memory on 1024 bytes; both are counted on.
     // Were it ever not so, the launch would do nothing but say so.
+    start_next();
     const bool placed = *reinterpret_cast<volatile uint32_t*>(smem + Sh::kTmem) == 0 && (smem_addr(smem) & 1023) == 0;
     if (!placed && t == 0) atomicOr(err, kErrBadSlot);
     const Rings<D> rings = {smem + Sh::kRings, bars + kRaw, bars + kRaw + 2 * kWinExpand, reinterpret_cast<int32_t*>(smem + Sh::kWhat)};
@@ -277,6 +278,7 @@ __global__ void __launch_bounds__(kWeighThreads) weigh_kernel(const __grid_const
     __shared__ float2 some[kWeighThreads];
     __shared__ int2 ctas[kWeighRows / 128];
     __shared__ float got[WIDE ? 8 * kWeighThreads / 32 : 8 * kWeighThreads];  // of a block
+    before_done();
     const BlockWeighSeq& e = p.seqs[blockIdx.z];
     const int h = blockIdx.y, t = threadIdx.x, blocks = (e.tiles + (1 << p.log2_tiles) - 1) >> p.log2_tiles;
     const int first = blockIdx.x * p.blocks;
@@ -398,14 +400,9 @@ int launch_block_weigh(const BlockWeighParams& p, void* stream) {
         BlockWeighArgs<16> few;
         static_cast<BlockWeighHead&>(few) = p;
         for (int i = 0; i < p.n_seqs; ++i) few.seqs[i] = p.seqs[i];
-        if (p.lanes == 32) weigh_kernel<16, true><<<grid, kWeighThreads, 0, t>>>(few);
-        else weigh_kernel<16, false><<<grid, kWeighThreads, 0, t>>>(few);
-    } else if (p.lanes == 32) {
-        weigh_kernel<kBlockMaxSeqs, true><<<grid, kWeighThreads, 0, t>>>(p);
-    } else {
-        weigh_kernel<kBlockMaxSeqs, false><<<grid, kWeighThreads, 0, t>>>(p);
+        return launch_behind(p.lanes == 32 ? weigh_kernel<16, true> : weigh_kernel<16, false>, grid, kWeighThreads, 0, t, few);
     }
-    return (int)cudaGetLastError();
+    return launch_behind(p.lanes == 32 ? weigh_kernel<kBlockMaxSeqs, true> : weigh_kernel<kBlockMaxSeqs, false>, grid, kWeighThreads, 0, t, p);
 }
 
 }  // namespace kvarn
