@@ -29,6 +29,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
     __shared__ int counts[kSelWarps][256];
     __shared__ int found[2];
     __shared__ int warp_sum[2][kSelWarps];
+    before_done();
     start_next();
     const BlockEvictSeq& e = p.seqs[blockIdx.y];
     const int h = blockIdx.x, t = threadIdx.x, w = t >> 5, lane = t & 31, full = e.full;
@@ -154,13 +155,12 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constan
 
 int launch_block_evict(const BlockEvictParams& p, void* stream) {
     cudaStream_t s = (cudaStream_t)stream;
-    select_kernel<<<dim3(p.c.hkv, p.n_all), kSelThreads, 0, s>>>(p);
-    if (p.n_seqs > 0) {
+    const int rc = launch_behind(select_kernel, dim3(p.c.hkv, p.n_all), kSelThreads, 0, s, p);
+    if (rc == 0 && p.n_seqs > 0) {
         const int pieces = p.c.hkv * ((p.c.block / kTileTokens) * tile_bytes(p.c.d) / 16);
-        const int rc = (int)cudaGetLastError();
-        return rc ? rc : launch_behind(move_kernel, dim3((pieces + kMoveThreads - 1) / kMoveThreads, p.n_seqs), kMoveThreads, 0, s, p);
+        return launch_behind(move_kernel, dim3((pieces + kMoveThreads - 1) / kMoveThreads, p.n_seqs), kMoveThreads, 0, s, p);
     }
-    return (int)cudaGetLastError();
+    return rc;
 }
 
 }  // namespace kvarn

@@ -277,6 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1) flat_kernel(const __grid_constant
     const int t = threadIdx.x, w = t >> 5, lane = t & 31;
     int32_t* err = reinterpret_cast<int32_t*>(p.c.base + p.c.lay.err);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Sh::kBars);
+    start_next();
     if (t == 0) {
         for (int k = 0; k < kRing; ++k) {
             mbar_init(bars + kKFull + k, 128);
@@ -308,7 +309,6 @@ __global__ void __launch_bounds__(kThreads, 1) flat_kernel(const __grid_constant
     tc_fence_after();
     // All of tensor memory is this CTA's, so it starts at address 0, and shared memory on 1024 bytes; both are counted on.
     // Were it ever not so, the launch would do nothing but say so.
-    start_next();
     const bool placed = *reinterpret_cast<volatile uint32_t*>(smem + Sh::kTmem) == 0 && (smem_addr(smem) & 1023) == 0;
     if (!placed && t == 0) atomicOr(err, kErrBadSlot);
     const Rings<D> rings = {smem + Sh::kRings, bars + kRaw, bars + kRaw + 2 * kExpWarps, reinterpret_cast<int32_t*>(smem + Sh::kWhat)};
@@ -443,6 +443,7 @@ int launch(const BlockFlatParams& p, int pairs, cudaStream_t s) {
     static SmemOnce once;
     const int e = once.allow(reinterpret_cast<const void*>(flat_kernel<D, INT8, BF16>), Shape<D>::kSmem);
     if (e) return e;
+    // (not behind the kernel before: 117 us for the call where it takes 110)
     flat_kernel<D, INT8, BF16><<<p.grid, kThreads, Shape<D>::kSmem, s>>>(p);
     const int rc = (int)cudaGetLastError();
     return rc ? rc : launch_behind(join_kernel<D, BF16>, dim3(pairs, 4, D / 32), 32 * kJoinWarps, 0, s, p);

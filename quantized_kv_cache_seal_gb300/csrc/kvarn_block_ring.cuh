@@ -225,7 +225,7 @@ __device__ __forceinline__ void fill_rings(const P& p, const Rings<D>& rings, in
         if (!more) return a;
         const auto& e = p.seqs[w.i];
         a = Part{e.seq, e.n, w.h, 4 * j + wp, -1};
-        if (a.tile < e.n >> c.log2_block << sh) a.slot = __ldg(block_table(c, e.seq) + (a.tile >> sh));
+        if (a.tile < e.n >> c.log2_block << sh) a.slot = read<true>(block_table(c, e.seq) + (a.tile >> sh));
         skip();
         if (!SIDES) skip();
         return a;

@@ -198,6 +198,8 @@ __global__ void __launch_bounds__(kWinThreads, 1) window_kernel(const __grid_con
     const int t = threadIdx.x, w = t >> 5, lane = t & 31;
     int32_t* err = reinterpret_cast<int32_t*>(p.c.base + p.c.lay.err);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Sh::kBars);
+    before_done();  // (ahead of tensor memory, which the kernel before may hold)
+    start_next();
     if (t == 0) {
         for (int k = 0; k < kWinRing; ++k) {
             mbar_init(bars + kKFull + k, 128);
@@ -224,7 +226,6 @@ __global__ void __launch_bounds__(kWinThreads, 1) window_kernel(const __grid_con
     tc_fence_after();
     // All of tensor memory is this CTA's, so it starts at address 0, and shared memory on 1024 bytes; both are counted on.
     // Were it ever not so, the launch would do nothing but say so.
-    start_next();
     const bool placed = *reinterpret_cast<volatile uint32_t*>(smem + Sh::kTmem) == 0 && (smem_addr(smem) & 1023) == 0;
     if (!placed && t == 0) atomicOr(err, kErrBadSlot);
     const Rings<D> rings = {smem + Sh::kRings, bars + kRaw, bars + kRaw + 2 * kWinExpand, reinterpret_cast<int32_t*>(smem + Sh::kWhat)};
@@ -373,8 +374,7 @@ int launch(const BlockWindowParams& p, cudaStream_t s) {
     static SmemOnce once;
     const int e = once.allow(reinterpret_cast<const void*>(window_kernel<D, INT8, BF16>), WinShape<D>::kSmem);
     if (e) return e;
-    window_kernel<D, INT8, BF16><<<p.grid, kWinThreads, WinShape<D>::kSmem, s>>>(p);
-    return (int)cudaGetLastError();
+    return launch_behind(window_kernel<D, INT8, BF16>, p.grid, kWinThreads, WinShape<D>::kSmem, s, p);
 }
 
 }  // namespace
