@@ -418,3 +418,44 @@ def test_non_finite_values_on_both_sides(hkv):
     want[150:, 0, 9] = True
     assert torch.equal(~torch.isfinite(out), want)
     assert c.check_device_error() == 0
+
+
+@pytest.mark.parametrize("first", ["nothing", "copy", "other stream", "both"])
+def test_captured_behind_other_work(first):
+    """A graph whose first kernel is an attention call's, or that has a copy, another stream's work or both right before it."""
+    c = make(max_seqs=10, num_q_heads=8, num_kv_heads=2)
+    fill(c, [40 + 30 * i for i in range(9)] + [700], torch.float16, 970)
+    ids, pre = list(range(9)), [9] * 4 + [None] + [9] * 4
+    given = tokens(45, 8, 128, torch.float16, 980, 0.3)
+    q, w, more = torch.empty_like(given), c.new_weights()[0], torch.zeros(1 << 22, device="cuda")
+
+    def calls():
+        return (c.decode_attention(0, ids, q[:9], prefix_ids=pre, weights=w), c.prefill_attention(0, ids, [5] * 9, q, prefix_ids=pre))
+
+    q.copy_(given)
+    want = [x.clone() for x in calls()] + [w.clone()]
+    torch.cuda.synchronize()
+    s, t, g = torch.cuda.Stream(), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        if first in ("other stream", "both"):
+            t.wait_stream(s)
+            with torch.cuda.stream(t):
+                for _ in range(4):
+                    more.add_(1)
+                q.copy_(given)
+            if first == "both":
+                w.zero_()
+            s.wait_stream(t)
+        elif first == "copy":
+            q.copy_(given)
+        got = calls()
+    for _ in range(3):
+        w.zero_()
+        if first != "nothing":
+            q.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            g.replay()
+        s.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip((*got, w), want))
+    assert c.check_device_error() == 0
