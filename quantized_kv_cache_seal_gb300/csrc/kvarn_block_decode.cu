@@ -329,7 +329,10 @@ __device__ void join_heads(const BlockDecodeParams& p, const More& x, const uint
         float4 y = make_float4(o.x * u * inv, o.y * u * inv, o.z * u * inv, o.w * u * inv);
         if (kMore && x.totals && lane == 0) {  // a prefix's 2^lse in units of l
             float2 t = make_float2(m, l);
-            if (merged) t = joined(t, make_float2(x.pre_lse[row + head] + (kShift - 12.f), 1.f));
+            if (merged) {  // (nothing where every logit of it is -inf)
+                const float pre = x.pre_lse[row + head];
+                t = joined(t, make_float2(pre + (kShift - 12.f), pre == kNegInf ? 0.f : 1.f));
+            }
             x.totals[row + head] = t;
         }
         if (kMore && merged) {  // with the finished row over the shared prefix
