@@ -119,7 +119,7 @@ constexpr int kPairCost = 8;
 struct BlockDecodeMore {
     int32_t alone;             // 1: the line is cut over the warps
     float2* sums;              // [units][r] or null: maximum and sum of each tile's weights, by head
-    float2* totals;            // [rows][Hq] (with sums): of each row over all its keys, a prefix's among them
+    float2* totals;            // [rows][Hq] (with sums): of each row over all its keys, a prefix's among them; where merged says, it holds the prefix's before
     const float *pre_o, *pre_lse;  // rows finished over shared prefixes (pre_lse null: none), [rows][Hq][D] and [rows][Hq]
     uint32_t merged[kBlockMaxSeqs / 32];  // bit i: sequence entry i takes its row from there
     int32_t pre[kBlockMaxSeqs], pre_n[kBlockMaxSeqs];  // sequence whose pre_n tokens come before entry i's own (0: none)
@@ -146,6 +146,7 @@ struct BlockPrefillParams {
 struct BlockPrefillMore {
     int32_t flat;        // 1: every query sees all of the entry's n tokens, and finished rows go to pre_o and pre_lse
     float *pre_o, *pre_lse;  // f32 [rows][Hq][D], [rows][Hq]: written if flat; else added where merged says
+    float2* totals;      // [rows][Hq] or null, if flat: a row's maximum and sum, in decode's units
     uint32_t merged[kBlockMaxSeqs / 32];  // bit i: entry i
     int32_t pre[kBlockMaxSeqs];    // a prefix whose steps come first in the segments of entry i (not if flat)
     int32_t pre_n[kBlockMaxSeqs];  // its tokens, 0: none
@@ -169,6 +170,7 @@ struct BlockFlatParams {
     const uint16_t* q;
     float* parts;            // [pairs + grid][2][128 (D + 3)]
     float *pre_o, *pre_lse;  // f32 [rows][Hq][D], [rows][Hq]
+    float2* totals;          // [rows][Hq] or null: a row's maximum and sum, in decode's units
     int32_t n_seqs, hq, r, grid;
     int64_t units;           // steps of all sequences, KV heads and row tiles
     float scale_log2;

@@ -51,7 +51,7 @@ struct More {
 #endif
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr float kShift = 15.f;  // weights are at most 2^15
+constexpr float kShift = 15.f;  // weights are at most 2^15 (total_of counts on it)
 
 template <int D>
 struct Shape {
@@ -327,12 +327,9 @@ __device__ void join_heads(const BlockDecodeParams& p, const More& x, const uint
     auto give = [&](int head, float4 o, float m, float l) {
         const float inv = l == 0.f ? 0.f : 1.f / l, u = kDenomUnit;
         float4 y = make_float4(o.x * u * inv, o.y * u * inv, o.z * u * inv, o.w * u * inv);
-        if (kMore && x.totals && lane == 0) {  // a prefix's 2^lse in units of l
+        if (kMore && x.totals && lane == 0) {
             float2 t = make_float2(m, l);
-            if (merged) {  // (nothing where every logit of it is -inf)
-                const float pre = x.pre_lse[row + head];
-                t = joined(t, make_float2(pre + (kShift - 12.f), pre == kNegInf ? 0.f : 1.f));
-            }
+            if (merged) t = joined(t, x.totals[row + head]);
             x.totals[row + head] = t;
         }
         if (kMore && merged) {  // with the finished row over the shared prefix

@@ -199,6 +199,12 @@ __device__ __forceinline__ int warp_exponent_v(uint32_t top) {
 __device__ __forceinline__ float lse_of(float m, float l, float shift) {
     return l == 0.f ? kNegInf : log2f(l) + (m - shift + 12.f);
 }
+// The sum itself, as a maximum and a denominator with decode's shift of 15. No logarithm: one word of it would be rounded at
+// the logits' size. (Denominators near fp32's end, of V scales near 2^-100, keep some powers of two in the maximum.)
+__device__ __forceinline__ float2 total_of(float m, float l, float shift) {
+    const int up = l > power2(100) ? 32 : 0;
+    return make_float2(m + (float)up, l * power2(15 - (int)shift - up));
+}
 // A row over some keys and the row over others make the row over all of them: their shares, from the log2 of their
 // sums; zeros where there are no keys on either side. NaN stays.
 __device__ __forceinline__ float2 merge_factors(float a, float b) {

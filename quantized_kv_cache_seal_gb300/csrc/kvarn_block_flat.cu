@@ -410,7 +410,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
     const int all = tile * 128 + row;
     if (all >= e.rows) return;
     const size_t out = (size_t)(e.q_row + all / p.r) * p.hq + h * p.r + all % p.r;
-    if (w == 0 && blockIdx.z == 0) p.pre_lse[out] = lse_of(m, l, kShift);
+    if (w == 0 && blockIdx.z == 0) {
+        p.pre_lse[out] = lse_of(m, l, kShift);
+        if (p.totals) p.totals[out] = total_of(m, l, kShift);
+    }
     const float inv = kDenomUnit * (l == 0.f ? 0.f : 1.f / l);
     {
         static_assert(kJoinWarps * 4 == 32, "channels of a CTA");

@@ -297,7 +297,7 @@ struct Beside {
     const int32_t* before = nullptr;   // a prefix whose tokens come first in the sequence's line, -1 for none
     const uint8_t* finished = nullptr; // 1: its rows over a prefix are in pre_o and pre_lse
     float *pre_o = nullptr, *pre_lse = nullptr;
-    float2 *sums = nullptr, *totals = nullptr;  // decode: the tiles' sums, the rows'
+    float2 *sums = nullptr, *totals = nullptr;  // decode: the tiles' sums, the rows' (the prefixes' pass leaves its part there)
     float* weights = nullptr;          // decode: what the blocks have received, added to
 };
 
@@ -473,6 +473,7 @@ kvarn_status run_flat(kvarn_block_cache* c, int32_t layer, int32_t n_entries, co
     p.parts = (float*)(c->view.base + c->view.lay.partials);
     p.pre_o = beside.pre_o;
     p.pre_lse = beside.pre_lse;
+    p.totals = beside.totals;
     p.n_seqs = n_entries;
     p.hq = c->cfg.num_q_heads;
     p.r = c->r;
@@ -538,6 +539,7 @@ kvarn_status run_tiles(kvarn_block_cache* c, int32_t layer, int32_t n_entries, c
     x.flat = flat;
     x.pre_o = beside.pre_o;
     x.pre_lse = beside.pre_lse;
+    x.totals = flat ? beside.totals : nullptr;
     mark(x.merged, finished, p.n_seqs);
     // Whole segments, the longest first, end when the longest does or the SMs have shared out all;
     // the line of all steps cut evenly ends a share of the steps later, and then costs about four more
@@ -759,6 +761,11 @@ kvarn_status run_attend(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, con
     for (int g = 0; g < n_groups; ++g)
         if (walked(g)) groups[n_once++] = groups[g];
     Beside b;
+    if (weights) {
+        b.weights = weights;
+        b.sums = (float2*)((uint8_t*)workspace + w.sums);
+        b.totals = (float2*)((uint8_t*)workspace + w.totals);
+    }
     if (n_once > 0) {
         b.pre_o = (float*)((uint8_t*)workspace + w.pre_o);
         b.pre_lse = (float*)((uint8_t*)workspace + w.pre_lse);
@@ -770,11 +777,6 @@ kvarn_status run_attend(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, con
         if (finished[i]) before[i] = -1;
     if (std::any_of(before, before + n, [](int32_t pre) { return pre >= 0; }) || single) b.before = before;
     if (!single) return run_prefill(c, layer, n, one, lens, q, out, scale, stream, b);
-    if (weights) {
-        b.weights = weights;
-        b.sums = (float2*)((uint8_t*)workspace + w.sums);
-        b.totals = (float2*)((uint8_t*)workspace + w.totals);
-    }
     return run_decode(c, layer, n, one, q, out, scale, stream, b);
 }
 

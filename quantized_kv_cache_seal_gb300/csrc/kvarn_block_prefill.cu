@@ -53,6 +53,7 @@ constexpr bool kMore = false;
 struct More {
     int32_t flat;
     float *pre_o, *pre_lse;
+    float2* totals;
     uint32_t merged[1];
     int32_t pre[1], pre_n[1];
 };
@@ -680,6 +681,7 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, const 
             if (__builtin_expect(bad, 0) && valid)
                 add_non_finite<D, BF16>(p.c, e.seq, e.n, w.s.kvh, 0, pos + 1, nullptr, x.pre_o + (size_t)row * D);
             if (valid) x.pre_lse[row] = lse_of(m, l, kShift);
+            if (valid && x.totals) x.totals[row] = total_of(m, l, kShift);
         } else {
             float* part = reinterpret_cast<float*>(p.c.base + p.c.lay.partials) +
                           (size_t)(2 * blockIdx.x + (w.s.j0 == 0 ? 1 : 0)) * (256 * (D + 2));
@@ -938,6 +940,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_more_kernel(const __g
         if (x.flat) {
             if (live) *reinterpret_cast<float4*>(x.pre_o + row[i] * D + 4 * lane) = v;
             if (lane == 0) x.pre_lse[row[i]] = lse;
+            if (lane == 0 && x.totals) x.totals[row[i]] = total_of(big[i], l[i], kShift);
             continue;
         }
         if (merged) {
