@@ -444,11 +444,21 @@ kvarn_status kvarn_block_window_workspace(kvarn_block_cache* cache, int32_t laye
                                           const int32_t* q_lens, size_t* bytes);
 
 /* Add the weights that the last q_lens[i] <= 128 tokens of each sequence give to its blocks, each over the tokens at
- * positions up to its own: what the end of a prompt needs of it. q: [sum(q_lens)][num_q_heads][head_dim], their queries.
+ * positions up to its own, of its sequence alone: what the end of a prompt needs of it. q: [sum(q_lens)][num_q_heads][head_dim], their queries.
  * Reads K alone. Can be captured. */
 kvarn_status kvarn_block_window_weights(kvarn_block_cache* cache, int32_t layer, int32_t n_seqs, const int32_t* seq_ids,
                                         const int32_t* q_lens, const void* q, float softmax_scale, float* weights,
                                         void* workspace, size_t workspace_bytes, void* stream);
+
+/* The same two behind prefixes (NULL: none): the softmax is that over prefix and sequence, as in kvarn_block_attend, so that what
+ * the end of a prompt adds and what later steps behind the same prefix add are shares of the same. */
+kvarn_status kvarn_block_window_workspace_prefixes(kvarn_block_cache* cache, int32_t layer, int32_t n_seqs,
+                                                   const int32_t* seq_ids, const int32_t* prefix_ids, const int32_t* q_lens,
+                                                   size_t* bytes);
+kvarn_status kvarn_block_window_weights_prefixes(kvarn_block_cache* cache, int32_t layer, int32_t n_seqs,
+                                                 const int32_t* seq_ids, const int32_t* prefix_ids, const int32_t* q_lens,
+                                                 const void* q, float softmax_scale, float* weights, void* workspace,
+                                                 size_t workspace_bytes, void* stream);
 
 /* Cut each sequence's full blocks in `layer` to `keep` where it has more: every KV head keeps its first `first` and last
  * `last` blocks (first + last <= keep) and, of the others, those with the largest weights (ties: the lowest index; NaN below

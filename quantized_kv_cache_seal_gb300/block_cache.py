@@ -141,8 +141,7 @@ class BlockCache:
 
     def _attend(self, layer, seq_ids, prefix_ids, counts, q, out, scale, weights, stream, k=None, ks=0, v=None, vs=0):
         """The calls with prefixes or weights; counts: queries of each sequence (None: one), or tokens to append if k."""
-        if prefix_ids is not None and None in prefix_ids:
-            prefix_ids = [-1 if x is None else x for x in prefix_ids]
+        prefix_ids = _prefixes(prefix_ids)
         if weights is not None:
             self._weights(weights)
         with K.on_device(self.device, stream) as s:
@@ -258,17 +257,20 @@ class BlockCache:
         return out
 
     def window_weights(self, layer: int, seq_ids: Sequence[int], q_lens: Sequence[int], q: torch.Tensor,
-                       weights: torch.Tensor, scale: Optional[float] = None, stream=None):
+                       weights: torch.Tensor, scale: Optional[float] = None, stream=None,
+                       prefix_ids: Optional[Sequence[Optional[int]]] = None):
         """Add to ``weights`` what the last q_lens[i] (128 at most) tokens of each sequence give its blocks, each over
-        the tokens up to its own; q: [sum(q_lens)][Hq][D], their queries."""
+        the tokens up to its own, behind those of its prefix; q: [sum(q_lens)][Hq][D], their queries. Name the prefixes that the
+        sequences are attended with: shares of another softmax do not compare with those of ``decode_attention``."""
         _same_length(seq_ids, q_lens)
         self._dense(q, sum(q_lens), "q")
         self._weights(weights)
+        prefix_ids = _prefixes(prefix_ids)
         with K.on_device(self.device, stream) as s:
             scale = self.scale if scale is None else scale
-            self._in_space(stream, lambda space, n: K.kvarn_block_window_weights(self.handle, layer, seq_ids, q_lens, q, scale,
-                                                                                 weights, space, n, s),
-                           lambda: K.kvarn_block_window_workspace(self.handle, layer, seq_ids, q_lens))
+            self._in_space(stream, lambda space, n: K.kvarn_block_window_weights_prefixes(
+                self.handle, layer, seq_ids, prefix_ids, q_lens, q, scale, weights, space, n, s),
+                           lambda: K.kvarn_block_window_workspace_prefixes(self.handle, layer, seq_ids, prefix_ids, q_lens))
             self._used(stream, s, q, weights)
 
     def evict(self, layer: int, seq_ids: Sequence[int], weights: torch.Tensor, keep: int, first: int = 1, last: int = 1,
@@ -298,6 +300,11 @@ class BlockCache:
         with K.on_device(self.device, stream) as s:
             self._used(stream, s)
             return K.kvarn_block_check_device_error(self.handle, s)
+
+
+def _prefixes(ids):
+    """One prefix a sequence as the library takes them: -1 for none."""
+    return [-1 if x is None else x for x in ids] if ids is not None and None in ids else ids
 
 
 def _same_length(seq_ids, counts):

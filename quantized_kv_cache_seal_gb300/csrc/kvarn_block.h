@@ -158,10 +158,11 @@ struct BlockRowsSeq {
     int32_t rows;        // q_len * r
     int32_t pad;         // rows rounded up to 8 (window)
     int32_t row_tiles;   // of 128 rows
-    int32_t steps;       // of 128 of its tokens
+    int32_t steps;       // of 128 tokens
     int32_t unit_begin;  // prefix of Hkv * row_tiles * steps
     int32_t pair_begin;  // prefix of Hkv * row_tiles
     int64_t sum_begin;   // prefix of Hkv * tiles * pad (window)
+    int32_t pre, pre_n;  // window: sequence whose pre_n tokens the rows see before its own, in steps of their own (0: none)
 };
 
 // Queries of all sequences behind a shared prefix, which see all of it.
@@ -197,7 +198,7 @@ struct BlockWeighSeq {
     int32_t before, tiles;    // tiles of a prefix in front, its own
     int32_t stride;           // places for them
     int32_t row;              // decode: of totals
-    int32_t unit_begin, pair_begin;  // window: as there
+    int32_t unit_begin, pair_begin, steps;  // window: as there
     int64_t sum_begin;
 };
 struct BlockWeighHead {

@@ -401,7 +401,7 @@ kvarn_status run_decode(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, con
         s.tiles = e.units - s.before - (x.alone ? kPairCost : 0);
         s.stride = e.units;
         s.row = i;
-        s.unit_begin = s.pair_begin = 0;
+        s.unit_begin = s.pair_begin = s.steps = 0;
         s.sum_begin = (int64_t)e.unit_begin * c->r;
     }
     return run_weigh(c, wp, stream);
@@ -575,17 +575,28 @@ kvarn_status run_tiles(kvarn_block_cache* c, int32_t layer, int32_t n_entries, c
 // ---- prefixes and weights ----
 
 // The prefix of each sequence (-1 for none) and that none of them is a sequence of the call.
-kvarn_status check_prefixes(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* ids, const int32_t* prefix_ids,
-                            const int32_t* q_lens, const int32_t* added) {
+kvarn_status check_prefix_ids(kvarn_block_cache* c, int32_t n_seqs, const int32_t* ids, const int32_t* prefix_ids) {
     if (!prefix_ids) return KVARN_OK;
     kvarn_status st = KVARN_OK;
     for (int i = 0; i < n_seqs; ++i) c->seen[ids[i]] = 1;
-    int64_t tiles = 0, steps = 0;
     for (int i = 0; i < n_seqs && !st; ++i) {
         const int32_t pre = prefix_ids[i];
         if (pre < -1 || pre >= c->cfg.max_seqs) st = fail(KVARN_EINVAL, "no such prefix");
         else if (pre >= 0 && c->seen[pre]) st = fail(KVARN_EINVAL, "a prefix is a sequence of the call");
-        if (st) break;
+    }
+    for (int i = 0; i < n_seqs; ++i) c->seen[ids[i]] = 0;
+    return st;
+}
+
+// The prefixes of an attention call, and that its work with them can be counted.
+kvarn_status check_prefixes(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* ids, const int32_t* prefix_ids,
+                            const int32_t* q_lens, const int32_t* added) {
+    if (!prefix_ids) return KVARN_OK;
+    kvarn_status st = check_prefix_ids(c, n_seqs, ids, prefix_ids);
+    if (st) return st;
+    int64_t tiles = 0, steps = 0;
+    for (int i = 0; i < n_seqs; ++i) {
+        const int32_t pre = prefix_ids[i];
         const int64_t own = c->L(ids[i], layer) + (added ? (int64_t)added[i] : 0), most_pairs = head_pairs(c, q_lens ? q_lens[i] : 1);
         tiles += head_tiles(own);
         steps += most_pairs * ((own + 127) / 128);
@@ -594,10 +605,9 @@ kvarn_status check_prefixes(kvarn_block_cache* c, int32_t layer, int32_t n_seqs,
         tiles += tiles_of(n);
         steps += most_pairs * ((n + 127) / 128);
     }
-    for (int i = 0; i < n_seqs; ++i) c->seen[ids[i]] = 0;
-    if (!st && (tiles + n_seqs * (1 + kPairCost)) * c->cfg.num_kv_heads >= 1ll << 31) st = fail(KVARN_ECAPACITY, "2^31 tiles of 32 tokens or more in a call");
-    if (!st && steps * c->cfg.num_kv_heads >= 1ll << 31) st = fail(KVARN_ECAPACITY, "2^31 steps of 128 keys or more in a call");
-    return st;
+    if ((tiles + n_seqs * (1 + kPairCost)) * c->cfg.num_kv_heads >= 1ll << 31) return fail(KVARN_ECAPACITY, "2^31 tiles of 32 tokens or more in a call");
+    if (steps * c->cfg.num_kv_heads >= 1ll << 31) return fail(KVARN_ECAPACITY, "2^31 steps of 128 keys or more in a call");
+    return KVARN_OK;
 }
 
 // The parts of an attention call's workspace.
@@ -662,9 +672,9 @@ kvarn_status check_attend(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, c
     return check_beside(c, rows, q, out, weights, workspace, bytes, *w);
 }
 
-// The line of a window_weights call and its workspace.
-kvarn_status plan_window(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* ids, const int32_t* q_lens,
-                         BlockWindowParams& p, Workspace* w) {
+// The line of a window_weights call and its workspace. (Prefixes are known to be sequences of the cache.)
+kvarn_status plan_window(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* ids, const int32_t* prefix_ids,
+                         const int32_t* q_lens, BlockWindowParams& p, Workspace* w) {
     const int hkv = c->cfg.num_kv_heads;
     int64_t rows = 0, units = 0, pairs = 0, sums = 0;
     p.n_seqs = 0;
@@ -681,7 +691,9 @@ kvarn_status plan_window(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, co
             e.rows = (int32_t)m * c->r;
             e.pad = (e.rows + 7) / 8 * 8;
             e.row_tiles = (e.rows + 127) / 128;
-            e.steps = (int32_t)((n + 127) / 128);
+            e.pre = prefix_ids ? prefix_ids[i] : -1;
+            e.pre_n = e.pre >= 0 ? c->L(e.pre, layer) : 0;
+            e.steps = (int32_t)(key_steps(e.pre_n) + key_steps(n));
             e.unit_begin = (int32_t)units;
             e.pair_begin = (int32_t)pairs;
             e.sum_begin = sums;
@@ -1002,15 +1014,21 @@ kvarn_status kvarn_block_append_attend(kvarn_block_cache* c, int32_t layer, int3
 
 kvarn_status kvarn_block_window_workspace(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* seq_ids,
                                           const int32_t* q_lens, size_t* bytes) {
+    return kvarn_block_window_workspace_prefixes(c, layer, n_seqs, seq_ids, nullptr, q_lens, bytes);
+}
+
+kvarn_status kvarn_block_window_workspace_prefixes(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* seq_ids,
+                                                   const int32_t* prefix_ids, const int32_t* q_lens, size_t* bytes) {
     if (!c || !bytes) return fail(KVARN_EINVAL, "no cache, or no place for the size");
     if (layer < 0 || layer >= c->cfg.num_layers) return fail(KVARN_EINVAL, "no such layer");
     if (n_seqs < 0 || (n_seqs > 0 && (!seq_ids || !q_lens))) return fail(KVARN_EINVAL, "bad sequence list");
     if (n_seqs > kBlockMaxSeqs) return fail(KVARN_ECAPACITY, "more than 256 sequences in a call");
     for (int i = 0; i < n_seqs; ++i)
-        if (seq_ids[i] < 0 || seq_ids[i] >= c->cfg.max_seqs) return fail(KVARN_EINVAL, "a sequence id is out of range");
+        if (seq_ids[i] < 0 || seq_ids[i] >= c->cfg.max_seqs || (prefix_ids && (prefix_ids[i] < -1 || prefix_ids[i] >= c->cfg.max_seqs)))
+            return fail(KVARN_EINVAL, "a sequence id is out of range");
     static thread_local BlockWindowParams p;
     Workspace w;
-    const kvarn_status st = plan_window(c, layer, n_seqs, seq_ids, q_lens, p, &w);
+    const kvarn_status st = plan_window(c, layer, n_seqs, seq_ids, prefix_ids, q_lens, p, &w);
     if (st == KVARN_OK) *bytes = w.total;
     return st;
 }
@@ -1018,6 +1036,14 @@ kvarn_status kvarn_block_window_workspace(kvarn_block_cache* c, int32_t layer, i
 kvarn_status kvarn_block_window_weights(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* seq_ids,
                                         const int32_t* q_lens, const void* q, float softmax_scale, float* weights,
                                         void* workspace, size_t workspace_bytes, void* stream) {
+    return kvarn_block_window_weights_prefixes(c, layer, n_seqs, seq_ids, nullptr, q_lens, q, softmax_scale, weights, workspace,
+                                               workspace_bytes, stream);
+}
+
+kvarn_status kvarn_block_window_weights_prefixes(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* seq_ids,
+                                                 const int32_t* prefix_ids, const int32_t* q_lens, const void* q,
+                                                 float softmax_scale, float* weights, void* workspace, size_t workspace_bytes,
+                                                 void* stream) {
     kvarn_status st = check_call(c, layer, n_seqs, seq_ids, stream, false);
     if (st) return st;
     if (!std::isfinite(softmax_scale * kLog2e)) return fail(KVARN_EINVAL, "softmax_scale must be finite, below 2^127");
@@ -1025,7 +1051,9 @@ kvarn_status kvarn_block_window_weights(kvarn_block_cache* c, int32_t layer, int
     static thread_local BlockWindowParams p;
     static thread_local BlockWeighParams wp;
     Workspace w;
-    st = plan_window(c, layer, n_seqs, seq_ids, q_lens, p, &w);
+    st = check_prefix_ids(c, n_seqs, seq_ids, prefix_ids);
+    if (st) return st;
+    st = plan_window(c, layer, n_seqs, seq_ids, prefix_ids, q_lens, p, &w);
     if (st || p.n_seqs == 0) return st;
     if (!q || !aligned16(q)) return fail(KVARN_EINVAL, "q must be 16-byte aligned");
     if (!weights) return fail(KVARN_EINVAL, "no weights");
@@ -1050,7 +1078,7 @@ kvarn_status kvarn_block_window_weights(kvarn_block_cache* c, int32_t layer, int
     wp.n_seqs = p.n_seqs;
     for (int i = 0; i < p.n_seqs; ++i) {
         const BlockRowsSeq& e = p.seqs[i];
-        wp.seqs[i] = BlockWeighSeq{e.seq, e.rows, e.pad, 0, tiles_of(e.n), tiles_of(e.n), 0, e.unit_begin, e.pair_begin, e.sum_begin};
+        wp.seqs[i] = BlockWeighSeq{e.seq, e.rows, e.pad, 0, tiles_of(e.n), tiles_of(e.n), 0, e.unit_begin, e.pair_begin, e.steps, e.sum_begin};
     }
     return run_weigh(c, wp, stream);
 }

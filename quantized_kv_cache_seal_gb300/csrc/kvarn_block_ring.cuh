@@ -225,7 +225,12 @@ __device__ __forceinline__ void fill_rings(const P& p, const Rings<D>& rings, in
         if (!more) return a;
         const auto& e = p.seqs[w.i];
         a = Part{e.seq, e.n, w.h, 4 * j + wp, -1};
-        if (a.tile < e.n >> c.log2_block << sh) a.slot = read<true>(block_table(c, e.seq) + (a.tile >> sh));
+        if (!SIDES && e.pre_n > 0) {
+            const int before = (e.pre_n + 127) / 128;
+            if (j < before) a.seq = e.pre, a.n = e.pre_n;
+            else a.tile -= 4 * before;
+        }
+        if (a.tile < a.n >> c.log2_block << sh) a.slot = read<true>(block_table(c, a.seq) + (a.tile >> sh));
         skip();
         if (!SIDES) skip();
         return a;

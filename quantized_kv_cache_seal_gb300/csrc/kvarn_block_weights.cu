@@ -128,7 +128,7 @@ __device__ __forceinline__ void win_softmax(const BlockWindowParams& p, uint8_t*
         const BlockRowsSeq& e = p.seqs[w.i];
         const int row = w.tile * 128 + et, tiles = (e.n + kTileTokens - 1) / kTileTokens, pad = e.pad;
         const bool valid = row < e.rows;
-        const int pos = valid ? e.n - e.q_len + row / p.r : e.n - 1;
+        const int pos = valid ? e.n - e.q_len + row / p.r : e.n - 1, before = (e.pre_n + kWinStep - 1) / kWinStep;
         float2* out = p.sums + e.sum_begin + (int64_t)w.h * tiles * pad + row;
         float2 total = make_float2(kNegInf, 0.f);
         float qs = 1.f;
@@ -147,7 +147,7 @@ __device__ __forceinline__ void win_softmax(const BlockWindowParams& p, uint8_t*
             bar_wait(bars + kSFull + (kk & 3), (uint32_t)(kk >> 2 & 1), err);
             __syncwarp();
             tc_fence_after();
-            const int lim = pos + 1 - j * kWinStep;  // visible columns
+            const int lim = j < before ? e.pre_n - j * kWinStep : pos + 1 - (j - before) * kWinStep;  // visible columns
             const bool plain = __all_sync(0xffffffffu, lim >= kWinStep);
             // (rolled: unrolled, the roles together would not fit the instruction cache)
 #pragma unroll 1
@@ -180,7 +180,8 @@ __device__ __forceinline__ void win_softmax(const BlockWindowParams& p, uint8_t*
                 }
                 s0 = __fadd2_rn(s0, s1);
                 const float2 part = make_float2(m, s0.x + s0.y);
-                if (valid && 4 * j + ch < tiles) out[(int64_t)(4 * j + ch) * pad] = part;
+                const int tile = 4 * (j - before) + ch;  // (of a prefix nothing is noted but the rows' totals)
+                if (valid && (unsigned)tile < (unsigned)tiles) out[(int64_t)tile * pad] = part;
                 total = joined(total, part);
             }
             if (coming) ready(seg + 1);
@@ -285,10 +286,9 @@ __global__ void __launch_bounds__(kWeighThreads) weigh_kernel(const __grid_const
     const int first = blockIdx.x * p.blocks;
     if (first >= blocks) return;
     if (p.grid > 0) {  // the CTAs that share each row tile's pair
-        const int steps = (e.tiles + 3) / 4;
         if (t < (e.rows + 127) / 128) {
-            const int64_t u = e.unit_begin + (int64_t)(h * ((e.rows + 127) / 128) + t) * steps;
-            ctas[t] = make_int2(cta_of(u, p.units, p.grid), cta_of(u + steps - 1, p.units, p.grid));
+            const int64_t u = e.unit_begin + (int64_t)(h * ((e.rows + 127) / 128) + t) * e.steps;
+            ctas[t] = make_int2(cta_of(u, p.units, p.grid), cta_of(u + e.steps - 1, p.units, p.grid));
         }
         __syncthreads();
     }

@@ -35,7 +35,8 @@ EXPORTS = [
     "kvarn_block_read", "kvarn_block_decode_attention", "kvarn_block_decode_step", "kvarn_block_prefill_attention",
     "kvarn_block_prefill", "kvarn_block_release", "kvarn_block_length", "kvarn_block_check_device_error",
     "kvarn_qk_norm_rope", "kvarn_qk_norm_rope_axes", "kvarn_block_attend_workspace", "kvarn_block_attend",
-    "kvarn_block_append_attend", "kvarn_block_window_workspace", "kvarn_block_window_weights", "kvarn_block_evict",
+    "kvarn_block_append_attend", "kvarn_block_window_workspace", "kvarn_block_window_weights",
+    "kvarn_block_window_workspace_prefixes", "kvarn_block_window_weights_prefixes", "kvarn_block_evict",
 ]
 
 
@@ -143,6 +144,8 @@ def load(build_if_missing: bool = True):
     L.kvarn_block_append_attend.argtypes = [P, I32, I32, IP, IP, IP, P, I64, P, I64, P, P, F, P, P, SZ, P]
     L.kvarn_block_window_workspace.argtypes = [P, I32, I32, IP, IP, ctypes.POINTER(SZ)]
     L.kvarn_block_window_weights.argtypes = [P, I32, I32, IP, IP, P, F, P, P, SZ, P]
+    L.kvarn_block_window_workspace_prefixes.argtypes = [P, I32, I32, IP, IP, IP, ctypes.POINTER(SZ)]
+    L.kvarn_block_window_weights_prefixes.argtypes = [P, I32, I32, IP, IP, IP, P, F, P, P, SZ, P]
     L.kvarn_block_evict.argtypes = [P, I32, I32, IP, I32, I32, I32, P, P, P]
     for name in EXPORTS:
         fn = getattr(L, name)
@@ -541,6 +544,23 @@ def kvarn_block_window_weights(handle, layer, seq_ids, q_lens, q, softmax_scale,
     _check_why(load().kvarn_block_window_weights(handle, layer, len(seq_ids), _i32(seq_ids), _counts(q_lens, seq_ids),
                                                  _ptr(q), float(softmax_scale), _ptr(weights), _ptr(workspace),
                                                  workspace_bytes, _stream(stream)), "kvarn_block_window_weights")
+
+
+def kvarn_block_window_workspace_prefixes(handle, layer, seq_ids, prefix_ids, q_lens) -> int:
+    n = ctypes.c_size_t()
+    _check_why(load().kvarn_block_window_workspace_prefixes(handle, layer, len(seq_ids), _i32(seq_ids),
+                                                            _optional(prefix_ids, seq_ids), _counts(q_lens, seq_ids),
+                                                            ctypes.byref(n)), "kvarn_block_window_workspace_prefixes")
+    return n.value
+
+
+def kvarn_block_window_weights_prefixes(handle, layer, seq_ids, prefix_ids, q_lens, q, softmax_scale, weights, workspace,
+                                        workspace_bytes, stream=None):
+    _check_why(load().kvarn_block_window_weights_prefixes(handle, layer, len(seq_ids), _i32(seq_ids),
+                                                          _optional(prefix_ids, seq_ids), _counts(q_lens, seq_ids), _ptr(q),
+                                                          float(softmax_scale), _ptr(weights), _ptr(workspace),
+                                                          workspace_bytes, _stream(stream)),
+               "kvarn_block_window_weights_prefixes")
 
 
 def kvarn_block_evict(handle, layer, seq_ids, keep, first, last, weights, kept, stream=None):

@@ -1,0 +1,59 @@
+"""CPU tests of calls behind shared prefixes (include/kvarn.h): refusals and workspaces. No kernel is launched: caches here use
+KVARN_FLAG_HOST_ONLY."""
+import ctypes
+
+import pytest
+import torch
+
+from quantized_kv_cache_seal_gb300 import kvarn as K
+from quantized_kv_cache_seal_gb300.block_cache import BlockCache
+from tests.test_block_host import FAKE, refused
+from tests.test_block_more_host import SPACE, W, filled
+
+
+def test_window_behind_prefixes_refusals():
+    c = filled()
+    call = lambda ids, pre, m, q=FAKE, w=W, space=SPACE, n=1 << 40: K.kvarn_block_window_weights_prefixes(
+        c, 0, ids, pre, m, q, 1.0, w, space, n)
+    call([0, 1, 2], [5, -1, 5], [100, 1, 0])
+    call([0], [4], [3])  # an empty prefix
+    call([0], None, [3])
+    for pre in ([6], [-2], [0], [2 ** 31 - 1]):
+        refused(1, call, [0], pre, [1])
+    refused(1, call, [0, 1], [1, -1], [1, 1])  # a prefix in the call
+    refused(1, call, [0], [5], [101])
+    refused(1, call, [5], [0], [129])
+    refused(1, call, [0], [5], [1], FAKE, FAKE)
+    refused(1, call, [0], [5], [1], FAKE, W, SPACE + 8)
+    size = lambda *a: K.kvarn_block_window_workspace_prefixes(c, 0, *a)
+    # sums of 2 heads, 4 tiles, 3 x 4 rows up to 16; rows of 2 (pairs) and a thread block a step, in three parts: a step of each
+    # pair's own, three of the prefix
+    need = lambda steps: 8 * 2 * 4 * 16 + (2 + 2 * steps) * 3 * 128 * 8
+    assert size([0], [5], [3]) == need(1 + 3) and size([0], [-1], [3]) == size([0], None, [3]) == need(1)
+    assert size([0], [4], [3]) == need(1) and size([2], [5], [0]) == 0
+    for bad in (([6], [5], [1]), ([0], [6], [1]), ([0], [-2], [1]), ([0], [5], [101])):
+        refused(1, size, *bad)
+    call([0], [5], [3], n=need(4))
+    refused(1, call, [0], [5], [3], n=need(4) - 1)
+    # ids refused once are free for the next call
+    call([0, 1], [5, 5], [1, 1])
+    for wrong in ([5], [5, 5, 5]):
+        with pytest.raises(ValueError):
+            call([0, 1], wrong, [1, 1])
+    L, n = K.load(), ctypes.c_size_t()
+    assert L.kvarn_block_window_workspace_prefixes(None, 0, 0, None, None, None, ctypes.byref(n)) == 1
+    assert L.kvarn_block_window_weights_prefixes(None, 0, 0, None, None, None, None, 1.0, None, None, 0, None) == 1
+    K.kvarn_block_destroy(c)
+
+
+def test_window_behind_prefixes_through_the_wrapper():
+    c = BlockCache(max_seqs=4, num_q_heads=8, num_kv_heads=2, max_seq_len=1000, block_tokens=64, device="cpu",
+                   flags=K.KVARN_FLAG_HOST_ONLY)
+    w, kv = c.new_weights()[0], torch.zeros(100, 2, 128, dtype=torch.float16)
+    c.append(0, [0, 3], [40, 60], kv, kv)
+    q = torch.zeros(4, 8, 128, dtype=torch.float16)
+    c.window_weights(0, [0, 1], [4, 0], q, w, prefix_ids=[3, None])
+    with pytest.raises(K.KVarNError):
+        c.window_weights(0, [0, 1], [4, 0], q, w, prefix_ids=[1, None])
+    with pytest.raises(ValueError):
+        c.window_weights(0, [0, 1], [4, 0], q, w, prefix_ids=[3])

@@ -4,8 +4,8 @@ import pytest
 import torch
 
 from tests import block_ref
-from tests.test_gpu_block import TYPES, make, tokens
-from tests.test_gpu_block_evict import near, some_weights
+from tests.test_gpu_block import TYPES, fill, make, tokens
+from tests.test_gpu_block_evict import SHAPES, near, received, some_weights
 
 pytestmark = pytest.mark.gpu
 
@@ -72,3 +72,140 @@ def test_logits_far_from_zero(seqs, n, hkv, dtype):
         want = torch.stack([p[:, :32].sum(-1), p[:, 32:].sum(-1)], -1)
         near(w[s], torch.zeros_like(w[s]), want, want * 2.0 ** -16, s)
     assert c.check_device_error() == 0
+
+
+# ------------------------------------------------------------------------------------------------ last queries of a prompt
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("block,dim,hkv,r", SHAPES)
+def test_window_behind_a_prefix(dtype, code, block, dim, hkv, r):
+    """Prompts' last queries: shares of the softmax over prefix and sequence, of the prefix itself nothing. Prefixes of every
+    kind of length, one for several sequences, none and an empty one."""
+    dt = TYPES[dtype]
+    lens = [1, 45, 128, 129, 300, 60, 260, 1, 129, 5 * block - 1, 777]
+    m_of = [1, 45, 0, 128, 37, 2, 100]
+    c = make(max_seqs=12, num_q_heads=hkv * r, num_kv_heads=hkv, head_dim=dim, block_tokens=block, code=code, dtype=dt)
+    k, _ = fill(c, lens, dt, 1020)
+    ids = [4, 0, 2, 6, 1, 3, 5]
+    pre = [7, 8, 8, 10, None, 9, 11]  # 11 is empty
+    m = [m_of[s] for s in ids]
+    q = tokens(sum(m), hkv * r, dim, dt, 1030, 0.3)
+    w = some_weights(c, 1031)
+    before = w.clone()
+    c.window_weights(0, ids, m, q, w, prefix_ids=pre)
+    at = 0
+    for s, p, n in zip(ids, pre, m):
+        parts, first = [block_ref.hold(k[s], block, code)], 0
+        if p not in (None, 11):
+            parts.insert(0, block_ref.hold(k[p], block, code))
+            first = lens[p]
+        if n:
+            want, tol = received(q[at:at + n], torch.cat(parts), dim ** -0.5, [first + lens[s] - n + t for t in range(n)], block, first)
+            near(w[s], before[s], want, tol, s)
+        else:
+            assert torch.equal(w[s], before[s])
+        at += n
+    assert torch.equal(w[7:], before[7:])
+    again = before.clone()
+    c.window_weights(0, ids, m, q, again, prefix_ids=pre)
+    assert torch.equal(w, again)
+    # without a prefix by either form
+    a, b = before.clone(), before.clone()
+    c.window_weights(0, ids, m, q, a)
+    c.window_weights(0, ids, m, q, b, prefix_ids=[-1] * 7)
+    assert torch.equal(a, b)
+    assert c.check_device_error() == 0
+
+
+@pytest.mark.parametrize("scale", [-0.05, 0.0, 0.5])
+def test_window_and_decode_agree_behind_a_prefix(scale):
+    """One query of a sequence either way, against the definition."""
+    c = make(max_seqs=4, block_tokens=64, num_q_heads=10, num_kv_heads=2, dtype=torch.bfloat16)
+    lens = [200, 63, 1, 333]
+    k, _ = fill(c, lens, torch.bfloat16, 1040)
+    q = tokens(3, 10, 128, torch.bfloat16, 1041, 0.3)
+    a, b = (torch.zeros(c.weights_shape, device="cuda") for _ in (0, 1))
+    c.decode_attention(0, [0, 1, 2], q, scale=scale, weights=a, prefix_ids=[3, 3, None])
+    c.window_weights(0, [0, 1, 2], [1, 1, 1], q, b, scale=scale, prefix_ids=[3, 3, None])
+    for s in range(3):
+        first = 0 if s == 2 else 333
+        held = [block_ref.hold(k[x], 64, "e4m3") for x in ([s] if s == 2 else [3, s])]
+        want, tol = received(q[s:s + 1], torch.cat(held), scale, [first + lens[s] - 1], 64, first)
+        for w in (a, b):
+            near(w[s], torch.zeros_like(w[s]), want, tol, s)
+
+
+def test_window_behind_a_long_prefix():
+    """Steps of prefix and sequence cut over every SM: the same bits each time, and right; a prefix with a NaN key behind which rows
+    of its head add nothing."""
+    lens, n = [2500, 33, 700, 1, 1024, 300], 9001
+    c = make(max_seqs=8, num_q_heads=40, num_kv_heads=10, block_tokens=32, dtype=torch.bfloat16, max_seq_len=9001,
+             pool_blocks=sum(x // 32 for x in lens + [n]) + 2)
+    k, _ = fill(c, lens + [n], torch.bfloat16, 1050)
+    bad = tokens(40, 10, 128, torch.bfloat16, 1052)
+    bad[35, 2, 7] = float("nan")
+    c.append(0, [7], [40], bad, bad)
+    ids, m = list(range(6)), [32, 33, 1, 1, 128, 7]
+    q = tokens(sum(m), 40, 128, torch.bfloat16, 1053, 0.3)
+    pre = [6, 6, None, 6, 6, 7]
+    first = torch.zeros(c.weights_shape, device="cuda")
+    c.window_weights(0, ids, m, q, first, prefix_ids=pre)
+    for _ in range(20):
+        w = torch.zeros_like(first)
+        c.window_weights(0, ids, m, q, w, prefix_ids=pre)
+        assert torch.equal(w, first)
+    assert torch.isfinite(first).all() and not first[5, 2].any() and first[5, 3].any() and not first[6:].any()
+    at = 0
+    for s in range(6):
+        if s < 5:
+            held = [block_ref.hold(k[x][:, :1], 32, "e4m3") for x in ([6, s] if pre[s] == 6 else [s])]
+            skip = n if pre[s] == 6 else 0
+            want, tol = received(q[at:at + m[s], :4], torch.cat(held), 128 ** -0.5,
+                                 [skip + lens[s] - m[s] + t for t in range(m[s])], 32, skip)
+            # received()'s bound is for 2^12 tokens; sums of 2^14 in turn add as many roundings four times
+            near(first[s, :1], torch.zeros_like(first[s, :1]), want, tol + want * 2.0 ** -14, s)
+        at += m[s]
+    assert c.check_device_error() == 0
+
+
+def test_window_behind_a_prefix_captured_and_on_other_streams():
+    c = make(max_seqs=3, block_tokens=32)
+    fill(c, [300, 200, 150], torch.float16, 1060)
+    qs = [tokens(8, 8, 128, torch.float16, s, 0.3) for s in (1062, 1063)]
+    w, g, s = torch.zeros(c.weights_shape, device="cuda"), torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        static, want = qs[0].clone(), torch.zeros_like(w)
+        for q in qs * 2:
+            c.window_weights(0, [0, 1], [4, 4], q, want, prefix_ids=[2, 2])
+        with torch.cuda.graph(g, stream=s):
+            c.window_weights(0, [0, 1], [4, 4], static, w, prefix_ids=[2, 2])
+        for q in qs * 2:
+            static.copy_(q)
+            g.replay()
+    s.synchronize()
+    assert torch.equal(w, want) and w.any()
+    for t in (torch.cuda.Stream(), torch.cuda.Stream().cuda_stream):
+        w = torch.zeros_like(want)
+        torch.cuda.synchronize()
+        for q in qs * 2:
+            c.window_weights(0, [0, 1], [4, 4], q, w, prefix_ids=[2, 2], stream=t)
+        torch.cuda.synchronize()
+        assert torch.equal(w, want)
+
+
+def test_window_behind_a_prefix_leaves_the_rest_of_its_workspace():
+    from quantized_kv_cache_seal_gb300 import kvarn as K
+    c = make(max_seqs=3, num_q_heads=10, num_kv_heads=2, block_tokens=32)
+    fill(c, [300, 33, 1000], torch.float16, 1070)
+    q = tokens(10, 10, 128, torch.float16, 1071, 0.3)
+    w = torch.zeros(c.weights_shape, device="cuda")
+    n = K.kvarn_block_window_workspace_prefixes(c.handle, 0, [0, 1], [2, 2], [7, 3])
+    assert n > K.kvarn_block_window_workspace(c.handle, 0, [0, 1], [7, 3]) > 0
+    space = torch.full((n + 1024,), 0xa5, dtype=torch.uint8, device="cuda")
+    base = (space.data_ptr() + 255) // 256 * 256 + 256
+    K.kvarn_block_window_weights_prefixes(c.handle, 0, [0, 1], [2, 2], [7, 3], q, 0.1, w, base, n,
+                                          torch.cuda.current_stream().cuda_stream)
+    at = base - space.data_ptr()
+    assert bool((space[:at] == 0xa5).all()) and bool((space[at + n:] == 0xa5).all())
+    assert w[0].any() and w[1].any() and not w[2].any()
