@@ -163,7 +163,8 @@ class BlockCache:
 
     def _in_space(self, given, call, need):
         """call(workspace, bytes) with the cache's own, which grows where need() says that it is too small. Calls of one
-        cache are ordered on the GPU, so that they can share it. Spaces that were outgrown stay: captured graphs use them."""
+        cache are ordered on the GPU, so that they can share it. Spaces that were outgrown stay, since captured graphs use
+        them; each is at least twice as large as the one before, so that all of them together take less than the last one."""
         space = self._spaces[-1]
         try:
             return call(space, space.numel())

@@ -45,6 +45,7 @@ kvarn_status cuda_fail(int rc, const char* what) {
 }
 
 constexpr int kWindowTokens = 128;   // queries of a sequence in window_weights
+constexpr int kSmallRows = 1 << 22;  // bytes
 constexpr int kOwnSteps = 18;        // of each SM: what a pass over the prefixes takes beside its steps
 constexpr int kChangeSteps = 4;      // of an SM: what a change of segment takes
 constexpr float kLog2e = 1.4426950408889634f;
@@ -610,6 +611,70 @@ kvarn_status check_prefixes(kvarn_block_cache* c, int32_t layer, int32_t n_seqs,
     return KVARN_OK;
 }
 
+// Is a prefix of a group of single queries better walked once, as tiles of 128 rows (two more launches), than by each
+// sequence? (Measured, 32 / 8 heads of 128, us once and each: 4 sequences behind 32k 42 and 45; 8 behind 8k 30 and 28, behind
+// 32k 42 and 79; 16 behind 2k 24 and 20, behind 8k 31 and 45; 64 behind 512 41 and 28, behind 2k 47 and 52, behind 32k 83 and 543. With
+// 16 / 2 heads: 32 behind 8k 35 and 32, 64 behind 8k 34 and 49.)
+bool walked_once(const kvarn_block_cache* c, const Entry& g) {
+    const int64_t each = (int64_t)g.q_len * g.n, once = head_pairs(c, g.q_len) * (int64_t)g.n;
+    return each >= 4 * once && each * c->cfg.num_kv_heads > 600000;
+}
+
+// The same for more queries, whose row tiles are filled by each sequence's own: `extra` steps of all KV heads are what the prefixes
+// take more that way. Walked once they take a launch of their own and fp32 rows that are joined. (Measured, 32 / 8 heads of 128, us once
+// and each: 8 sequences of 17 to 200 queries behind 2k, 2.5 extra steps a SM, 57 and 42; 4 of 400 to 700 behind 16k, 6.7, 421 and
+// 398; 32 of 2 to 16 behind 1k, 11.4, 60 and 43; 8 of 30 to 100 behind 8k, 16.8, 123 and 114; 8 of 2 to 16 behind 8k, 20.2, 54 and 63;
+// 16 of 40 to 64 behind 16k, 20.2, 197 and 225; 64 behind four of 2k, 22.7, 137 and 154.)
+bool stacked(const kvarn_block_cache* c, int64_t extra) { return extra > (int64_t)kOwnSteps * c->sms; }
+
+// How an attention call with prefixes goes: its sequences with queries, and the runs of them whose prefix is walked once. (Depends
+// on query counts and the prefixes' lengths alone.)
+struct AttendPlan {
+    int32_t ids[kBlockMaxSeqs], lens[kBlockMaxSeqs], before[kBlockMaxSeqs];  // before: a prefix that the sequence walks itself, -1 for none
+    uint8_t finished[kBlockMaxSeqs];  // 1: its prefix is walked once
+    Entry once[kBlockMaxSeqs];        // rows behind such a prefix
+    int32_t n, n_once;
+    bool single;
+};
+void plan_attend(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* ids, const int32_t* prefix_ids,
+                 const int32_t* q_lens, AttendPlan& a) {
+    Entry groups[kBlockMaxSeqs];
+    int64_t extra = 0, row = 0;
+    int32_t n_groups = 0;
+    a.single = !q_lens || single_queries(n_seqs, q_lens);
+    a.n = a.n_once = 0;
+    // Sequences without queries leave; runs of one prefix become groups of rows.
+    for (int i = 0; i < n_seqs; ++i) {
+        const int32_t m = q_lens ? q_lens[i] : 1;
+        if (m == 0) continue;
+        const int32_t pre = prefix_ids && prefix_ids[i] >= 0 && c->L(prefix_ids[i], layer) > 0 ? prefix_ids[i] : -1;
+        a.ids[a.n] = ids[i];
+        a.before[a.n] = pre;
+        a.lens[a.n] = m;
+        if (pre >= 0) {
+            if (a.n == 0 || a.before[a.n - 1] != pre) groups[n_groups++] = Entry{pre, c->L(pre, layer), 0, (int32_t)row, -1, 0};
+            groups[n_groups - 1].q_len += m;
+            extra += head_pairs(c, m) * key_steps(c->L(pre, layer));
+        }
+        ++a.n;
+        row += m;
+    }
+    // Sequences can also walk a prefix each by itself, in the one launch that takes their own tokens. The groups whose
+    // prefix is better walked once are those where that takes longer than the tiles' steps.
+    for (int g = 0; g < n_groups; ++g) extra -= head_pairs(c, groups[g].q_len) * key_steps(groups[g].n);
+    const bool together = stacked(c, extra * c->cfg.num_kv_heads);
+    auto walked = [&](int g) { return a.single ? walked_once(c, groups[g]) : together; };
+    for (int i = 0, g = -1, last = -1; i < a.n; ++i) {
+        const int32_t pre = a.before[i];
+        if (pre >= 0 && pre != last) ++g;
+        last = pre;
+        a.finished[i] = pre >= 0 && walked(g);
+        if (a.finished[i]) a.before[i] = -1;
+    }
+    for (int g = 0; g < n_groups; ++g)
+        if (walked(g)) a.once[a.n_once++] = groups[g];
+}
+
 // The parts of an attention call's workspace.
 struct Workspace {
     size_t pre_o = 0, pre_lse = 0, sums = 0, totals = 0, total = 0;
@@ -629,7 +694,15 @@ bool make_workspace(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const i
         off = (off + n + 255) / 256 * 256;
         return (size_t)o;
     };
-    w->pre_o = take(any ? rows * c->cfg.num_q_heads * c->cfg.head_dim * 4 : 0);
+    // Rows over prefixes: where one is walked once; small ones in any case, so that the workspace of a batch's steps goes by its
+    // counts alone.
+    const unsigned __int128 rows_o = rows * c->cfg.num_q_heads * c->cfg.head_dim * 4;
+    if (any && rows_o > kSmallRows && rows < 1ll << 31) {
+        AttendPlan a;
+        plan_attend(c, layer, n_seqs, ids, prefix_ids, q_lens, a);
+        any = a.n_once > 0;
+    }
+    w->pre_o = take(any ? rows_o : 0);
     w->pre_lse = take(any ? rows * c->cfg.num_q_heads * 4 : 0);
     w->sums = take(weights ? tiles * c->cfg.num_q_heads * 8 : 0);
     w->totals = take(weights ? rows * c->cfg.num_q_heads * 8 : 0);
@@ -711,85 +784,28 @@ kvarn_status plan_window(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, co
     return KVARN_OK;
 }
 
-// Is a prefix of a group of single queries better walked once, as tiles of 128 rows (two more launches), than by each
-// sequence? (Measured, 32 / 8 heads of 128, us once and each: 4 sequences behind 32k 42 and 45; 8 behind 8k 30 and 28, behind
-// 32k 42 and 79; 16 behind 2k 24 and 20, behind 8k 31 and 45; 64 behind 512 41 and 28, behind 2k 47 and 52, behind 32k 83 and 543. With
-// 16 / 2 heads: 32 behind 8k 35 and 32, 64 behind 8k 34 and 49.)
-bool walked_once(const kvarn_block_cache* c, const Entry& g) {
-    const int64_t each = (int64_t)g.q_len * g.n, once = head_pairs(c, g.q_len) * (int64_t)g.n;
-    return each >= 4 * once && each * c->cfg.num_kv_heads > 600000;
-}
-
-// The same for more queries, whose row tiles are filled by each sequence's own: `extra` steps of all KV heads are what the prefixes
-// take more that way. Walked once they take a launch of their own and fp32 rows that are joined. (Measured, 32 / 8 heads of 128, us once
-// and each: 8 sequences of 17 to 200 queries behind 2k, 2.5 extra steps a SM, 57 and 42; 4 of 400 to 700 behind 16k, 6.7, 421 and
-// 398; 32 of 2 to 16 behind 1k, 11.4, 60 and 43; 8 of 30 to 100 behind 8k, 16.8, 123 and 114; 8 of 2 to 16 behind 8k, 20.2, 54 and 63;
-// 16 of 40 to 64 behind 16k, 20.2, 197 and 225; 64 behind four of 2k, 22.7, 137 and 154.)
-bool stacked(const kvarn_block_cache* c, int64_t extra) { return extra > (int64_t)kOwnSteps * c->sms; }
-
 kvarn_status run_attend(kvarn_block_cache* c, int32_t layer, int32_t n_seqs, const int32_t* ids, const int32_t* prefix_ids,
                         const int32_t* q_lens, const void* q, void* out, float scale, float* weights, void* workspace,
                         const Workspace& w, void* stream) {
-    const bool single = !q_lens || single_queries(n_seqs, q_lens);
-    int32_t one[kBlockMaxSeqs], before[kBlockMaxSeqs], lens[kBlockMaxSeqs];
-    uint8_t finished[kBlockMaxSeqs];
-    Entry groups[kBlockMaxSeqs];
-    int64_t extra = 0;
-    int32_t n = 0, n_groups = 0;
-    int64_t row = 0;
-    // Sequences without queries leave; runs of one prefix become groups of rows.
-    for (int i = 0; i < n_seqs; ++i) {
-        const int32_t m = q_lens ? q_lens[i] : 1;
-        if (m == 0) continue;
-        const int32_t pre = prefix_ids && prefix_ids[i] >= 0 && c->L(prefix_ids[i], layer) > 0 ? prefix_ids[i] : -1;
-        one[n] = ids[i];
-        before[n] = pre;
-        finished[n] = 0;
-        lens[n] = m;
-        if (pre >= 0) {
-            if (n == 0 || before[n - 1] != pre) groups[n_groups++] = Entry{pre, c->L(pre, layer), 0, (int32_t)row, -1, 0};
-            groups[n_groups - 1].q_len += m;
-            extra += head_pairs(c, m) * key_steps(c->L(pre, layer));
-        }
-        ++n;
-        row += m;
-    }
-    if (n == 0) return KVARN_OK;
-    // Sequences can also walk a prefix each by itself, in the one launch that takes their own tokens. The groups whose
-    // prefix is better walked once are those where that takes longer than the tiles' steps.
-    for (int g = 0; g < n_groups; ++g) extra -= head_pairs(c, groups[g].q_len) * key_steps(groups[g].n);
-    const bool together = stacked(c, extra * c->cfg.num_kv_heads);
-    auto walked = [&](int g) { return single ? walked_once(c, groups[g]) : together; };
-    int32_t n_once = 0;
-    for (int i = 0, g = -1, last = -1; i < n; ++i) {
-        if (before[i] < 0) {
-            last = -1;
-            continue;
-        }
-        if (before[i] != last) ++g;
-        last = before[i];
-        finished[i] = walked(g);
-    }
-    for (int g = 0; g < n_groups; ++g)
-        if (walked(g)) groups[n_once++] = groups[g];
+    AttendPlan a;
+    plan_attend(c, layer, n_seqs, ids, prefix_ids, q_lens, a);
+    if (a.n == 0) return KVARN_OK;
     Beside b;
     if (weights) {
         b.weights = weights;
         b.sums = (float2*)((uint8_t*)workspace + w.sums);
         b.totals = (float2*)((uint8_t*)workspace + w.totals);
     }
-    if (n_once > 0) {
+    if (a.n_once > 0) {
         b.pre_o = (float*)((uint8_t*)workspace + w.pre_o);
         b.pre_lse = (float*)((uint8_t*)workspace + w.pre_lse);
-        const kvarn_status st = run_tiles(c, layer, n_once, groups, true, q, nullptr, scale, stream, b);
+        const kvarn_status st = run_tiles(c, layer, a.n_once, a.once, true, q, nullptr, scale, stream, b);
         if (st) return st;
     }
-    b.finished = finished;
-    for (int i = 0; i < n; ++i)
-        if (finished[i]) before[i] = -1;
-    if (std::any_of(before, before + n, [](int32_t pre) { return pre >= 0; }) || single) b.before = before;
-    if (!single) return run_prefill(c, layer, n, one, lens, q, out, scale, stream, b);
-    return run_decode(c, layer, n, one, q, out, scale, stream, b);
+    b.finished = a.finished;
+    if (a.single || std::any_of(a.before, a.before + a.n, [](int32_t pre) { return pre >= 0; })) b.before = a.before;
+    if (!a.single) return run_prefill(c, layer, a.n, a.ids, a.lens, q, out, scale, stream, b);
+    return run_decode(c, layer, a.n, a.ids, q, out, scale, stream, b);
 }
 
 // Do any of the n rows of `len` values at a, `stride` apart, touch one of b's? (Values of 16 bits.)

@@ -7,7 +7,7 @@ import torch
 
 from quantized_kv_cache_seal_gb300 import kvarn as K
 from quantized_kv_cache_seal_gb300.block_cache import BlockCache
-from tests.test_block_host import FAKE, refused
+from tests.test_block_host import FAKE, cache, refused
 from tests.test_block_more_host import SPACE, W, filled
 
 
@@ -57,3 +57,37 @@ def test_window_behind_prefixes_through_the_wrapper():
         c.window_weights(0, [0, 1], [4, 0], q, w, prefix_ids=[1, None])
     with pytest.raises(ValueError):
         c.window_weights(0, [0, 1], [4, 0], q, w, prefix_ids=[3])
+
+
+def test_no_workspace_for_rows_that_no_launch_writes():
+    """Prompts of many queries that walk their prefix themselves want no fp32 rows; questions whose rows stand together do."""
+    up = lambda n: -(-n // 256) * 256
+    c = cache(max_seqs=202, num_q_heads=32, num_kv_heads=8, max_seq_len=1 << 17, pool_blocks=1 << 14, num_layers=1)
+    K.kvarn_block_append(c, 0, [0, 1, 201] + list(range(2, 201)), [65536, 70000, 16384] + [50] * 199, FAKE, 1024, FAKE, 1024)
+    size = lambda *a: K.kvarn_block_attend_workspace(c, 0, *a)
+    call = lambda ids, pre, m, space, n: K.kvarn_block_attend(c, 0, ids, pre, m, FAKE, FAKE, 1.0, None, space, n)
+    for ids, pre, m in (([0], [201], [65536]), ([0, 1], [201, 201], [60000, 70000]), ([0, 1, 2], [201, -1, 200], [4096, 1, 50])):
+        assert size(ids, pre, m) == 0
+        call(ids, pre, m, None, 0)
+    assert size([0], [201], [65000], True) == 0
+    K.kvarn_block_append_attend(c, 0, [0], [201], [65000], FAKE, 1024, FAKE, 1024, FAKE, FAKE, 1.0, None, None, 0)
+    # 199 questions of 40 tokens over 16,384: walked once
+    ids, rows = list(range(2, 201)), 199 * 40 * 32
+    need = up(rows * 128 * 4) + up(rows * 4)
+    assert size(ids, [201] * 199, [40] * 199) == need
+    call(ids, [201] * 199, [40] * 199, SPACE, need)
+    refused(1, call, ids, [201] * 199, [40] * 199, SPACE, need - 1)
+    refused(1, call, ids, [201] * 199, [40] * 199, None, need)
+    # rows that no call could have: 2^32 of 2^14 bytes, more than a workspace may take
+    refused(3, size, [0, 1], [201, 201], [2 ** 31 - 1] * 2)
+    K.kvarn_block_destroy(c)
+
+
+def test_a_long_prompt_leaves_the_wrappers_workspace():
+    c = BlockCache(max_seqs=2, num_q_heads=8, num_kv_heads=2, max_seq_len=30000, block_tokens=64, device="cpu",
+                   flags=K.KVARN_FLAG_HOST_ONLY)
+    kv, q = torch.zeros(20300, 2, 128, dtype=torch.float16), torch.zeros(20000, 8, 128, dtype=torch.float16)
+    c.append(0, [1], [300], kv[:300], kv[:300])
+    c.prefill(0, [0], [20000], kv[300:], kv[300:], q, prefix_ids=[1])
+    c.prefill_attention(0, [0], [20000], q, prefix_ids=[1])
+    assert len(c._spaces) == 1
