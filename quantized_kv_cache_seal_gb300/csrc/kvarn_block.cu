@@ -358,20 +358,20 @@ int launch_block_read(const BlockReadParams& p, void* stream) {
 
 int launch_block_init(const BlockView& c, void* stream) {
     // error word, block table and the split counters
-    return (int)cudaMemsetAsync(c.base + c.lay.err, 0, c.lay.partials - c.lay.err, (cudaStream_t)stream);
+    return taken(cudaMemsetAsync(c.base + c.lay.err, 0, c.lay.partials - c.lay.err, (cudaStream_t)stream));
 }
 
 int launch_block_clear_errors(const BlockView& c, void* stream) {
     cudaStream_t s = (cudaStream_t)stream;
     const cudaError_t e = cudaMemsetAsync(c.base + c.lay.err, 0, 16, s);
-    return (int)(e != cudaSuccess ? e : cudaMemsetAsync(c.base + c.lay.counters, 0, c.lay.partials - c.lay.counters, s));
+    return taken(e != cudaSuccess ? e : cudaMemsetAsync(c.base + c.lay.counters, 0, c.lay.partials - c.lay.counters, s));
 }
 
 int stream_capturing(void* stream, int* capturing) {
     cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
     const cudaError_t e = cudaStreamIsCapturing((cudaStream_t)stream, &st);
     *capturing = st != cudaStreamCaptureStatusNone;
-    return (int)e;
+    return taken(e);
 }
 
 }  // namespace kvarn

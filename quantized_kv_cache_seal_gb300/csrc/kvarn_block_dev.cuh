@@ -12,6 +12,12 @@
 
 namespace kvarn {
 
+// A runtime call's error, which is reported here and no longer stands in the runtime for the next launch to find.
+inline int taken(cudaError_t e) {
+    if (e != cudaSuccess) (void)cudaGetLastError();
+    return (int)e;
+}
+
 // A kernel's dynamic shared memory limit, raised once on each device (the attribute is the device's).
 struct SmemOnce {
     std::atomic<uint64_t> done{0};
@@ -19,10 +25,10 @@ struct SmemOnce {
         int dev = 0;
         cudaError_t e = cudaGetDevice(&dev);
         const uint64_t bit = 1ull << (dev & 63);
-        if (e != cudaSuccess || (dev < 64 && (done.load() & bit))) return (int)e;
+        if (e != cudaSuccess || (dev < 64 && (done.load() & bit))) return taken(e);
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e == cudaSuccess && dev < 64) done.fetch_or(bit);
-        return (int)e;
+        return taken(e);
     }
 };
 
@@ -49,7 +55,7 @@ int launch_behind(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, 
     config.stream = s;
     config.attrs = &early;
     config.numAttrs = 1;
-    return (int)cudaLaunchKernelEx(&config, kernel, args...);
+    return taken(cudaLaunchKernelEx(&config, kernel, args...));
 }
 
 __device__ __forceinline__ const int32_t* block_table(const BlockView& c, int seq) {
