@@ -138,16 +138,19 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constan
 #pragma unroll 1
     for (int j0 = 0; j0 < p.keep; j0 += kMoveAhead) {
         uint4 x[kMoveAhead];
-        bool moves[kMoveAhead];
+        int to[kMoveAhead];  // -1: stays
 #pragma unroll
         for (int z = 0; z < kMoveAhead; ++z) {
             const int from = j0 + z < p.keep ? kept[j0 + z] : j0 + z;
-            moves[z] = from != j0 + z;
-            if (moves[z]) x[z] = pool[__ldg(table + from) * slot];
+            to[z] = -1;
+            if (from != j0 + z) {
+                to[z] = read<true>(table + j0 + z);
+                x[z] = pool[read<true>(table + from) * slot];
+            }
         }
 #pragma unroll
         for (int z = 0; z < kMoveAhead; ++z)
-            if (moves[z]) pool[__ldg(table + j0 + z) * slot] = x[z];
+            if (to[z] >= 0) pool[to[z] * slot] = x[z];
     }
 }
 
