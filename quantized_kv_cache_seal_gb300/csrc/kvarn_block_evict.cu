@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
         }
     }
     // the blocks that stay, in order: weights above `at`, and the first `need` of those at it
-    const float rest = full < p.cols ? weights[full] : 0.f;  // the partial block's
+    const float rest = weights[full];  // the partial block's (full < cols: there is a place for it)
     int kept_before = 0, same_before = 0;
     for (int i0 = 0; i0 < full; i0 += kSelThreads) {
         const int i = i0 + t;
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
         }
         __syncthreads();
     }
-    for (int i = p.keep + t; i <= min(full, p.cols - 1); i += kSelThreads) weights[i] = i == p.keep ? rest : 0.f;
+    for (int i = p.keep + t; i <= full; i += kSelThreads) weights[i] = i == p.keep ? rest : 0.f;
 }
 
 __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constant__ BlockEvictParams p) {
