@@ -607,6 +607,13 @@ kvarn_status check_prefixes(kvarn_block_cache* c, int32_t layer, int32_t n_seqs,
         steps += most_pairs * ((n + 127) / 128);
     }
     if ((tiles + n_seqs * (1 + kPairCost)) * c->cfg.num_kv_heads >= 1ll << 31) return fail(KVARN_ECAPACITY, "2^31 tiles of 32 tokens or more in a call");
+    if (steps * c->cfg.num_kv_heads >= 1ll << 31) {  // every pair counted as long as the last: now exactly
+        steps = 0;
+        for (int i = 0; i < n_seqs; ++i) {
+            const int64_t own = c->L(ids[i], layer) + (added ? (int64_t)added[i] : 0), m = q_lens ? q_lens[i] : 1;
+            steps += head_steps(c, own, m) + head_pairs(c, m) * (prefix_ids[i] >= 0 ? key_steps(c->L(prefix_ids[i], layer)) : 0);
+        }
+    }
     if (steps * c->cfg.num_kv_heads >= 1ll << 31) return fail(KVARN_ECAPACITY, "2^31 steps of 128 keys or more in a call");
     return KVARN_OK;
 }

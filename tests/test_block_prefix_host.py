@@ -91,3 +91,19 @@ def test_a_long_prompt_leaves_the_wrappers_workspace():
     c.prefill(0, [0], [20000], kv[300:], kv[300:], q, prefix_ids=[1])
     c.prefill_attention(0, [0], [20000], q, prefix_ids=[1])
     assert len(c._spaces) == 1
+
+
+def test_steps_of_long_prompts_are_counted_exactly():
+    """A prompt of 2^20 tokens has half of the 2^31 steps that its pairs would have if all were as long as the last: no more of a
+    refusal with prefixes than without. Behind a prefix of as many tokens it has 2^31 more, and its second half 2^30."""
+    n = 1 << 20
+    c = cache(max_seqs=4, num_q_heads=64, num_kv_heads=64, max_seq_len=n, pool_blocks=1 << 16, num_layers=1)
+    K.kvarn_block_append(c, 0, [0, 2], [n, 128], FAKE, 64 * 128, FAKE, 64 * 128)
+    call = lambda pre, m: K.kvarn_block_attend(c, 0, [0], pre, [m], FAKE, 1 << 40, 1.0, None, SPACE, 1 << 40)
+    K.kvarn_block_prefill_attention(c, 0, [0], [n], FAKE, 1 << 40, 1.0)
+    for pre in (None, [-1], [3], [2]):
+        call(pre, n)
+    K.kvarn_block_append(c, 0, [1], [n], FAKE, 64 * 128, FAKE, 64 * 128)
+    refused(3, call, [1], n)
+    call([1], n // 2)
+    K.kvarn_block_destroy(c)
