@@ -605,12 +605,12 @@ __device__ __forceinline__ void softmax_role(const BlockPrefillParams& p, const 
             return *reinterpret_cast<const uint4*>(rows + piece * kAtom + swz(4 * k + (lane >> 3), lane & 7));
         };
         if (kMore && x.pre_lse && !x.flat && w.whole() && (x.merged[w.s.i >> 5] >> (w.s.i & 31) & 1)) {
-            // the finished rows over the shared prefix, in units of O
+            // with the finished rows over the shared prefix; as those, which may be of the type's largest values, the joined ones
+            // have no units (larger ones of 2^12 would leave fp32)
             float2 f = make_float2(1.f, 0.f);
             if (valid) f = merge_factors(lse_of(m, l, kShift), x.pre_lse[row]);
-            f.x *= l == 0.f ? 0.f : 1.f / l;
-            f.y *= 1.f / kDenomUnit;
-            l = 1.f;
+            f.x *= kDenomUnit * (l == 0.f ? 0.f : 1.f / l);
+            l = kDenomUnit;
 #pragma unroll 1
             for (int ch = 0; ch < D / 32; ++ch) {
                 uint32_t o[32];
