@@ -24,7 +24,9 @@ class BlockCache:
     nothing: keep the tensors and the cache until its work is done. Results belong to the stream that wrote them.
 
     Attention takes ``prefix_ids``, one a sequence (None or -1: none): sequences of the cache whose tokens stand in front
-    of the sequence's own; neighbours in the call that name the same one share its reading where that is quicker. With ``weights``, a layer of
+    of the sequence's own; neighbours in the call that name the same one share its reading where that is quicker. (Calls with
+    prefixes or weights take kernels of their own, of the same definition and bounds but not always the same last bits; single
+    queries of many short sequences are quicker there also with no prefix named, ``prefix_ids=[None] * n``.) With ``weights``, a layer of
     ``new_weights()``, single queries add up what each block receives of their softmax weights, ``window_weights`` adds
     the last queries' of prompts, and ``evict`` keeps the blocks with the most."""
 

@@ -7,7 +7,7 @@
 // With a single tile nothing but depth hides the memory: codes come by bulk copies into rings of eight expansion warps (four
 // take K, four V, a warp 32 tokens), 66 KB in flight a SM. The line of all steps is cut evenly over the CTAs; each leaves its
 // sums, unnormalised, and join_kernel adds them in order into fp32 rows with the log2 of their denominators, which the kernels that
-// take the sequences' own tokens join with theirs. Every wait is bounded and sets the error word when it gives up.
+// take the sequences' own tokens join with theirs (where blocks' weights are noted, also the denominators as maximum and sum). Every wait is bounded and sets the error word when it gives up.
 //
 // Measured, 32 sequences behind each of two prefixes of 32k, 40 / 10 heads, int8, bf16 (128 rows of a KV head, 43 GFLOP, 168 MB): 57 us and
 // 8 for the join; two row tiles at a time, as prefill takes them, 83 and 11. Bound by the chain of a step: weights of one tile, its

@@ -621,7 +621,9 @@ kvarn_status check_prefixes(kvarn_block_cache* c, int32_t layer, int32_t n_seqs,
 // Is a prefix of a group of single queries better walked once, as tiles of 128 rows (two more launches), than by each
 // sequence? (Measured, 32 / 8 heads of 128, us once and each: 4 sequences behind 32k 42 and 45; 8 behind 8k 30 and 28, behind
 // 32k 42 and 79; 16 behind 2k 24 and 20, behind 8k 31 and 45; 64 behind 512 41 and 28, behind 2k 47 and 52, behind 32k 83 and 543. With
-// 16 / 2 heads: 32 behind 8k 35 and 32, 64 behind 8k 34 and 49.)
+// 16 / 2 heads: 32 behind 8k 35 and 32, 64 behind 8k 34 and 49.) Each group is judged by itself, as if it paid for the two launches
+// alone, and all measurements are of one group or two: many groups in a call, each under the limit, are walked by every
+// sequence although one pass would do for all. Nor does the limit know head_dim (half the bytes at 64).
 bool walked_once(const kvarn_block_cache* c, const Entry& g) {
     const int64_t each = (int64_t)g.q_len * g.n, once = head_pairs(c, g.q_len) * (int64_t)g.n;
     return each >= 4 * once && each * c->cfg.num_kv_heads > 600000;
@@ -631,7 +633,8 @@ bool walked_once(const kvarn_block_cache* c, const Entry& g) {
 // take more that way. Walked once they take a launch of their own and fp32 rows that are joined. (Measured, 32 / 8 heads of 128, us once
 // and each: 8 sequences of 17 to 200 queries behind 2k, 2.5 extra steps a SM, 57 and 42; 4 of 400 to 700 behind 16k, 6.7, 421 and
 // 398; 32 of 2 to 16 behind 1k, 11.4, 60 and 43; 8 of 30 to 100 behind 8k, 16.8, 123 and 114; 8 of 2 to 16 behind 8k, 20.2, 54 and 63;
-// 16 of 40 to 64 behind 16k, 20.2, 197 and 225; 64 behind four of 2k, 22.7, 137 and 154.)
+// 16 of 40 to 64 behind 16k, 20.2, 197 and 225; 64 behind four of 2k, 22.7, 137 and 154.) One answer for all prefixes of a call, also
+// where one has many short questions and another a long prompt.
 bool stacked(const kvarn_block_cache* c, int64_t extra) { return extra > (int64_t)kOwnSteps * c->sms; }
 
 // How an attention call with prefixes goes: its sequences with queries, and the runs of them whose prefix is walked once. (Depends
